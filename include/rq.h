@@ -44,7 +44,9 @@ typedef enum {
     RQ_ERR_ALLOC = 5,      /* device or host allocation failed                */
     RQ_ERR_CUDA = 6,       /* a CUDA call or kernel launch failed             */
     RQ_ERR_TIMEOUT = 7,    /* a kernel gave up on a pipeline wait (see below) */
-    RQ_ERR_ARCH = 8        /* device lacks sm_103 features (tcgen05, TMA)     */
+    RQ_ERR_ARCH = 8,       /* device lacks sm_103 features (tcgen05, TMA)     */
+    RQ_ERR_INDEX = 9       /* a kernel met an index outside its array (a cache
+                              slot, a page, a position); rq_get_device_status */
 } rq_status;
 
 /* GGUF tensor type ids. */
@@ -299,6 +301,193 @@ rq_status rq_fp8_linear_noalloc(const float *x, const uint8_t *w_fp8,
 /* Forget the cached FP8 activation (bump the generation). */
 rq_status rq_act_cache_invalidate(rq_ctx *ctx);
 
+/* ------------------------------------------ quantized K/V cache ------- */
+
+/* The steps of a decoder layer between its q/k/v products and its o product,
+ * and the step from probabilities to tokens.  The source pages have no
+ * counterpart to these entry points: the layer's linears above produce their
+ * inputs (f32) and read their outputs.
+ *
+ * Activations are f32, f16 or bf16; every sum, norm and softmax statistic is
+ * f32 (the token draws are exact integers), and a result is rounded once. */
+typedef enum { RQ_F32 = 0, RQ_F16 = 1, RQ_BF16 = 2 } rq_dtype;
+
+/* One byte per cached value, one f32 scale per cached row (the head_dim
+ * values of one token and kv head): value = code * scale.  With A the row's
+ * largest finite magnitude, A' = max(A, 2^-100) and top the format's largest
+ * value (448 or 127):  scale = A' / top,  code = rn(x * (top * (1 / A'))),
+ * each operation one correctly rounded f32 operation and rn the round to
+ * nearest even into the format, limited to +-top.  A value that is not finite takes +-top with its own
+ * sign, so the NaN codes of E4M3 are never written (they must not be in rows
+ * that are read). */
+typedef enum { RQ_KV_E4M3 = 0, RQ_KV_I8 = 1 } rq_kv_format;
+
+/* A paged cache, described by the caller, who owns its memory:
+ *   k, v:  codes [pages][kv_heads][page_size][head_dim], 16-byte aligned.
+ *   k_scale, v_scale:  f32 [pages][kv_heads][page_size], 16-byte aligned.
+ *   page_size: 16, 32, 64, 128 or 256 tokens.  head_dim: 64, 128 or 256.
+ *   pages >= 1, kv_heads >= 1, pages * kv_heads < 2^31.
+ * A slot names one token's place: slot = page * page_size + offset.  The
+ * struct is read on the host during the call; it need not outlive it. */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int64_t pages;
+    int page_size, kv_heads, head_dim;
+    int format; /* rq_kv_format */
+} rq_kv_cache;
+
+/* What one layer's norms and rotation of q and k need, fixed for the layer:
+ *   q_weight, k_weight: f32 [head_dim] norm weights, 16-byte aligned, or NULL
+ *     for no norm of that side.  The norm is x * rsqrt(mean(x^2) + eps) *
+ *     weight over each head's head_dim values.
+ *   cos_table, sin_table: f32 [positions][rotary_dim / 2], 16-byte aligned
+ *     (NULL when rotary_dim is 0).
+ *   rotary_dim: the leading coordinates of each head that turn, 0 or a
+ *     multiple of 16 up to head_dim; coordinate pairs are (i, i +
+ *     rotary_dim / 2), or (2 i, 2 i + 1) when interleaved is nonzero:
+ *     (a, b) -> (a cos - b sin, b cos + a sin). */
+typedef struct {
+    const float *q_weight, *k_weight;
+    const float *cos_table, *sin_table;
+    int64_t positions;
+    int q_heads, kv_heads, head_dim;
+    int rotary_dim, interleaved;
+    float eps;
+} rq_qk_params;
+
+/* Per-head norm and position rotation of q and k in one pass:
+ *   q: [tokens][q_heads][head_dim], k: [tokens][kv_heads][head_dim] of dtype,
+ *     a token's heads contiguous, consecutive tokens q_stride / k_stride
+ *     elements apart (at least the row, and a multiple of 16 bytes).
+ *   position: int32 [tokens], rows of the tables (ignored, may be NULL, when
+ *     rotary_dim is 0).  A token whose position is outside the tables is not
+ *     turned and RQ_ERR_INDEX is recorded for rq_get_device_status.
+ *   q_out, k_out: dense, of dtype.  q_out may be q and k_out may be k where
+ *     those are dense.
+ * q or k may be NULL together with its output: that side is left out.
+ * All pointers 16-byte aligned (position: 4).  tokens == 0 does nothing.
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_QTYPE (dtype), RQ_ERR_CUDA. */
+rq_status rq_qk_norm_rope(const rq_qk_params *params_host, int dtype, const void *q,
+                          int64_t q_stride, const void *k, int64_t k_stride,
+                          const int32_t *position, void *q_out, void *k_out,
+                          int tokens, rq_stream_t stream);
+
+/* The same, with k (after norm and rotation) and v quantized straight from
+ * f32 into the cache at slot[t] in the same pass:
+ *   v: like k, v_stride.   slot: int64 [tokens], 8-byte aligned; a negative
+ *   slot writes nothing for its token, one past the cache writes nothing and
+ *   records RQ_ERR_INDEX.  Two tokens of one call must not share a slot.
+ * The cache's kv_heads and head_dim must be the params'.  q may be NULL with
+ * q_out.  Errors: as rq_qk_norm_rope, and those of rq_kv_write. */
+rq_status rq_qkv_to_cache(const rq_qk_params *params_host, int dtype, const void *q,
+                          int64_t q_stride, const void *k, int64_t k_stride,
+                          const void *v, int64_t v_stride, const int32_t *position,
+                          void *q_out, const rq_kv_cache *cache_host,
+                          const int64_t *slot, int tokens, rq_stream_t stream);
+
+/* Quantize k and v rows into the cache as they are (no norm, no rotation).
+ * Arguments as above.  Errors: RQ_ERR_NULL, RQ_ERR_SHAPE (sizes, strides or
+ * alignment), RQ_ERR_QTYPE (dtype or cache format), RQ_ERR_CUDA. */
+rq_status rq_kv_write(const rq_kv_cache *cache_host, int dtype, const void *k,
+                      int64_t k_stride, const void *v, int64_t v_stride,
+                      const int64_t *slot, int tokens, rq_stream_t stream);
+
+/* Read the cache back: k_out, v_out [tokens][kv_heads][head_dim] of dtype,
+ * dense, 16-byte aligned: code * scale of slot[t] (one f32 product, then the
+ * dtype's rounding), zeros for a negative slot; a slot past the cache reads
+ * as zeros and records RQ_ERR_INDEX.  Errors: as rq_kv_write. */
+rq_status rq_kv_read(const rq_kv_cache *cache_host, int dtype, const int64_t *slot,
+                     void *k_out, void *v_out, int tokens, rq_stream_t stream);
+
+/* Attention of new tokens over the paged quantized cache: single tokens,
+ * drafted chains and trees, prompts.  Sequence b has length[b] cached tokens
+ * and `new_tokens` new ones, whose keys and values are already in the cache
+ * at the places length[b] .. length[b] + new_tokens - 1 of the sequence:
+ *   out[b, i, h] = sum_j softmax_j(scale * q[b, i, h] . k[j, h']) v[j, h'],
+ *   h' = h / (q_heads / kv_heads),
+ * over the places j < length[b], and of the new ones over
+ *   tree == NULL:  new tokens 0 .. i (a chain or a prompt);
+ *   tree != NULL:  new token j where bit j of tree[b, i] is set (the draft
+ *                  itself and those before it on its path, say); bits from
+ *                  new_tokens on are ignored.  new_tokens <= 64.
+ * A row that sees nothing gives zeros.  length[b] < 0 marks an unused
+ * sequence: zeros.  A row whose q is not finite gives NaN.
+ *   q: [batch * new_tokens][q_heads][head_dim] of dtype, consecutive tokens
+ *     q_stride elements apart.   out: the same shape, dense.
+ *   page_table: int32 [batch][max_pages]; place p of sequence b is offset
+ *     p % page_size of page page_table[b, p / page_size].  Entries past the
+ *     sequence's last place are not read.  A page outside the cache reads as
+ *     page 0, places past max_pages pages are not seen; both record
+ *     RQ_ERR_INDEX.
+ *   scale: finite, above 0.   q_heads: a multiple of kv_heads.
+ * What lies in the cache behind a sequence's places, or under a cleared
+ * bit, does not reach the output.
+ * Accuracy: with f32 activations q, the probabilities and both products are
+ * carried to about 22 bits (each f32 operand split into two f16 parts, codes
+ * exact in f16, f32 sums); with f16 / bf16 activations q and the
+ * probabilities are f16 operands (11 bits).
+ * Partial results of split sequences live in scratch owned by ctx, which
+ * grows on a call that needs more (allocating: call once at the largest
+ * sizes before a stream capture); they are joined in a fixed order, so equal
+ * calls give equal bits.
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_QTYPE (dtype or format),
+ * RQ_ERR_ALLOC, RQ_ERR_CUDA, RQ_ERR_ARCH (no tensor maps). */
+rq_status rq_cache_attention(rq_ctx *ctx, const rq_kv_cache *cache_host, int dtype,
+                             const void *q, int64_t q_stride, void *out, int batch,
+                             int new_tokens, int q_heads, const int32_t *page_table,
+                             int max_pages, const int32_t *length,
+                             const uint64_t *tree, float scale, rq_stream_t stream);
+
+/* ------------------------------------- verification of drafted tokens -- */
+
+/* Keep or reject a chain of drafted tokens per sequence, and draw the next
+ * token, so that the kept tokens and the drawn one are distributed as the
+ * target's own:
+ *   token: int32 [batch][drafts].
+ *   p: f32 [batch][drafts + 1][vocab], the target's probabilities at the
+ *     place of each draft and after the last one.
+ *   q: f32 [batch][drafts][vocab], the distributions the drafts were drawn
+ *     from, or NULL for drafts that were not drawn (q one-hot).
+ *   u: f32 [batch][drafts + 1] random numbers in [0, 1): u[b, i] decides
+ *     draft i, u[b, drafts] draws the next token.
+ * Draft i with token x is kept if u[i] * q[i][x] < p[i][x] (one f32 product;
+ * q one-hot: u[i] < p[i][x]); accepted[b] = drafts kept before the first that
+ * is not.  The next token is drawn from the weights max(p - q, 0) at the
+ * rejected draft's place (q one-hot: p with the draft's own entry 0), or
+ * from p after the last draft; weights that are all zero fall back to p.  A
+ * draft token outside 0 .. vocab-1 ends the chain there, and the next token
+ * is drawn from p (drafts of unequal number).
+ * The draw is exact: weights are whole numbers, floor(min(w, 1) * 2^36) (NaN:
+ * 0), and the next token is the first whose running sum exceeds
+ * floor(U * total / 2^24), U = floor(u * 2^24) limited to 0 .. 2^24-1, so
+ * that it depends on no order of summation; -1 if p has no weight either.
+ *   accepted, next: int32 [batch].
+ * drafts >= 0 (token, q may be NULL at 0), 1 <= vocab <= 2^20, batch >= 1.
+ * p and q: 4-byte aligned.
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_CUDA. */
+rq_status rq_verify_chain(const int32_t *token, const float *p, const float *q,
+                          const float *u, int32_t *accepted, int32_t *next, int batch,
+                          int drafts, int vocab, rq_stream_t stream);
+
+/* The same for trees of drafts that were not drawn at random (a node's
+ * likeliest continuations, say): at each node the target's token is drawn
+ * and the walk goes on where a draft holds it.
+ *   parent: int32 [batch][drafts], parent[b, i] < i, or -1 for the last
+ *     token before the drafts; a draft whose parent is outside -1 .. i-1 is
+ *     not reached.  p: f32 [batch][drafts + 1][vocab]: row 0 after the last
+ *     token, row 1 + i after draft i.   u: f32 [batch][drafts + 1] likewise.
+ * Starting at the last token: y is drawn from the node's p with the node's u
+ * (exactly as above); the first draft whose parent is the node and whose
+ * token is y is accepted and becomes the node; without one, y is the next
+ * token.   accepted, next: int32 [batch].   path: int32 [batch][drafts], the
+ * accepted drafts in order, then -1.   drafts <= 1024.
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_CUDA. */
+rq_status rq_verify_tree(const int32_t *token, const int32_t *parent, const float *p,
+                         const float *u, int32_t *accepted, int32_t *next,
+                         int32_t *path, int batch, int drafts, int vocab,
+                         rq_stream_t stream);
+
 /* ----------------------------------------------------------- tracing --- */
 
 /* Kernel-level tracing of rq_linear, the device-side counterpart of the
@@ -339,10 +528,12 @@ rq_status rq_ctx_trace_kinds(rq_ctx *ctx, unsigned int mask);
 rq_status rq_ctx_trace_end(rq_ctx *ctx, int64_t *counts_host, double *ms_host);
 
 /* Synchronise `stream`, then report and clear the library's device error
- * word: RQ_ERR_TIMEOUT if a GEMM or GEMV pipeline wait, or the one-pass
- * quantization's grid barrier, exceeded its time limit (the kernel then
- * stopped early and its output is incomplete), RQ_ERR_CUDA if
- * the synchronisation itself failed, RQ_OK otherwise. */
+ * word: RQ_ERR_TIMEOUT if a GEMM, GEMV or attention pipeline wait, or the
+ * one-pass quantization's grid barrier, exceeded its time limit (the kernel
+ * then stopped early and its output is incomplete), RQ_ERR_INDEX if a cache
+ * or attention kernel met a slot, page or position outside its array (it
+ * went on without it), RQ_ERR_CUDA if the synchronisation itself failed,
+ * RQ_OK otherwise. */
 rq_status rq_get_device_status(rq_stream_t stream);
 
 /* Test hook for the timeout path: launches one block that waits on an

@@ -19,9 +19,11 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "rq.h")
 
 RQ_Q4K = 12
 RQ_Q6K = 14
+RQ_F32, RQ_F16, RQ_BF16 = 0, 1, 2
+RQ_KV_E4M3, RQ_KV_I8 = 0, 1
 STATUS = {0: "RQ_OK", 1: "RQ_ERR_NULL", 2: "RQ_ERR_SHAPE", 3: "RQ_ERR_QTYPE",
           4: "RQ_ERR_NOT_CACHED", 5: "RQ_ERR_ALLOC", 6: "RQ_ERR_CUDA",
-          7: "RQ_ERR_TIMEOUT", 8: "RQ_ERR_ARCH"}
+          7: "RQ_ERR_TIMEOUT", 8: "RQ_ERR_ARCH", 9: "RQ_ERR_INDEX"}
 
 
 class RqError(RuntimeError):
@@ -67,6 +69,15 @@ _SIGS = {
     "rq_get_device_status": ([_vp], _i32),
     "rq_debug_wait_timeout": ([_i64, _vp], _i32),
     "rq_gemv_exact_outputs": ([_vp, ctypes.POINTER(_i64)], _i32),
+    "rq_qk_norm_rope": ([_vp, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp], _i32),
+    "rq_qkv_to_cache": ([_vp, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i32,
+                         _vp], _i32),
+    "rq_kv_write": ([_vp, _i32, _vp, _i64, _vp, _i64, _vp, _i32, _vp], _i32),
+    "rq_kv_read": ([_vp, _i32, _vp, _vp, _vp, _i32, _vp], _i32),
+    "rq_cache_attention": ([_vp, _vp, _i32, _vp, _i64, _vp, _i32, _i32, _i32, _vp, _i32, _vp,
+                            _vp, ctypes.c_float, _vp], _i32),
+    "rq_verify_chain": ([_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp], _i32),
+    "rq_verify_tree": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp], _i32),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -162,6 +173,179 @@ def rq_gemv_exact_outputs(stream=None):
     return n.value
 
 
+class _KVCacheStruct(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("pages", _i64),
+                ("page_size", _i32), ("kv_heads", _i32), ("head_dim", _i32), ("format", _i32)]
+
+
+class _QKParamsStruct(ctypes.Structure):
+    _fields_ = [("q_weight", _vp), ("k_weight", _vp), ("cos_table", _vp), ("sin_table", _vp),
+                ("positions", _i64), ("q_heads", _i32), ("kv_heads", _i32), ("head_dim", _i32),
+                ("rotary_dim", _i32), ("interleaved", _i32), ("eps", ctypes.c_float)]
+
+
+class KVCache:
+    """A paged quantized K/V cache (rq_kv_cache): codes k, v
+    [pages, kv_heads, page_size, head_dim] of one byte and f32 scales k_scale,
+    v_scale [pages, kv_heads, page_size].  The constructor allocates them;
+    from_tensors takes the caller's."""
+
+    def __init__(self, pages, page_size, kv_heads, head_dim, format=RQ_KV_E4M3, device="cuda"):
+        import torch
+        code = torch.float8_e4m3fn if format == RQ_KV_E4M3 else torch.int8
+        shape = (pages, kv_heads, page_size)
+        self._set(torch.zeros(shape + (head_dim,), dtype=torch.uint8, device=device).view(code),
+                  torch.zeros(shape + (head_dim,), dtype=torch.uint8, device=device).view(code),
+                  torch.zeros(shape, dtype=torch.float32, device=device),
+                  torch.zeros(shape, dtype=torch.float32, device=device), format)
+
+    @classmethod
+    def from_tensors(cls, k, v, k_scale, v_scale, format=RQ_KV_E4M3):
+        c = cls.__new__(cls)
+        c._set(k, v, k_scale, v_scale, format)
+        return c
+
+    def _set(self, k, v, k_scale, v_scale, format):
+        for t in (k, v, k_scale, v_scale):
+            if not t.is_contiguous():
+                raise RqError(2, "KVCache: tensors must be dense")
+        if (k.dim() != 4 or v.shape != k.shape or k_scale.shape != k.shape[:3] or
+                v_scale.shape != k.shape[:3] or k.element_size() != 1 or v.element_size() != 1 or
+                k_scale.element_size() != 4 or v_scale.element_size() != 4):
+            raise RqError(2, "KVCache")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.format = format
+        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.struct = _KVCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                                     v_scale.data_ptr(), self.pages, self.page_size,
+                                     self.kv_heads, self.head_dim, format)
+        self.address = ctypes.addressof(self.struct)
+
+
+class QKParams:
+    """One layer's norm weights and rotation tables (rq_qk_params); cos, sin:
+    f32 [positions, rotary_dim / 2]."""
+
+    def __init__(self, q_heads, kv_heads, head_dim, q_weight=None, k_weight=None, eps=1e-6,
+                 cos=None, sin=None, rotary_dim=None, interleaved=False):
+        if rotary_dim is None:
+            rotary_dim = 0 if cos is None else head_dim
+        for t in (q_weight, k_weight, cos, sin):
+            if t is not None and not (t.is_contiguous() and t.element_size() == 4):
+                raise RqError(2, "QKParams: weights and tables are dense f32")
+        for t in (q_weight, k_weight):
+            if t is not None and t.numel() != head_dim:
+                raise RqError(2, "QKParams: a weight per coordinate of a head")
+        if cos is not None and (sin is None or cos.dim() != 2 or sin.shape != cos.shape or
+                                cos.shape[1] * 2 != rotary_dim):
+            raise RqError(2, "QKParams: tables are [positions, rotary_dim / 2]")
+        self.tensors = (q_weight, k_weight, cos, sin)
+        self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
+        self.struct = _QKParamsStruct(_ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
+                                      0 if cos is None else cos.shape[0], q_heads, kv_heads,
+                                      head_dim, rotary_dim, int(bool(interleaved)), eps)
+        self.address = ctypes.addressof(self.struct)
+
+
+_DTYPES = {}
+
+
+def _dtype(t, dtype):
+    """rq_dtype of a tensor, or the given one where t is an address."""
+    if dtype is not None:
+        return dtype
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: RQ_F32, torch.float16: RQ_F16, torch.bfloat16: RQ_BF16})
+    return _DTYPES.get(t.dtype, -1)
+
+
+def _row_stride(t, heads, head_dim, stride, where):
+    """Elements between a tensor's consecutive tokens: [tokens, heads,
+    head_dim], [batch, tokens, heads, head_dim] or [tokens, heads * head_dim]
+    with dense heads; `stride` where t is an address (None: dense)."""
+    row = heads * head_dim
+    if stride is not None:
+        return stride
+    if t is None or isinstance(t, int):
+        return row
+    if t.is_contiguous():
+        return row
+    shape, st = t.shape, t.stride()
+    if shape[-1] not in (head_dim, row) or st[-1] != 1:
+        raise RqError(2, where)
+    lead = len(shape) - 1
+    if shape[-1] == head_dim and len(shape) > 2:
+        lead -= 1
+        if shape[lead] > 1 and st[lead] != head_dim:
+            raise RqError(2, where)
+    # what is left counts tokens: one distance throughout
+    token, step = None, None
+    for i in range(lead - 1, -1, -1):
+        if shape[i] == 1:
+            continue
+        if token is None:
+            token, step = st[i], st[i] * shape[i]
+        elif st[i] != step:
+            raise RqError(2, where)
+        else:
+            step = st[i] * shape[i]
+    return row if token is None else token
+
+
+def rq_qk_norm_rope(params, q, k, position, q_out, k_out, tokens, dtype=None, q_stride=None,
+                    k_stride=None, stream=None):
+    """Per-head norm and position rotation: q -> q_out, k -> k_out (either
+    pair may be None)."""
+    d = params.head_dim
+    qs = _row_stride(q, params.q_heads, d, q_stride, "rq_qk_norm_rope: q")
+    ks = _row_stride(k, params.kv_heads, d, k_stride, "rq_qk_norm_rope: k")
+    _check(_lib.rq_qk_norm_rope(params.address, _dtype(k if q is None else q, dtype), _ptr(q), qs,
+                                _ptr(k), ks, _ptr(position), _ptr(q_out), _ptr(k_out), tokens,
+                                _stream(stream)), "rq_qk_norm_rope")
+
+
+def rq_qkv_to_cache(params, q, k, v, position, q_out, cache, slot, tokens, dtype=None,
+                    q_stride=None, k_stride=None, v_stride=None, stream=None):
+    """The same, with k and v quantized into the cache at slot (int64)."""
+    d, hk = params.head_dim, params.kv_heads
+    qs = _row_stride(q, params.q_heads, d, q_stride, "rq_qkv_to_cache: q")
+    ks = _row_stride(k, hk, d, k_stride, "rq_qkv_to_cache: k")
+    vs = _row_stride(v, hk, d, v_stride, "rq_qkv_to_cache: v")
+    _check(_lib.rq_qkv_to_cache(params.address, _dtype(k, dtype), _ptr(q), qs, _ptr(k), ks,
+                                _ptr(v), vs, _ptr(position), _ptr(q_out), cache.address,
+                                _ptr(slot), tokens, _stream(stream)), "rq_qkv_to_cache")
+
+
+def rq_kv_write(cache, k, v, slot, tokens, dtype=None, k_stride=None, v_stride=None,
+                stream=None):
+    """Quantize k and v rows into the cache at slot (int64)."""
+    ks = _row_stride(k, cache.kv_heads, cache.head_dim, k_stride, "rq_kv_write: k")
+    vs = _row_stride(v, cache.kv_heads, cache.head_dim, v_stride, "rq_kv_write: v")
+    _check(_lib.rq_kv_write(cache.address, _dtype(k, dtype), _ptr(k), ks, _ptr(v), vs, _ptr(slot),
+                            tokens, _stream(stream)), "rq_kv_write")
+
+
+def rq_kv_read(cache, slot, k_out, v_out, tokens, dtype=None, stream=None):
+    """Read the cache back at slot (int64) into dense rows."""
+    _check(_lib.rq_kv_read(cache.address, _dtype(k_out, dtype), _ptr(slot), _ptr(k_out),
+                           _ptr(v_out), tokens, _stream(stream)), "rq_kv_read")
+
+
+def rq_verify_chain(token, p, q, u, accepted, next, batch, drafts, vocab, stream=None):
+    """Keep or reject chains of drafts and draw the next token (q may be None)."""
+    _check(_lib.rq_verify_chain(_ptr(token), _ptr(p), _ptr(q), _ptr(u), _ptr(accepted),
+                                _ptr(next), batch, drafts, vocab, _stream(stream)),
+           "rq_verify_chain")
+
+
+def rq_verify_tree(token, parent, p, u, accepted, next, path, batch, drafts, vocab, stream=None):
+    """Walk trees of drafts by draws from the target, and draw the next token."""
+    _check(_lib.rq_verify_tree(_ptr(token), _ptr(parent), _ptr(p), _ptr(u), _ptr(accepted),
+                               _ptr(next), _ptr(path), batch, drafts, vocab, _stream(stream)),
+           "rq_verify_tree")
+
+
 class Context:
     """Owns an rq_ctx: FP8 weight cache, activation scratch, device scalars."""
 
@@ -233,6 +417,19 @@ class Context:
     def rq_linear(self, qtype, w, x, y, M, N, K, stream=None):
         _check(_lib.rq_linear(self._h, qtype, _ptr(w), _ptr(x), _ptr(y), M, N, K,
                               _stream(stream)), "rq_linear")
+
+    def rq_cache_attention(self, cache, q, out, page_table, length, batch, new_tokens, q_heads,
+                           scale, tree=None, max_pages=None, dtype=None, q_stride=None,
+                           stream=None):
+        """Attention of batch x new_tokens tokens over the cache; tree: 64-bit
+        words [batch, new_tokens] of visible new tokens, None: causal."""
+        qs = _row_stride(q, q_heads, cache.head_dim, q_stride, "rq_cache_attention: q")
+        if max_pages is None:
+            max_pages = page_table.shape[1]
+        _check(_lib.rq_cache_attention(self._h, cache.address, _dtype(q, dtype), _ptr(q), qs,
+                                       _ptr(out), batch, new_tokens, q_heads, _ptr(page_table),
+                                       max_pages, _ptr(length), _ptr(tree), scale,
+                                       _stream(stream)), "rq_cache_attention")
 
     TRACE_KINDS = ("gemv", "absmax", "quant", "gemm", "wcache")
 

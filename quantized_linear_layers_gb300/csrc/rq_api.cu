@@ -115,6 +115,7 @@ struct rq_ctx {
   int act_M = 0, act_K = 0;
   uint64_t act_gen = 0, gen = 1;
   int64_t hits = 0, misses = 0;
+  AttnScratch attn;  // partial rows of split sequences
 };
 
 namespace {
@@ -170,6 +171,7 @@ const char* rq_status_string(rq_status s) {
     case RQ_ERR_CUDA: return "CUDA error";
     case RQ_ERR_TIMEOUT: return "device pipeline wait timed out";
     case RQ_ERR_ARCH: return "device lacks sm_103 features";
+    case RQ_ERR_INDEX: return "index outside its array on the device";
   }
   return "unknown status";
 }
@@ -248,6 +250,7 @@ void rq_ctx_destroy(rq_ctx* ctx) {
   if (ctx->absmax) cudaFree(ctx->absmax);
   if (ctx->slots) cudaFree(ctx->slots);
   if (ctx->fused_slots) cudaFree(ctx->fused_slots);
+  ctx->attn.release();
   delete ctx;
 }
 
@@ -595,6 +598,209 @@ rq_status rq_linear_group(rq_ctx* ctx, int count, const rq_qtype* qtypes, const 
   // a group cache built by an earlier call may be loaded early (as in rq_linear)
   return launch_fp8_gemm_group(xq, xdeq, it->second.fp8, count, it->second.starts, y, deqs, M,
                                K, st, hit);
+}
+
+// ------------------------------------------------- quantized K/V cache --
+
+static rq_status check_dtype(int dtype) {
+  return dtype == RQ_F32 || dtype == RQ_F16 || dtype == RQ_BF16 ? RQ_OK : RQ_ERR_QTYPE;
+}
+
+static int width_of(int dtype) { return dtype == RQ_F32 ? 4 : 2; }
+
+static bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
+
+static rq_status check_cache(const rq_kv_cache* c) {
+  if (c == nullptr || c->k == nullptr || c->v == nullptr || c->k_scale == nullptr ||
+      c->v_scale == nullptr)
+    return RQ_ERR_NULL;
+  if (c->format != RQ_KV_E4M3 && c->format != RQ_KV_I8) return RQ_ERR_QTYPE;
+  if (!head_dim_ok(c->head_dim) || c->kv_heads < 1 || c->pages < 1 ||
+      c->pages > 0x7FFFFFFFLL / c->kv_heads)
+    return RQ_ERR_SHAPE;
+  const int p = c->page_size;
+  if (p != 16 && p != 32 && p != 64 && p != 128 && p != 256) return RQ_ERR_SHAPE;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 16) ||
+      !aligned(c->v_scale, 16))
+    return RQ_ERR_SHAPE;
+  return RQ_OK;
+}
+
+// Rows of `heads` heads per token: pointer and token stride.
+static rq_status check_rows(const void* p, int64_t stride, int heads, int head_dim, int dtype) {
+  const int w = width_of(dtype);
+  if (!aligned(p, 16) || stride < (int64_t)heads * head_dim || stride % (16 / w) != 0 ||
+      stride > (int64_t)1 << 40)
+    return RQ_ERR_SHAPE;
+  return RQ_OK;
+}
+
+static rq_status check_qk(const rq_qk_params* p, const int32_t* position) {
+  if (p == nullptr) return RQ_ERR_NULL;
+  if (!head_dim_ok(p->head_dim) || p->q_heads < 0 || p->kv_heads < 0 || p->rotary_dim < 0 ||
+      p->rotary_dim > p->head_dim || p->rotary_dim % 16 != 0)
+    return RQ_ERR_SHAPE;
+  if (p->rotary_dim > 0) {
+    if (p->cos_table == nullptr || p->sin_table == nullptr || position == nullptr)
+      return RQ_ERR_NULL;
+    if (p->positions < 1 || !aligned(p->cos_table, 16) || !aligned(p->sin_table, 16) ||
+        !aligned(position, 4))
+      return RQ_ERR_SHAPE;
+  }
+  if (!aligned(p->q_weight, 16) || !aligned(p->k_weight, 16) || !(p->eps >= 0.0f))
+    return RQ_ERR_SHAPE;
+  return RQ_OK;
+}
+
+// Blocks of 8 warps, at most one row a warp: keep the grid below 2^31.
+static bool tokens_ok(int tokens, int rows) {
+  return tokens >= 0 && rows >= 1 && (int64_t)tokens * rows < (int64_t)1 << 33;
+}
+
+rq_status rq_qk_norm_rope(const rq_qk_params* params, int dtype, const void* q, int64_t q_stride,
+                          const void* k, int64_t k_stride, const int32_t* position, void* q_out,
+                          void* k_out, int tokens, rq_stream_t stream) {
+  rq_status s = check_qk(params, position);
+  if (s != RQ_OK) return s;
+  if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr) ||
+      (q == nullptr && k == nullptr))
+    return RQ_ERR_NULL;
+  s = check_dtype(dtype);
+  if (s != RQ_OK) return s;
+  if ((q != nullptr && params->q_heads < 1) || (k != nullptr && params->kv_heads < 1) ||
+      !tokens_ok(tokens, (q ? params->q_heads : 0) + (k ? params->kv_heads : 0)))
+    return RQ_ERR_SHAPE;
+  if (q != nullptr) s = check_rows(q, q_stride, params->q_heads, params->head_dim, dtype);
+  if (s == RQ_OK && k != nullptr)
+    s = check_rows(k, k_stride, params->kv_heads, params->head_dim, dtype);
+  if (s != RQ_OK) return s;
+  if (!aligned(q_out, 16) || !aligned(k_out, 16)) return RQ_ERR_SHAPE;
+  if (tokens == 0) return RQ_OK;
+  return launch_qkv_rows(params, dtype, q, q_stride, k, k_stride, nullptr, 0, position, q_out,
+                         k_out, nullptr, nullptr, tokens, reinterpret_cast<cudaStream_t>(stream));
+}
+
+static rq_status check_store(const rq_kv_cache* cache, int dtype, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, const int64_t* slot, int tokens) {
+  rq_status s = check_cache(cache);
+  if (s != RQ_OK) return s;
+  if (k == nullptr || v == nullptr || slot == nullptr) return RQ_ERR_NULL;
+  s = check_dtype(dtype);
+  if (s != RQ_OK) return s;
+  if (!aligned(slot, 8) || !tokens_ok(tokens, 2 * cache->kv_heads)) return RQ_ERR_SHAPE;
+  s = check_rows(k, k_stride, cache->kv_heads, cache->head_dim, dtype);
+  if (s == RQ_OK) s = check_rows(v, v_stride, cache->kv_heads, cache->head_dim, dtype);
+  return s;
+}
+
+rq_status rq_qkv_to_cache(const rq_qk_params* params, int dtype, const void* q, int64_t q_stride,
+                          const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          const int32_t* position, void* q_out, const rq_kv_cache* cache,
+                          const int64_t* slot, int tokens, rq_stream_t stream) {
+  rq_status s = check_qk(params, position);
+  if (s != RQ_OK) return s;
+  s = check_store(cache, dtype, k, k_stride, v, v_stride, slot, tokens);
+  if (s != RQ_OK) return s;
+  if ((q == nullptr) != (q_out == nullptr)) return RQ_ERR_NULL;
+  if (params->kv_heads != cache->kv_heads || params->head_dim != cache->head_dim)
+    return RQ_ERR_SHAPE;
+  if (q != nullptr) {
+    if (params->q_heads < 1 || !aligned(q_out, 16) ||
+        !tokens_ok(tokens, params->q_heads + 2 * params->kv_heads))
+      return RQ_ERR_SHAPE;
+    s = check_rows(q, q_stride, params->q_heads, params->head_dim, dtype);
+    if (s != RQ_OK) return s;
+  }
+  if (tokens == 0) return RQ_OK;
+  return launch_qkv_rows(params, dtype, q, q_stride, k, k_stride, v, v_stride, position, q_out,
+                         nullptr, cache, slot, tokens, reinterpret_cast<cudaStream_t>(stream));
+}
+
+rq_status rq_kv_write(const rq_kv_cache* cache, int dtype, const void* k, int64_t k_stride,
+                      const void* v, int64_t v_stride, const int64_t* slot, int tokens,
+                      rq_stream_t stream) {
+  rq_status s = check_store(cache, dtype, k, k_stride, v, v_stride, slot, tokens);
+  if (s != RQ_OK || tokens == 0) return s;
+  return launch_qkv_rows(nullptr, dtype, nullptr, 0, k, k_stride, v, v_stride, nullptr, nullptr,
+                         nullptr, cache, slot, tokens, reinterpret_cast<cudaStream_t>(stream));
+}
+
+rq_status rq_kv_read(const rq_kv_cache* cache, int dtype, const int64_t* slot, void* k_out,
+                     void* v_out, int tokens, rq_stream_t stream) {
+  rq_status s = check_cache(cache);
+  if (s != RQ_OK) return s;
+  if (slot == nullptr || k_out == nullptr || v_out == nullptr) return RQ_ERR_NULL;
+  s = check_dtype(dtype);
+  if (s != RQ_OK) return s;
+  if (!aligned(slot, 8) || !aligned(k_out, 16) || !aligned(v_out, 16) ||
+      !tokens_ok(tokens, cache->kv_heads))
+    return RQ_ERR_SHAPE;
+  if (tokens == 0) return RQ_OK;
+  return launch_kv_read(*cache, dtype, slot, k_out, v_out, tokens,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+rq_status rq_cache_attention(rq_ctx* ctx, const rq_kv_cache* cache, int dtype, const void* q,
+                             int64_t q_stride, void* out, int batch, int new_tokens, int q_heads,
+                             const int32_t* page_table, int max_pages, const int32_t* length,
+                             const uint64_t* tree, float scale, rq_stream_t stream) {
+  if (ctx == nullptr) return RQ_ERR_NULL;
+  rq_status s = check_cache(cache);
+  if (s != RQ_OK) return s;
+  if (q == nullptr || out == nullptr || page_table == nullptr || length == nullptr)
+    return RQ_ERR_NULL;
+  s = check_dtype(dtype);
+  if (s != RQ_OK) return s;
+  if (batch < 0 || new_tokens < 1 || q_heads < 1 || q_heads % cache->kv_heads != 0 ||
+      max_pages < 1 || (tree != nullptr && new_tokens > 64) ||
+      (int64_t)new_tokens * q_heads > 0x7FFFFFFFLL || !(scale > 0.0f) || !(scale < 1e30f))
+    return RQ_ERR_SHAPE;
+  s = check_rows(q, q_stride, q_heads, cache->head_dim, dtype);
+  if (s != RQ_OK) return s;
+  if (!aligned(out, 16) || !aligned(page_table, 4) || !aligned(length, 4) || !aligned(tree, 8))
+    return RQ_ERR_SHAPE;
+  if (batch == 0) return RQ_OK;
+  const AttnCall call = {cache, dtype,     q,          q_stride,  out,    batch, new_tokens,
+                         q_heads, page_table, max_pages, length, tree, scale};
+  return launch_cache_attention(call, &ctx->attn, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------- verification of drafts --
+
+static rq_status check_verify(const int32_t* token, const float* p, const float* u,
+                              const int32_t* accepted, const int32_t* next, int batch, int drafts,
+                              int vocab) {
+  if (p == nullptr || u == nullptr || accepted == nullptr || next == nullptr ||
+      (drafts > 0 && token == nullptr))
+    return RQ_ERR_NULL;
+  if (batch < 0 || batch > (1 << 27) || drafts < 0 || vocab < 1 || vocab > (1 << 20) ||
+      !aligned(p, 4) || !aligned(u, 4) || !aligned(token, 4) || !aligned(accepted, 4) ||
+      !aligned(next, 4))
+    return RQ_ERR_SHAPE;
+  return RQ_OK;
+}
+
+rq_status rq_verify_chain(const int32_t* token, const float* p, const float* q, const float* u,
+                          int32_t* accepted, int32_t* next, int batch, int drafts, int vocab,
+                          rq_stream_t stream) {
+  const rq_status s = check_verify(token, p, u, accepted, next, batch, drafts, vocab);
+  if (s != RQ_OK) return s;
+  if (!aligned(q, 4)) return RQ_ERR_SHAPE;
+  if (batch == 0) return RQ_OK;
+  return launch_verify_chain(token, p, q, u, accepted, next, batch, drafts, vocab,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+rq_status rq_verify_tree(const int32_t* token, const int32_t* parent, const float* p,
+                         const float* u, int32_t* accepted, int32_t* next, int32_t* path,
+                         int batch, int drafts, int vocab, rq_stream_t stream) {
+  const rq_status s = check_verify(token, p, u, accepted, next, batch, drafts, vocab);
+  if (s != RQ_OK) return s;
+  if (drafts > 0 && (parent == nullptr || path == nullptr)) return RQ_ERR_NULL;
+  if (drafts > 1024 || !aligned(parent, 4) || !aligned(path, 4)) return RQ_ERR_SHAPE;
+  if (batch == 0) return RQ_OK;
+  return launch_verify_tree(token, parent, p, u, accepted, next, path, batch, drafts, vocab,
+                            reinterpret_cast<cudaStream_t>(stream));
 }
 
 rq_status rq_ctx_trace_begin(rq_ctx* ctx, int capacity) {

@@ -1214,10 +1214,19 @@ rq_status read_and_clear_device_error(cudaStream_t st) {
   if (gemv == RQ_ERR_CUDA) return gemv;
   const rq_status quant = read_and_clear_quant_error();
   if (quant == RQ_ERR_CUDA) return quant;
+  const rq_status attn = read_and_clear_attn_error();
+  if (attn == RQ_ERR_CUDA) return attn;
+  const rq_status kv = read_and_clear_kv_error();
+  if (kv == RQ_ERR_CUDA) return kv;
   unsigned int v = 0;
   if (cudaMemcpyFromSymbol(&v, g_rq_device_error, sizeof(v)) != cudaSuccess)
     return RQ_ERR_CUDA;
-  if (v == 0) return gemv != RQ_OK ? gemv : quant;
+  if (v == 0) {
+    // a timeout first, then an index
+    for (rq_status s : {gemv, quant, attn, kv})
+      if (s == RQ_ERR_TIMEOUT) return s;
+    return attn != RQ_OK ? attn : kv;
+  }
   const unsigned int zero = 0;
   if (cudaMemcpyToSymbol(g_rq_device_error, &zero, sizeof(zero)) != cudaSuccess)
     return RQ_ERR_CUDA;

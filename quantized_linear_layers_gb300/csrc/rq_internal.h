@@ -127,6 +127,58 @@ rq_status launch_fp8_gemm_group(const uint8_t* x_fp8, const float* x_deq,
                                 float* const* ys, const float* const* w_deqs, int M, int K,
                                 cudaStream_t st, bool w_early = false);
 rq_status read_and_clear_device_error(cudaStream_t st);
+
+// rq_kv.cu ------------------------------------------------------------------
+// Norm (p's weights, if any) and rotation of q and k rows; k and v rows into
+// the cache at `slot`, or k rows to k_out when cache is null.  p null: no
+// norm, no rotation, no q.  q, k or v null: that side is left out.
+rq_status launch_qkv_rows(const rq_qk_params* p, int dtype, const void* q, int64_t q_stride,
+                          const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          const int32_t* position, void* q_out, void* k_out,
+                          const rq_kv_cache* cache, const int64_t* slot, int tokens,
+                          cudaStream_t st);
+rq_status launch_kv_read(const rq_kv_cache& cache, int dtype, const int64_t* slot, void* k_out,
+                         void* v_out, int tokens, cudaStream_t st);
+// Read and clear the cache kernels' device error word (after a sync).
+rq_status read_and_clear_kv_error();
+
+// rq_attn.cu ----------------------------------------------------------------
+struct AttnCall {
+  const rq_kv_cache* cache;
+  int dtype;
+  const void* q;
+  int64_t q_stride;
+  void* out;
+  int batch, new_tokens, q_heads;
+  const int32_t* page_table;
+  int max_pages;
+  const int32_t* length;
+  const uint64_t* tree;
+  float scale;
+};
+// Scratch of split sequences: partial rows, and one arrival counter per
+// segment, at zero between launches.  Used on one stream at a time.
+struct AttnScratch {
+  float* part = nullptr;
+  size_t part_cap = 0;
+  unsigned int* counter = nullptr;
+  size_t counter_cap = 0;
+  rq_status reserve(size_t part_bytes, size_t counters, cudaStream_t st);
+  void release();
+};
+rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cudaStream_t st);
+// Read and clear the attention kernels' device error word (after a sync).
+rq_status read_and_clear_attn_error();
+
+// rq_verify.cu --------------------------------------------------------------
+rq_status launch_verify_chain(const int32_t* token, const float* p, const float* q,
+                              const float* u, int32_t* accepted, int32_t* next, int batch,
+                              int drafts, int vocab, cudaStream_t st);
+rq_status launch_verify_tree(const int32_t* token, const int32_t* parent, const float* p,
+                             const float* u, int32_t* accepted, int32_t* next, int32_t* path,
+                             int batch, int drafts, int vocab, cudaStream_t st);
+
+// rq_gemm.cu ----------------------------------------------------------------
 rq_status launch_debug_wait_timeout(int64_t limit_ns, cudaStream_t st);
 
 }  // namespace rq

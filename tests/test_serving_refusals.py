@@ -1,0 +1,179 @@
+"""The cache, attention and verification entry points refuse bad arguments on
+the host, before anything is launched (CPU only)."""
+import ctypes
+
+import pytest
+
+A = 0x10000          # aligned fake address: never dereferenced
+NULL = None
+
+
+@pytest.fixture(scope="module")
+def rq():
+    import __graft_entry__
+    __graft_entry__.build()
+    import quantized_linear_layers_gb300 as rq
+    return rq
+
+
+def cache(rq, **over):
+    f = dict(k=A, v=A, k_scale=A, v_scale=A, pages=4, page_size=64, kv_heads=4, head_dim=128,
+             format=0)
+    f.update(over)
+    return ctypes.byref(rq._KVCacheStruct(**f))
+
+
+def params(rq, **over):
+    f = dict(q_weight=A, k_weight=A, cos_table=A, sin_table=A, positions=16, q_heads=28,
+             kv_heads=4, head_dim=128, rotary_dim=128, interleaved=0, eps=1e-6)
+    f.update(over)
+    return ctypes.byref(rq._QKParamsStruct(**f))
+
+
+BAD_CACHE = [(dict(k=None), 1), (dict(v=None), 1), (dict(k_scale=None), 1),
+             (dict(v_scale=None), 1), (dict(format=2), 3), (dict(format=-1), 3),
+             (dict(page_size=0), 2), (dict(page_size=48), 2), (dict(page_size=8), 2),
+             (dict(page_size=512), 2), (dict(head_dim=96), 2), (dict(head_dim=0), 2),
+             (dict(kv_heads=0), 2), (dict(pages=0), 2), (dict(pages=1 << 30), 2),
+             (dict(k=A + 8), 2), (dict(v=A + 1), 2), (dict(k_scale=A + 4), 2),
+             (dict(v_scale=A + 8), 2)]
+
+
+@pytest.mark.parametrize("over,status", BAD_CACHE)
+def test_bad_caches(rq, over, status):
+    lib, c = rq.lib(), cache(rq, **over)
+    assert lib.rq_kv_write(c, 0, A, 512, A, 512, A, 1, NULL) == status
+    assert lib.rq_kv_read(c, 0, A, A, A, 1, NULL) == status
+    assert lib.rq_qkv_to_cache(params(rq), 0, A, 3584, A, 512, A, 512, A, A, c, A, 1,
+                               NULL) == status
+    assert lib.rq_cache_attention(ctypes.c_void_p(A), c, 0, A, 3584, A, 1, 1, 28, A, 4, A, NULL,
+                                  0.1, NULL) == status
+
+
+def test_null_cache_and_params(rq):
+    lib = rq.lib()
+    assert lib.rq_kv_write(NULL, 0, A, 512, A, 512, A, 1, NULL) == 1
+    assert lib.rq_kv_read(NULL, 0, A, A, A, 1, NULL) == 1
+    assert lib.rq_qkv_to_cache(NULL, 0, A, 3584, A, 512, A, 512, A, A, cache(rq), A, 1, NULL) == 1
+    assert lib.rq_qk_norm_rope(NULL, 0, A, 3584, A, 512, A, A, A, 1, NULL) == 1
+    assert lib.rq_cache_attention(NULL, cache(rq), 0, A, 3584, A, 1, 1, 28, A, 4, A, NULL, 0.1,
+                                  NULL) == 1
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(head_dim=80), 2), (dict(rotary_dim=136), 2), (dict(rotary_dim=24), 2),
+    (dict(rotary_dim=-16), 2), (dict(cos_table=None), 1), (dict(sin_table=None), 1),
+    (dict(positions=0), 2), (dict(cos_table=A + 4), 2), (dict(q_weight=A + 4), 2),
+    (dict(k_weight=A + 8), 2), (dict(eps=-1.0), 2), (dict(eps=float("nan")), 2),
+    (dict(q_heads=0), 2), (dict(kv_heads=0), 2)])
+def test_bad_params(rq, over, status):
+    lib, p = rq.lib(), params(rq, **over)
+    assert lib.rq_qk_norm_rope(p, 0, A, 1 << 16, A, 1 << 16, A, A, A, 1, NULL) == status
+    assert lib.rq_qkv_to_cache(p, 0, A, 1 << 16, A, 1 << 16, A, 1 << 16, A, A, cache(rq), A, 1,
+                               NULL) == status
+
+
+def test_bad_rows(rq):
+    lib, p, c = rq.lib(), params(rq), cache(rq)
+    nr = lib.rq_qk_norm_rope
+    assert nr(p, 0, A, 3584, A, 512, NULL, A, A, 1, NULL) == 1        # positions wanted
+    assert nr(p, 0, A, 3584, A, 512, A, NULL, A, 1, NULL) == 1        # q without its output
+    assert nr(p, 0, NULL, 0, A, 512, A, A, A, 1, NULL) == 1
+    assert nr(p, 0, NULL, 0, NULL, 0, A, NULL, NULL, 1, NULL) == 1    # nothing to do
+    assert nr(p, 3, A, 3584, A, 512, A, A, A, 1, NULL) == 3           # dtype
+    assert nr(p, 0, A + 4, 3584, A, 512, A, A, A, 1, NULL) == 2
+    assert nr(p, 0, A, 3583, A, 512, A, A, A, 1, NULL) == 2           # heads overlap
+    assert nr(p, 0, A, 3586, A, 512, A, A, A, 1, NULL) == 2           # stride not 16 bytes
+    assert nr(p, 1, A, 3588, A, 512, A, A, A, 1, NULL) == 2
+    assert nr(p, 0, A, 3584, A, 511, A, A, A, 1, NULL) == 2
+    assert nr(p, 0, A, 3584, A, 512, A + 2, A, A, 1, NULL) == 2
+    assert nr(p, 0, A, 3584, A, 512, A, A + 8, A, 1, NULL) == 2
+    assert nr(p, 0, A, 3584, A, 512, A, A, A, -1, NULL) == 2
+    assert nr(p, 0, A, 3584, A, 512, A, A, A, 0, NULL) == 0           # nothing to do
+    tc = lib.rq_qkv_to_cache
+    assert tc(p, 0, A, 3584, A, 512, NULL, 512, A, A, c, A, 1, NULL) == 1
+    assert tc(p, 0, A, 3584, A, 512, A, 512, A, A, c, NULL, 1, NULL) == 1
+    assert tc(p, 0, A, 3584, A, 512, A, 512, A, NULL, c, A, 1, NULL) == 1
+    assert tc(p, 0, A, 3584, A, 512, A, 512, A, A, c, A + 4, 1, NULL) == 2
+    assert tc(p, 0, A, 3584, A, 512, A, 512, A, A, cache(rq, kv_heads=2), A, 1, NULL) == 2
+    assert tc(p, 0, A, 3584, A, 512, A, 512, A, A, cache(rq, head_dim=64), A, 1, NULL) == 2
+    assert tc(p, 0, A, 3584, A, 512, A, 512, A, A, c, A, 0, NULL) == 0
+    kw = lib.rq_kv_write
+    assert kw(c, 7, A, 512, A, 512, A, 1, NULL) == 3
+    assert kw(c, 0, NULL, 512, A, 512, A, 1, NULL) == 1
+    assert kw(c, 0, A, 512, A, 508, A, 1, NULL) == 2
+    assert kw(c, 0, A, 512, A + 4, 512, A, 1, NULL) == 2
+    assert kw(c, 0, A, 512, A, 512, A, 0, NULL) == 0
+    kr = lib.rq_kv_read
+    assert kr(c, 0, NULL, A, A, 1, NULL) == 1
+    assert kr(c, 0, A, NULL, A, 1, NULL) == 1
+    assert kr(c, 5, A, A, A, 1, NULL) == 3
+    assert kr(c, 0, A, A + 8, A, 1, NULL) == 2
+    assert kr(c, 0, A, A, A, 0, NULL) == 0
+
+
+def test_bad_attention(rq):
+    lib, c = rq.lib(), cache(rq)
+    ctx = ctypes.c_void_p(A)        # not dereferenced: the checks come first
+
+    def call(dtype=0, q=A, stride=3584, out=A, batch=1, new=1, heads=28, table=A, pages=4,
+             length=A, tree=NULL, scale=0.1):
+        return lib.rq_cache_attention(ctx, c, dtype, q, stride, out, batch, new, heads, table,
+                                      pages, length, tree, scale, NULL)
+
+    for name in ("q", "out", "table", "length"):
+        assert call(**{name: NULL}) == 1
+    assert call(dtype=3) == 3
+    for over in (dict(batch=-1), dict(new=0), dict(heads=0), dict(heads=30, stride=3840),
+                 dict(pages=0), dict(tree=A, new=65), dict(scale=0.0), dict(scale=-1.0),
+                 dict(scale=float("nan")), dict(scale=float("inf")), dict(q=A + 4),
+                 dict(stride=3580), dict(stride=3586), dict(out=A + 8), dict(table=A + 2),
+                 dict(length=A + 1), dict(tree=A + 4)):
+        assert call(**over) == 2, over
+    assert call(batch=0) == 0
+
+
+def test_bad_verification(rq):
+    lib = rq.lib()
+    chain, tree = lib.rq_verify_chain, lib.rq_verify_tree
+    assert chain(NULL, A, A, A, A, A, 1, 1, 10, NULL) == 1
+    assert chain(A, NULL, A, A, A, A, 1, 1, 10, NULL) == 1
+    assert chain(A, A, A, NULL, A, A, 1, 1, 10, NULL) == 1
+    assert chain(A, A, A, A, NULL, A, 1, 1, 10, NULL) == 1
+    assert chain(A, A, A, A, A, NULL, 1, 1, 10, NULL) == 1
+    for b, n, v in ((-1, 1, 10), (1, -1, 10), (1, 1, 0), (1, 1, (1 << 20) + 1)):
+        assert chain(A, A, A, A, A, A, b, n, v, NULL) == 2
+        assert tree(A, A, A, A, A, A, A, b, n, v, NULL) == 2
+    assert chain(A, A + 2, A, A, A, A, 1, 1, 10, NULL) == 2
+    assert chain(A, A, A + 1, A, A, A, 1, 1, 10, NULL) == 2
+    assert chain(A, A, A, A, A, A, 0, 1, 10, NULL) == 0
+    assert tree(A, NULL, A, A, A, A, A, 1, 1, 10, NULL) == 1
+    assert tree(A, A, A, A, A, A, NULL, 1, 1, 10, NULL) == 1
+    assert tree(A, A, A, A, A, A, A, 1, 1025, 10, NULL) == 2
+    assert tree(A, A + 2, A, A, A, A, A, 1, 1, 10, NULL) == 2
+    assert tree(A, A, A, A, A, A, A, 0, 1, 10, NULL) == 0
+
+
+def test_binding_refuses_tensors_that_are_not_rows(rq):
+    import torch
+    x = torch.zeros(6, 8, 64)
+    assert rq._row_stride(x, 8, 64, None, "x") == 512
+    assert rq._row_stride(x[::2], 8, 64, None, "x") == 1024
+    assert rq._row_stride(x[:, 2:4], 2, 64, None, "x") == 512
+    assert rq._row_stride(x[:1], 8, 64, None, "x") == 512
+    assert rq._row_stride(x.view(6, 512), 8, 64, None, "x") == 512
+    assert rq._row_stride(x.view(2, 3, 8, 64)[:, :, :2], 2, 64, None, "x") == 512
+    for bad in (x.transpose(0, 1), x[..., ::2], x.view(2, 3, 8, 64)[:, :2], x[:, ::2]):
+        with pytest.raises(rq.RqError):
+            rq._row_stride(bad, bad.shape[-2], 64, None, "x")
+    k = torch.zeros(2, 4, 16, 64, dtype=torch.int8)
+    s = torch.zeros(2, 4, 16)
+    rq.KVCache.from_tensors(k, k, s, s, format=rq.RQ_KV_I8)
+    for args in ((k.transpose(1, 2), k, s, s), (k, k[:1], s, s), (k, k, s[..., :8], s),
+                 (k, k, s, s.half()), (k.float(), k, s, s)):
+        with pytest.raises(rq.RqError):
+            rq.KVCache.from_tensors(*args, format=rq.RQ_KV_I8)
+    with pytest.raises(rq.RqError):
+        rq.QKParams(2, 1, 64, q_weight=torch.ones(32))
+    with pytest.raises(rq.RqError):
+        rq.QKParams(2, 1, 64, cos=torch.ones(8, 32), sin=torch.ones(8, 16))

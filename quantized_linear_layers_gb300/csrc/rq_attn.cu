@@ -25,10 +25,10 @@ namespace {
 // bit 0: a pipeline wait ran out; bit 1: an index outside its array
 __device__ unsigned int g_attn_error = 0;
 
-constexpr int kTile = 64;            // keys per pipeline stage
-constexpr int kWarps = 4;            // consumer warps, 16 keys of a tile each
-constexpr int kAttnThreads = (kWarps + 1) * 32;
-constexpr int kMaxItems = 2048;
+constexpr int kKeys = 16;            // keys of a unit: one warp's step
+constexpr int kRows = 8;             // query rows of a segment
+constexpr int kMaxItems = 1024;
+constexpr int kJoin = 8;             // partials joined at once
 
 struct AttnArgs {
   const void* q;
@@ -38,7 +38,7 @@ struct AttnArgs {
   const int32_t *table, *length;
   const unsigned long long* tree;
   int batch, new_tokens, q_heads, kv_heads, group, rows, row_tiles;
-  int max_pages, lg_page, lg_box;
+  int max_pages, lg_page;
   int64_t pages;
   float scale_log2;
   int dtype;
@@ -50,25 +50,31 @@ struct AttnArgs {
 
 template <int D>
 struct Geometry {
-  static constexpr int kPanel = D < 128 ? D : 128;     // bytes of a row in one swizzled panel
+  static constexpr int kPanel = D < 128 ? D : 128;  // bytes of a row in one swizzled panel
   static constexpr int kPanels = D / kPanel;
-  static constexpr int kBytes = kTile * D;              // codes of K (or V) in a stage
-  static constexpr int kStage = 2 * kBytes + 2 * kTile * 4;
-  static constexpr int kStages = D == 64 ? 8 : D == 128 ? 4 : 3;
-  static constexpr int kStageAlign = (kStage + 1023) / 1024 * 1024;
+  static constexpr int kBytes = kKeys * D;          // codes of K (or V) in a unit
+  // as many warps as the registers of an SM hold: the output rows alone are
+  // D / 2 registers a thread, the query rows D / 4
+  static constexpr int kWarps = D == 64 ? 16 : D == 128 ? 12 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kStages = D == 256 ? 2 : 3;  // units in flight per warp
+  static constexpr int kRing = kWarps * kStages * 2 * kBytes;
 };
 
-// Shared memory after the stages.
-template <int D, int ROWS>
+// Shared memory after the ring.
+template <int D>
 struct Tail {
-  static constexpr int kPitch = D + 4;
-  float o[kWarps][ROWS][kPitch];
-  float m[kWarps][ROWS], l[kWarps][ROWS];
-  float c[ROWS];
-  uint64_t full[8], empty[8];
+  static constexpr int kWarps = Geometry<D>::kWarps;
+  static constexpr int kStages = Geometry<D>::kStages;
+  float scale[kWarps][kStages][2][kKeys];  // ks, vs of the units in flight
+  float o[kWarps][kRows][D + 4];
+  float m[kWarps][kRows], l[kWarps][kRows];
+  float c[kRows];
+  uint64_t full[kWarps][kStages];
   int flag;
-  int total;  // tiles of one kv head over all items
-  int item_start[kMaxItems + 1];
+  int warp_sum[kWarps];
+  int item_start[kMaxItems + 1];  // units before each item, for one kv head
+  int item_places[kMaxItems];     // places its rows may see
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -111,27 +117,45 @@ __device__ __forceinline__ uint32_t split_half2(float a, float b, uint32_t& lo) 
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Four codes of a word as two f16 pairs: (byte 0, byte 2) and (byte 1, byte 3).
-// E4M3 codes keep their bits at f16's places, sign | 4 exponent bits | 3
-// mantissa bits, which is the code's value times 2^-8 (exponent bias 15 - 7;
-// its subnormals are f16 subnormals).  8-bit integers, biased by 128, become
-// the low mantissa bits of 1024 + b, from which 1152 is subtracted: exact.
+// Codes as f16 pairs, exactly.  E4M3 has a conversion; 8-bit integers, biased
+// by 128, become the low mantissa bits of 1024 + b, less 1152.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)two));
+  return h;
+}
+
+__device__ __forceinline__ uint32_t minus_1152(uint32_t h) {
+  const uint32_t bias = 0x64806480u;
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h),
+                            *reinterpret_cast<const __half2*>(&bias));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Bytes (0, 1) and (2, 3) of a word.
 template <bool I8>
-__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& even, uint32_t& odd) {
-  if constexpr (!I8) {
-    even = ((w << 8) & 0x80008000u) | ((w << 7) & 0x3F803F80u);
-    odd = (w & 0x80008000u) | ((w >> 1) & 0x3F803F80u);
-  } else {
+__device__ __forceinline__ void codes_in_order(uint32_t w, uint32_t& a, uint32_t& b) {
+  if constexpr (I8) {
     const uint32_t u = w ^ 0x80808080u;
-    const uint32_t e = (u & 0x00FF00FFu) | 0x64006400u;
-    const uint32_t o = ((u >> 8) & 0x00FF00FFu) | 0x64006400u;
-    const uint32_t bias = 0x64806480u;  // 1152
-    const __half2 eh = __hsub2(*reinterpret_cast<const __half2*>(&e),
-                               *reinterpret_cast<const __half2*>(&bias));
-    const __half2 oh = __hsub2(*reinterpret_cast<const __half2*>(&o),
-                               *reinterpret_cast<const __half2*>(&bias));
-    even = *reinterpret_cast<const uint32_t*>(&eh);
-    odd = *reinterpret_cast<const uint32_t*>(&oh);
+    a = minus_1152(__byte_perm(u, 0x64646464u, 0x4140));
+    b = minus_1152(__byte_perm(u, 0x64646464u, 0x4342));
+  } else {
+    a = e4m3_pair(w & 0xFFFFu);
+    b = e4m3_pair(w >> 16);
+  }
+}
+
+// Bytes (0, 2) and (1, 3).
+template <bool I8>
+__device__ __forceinline__ void codes_across(uint32_t w, uint32_t& a, uint32_t& b) {
+  if constexpr (I8) {
+    const uint32_t u = w ^ 0x80808080u;
+    a = minus_1152(__byte_perm(u, 0x64646464u, 0x4240));
+    b = minus_1152(__byte_perm(u, 0x64646464u, 0x4341));
+  } else {
+    const uint32_t x = e4m3_pair(w & 0xFFFFu), y = e4m3_pair(w >> 16);
+    a = __byte_perm(x, y, 0x5410);
+    b = __byte_perm(x, y, 0x7632);
   }
 }
 
@@ -152,8 +176,22 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
-__device__ __forceinline__ void consumer_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+// (v, mx, sum) joined with another partial row: its output piece, and its
+// maximum and sum.
+__device__ __forceinline__ void merge(float4& v, float& mx, float& sum, const float4& ov,
+                                      const float2& ml, float c) {
+  const float mn = fmaxf(mx, ml.x);
+  if (mn == -INFINITY) {
+    sum += ml.y;  // 0, or the NaN of a row whose scores all are
+    return;
+  }
+  const float f0 = ex2((mx - mn) * c), f1 = ex2((ml.x - mn) * c);
+  v.x = v.x * f0 + ov.x * f1;
+  v.y = v.y * f0 + ov.y * f1;
+  v.z = v.z * f0 + ov.z * f1;
+  v.w = v.w * f0 + ov.w * f1;
+  sum = sum * f0 + ml.y * f1;
+  mx = mn;
 }
 
 // Places of a sequence that its new tokens may see, over all row tiles; 0 for
@@ -167,19 +205,20 @@ __device__ __forceinline__ int64_t places(const AttnArgs& a, int b, int64_t* len
   const int64_t most = (int64_t)a.max_pages << a.lg_page;
   int64_t kv = n + a.new_tokens;
   if (kv > most) {
-    if (threadIdx.x == 0) atomicOr(&g_attn_error, 2u);
+    atomicOr(&g_attn_error, 2u);
     kv = most;
   }
   *len = n < kv ? n : kv;
   return kv;
 }
 
-// Last place + 1 that row tile rt may see.
-template <int ROWS>
+// Last place + 1 that row tile rt may see.  Up to 64 new tokens every tile
+// takes them all: a chain is then cut as a tree of one branch is, and gives
+// its bits.
 __device__ __forceinline__ int64_t tile_places(const AttnArgs& a, int rt, int64_t len,
                                                int64_t kv) {
-  if (a.tree != nullptr || kv == 0) return kv;
-  int last = (rt + 1) * ROWS;
+  if (a.new_tokens <= 64 || kv == 0) return kv;
+  int last = (rt + 1) * kRows;
   last = (last < a.rows ? last : a.rows) - 1;
   const int64_t end = len + last / a.group + 1;
   return end < kv ? end : kv;
@@ -188,53 +227,49 @@ __device__ __forceinline__ int64_t tile_places(const AttnArgs& a, int rt, int64_
 // ------------------------------------------------------------ the kernel --
 //
 // Work is the sequence of segments (sequence, row tile, kv head), each a run
-// of 64-key tiles, laid end to end; CTA c of C takes an equal run of it, so
+// of 16-key units, laid end to end; CTA c of C takes an equal run of it, so
 // that ragged lengths load the SMs evenly and a single long sequence spreads
 // over all of them.  A segment cut between CTAs is joined by the last of them
 // to finish, in CTA order, from partial (max, sum, output) rows in scratch.
 //
-// Within a CTA a producer thread keeps a ring of tiles in flight by TMA, and
-// four warps each take 16 keys of every tile with a softmax of their own (no
-// exchange inside the loop); their results are joined when the segment ends.
-// A warp's tile of 16 rows holds ROWS = 16 rows of 16-bit activations, or 8
-// rows of f32 as high parts (rows 0-7) and low parts (8-15).
-template <int D, bool I8, bool F32>
-__global__ void __launch_bounds__(kAttnThreads)
+// Within a CTA the warps take units in turn, each with its own ring of units
+// in flight (TMA, refilled by the warp itself, on into the next segment) and
+// a softmax of its own, so that nothing is exchanged inside the loop; their
+// results are joined when the segment ends.  A warp's 16-row tile holds the
+// high f16 parts of 8 query rows and below them their low parts: an f32 row
+// costs no product more than an f16 one would.
+template <int D, bool I8>
+__global__ void __launch_bounds__(Geometry<D>::kThreads, 1)
 attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
             const AttnArgs a) {
-  constexpr int ROWS = F32 ? 8 : 16;
   using G = Geometry<D>;
-  using TailT = Tail<D, ROWS>;
-  constexpr int S = G::kStages;
+  using TailT = Tail<D>;
+  constexpr int W = G::kWarps, S = G::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  TailT& tail = *reinterpret_cast<TailT*>(smem + S * G::kStageAlign);
+  TailT& tail = *reinterpret_cast<TailT*>(smem + G::kRing);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t smem_base = smem_u32(smem);
+  const uint32_t ring = smem_u32(smem) + warp * (S * 2 * G::kBytes);
 
-  if (tid == 0) {
-    for (int i = 0; i < S; ++i) {
-      mbar_init(smem_u32(&tail.full[i]), 1);
-      mbar_init(smem_u32(&tail.empty[i]), kWarps);
-    }
-    mbar_fence_init();
-  }
+  if (lane == 0)
+    for (int i = 0; i < S; ++i) mbar_init(smem_u32(&tail.full[warp][i]), 1);
+  mbar_fence_init();
   pdl_wait();
   pdl_trigger();
 
   const int items = a.batch * a.row_tiles;
-  int64_t u0, u1;  // this CTA's run of tiles
-  int64_t units = 0;
+  int64_t u0 = 0, u1 = 1, units = 1;  // this CTA's run of units
   int ctas = (int)gridDim.x;
   if (!a.direct) {
-    // tiles before each item (sequence, row tile), for one kv head
     int carry = 0;
-    for (int base = 0; base < items; base += kAttnThreads) {
+    for (int base = 0; base < items; base += G::kThreads) {
       const int i = base + tid;
       int n = 0;
       if (i < items) {
         int64_t len;
         const int64_t kv = places(a, i / a.row_tiles, &len);
-        n = (int)((tile_places<ROWS>(a, i % a.row_tiles, len, kv) + kTile - 1) / kTile);
+        const int64_t mine = tile_places(a, i % a.row_tiles, len, kv);
+        tail.item_places[i] = (int)mine;
+        n = (int)((mine + kKeys - 1) / kKeys);
         if (n < 1) n = 1;
       }
       int scan = n;
@@ -244,11 +279,11 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
         if (lane >= o) scan += x;
       }
       __syncthreads();
-      if (lane == 31) reinterpret_cast<int*>(tail.o)[warp] = scan;
+      if (lane == 31) tail.warp_sum[warp] = scan;
       __syncthreads();
       int before = carry;
-      for (int w = 0; w <= kWarps; ++w) {
-        const int x = reinterpret_cast<int*>(tail.o)[w];
+      for (int w = 0; w < W; ++w) {
+        const int x = tail.warp_sum[w];
         if (w < warp) before += x;
         carry += x;
       }
@@ -256,24 +291,46 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
     }
     if (tid == 0) tail.item_start[items] = carry;
     units = (int64_t)carry * a.kv_heads;
-    // no CTA below two tiles: joining costs more than it saves there
-    if (ctas > (units + 1) / 2) ctas = (int)((units + 1) / 2);
+    // no CTA below one unit per warp
+    if (ctas > (units + W - 1) / W) ctas = (int)((units + W - 1) / W);
     u0 = (int)blockIdx.x < ctas ? units * blockIdx.x / ctas : 0;
     u1 = (int)blockIdx.x < ctas ? units * (blockIdx.x + 1) / ctas : 0;
-  } else {
-    u0 = 0;
-    u1 = 1;
   }
   __syncthreads();
   if (u0 >= u1) return;
 
-  // the first segment: item, head and first tile
-  int item, head;
-  int64_t tile0;
+  // A segment's part in this run: units [first, end) of it.
+  struct Segment {
+    int item, head, first, end, kv;
+    int64_t left;  // units of the run after it
+  };
+  auto open = [&](Segment& g) {  // item, head, first and left (from `first` on) are set
+    if (a.direct) {
+      int64_t len;
+      const int64_t kv = places(a, g.item / a.row_tiles, &len);
+      g.kv = (int)tile_places(a, g.item % a.row_tiles, len, kv);
+      g.end = g.kv < 1 ? 1 : (g.kv + kKeys - 1) / kKeys;
+      g.left = 0;
+    } else {
+      g.kv = tail.item_places[g.item];
+      const int n = tail.item_start[g.item + 1] - tail.item_start[g.item];
+      g.end = g.left < n - g.first ? g.first + (int)g.left : n;
+      g.left -= g.end - g.first;
+    }
+  };
+  auto next = [&](Segment& g) {
+    if (++g.head == a.kv_heads) {
+      g.head = 0;
+      ++g.item;
+    }
+    g.first = 0;
+    open(g);
+  };
+  Segment seg;
   if (a.direct) {
-    item = (int)(blockIdx.x % (unsigned)items);
-    head = (int)(blockIdx.x / (unsigned)items);
-    tile0 = 0;
+    seg.item = (int)(blockIdx.x % (unsigned)items);
+    seg.head = (int)(blockIdx.x / (unsigned)items);
+    seg.first = 0;
   } else {
     int lo = 0, hi = items - 1;
     while (lo < hi) {
@@ -283,487 +340,434 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
       else
         hi = mid - 1;
     }
-    item = lo;
-    const int n = tail.item_start[item + 1] - tail.item_start[item];
-    const int64_t rest = u0 - (int64_t)tail.item_start[item] * a.kv_heads;
-    head = (int)(rest / n);
-    tile0 = rest - (int64_t)head * n;
+    const int n = tail.item_start[lo + 1] - tail.item_start[lo];
+    const int64_t rest = u0 - (int64_t)tail.item_start[lo] * a.kv_heads;
+    seg.item = lo;
+    seg.head = (int)(rest / n);
+    seg.first = (int)(rest - (int64_t)seg.head * n);
   }
+  seg.left = u1 - u0;
+  open(seg);
 
-  int stage = 0;
-  uint32_t phase = 0;
-  int64_t at = u0;  // position in the run
-  bool ok = true;
-  int seg = 0;
-
-  while (at < u1) {
-    const int b = item / a.row_tiles, rt = item % a.row_tiles;
-    int64_t len;
-    const int64_t kv_all = places(a, b, &len);
-    const int64_t kv = tile_places<ROWS>(a, rt, len, kv_all);
-    int64_t n = (kv + kTile - 1) / kTile;
-    if (n < 1) n = 1;
-    int64_t tile1 = n;
-    if (a.direct)
-      at = u1;
-    else {
-      if (tile0 + (u1 - at) < tile1) tile1 = tile0 + (u1 - at);
-      at += tile1 - tile0;
+  // -------- the warp's loads, S units ahead of its products
+  Segment ld = seg;
+  int unit = ld.first + warp;  // next unit to load
+  int window = -1, pages_of = 0;  // lane i: page of unit window + i W
+  bool more = true;
+  int issued = 0;  // units loaded so far
+  auto page_window = [&](int from) {
+    window = from;
+    const int64_t u = from + (int64_t)lane * W;
+    pages_of = 0;
+    if (u < ld.end && u * kKeys < ld.kv) {
+      const int64_t page = a.table[(int64_t)(ld.item / a.row_tiles) * a.max_pages +
+                                   ((u * kKeys) >> a.lg_page)];
+      if (page >= 0 && page < a.pages)
+        pages_of = (int)page;
+      else
+        atomicOr(&g_attn_error, 2u);
     }
+  };
+  auto load_one = [&]() {  // loads the warp's next unit, if there is one
+    while (more && unit >= ld.end) {
+      if (ld.left > 0) {
+        next(ld);
+        unit = warp;
+        window = -1;
+      } else {
+        more = false;
+      }
+    }
+    if (!more) return;
+    if (window < 0 || unit >= window + 32 * W) page_window(unit);
+    const int page = __shfl_sync(0xFFFFFFFFu, pages_of, (unit - window) / W);
+    const int st = issued % S;
+    if (lane == 0) {
+      const uint32_t bar = smem_u32(&tail.full[warp][st]);
+      if (unit * kKeys >= ld.kv) {
+        mbar_arrive(bar);  // an unused sequence: nothing to load
+      } else {
+        const int off = (unit * kKeys) & ((1 << a.lg_page) - 1);
+        const int plane = page * a.kv_heads + ld.head;
+        const int64_t row = ((int64_t)plane << a.lg_page) + off;
+        const uint32_t kd = ring + st * (2 * G::kBytes), vd = kd + G::kBytes;
+        const uint32_t sd = smem_u32(&tail.scale[warp][st][0][0]);
+        mbar_arrive_expect_tx(bar, 2 * G::kBytes + 2 * kKeys * 4);
+#pragma unroll
+        for (int h = 0; h < G::kPanels; ++h) {
+          tma_rows(kd + h * kKeys * G::kPanel, &map_k, h * G::kPanel, off, plane, bar);
+          tma_rows(vd + h * kKeys * G::kPanel, &map_v, h * G::kPanel, off, plane, bar);
+        }
+        bulk_g2s(sd, a.ks + row, kKeys * 4, bar);
+        bulk_g2s(sd + kKeys * 4, a.vs + row, kKeys * 4, bar);
+      }
+    }
+    ++issued;
+    unit += W;
+  };
+  for (int i = 0; i < S; ++i) load_one();
 
-    if (warp == kWarps) {
-      // ---------------------------------------------------- producer ----
-      if (lane == 0 && ok) {
-        const int box = 1 << a.lg_box;
-        for (int64_t t = tile0; t < tile1; ++t) {
-          ok = mbar_wait(smem_u32(&tail.empty[stage]), phase ^ 1u, a.wait_limit_ns, &g_attn_error);
-          if (!ok) break;
-          const int64_t p0 = t * kTile;
-          const uint32_t bar = smem_u32(&tail.full[stage]);
-          const uint32_t kd = smem_base + stage * G::kStageAlign;
-          const uint32_t vd = kd + G::kBytes, sd = vd + G::kBytes;
-          int64_t left = kv - p0;
-          if (left > kTile) left = kTile;
-          const int boxes = left > 0 ? (int)((left + box - 1) >> a.lg_box) : 0;
-          mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * (2 * D + 8)));
-          for (int i = 0; i < boxes; ++i) {
-            const int64_t p = p0 + i * box;
-            int64_t page = a.table[(int64_t)b * a.max_pages + (p >> a.lg_page)];
-            if (page < 0 || page >= a.pages) {
-              atomicOr(&g_attn_error, 2u);
-              page = 0;
-            }
-            const int off = (int)(p & ((1 << a.lg_page) - 1));
-            const int plane = (int)(page * a.kv_heads + head);
-            const int64_t row = ((int64_t)plane << a.lg_page) + off;
-#pragma unroll
-            for (int h = 0; h < G::kPanels; ++h) {
-              const uint32_t to = h * kTile * G::kPanel + i * box * G::kPanel;
-              tma_rows(kd + to, &map_k, h * G::kPanel, off, plane, bar);
-              tma_rows(vd + to, &map_v, h * G::kPanel, off, plane, bar);
-            }
-            bulk_g2s(sd + i * box * 4, a.ks + row, (uint32_t)(box * 4), bar);
-            bulk_g2s(sd + kTile * 4 + i * box * 4, a.vs + row, (uint32_t)(box * 4), bar);
-          }
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-      }
-    } else {
-      // --------------------------------------------------- consumers ----
-      const int g = lane >> 2, t4 = lane & 3;
-      // rows of this thread's accumulators: g (and g + 8 when 16 rows)
-      constexpr int NR = F32 ? 1 : 2;
-      int tok[NR];
-      unsigned long long bits[NR];
-      float c[NR];  // 2^x per unit of the raw score x = acc * ks
-      uint32_t qa[D / 16][4];
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const int row = rt * ROWS + g + 8 * r;
-        const bool live = row < a.rows;
-        tok[r] = live ? row / a.group : 0;
-        bits[r] = 0;
-        if (live && a.tree != nullptr) bits[r] = a.tree[(int64_t)b * a.new_tokens + tok[r]];
-        const int64_t off = ((int64_t)b * a.new_tokens + tok[r]) * a.q_stride +
-                            (int64_t)(head * a.group + (live ? row % a.group : 0)) * D;
-        float x[D / 16][4];
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int64_t e = off + 16 * i + 4 * t4;
-          if (F32) {
-            const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + e);
-            x[i][0] = v.x;
-            x[i][1] = v.y;
-            x[i][2] = v.z;
-            x[i][3] = v.w;
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + e);
-            if (a.dtype == RQ_F16) {
-              const float2 f0 = half_pair(v.x), f1 = half_pair(v.y);
-              x[i][0] = f0.x;
-              x[i][1] = f0.y;
-              x[i][2] = f1.x;
-              x[i][3] = f1.y;
-            } else {
-              x[i][0] = __uint_as_float(v.x << 16);
-              x[i][1] = __uint_as_float(v.x & 0xFFFF0000u);
-              x[i][2] = __uint_as_float(v.y << 16);
-              x[i][3] = __uint_as_float(v.y & 0xFFFF0000u);
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (!live) x[i][k] = 0.0f;
-            top = fmaxf(top, fabsf(x[i][k]));
-          }
-        }
-        // the row times a power of two, so that its f16 parts lie well inside
-        // f16's range: largest entry in [2^13, 2^14)
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        int e = 0;
-        if (top > 0.0f && top <= 3.4e38f) {
-          e = 13 - (int)((__float_as_uint(top) >> 23) & 0xFFu) + 127;
-          e = e < -126 ? -126 : e > 100 ? 100 : e;
-        }
-        const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-        c[r] = fmaxf(a.scale_log2 / up * (I8 ? 1.0f : 256.0f), 0x1p-126f);
-        if (!(top <= 3.4e38f)) c[r] = NAN;  // an infinity in q
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const float x0 = x[i][0] * up, x1 = x[i][1] * up, x2 = x[i][2] * up, x3 = x[i][3] * up;
-          if (F32) {
-            qa[i][0] = split_half2(x0, x2, qa[i][1]);
-            qa[i][2] = split_half2(x1, x3, qa[i][3]);
-          } else {
-            qa[i][r] = pack_half2(x0, x2);
-            qa[i][2 + r] = pack_half2(x1, x3);
-          }
-        }
-      }
-
-      float o[D / 8][4];
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
-      float m[NR], l[NR];
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.0f;
-      }
-      float vref = 0x1p-112f;  // power of two at or above every vs so far
-      const int kr = 16 * warp;  // this warp's keys in the tile
-
-      for (int64_t t = tile0; t < tile1; ++t) {
-        if (ok) ok = mbar_wait(smem_u32(&tail.full[stage]), phase, a.wait_limit_ns, &g_attn_error);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        const int64_t first = t * kTile + kr;  // place of this warp's first key
-        if (ok && first < kv) {
-          const uint32_t kd = smem_base + stage * G::kStageAlign;
-          const uint32_t vd = kd + G::kBytes;
-          const float* sc =
-              reinterpret_cast<const float*>(smem + stage * G::kStageAlign + 2 * G::kBytes) + kr;
-          // ---- scores of 16 keys
-          float s[2][4];
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s[i][k] = 0.0f;
-          // matrix lane / 8: keys 0-7 or 8-15, 16 dims i or i + 1
-          const int krow = kr + ((lane >> 3) & 1) * 8 + (lane & 7);
-#pragma unroll
-          for (int i = 0; i < D / 16; i += 2) {
-            const int chunk = i + (lane >> 4);
-            uint32_t w[4];
-            ldsm4(w, kd + (chunk / (G::kPanel / 16)) * (kTile * G::kPanel) +
-                         swizzled<G::kPanel>(krow, chunk % (G::kPanel / 16)));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t b0, b1;
-              codes_to_half<I8>(w[k], b0, b1);
-              mma(s[k & 1], qa[i + (k >> 1)], b0, b1);
-            }
-          }
-          // ---- their scales, and what is seen
-          float2 ks[2], vs[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            ks[i] = *reinterpret_cast<const float2*>(sc + 8 * i + 2 * t4);
-            vs[i] = *reinterpret_cast<const float2*>(sc + kTile + 8 * i + 2 * t4);
-          }
-          unsigned int seen[NR];
-          const bool all = first + 16 <= len;
-#pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            seen[r] = 0xFu;
-            if (!all) {
-              seen[r] = 0;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int64_t place = first + 8 * (k >> 1) + 2 * t4 + (k & 1);
-                const int64_t draft = place - len;
-                bool see = place < kv;
-                if (draft >= 0)
-                  see = see && (a.tree == nullptr ? draft <= tok[r]
-                                                  : (draft < 64 && ((bits[r] >> draft) & 1ull)));
-                if (see) seen[r] |= 1u << k;
-              }
-            }
-          }
-          float x[NR][4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float kk = (k & 1) ? ks[k >> 1].y : ks[k >> 1].x;
-            if (F32) {
-              x[0][k] = (s[k >> 1][k & 1] + s[k >> 1][2 + (k & 1)]) * kk;
-            } else {
-#pragma unroll
-              for (int r = 0; r < NR; ++r) x[r][k] = s[k >> 1][2 * r + (k & 1)] * kk;
-            }
-          }
-          if (!all)
-#pragma unroll
-            for (int r = 0; r < NR; ++r)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (!((seen[r] >> k) & 1u)) x[r][k] = -INFINITY;
-          // ---- running maximum; value scales relative to their own
-          float vt = 0.0f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float vv = (k & 1) ? vs[k >> 1].y : vs[k >> 1].x;
-            const int64_t place = first + 8 * (k >> 1) + 2 * t4 + (k & 1);
-            if (place < kv && vv <= 1e37f) vt = fmaxf(vt, vv);  // NaN, Inf left out
-          }
-          vt = fmaxf(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, 1));
-          vt = fmaxf(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, 2));
-          float mn[NR];
-          bool moved = vt > vref;
-#pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            mn[r] = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
-            mn[r] = fmaxf(mn[r], __shfl_xor_sync(0xFFFFFFFFu, mn[r], 1));
-            mn[r] = fmaxf(mn[r], __shfl_xor_sync(0xFFFFFFFFu, mn[r], 2));
-            mn[r] = fmaxf(mn[r], m[r]);
-            moved = moved || mn[r] > m[r];
-          }
-          if (__any_sync(0xFFFFFFFFu, moved)) {
-            float vnew = vref;
-            if (vt > vref)  // four times the next power of two: rarely passed again
-              vnew = __uint_as_float(((__float_as_uint(vt) & 0x7F800000u) + (2u << 23)));
-            const float vdown = vref / vnew;
-            vref = vnew;
-            float f[NR];
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-              const float al = m[r] == -INFINITY ? 0.0f : ex2((m[r] - mn[r]) * c[r]);
-              l[r] *= al;
-              m[r] = mn[r];
-              f[r] = al * vdown;
-            }
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              o[i][0] *= f[0];
-              o[i][1] *= f[0];
-              o[i][2] *= f[NR - 1];
-              o[i][3] *= f[NR - 1];
-            }
-          }
-          const float inv = __uint_as_float(((254u + 14u) << 23) - (__float_as_uint(vref)));  // 2^14 / vref
-          uint32_t pa[4];
-          float w[NR][4];
-#pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            const float mr = m[r] == -INFINITY ? 0.0f : m[r];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float p = ex2((x[r][k] - mr) * c[r]);
-              l[r] += p;
-              const float vv = (k & 1) ? vs[k >> 1].y : vs[k >> 1].x;
-              w[r][k] = p * (vv * inv);
-              if (!all && !((seen[r] >> k) & 1u)) w[r][k] = 0.0f;
-            }
-          }
-          if (F32) {
-            pa[0] = split_half2(w[0][0], w[0][1], pa[1]);
-            pa[2] = split_half2(w[0][2], w[0][3], pa[3]);
-          } else {
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-              pa[r] = pack_half2(w[r][0], w[r][1]);
-              pa[2 + r] = pack_half2(w[r][2], w[r][3]);
-            }
-          }
-          // ---- output
-          const int vrow = kr + ((lane >> 3) & 1) * 8 + (lane & 7);
-#pragma unroll
-          for (int i = 0; i < D / 16; i += 2) {
-            const int chunk = i + (lane >> 4);
-            uint32_t v[4];
-            ldsm4t(v, vd + (chunk / (G::kPanel / 16)) * (kTile * G::kPanel) +
-                          swizzled<G::kPanel>(vrow, chunk % (G::kPanel / 16)));
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t e0, e1, o0, o1;
-              codes_to_half<I8>(v[2 * k], e0, o0);
-              codes_to_half<I8>(v[2 * k + 1], e1, o1);
-              mma(o[2 * (i + k)], pa, e0, e1);
-              mma(o[2 * (i + k) + 1], pa, o0, o1);
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&tail.empty[stage]));
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-
-      // ---- join the four warps
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
-        if (t4 == 0) {
-          tail.m[warp][g + 8 * r] = m[r];
-          tail.l[warp][g + 8 * r] = l[r];
-          tail.c[g + 8 * r] = c[r];  // the same from every warp
-        }
-      }
-      const float back = vref * (I8 ? 0x1p-14f : 0x1p-6f);
+  const int g = lane >> 2, t4 = lane & 3;
+  int done = 0;  // units taken so far
+  bool ok = true;
+  for (int nseg = 0;; ++nseg) {
+    const int b = seg.item / a.row_tiles, rt = seg.item % a.row_tiles;
+    const int n_all = a.length[b];
+    const int kv = seg.kv;
+    const int len = n_all < 0 ? 0 : n_all < kv ? n_all : kv;  // places every row sees
+    // this thread's row: g
+    const int row_of = rt * kRows + g;
+    const bool live = row_of < a.rows;
+    const int tok = live ? row_of / a.group : 0;
+    unsigned long long bits = 0;
+    if (live && a.tree != nullptr) bits = a.tree[(int64_t)b * a.new_tokens + tok];
+    float c;  // powers of two per unit of the raw score x = (q . k8) ks
+    uint32_t qa[D / 16][4];
+    {
+      const int64_t off = ((int64_t)b * a.new_tokens + tok) * a.q_stride +
+                          (int64_t)(seg.head * a.group + (live ? row_of % a.group : 0)) * D;
+      float x[D / 16][4];
+      float top = 0.0f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        // dims 16 i + 4 t4 ..: even tile's two columns and odd tile's two
-        if (F32) {
-          float4 v;
-          v.x = (o[2 * i][0] + o[2 * i][2]) * back;
-          v.y = (o[2 * i + 1][0] + o[2 * i + 1][2]) * back;
-          v.z = (o[2 * i][1] + o[2 * i][3]) * back;
-          v.w = (o[2 * i + 1][1] + o[2 * i + 1][3]) * back;
-          *reinterpret_cast<float4*>(&tail.o[warp][g][16 * i + 4 * t4]) = v;
+        const int64_t e = off + 16 * i + 4 * t4;
+        if (a.dtype == RQ_F32) {
+          const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + e);
+          x[i][0] = v.x;
+          x[i][1] = v.y;
+          x[i][2] = v.z;
+          x[i][3] = v.w;
         } else {
-#pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            float4 v;
-            v.x = o[2 * i][2 * r] * back;
-            v.y = o[2 * i + 1][2 * r] * back;
-            v.z = o[2 * i][2 * r + 1] * back;
-            v.w = o[2 * i + 1][2 * r + 1] * back;
-            *reinterpret_cast<float4*>(&tail.o[warp][g + 8 * r][16 * i + 4 * t4]) = v;
-          }
-        }
-      }
-      consumer_sync();
-
-      // which CTAs share this segment
-      int64_t parts = 1, cta0 = 0, s0 = 0;
-      if (!a.direct) {
-        s0 = (int64_t)tail.item_start[item] * a.kv_heads + head * n;
-        cta0 = ((s0 + 1) * ctas - 1) / units;
-        parts = ((s0 + n) * ctas - 1) / units - cta0 + 1;
-      }
-      bool last = true;
-      constexpr int kVec = D / 4;
-      constexpr int kPartRow = D + 4;  // output, then max and sum
-      if (parts > 1) {
-        float* part = a.part + ((int64_t)blockIdx.x * 2 + (seg == 0 ? 0 : 1)) * ROWS * kPartRow;
-        for (int i = tid; i < ROWS * kVec; i += kWarps * 32) {
-          const int r = i / kVec, d = (i % kVec) * 4;
-          if (rt * ROWS + r >= a.rows) continue;
-          float mx = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, tail.m[w][r]);
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          float sum = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float mw = tail.m[w][r];
-            const float f = mw == -INFINITY ? 0.0f : ex2((mw - mx) * tail.c[r]);
-            const float4 ow = *reinterpret_cast<const float4*>(&tail.o[w][r][d]);
-            v.x = fmaf(ow.x, f, v.x);
-            v.y = fmaf(ow.y, f, v.y);
-            v.z = fmaf(ow.z, f, v.z);
-            v.w = fmaf(ow.w, f, v.w);
-            sum = fmaf(tail.l[w][r], f, sum);
-          }
-          __stcg(reinterpret_cast<float4*>(part + r * kPartRow + d), v);
-          if (d == 0) __stcg(reinterpret_cast<float2*>(part + r * kPartRow + D), make_float2(mx, sum));
-        }
-        __threadfence();
-        consumer_sync();
-        if (tid == 0) {
-          unsigned int* ctr = a.counter + ((int64_t)item * a.kv_heads + head);
-          const unsigned int old = atomicAdd(ctr, 1u);
-          tail.flag = old == (unsigned int)(parts - 1);
-          if (tail.flag) *ctr = 0u;
-        }
-        consumer_sync();
-        last = tail.flag != 0;
-        __threadfence();
-      }
-      if (last) {
-        for (int i = tid; i < ROWS * kVec; i += kWarps * 32) {
-          const int r = i / kVec, d = (i % kVec) * 4;
-          const int row = rt * ROWS + r;
-          if (row >= a.rows) continue;
-          const float cr = tail.c[r];
-          float mx = -INFINITY, sum = 0.0f;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          const int count = parts > 1 ? (int)parts : kWarps;
-          for (int p = 0; p < count; ++p) {
-            float4 ov;
-            float2 ml;
-            if (parts > 1) {
-              const int64_t cta = cta0 + p;
-              const int slot = p == 0 && units * cta / ctas < s0 ? 1 : 0;
-              const float* part = a.part + (cta * 2 + slot) * ROWS * kPartRow + r * kPartRow;
-              ov = __ldcg(reinterpret_cast<const float4*>(part + d));
-              ml = __ldcg(reinterpret_cast<const float2*>(part + D));
-            } else {
-              ov = *reinterpret_cast<const float4*>(&tail.o[p][r][d]);
-              ml = make_float2(tail.m[p][r], tail.l[p][r]);
-            }
-            const float mn = fmaxf(mx, ml.x);
-            if (mn == -INFINITY) {
-              sum += ml.y;  // 0, or the NaN of a row whose scores all are
-              continue;
-            }
-            const float f0 = ex2((mx - mn) * cr), f1 = ex2((ml.x - mn) * cr);
-            v.x = v.x * f0 + ov.x * f1;
-            v.y = v.y * f0 + ov.y * f1;
-            v.z = v.z * f0 + ov.z * f1;
-            v.w = v.w * f0 + ov.w * f1;
-            sum = sum * f0 + ml.y * f1;
-            mx = mn;
-          }
-          // nothing seen: zeros (a NaN sum stays a NaN)
-          const float r1 = sum == 0.0f ? 0.0f : 1.0f / sum;
-          v.x *= r1;
-          v.y *= r1;
-          v.z *= r1;
-          v.w *= r1;
-          const int64_t dst = (((int64_t)b * a.new_tokens + row / a.group) * a.q_heads +
-                               head * a.group + row % a.group) * D + d;
-          if (F32) {
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + dst) = v;
-          } else if (a.dtype == RQ_F16) {
-            const uint2 h = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + dst) = h;
+          const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + e);
+          if (a.dtype == RQ_F16) {
+            const float2 f0 = half_pair(v.x), f1 = half_pair(v.y);
+            x[i][0] = f0.x;
+            x[i][1] = f0.y;
+            x[i][2] = f1.x;
+            x[i][3] = f1.y;
           } else {
-            const __nv_bfloat162 h0 = __floats2bfloat162_rn(v.x, v.y);
-            const __nv_bfloat162 h1 = __floats2bfloat162_rn(v.z, v.w);
-            const uint2 h = make_uint2(*reinterpret_cast<const uint32_t*>(&h0),
-                                       *reinterpret_cast<const uint32_t*>(&h1));
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + dst) = h;
+            x[i][0] = __uint_as_float(v.x << 16);
+            x[i][1] = __uint_as_float(v.x & 0xFFFF0000u);
+            x[i][2] = __uint_as_float(v.y << 16);
+            x[i][3] = __uint_as_float(v.y & 0xFFFF0000u);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (!live) x[i][k] = 0.0f;
+          top = fmaxf(top, fabsf(x[i][k]));
+        }
+      }
+      // the row times a power of two, so that its f16 parts lie well inside
+      // f16's range: largest entry in [2^13, 2^14)
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      int e = 0;
+      if (top > 0.0f && top <= 3.4e38f) {
+        e = 13 - (int)((__float_as_uint(top) >> 23) & 0xFFu) + 127;
+        e = e < -126 ? -126 : e > 100 ? 100 : e;
+      }
+      const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+      c = fmaxf(a.scale_log2 / up, 0x1p-126f);
+      if (!(top <= 3.4e38f)) c = NAN;  // an infinity in q
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        qa[i][0] = split_half2(x[i][0] * up, x[i][1] * up, qa[i][1]);
+        qa[i][2] = split_half2(x[i][2] * up, x[i][3] * up, qa[i][3]);
+      }
+    }
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
+    float m = -INFINITY, l = 0.0f;
+    float vref = 0x1p-112f;  // power of two at or above every vs so far
+
+    for (int u = seg.first + warp; u < seg.end; u += W) {
+      const int st = done % S;
+      if (ok)
+        ok = mbar_wait_fast(smem_u32(&tail.full[warp][st]), (uint32_t)(done / S) & 1u,
+                            a.wait_limit_ns, &g_attn_error);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      ++done;
+      const int first = u * kKeys;  // place of the first key
+      const bool all = first + kKeys <= len;
+      const uint32_t kd = ring + st * (2 * G::kBytes), vd = kd + G::kBytes;
+      // ---- scores
+      float s[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[i][k] = 0.0f;
+      // ldmatrix's matrix lane / 8: keys 0-7 or 8-15, 16 dims i or i + 1
+      const int mrow = ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+      for (int i = 0; i < D / 16; i += 2) {
+        const int chunk = i + (lane >> 4);
+        uint32_t w[4];
+        ldsm4(w, kd + (chunk / (G::kPanel / 16)) * (kKeys * G::kPanel) +
+                     swizzled<G::kPanel>(mrow, chunk % (G::kPanel / 16)));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t b0, b1;
+          codes_in_order<I8>(w[k], b0, b1);
+          mma(s[k & 1], qa[i + (k >> 1)], b0, b1);
+        }
+      }
+      // ---- scales: this thread's keys are 2 t4, 2 t4 + 1 and 8 more
+      const float* sc = &tail.scale[warp][st][0][0];
+      const float2 ka = *reinterpret_cast<const float2*>(sc + 2 * t4);
+      const float2 kb = *reinterpret_cast<const float2*>(sc + 8 + 2 * t4);
+      const float2 va = *reinterpret_cast<const float2*>(sc + kKeys + 2 * t4);
+      const float2 vb = *reinterpret_cast<const float2*>(sc + kKeys + 8 + 2 * t4);
+      float x[4] = {(s[0][0] + s[0][2]) * ka.x, (s[0][1] + s[0][3]) * ka.y,
+                    (s[1][0] + s[1][2]) * kb.x, (s[1][1] + s[1][3]) * kb.y};
+      float vv[4] = {va.x, va.y, vb.x, vb.y};
+      uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};  // V bytes of keys that exist
+      if (!all) {
+        keep[0] = keep[1] = 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int place = first + 8 * (k >> 1) + 2 * t4 + (k & 1);
+          const int draft = place - len;
+          bool see = place < kv;
+          if (see) keep[k >> 1] |= 0xFFFFu << (16 * (k & 1));
+          if (draft >= 0)
+            see = see && (a.tree == nullptr ? draft <= tok
+                                            : (draft < 64 && ((bits >> draft) & 1ull) != 0ull));
+          if (!see) {
+            x[k] = -INFINITY;
+            vv[k] = 0.0f;
           }
         }
       }
-      consumer_sync();  // the joined rows are read before the next segment's are written
+      // ---- running maximum, and the values' scales relative to theirs; both
+      // seldom move, so that most units pay one vote for them
+      const float xm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      float vt = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) vt = fmaxf(vt, vv[k] <= 1e37f ? vv[k] : 0.0f);  // no NaN, Inf
+      if (__any_sync(0xFFFFFFFFu, xm > m || vt > vref)) {
+        float mn = fmaxf(xm, __shfl_xor_sync(0xFFFFFFFFu, xm, 1));
+        mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 2));
+        mn = fmaxf(mn, m);
+        vt = fmaxf(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, 1));
+        vt = fmaxf(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, 2));
+#pragma unroll
+        for (int i = 4; i < 32; i <<= 1) vt = fmaxf(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, i));
+        float vnew = vref;
+        if (vt > vref)  // four times the next power of two: rarely passed again
+          vnew = __uint_as_float((__float_as_uint(vt) & 0x7F800000u) + (2u << 23));
+        const float al = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
+        const float f = al * (vref / vnew);
+        vref = vnew;
+        l *= al;
+        m = mn;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[i][k] *= f;
+      }
+      // 2^14 / vref: the weights p vs / vref lie below 2^14, well inside f16
+      const float inv = __uint_as_float((268u << 23) - __float_as_uint(vref));
+      const float mr = m == -INFINITY ? 0.0f : m;
+      float w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float p = ex2((x[k] - mr) * c);
+        l += p;
+        w[k] = p * (vv[k] * inv);
+      }
+      uint32_t pa[4];
+      pa[0] = split_half2(w[0], w[1], pa[1]);
+      pa[2] = split_half2(w[2], w[3], pa[3]);
+      // ---- output
+#pragma unroll
+      for (int i = 0; i < D / 16; i += 2) {
+        const int chunk = i + (lane >> 4);
+        uint32_t v[4];
+        ldsm4t(v, vd + (chunk / (G::kPanel / 16)) * (kKeys * G::kPanel) +
+                      swizzled<G::kPanel>(mrow, chunk % (G::kPanel / 16)));
+        if (!all)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] &= keep[k & 1];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t e0, e1, o0, o1;
+          codes_across<I8>(v[2 * k], e0, o0);
+          codes_across<I8>(v[2 * k + 1], e1, o1);
+          mma(o[2 * (i + k)], pa, e0, e1);
+          mma(o[2 * (i + k) + 1], pa, o0, o1);
+        }
+      }
+      __syncwarp();
+      load_one();
     }
 
-    ++seg;
-    tile0 = 0;
-    if (++head == a.kv_heads) {
-      head = 0;
-      ++item;
+    // ---- join the warps: every lane of a row's four holds part of its sum
+    l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+    l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+    if (t4 == 0) {
+      tail.m[warp][g] = m;
+      tail.l[warp][g] = l;
+      tail.c[g] = c;  // the same from every warp
     }
+    const float back = vref * 0x1p-14f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+      // dims 16 i + 4 t4 ..: the even tile's two columns and the odd tile's
+      *reinterpret_cast<float4*>(&tail.o[warp][g][16 * i + 4 * t4]) =
+          make_float4((o[2 * i][0] + o[2 * i][2]) * back, (o[2 * i + 1][0] + o[2 * i + 1][2]) * back,
+                      (o[2 * i][1] + o[2 * i][3]) * back, (o[2 * i + 1][1] + o[2 * i + 1][3]) * back);
+    __syncthreads();
+
+    // which CTAs share this segment
+    int64_t parts = 1, cta0 = 0, s0 = 0;
+    if (!a.direct) {
+      const int n = tail.item_start[seg.item + 1] - tail.item_start[seg.item];
+      s0 = (int64_t)tail.item_start[seg.item] * a.kv_heads + (int64_t)seg.head * n;
+      cta0 = ((s0 + 1) * ctas - 1) / units;
+      parts = ((s0 + n) * ctas - 1) / units - cta0 + 1;
+    }
+    constexpr int kVec = D / 4;
+    constexpr int kPartRow = D + 4;  // output, then max and sum
+    // A partial row set of this segment, by part number.
+    auto part_at = [&](int64_t p) -> int64_t {
+      const int64_t cta = cta0 + p;
+      return cta * 2 + (p == 0 && units * cta / ctas < s0 ? 1 : 0);
+    };
+    // Join this thread's piece of `count` partials, `step` parts apart from
+    // part p0 on, eight loads in flight at a time; in part order.
+    auto join = [&](int64_t p0, int64_t step, int count, int r, int d, float4& v, float& mx,
+                    float& sum) {
+      const float cr = tail.c[r];
+      for (int q0 = 0; q0 < count; q0 += kJoin) {
+        float4 ov[kJoin];
+        float2 ml[kJoin];
+#pragma unroll
+        for (int k = 0; k < kJoin; ++k) {
+          ml[k] = make_float2(-INFINITY, 0.0f);
+          ov[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (q0 + k < count) {
+            const float* part = a.part + (part_at(p0 + (q0 + k) * step) * kRows + r) * kPartRow;
+            ov[k] = __ldcg(reinterpret_cast<const float4*>(part + d));
+            ml[k] = __ldcg(reinterpret_cast<const float2*>(part + D));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kJoin; ++k) merge(v, mx, sum, ov[k], ml[k], cr);
+      }
+    };
+    auto arrive = [&](unsigned int* ctr, unsigned int of) -> bool {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const unsigned int old = atomicAdd(ctr, 1u);
+        tail.flag = old == of - 1u;
+        if (tail.flag) *ctr = 0u;
+      }
+      __syncthreads();
+      const bool is_last = tail.flag != 0;
+      __threadfence();
+      return is_last;
+    };
+    auto store_part = [&](int64_t slot, int r, int d, const float4& v, float mx, float sum) {
+      float* part = a.part + (slot * kRows + r) * kPartRow;
+      __stcg(reinterpret_cast<float4*>(part + d), v);
+      if (d == 0) __stcg(reinterpret_cast<float2*>(part + D), make_float2(mx, sum));
+    };
+    constexpr int kPieces = (kRows * kVec + G::kThreads - 1) / G::kThreads;
+    float4 v[kPieces];
+    float mx[kPieces], sum[kPieces];
+    bool mine[kPieces];
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int i = tid + k * G::kThreads, r = i / kVec, d = (i % kVec) * 4;
+      mine[k] = i < kRows * kVec && rt * kRows + r < a.rows;
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      mx[k] = -INFINITY;
+      sum[k] = 0.0f;
+      if (!mine[k]) continue;
+#pragma unroll 4
+      for (int w = 0; w < W; ++w)
+        merge(v[k], mx[k], sum[k], *reinterpret_cast<const float4*>(&tail.o[w][r][d]),
+              make_float2(tail.m[w][r], tail.l[w][r]), tail.c[r]);
+    }
+    bool last = true;
+    if (parts > 1) {
+      // Two levels, so that no CTA reads more than a few dozen partials: the
+      // last of each kJoin neighbours joins theirs, the last of those joins
+      // the groups.
+      const int64_t p = blockIdx.x - cta0, first_of = p / kJoin * kJoin;
+      const int members = (int)(parts - first_of < kJoin ? parts - first_of : kJoin);
+      const int groups = (int)((parts + kJoin - 1) / kJoin);
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int i = tid + k * G::kThreads, r = i / kVec, d = (i % kVec) * 4;
+        if (mine[k]) store_part(part_at(p), r, d, v[k], mx[k], sum[k]);
+      }
+      const int64_t slot = part_at(first_of);
+      last = arrive(a.counter + slot, (unsigned int)members);
+      for (int level = 0; last && level < 2; ++level) {
+        if (level == 1) {
+          if (groups == 1) break;
+          last = arrive(a.counter + 2 * gridDim.x + (int64_t)seg.item * a.kv_heads + seg.head,
+                        (unsigned int)groups);
+          if (!last) break;
+        }
+#pragma unroll
+        for (int k = 0; k < kPieces; ++k) {
+          const int i = tid + k * G::kThreads, r = i / kVec, d = (i % kVec) * 4;
+          if (!mine[k]) continue;
+          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          mx[k] = -INFINITY;
+          sum[k] = 0.0f;
+          if (level == 0)
+            join(first_of, 1, members, r, d, v[k], mx[k], sum[k]);
+          else
+            join(0, kJoin, groups, r, d, v[k], mx[k], sum[k]);
+          if (level == 0 && groups > 1) store_part(slot, r, d, v[k], mx[k], sum[k]);
+        }
+      }
+    }
+    if (last) {
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int i = tid + k * G::kThreads, r = i / kVec, d = (i % kVec) * 4;
+        const int row = rt * kRows + r;
+        if (!mine[k]) continue;
+        // nothing seen: zeros (a NaN sum stays a NaN)
+        const float r1 = sum[k] == 0.0f ? 0.0f : 1.0f / sum[k];
+        const float4 y = make_float4(v[k].x * r1, v[k].y * r1, v[k].z * r1, v[k].w * r1);
+        const int64_t dst = (((int64_t)b * a.new_tokens + row / a.group) * a.q_heads +
+                             seg.head * a.group + row % a.group) * D + d;
+        if (a.dtype == RQ_F32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + dst) = y;
+        } else if (a.dtype == RQ_F16) {
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + dst) =
+              make_uint2(pack_half2(y.x, y.y), pack_half2(y.z, y.w));
+        } else {
+          const __nv_bfloat162 h0 = __floats2bfloat162_rn(y.x, y.y);
+          const __nv_bfloat162 h1 = __floats2bfloat162_rn(y.z, y.w);
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + dst) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&h0),
+                         *reinterpret_cast<const uint32_t*>(&h1));
+        }
+      }
+    }
+    if (seg.left == 0) break;
+    __syncthreads();  // the joined rows are read before the next segment's are written
+    next(seg);
   }
 
-  // a producer that gave up: its last copies are waited for before it ends
-  if (warp == kWarps && lane == 0 && !ok) {
-    for (int i = 0; i < S; ++i) {
-      stage = stage == 0 ? S - 1 : stage - 1;
-      if (stage == S - 1) phase ^= 1u;
-      mbar_wait(smem_u32(&tail.full[stage]), phase, a.wait_limit_ns, &g_attn_error);
-    }
-  }
+  // a warp that gave up: its copies in flight are waited for before it ends
+  if (!ok)
+    for (; done < issued; ++done)
+      mbar_wait(smem_u32(&tail.full[warp][done % S]), (uint32_t)(done / S) & 1u, a.wait_limit_ns,
+                &g_attn_error);
 }
 
 // ------------------------------------------------------------- host side --
@@ -809,56 +813,28 @@ int lg(int v) {
   return l;
 }
 
-struct Plan {
-  int rows, ctas;
-  bool direct;
-};
-
 using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const AttnArgs);
 
-template <int D, bool I8, bool F32>
-rq_status kernel_of(Kernel* k, int* smem, int* per_sm) {
-  constexpr int ROWS = F32 ? 8 : 16;
-  constexpr int bytes =
-      Geometry<D>::kStages * Geometry<D>::kStageAlign + (int)sizeof(Tail<D, ROWS>);
-  static int resident = 0;
-  if (resident == 0) {
-    if (cudaFuncSetAttribute(attn_kernel<D, I8, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+template <int D, bool I8>
+rq_status launch_d(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, unsigned grid,
+                   cudaStream_t st) {
+  constexpr int bytes = Geometry<D>::kRing + (int)sizeof(Tail<D>);
+  static_assert(bytes <= 232448, "shared memory of one CTA");
+  static bool ready = false;
+  if (!ready) {
+    if (cudaFuncSetAttribute(attn_kernel<D, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              bytes) != cudaSuccess)
       return RQ_ERR_CUDA;
-    int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attn_kernel<D, I8, F32>, kAttnThreads,
-                                                      bytes) != cudaSuccess ||
-        n < 1)
-      return RQ_ERR_CUDA;
-    resident = n;
+    ready = true;
   }
-  *k = attn_kernel<D, I8, F32>;
-  *smem = bytes;
-  *per_sm = resident;
-  return RQ_OK;
-}
-
-template <int D>
-rq_status kernel_for(bool i8, bool f32, Kernel* k, int* smem, int* per_sm) {
-  if (i8) return f32 ? kernel_of<D, true, true>(k, smem, per_sm)
-                     : kernel_of<D, true, false>(k, smem, per_sm);
-  return f32 ? kernel_of<D, false, true>(k, smem, per_sm)
-             : kernel_of<D, false, false>(k, smem, per_sm);
+  return launch_kernel(attn_kernel<D, I8>, dim3(grid), dim3(Geometry<D>::kThreads), (size_t)bytes,
+                       st, mk, mv, a);
 }
 
 }  // namespace
 
 rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cudaStream_t st) {
   const rq_kv_cache& c = *call.cache;
-  const bool f32 = call.dtype == RQ_F32, i8 = c.format == RQ_KV_I8;
-  Kernel kernel = nullptr;
-  int smem = 0, per_sm = 0;
-  rq_status s = c.head_dim == 64    ? kernel_for<64>(i8, f32, &kernel, &smem, &per_sm)
-                : c.head_dim == 128 ? kernel_for<128>(i8, f32, &kernel, &smem, &per_sm)
-                                    : kernel_for<256>(i8, f32, &kernel, &smem, &per_sm);
-  if (s != RQ_OK) return s;
-
   AttnArgs a = {};
   a.q = call.q;
   a.out = call.out;
@@ -874,36 +850,40 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
   a.kv_heads = c.kv_heads;
   a.group = call.q_heads / c.kv_heads;
   a.rows = call.new_tokens * a.group;
-  const int tile_rows = f32 ? 8 : 16;
-  a.row_tiles = (a.rows + tile_rows - 1) / tile_rows;
+  a.row_tiles = (a.rows + kRows - 1) / kRows;
   a.max_pages = call.max_pages;
   a.lg_page = lg(c.page_size);
-  a.lg_box = a.lg_page < 6 ? a.lg_page : 6;
   a.pages = c.pages;
   a.scale_log2 = (float)((double)call.scale * 1.4426950408889634);
   a.dtype = call.dtype;
   a.wait_limit_ns = kWaitLimitNs;
 
   CUtensorMap mk, mv;
-  if (!codes_map(&mk, c.k, c, 1 << a.lg_box) || !codes_map(&mv, c.v, c, 1 << a.lg_box))
-    return RQ_ERR_ARCH;
+  if (!codes_map(&mk, c.k, c, kKeys) || !codes_map(&mv, c.v, c, kKeys)) return RQ_ERR_ARCH;
 
   const int64_t items = (int64_t)call.batch * a.row_tiles;
   const int64_t segments = items * c.kv_heads;
-  int64_t grid = (int64_t)device_sm_count() * per_sm;
+  int64_t grid = device_sm_count();
   a.direct = items > kMaxItems;
   if (a.direct) {
     grid = segments;
     if (grid > 0x7FFFFFFF) return RQ_ERR_SHAPE;
   } else {
-    const size_t part = sizeof(float) * 2 * (size_t)grid * tile_rows * (c.head_dim + 4);
-    s = scratch->reserve(part, (size_t)segments, st);
+    const size_t part = sizeof(float) * 2 * (size_t)grid * kRows * (c.head_dim + 4);
+    const rq_status s = scratch->reserve(part, 2 * (size_t)grid + (size_t)segments, st);
     if (s != RQ_OK) return s;
     a.part = scratch->part;
     a.counter = scratch->counter;
   }
-  return launch_kernel(kernel, dim3((unsigned)grid), dim3(kAttnThreads), (size_t)smem, st, mk, mv,
-                       a);
+  const unsigned g = (unsigned)grid;
+  const bool i8 = c.format == RQ_KV_I8;
+  switch (c.head_dim) {
+    case 64: return i8 ? launch_d<64, true>(mk, mv, a, g, st) : launch_d<64, false>(mk, mv, a, g, st);
+    case 128:
+      return i8 ? launch_d<128, true>(mk, mv, a, g, st) : launch_d<128, false>(mk, mv, a, g, st);
+    default:
+      return i8 ? launch_d<256, true>(mk, mv, a, g, st) : launch_d<256, false>(mk, mv, a, g, st);
+  }
 }
 
 rq_status AttnScratch::reserve(size_t part_bytes, size_t counters, cudaStream_t st) {

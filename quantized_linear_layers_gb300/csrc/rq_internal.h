@@ -156,8 +156,8 @@ struct AttnCall {
   const uint64_t* tree;
   float scale;
 };
-// Scratch of split sequences: partial rows, and one arrival counter per
-// segment, at zero between launches.  Used on one stream at a time.
+// Scratch of split sequences: partial rows, and the arrival counters of the
+// joins, at zero between launches.  Used on one stream at a time.
 struct AttnScratch {
   float* part = nullptr;
   size_t part_cap = 0;

@@ -33,7 +33,7 @@ constexpr int kJoin = 8;             // partials joined at once
 struct AttnArgs {
   const void* q;
   void* out;
-  int64_t q_stride;
+  int64_t q_stride, q_bytes;
   const float *ks, *vs;
   const int32_t *table, *length;
   const unsigned long long* tree;
@@ -72,9 +72,9 @@ struct Tail {
   float c[kRows];
   uint64_t full[kWarps][kStages];
   int flag;
-  int warp_sum[kWarps];
+  int warp_sum[kWarps], warp_most[kWarps];
   int item_start[kMaxItems + 1];  // units before each item, for one kv head
-  int item_places[kMaxItems];     // places its rows may see
+  int length[kMaxItems];          // the sequences' lengths
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -194,43 +194,40 @@ __device__ __forceinline__ void merge(float4& v, float& mx, float& sum, const fl
   mx = mn;
 }
 
-// Places of a sequence that its new tokens may see, over all row tiles; 0 for
-// an unused one.  *len: places every row sees.
-__device__ __forceinline__ int64_t places(const AttnArgs& a, int b, int64_t* len) {
-  const int64_t n = a.length[b];
-  if (n < 0) {
-    *len = 0;
-    return 0;
-  }
+// Places that row tile rt of a sequence of n cached tokens may see (0: an
+// unused sequence).  Up to 64 new tokens every tile takes them all: a chain
+// is then cut as a tree of one branch is, and gives its bits.
+__device__ __forceinline__ int tile_places(const AttnArgs& a, int n, int rt) {
+  if (n < 0) return 0;
   const int64_t most = (int64_t)a.max_pages << a.lg_page;
-  int64_t kv = n + a.new_tokens;
+  int64_t kv = (int64_t)n + a.new_tokens;
   if (kv > most) {
     atomicOr(&g_attn_error, 2u);
     kv = most;
   }
-  *len = n < kv ? n : kv;
-  return kv;
+  if (a.new_tokens > 64) {
+    int last = (rt + 1) * kRows;
+    last = (last < a.rows ? last : a.rows) - 1;
+    const int64_t end = (int64_t)n + last / a.group + 1;
+    kv = end < kv ? end : kv;
+  }
+  return (int)(kv < 0x7FFFFF00 ? kv : 0x7FFFFF00);
 }
 
-// Last place + 1 that row tile rt may see.  Up to 64 new tokens every tile
-// takes them all: a chain is then cut as a tree of one branch is, and gives
-// its bits.
-__device__ __forceinline__ int64_t tile_places(const AttnArgs& a, int rt, int64_t len,
-                                               int64_t kv) {
-  if (a.new_tokens <= 64 || kv == 0) return kv;
-  int last = (rt + 1) * kRows;
-  last = (last < a.rows ? last : a.rows) - 1;
-  const int64_t end = len + last / a.group + 1;
-  return end < kv ? end : kv;
+// Fetch what the launch reads first and only once, q and the page table, into
+// L2 while the lengths are on their way.
+__device__ __forceinline__ void prefetch_l2(const void* base, int64_t bytes) {
+  const int64_t line = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 128;
+  if (line < bytes)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(base) + line));
 }
 
 // ------------------------------------------------------------ the kernel --
 //
 // Work is the sequence of segments (sequence, row tile, kv head), each a run
-// of 16-key units, laid end to end; CTA c of C takes an equal run of it, so
-// that ragged lengths load the SMs evenly and a single long sequence spreads
-// over all of them.  A segment cut between CTAs is joined by the last of them
-// to finish, in CTA order, from partial (max, sum, output) rows in scratch.
+// of 16-key units.  How it is cut (Split) follows from the lengths, which only
+// the device knows; a segment cut between CTAs is joined by the last of them
+// to finish, in part order, from partial (max, sum, output) rows in scratch.
 //
 // Within a CTA the warps take units in turn, each with its own ring of units
 // in flight (TMA, refilled by the warp itself, on into the next segment) and
@@ -257,65 +254,89 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
   pdl_trigger();
 
   const int items = a.batch * a.row_tiles;
-  int64_t u0 = 0, u1 = 1, units = 1;  // this CTA's run of units
-  int ctas = (int)gridDim.x;
+  prefetch_l2(a.q, a.q_bytes);
+  prefetch_l2(a.table, (int64_t)a.batch * a.max_pages * 4);
+  int64_t units = 1;
+  int most = 1;  // units of the longest segment
   if (!a.direct) {
     int carry = 0;
     for (int base = 0; base < items; base += G::kThreads) {
       const int i = base + tid;
       int n = 0;
       if (i < items) {
-        int64_t len;
-        const int64_t kv = places(a, i / a.row_tiles, &len);
-        const int64_t mine = tile_places(a, i % a.row_tiles, len, kv);
-        tail.item_places[i] = (int)mine;
-        n = (int)((mine + kKeys - 1) / kKeys);
+        const int bi = i / a.row_tiles, ri = i - bi * a.row_tiles;
+        const int len = a.length[bi];
+        if (ri == 0) tail.length[bi] = len;
+        n = (tile_places(a, len, ri) + kKeys - 1) / kKeys;
         if (n < 1) n = 1;
       }
-      int scan = n;
+      int scan = n, top = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xFFFFFFFFu, scan, o);
         if (lane >= o) scan += x;
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
       }
       __syncthreads();
-      if (lane == 31) tail.warp_sum[warp] = scan;
+      if (lane == 31) {
+        tail.warp_sum[warp] = scan;
+        tail.warp_most[warp] = top;
+      }
       __syncthreads();
       int before = carry;
+#pragma unroll
       for (int w = 0; w < W; ++w) {
         const int x = tail.warp_sum[w];
         if (w < warp) before += x;
         carry += x;
+        most = max(most, tail.warp_most[w]);
       }
       if (i < items) tail.item_start[i] = before + scan - n;
     }
     if (tid == 0) tail.item_start[items] = carry;
     units = (int64_t)carry * a.kv_heads;
-    // no CTA below one unit per warp
-    if (ctas > (units + W - 1) / W) ctas = (int)((units + W - 1) / W);
-    u0 = (int)blockIdx.x < ctas ? units * blockIdx.x / ctas : 0;
-    u1 = (int)blockIdx.x < ctas ? units * (blockIdx.x + 1) / ctas : 0;
+    __syncthreads();
   }
-  __syncthreads();
-  if (u0 >= u1) return;
 
-  // A segment's part in this run: units [first, end) of it.
+  // How the segments are cut:
+  //   kParts: every segment in up to `split` equal parts, one CTA each;
+  //   kWhole: a run of whole segments per CTA;
+  //   kRun: an equal run of units per CTA, wherever segments begin or end.
+  // Joining a segment over CTAs costs as much as about 4 rounds of its CTA's
+  // warps (2.5 us against 0.6 us a round), and so does beginning another one:
+  // no part is made smaller than that, segments that short stay whole, and a
+  // run may begin and end inside segments only where that evens out more.
+  enum { kParts, kWhole, kRun };
+  constexpr int kRound = 4 * W;  // units of 4 rounds
+  const int64_t segments = (int64_t)items * a.kv_heads;
+  const int grid = (int)gridDim.x;
+  int cut = kWhole, split = 1;
+  if (!a.direct) {
+    if (segments <= grid) {
+      split = min(grid / (int)segments, (most + kRound - 1) / kRound);
+      const int64_t even = (units + (int64_t)grid * W - 1) / ((int64_t)grid * W);
+      cut = (most + split * W - 1) / (split * W) <= even + 4 ? kParts : kRun;
+    } else if (most > kRound) {
+      cut = kRun;
+    }
+  }
+
+  // A segment's part in this CTA's work: units [first, end) of it.
   struct Segment {
     int item, head, first, end, kv;
-    int64_t left;  // units of the run after it
+    int64_t left;  // units (kRun) or segments (else) after it
   };
-  auto open = [&](Segment& g) {  // item, head, first and left (from `first` on) are set
-    if (a.direct) {
-      int64_t len;
-      const int64_t kv = places(a, g.item / a.row_tiles, &len);
-      g.kv = (int)tile_places(a, g.item % a.row_tiles, len, kv);
-      g.end = g.kv < 1 ? 1 : (g.kv + kKeys - 1) / kKeys;
-      g.left = 0;
-    } else {
-      g.kv = tail.item_places[g.item];
-      const int n = tail.item_start[g.item + 1] - tail.item_start[g.item];
+  auto length_of = [&](int bi) -> int { return a.direct ? a.length[bi] : tail.length[bi]; };
+  auto open = [&](Segment& g) {  // item, head, first and left are set
+    const int bi = g.item / a.row_tiles;
+    g.kv = tile_places(a, length_of(bi), g.item - bi * a.row_tiles);
+    const int n = g.kv < 1 ? 1 : (g.kv + kKeys - 1) / kKeys;
+    if (cut == kRun) {
       g.end = g.left < n - g.first ? g.first + (int)g.left : n;
       g.left -= g.end - g.first;
+    } else {
+      g.end = n;
+      --g.left;
     }
   };
   auto next = [&](Segment& g) {
@@ -327,11 +348,11 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
     open(g);
   };
   Segment seg;
-  if (a.direct) {
-    seg.item = (int)(blockIdx.x % (unsigned)items);
-    seg.head = (int)(blockIdx.x / (unsigned)items);
-    seg.first = 0;
-  } else {
+  int parts = 1, part = 0;  // kParts: of this CTA's segment
+  seg.first = 0;
+  if (cut == kRun) {
+    const int64_t u0 = units * blockIdx.x / grid, u1 = units * (blockIdx.x + 1) / grid;
+    if (u0 >= u1) return;
     int lo = 0, hi = items - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -341,13 +362,36 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
         hi = mid - 1;
     }
     const int n = tail.item_start[lo + 1] - tail.item_start[lo];
-    const int64_t rest = u0 - (int64_t)tail.item_start[lo] * a.kv_heads;
+    const int rest = (int)(u0 - (int64_t)tail.item_start[lo] * a.kv_heads);
     seg.item = lo;
-    seg.head = (int)(rest / n);
-    seg.first = (int)(rest - (int64_t)seg.head * n);
+    seg.head = rest / n;
+    seg.first = rest - seg.head * n;
+    seg.left = u1 - u0;
+    open(seg);
+  } else {
+    int64_t s0 = blockIdx.x, s1 = s0 + 1;
+    if (cut == kParts) {
+      s0 /= split;
+      s1 = s0 + 1;
+      part = (int)blockIdx.x - (int)s0 * split;
+      if (s0 >= segments) return;
+    } else if (!a.direct) {
+      s0 = segments * blockIdx.x / grid;
+      s1 = segments * (blockIdx.x + 1) / grid;
+      if (s0 >= s1) return;
+    }
+    seg.item = (int)(s0 / a.kv_heads);
+    seg.head = (int)(s0 - (int64_t)seg.item * a.kv_heads);
+    seg.left = s1 - s0;
+    open(seg);
+    if (cut == kParts) {
+      const int n = seg.end;
+      parts = min(split, (n + kRound - 1) / kRound);
+      if (part >= parts) return;
+      seg.first = (int)((int64_t)n * part / parts);
+      seg.end = (int)((int64_t)n * (part + 1) / parts);
+    }
   }
-  seg.left = u1 - u0;
-  open(seg);
 
   // -------- the warp's loads, S units ahead of its products
   Segment ld = seg;
@@ -405,16 +449,12 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
     ++issued;
     unit += W;
   };
-  for (int i = 0; i < S; ++i) load_one();
-
   const int g = lane >> 2, t4 = lane & 3;
-  int done = 0;  // units taken so far
   bool ok = true;
+  int done = 0;  // units taken so far
   for (int nseg = 0;; ++nseg) {
-    const int b = seg.item / a.row_tiles, rt = seg.item % a.row_tiles;
-    const int n_all = a.length[b];
+    const int b = seg.item / a.row_tiles, rt = seg.item - b * a.row_tiles;
     const int kv = seg.kv;
-    const int len = n_all < 0 ? 0 : n_all < kv ? n_all : kv;  // places every row sees
     // this thread's row: g
     const int row_of = rt * kRows + g;
     const bool live = row_of < a.rows;
@@ -426,30 +466,48 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
     {
       const int64_t off = ((int64_t)b * a.new_tokens + tok) * a.q_stride +
                           (int64_t)(seg.head * a.group + (live ? row_of % a.group : 0)) * D;
+      // the first loads of keys and values go out while q is on its way (or
+      // before it, where its raw values would not stay in registers)
+      if (nseg == 0 && D == 256)
+        for (int i = 0; i < S; ++i) load_one();
       float x[D / 16][4];
       float top = 0.0f;
+      if (a.dtype == RQ_F32) {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const int64_t e = off + 16 * i + 4 * t4;
-        if (a.dtype == RQ_F32) {
-          const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + e);
+        for (int i = 0; i < D / 16; ++i) {
+          const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + off +
+                                                            16 * i + 4 * t4);
           x[i][0] = v.x;
           x[i][1] = v.y;
           x[i][2] = v.z;
           x[i][3] = v.w;
-        } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + e);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + off +
+                                                          16 * i + 4 * t4);
+          x[i][0] = __uint_as_float(v.x);  // unpacked below
+          x[i][1] = __uint_as_float(v.y);
+        }
+      }
+      if (nseg == 0 && D < 256)
+        for (int i = 0; i < S; ++i) load_one();
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        if (a.dtype != RQ_F32) {
+          const uint32_t lo = __float_as_uint(x[i][0]), hi = __float_as_uint(x[i][1]);
           if (a.dtype == RQ_F16) {
-            const float2 f0 = half_pair(v.x), f1 = half_pair(v.y);
+            const float2 f0 = half_pair(lo), f1 = half_pair(hi);
             x[i][0] = f0.x;
             x[i][1] = f0.y;
             x[i][2] = f1.x;
             x[i][3] = f1.y;
           } else {
-            x[i][0] = __uint_as_float(v.x << 16);
-            x[i][1] = __uint_as_float(v.x & 0xFFFF0000u);
-            x[i][2] = __uint_as_float(v.y << 16);
-            x[i][3] = __uint_as_float(v.y & 0xFFFF0000u);
+            x[i][0] = __uint_as_float(lo << 16);
+            x[i][1] = __uint_as_float(lo & 0xFFFF0000u);
+            x[i][2] = __uint_as_float(hi << 16);
+            x[i][3] = __uint_as_float(hi & 0xFFFF0000u);
           }
         }
 #pragma unroll
@@ -482,6 +540,8 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
     for (int i = 0; i < D / 8; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
+    const int n_all = length_of(b);
+    const int len = n_all < 0 ? 0 : n_all < kv ? n_all : kv;  // places every row sees
     float m = -INFINITY, l = 0.0f;
     float vref = 0x1p-112f;  // power of two at or above every vs so far
 
@@ -624,21 +684,23 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
                       (o[2 * i][1] + o[2 * i][3]) * back, (o[2 * i + 1][1] + o[2 * i + 1][3]) * back);
     __syncthreads();
 
-    // which CTAs share this segment
-    int64_t parts = 1, cta0 = 0, s0 = 0;
-    if (!a.direct) {
+    // which CTAs share this segment, from CTA cta0 on; its first part lies in
+    // that CTA's second set of rows where the CTA's work began earlier
+    int64_t cta0 = blockIdx.x - part;
+    bool second = false;
+    if (cut == kRun) {
       const int n = tail.item_start[seg.item + 1] - tail.item_start[seg.item];
-      s0 = (int64_t)tail.item_start[seg.item] * a.kv_heads + (int64_t)seg.head * n;
-      cta0 = ((s0 + 1) * ctas - 1) / units;
-      parts = ((s0 + n) * ctas - 1) / units - cta0 + 1;
+      const int64_t s0 =
+          (int64_t)tail.item_start[seg.item] * a.kv_heads + (int64_t)seg.head * n;
+      cta0 = ((s0 + 1) * grid - 1) / units;
+      parts = (int)(((s0 + n) * grid - 1) / units - cta0) + 1;
+      part = (int)(blockIdx.x - cta0);
+      second = units * cta0 / grid < s0;
     }
     constexpr int kVec = D / 4;
     constexpr int kPartRow = D + 4;  // output, then max and sum
     // A partial row set of this segment, by part number.
-    auto part_at = [&](int64_t p) -> int64_t {
-      const int64_t cta = cta0 + p;
-      return cta * 2 + (p == 0 && units * cta / ctas < s0 ? 1 : 0);
-    };
+    auto part_at = [&](int64_t p) -> int64_t { return (cta0 + p) * 2 + (p == 0 && second ? 1 : 0); };
     // Join this thread's piece of `count` partials, `step` parts apart from
     // part p0 on, eight loads in flight at a time; in part order.
     auto join = [&](int64_t p0, int64_t step, int count, int r, int d, float4& v, float& mx,
@@ -691,23 +753,37 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
       mx[k] = -INFINITY;
       sum[k] = 0.0f;
       if (!mine[k]) continue;
-#pragma unroll 4
-      for (int w = 0; w < W; ++w)
-        merge(v[k], mx[k], sum[k], *reinterpret_cast<const float4*>(&tail.o[w][r][d]),
-              make_float2(tail.m[w][r], tail.l[w][r]), tail.c[r]);
+      float mw[W];
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        mw[w] = tail.m[w][r];
+        mx[k] = fmaxf(mx[k], mw[w]);
+      }
+      const float cr = tail.c[r], base = mx[k] == -INFINITY ? 0.0f : mx[k];
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float f = ex2((mw[w] - base) * cr);
+        const float4 ov = *reinterpret_cast<const float4*>(&tail.o[w][r][d]);
+        v[k].x = fmaf(ov.x, f, v[k].x);
+        v[k].y = fmaf(ov.y, f, v[k].y);
+        v[k].z = fmaf(ov.z, f, v[k].z);
+        v[k].w = fmaf(ov.w, f, v[k].w);
+        // a warp whose scores are all NaN has no maximum, but its sum counts
+        sum[k] += mw[w] == -INFINITY ? tail.l[w][r] : tail.l[w][r] * f;
+      }
     }
     bool last = true;
     if (parts > 1) {
       // Two levels, so that no CTA reads more than a few dozen partials: the
       // last of each kJoin neighbours joins theirs, the last of those joins
       // the groups.
-      const int64_t p = blockIdx.x - cta0, first_of = p / kJoin * kJoin;
-      const int members = (int)(parts - first_of < kJoin ? parts - first_of : kJoin);
-      const int groups = (int)((parts + kJoin - 1) / kJoin);
+      const int first_of = part / kJoin * kJoin;
+      const int members = min(parts - first_of, kJoin);
+      const int groups = (parts + kJoin - 1) / kJoin;
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
         const int i = tid + k * G::kThreads, r = i / kVec, d = (i % kVec) * 4;
-        if (mine[k]) store_part(part_at(p), r, d, v[k], mx[k], sum[k]);
+        if (mine[k]) store_part(part_at(part), r, d, v[k], mx[k], sum[k]);
       }
       const int64_t slot = part_at(first_of);
       last = arrive(a.counter + slot, (unsigned int)members);
@@ -758,7 +834,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
         }
       }
     }
-    if (seg.left == 0) break;
+    if (seg.left <= 0) break;
     __syncthreads();  // the joined rows are read before the next segment's are written
     next(seg);
   }
@@ -839,6 +915,8 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
   a.q = call.q;
   a.out = call.out;
   a.q_stride = call.q_stride;
+  a.q_bytes = (((int64_t)call.batch * call.new_tokens - 1) * call.q_stride +
+               (int64_t)call.q_heads * c.head_dim) * (call.dtype == RQ_F32 ? 4 : 2);
   a.ks = c.k_scale;
   a.vs = c.v_scale;
   a.table = call.page_table;

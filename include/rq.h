@@ -432,7 +432,7 @@ rq_status rq_kv_read(const rq_kv_cache *cache_host, int dtype, const int64_t *sl
  * sizes before a stream capture); they are joined in a fixed order, so equal
  * calls give equal bits.
  * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_QTYPE (dtype or format),
- * RQ_ERR_ALLOC, RQ_ERR_CUDA, RQ_ERR_ARCH (no tensor maps). */
+ * RQ_ERR_ALLOC, RQ_ERR_CUDA. */
 rq_status rq_cache_attention(rq_ctx *ctx, const rq_kv_cache *cache_host, int dtype,
                              const void *q, int64_t q_stride, void *out, int batch,
                              int new_tokens, int q_heads, const int32_t *page_table,
@@ -528,9 +528,9 @@ rq_status rq_ctx_trace_kinds(rq_ctx *ctx, unsigned int mask);
 rq_status rq_ctx_trace_end(rq_ctx *ctx, int64_t *counts_host, double *ms_host);
 
 /* Synchronise `stream`, then report and clear the library's device error
- * word: RQ_ERR_TIMEOUT if a GEMM, GEMV or attention pipeline wait, or the
- * one-pass quantization's grid barrier, exceeded its time limit (the kernel
- * then stopped early and its output is incomplete), RQ_ERR_INDEX if a cache
+ * word: RQ_ERR_TIMEOUT if a GEMM or GEMV pipeline wait, or the one-pass
+ * quantization's grid barrier, exceeded its time limit (the kernel then
+ * stopped early and its output is incomplete), RQ_ERR_INDEX if a cache
  * or attention kernel met a slot, page or position outside its array (it
  * went on without it), RQ_ERR_CUDA if the synchronisation itself failed,
  * RQ_OK otherwise. */

@@ -8,9 +8,7 @@
 // formats are exact in f16, so the two products run on f16 tensor
 // instructions with f32 sums: an f32 operand (q, p vs) is split into a high
 // and a low f16 part, 22 bits in all, which occupy two rows of the tile.
-#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cudaTypedefs.h>
 
 #include <cmath>
 #include <cstdlib>
@@ -22,10 +20,11 @@ namespace rq {
 
 namespace {
 
-// bit 0: a pipeline wait ran out; bit 1: an index outside its array
+// bit 1: an index outside its array
 __device__ unsigned int g_attn_error = 0;
 
 constexpr int kKeys = 16;            // keys of a unit: one warp's step
+constexpr int kCtas = 2;             // per SM
 constexpr int kRows = 8;             // query rows of a segment
 constexpr int kMaxItems = 1024;
 constexpr int kJoin = 8;             // partials joined at once
@@ -34,6 +33,7 @@ struct AttnArgs {
   const void* q;
   void* out;
   int64_t q_stride, q_bytes;
+  const uint8_t *k, *v;
   const float *ks, *vs;
   const int32_t *table, *length;
   const unsigned long long* tree;
@@ -45,7 +45,6 @@ struct AttnArgs {
   int direct;  // one CTA per segment, no splitting
   float* part;
   unsigned int* counter;
-  uint64_t wait_limit_ns;
 };
 
 template <int D>
@@ -53,9 +52,10 @@ struct Geometry {
   static constexpr int kPanel = D < 128 ? D : 128;  // bytes of a row in one swizzled panel
   static constexpr int kPanels = D / kPanel;
   static constexpr int kBytes = kKeys * D;          // codes of K (or V) in a unit
-  // as many warps as the registers of an SM hold: the output rows alone are
-  // D / 2 registers a thread, the query rows D / 4
-  static constexpr int kWarps = D == 64 ? 16 : D == 128 ? 12 : 8;
+  // Two CTAs per SM, so that one streams while the other begins or joins a
+  // segment, and as many warps as the registers hold: the output rows alone
+  // are D / 2 registers a thread, the query rows D / 4.
+  static constexpr int kWarps = D == 64 ? 8 : D == 128 ? 6 : 4;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStages = D == 256 ? 2 : 3;  // units in flight per warp
   static constexpr int kRing = kWarps * kStages * 2 * kBytes;
@@ -70,7 +70,6 @@ struct Tail {
   float o[kWarps][kRows][D + 4];
   float m[kWarps][kRows], l[kWarps][kRows];
   float c[kRows];
-  uint64_t full[kWarps][kStages];
   int flag;
   int warp_sum[kWarps], warp_most[kWarps];
   int item_start[kMaxItems + 1];  // units before each item, for one kv head
@@ -97,7 +96,7 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                     uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -159,21 +158,40 @@ __device__ __forceinline__ void codes_across(uint32_t w, uint32_t& a, uint32_t& 
   }
 }
 
-// Byte offset of 16-byte chunk c of row r in a panel of rows of kPanel bytes,
-// as the tensor map's swizzle lays it down.
+// Byte offset of 16-byte chunk c of row r in a panel of rows of PANEL bytes:
+// eight rows' chunks of one column lie in different banks.
 template <int PANEL>
 __device__ __forceinline__ uint32_t swizzled(int r, int c) {
   if constexpr (PANEL == 128) return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
   return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int row,
-                                         int plane, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(row), "r"(plane), "r"(bar)
-      : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// All but the newest N groups of copies have landed.
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A unit's 16 rows, which lie one after another, into its panels: lane l
+// takes 16-byte pieces l, l + 32, ...  The swizzle's terms of the lane and of
+// the piece fall on separate bits, so each piece's place is `dst` (the
+// lane's, of the first piece) with constants.
+template <int D>
+__device__ __forceinline__ void copy_rows(uint32_t dst, const uint8_t* src) {
+  constexpr int kPieces = kKeys * D / 512;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    constexpr int kRowsPer = 512 / D;  // rows that a warp's pieces span
+    const uint32_t to = D == 64 ? dst + i * 512
+                                : (dst ^ (((i * kRowsPer) & 7) << 4)) + i * kRowsPer * 128;
+    copy16(to, src + i * 512);
+  }
 }
 
 // (v, mx, sum) joined with another partial row: its output piece, and its
@@ -230,15 +248,14 @@ __device__ __forceinline__ void prefetch_l2(const void* base, int64_t bytes) {
 // to finish, in part order, from partial (max, sum, output) rows in scratch.
 //
 // Within a CTA the warps take units in turn, each with its own ring of units
-// in flight (TMA, refilled by the warp itself, on into the next segment) and
-// a softmax of its own, so that nothing is exchanged inside the loop; their
-// results are joined when the segment ends.  A warp's 16-row tile holds the
+// in flight (asynchronous copies, on into the next segment) and a softmax of
+// its own, so that nothing is exchanged inside the loop; their results are
+// joined when the segment ends.  A warp's 16-row tile holds the
 // high f16 parts of 8 query rows and below them their low parts: an f32 row
 // costs no product more than an f16 one would.
 template <int D, bool I8>
-__global__ void __launch_bounds__(Geometry<D>::kThreads, 1)
-attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-            const AttnArgs a) {
+__global__ void __launch_bounds__(Geometry<D>::kThreads, kCtas)
+attn_kernel(const AttnArgs a) {
   using G = Geometry<D>;
   using TailT = Tail<D>;
   constexpr int W = G::kWarps, S = G::kStages;
@@ -247,9 +264,6 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = smem_u32(smem) + warp * (S * 2 * G::kBytes);
 
-  if (lane == 0)
-    for (int i = 0; i < S; ++i) mbar_init(smem_u32(&tail.full[warp][i]), 1);
-  mbar_fence_init();
   pdl_wait();
   pdl_trigger();
 
@@ -395,13 +409,12 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
 
   // -------- the warp's loads, S units ahead of its products
   Segment ld = seg;
-  int unit = ld.first + warp;  // next unit to load
-  int window = -1, pages_of = 0;  // lane i: page of unit window + i W
-  bool more = true;
-  int issued = 0;  // units loaded so far
-  auto page_window = [&](int from) {
-    window = from;
-    const int64_t u = from + (int64_t)lane * W;
+  int unit = ld.first + warp;          // next unit to load
+  int in_window = 32, pages_of = 0;    // lane i: page of the window's unit i, W units apart
+  int ld_stage = 0;
+  auto page_window = [&]() {
+    in_window = 0;
+    const int64_t u = unit + (int64_t)lane * W;
     pages_of = 0;
     if (u < ld.end && u * kKeys < ld.kv) {
       const int64_t page = a.table[(int64_t)(ld.item / a.row_tiles) * a.max_pages +
@@ -412,46 +425,39 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
         atomicOr(&g_attn_error, 2u);
     }
   };
-  auto load_one = [&]() {  // loads the warp's next unit, if there is one
-    while (more && unit >= ld.end) {
-      if (ld.left > 0) {
-        next(ld);
-        unit = warp;
-        window = -1;
-      } else {
-        more = false;
-      }
+  const int page_mask = (1 << a.lg_page) - 1;
+  // where this lane's first piece of a unit goes
+  const int piece_row = lane * 16 / D, piece_chunk = lane * 16 % D / 16;
+  const uint32_t piece = (piece_chunk / (G::kPanel / 16)) * (kKeys * G::kPanel) +
+                         swizzled<G::kPanel>(piece_row, piece_chunk % (G::kPanel / 16));
+  auto load_one = [&]() {  // starts copying the warp's next unit, if there is one
+    while (unit >= ld.end && ld.left > 0) {
+      next(ld);
+      unit = warp;
+      in_window = 32;
     }
-    if (!more) return;
-    if (window < 0 || unit >= window + 32 * W) page_window(unit);
-    const int page = __shfl_sync(0xFFFFFFFFu, pages_of, (unit - window) / W);
-    const int st = issued % S;
-    if (lane == 0) {
-      const uint32_t bar = smem_u32(&tail.full[warp][st]);
-      if (unit * kKeys >= ld.kv) {
-        mbar_arrive(bar);  // an unused sequence: nothing to load
-      } else {
-        const int off = (unit * kKeys) & ((1 << a.lg_page) - 1);
-        const int plane = page * a.kv_heads + ld.head;
-        const int64_t row = ((int64_t)plane << a.lg_page) + off;
-        const uint32_t kd = ring + st * (2 * G::kBytes), vd = kd + G::kBytes;
-        const uint32_t sd = smem_u32(&tail.scale[warp][st][0][0]);
-        mbar_arrive_expect_tx(bar, 2 * G::kBytes + 2 * kKeys * 4);
-#pragma unroll
-        for (int h = 0; h < G::kPanels; ++h) {
-          tma_rows(kd + h * kKeys * G::kPanel, &map_k, h * G::kPanel, off, plane, bar);
-          tma_rows(vd + h * kKeys * G::kPanel, &map_v, h * G::kPanel, off, plane, bar);
-        }
-        bulk_g2s(sd, a.ks + row, kKeys * 4, bar);
-        bulk_g2s(sd + kKeys * 4, a.vs + row, kKeys * 4, bar);
-      }
+    if (unit < ld.end && ld.kv > 0) {
+      if (in_window == 32) page_window();
+      const int page = __shfl_sync(0xFFFFFFFFu, pages_of, in_window);
+      ++in_window;
+      const int64_t row = ((int64_t)(page * a.kv_heads + ld.head) << a.lg_page) +
+                          ((unit * kKeys) & page_mask);
+      const uint32_t to = ring + ld_stage * (2 * G::kBytes) + piece;
+      copy_rows<D>(to, a.k + row * D + lane * 16);
+      copy_rows<D>(to + G::kBytes, a.v + row * D + lane * 16);
+      if (lane < 8)
+        copy16(smem_u32(&tail.scale[warp][ld_stage][0][0]) + lane * 16,
+               (lane < 4 ? a.ks : a.vs - 16) + row + lane * 4);
     }
-    ++issued;
+    copy_commit();  // a group for every unit, there or not
+    ld_stage = ld_stage == S - 1 ? 0 : ld_stage + 1;
     unit += W;
   };
+
   const int g = lane >> 2, t4 = lane & 3;
-  bool ok = true;
-  int done = 0;  // units taken so far
+  const uint32_t matrix =
+      swizzled<G::kPanel>(((lane >> 3) & 1) * 8 + (lane & 7), lane >> 4);
+  int st = 0;  // ring stage of the next unit
   for (int nseg = 0;; ++nseg) {
     const int b = seg.item / a.row_tiles, rt = seg.item - b * a.row_tiles;
     const int kv = seg.kv;
@@ -546,30 +552,27 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
     float vref = 0x1p-112f;  // power of two at or above every vs so far
 
     for (int u = seg.first + warp; u < seg.end; u += W) {
-      const int st = done % S;
-      if (ok)
-        ok = mbar_wait_fast(smem_u32(&tail.full[warp][st]), (uint32_t)(done / S) & 1u,
-                            a.wait_limit_ns, &g_attn_error);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
-      ++done;
+      copy_wait<S - 1>();
+      __syncwarp();
       const int first = u * kKeys;  // place of the first key
       const bool all = first + kKeys <= len;
       const uint32_t kd = ring + st * (2 * G::kBytes), vd = kd + G::kBytes;
+      // ldmatrix's matrix lane / 8: keys 0-7 or 8-15, 16 dims i or i + 1 (i
+      // even, so that it only flips bits of the swizzled place)
+      auto matrix_at = [&](uint32_t base, int i) -> uint32_t {
+        constexpr int kChunks = G::kPanel / 16;
+        return ((base + matrix) ^ ((i % kChunks) << 4)) + (i / kChunks) * (kKeys * G::kPanel);
+      };
       // ---- scores
       float s[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[i][k] = 0.0f;
-      // ldmatrix's matrix lane / 8: keys 0-7 or 8-15, 16 dims i or i + 1
-      const int mrow = ((lane >> 3) & 1) * 8 + (lane & 7);
 #pragma unroll
       for (int i = 0; i < D / 16; i += 2) {
-        const int chunk = i + (lane >> 4);
         uint32_t w[4];
-        ldsm4(w, kd + (chunk / (G::kPanel / 16)) * (kKeys * G::kPanel) +
-                     swizzled<G::kPanel>(mrow, chunk % (G::kPanel / 16)));
+        ldsm4(w, matrix_at(kd, i));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t b0, b1;
@@ -586,15 +589,26 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
       float x[4] = {(s[0][0] + s[0][2]) * ka.x, (s[0][1] + s[0][3]) * ka.y,
                     (s[1][0] + s[1][2]) * kb.x, (s[1][1] + s[1][3]) * kb.y};
       float vv[4] = {va.x, va.y, vb.x, vb.y};
-      uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};  // V bytes of keys that exist
       if (!all) {
-        keep[0] = keep[1] = 0u;
+        // what lies past the last place: no scores, and zeros in place of V
+        // (its codes could be anything, and 0 * NaN is not 0)
+        if (first + kKeys > kv) {
+          const int keys = kv > first ? kv - first : 0;
+          for (int i = keys * (D / 16) + lane; i < kKeys * (D / 16); i += 32) {
+            const int r = i / (D / 16), ch = i % (D / 16);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             vd + (ch / (G::kPanel / 16)) * (kKeys * G::kPanel) +
+                             swizzled<G::kPanel>(r, ch % (G::kPanel / 16))),
+                         "r"(0)
+                         : "memory");
+          }
+          __syncwarp();
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int place = first + 8 * (k >> 1) + 2 * t4 + (k & 1);
           const int draft = place - len;
           bool see = place < kv;
-          if (see) keep[k >> 1] |= 0xFFFFu << (16 * (k & 1));
           if (draft >= 0)
             see = see && (a.tree == nullptr ? draft <= tok
                                             : (draft < 64 && ((bits >> draft) & 1ull) != 0ull));
@@ -607,10 +621,11 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
       // ---- running maximum, and the values' scales relative to theirs; both
       // seldom move, so that most units pay one vote for them
       const float xm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-      float vt = 0.0f;
+      if (__any_sync(0xFFFFFFFFu,
+                     xm > m || fmaxf(fmaxf(vv[0], vv[1]), fmaxf(vv[2], vv[3])) > vref)) {
+        float vt = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) vt = fmaxf(vt, vv[k] <= 1e37f ? vv[k] : 0.0f);  // no NaN, Inf
-      if (__any_sync(0xFFFFFFFFu, xm > m || vt > vref)) {
+        for (int k = 0; k < 4; ++k) vt = fmaxf(vt, vv[k] <= 1e37f ? vv[k] : 0.0f);  // no NaN, Inf
         float mn = fmaxf(xm, __shfl_xor_sync(0xFFFFFFFFu, xm, 1));
         mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 2));
         mn = fmaxf(mn, m);
@@ -647,13 +662,8 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
       // ---- output
 #pragma unroll
       for (int i = 0; i < D / 16; i += 2) {
-        const int chunk = i + (lane >> 4);
         uint32_t v[4];
-        ldsm4t(v, vd + (chunk / (G::kPanel / 16)) * (kKeys * G::kPanel) +
-                      swizzled<G::kPanel>(mrow, chunk % (G::kPanel / 16)));
-        if (!all)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] &= keep[k & 1];
+        ldsm4t(v, matrix_at(vd, i));
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t e0, e1, o0, o1;
@@ -664,6 +674,7 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
         }
       }
       __syncwarp();
+      st = st == S - 1 ? 0 : st + 1;
       load_one();
     }
 
@@ -838,50 +849,9 @@ attn_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ C
     __syncthreads();  // the joined rows are read before the next segment's are written
     next(seg);
   }
-
-  // a warp that gave up: its copies in flight are waited for before it ends
-  if (!ok)
-    for (; done < issued; ++done)
-      mbar_wait(smem_u32(&tail.full[warp][done % S]), (uint32_t)(done / S) & 1u, a.wait_limit_ns,
-                &g_attn_error);
 }
 
 // ------------------------------------------------------------- host side --
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
-}
-
-// 3-D map over codes [pages * kv_heads][page_size][head_dim], box = one panel
-// of `box` rows; coordinates stay below 2^31 however long the cache is.
-bool codes_map(CUtensorMap* map, const void* base, const rq_kv_cache& c, int box) {
-  auto fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size,
-                              (cuuint64_t)(c.pages * c.kv_heads)};
-  const cuuint64_t strides[2] = {(cuuint64_t)c.head_dim,
-                                 (cuuint64_t)c.head_dim * (cuuint64_t)c.page_size};
-  const cuuint32_t panel = c.head_dim < 128 ? 64 : 128;
-  const cuuint32_t boxes[3] = {panel, (cuuint32_t)box, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r =
-      fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, boxes,
-         estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-         panel == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
 
 int lg(int v) {
   int l = 0;
@@ -889,13 +859,10 @@ int lg(int v) {
   return l;
 }
 
-using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const AttnArgs);
-
 template <int D, bool I8>
-rq_status launch_d(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, unsigned grid,
-                   cudaStream_t st) {
+rq_status launch_d(const AttnArgs& a, unsigned grid, cudaStream_t st) {
   constexpr int bytes = Geometry<D>::kRing + (int)sizeof(Tail<D>);
-  static_assert(bytes <= 232448, "shared memory of one CTA");
+  static_assert(kCtas * (bytes + 1024) <= 233472, "shared memory of an SM");
   static bool ready = false;
   if (!ready) {
     if (cudaFuncSetAttribute(attn_kernel<D, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -904,7 +871,7 @@ rq_status launch_d(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs&
     ready = true;
   }
   return launch_kernel(attn_kernel<D, I8>, dim3(grid), dim3(Geometry<D>::kThreads), (size_t)bytes,
-                       st, mk, mv, a);
+                       st, a);
 }
 
 }  // namespace
@@ -917,6 +884,8 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
   a.q_stride = call.q_stride;
   a.q_bytes = (((int64_t)call.batch * call.new_tokens - 1) * call.q_stride +
                (int64_t)call.q_heads * c.head_dim) * (call.dtype == RQ_F32 ? 4 : 2);
+  a.k = static_cast<const uint8_t*>(c.k);
+  a.v = static_cast<const uint8_t*>(c.v);
   a.ks = c.k_scale;
   a.vs = c.v_scale;
   a.table = call.page_table;
@@ -934,14 +903,10 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
   a.pages = c.pages;
   a.scale_log2 = (float)((double)call.scale * 1.4426950408889634);
   a.dtype = call.dtype;
-  a.wait_limit_ns = kWaitLimitNs;
-
-  CUtensorMap mk, mv;
-  if (!codes_map(&mk, c.k, c, kKeys) || !codes_map(&mv, c.v, c, kKeys)) return RQ_ERR_ARCH;
 
   const int64_t items = (int64_t)call.batch * a.row_tiles;
   const int64_t segments = items * c.kv_heads;
-  int64_t grid = device_sm_count();
+  int64_t grid = (int64_t)kCtas * device_sm_count();
   a.direct = items > kMaxItems;
   if (a.direct) {
     grid = segments;
@@ -956,11 +921,11 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
   const unsigned g = (unsigned)grid;
   const bool i8 = c.format == RQ_KV_I8;
   switch (c.head_dim) {
-    case 64: return i8 ? launch_d<64, true>(mk, mv, a, g, st) : launch_d<64, false>(mk, mv, a, g, st);
+    case 64: return i8 ? launch_d<64, true>(a, g, st) : launch_d<64, false>(a, g, st);
     case 128:
-      return i8 ? launch_d<128, true>(mk, mv, a, g, st) : launch_d<128, false>(mk, mv, a, g, st);
+      return i8 ? launch_d<128, true>(a, g, st) : launch_d<128, false>(a, g, st);
     default:
-      return i8 ? launch_d<256, true>(mk, mv, a, g, st) : launch_d<256, false>(mk, mv, a, g, st);
+      return i8 ? launch_d<256, true>(a, g, st) : launch_d<256, false>(a, g, st);
   }
 }
 
@@ -1009,7 +974,7 @@ rq_status read_and_clear_attn_error() {
   if (v == 0) return RQ_OK;
   const unsigned int zero = 0;
   if (cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(zero)) != cudaSuccess) return RQ_ERR_CUDA;
-  return (v & 1u) ? RQ_ERR_TIMEOUT : RQ_ERR_INDEX;
+  return RQ_ERR_INDEX;
 }
 
 }  // namespace rq

@@ -528,9 +528,9 @@ rq_status rq_ctx_trace_kinds(rq_ctx *ctx, unsigned int mask);
 rq_status rq_ctx_trace_end(rq_ctx *ctx, int64_t *counts_host, double *ms_host);
 
 /* Synchronise `stream`, then report and clear the library's device error
- * word: RQ_ERR_TIMEOUT if a GEMM or GEMV pipeline wait, or the one-pass
- * quantization's grid barrier, exceeded its time limit (the kernel then
- * stopped early and its output is incomplete), RQ_ERR_INDEX if a cache
+ * word: RQ_ERR_TIMEOUT if a GEMM, GEMV or attention pipeline wait, or the
+ * one-pass quantization's grid barrier, exceeded its time limit (the kernel
+ * then stopped early and its output is incomplete), RQ_ERR_INDEX if a cache
  * or attention kernel met a slot, page or position outside its array (it
  * went on without it), RQ_ERR_CUDA if the synchronisation itself failed,
  * RQ_OK otherwise. */

@@ -8,44 +8,26 @@
 // formats are exact in f16, so the two products run on f16 tensor
 // instructions with f32 sums: an f32 operand (q, p vs) is split into a high
 // and a low f16 part, 22 bits in all, which occupy two rows of the tile.
-#include <cuda_bf16.h>
 
 #include <cmath>
 #include <cstdlib>
 
-#include "rq_device.cuh"
-#include "rq_internal.h"
+#include "rq_attn.cuh"
 
 namespace rq {
 
 namespace {
 
-// bit 1: an index outside its array
+// bit 0: a pipeline wait ran out; bit 1: an index outside its array
 __device__ unsigned int g_attn_error = 0;
 
 constexpr int kKeys = 16;            // keys of a unit: one warp's step
 constexpr int kCtas = 2;             // per SM
 constexpr int kRows = 8;             // query rows of a segment
-constexpr int kMaxItems = 1024;
 constexpr int kJoin = 8;             // partials joined at once
 
-struct AttnArgs {
-  const void* q;
-  void* out;
-  int64_t q_stride, q_bytes;
-  const uint8_t *k, *v;
-  const float *ks, *vs;
-  const int32_t *table, *length;
-  const unsigned long long* tree;
-  int batch, new_tokens, q_heads, kv_heads, group, rows, row_tiles;
-  int max_pages, lg_page;
-  int64_t pages;
-  float scale_log2;
-  int dtype;
-  int direct;  // one CTA per segment, no splitting
-  float* part;
-  unsigned int* counter;
-};
+// From this many query rows per kv head on, rq_attn_rows.cu's kernel runs.
+constexpr int kManyRows = 64;
 
 template <int D>
 struct Geometry {
@@ -71,16 +53,8 @@ struct Tail {
   float m[kWarps][kRows], l[kWarps][kRows];
   float c[kRows];
   int flag;
-  int warp_sum[kWarps], warp_most[kWarps];
-  int item_start[kMaxItems + 1];  // units before each item, for one kv head
-  int length[kMaxItems];          // the sequences' lengths
+  CutShared cut;
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -101,61 +75,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// (a, b) as an f16 pair and, in `lo`, what the rounding left over.
-__device__ __forceinline__ uint32_t split_half2(float a, float b, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(a, b);
-  const float2 f = __half22float2(h);
-  lo = pack_half2(a - f.x, b - f.y);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Codes as f16 pairs, exactly.  E4M3 has a conversion; 8-bit integers, biased
-// by 128, become the low mantissa bits of 1024 + b, less 1152.
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)two));
-  return h;
-}
-
-__device__ __forceinline__ uint32_t minus_1152(uint32_t h) {
-  const uint32_t bias = 0x64806480u;
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h),
-                            *reinterpret_cast<const __half2*>(&bias));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// Bytes (0, 1) and (2, 3) of a word.
-template <bool I8>
-__device__ __forceinline__ void codes_in_order(uint32_t w, uint32_t& a, uint32_t& b) {
-  if constexpr (I8) {
-    const uint32_t u = w ^ 0x80808080u;
-    a = minus_1152(__byte_perm(u, 0x64646464u, 0x4140));
-    b = minus_1152(__byte_perm(u, 0x64646464u, 0x4342));
-  } else {
-    a = e4m3_pair(w & 0xFFFFu);
-    b = e4m3_pair(w >> 16);
-  }
-}
-
-// Bytes (0, 2) and (1, 3).
-template <bool I8>
-__device__ __forceinline__ void codes_across(uint32_t w, uint32_t& a, uint32_t& b) {
-  if constexpr (I8) {
-    const uint32_t u = w ^ 0x80808080u;
-    a = minus_1152(__byte_perm(u, 0x64646464u, 0x4240));
-    b = minus_1152(__byte_perm(u, 0x64646464u, 0x4341));
-  } else {
-    const uint32_t x = e4m3_pair(w & 0xFFFFu), y = e4m3_pair(w >> 16);
-    a = __byte_perm(x, y, 0x5410);
-    b = __byte_perm(x, y, 0x7632);
-  }
 }
 
 // Byte offset of 16-byte chunk c of row r in a panel of rows of PANEL bytes:
@@ -194,58 +113,12 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, const uint8_t* src) {
   }
 }
 
-// (v, mx, sum) joined with another partial row: its output piece, and its
-// maximum and sum.
-__device__ __forceinline__ void merge(float4& v, float& mx, float& sum, const float4& ov,
-                                      const float2& ml, float c) {
-  const float mn = fmaxf(mx, ml.x);
-  if (mn == -INFINITY) {
-    sum += ml.y;  // 0, or the NaN of a row whose scores all are
-    return;
-  }
-  const float f0 = ex2((mx - mn) * c), f1 = ex2((ml.x - mn) * c);
-  v.x = v.x * f0 + ov.x * f1;
-  v.y = v.y * f0 + ov.y * f1;
-  v.z = v.z * f0 + ov.z * f1;
-  v.w = v.w * f0 + ov.w * f1;
-  sum = sum * f0 + ml.y * f1;
-  mx = mn;
-}
-
-// Places that row tile rt of a sequence of n cached tokens may see (0: an
-// unused sequence).  Up to 64 new tokens every tile takes them all: a chain
-// is then cut as a tree of one branch is, and gives its bits.
-__device__ __forceinline__ int tile_places(const AttnArgs& a, int n, int rt) {
-  if (n < 0) return 0;
-  const int64_t most = (int64_t)a.max_pages << a.lg_page;
-  int64_t kv = (int64_t)n + a.new_tokens;
-  if (kv > most) {
-    atomicOr(&g_attn_error, 2u);
-    kv = most;
-  }
-  if (a.new_tokens > 64) {
-    int last = (rt + 1) * kRows;
-    last = (last < a.rows ? last : a.rows) - 1;
-    const int64_t end = (int64_t)n + last / a.group + 1;
-    kv = end < kv ? end : kv;
-  }
-  return (int)(kv < 0x7FFFFF00 ? kv : 0x7FFFFF00);
-}
-
-// Fetch what the launch reads first and only once, q and the page table, into
-// L2 while the lengths are on their way.
-__device__ __forceinline__ void prefetch_l2(const void* base, int64_t bytes) {
-  const int64_t line = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 128;
-  if (line < bytes)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(base) + line));
-}
-
 // ------------------------------------------------------------ the kernel --
 //
-// Work is the sequence of segments (sequence, row tile, kv head), each a run
-// of 16-key units.  How it is cut (Split) follows from the lengths, which only
-// the device knows; a segment cut between CTAs is joined by the last of them
-// to finish, in part order, from partial (max, sum, output) rows in scratch.
+// How the work is cut between CTAs: Cutter.  A segment cut between CTAs is
+// joined by the last of them to finish, in part order, from partial (max,
+// sum, output) rows in scratch.  A round of its warps takes about 0.6 us,
+// joining or beginning a segment 2.5 us.
 //
 // Within a CTA the warps take units in turn, each with its own ring of units
 // in flight (asynchronous copies, on into the next segment) and a softmax of
@@ -267,145 +140,12 @@ attn_kernel(const AttnArgs a) {
   pdl_wait();
   pdl_trigger();
 
-  const int items = a.batch * a.row_tiles;
   prefetch_l2(a.q, a.q_bytes);
   prefetch_l2(a.table, (int64_t)a.batch * a.max_pages * 4);
-  int64_t units = 1;
-  int most = 1;  // units of the longest segment
-  if (!a.direct) {
-    int carry = 0;
-    for (int base = 0; base < items; base += G::kThreads) {
-      const int i = base + tid;
-      int n = 0;
-      if (i < items) {
-        const int bi = i / a.row_tiles, ri = i - bi * a.row_tiles;
-        const int len = a.length[bi];
-        if (ri == 0) tail.length[bi] = len;
-        n = (tile_places(a, len, ri) + kKeys - 1) / kKeys;
-        if (n < 1) n = 1;
-      }
-      int scan = n, top = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xFFFFFFFFu, scan, o);
-        if (lane >= o) scan += x;
-        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      }
-      __syncthreads();
-      if (lane == 31) {
-        tail.warp_sum[warp] = scan;
-        tail.warp_most[warp] = top;
-      }
-      __syncthreads();
-      int before = carry;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const int x = tail.warp_sum[w];
-        if (w < warp) before += x;
-        carry += x;
-        most = max(most, tail.warp_most[w]);
-      }
-      if (i < items) tail.item_start[i] = before + scan - n;
-    }
-    if (tid == 0) tail.item_start[items] = carry;
-    units = (int64_t)carry * a.kv_heads;
-    __syncthreads();
-  }
-
-  // How the segments are cut:
-  //   kParts: every segment in up to `split` equal parts, one CTA each;
-  //   kWhole: a run of whole segments per CTA;
-  //   kRun: an equal run of units per CTA, wherever segments begin or end.
-  // Joining a segment over CTAs costs as much as about 4 rounds of its CTA's
-  // warps (2.5 us against 0.6 us a round), and so does beginning another one:
-  // no part is made smaller than that, segments that short stay whole, and a
-  // run may begin and end inside segments only where that evens out more.
-  enum { kParts, kWhole, kRun };
-  constexpr int kRound = 4 * W;  // units of 4 rounds
-  const int64_t segments = (int64_t)items * a.kv_heads;
-  const int grid = (int)gridDim.x;
-  int cut = kWhole, split = 1;
-  if (!a.direct) {
-    if (segments <= grid) {
-      split = min(grid / (int)segments, (most + kRound - 1) / kRound);
-      const int64_t even = (units + (int64_t)grid * W - 1) / ((int64_t)grid * W);
-      cut = (most + split * W - 1) / (split * W) <= even + 4 ? kParts : kRun;
-    } else if (most > kRound) {
-      cut = kRun;
-    }
-  }
-
-  // A segment's part in this CTA's work: units [first, end) of it.
-  struct Segment {
-    int item, head, first, end, kv;
-    int64_t left;  // units (kRun) or segments (else) after it
-  };
-  auto length_of = [&](int bi) -> int { return a.direct ? a.length[bi] : tail.length[bi]; };
-  auto open = [&](Segment& g) {  // item, head, first and left are set
-    const int bi = g.item / a.row_tiles;
-    g.kv = tile_places(a, length_of(bi), g.item - bi * a.row_tiles);
-    const int n = g.kv < 1 ? 1 : (g.kv + kKeys - 1) / kKeys;
-    if (cut == kRun) {
-      g.end = g.left < n - g.first ? g.first + (int)g.left : n;
-      g.left -= g.end - g.first;
-    } else {
-      g.end = n;
-      --g.left;
-    }
-  };
-  auto next = [&](Segment& g) {
-    if (++g.head == a.kv_heads) {
-      g.head = 0;
-      ++g.item;
-    }
-    g.first = 0;
-    open(g);
-  };
+  Cutter<kRows, kKeys, W, 4> cutter(a, tail.cut);
+  cutter.template choose<G::kThreads>();
   Segment seg;
-  int parts = 1, part = 0;  // kParts: of this CTA's segment
-  seg.first = 0;
-  if (cut == kRun) {
-    const int64_t u0 = units * blockIdx.x / grid, u1 = units * (blockIdx.x + 1) / grid;
-    if (u0 >= u1) return;
-    int lo = 0, hi = items - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((int64_t)tail.item_start[mid] * a.kv_heads <= u0)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    const int n = tail.item_start[lo + 1] - tail.item_start[lo];
-    const int rest = (int)(u0 - (int64_t)tail.item_start[lo] * a.kv_heads);
-    seg.item = lo;
-    seg.head = rest / n;
-    seg.first = rest - seg.head * n;
-    seg.left = u1 - u0;
-    open(seg);
-  } else {
-    int64_t s0 = blockIdx.x, s1 = s0 + 1;
-    if (cut == kParts) {
-      s0 /= split;
-      s1 = s0 + 1;
-      part = (int)blockIdx.x - (int)s0 * split;
-      if (s0 >= segments) return;
-    } else if (!a.direct) {
-      s0 = segments * blockIdx.x / grid;
-      s1 = segments * (blockIdx.x + 1) / grid;
-      if (s0 >= s1) return;
-    }
-    seg.item = (int)(s0 / a.kv_heads);
-    seg.head = (int)(s0 - (int64_t)seg.item * a.kv_heads);
-    seg.left = s1 - s0;
-    open(seg);
-    if (cut == kParts) {
-      const int n = seg.end;
-      parts = min(split, (n + kRound - 1) / kRound);
-      if (part >= parts) return;
-      seg.first = (int)((int64_t)n * part / parts);
-      seg.end = (int)((int64_t)n * (part + 1) / parts);
-    }
-  }
+  if (!cutter.begin(seg)) return;
 
   // -------- the warp's loads, S units ahead of its products
   Segment ld = seg;
@@ -416,14 +156,7 @@ attn_kernel(const AttnArgs a) {
     in_window = 0;
     const int64_t u = unit + (int64_t)lane * W;
     pages_of = 0;
-    if (u < ld.end && u * kKeys < ld.kv) {
-      const int64_t page = a.table[(int64_t)(ld.item / a.row_tiles) * a.max_pages +
-                                   ((u * kKeys) >> a.lg_page)];
-      if (page >= 0 && page < a.pages)
-        pages_of = (int)page;
-      else
-        atomicOr(&g_attn_error, 2u);
-    }
+    if (u < ld.end && u * kKeys < ld.kv) pages_of = page_of(a, ld.item / a.row_tiles, u * kKeys);
   };
   const int page_mask = (1 << a.lg_page) - 1;
   // where this lane's first piece of a unit goes
@@ -432,7 +165,7 @@ attn_kernel(const AttnArgs a) {
                          swizzled<G::kPanel>(piece_row, piece_chunk % (G::kPanel / 16));
   auto load_one = [&]() {  // starts copying the warp's next unit, if there is one
     while (unit >= ld.end && ld.left > 0) {
-      next(ld);
+      cutter.next(ld);
       unit = warp;
       in_window = 32;
     }
@@ -546,7 +279,7 @@ attn_kernel(const AttnArgs a) {
     for (int i = 0; i < D / 8; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
-    const int n_all = length_of(b);
+    const int n_all = cutter.length(b);
     const int len = n_all < 0 ? 0 : n_all < kv ? n_all : kv;  // places every row sees
     float m = -INFINITY, l = 0.0f;
     float vref = 0x1p-112f;  // power of two at or above every vs so far
@@ -695,19 +428,10 @@ attn_kernel(const AttnArgs a) {
                       (o[2 * i][1] + o[2 * i][3]) * back, (o[2 * i + 1][1] + o[2 * i + 1][3]) * back);
     __syncthreads();
 
-    // which CTAs share this segment, from CTA cta0 on; its first part lies in
-    // that CTA's second set of rows where the CTA's work began earlier
-    int64_t cta0 = blockIdx.x - part;
-    bool second = false;
-    if (cut == kRun) {
-      const int n = tail.item_start[seg.item + 1] - tail.item_start[seg.item];
-      const int64_t s0 =
-          (int64_t)tail.item_start[seg.item] * a.kv_heads + (int64_t)seg.head * n;
-      cta0 = ((s0 + 1) * grid - 1) / units;
-      parts = (int)(((s0 + n) * grid - 1) / units - cta0) + 1;
-      part = (int)(blockIdx.x - cta0);
-      second = units * cta0 / grid < s0;
-    }
+    const auto share = cutter.sharers(seg);
+    const int64_t cta0 = share.cta0;
+    const int parts = share.parts, part = share.part;
+    const bool second = share.second;
     constexpr int kVec = D / 4;
     constexpr int kPartRow = D + 4;  // output, then max and sum
     // A partial row set of this segment, by part number.
@@ -847,7 +571,7 @@ attn_kernel(const AttnArgs a) {
     }
     if (seg.left <= 0) break;
     __syncthreads();  // the joined rows are read before the next segment's are written
-    next(seg);
+    cutter.next(seg);
   }
 }
 
@@ -879,6 +603,10 @@ rq_status launch_d(const AttnArgs& a, unsigned grid, cudaStream_t st) {
 rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cudaStream_t st) {
   const rq_kv_cache& c = *call.cache;
   AttnArgs a = {};
+  static void* word = nullptr;
+  if (word == nullptr && cudaGetSymbolAddress(&word, g_attn_error) != cudaSuccess)
+    return RQ_ERR_CUDA;
+  a.error = static_cast<unsigned int*>(word);
   a.q = call.q;
   a.out = call.out;
   a.q_stride = call.q_stride;
@@ -903,6 +631,9 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
   a.pages = c.pages;
   a.scale_log2 = (float)((double)call.scale * 1.4426950408889634);
   a.dtype = call.dtype;
+
+  if (a.rows >= kManyRows && c.head_dim <= 128)
+    return launch_attention_rows(a, c.head_dim, c.format == RQ_KV_I8, scratch, st);
 
   const int64_t items = (int64_t)call.batch * a.row_tiles;
   const int64_t segments = items * c.kv_heads;
@@ -974,7 +705,7 @@ rq_status read_and_clear_attn_error() {
   if (v == 0) return RQ_OK;
   const unsigned int zero = 0;
   if (cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(zero)) != cudaSuccess) return RQ_ERR_CUDA;
-  return RQ_ERR_INDEX;
+  return (v & 1u) ? RQ_ERR_TIMEOUT : RQ_ERR_INDEX;
 }
 
 }  // namespace rq

@@ -1,0 +1,366 @@
+// rq_attn.cuh -- what the attention kernels share: their arguments, how work
+// is cut between CTAs, and the exact conversion of cache codes (sm_103a).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "rq_device.cuh"
+#include "rq_internal.h"
+
+namespace rq {
+
+constexpr int kMaxItems = 1024;  // (sequence, row tile) pairs that a launch cuts by length
+
+struct AttnArgs {
+  const void* q;
+  void* out;
+  int64_t q_stride, q_bytes;
+  const uint8_t *k, *v;
+  const float *ks, *vs;
+  const int32_t *table, *length;
+  const unsigned long long* tree;
+  int batch, new_tokens, q_heads, kv_heads, group, rows, row_tiles;
+  int max_pages, lg_page;
+  int64_t pages;
+  float scale_log2;
+  int dtype;
+  int direct;  // one CTA per segment, no splitting
+  float* part;
+  unsigned int* counter;
+  unsigned int* error;  // bit 1: an index outside its array
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// (a, b) as an f16 pair and, in `lo`, what the rounding left over.
+__device__ __forceinline__ uint32_t split_half2(float a, float b, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  lo = pack_half2(a - f.x, b - f.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Codes as f16 pairs, exactly.  E4M3 has a conversion; 8-bit integers, biased
+// by 128, become the low mantissa bits of 1024 + b, less 1152.
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)two));
+  return h;
+}
+
+__device__ __forceinline__ uint32_t minus_1152(uint32_t h) {
+  const uint32_t bias = 0x64806480u;
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h),
+                            *reinterpret_cast<const __half2*>(&bias));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Bytes (0, 1) and (2, 3) of a word.
+template <bool I8>
+__device__ __forceinline__ void codes_in_order(uint32_t w, uint32_t& a, uint32_t& b) {
+  if constexpr (I8) {
+    const uint32_t u = w ^ 0x80808080u;
+    a = minus_1152(__byte_perm(u, 0x64646464u, 0x4140));
+    b = minus_1152(__byte_perm(u, 0x64646464u, 0x4342));
+  } else {
+    a = e4m3_pair(w & 0xFFFFu);
+    b = e4m3_pair(w >> 16);
+  }
+}
+
+// Bytes (0, 2) and (1, 3).
+template <bool I8>
+__device__ __forceinline__ void codes_across(uint32_t w, uint32_t& a, uint32_t& b) {
+  if constexpr (I8) {
+    const uint32_t u = w ^ 0x80808080u;
+    a = minus_1152(__byte_perm(u, 0x64646464u, 0x4240));
+    b = minus_1152(__byte_perm(u, 0x64646464u, 0x4341));
+  } else {
+    const uint32_t x = e4m3_pair(w & 0xFFFFu), y = e4m3_pair(w >> 16);
+    a = __byte_perm(x, y, 0x5410);
+    b = __byte_perm(x, y, 0x7632);
+  }
+}
+
+// (v, mx, sum) joined with another partial row: its output piece, and its
+// maximum and sum.
+__device__ __forceinline__ void merge(float4& v, float& mx, float& sum, const float4& ov,
+                                      const float2& ml, float c) {
+  const float mn = fmaxf(mx, ml.x);
+  if (mn == -INFINITY) {
+    sum += ml.y;  // 0, or the NaN of a row whose scores all are
+    return;
+  }
+  const float f0 = ex2((mx - mn) * c), f1 = ex2((ml.x - mn) * c);
+  v.x = v.x * f0 + ov.x * f1;
+  v.y = v.y * f0 + ov.y * f1;
+  v.z = v.z * f0 + ov.z * f1;
+  v.w = v.w * f0 + ov.w * f1;
+  sum = sum * f0 + ml.y * f1;
+  mx = mn;
+}
+
+// Fetch what the launch reads first and only once, q and the page table, into
+// L2 while the lengths are on their way.
+__device__ __forceinline__ void prefetch_l2(const void* base, int64_t bytes) {
+  const int64_t line = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 128;
+  if (line < bytes)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const uint8_t*>(base) + line));
+}
+
+// The page of place `place` of sequence b; page 0 where the table's entry
+// lies outside the cache.
+__device__ __forceinline__ int page_of(const AttnArgs& a, int b, int64_t place) {
+  const int64_t page = a.table[(int64_t)b * a.max_pages + (place >> a.lg_page)];
+  if (page >= 0 && page < a.pages) return (int)page;
+  atomicOr(a.error, 2u);
+  return 0;
+}
+
+// A segment's part in a CTA's work: units [first, end) of it.
+struct Segment {
+  int item, head, first, end;
+  int kv;        // places its rows may see, 0: an unused sequence
+  int64_t left;  // units (kRun) or segments (else) of the CTA's work after it
+};
+
+struct CutShared {
+  int warp_sum[32], warp_most[32];
+  int cut, split;
+  int64_t units;                  // of all segments
+  int item_start[kMaxItems + 1];  // units before each item, for one kv head
+  int length[kMaxItems];          // the sequences' lengths
+};
+
+// Work is the sequence of segments (sequence, row tile of ROWS rows, kv
+// head), each a run of units of KEYS keys, of which a CTA takes STEP in a
+// round.  How it is cut follows from the lengths, which only the device
+// knows:
+//   kParts: every segment in up to `split` equal parts, one CTA each;
+//   kWhole: a run of whole segments per CTA;
+//   kRun: an equal run of units per CTA, wherever segments begin or end.
+// Joining a segment over CTAs costs as much as about ROUNDS rounds, and so
+// does beginning another one: no part is made smaller than that, segments
+// that short stay whole, and a run may begin and end inside segments only
+// where that evens out more.
+template <int ROWS, int KEYS, int STEP, int ROUNDS>
+struct Cutter {
+  enum { kParts, kWhole, kRun };
+  static constexpr int kLeast = ROUNDS * STEP;
+  const AttnArgs& a;
+  CutShared& sh;
+
+  __device__ __forceinline__ Cutter(const AttnArgs& args, CutShared& shared)
+      : a(args), sh(shared) {}
+
+  // Places that row tile rt of a sequence of n cached tokens may see.  Up to
+  // 64 new tokens every tile takes them all: a chain is then cut as a tree of
+  // one branch is, and gives its bits.
+  __device__ __forceinline__ int places(int n, int rt) const {
+    if (n < 0) return 0;
+    const int64_t limit = (int64_t)a.max_pages << a.lg_page;
+    int64_t kv = (int64_t)n + a.new_tokens;
+    if (kv > limit) {
+      atomicOr(a.error, 2u);
+      kv = limit;
+    }
+    if (a.new_tokens > 64) {
+      int last = (rt + 1) * ROWS;
+      last = (last < a.rows ? last : a.rows) - 1;
+      const int64_t end = (int64_t)n + last / a.group + 1;
+      kv = end < kv ? end : kv;
+    }
+    return (int)(kv < 0x7FFFFF00 ? kv : 0x7FFFFF00);
+  }
+
+  __device__ __forceinline__ int units_of(int kv) const {
+    return kv < 1 ? 1 : (kv + KEYS - 1) / KEYS;
+  }
+
+  __device__ __forceinline__ int length(int b) const { return a.direct ? a.length[b] : sh.length[b]; }
+
+  // Reads the lengths and chooses the cut (all threads of the CTA; THREADS a
+  // multiple of 32).
+  template <int THREADS>
+  __device__ __forceinline__ void choose() {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int items = a.batch * a.row_tiles, grid = (int)gridDim.x;
+    if (a.direct) {
+      if (tid == 0) {
+        sh.cut = kWhole;
+        sh.split = 1;
+      }
+      __syncthreads();
+      return;
+    }
+    int carry = 0, most = 1;
+    for (int base = 0; base < items; base += THREADS) {
+      const int i = base + tid;
+      int n = 0;
+      if (i < items) {
+        const int b = i / a.row_tiles, rt = i - b * a.row_tiles;
+        const int len = a.length[b];
+        if (rt == 0) sh.length[b] = len;
+        n = units_of(places(len, rt));
+      }
+      int scan = n, top = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+        if (lane >= o) scan += x;
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      }
+      __syncthreads();
+      if (lane == 31) {
+        sh.warp_sum[warp] = scan;
+        sh.warp_most[warp] = top;
+      }
+      __syncthreads();
+      int before = carry;
+#pragma unroll
+      for (int w = 0; w < THREADS / 32; ++w) {
+        const int x = sh.warp_sum[w];
+        if (w < warp) before += x;
+        carry += x;
+        most = max(most, sh.warp_most[w]);
+      }
+      if (i < items) sh.item_start[i] = before + scan - n;
+    }
+    if (tid == 0) {
+      const int64_t units = (int64_t)carry * a.kv_heads;
+      const int64_t segments = (int64_t)items * a.kv_heads;
+      int cut = kWhole, split = 1;
+      if (segments <= grid) {
+        split = min(grid / (int)segments, (most + kLeast - 1) / kLeast);
+        const int64_t even = (units + (int64_t)grid * STEP - 1) / ((int64_t)grid * STEP);
+        cut = (most + split * STEP - 1) / (split * STEP) <= even + ROUNDS ? kParts : kRun;
+      } else if (most > kLeast) {
+        cut = kRun;
+      }
+      sh.item_start[items] = carry;
+      sh.units = units;
+      sh.cut = cut;
+      sh.split = split;
+    }
+    __syncthreads();
+  }
+
+  __device__ __forceinline__ void open(Segment& g) const {  // item, head, first, left are set
+    const int b = g.item / a.row_tiles;
+    g.kv = places(length(b), g.item - b * a.row_tiles);
+    const int n = units_of(g.kv);
+    if (sh.cut == kRun) {
+      g.end = g.left < n - g.first ? g.first + (int)g.left : n;
+      g.left -= g.end - g.first;
+    } else {
+      g.end = n;
+      --g.left;
+    }
+  }
+
+  __device__ __forceinline__ void next(Segment& g) const {
+    if (++g.head == a.kv_heads) {
+      g.head = 0;
+      ++g.item;
+    }
+    g.first = 0;
+    open(g);
+  }
+
+  // kParts: units [first, end) of a segment of n that are part `part` of it.
+  __device__ __forceinline__ bool part_of(int n, int part, int* parts, int* first, int* end) const {
+    *parts = min(sh.split, (n + kLeast - 1) / kLeast);
+    if (part >= *parts) return false;
+    *first = (int)((int64_t)n * part / *parts);
+    *end = (int)((int64_t)n * (part + 1) / *parts);
+    return true;
+  }
+
+  // This CTA's first segment; false if it has no work.
+  __device__ __forceinline__ bool begin(Segment& g) const {
+    const int grid = (int)gridDim.x, items = a.batch * a.row_tiles;
+    g.first = 0;
+    if (sh.cut == kRun) {
+      const int64_t u0 = sh.units * blockIdx.x / grid, u1 = sh.units * (blockIdx.x + 1) / grid;
+      if (u0 >= u1) return false;
+      int lo = 0, hi = items - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int64_t)sh.item_start[mid] * a.kv_heads <= u0)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const int n = sh.item_start[lo + 1] - sh.item_start[lo];
+      const int rest = (int)(u0 - (int64_t)sh.item_start[lo] * a.kv_heads);
+      g.item = lo;
+      g.head = rest / n;
+      g.first = rest - g.head * n;
+      g.left = u1 - u0;
+      open(g);
+      return true;
+    }
+    const int segments = items * a.kv_heads;
+    int s0 = (int)blockIdx.x, s1 = s0 + 1;
+    if (sh.cut == kParts) {
+      s0 /= sh.split;
+      s1 = s0 + 1;
+      if (s0 >= segments) return false;
+    } else if (!a.direct) {
+      s0 = (int)((int64_t)segments * blockIdx.x / grid);
+      s1 = (int)((int64_t)segments * (blockIdx.x + 1) / grid);
+      if (s0 >= s1) return false;
+    }
+    g.item = s0 / a.kv_heads;
+    g.head = s0 - g.item * a.kv_heads;
+    g.left = s1 - s0;
+    open(g);
+    if (sh.cut == kParts) {
+      int parts;
+      return part_of(g.end, (int)blockIdx.x - s0 * sh.split, &parts, &g.first, &g.end);
+    }
+    return true;
+  }
+
+  // Which CTAs share the segment: `parts` from CTA cta0 on, of which this is
+  // number `part`; second: the first one's part lies in that CTA's second set
+  // of partial rows, because its work began in an earlier segment.
+  struct Sharers {
+    int64_t cta0;
+    int parts, part;
+    bool second;
+  };
+  __device__ __forceinline__ Sharers sharers(const Segment& g) const {
+    Sharers r = {(int64_t)blockIdx.x, 1, 0, false};
+    if (sh.cut == kRun) {
+      const int grid = (int)gridDim.x;
+      const int n = sh.item_start[g.item + 1] - sh.item_start[g.item];
+      const int64_t s0 = (int64_t)sh.item_start[g.item] * a.kv_heads + (int64_t)g.head * n;
+      r.cta0 = ((s0 + 1) * grid - 1) / sh.units;
+      r.parts = (int)(((s0 + n) * grid - 1) / sh.units - r.cta0) + 1;
+      r.part = (int)(blockIdx.x - r.cta0);
+      r.second = sh.units * r.cta0 / grid < s0;
+    } else if (sh.cut == kParts) {
+      r.part = (int)blockIdx.x % sh.split;
+      r.cta0 = (int64_t)blockIdx.x - r.part;
+      int first, end;
+      part_of(units_of(g.kv), r.part, &r.parts, &first, &end);
+    }
+    return r;
+  }
+};
+
+// rq_attn_rows.cu: the kernel for many query rows per sequence.
+rq_status launch_attention_rows(AttnArgs a, int head_dim, bool i8, AttnScratch* scratch,
+                                cudaStream_t st);
+
+}  // namespace rq

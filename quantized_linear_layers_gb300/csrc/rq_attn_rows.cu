@@ -1,0 +1,960 @@
+// rq_attn_rows.cu -- attention of many query rows over the paged quantized
+// cache on tcgen05 (sm_103a): drafted trees and prompts, whose heads of one kv
+// head and tokens of one sequence make up tiles of 128 rows.
+//
+// The mathematics is that of rq_attn.cu.  Per CTA up to two tiles of 128 rows
+// share 64 keys at a time:
+//   warps 0-3, 4-7   softmax of tile 0 and 1: a thread owns a row
+//   warps 8-11       codes of K and V to f16 in shared memory, two units deep
+//   warp 12          allocates TMEM; one thread issues the products
+//   warp 13          the scales
+//   warp 14          asks codes into L2, three units ahead (15 idle)
+// S = Q K^T (A = Q from shared memory) lands in one of two TMEM buffers per
+// row tile; its softmax writes P over it, as f16 high and low parts for f32
+// rows (64 + 64 keys in S's 64 columns), and P V takes A = P from TMEM and
+// adds to O in TMEM.  While a row tile's softmax runs, the tensor cores work
+// on its next scores and on the other tile.  f32 rows take both products
+// twice (Q high and low, P high and low), 16-bit rows once.
+#include "rq_attn.cuh"
+
+namespace rq {
+
+namespace {
+
+constexpr int kKeys = 64;                 // keys of a unit
+constexpr int kTileRows = 128;            // rows of one accumulator
+constexpr int kRows = 2 * kTileRows;      // rows of a segment
+constexpr int kSoft = 256;                // softmax threads
+constexpr int kThreads = 512;
+// Registers a thread of each group of four warps takes: 256 x 168 + 128 x 96
+// + 128 x 80 = 512 x 128, the launch's own.
+constexpr int kSoftRegs = 160, kConvertRegs = 104, kIssueRegs = 88;
+constexpr int kScales = 4;                // units whose scales are kept
+constexpr int kAhead = 3;                 // units that codes are asked into L2 ahead of use
+constexpr float kLazy = 8.0f;             // a maximum is kept while scores pass it by less than 2^8
+constexpr float kUp = 128.0f;             // weights p vs / vref are kept 2^7 times larger in f16
+
+template <int D, bool SPLIT>
+struct Layout {
+  static constexpr int kPanels = D / 64;                      // 128-byte panels of an f16 row
+  static constexpr int kQPanel = kTileRows * 128;
+  static constexpr int kQTile = kPanels * kQPanel;            // one part of one row tile
+  static constexpr int kQ = 2 * (SPLIT ? 2 : 1) * kQTile;
+  static constexpr int kPanel = kKeys * 128;
+  static constexpr int kB = kPanels * kPanel;                 // K (or V) of a unit
+  static constexpr int kTail = kQ + 4 * kB;                   // two units of K and V
+};
+
+struct RowsTail {
+  float ks[kScales][kKeys], vs[kScales][kKeys];  // vs relative to vref, times kUp
+  float vref[kScales];
+  uint64_t q_full[2], k_full[2], k_free[2], v_full[2], v_free[2], sc_full[kScales];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2], drained;
+  uint32_t tmem;
+  int flag;
+  CutShared cut;
+};
+
+// ------------------------------------------------------------ PTX wrappers --
+
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Matrix descriptors, 128-byte swizzle.  K-major (rows of 128 bytes along the
+// product's inner dimension, 8-row groups 1024 bytes apart) for Q and K;
+// N-major for V (rows of 128 bytes along the output's columns, one per key:
+// 8-key groups 1024 bytes apart, 64-column panels `panel` bytes apart).  The
+// upper word is one constant (stride 1024, version 1, swizzle 128 bytes), the
+// lower one the address and the leading offset, in 16-byte units: steps inside
+// a tile are additions to it.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_k_major(uint32_t addr) {
+  return ((addr & 0x3FFFFu) >> 4) | 1u << 16;
+}
+__device__ __forceinline__ uint32_t desc_n_major(uint32_t addr, uint32_t panel) {
+  return ((addr & 0x3FFFFu) >> 4) | (panel >> 4) << 16;
+}
+
+// kind::f16: D = f32 (bit 4), A = B = f16 (0), B's major-ness at bit 16,
+// N >> 3 at bits 17-22, M >> 4 at bits 24-28.
+constexpr uint32_t instr(int n, bool b_n_major) {
+  return (1u << 4) | (b_n_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 |
+         (uint32_t)(kTileRows >> 4) << 24;
+}
+
+// One thread of the warp.  Branching on this rather than on a lane number
+// lets the operands of the products stay in uniform registers: measured, a
+// 128 x 64 x 16 product then issues every 48 cycles instead of 95, a
+// 128 x 128 x 16 one every 64, which is what they take.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0u;
+}
+
+template <bool ADD>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "n"(kDescHigh), "n"(ADD ? 1 : 0)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "n"(kDescHigh), "r"(add)
+      : "memory");
+}
+
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+        "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+        "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]),
+        "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]),
+        "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float* v) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+        "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+        "=r"(u[14]), "=r"(u[15])
+      : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* u) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
+      "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]),
+      "r"(u[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Pairs of f32, one instruction for both.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+// The pair w as f16 high parts and, in `lo`, f16 low parts.  The high part is
+// w cut to f16's 11 bits, whose conversion is exact, so that the rest w - high
+// is as well: 21 bits in all, for one logic operation a value where rounding
+// would cost a conversion back.
+__device__ __forceinline__ uint32_t cut_half2(float2 w, uint32_t& lo) {
+  const float2 h = make_float2(__uint_as_float(__float_as_uint(w.x) & 0xFFFFE000u),
+                               __uint_as_float(__float_as_uint(w.y) & 0xFFFFE000u));
+  const float2 r = add2(w, make_float2(-h.x, -h.y));
+  lo = pack_half2(r.x, r.y);
+  return pack_half2(h.x, h.y);
+}
+
+__device__ __forceinline__ void soft_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory");
+}
+
+// A warp's wait for a barrier phase; after one wait has run out, no further
+// one is made, so that every role comes to its end.
+__device__ __forceinline__ void wait(bool& ok, const uint64_t& bar, uint32_t parity,
+                                     unsigned int* error) {
+  if (ok) {  // (in line: a call would spill what the roles hold in registers)
+    const uint32_t addr = smem_u32(&bar);
+    bool done = mbar_try_wait(addr, parity & 1u);
+    if (!done) {
+      const uint64_t t0 = globaltimer();
+      do {
+        done = mbar_try_wait(addr, parity & 1u);
+      } while (!done && globaltimer() - t0 <= kWaitLimitNs);
+      if (!done) atomicOr(error, 1u);
+    }
+    ok = done;
+  }
+  ok = __all_sync(0xFFFFFFFFu, ok);
+}
+
+// The pages of a segment's units, four 16-key boxes each: every lane holds the
+// (page, kv head) plane of one box of the present window of 32 boxes (8 units)
+// and of the next, so that no fetch waits for the page table.
+struct PageWindow {
+  int cur, nxt, window;
+  __device__ __forceinline__ int load(const AttnArgs& a, const Segment& g, int w, int lane) const {
+    const int64_t place = ((int64_t)w * 32 + lane) * 16;
+    return place < g.kv ? page_of(a, g.item / a.row_tiles, place) * a.kv_heads + g.head : 0;
+  }
+  __device__ __forceinline__ void open(const AttnArgs& a, const Segment& g, int u, int lane) {
+    window = u >> 3;
+    cur = load(a, g, window, lane);
+    nxt = load(a, g, window + 1, lane);
+  }
+  __device__ __forceinline__ void step(const AttnArgs& a, const Segment& g, int u, int lane) {
+    if (u >> 3 == window) return;
+    window = u >> 3;
+    cur = nxt;
+    nxt = load(a, g, window + 1, lane);
+  }
+  __device__ __forceinline__ int plane(int box) const {  // of the present window
+    return __shfl_sync(0xFFFFFFFFu, cur, box & 31);
+  }
+};
+
+// ------------------------------------------------------------- the kernel --
+
+template <int D, bool I8, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a) {
+  using L = Layout<D, SPLIT>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  RowsTail& tail = *reinterpret_cast<RowsTail*>(smem + L::kTail);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t q_base = smem_u32(smem);
+  const uint32_t kv_base = q_base + L::kQ;  // unit u: K at (u & 1) 2 kB, V behind it
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&tail.q_full[i]), 4);
+      mbar_init(smem_u32(&tail.k_full[i]), 4);
+      mbar_init(smem_u32(&tail.v_full[i]), 4);
+      mbar_init(smem_u32(&tail.k_free[i]), 1);
+      mbar_init(smem_u32(&tail.v_free[i]), 1);
+      mbar_init(smem_u32(&tail.pv_done[i]), 1);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(smem_u32(&tail.s_full[i][j]), 1);
+        mbar_init(smem_u32(&tail.p_full[i][j]), 4);
+      }
+    }
+    for (int i = 0; i < kScales; ++i) mbar_init(smem_u32(&tail.sc_full[i]), 1);
+    mbar_init(smem_u32(&tail.drained), 1);
+    mbar_fence_init();
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(&tail.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tail.tmem;
+  pdl_wait();
+  pdl_trigger();
+  prefetch_l2(a.q, a.q_bytes);
+  prefetch_l2(a.table, (int64_t)a.batch * a.max_pages * 4);
+  Cutter<kRows, kKeys, 1, 8> cutter(a, tail.cut);
+  cutter.template choose<kThreads>();
+  Segment seg;
+  const bool work = cutter.begin(seg);
+  bool ok = true;
+
+  if (warp < 8)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+  else if (warp < 12)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+
+  if (work && warp < 8) {
+    // ------------------------------------------------------- softmax ----
+    const int w = warp >> 2, quad = warp & 3;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const uint32_t s_col = tmem + w * 256 + lanes, o_col = s_col + 128;
+    uint32_t units = 0, segs = 0;  // of this row tile so far
+    uint32_t all_units = 0;        // of the CTA: the scales' ring
+    for (bool first_seg = true;; first_seg = false) {
+      const int b = seg.item / a.row_tiles, rt = seg.item - b * a.row_tiles;
+      const int row0 = rt * kRows + w * kTileRows;
+      const int n_units = seg.end - seg.first;
+      float l = 0.0f, ref = -INFINITY, c = 0.0f, vref = 0x1p-112f;
+      if (row0 < a.rows) {
+        // ---- this warp's 32 query rows, to f16 parts in shared memory
+        constexpr int E = D / 32;
+        const int my_row = row0 + quad * 32 + lane;
+        const bool live = my_row < a.rows;
+        const int tok = live ? my_row / a.group : 0;
+        const int64_t my_off =
+            ((int64_t)b * a.new_tokens + tok) * a.q_stride +
+            (int64_t)(seg.head * a.group + (live ? my_row - tok * a.group : 0)) * D;
+#pragma unroll 4
+        for (int r = 0; r < 32; ++r) {
+          const int64_t off = __shfl_sync(0xFFFFFFFFu, my_off, r) + lane * E;
+          const bool row_live = row0 + quad * 32 + r < a.rows;
+          float x[E];
+          if (a.dtype == RQ_F32) {
+            const float* p = static_cast<const float*>(a.q) + off;
+            if constexpr (E == 4) {
+              const float4 v = *reinterpret_cast<const float4*>(p);
+              x[0] = v.x;
+              x[1] = v.y;
+              x[2] = v.z;
+              x[3] = v.w;
+            } else {
+              const float2 v = *reinterpret_cast<const float2*>(p);
+              x[0] = v.x;
+              x[1] = v.y;
+            }
+          } else {
+            const uint16_t* p = static_cast<const uint16_t*>(a.q) + off;
+            uint32_t raw[E / 2];
+            if constexpr (E == 4) {
+              const uint2 v = *reinterpret_cast<const uint2*>(p);
+              raw[0] = v.x;
+              raw[1] = v.y;
+            } else {
+              raw[0] = *reinterpret_cast<const uint32_t*>(p);
+            }
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+              if (a.dtype == RQ_F16) {
+                const float2 f = half_pair(raw[i]);
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+              } else {
+                x[2 * i] = __uint_as_float(raw[i] << 16);
+                x[2 * i + 1] = __uint_as_float(raw[i] & 0xFFFF0000u);
+              }
+            }
+          }
+          float top = 0.0f;
+#pragma unroll
+          for (int i = 0; i < E; ++i) {
+            if (!row_live) x[i] = 0.0f;
+            top = fmaxf(top, fabsf(x[i]));
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+          // times a power of two: the largest entry in [2^13, 2^14)
+          int e = 0;
+          if (top > 0.0f && top <= 3.4e38f) {
+            e = 13 - (int)((__float_as_uint(top) >> 23) & 0xFFu) + 127;
+            e = e < -126 ? -126 : e > 100 ? 100 : e;
+          }
+          const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+          if (lane == r) {
+            c = fmaxf(a.scale_log2 / up, 0x1p-126f);
+            if (!(top <= 3.4e38f)) c = NAN;  // an infinity in q
+          }
+          const int row = quad * 32 + r;
+          const int byte = lane * E * 2;
+          const uint32_t at = q_base + w * ((SPLIT ? 2 : 1) * L::kQTile) +
+                              (byte >> 7) * L::kQPanel + row * 128 +
+                              ((((byte >> 4) & 7) ^ (row & 7)) << 4) + (byte & 15);
+          uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+          for (int i = 0; i < E / 2; ++i)
+            hi[i] = split_half2(x[2 * i] * up, x[2 * i + 1] * up, lo[i]);
+          if constexpr (E == 4) {
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1])
+                         : "memory");
+            if (SPLIT)
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + L::kQTile), "r"(lo[0]),
+                           "r"(lo[1])
+                           : "memory");
+          } else {
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(hi[0]) : "memory");
+            if (SPLIT)
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + L::kQTile), "r"(lo[0]) : "memory");
+          }
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&tail.q_full[w]));
+
+        unsigned long long bits = 0;
+        if (live && a.tree != nullptr) bits = a.tree[(int64_t)b * a.new_tokens + tok];
+        const int kv = seg.kv;
+        const int n_all = cutter.length(b);
+        const int len = n_all < 0 ? 0 : n_all < kv ? n_all : kv;
+
+        for (int u = 0; u < n_units; ++u) {
+          const uint32_t sc = (all_units + u) % kScales;
+          const uint32_t buf = units & 1u;
+          wait(ok, tail.sc_full[sc], (all_units + u) / kScales, a.error);
+          wait(ok, tail.s_full[w][buf], units >> 1, a.error);
+          fence_after();
+          float x[kKeys];
+          tmem_ld32(s_col + buf * kKeys, x);
+          tmem_ld32(s_col + buf * kKeys + 32, x + 32);
+          tmem_ld_wait();
+          const float4* ks = reinterpret_cast<const float4*>(tail.ks[sc]);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < kKeys / 4; ++i) {
+            const float4 k4 = ks[i];
+            const float2 xa = mul2(make_float2(x[4 * i], x[4 * i + 1]), make_float2(k4.x, k4.y));
+            const float2 xb = mul2(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(k4.z, k4.w));
+            x[4 * i] = xa.x;
+            x[4 * i + 1] = xa.y;
+            x[4 * i + 2] = xb.x;
+            x[4 * i + 3] = xb.y;
+          }
+          const int p0 = (seg.first + u) * kKeys;
+          const bool edge = p0 + kKeys > len;
+          if (edge) {
+            // bit k: key k of the unit is seen
+            const int before = len - p0;  // keys that every row sees
+            unsigned long long see =
+                before >= 64 ? ~0ull : before > 0 ? (1ull << before) - 1ull : 0ull;
+            if (a.tree != nullptr) {
+              if (before > -64 && before < 64)
+                see |= before >= 0 ? bits << before : bits >> -before;
+            } else {
+              const int upto = before + tok + 1;
+              if (upto > 0) see |= upto >= 64 ? ~0ull : (1ull << upto) - 1ull;
+            }
+            const int exist = kv - p0;
+            if (exist < 64) see &= exist > 0 ? (1ull << exist) - 1ull : 0ull;
+            const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (!((s0 >> i) & 1u)) x[i] = -INFINITY;
+              if (!((s1 >> i) & 1u)) x[32 + i] = -INFINITY;
+            }
+          }
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < kKeys; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], fmaxf(x[i + k], x[i + k + 4]));
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          // The reference that the row's weights are relative to moves only
+          // when a score passes it by 2^8 (f16 has room for that), so that O
+          // is seldom scaled anew.
+          const float now = mx * c;  // powers of two
+          const float vnow = tail.vref[sc];
+          const bool moves = now > ref + kLazy || vnow != vref;
+          if (__any_sync(0xFFFFFFFFu, moves)) {
+            const float to = fmaxf(ref, now);
+            const float al = ref == -INFINITY ? 0.0f : ex2(ref - to);
+            const float f = al * (vref / vnow);
+            l *= al;
+            ref = to;
+            vref = vnow;
+            if (u > 0) {
+              wait(ok, tail.pv_done[w], units - 1u, a.error);
+              fence_after();
+#pragma unroll
+              for (int d = 0; d < D; d += 16) {
+                float o[16];
+                tmem_ld16(o_col + d, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] *= f;
+                tmem_st16(o_col + d, reinterpret_cast<const uint32_t*>(o));
+              }
+              tmem_st_wait();
+            }
+          }
+          const float base = ref == -INFINITY ? 0.0f : ref;
+          const float4* vs = reinterpret_cast<const float4*>(tail.vs[sc]);
+          const float2 c2 = make_float2(c, c), nb = make_float2(-base, -base);
+          float2 l2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 v4 = vs[8 * half + i];
+              const float* xi = x + 32 * half + 4 * i;
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float2 p = fma2(make_float2(xi[2 * k], xi[2 * k + 1]), c2, nb);
+                p.x = ex2(p.x);
+                p.y = ex2(p.y);
+                l2 = add2(l2, p);
+                float2 wt = mul2(p, k == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
+                if (edge) {  // a scale under a cleared bit may be anything
+                  wt.x = p.x == 0.0f ? 0.0f : wt.x;
+                  wt.y = p.y == 0.0f ? 0.0f : wt.y;
+                }
+                if constexpr (SPLIT)
+                  hi[2 * i + k] = cut_half2(wt, lo[2 * i + k]);
+                else
+                  hi[2 * i + k] = pack_half2(wt.x, wt.y);
+              }
+            }
+            tmem_st16(s_col + buf * kKeys + 16 * half, hi);
+            if constexpr (SPLIT) tmem_st16(s_col + buf * kKeys + 32 + 16 * half, lo);
+          }
+          l += l2.x + l2.y;
+          tmem_st_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&tail.p_full[w][buf]));
+          ++units;
+        }
+        // ---- the segment's output rows
+        wait(ok, tail.pv_done[w], units - 1u, a.error);
+        fence_after();
+      }
+      all_units += n_units;
+      ++segs;
+
+      // a.part holds per CTA two sets of kRows rows of D values, reference
+      // and sum (D + 4 floats)
+      const auto share = cutter.sharers(seg);
+      const int parts = share.parts, part = share.part;
+      constexpr int kPartRow = D + 4;
+      auto set_at = [&](int p) -> float* {
+        return a.part + ((share.cta0 + p) * 2 + (p == 0 && share.second ? 1 : 0)) *
+                            (int64_t)kRows * kPartRow;
+      };
+      const int my = w * kTileRows + quad * 32 + lane;  // row of the segment
+      const int row = rt * kRows + my;
+      const bool live = row < a.rows;
+      const float back = vref * (1.0f / kUp);
+      const int tok = live ? row / a.group : 0;
+      const int64_t dst = (((int64_t)b * a.new_tokens + tok) * a.q_heads + seg.head * a.group +
+                           (live ? row - tok * a.group : 0)) * D;
+      auto store_out = [&](int64_t at, const float4& y) {
+        if (SPLIT) {
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = y;
+        } else if (a.dtype == RQ_F16) {
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+              make_uint2(pack_half2(y.x, y.y), pack_half2(y.z, y.w));
+        } else {
+          const __nv_bfloat162 h0 = __floats2bfloat162_rn(y.x, y.y);
+          const __nv_bfloat162 h1 = __floats2bfloat162_rn(y.z, y.w);
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&h0),
+                         *reinterpret_cast<const uint32_t*>(&h1));
+        }
+      };
+      if (row0 < a.rows) {
+        const float r1 = parts > 1 ? back : l == 0.0f ? 0.0f : back / l;
+#pragma unroll
+        for (int d = 0; d < D; d += 32) {
+          float o[32];
+          tmem_ld32(o_col + d, o);
+          tmem_ld_wait();
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 y =
+                  make_float4(o[i] * r1, o[i + 1] * r1, o[i + 2] * r1, o[i + 3] * r1);
+              if (parts > 1)
+                __stcg(reinterpret_cast<float4*>(set_at(part) + my * kPartRow + d + i), y);
+              else
+                store_out(dst + d + i, y);
+            }
+          }
+        }
+        if (parts > 1 && live)
+          __stcg(reinterpret_cast<float2*>(set_at(part) + my * kPartRow + D), make_float2(ref, l));
+        fence_before();
+      }
+      if (parts > 1) {
+        __threadfence();
+        soft_sync();
+        if (tid == 0) {
+          unsigned int* ctr = a.counter + (int64_t)seg.item * a.kv_heads + seg.head;
+          const unsigned int old = atomicAdd(ctr, 1u);
+          tail.flag = old == (unsigned int)(parts - 1);
+          if (tail.flag) *ctr = 0u;
+        }
+        soft_sync();
+        const bool last = tail.flag != 0;
+        __threadfence();
+        if (last) {
+          // 16 bytes of a row per thread, four rows' pieces at a time, in
+          // part order
+          constexpr int kVec = D / 4, kStep = kSoft / kVec;  // rows taken at once
+          const int d = (tid % kVec) * 4;
+          const int rows = min(kRows, a.rows - rt * kRows);
+          for (int r0 = tid / kVec; r0 < rows; r0 += 4 * kStep) {
+            float4 v[4];
+            float mx[4], sum[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+              mx[k] = -INFINITY;
+              sum[k] = 0.0f;
+            }
+            for (int p = 0; p < parts; ++p) {
+              const float* set = set_at(p);
+              float4 ov[4];
+              float2 ml[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int r = min(r0 + k * kStep, rows - 1);
+                ov[k] = __ldcg(reinterpret_cast<const float4*>(set + r * kPartRow + d));
+                ml[k] = __ldcg(reinterpret_cast<const float2*>(set + r * kPartRow + D));
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) merge(v[k], mx[k], sum[k], ov[k], ml[k], 1.0f);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = r0 + k * kStep;
+              if (r >= rows) continue;
+              const int rr = rt * kRows + r, tk = rr / a.group;
+              const float f = sum[k] == 0.0f ? 0.0f : 1.0f / sum[k];
+              store_out((((int64_t)b * a.new_tokens + tk) * a.q_heads + seg.head * a.group + rr -
+                         tk * a.group) * D + d,
+                        make_float4(v[k].x * f, v[k].y * f, v[k].z * f, v[k].w * f));
+            }
+          }
+        }
+        soft_sync();  // the flag is read before the next segment's is set
+      }
+      if (seg.left <= 0) break;
+      cutter.next(seg);
+    }
+  } else if (work && warp < 12) {
+    // --------------------------------------------------- conversion ----
+    constexpr int kChunks = D / 16;                    // 16-code chunks of a row
+    constexpr int N = kKeys * kChunks / 128;           // of K (and of V) per thread and unit
+    const int t = tid - kSoft;
+    const int chunk = t % kChunks, row_a = t / kChunks;
+    constexpr int kRowStep = 128 / kChunks;
+    // where chunk `chunk` of row r goes: 32 bytes of an f16 row
+    const uint32_t at = (chunk >> 2) * L::kPanel;
+    const int c16 = (chunk & 3) * 2;
+    uint4 kc[N], vc[N];  // the next unit's codes, on their way into registers
+    PageWindow pages;
+    const int page_mask = (1 << a.lg_page) - 1, page_bytes = D << a.lg_page;
+    const uint8_t *k_at = a.k + chunk * 16, *v_at = a.v + chunk * 16;
+    auto fetch = [&](const Segment& g, int u, uint4 (&c)[N], const uint8_t* codes) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int key = row_a + n * kRowStep;
+        const int plane = pages.plane(u * 4 + (key >> 4));
+        c[n] = make_uint4(0u, 0u, 0u, 0u);
+        if (u * kKeys + key < g.kv)
+          c[n] = ldg_nc_v4(codes + (int64_t)plane * page_bytes + ((u * kKeys + key) & page_mask) * D);
+      }
+    };
+    auto convert = [&](const uint4 (&codes)[N], uint32_t base) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int r = row_a + n * kRowStep;
+        const uint32_t words[4] = {codes[n].x, codes[n].y, codes[n].z, codes[n].w};
+        uint32_t h[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) codes_in_order<I8>(words[i], h[2 * i], h[2 * i + 1]);
+        const uint32_t to = base + at + r * 128;
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         to + ((c16 ^ (r & 7)) << 4)),
+                     "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                     : "memory");
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         to + (((c16 + 1) ^ (r & 7)) << 4)),
+                     "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
+                     : "memory");
+      }
+    };
+    pages.open(a, seg, seg.first, lane);
+    fetch(seg, seg.first, kc, k_at);
+    fetch(seg, seg.first, vc, v_at);
+    uint32_t units = 0;
+    for (int u = seg.first;;) {
+      // the unit after this one, whose codes are fetched as soon as this
+      // one's have left their registers
+      Segment after = seg;
+      int un = u + 1;
+      bool more = true;
+      if (un == seg.end) {
+        more = seg.left > 0;
+        if (more) {
+          cutter.next(after);
+          un = after.first;
+        }
+      }
+      const uint32_t buf = units & 1u;
+      const uint32_t kb = kv_base + buf * (2 * L::kB), vb = kb + L::kB;
+      wait(ok, tail.k_free[buf], (units >> 1) ^ 1u, a.error);
+      convert(kc, kb);
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&tail.k_full[buf]));
+      if (more) {
+        if (un == u + 1)
+          pages.step(a, after, un, lane);
+        else
+          pages.open(a, after, un, lane);
+        fetch(after, un, kc, k_at);
+      }
+      wait(ok, tail.v_free[buf], (units >> 1) ^ 1u, a.error);
+      convert(vc, vb);
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&tail.v_full[buf]));
+      if (!more) break;
+      fetch(after, un, vc, v_at);
+      seg = after;
+      u = un;
+      ++units;
+    }
+  } else if (work && warp == 13) {
+    // -------------------------------------------------------- scales ----
+    uint32_t units = 0;
+    const int page_mask = (1 << a.lg_page) - 1;
+    for (;;) {
+      float vref = 0x1p-112f;
+      PageWindow pages;
+      pages.open(a, seg, seg.first, lane);
+      float s[4];
+      auto fetch = [&](int u) {  // of keys lane and lane + 32
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int key = lane + 32 * n;
+          const int64_t row = ((int64_t)pages.plane(u * 4 + (key >> 4)) << a.lg_page) +
+                              ((u * kKeys + key) & page_mask);
+          s[2 * n] = s[2 * n + 1] = 0.0f;
+          if (u * kKeys + key < seg.kv) {
+            s[2 * n] = __ldg(a.ks + row);
+            s[2 * n + 1] = __ldg(a.vs + row);
+          }
+        }
+      };
+      fetch(seg.first);
+      for (int u = seg.first; u < seg.end; ++u, ++units) {
+        // value scales relative to a power of two at or above all so far;
+        // four times the next one when it moves, so that it seldom does
+        float vt = fmaxf(s[1] <= 1e37f ? s[1] : 0.0f, s[3] <= 1e37f ? s[3] : 0.0f);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) vt = fmaxf(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, o));
+        if (vt > vref) vref = __uint_as_float((__float_as_uint(vt) & 0x7F800000u) + (2u << 23));
+        const float inv = kUp / vref;
+        // the ring's place is free once the unit two before is done with
+        // (its own occupant was the one four before)
+        const uint32_t sc = units % kScales;
+        wait(ok, tail.v_free[units & 1u], (units >> 1) ^ 1u, a.error);
+        tail.ks[sc][lane] = s[0];
+        tail.ks[sc][lane + 32] = s[2];
+        tail.vs[sc][lane] = s[1] * inv;
+        tail.vs[sc][lane + 32] = s[3] * inv;
+        if (lane == 0) tail.vref[sc] = vref;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&tail.sc_full[sc]));
+        if (u + 1 < seg.end) {
+          pages.step(a, seg, u + 1, lane);
+          fetch(u + 1);
+        }
+      }
+      if (seg.left <= 0) break;
+      cutter.next(seg);
+    }
+  } else if (work && warp == 14) {
+    // -------- codes into L2, kAhead units before they are fetched: lanes
+    // 0-3 the boxes of K, 4-7 those of V
+    uint32_t units = 0;
+    const int page_mask = (1 << a.lg_page) - 1, page_bytes = D << a.lg_page;
+    for (;;) {
+      PageWindow pages;
+      pages.open(a, seg, seg.first, lane);
+      int asked = seg.first + 1;
+      for (int u = seg.first; u < seg.end; ++u, ++units) {
+        for (; asked <= u + kAhead && asked < seg.end; ++asked) {
+          pages.step(a, seg, asked, lane);
+          const int key = (lane & 3) * 16;
+          const int plane = pages.plane(asked * 4 + (lane & 3));
+          if (lane < 8 && asked * kKeys + key < seg.kv) {
+            const uint8_t* at = (lane < 4 ? a.k : a.v) + (int64_t)plane * page_bytes +
+                                ((asked * kKeys + key) & page_mask) * D;
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "n"(16 * D)
+                         : "memory");
+          }
+        }
+        wait(ok, tail.v_free[units & 1u], (units >> 1) ^ 1u, a.error);
+      }
+      if (seg.left <= 0) break;
+      cutter.next(seg);
+    }
+  } else if (work && warp == 12) {
+    // ------------------------------------------------------ products ----
+    // (the whole warp walks along, one lane issues)
+    constexpr uint32_t kS = instr(kKeys, false), kO = instr(D, true);
+    uint32_t units = 0, segs[2] = {0, 0}, mine[2] = {0, 0};
+    auto scores = [&](int w, uint32_t unit_no, uint32_t my_no) {  // by one thread
+      const uint32_t d = tmem + w * 256 + (my_no & 1u) * kKeys;
+      const uint32_t qd = desc_k_major(q_base + w * ((SPLIT ? 2 : 1) * L::kQTile));
+      const uint32_t kd = desc_k_major(kv_base + (unit_no & 1u) * (2 * L::kB));
+      mma_ss<false>(d, qd, kd, kS);
+#pragma unroll
+      for (int k = 1; k < 4; ++k) mma_ss<true>(d, qd + 2 * k, kd + 2 * k, kS);
+#pragma unroll
+      for (int i = 1; i < (SPLIT ? 2 : 1) * L::kPanels; ++i) {
+        // (the low part follows the high one)
+        const uint32_t at = qd + i * (L::kQPanel >> 4);
+        const uint32_t kp = kd + (i % L::kPanels) * (L::kPanel >> 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_ss<true>(d, at + 2 * k, kp + 2 * k, kS);
+      }
+      commit(smem_u32(&tail.s_full[w][my_no & 1u]));
+    };
+    for (;;) {
+      const int b = seg.item / a.row_tiles, rt = seg.item - b * a.row_tiles;
+      const int nw = rt * kRows + kTileRows < a.rows ? 2 : 1;
+      const int n = seg.end - seg.first;
+      // the first scores of the segment
+      wait(ok, tail.k_full[units & 1u], units >> 1, a.error);
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        if (w < nw) {
+          wait(ok, tail.q_full[w], segs[w], a.error);
+          fence_after();
+          if (elect_one()) {
+            scores(w, units, mine[w]);
+            if (w == nw - 1) commit(smem_u32(&tail.k_free[units & 1u]));
+          }
+          __syncwarp();
+          ++segs[w];
+        }
+      for (int u = 0; u < n; ++u) {
+        const uint32_t cur = units + u, buf = cur & 1u;
+        const bool more = u + 1 < n;
+        if (more) wait(ok, tail.k_full[(cur + 1) & 1u], (cur + 1) >> 1, a.error);
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          if (w < nw) {
+            const uint32_t p = mine[w]++;  // this unit's number of the row tile
+            if (more) {
+              fence_after();
+              if (elect_one()) {
+                scores(w, cur + 1, p + 1);
+                if (w == nw - 1) commit(smem_u32(&tail.k_free[(cur + 1) & 1u]));
+              }
+              __syncwarp();
+            }
+            if (w == 0) wait(ok, tail.v_full[buf], cur >> 1, a.error);
+            wait(ok, tail.p_full[w][p & 1u], p >> 1, a.error);
+            fence_after();
+            if (elect_one()) {
+              const uint32_t d = tmem + w * 256 + 128;
+              const uint32_t pa = tmem + w * 256 + (p & 1u) * kKeys;
+              const uint32_t vd =
+                  desc_n_major(kv_base + buf * (2 * L::kB) + L::kB, L::kPanel);
+#pragma unroll
+              for (int s = 0; s < (SPLIT ? 2 : 1); ++s)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_ts(d, pa + s * 32 + k * 8, vd + k * (2048 >> 4), kO, u | s | k);
+              commit(smem_u32(&tail.pv_done[w]));
+              if (w == nw - 1) commit(smem_u32(&tail.v_free[buf]));
+            }
+            __syncwarp();
+          }
+      }
+      units += n;
+      if (seg.left <= 0) break;
+      cutter.next(seg);
+    }
+    // every product has completed before TMEM is released
+    if (elect_one()) commit(smem_u32(&tail.drained));
+    __syncwarp();
+    bool drained = true;
+    wait(drained, tail.drained, 0, a.error);
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 12)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+template <int D, bool I8, bool SPLIT>
+rq_status launch_rows(const AttnArgs& a, unsigned grid, cudaStream_t st) {
+  constexpr int bytes = Layout<D, SPLIT>::kTail + (int)sizeof(RowsTail);
+  static_assert(bytes <= 232448, "shared memory of one CTA");
+  static bool ready = false;
+  if (!ready) {
+    if (cudaFuncSetAttribute(attn_rows_kernel<D, I8, SPLIT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+      return RQ_ERR_CUDA;
+    ready = true;
+  }
+  return launch_kernel(attn_rows_kernel<D, I8, SPLIT>, dim3(grid), dim3(kThreads), (size_t)bytes,
+                       st, a);
+}
+
+}  // namespace
+
+rq_status launch_attention_rows(AttnArgs a, int head_dim, bool i8, AttnScratch* scratch,
+                                cudaStream_t st) {
+  a.row_tiles = (a.rows + kRows - 1) / kRows;
+  const int64_t items = (int64_t)a.batch * a.row_tiles;
+  const int64_t segments = items * a.kv_heads;
+  int64_t grid = device_sm_count();
+  a.direct = items > kMaxItems;
+  if (a.direct) {
+    grid = segments;
+    if (grid > 0x7FFFFFFF) return RQ_ERR_SHAPE;
+  } else {
+    const size_t part = sizeof(float) * 2 * (size_t)grid * kRows * (head_dim + 4);
+    const rq_status s = scratch->reserve(part, (size_t)segments, st);
+    if (s != RQ_OK) return s;
+    a.part = scratch->part;
+    a.counter = scratch->counter;
+  }
+  const unsigned g = (unsigned)grid;
+  const bool split = a.dtype == RQ_F32;
+  if (head_dim == 64) {
+    if (i8)
+      return split ? launch_rows<64, true, true>(a, g, st) : launch_rows<64, true, false>(a, g, st);
+    return split ? launch_rows<64, false, true>(a, g, st) : launch_rows<64, false, false>(a, g, st);
+  }
+  if (i8)
+    return split ? launch_rows<128, true, true>(a, g, st) : launch_rows<128, true, false>(a, g, st);
+  return split ? launch_rows<128, false, true>(a, g, st) : launch_rows<128, false, false>(a, g, st);
+}
+
+}  // namespace rq

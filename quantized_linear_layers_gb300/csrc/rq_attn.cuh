@@ -27,6 +27,7 @@ struct AttnArgs {
   int direct;  // one CTA per segment, no splitting
   float* part;
   unsigned int* counter;
+  int4* shares;         // per segment, for a join after the launch (null: none)
   unsigned int* error;  // bit 1: an index outside its array
 };
 

@@ -5,10 +5,10 @@
 // The mathematics is that of rq_attn.cu.  Per CTA up to two tiles of 128 rows
 // share 64 keys at a time:
 //   warps 0-3, 4-7   softmax of tile 0 and 1: a thread owns a row
-//   warps 8-11       codes of K and V to f16 in shared memory, two units deep
-//   warp 12          allocates TMEM; one thread issues the products
-//   warp 13          the scales
-//   warp 14          asks codes into L2, three units ahead (15 idle)
+//   warps 8-15       codes of K and V to f16 in shared memory, two units deep
+//   warp 16          allocates TMEM; one thread issues the products
+//   warp 17          the scales
+//   warp 18          asks codes into L2, three units ahead (19 idle)
 // S = Q K^T (A = Q from shared memory) lands in one of two TMEM buffers per
 // row tile; its softmax writes P over it, as f16 high and low parts for f32
 // rows (64 + 64 keys in S's 64 columns), and P V takes A = P from TMEM and
@@ -25,10 +25,12 @@ constexpr int kKeys = 64;                 // keys of a unit
 constexpr int kTileRows = 128;            // rows of one accumulator
 constexpr int kRows = 2 * kTileRows;      // rows of a segment
 constexpr int kSoft = 256;                // softmax threads
-constexpr int kThreads = 512;
-// Registers a thread of each group of four warps takes: 256 x 168 + 128 x 96
-// + 128 x 80 = 512 x 128, the launch's own.
-constexpr int kSoftRegs = 160, kConvertRegs = 104, kIssueRegs = 88;
+constexpr int kConvert = 256;             // conversion threads
+constexpr int kThreads = kSoft + kConvert + 128;
+// Registers a thread: 256 x 144 + 256 x 64 + 128 x 64 = 640 x 96, the
+// launch's own.
+constexpr int kSoftRegs = 144, kConvertRegs = 64, kIssueRegs = 64;
+constexpr int kIssueWarp = (kSoft + kConvert) / 32;
 constexpr int kScales = 4;                // units whose scales are kept
 constexpr int kAhead = 3;                 // units that codes are asked into L2 ahead of use
 constexpr float kLazy = 8.0f;             // a maximum is kept while scores pass it by less than 2^8
@@ -45,13 +47,20 @@ struct Layout {
   static constexpr int kTail = kQ + 4 * kB;                   // two units of K and V
 };
 
+template <int D>
+constexpr int kPartRow = D + 4;  // a partial row: output, reference, sum
+
+template <bool W>
+struct Wide {
+  static constexpr bool value = W;
+};
+
 struct RowsTail {
   float ks[kScales][kKeys], vs[kScales][kKeys];  // vs relative to vref, times kUp
   float vref[kScales];
   uint64_t q_full[2], k_full[2], k_free[2], v_full[2], v_free[2], sc_full[kScales];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2], drained;
   uint32_t tmem;
-  int flag;
   CutShared cut;
 };
 
@@ -209,8 +218,44 @@ __device__ __forceinline__ uint32_t cut_half2(float2 w, uint32_t& lo) {
   return pack_half2(h.x, h.y);
 }
 
-__device__ __forceinline__ void soft_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory");
+// E values of a query row as they lie in memory (16-bit ones two to a word, in
+// x[0 .. E / 2)), and value i of them.
+template <int E, bool F32>
+__device__ __forceinline__ void load_q(const AttnArgs& a, int64_t off, float (&x)[E]) {
+  if constexpr (F32) {
+    const float* p = static_cast<const float*>(a.q) + off;
+    if constexpr (E == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p);
+      x[0] = v.x;
+      x[1] = v.y;
+      x[2] = v.z;
+      x[3] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(p);
+      x[0] = v.x;
+      x[1] = v.y;
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(a.q) + off;
+    if constexpr (E == 4) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      x[2] = __uint_as_float(v.x);
+      x[3] = __uint_as_float(v.y);
+    } else {
+      x[1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(p));
+    }
+  }
+}
+// (in the order i = 0, 1, ...: the words lie at the end, and value i overwrites x[i])
+template <int E, bool F32>
+__device__ __forceinline__ float q_value(bool f16, const float (&x)[E], int i) {
+  if constexpr (F32) return x[i];
+  const uint32_t w = __float_as_uint(x[E / 2 + i / 2]);
+  if (f16) {
+    const float2 f = half_pair(w);
+    return (i & 1) ? f.y : f.x;
+  }
+  return __uint_as_float((i & 1) ? w & 0xFFFF0000u : w << 16);
 }
 
 // A warp's wait for a barrier phase; after one wait has run out, no further
@@ -271,8 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&tail.q_full[i]), 4);
-      mbar_init(smem_u32(&tail.k_full[i]), 4);
-      mbar_init(smem_u32(&tail.v_full[i]), 4);
+      mbar_init(smem_u32(&tail.k_full[i]), kConvert / 32);
+      mbar_init(smem_u32(&tail.v_full[i]), kConvert / 32);
       mbar_init(smem_u32(&tail.k_free[i]), 1);
       mbar_init(smem_u32(&tail.v_free[i]), 1);
       mbar_init(smem_u32(&tail.pv_done[i]), 1);
@@ -285,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
     mbar_init(smem_u32(&tail.drained), 1);
     mbar_fence_init();
   }
-  if (warp == 12) {
+  if (warp == kIssueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_u32(&tail.tmem))
                  : "memory");
@@ -307,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
 
   if (warp < 8)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-  else if (warp < 12)
+  else if (warp < kIssueWarp)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
   else
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
@@ -317,9 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
     const int w = warp >> 2, quad = warp & 3;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t s_col = tmem + w * 256 + lanes, o_col = s_col + 128;
-    uint32_t units = 0, segs = 0;  // of this row tile so far
+    uint32_t units = 0;            // of this row tile so far
     uint32_t all_units = 0;        // of the CTA: the scales' ring
-    for (bool first_seg = true;; first_seg = false) {
+    for (;;) {
       const int b = seg.item / a.row_tiles, rt = seg.item - b * a.row_tiles;
       const int row0 = rt * kRows + w * kTileRows;
       const int n_units = seg.end - seg.first;
@@ -333,87 +378,85 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         const int64_t my_off =
             ((int64_t)b * a.new_tokens + tok) * a.q_stride +
             (int64_t)(seg.head * a.group + (live ? my_row - tok * a.group : 0)) * D;
-#pragma unroll 4
-        for (int r = 0; r < 32; ++r) {
-          const int64_t off = __shfl_sync(0xFFFFFFFFu, my_off, r) + lane * E;
-          const bool row_live = row0 + quad * 32 + r < a.rows;
-          float x[E];
-          if (a.dtype == RQ_F32) {
-            const float* p = static_cast<const float*>(a.q) + off;
-            if constexpr (E == 4) {
-              const float4 v = *reinterpret_cast<const float4*>(p);
-              x[0] = v.x;
-              x[1] = v.y;
-              x[2] = v.z;
-              x[3] = v.w;
-            } else {
-              const float2 v = *reinterpret_cast<const float2*>(p);
-              x[0] = v.x;
-              x[1] = v.y;
-            }
-          } else {
-            const uint16_t* p = static_cast<const uint16_t*>(a.q) + off;
-            uint32_t raw[E / 2];
-            if constexpr (E == 4) {
-              const uint2 v = *reinterpret_cast<const uint2*>(p);
-              raw[0] = v.x;
-              raw[1] = v.y;
-            } else {
-              raw[0] = *reinterpret_cast<const uint32_t*>(p);
+        const uint32_t q_at = q_base + w * ((SPLIT ? 2 : 1) * L::kQTile) + quad * 32 * 128;
+        for (int r0 = 0; r0 < 32; r0 += 16) {  // sixteen rows' loads in flight
+          float x[16][E];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int64_t off = __shfl_sync(0xFFFFFFFFu, my_off, r0 + r) + lane * E;
+            load_q<E, SPLIT>(a, off, x[r]);
+          }
+          float top[16];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const bool row_live = row0 + quad * 32 + r0 + r < a.rows;
+            top[r] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+              x[r][i] = row_live ? q_value<E, SPLIT>(a.dtype == RQ_F16, x[r], i) : 0.0f;
             }
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) {
-              if (a.dtype == RQ_F16) {
-                const float2 f = half_pair(raw[i]);
-                x[2 * i] = f.x;
-                x[2 * i + 1] = f.y;
-              } else {
-                x[2 * i] = __uint_as_float(raw[i] << 16);
-                x[2 * i + 1] = __uint_as_float(raw[i] & 0xFFFF0000u);
-              }
+            for (int i = 0; i < E; ++i) {
+              // a NaN counts as an infinity
+              const float m = fabsf(x[r][i]);
+              top[r] = fmaxf(top[r], m == m ? m : INFINITY);
             }
           }
-          float top = 0.0f;
+          // the rows' maxima, sixteen at once: each step halves the rows that
+          // a lane holds; lane bits 4, 3, 2, 1 are the row's bits 3, 2, 1, 0
 #pragma unroll
-          for (int i = 0; i < E; ++i) {
-            if (!row_live) x[i] = 0.0f;
-            top = fmaxf(top, fabsf(x[i]));
+          for (int n = 8, o = 16; n >= 1; n >>= 1, o >>= 1) {
+            const bool up_half = (lane & o) != 0;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+              const float keep = up_half ? top[i + n] : top[i];
+              const float give = up_half ? top[i] : top[i + n];
+              top[i] = fmaxf(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
+            }
           }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-          // times a power of two: the largest entry in [2^13, 2^14)
+          const float most = fmaxf(top[0], __shfl_xor_sync(0xFFFFFFFFu, top[0], 1));
+          // times a power of two: the largest entry in [2^13, 2^14); a row
+          // that is not finite becomes NaN
           int e = 0;
-          if (top > 0.0f && top <= 3.4e38f) {
-            e = 13 - (int)((__float_as_uint(top) >> 23) & 0xFFu) + 127;
+          if (most > 0.0f) {
+            e = 13 - (int)((__float_as_uint(most) >> 23) & 0xFFu) + 127;
             e = e < -126 ? -126 : e > 100 ? 100 : e;
           }
-          const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-          if (lane == r) {
-            c = fmaxf(a.scale_log2 / up, 0x1p-126f);
-            if (!(top <= 3.4e38f)) c = NAN;  // an infinity in q
-          }
-          const int row = quad * 32 + r;
-          const int byte = lane * E * 2;
-          const uint32_t at = q_base + w * ((SPLIT ? 2 : 1) * L::kQTile) +
-                              (byte >> 7) * L::kQPanel + row * 128 +
-                              ((((byte >> 4) & 7) ^ (row & 7)) << 4) + (byte & 15);
-          uint32_t hi[E / 2], lo[E / 2];
+          const float own = most <= 3.4e38f ? __uint_as_float((uint32_t)(e + 127) << 23) : NAN;
 #pragma unroll
-          for (int i = 0; i < E / 2; ++i)
-            hi[i] = split_half2(x[2 * i] * up, x[2 * i + 1] * up, lo[i]);
-          if constexpr (E == 4) {
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1])
-                         : "memory");
-            if (SPLIT)
-              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + L::kQTile), "r"(lo[0]),
-                           "r"(lo[1])
+          for (int r = 0; r < 16; ++r) {
+            const float up = __shfl_sync(
+                0xFFFFFFFFu, own,
+                ((r >> 3) & 1) * 16 + ((r >> 2) & 1) * 8 + ((r >> 1) & 1) * 4 + (r & 1) * 2);
+            if (lane == r0 + r) c = up;
+            const int byte = lane * E * 2;
+            const uint32_t at = q_at + (byte >> 7) * L::kQPanel + (r0 + r) * 128 +
+                                ((((byte >> 4) & 7) ^ (r & 7)) << 4) + (byte & 15);
+            uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+              const float2 v = make_float2(x[r][2 * i] * up, x[r][2 * i + 1] * up);
+              if (SPLIT)
+                hi[i] = cut_half2(v, lo[i]);
+              else
+                hi[i] = pack_half2(v.x, v.y);
+            }
+            if constexpr (E == 4) {
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1])
                            : "memory");
-          } else {
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(hi[0]) : "memory");
-            if (SPLIT)
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + L::kQTile), "r"(lo[0]) : "memory");
+              if (SPLIT)
+                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + L::kQTile),
+                             "r"(lo[0]), "r"(lo[1])
+                             : "memory");
+            } else {
+              asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(hi[0]) : "memory");
+              if (SPLIT)
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + L::kQTile), "r"(lo[0])
+                             : "memory");
+            }
           }
         }
+        c = c == c ? fmaxf(a.scale_log2 / c, 0x1p-126f) : NAN;
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&tail.q_full[w]));
@@ -546,140 +589,133 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         fence_after();
       }
       all_units += n_units;
-      ++segs;
 
       // a.part holds per CTA two sets of kRows rows of D values, reference
-      // and sum (D + 4 floats)
+      // and sum (D + 4 floats); the join kernel learns which sets are whose
       const auto share = cutter.sharers(seg);
-      const int parts = share.parts, part = share.part;
-      constexpr int kPartRow = D + 4;
-      auto set_at = [&](int p) -> float* {
-        return a.part + ((share.cta0 + p) * 2 + (p == 0 && share.second ? 1 : 0)) *
-                            (int64_t)kRows * kPartRow;
-      };
-      const int my = w * kTileRows + quad * 32 + lane;  // row of the segment
-      const int row = rt * kRows + my;
-      const bool live = row < a.rows;
-      const float back = vref * (1.0f / kUp);
-      const int tok = live ? row / a.group : 0;
-      const int64_t dst = (((int64_t)b * a.new_tokens + tok) * a.q_heads + seg.head * a.group +
-                           (live ? row - tok * a.group : 0)) * D;
-      auto store_out = [&](int64_t at, const float4& y) {
-        if (SPLIT) {
-          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = y;
-        } else if (a.dtype == RQ_F16) {
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-              make_uint2(pack_half2(y.x, y.y), pack_half2(y.z, y.w));
-        } else {
-          const __nv_bfloat162 h0 = __floats2bfloat162_rn(y.x, y.y);
-          const __nv_bfloat162 h1 = __floats2bfloat162_rn(y.z, y.w);
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&h0),
-                         *reinterpret_cast<const uint32_t*>(&h1));
-        }
-      };
+      const int parts = share.parts;
+      if (tid == 0 && a.shares != nullptr)
+        a.shares[seg.item * a.kv_heads + seg.head] =
+            make_int4(parts, (int)share.cta0, share.second ? 1 : 0, 0);
       if (row0 < a.rows) {
+        float* set = a.part + ((int64_t)blockIdx.x * 2 +
+                               (share.part == 0 && share.second ? 1 : 0)) *
+                                  (int64_t)kRows * kPartRow<D>;
+        const int my = w * kTileRows + quad * 32;  // the warp's first row of the segment
+        const int my_row = rt * kRows + my + lane;
+        const bool live = my_row < a.rows;
+        const int tok = live ? my_row / a.group : 0;
+        const int64_t my_dst = (((int64_t)b * a.new_tokens + tok) * a.q_heads +
+                                seg.head * a.group + (live ? my_row - tok * a.group : 0)) * D;
+        const float back = vref * (1.0f / kUp);
         const float r1 = parts > 1 ? back : l == 0.0f ? 0.0f : back / l;
+        // A thread holds a row; memory wants a warp to write one.  The rows
+        // pass through the warp's part of the query tile, which the segment's
+        // products are done with: as wide as a query row there, in 16-byte
+        // pieces whose places are exclusive-ored with the row against bank
+        // conflicts.
+        constexpr int kBytes = (SPLIT ? 2 : 1) * D * 2;
+        const uint32_t stage = q_base + w * ((SPLIT ? 2 : 1) * L::kQTile) + quad * 32 * kBytes;
+        auto pass = [&](auto wide, int d0) {  // columns from d0 on, as f32 or 16-bit values
+          constexpr bool kWide = decltype(wide)::value;
+          constexpr int kCols = kBytes / (kWide ? 4 : 2);
 #pragma unroll
-        for (int d = 0; d < D; d += 32) {
-          float o[32];
-          tmem_ld32(o_col + d, o);
-          tmem_ld_wait();
-          if (live) {
+          for (int d = 0; d < kCols; d += 32) {
+            float o[32];
+            tmem_ld32(o_col + d0 + d, o);
+            tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 y =
-                  make_float4(o[i] * r1, o[i + 1] * r1, o[i + 2] * r1, o[i + 3] * r1);
-              if (parts > 1)
-                __stcg(reinterpret_cast<float4*>(set_at(part) + my * kPartRow + d + i), y);
-              else
-                store_out(dst + d + i, y);
+            for (int i = 0; i < 32; ++i) o[i] *= r1;
+            uint32_t h[kWide ? 32 : 16];
+            if constexpr (kWide) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) h[i] = __float_as_uint(o[i]);
+            } else if (a.dtype == RQ_F16) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) h[i] = pack_half2(o[2 * i], o[2 * i + 1]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const __nv_bfloat162 t = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+                h[i] = *reinterpret_cast<const uint32_t*>(&t);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < (kWide ? 8 : 4); ++i) {
+              const int piece = d / (kWide ? 4 : 8) + i;
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               stage + lane * kBytes + ((piece ^ (lane & 7)) << 4)),
+                           "r"(h[4 * i]), "r"(h[4 * i + 1]), "r"(h[4 * i + 2]), "r"(h[4 * i + 3])
+                           : "memory");
             }
           }
+          __syncwarp();
+          constexpr int kPer = kBytes / 16, kTake = 32 / kPer;  // pieces of a row, rows at once
+#pragma unroll 4
+          for (int r0 = 0; r0 < 32; r0 += kTake) {
+            const int r = r0 + lane / kPer, piece = lane % kPer;
+            const int64_t dst = __shfl_sync(0xFFFFFFFFu, my_dst, r);
+            uint32_t h[4];
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+                         : "r"(stage + r * kBytes + ((piece ^ (r & 7)) << 4))
+                         : "memory");
+            if (rt * kRows + my + r >= a.rows) continue;
+            const uint4 v = make_uint4(h[0], h[1], h[2], h[3]);
+            if (parts > 1)
+              __stcg(reinterpret_cast<uint4*>(set + (my + r) * kPartRow<D> + d0) + piece, v);
+            else if (kWide)
+              *(reinterpret_cast<uint4*>(static_cast<float*>(a.out) + dst) + piece) = v;
+            else
+              *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + dst) + piece) = v;
+          }
+          __syncwarp();
+        };
+        if (SPLIT) {
+          pass(Wide<true>(), 0);
+        } else if (parts > 1) {
+          pass(Wide<true>(), 0);
+          pass(Wide<true>(), D / 2);
+        } else {
+          pass(Wide<false>(), 0);
         }
         if (parts > 1 && live)
-          __stcg(reinterpret_cast<float2*>(set_at(part) + my * kPartRow + D), make_float2(ref, l));
+          __stcg(reinterpret_cast<float2*>(set + (my + lane) * kPartRow<D> + D),
+                 make_float2(ref, l));
         fence_before();
-      }
-      if (parts > 1) {
-        __threadfence();
-        soft_sync();
-        if (tid == 0) {
-          unsigned int* ctr = a.counter + (int64_t)seg.item * a.kv_heads + seg.head;
-          const unsigned int old = atomicAdd(ctr, 1u);
-          tail.flag = old == (unsigned int)(parts - 1);
-          if (tail.flag) *ctr = 0u;
-        }
-        soft_sync();
-        const bool last = tail.flag != 0;
-        __threadfence();
-        if (last) {
-          // 16 bytes of a row per thread, four rows' pieces at a time, in
-          // part order
-          constexpr int kVec = D / 4, kStep = kSoft / kVec;  // rows taken at once
-          const int d = (tid % kVec) * 4;
-          const int rows = min(kRows, a.rows - rt * kRows);
-          for (int r0 = tid / kVec; r0 < rows; r0 += 4 * kStep) {
-            float4 v[4];
-            float mx[4], sum[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-              mx[k] = -INFINITY;
-              sum[k] = 0.0f;
-            }
-            for (int p = 0; p < parts; ++p) {
-              const float* set = set_at(p);
-              float4 ov[4];
-              float2 ml[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int r = min(r0 + k * kStep, rows - 1);
-                ov[k] = __ldcg(reinterpret_cast<const float4*>(set + r * kPartRow + d));
-                ml[k] = __ldcg(reinterpret_cast<const float2*>(set + r * kPartRow + D));
-              }
-#pragma unroll
-              for (int k = 0; k < 4; ++k) merge(v[k], mx[k], sum[k], ov[k], ml[k], 1.0f);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int r = r0 + k * kStep;
-              if (r >= rows) continue;
-              const int rr = rt * kRows + r, tk = rr / a.group;
-              const float f = sum[k] == 0.0f ? 0.0f : 1.0f / sum[k];
-              store_out((((int64_t)b * a.new_tokens + tk) * a.q_heads + seg.head * a.group + rr -
-                         tk * a.group) * D + d,
-                        make_float4(v[k].x * f, v[k].y * f, v[k].z * f, v[k].w * f));
-            }
-          }
-        }
-        soft_sync();  // the flag is read before the next segment's is set
+        // the query tile is all warps' again
+        asm volatile("bar.sync %0, 128;" ::"r"(2 + w) : "memory");
       }
       if (seg.left <= 0) break;
       cutter.next(seg);
     }
-  } else if (work && warp < 12) {
+  } else if (work && warp < kIssueWarp) {
     // --------------------------------------------------- conversion ----
     constexpr int kChunks = D / 16;                    // 16-code chunks of a row
-    constexpr int N = kKeys * kChunks / 128;           // of K (and of V) per thread and unit
+    constexpr int N = kKeys * kChunks / kConvert;      // of K (and of V) per thread and unit
     const int t = tid - kSoft;
     const int chunk = t % kChunks, row_a = t / kChunks;
-    constexpr int kRowStep = 128 / kChunks;
+    constexpr int kRowStep = kConvert / kChunks;
     // where chunk `chunk` of row r goes: 32 bytes of an f16 row
     const uint32_t at = (chunk >> 2) * L::kPanel;
     const int c16 = (chunk & 3) * 2;
     uint4 kc[N], vc[N];  // the next unit's codes, on their way into registers
     PageWindow pages;
     const int page_mask = (1 << a.lg_page) - 1, page_bytes = D << a.lg_page;
-    const uint8_t *k_at = a.k + chunk * 16, *v_at = a.v + chunk * 16;
-    auto fetch = [&](const Segment& g, int u, uint4 (&c)[N], const uint8_t* codes) {
+    int64_t off[N];  // of the next unit's rows, in K and V alike; negative: no such key
+    auto find = [&](const Segment& g, int u) {
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const int key = row_a + n * kRowStep;
-        const int plane = pages.plane(u * 4 + (key >> 4));
+        const int key = u * kKeys + row_a + n * kRowStep;
+        const int plane = pages.plane(key >> 4);
+        off[n] = key < g.kv ? (int64_t)plane * page_bytes + ((key & page_mask) * D + chunk * 16) : -1;
+      }
+    };
+    auto fetch = [&](uint4 (&c)[N], const uint8_t* codes) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
         c[n] = make_uint4(0u, 0u, 0u, 0u);
-        if (u * kKeys + key < g.kv)
-          c[n] = ldg_nc_v4(codes + (int64_t)plane * page_bytes + ((u * kKeys + key) & page_mask) * D);
+        if (off[n] >= 0) c[n] = ldg_nc_v4(codes + off[n]);
       }
     };
     auto convert = [&](const uint4 (&codes)[N], uint32_t base) {
@@ -702,48 +738,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       }
     };
     pages.open(a, seg, seg.first, lane);
-    fetch(seg, seg.first, kc, k_at);
-    fetch(seg, seg.first, vc, v_at);
+    find(seg, seg.first);
+    fetch(kc, a.k);
+    fetch(vc, a.v);
     uint32_t units = 0;
     for (int u = seg.first;;) {
-      // the unit after this one, whose codes are fetched as soon as this
-      // one's have left their registers
-      Segment after = seg;
-      int un = u + 1;
-      bool more = true;
-      if (un == seg.end) {
-        more = seg.left > 0;
-        if (more) {
-          cutter.next(after);
-          un = after.first;
-        }
-      }
-      const uint32_t buf = units & 1u;
-      const uint32_t kb = kv_base + buf * (2 * L::kB), vb = kb + L::kB;
-      wait(ok, tail.k_free[buf], (units >> 1) ^ 1u, a.error);
+      const uint32_t buf = units & 1u, turn = (units >> 1) ^ 1u;
+      const uint32_t kb = kv_base + buf * (2 * L::kB);
+      wait(ok, tail.k_free[buf], turn, a.error);
       convert(kc, kb);
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&tail.k_full[buf]));
-      if (more) {
-        if (un == u + 1)
-          pages.step(a, after, un, lane);
-        else
-          pages.open(a, after, un, lane);
-        fetch(after, un, kc, k_at);
+      // the next unit's codes are fetched as soon as this one's have left
+      // their registers
+      bool more = true;
+      if (++u < seg.end) {
+        pages.step(a, seg, u, lane);
+      } else {
+        more = seg.left > 0;
+        if (more) {
+          cutter.next(seg);
+          u = seg.first;
+          pages.open(a, seg, u, lane);
+        }
       }
-      wait(ok, tail.v_free[buf], (units >> 1) ^ 1u, a.error);
-      convert(vc, vb);
+      if (more) {
+        find(seg, u);
+        fetch(kc, a.k);
+      }
+      wait(ok, tail.v_free[buf], turn, a.error);
+      convert(vc, kb + L::kB);
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&tail.v_full[buf]));
       if (!more) break;
-      fetch(after, un, vc, v_at);
-      seg = after;
-      u = un;
+      fetch(vc, a.v);
       ++units;
     }
-  } else if (work && warp == 13) {
+  } else if (work && warp == kIssueWarp + 1) {
     // -------------------------------------------------------- scales ----
     uint32_t units = 0;
     const int page_mask = (1 << a.lg_page) - 1;
@@ -793,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       if (seg.left <= 0) break;
       cutter.next(seg);
     }
-  } else if (work && warp == 14) {
+  } else if (work && warp == kIssueWarp + 2) {
     // -------- codes into L2, kAhead units before they are fetched: lanes
     // 0-3 the boxes of K, 4-7 those of V
     uint32_t units = 0;
@@ -819,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       if (seg.left <= 0) break;
       cutter.next(seg);
     }
-  } else if (work && warp == 12) {
+  } else if (work && warp == kIssueWarp) {
     // ------------------------------------------------------ products ----
     // (the whole warp walks along, one lane issues)
     constexpr uint32_t kS = instr(kKeys, false), kO = instr(D, true);
@@ -907,8 +940,94 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 12)
+  if (warp == kIssueWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Joins the partial rows of segments that several CTAs share.  A warp takes a
+// row: its lanes hold the parts' weights 2^(ref_p - max ref) / sum, then the
+// row's columns.
+template <int D>
+__global__ void __launch_bounds__(256) join_rows_kernel(const AttnArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  constexpr int kBlocks = kRows / 8;  // CTAs per segment, eight rows each
+  const int s = (int)(blockIdx.x / kBlocks);
+  const int4 share = a.shares[s];
+  const int parts = share.x;
+  if (parts <= 1) return;
+  const int item = s / a.kv_heads, head = s - item * a.kv_heads;
+  const int b = item / a.row_tiles, rt = item - b * a.row_tiles;
+  const int r = (int)(blockIdx.x % kBlocks) * 8 + (threadIdx.x >> 5);
+  const int row = rt * kRows + r;
+  if (row >= a.rows) return;
+  auto row_at = [&](int p) -> const float* {
+    return a.part +
+           (((int64_t)(share.y + p) * 2 + (p == 0 ? share.z : 0)) * kRows + r) * kPartRow<D>;
+  };
+  float top = -INFINITY;
+  for (int p = lane; p < parts; p += 32) top = fmaxf(top, __ldcg(row_at(p) + D));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  const float base = top == -INFINITY ? 0.0f : top;
+  constexpr int E = D / 32;
+  float v[E] = {}, sum = 0.0f;
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+    float f = 0.0f, l = 0.0f;
+    if (p0 + lane < parts) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(row_at(p0 + lane) + D));
+      f = ex2(ml.x - base);
+      // a part whose scores are all NaN has no reference, but its sum counts
+      l = ml.x == -INFINITY ? ml.y : ml.y * f;
+    }
+    sum += warp_sum(l);
+    const int n = min(32, parts - p0);
+#pragma unroll 8
+    for (int p = 0; p < n; ++p) {
+      const float fp = __shfl_sync(0xFFFFFFFFu, f, p);
+      if constexpr (E == 4) {
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(row_at(p0 + p)) + lane);
+        v[0] = fmaf(o.x, fp, v[0]);
+        v[1] = fmaf(o.y, fp, v[1]);
+        v[2] = fmaf(o.z, fp, v[2]);
+        v[3] = fmaf(o.w, fp, v[3]);
+      } else {
+        const float2 o = __ldcg(reinterpret_cast<const float2*>(row_at(p0 + p)) + lane);
+        v[0] = fmaf(o.x, fp, v[0]);
+        v[1] = fmaf(o.y, fp, v[1]);
+      }
+    }
+  }
+  const float r1 = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < E; ++i) v[i] *= r1;
+  const int tok = row / a.group;
+  const int64_t dst = (((int64_t)b * a.new_tokens + tok) * a.q_heads + head * a.group + row -
+                       tok * a.group) * D + lane * E;
+  if (a.dtype == RQ_F32) {
+    float* out = static_cast<float*>(a.out) + dst;
+    if constexpr (E == 4)
+      *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<float2*>(out) = make_float2(v[0], v[1]);
+    return;
+  }
+  uint32_t h[E / 2];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    if (a.dtype == RQ_F16) {
+      h[i] = pack_half2(v[2 * i], v[2 * i + 1]);
+    } else {
+      const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      h[i] = *reinterpret_cast<const uint32_t*>(&t);
+    }
+  }
+  uint16_t* out = static_cast<uint16_t*>(a.out) + dst;
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(h[0], h[1]);
+  else
+    *reinterpret_cast<uint32_t*>(out) = h[0];
 }
 
 template <int D, bool I8, bool SPLIT>
@@ -922,8 +1041,11 @@ rq_status launch_rows(const AttnArgs& a, unsigned grid, cudaStream_t st) {
       return RQ_ERR_CUDA;
     ready = true;
   }
-  return launch_kernel(attn_rows_kernel<D, I8, SPLIT>, dim3(grid), dim3(kThreads), (size_t)bytes,
-                       st, a);
+  const rq_status s = launch_kernel(attn_rows_kernel<D, I8, SPLIT>, dim3(grid), dim3(kThreads),
+                                    (size_t)bytes, st, a);
+  if (s != RQ_OK || a.shares == nullptr) return s;
+  const unsigned segments = (unsigned)(a.batch * a.row_tiles * a.kv_heads);
+  return launch_kernel(join_rows_kernel<D>, dim3(segments * (kRows / 8)), dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -939,11 +1061,12 @@ rq_status launch_attention_rows(AttnArgs a, int head_dim, bool i8, AttnScratch* 
     grid = segments;
     if (grid > 0x7FFFFFFF) return RQ_ERR_SHAPE;
   } else {
+    // partial rows, and behind them who shares which segment
     const size_t part = sizeof(float) * 2 * (size_t)grid * kRows * (head_dim + 4);
-    const rq_status s = scratch->reserve(part, (size_t)segments, st);
+    const rq_status s = scratch->reserve(part + sizeof(int4) * (size_t)segments, 0, st);
     if (s != RQ_OK) return s;
     a.part = scratch->part;
-    a.counter = scratch->counter;
+    a.shares = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(scratch->part) + part);
   }
   const unsigned g = (unsigned)grid;
   const bool split = a.dtype == RQ_F32;

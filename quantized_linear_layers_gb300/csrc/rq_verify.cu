@@ -9,10 +9,11 @@
 // weights down to 1.5e-11 of 1 apart from zero while 2^20 of them still fit
 // 64 bits.
 //
-// One cluster of 8 CTAs takes a sequence: each CTA sums an eighth of the row,
-// the eight sums cross through distributed shared memory, and the CTA that
-// holds the point finds the token in its part.  No scratch, no atomics, one
-// launch; the walk down a tree is a loop of draws inside it.
+// One cluster of 8 CTAs takes a sequence: each of its 128 warps sums its part
+// of the row, every CTA receives all 128 sums through distributed shared
+// memory, and finds the token by itself in the part that holds the point: one
+// cluster barrier per draw, no scratch, no atomics across CTAs, one launch;
+// the walk down a tree is a loop of draws inside it.
 #include "rq_device.cuh"
 #include "rq_internal.h"
 
@@ -25,10 +26,11 @@ constexpr int kVWarps = kVThreads / 32;
 constexpr int kVCluster = 8;
 constexpr int kMaxTree = 1024;
 
+constexpr int kVParts = kVCluster * kVWarps;  // parts of a row, one a warp
+
 struct VerifyShared {
-  long long totals[2][kVCluster];  // by draw parity and CTA
+  long long sums[2][kVParts];  // by draw parity and part
   int found[2];
-  long long warp_sum[kVWarps];
   int first;
 };
 
@@ -49,7 +51,7 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ long long warp_sum_ll(long long v) {
+__device__ __forceinline__ unsigned int warp_sum_u(unsigned int v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
@@ -62,11 +64,61 @@ struct Row {
   int drop;        // entry counted as zero (-1: none)
 };
 
+// floor(min(w, 1) 2^36) in two halves of 18 bits, each as the bits of 2^23 + half:
+// additions rounded towards zero cut the fraction off, and the rest t - half
+// is exact.  (A conversion to 64-bit integers runs at a quarter of an
+// addition's rate or less.)
+constexpr unsigned int kHalfBase = 0x4B000000u;
+__device__ __forceinline__ void halves(float w, unsigned int& hi, unsigned int& lo) {
+  const float t = fminf(fmaxf(w, 0.0f), 1.0f) * 0x1p18f;  // a NaN becomes 0
+  const float a = __fadd_rz(t, 0x1p23f);
+  const float b = __fadd_rz((t - (a - 0x1p23f)) * 0x1p18f, 0x1p23f);
+  hi = __float_as_uint(a);
+  lo = __float_as_uint(b);
+}
+
+__device__ __forceinline__ float weight_of(const Row& row, int v) {
+  const float p = __ldg(row.p + v);
+  const float w = row.q != nullptr ? __fsub_rn(p, __ldg(row.q + v)) : p;
+  return v == row.drop ? 0.0f : w;
+}
+
 __device__ __forceinline__ long long weight(const Row& row, int v) {
-  float w = __ldg(row.p + v);
-  if (row.q != nullptr) w = __fsub_rn(w, __ldg(row.q + v));
-  if (v == row.drop || !(w > 0.0f)) return 0;
-  return __float2ll_rz(fminf(w, 1.0f) * 0x1p36f);
+  unsigned int hi, lo;
+  halves(weight_of(row, v), hi, lo);
+  return ((long long)(hi - kHalfBase) << 18) + (long long)(lo - kHalfBase);
+}
+
+// A warp's sum of the weights of entries [v0, v1), sixteen loads a lane in
+// flight.  A lane meets at most 2^20 / 128 / 32 entries and the padding of the
+// last round: the sums of halves stay below 2^27, so that 32-bit sums of the
+// raw bits, wrapping, still hold them.
+template <bool Q>
+__device__ __forceinline__ long long part_sum(const Row& row, int v0, int v1) {
+  constexpr int kBatch = 16;
+  unsigned int hi = 0u, lo = 0u, n = 0u;
+  for (int v = v0 + (int)(threadIdx.x & 31); v - (int)(threadIdx.x & 31) < v1; v += 32 * kBatch) {
+    float p[kBatch], q[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int x = v + 32 * i;
+      p[i] = x < v1 ? __ldg(row.p + x) : 0.0f;
+      q[i] = Q && x < v1 ? __ldg(row.q + x) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      float w = Q ? __fsub_rn(p[i], q[i]) : p[i];
+      if (!Q && v + 32 * i == row.drop) w = 0.0f;
+      unsigned int a, b;
+      halves(w, a, b);
+      hi += a;
+      lo += b;
+    }
+    n += kBatch;
+  }
+  hi = warp_sum_u(hi - n * kHalfBase);  // below 2^32 over a warp's 8192 entries of 2^18
+  lo = warp_sum_u(lo - n * kHalfBase);
+  return ((long long)hi << 18) + (long long)lo;
 }
 
 __device__ __forceinline__ unsigned int unit24(float u) {
@@ -74,71 +126,83 @@ __device__ __forceinline__ unsigned int unit24(float u) {
   return (unsigned int)fminf(u * 0x1p24f, 16777215.0f);
 }
 
+__device__ __forceinline__ int part_begin(int vocab, int part) {
+  return (int)((long long)vocab * part / kVParts);
+}
+
+__device__ __forceinline__ long long warp_scan(long long s, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xFFFFFFFFu, s, o);
+    if (lane >= o) s += x;
+  }
+  return s;
+}
+
 // One draw by the whole cluster; every thread of every CTA returns the token
 // in *token, and whether the row has any weight.  `d` counts the draws of
-// this launch (its parity picks the exchange buffers: a CTA writes buffer
-// d & 1 again only after the cluster barrier of draw d + 1, which every CTA
-// reaches after its last read of draw d).
+// this launch: its parity picks the exchange buffers, which a CTA writes again
+// only after the cluster barrier of draw d + 1, and every CTA reaches that
+// one after its last read of draw d.
 __device__ bool draw(VerifyShared& sh, const Row& row, float u, int vocab, int d, int* token) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t rank = cluster_rank();
-  // this warp's part: 32-entry chunks [c0, c1) of the row
-  const int chunks = (vocab + 31) / 32;
-  const int part = (int)rank * kVWarps + warp, parts = kVCluster * kVWarps;
-  const int c0 = (int)((long long)chunks * part / parts);
-  const int c1 = (int)((long long)chunks * (part + 1) / parts);
-  long long sum = 0;
-#pragma unroll 8
-  for (int c = c0; c < c1; ++c) {
-    const int v = c * 32 + lane;
-    if (v < vocab) sum += weight(row, v);
+  const int part = (int)cluster_rank() * kVWarps + warp;
+  const int v0 = part_begin(vocab, part), v1 = part_begin(vocab, part + 1);
+  const long long sum =
+      row.q != nullptr ? part_sum<true>(row, v0, v1) : part_sum<false>(row, v0, v1);
+  if (lane < kVCluster) {
+    const uint32_t dst = map_rank(smem_u32(&sh.sums[d & 1][part]), (uint32_t)lane);
+    asm volatile("st.shared::cluster.s64 [%0], %1;" ::"r"(dst), "l"(sum) : "memory");
   }
-  sum = warp_sum_ll(sum);
-  if (lane == 0) sh.warp_sum[warp] = sum;
-  __syncthreads();
+  cluster_sync();
   if (warp == 0) {
-    const long long cta = warp_sum_ll(lane < kVWarps ? sh.warp_sum[lane] : 0);
-    if (lane < kVCluster) {
-      const uint32_t dst =
-          map_rank(smem_u32(&sh.totals[d & 1][rank]), (uint32_t)lane);
-      asm volatile("st.shared::cluster.s64 [%0], %1;" ::"r"(dst), "l"(cta) : "memory");
-    }
-  }
-  cluster_sync();
-  long long before = 0, total = 0;
+    // the part that holds the point: lanes scan four parts each
+    constexpr int kPer = kVParts / 32;
+    long long s[kPer], mine = 0;
 #pragma unroll
-  for (int r = 0; r < kVCluster; ++r) {
-    const long long s = sh.totals[d & 1][r];
-    if (r < (int)rank) before += s;
-    total += s;
-  }
-  const long long un = unit24(u);
-  const long long point = un * (total >> 24) + ((un * (total & 0xFFFFFF)) >> 24);
-  for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
-  if (total > 0 && before <= point && point < before + sh.warp_sum[warp]) {
-    // the token is in this warp's part (of one warp of the cluster)
-    long long run = before;
+    for (int i = 0; i < kPer; ++i) {
+      s[i] = sh.sums[d & 1][lane * kPer + i];
+      mine += s[i];
+    }
+    const long long scan = warp_scan(mine, lane);
+    const long long total = __shfl_sync(0xFFFFFFFFu, scan, 31);
+    const long long un = unit24(u);
+    const long long point = un * (total >> 24) + ((un * (total & 0xFFFFFF)) >> 24);
     int found = -1;
-    for (int c = c0; c < c1 && found < 0; ++c) {
-      const int v = c * 32 + lane;
-      long long s = v < vocab ? weight(row, v) : 0;
+    if (total > 0) {
+      const int at = __ffs((int)__ballot_sync(0xFFFFFFFFu, scan > point)) - 1;
+      long long run = __shfl_sync(0xFFFFFFFFu, scan - mine, at);
+      int p = at * kPer;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xFFFFFFFFu, s, o);
-        if (lane >= o) s += x;
+      for (int i = 0; i < kPer - 1; ++i) {
+        const long long x = __shfl_sync(0xFFFFFFFFu, s[i], at);
+        if (p == at * kPer + i && run + x <= point) {
+          run += x;
+          ++p;
+        }
       }
-      const unsigned int past = __ballot_sync(0xFFFFFFFFu, run + s > point);
-      if (past != 0u) found = c * 32 + __ffs((int)past) - 1;
-      run += __shfl_sync(0xFFFFFFFFu, s, 31);
+      // narrow [a, b) to one entry: 32 runs of entries, one a lane, each time
+      int a = part_begin(vocab, p), b = part_begin(vocab, p + 1);
+      while (b - a > 1) {
+        const int len = (b - a + 31) / 32;
+        const int x0 = min(a + lane * len, b), x1 = min(x0 + len, b);
+        long long w = 0;
+#pragma unroll 8
+        for (int x = x0; x < x1; ++x) w += weight(row, x);
+        const long long sc = warp_scan(w, lane);
+        const int l = __ffs((int)__ballot_sync(0xFFFFFFFFu, run + sc > point)) - 1;
+        run += __shfl_sync(0xFFFFFFFFu, sc - w, l);
+        const int na = min(a + l * len, b);
+        b = min(na + len, b);
+        a = na;
+      }
+      found = a;
     }
-    if (lane < kVCluster) {
-      const uint32_t dst = map_rank(smem_u32(&sh.found[d & 1]), (uint32_t)lane);
-      asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(dst), "r"(found) : "memory");
-    }
+    if (lane == 0) sh.found[d & 1] = found;
   }
-  cluster_sync();
-  *token = total > 0 ? sh.found[d & 1] : -1;
-  return total > 0;
+  __syncthreads();
+  *token = sh.found[d & 1];
+  return *token >= 0;
 }
 
 __global__ void __cluster_dims__(kVCluster, 1, 1) __launch_bounds__(kVThreads)

@@ -652,9 +652,9 @@ static rq_status check_qk(const rq_qk_params* p, const int32_t* position) {
   return RQ_OK;
 }
 
-// Blocks of 8 warps, at most one row a warp: keep the grid below 2^31.
+// At most one row a warp, and warps are numbered in 31 bits.
 static bool tokens_ok(int tokens, int rows) {
-  return tokens >= 0 && rows >= 1 && (int64_t)tokens * rows < (int64_t)1 << 33;
+  return tokens >= 0 && rows >= 1 && (int64_t)tokens * rows < 0x7FFFFF00LL;
 }
 
 rq_status rq_qk_norm_rope(const rq_qk_params* params, int dtype, const void* q, int64_t q_stride,

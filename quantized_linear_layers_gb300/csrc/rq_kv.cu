@@ -34,10 +34,18 @@ struct RowsArgs {
   int64_t slots;
   int lg_page, hkv, format;
   int hq, hk, hv;  // rows of each kind per token (0: that side is left out)
-  int rows, tasks;  // hq + hk + hv, and tasks of RPW rows per token
+  int tq, tk;      // tasks of q and of k rows per token
+  int tasks;       // tasks per token; a warp takes one
+  uint32_t task_mul, task_shift;  // quotients by tasks: see divide
   int tokens, rotary, interleaved;
   float eps;
 };
+
+// n / d for n < 2^31 as a product with m = floor(2^32 (2^s - d) / d) + 1, s =
+// ceil(log2 d) (the round-up method of Granlund and Montgomery).
+__device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t mul, uint32_t shift) {
+  return (__umulhi(n, mul) + n) >> shift;
+}
 
 // E consecutive values of an activation row as floats, and back.
 template <typename T, int E>
@@ -122,12 +130,6 @@ __device__ __forceinline__ void load_table(const float* p, float (&x)[N]) {
   }
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  return v;
-}
-
 // One code byte; what is not finite takes its sign's largest code.
 __device__ __forceinline__ uint32_t encode_e4m3(float x, float s) {
   if (non_finite(x)) return saturated_code(x);
@@ -139,11 +141,56 @@ __device__ __forceinline__ uint32_t encode_i8(float x, float s) {
   return (uint32_t)__float2int_rn(fminf(fmaxf(y, -127.0f), 127.0f)) & 0xFFu;
 }
 
-// One warp takes RPW rows of one token at once: lane l holds values
-// [l E, l E + E) of each, E = D / 32.  The rotation's partner values are in
-// the lane rotary / 2 / E away (host: rotary % 16 == 0, so that distance is a
-// whole number), the sums and maxima are shuffles: a row is read once and
-// nothing passes through shared memory.
+// Two code bytes of finite values.  Integers by the addition of 1.5 2^23,
+// which rounds to the nearest even one and leaves it in the low bits; the
+// product with top / max is at most top but for two roundings, so that no
+// limit is needed before rounding.
+__device__ __forceinline__ uint32_t encode2(bool e4m3, float lo, float hi, float s) {
+  const float a = __fmul_rn(lo, s), b = __fmul_rn(hi, s);
+  if (e4m3) return cvt_e4m3x2(b, a);
+  return __byte_perm(__float_as_uint(a + 12582912.0f), __float_as_uint(b + 12582912.0f), 0x0040) &
+         0xFFFFu;
+}
+
+// 1 / sqrt(x): the approximate instruction and one Newton step.
+__device__ __forceinline__ float inv_sqrt(float x) {
+  const float y = rsqrtf(x);
+  const float h = 0.5f * x * y;
+  const float r = fmaf(-h, y, 0.5f);
+  // (an infinite or zero x leaves r NaN: the instruction's value stands)
+  return r == r ? fmaf(y, r, y) : y;
+}
+
+// Sums of R rows over the warp: a lane ends with row `R - 1 bits of its lane
+// number's top` -- for R = 4, row 2 b4 + b3 of lane bits 4 and 3 -- since each
+// of the first steps halves the rows that it holds instead of adding all of
+// them five times.
+template <int R>
+__device__ __forceinline__ float rows_sum(const float (&v)[R], int lane) {
+  if constexpr (R == 1) {
+    return warp_sum(v[0]);
+  } else {
+    static_assert(R == 4, "1 or 4 rows a warp");
+    const bool b4 = (lane & 16) != 0, b3 = (lane & 8) != 0;
+    const float k0 = b4 ? v[2] : v[0], g0 = b4 ? v[0] : v[2];
+    const float k1 = b4 ? v[3] : v[1], g1 = b4 ? v[1] : v[3];
+    const float a0 = k0 + __shfl_xor_sync(0xFFFFFFFFu, g0, 16);
+    const float a1 = k1 + __shfl_xor_sync(0xFFFFFFFFu, g1, 16);
+    float b = (b3 ? a1 : a0) + __shfl_xor_sync(0xFFFFFFFFu, b3 ? a0 : a1, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    return b;
+  }
+}
+
+// A warp takes RPW rows of one kind (q, k or v) and one token: lane l holds
+// values [l E, l E + E) of each, E = D / 32.  The rotation's partner values
+// are in the lane rotary / 2 / E away (host: rotary % 16 == 0, so that
+// distance is a whole number); sums are shuffles, maxima one warp reduction
+// of the magnitudes' bits: a row is read once and nothing passes through
+// shared memory.  Bound by memory from a few hundred tokens on (4096 tokens
+// of 28 + 4 + 4 heads of 128 in f32: 26 us, 5.4 TB/s), by launch and load
+// latency below.
 template <typename T, int E, int RPW>
 __global__ void __launch_bounds__(kRowThreads)
 rows_kernel(const RowsArgs a) {
@@ -151,30 +198,33 @@ rows_kernel(const RowsArgs a) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int64_t task = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = task / a.tasks;
-  if (t >= a.tokens) return;
-  const int j0 = (int)(task - t * a.tasks) * RPW;
+  const uint32_t task = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t t = divide(task, a.task_mul, a.task_shift);
+  if (t >= (uint32_t)a.tokens) return;
+  const int j = (int)(task - t * a.tasks);
   const int d0 = lane * E;
 
+  // the task's rows
+  const bool is_q = j < a.tq, is_k = !is_q && j < a.tq + a.tk;
+  const int h0 = (is_q ? j : is_k ? j - a.tq : j - a.tq - a.tk) * RPW;
+  const int n = min(RPW, (is_q ? a.hq : is_k ? a.hk : a.hv) - h0);
+  const T* src = static_cast<const T*>(is_q ? a.q : is_k ? a.k : a.v) +
+                 (int64_t)t * (is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride) +
+                 (int64_t)h0 * D + d0;
   float x[RPW][E];
 #pragma unroll
   for (int r = 0; r < RPW; ++r) {
-    const int j = j0 + r;
-    if (j >= a.rows) continue;
-    const T* p;
-    if (j < a.hq)
-      p = static_cast<const T*>(a.q) + t * a.q_stride + (int64_t)j * D;
-    else if (j < a.hq + a.hk)
-      p = static_cast<const T*>(a.k) + t * a.k_stride + (int64_t)(j - a.hq) * D;
-    else
-      p = static_cast<const T*>(a.v) + t * a.v_stride + (int64_t)(j - a.hq - a.hk) * D;
-    load_row<T, E>(p + d0, x[r]);
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[r][i] = 0.0f;
+    if (r < n) load_row<T, E>(src + r * D, x[r]);
   }
+  const bool stored = a.slot != nullptr && !is_q;
+  int64_t slot = -1;
+  if (stored) slot = a.slot[t];
 
   // the token's turn: cos and sin of this lane's pairs
   const int half = a.rotary >> 1;
-  bool turn = a.rotary > 0 && j0 < a.hq + a.hk;
+  bool turn = a.rotary > 0 && (is_q || is_k);
   float c[E], s[E];
   if (turn) {
     const int64_t at = a.position[t];
@@ -200,36 +250,30 @@ rows_kernel(const RowsArgs a) {
       }
     }
   }
-  const int hop = half / E;
-  const int partner = a.interleaved ? lane : (d0 < half ? lane + hop : lane - hop) & 31;
 
-  int64_t slot = -1;
-  if (a.slot != nullptr && j0 + RPW > a.hq) {
-    slot = a.slot[t];
-    if (slot >= a.slots) {
-      if (lane == 0) atomicOr(&g_kv_error, 2u);
-      slot = -1;
+  const float* weight = is_q ? a.q_weight : is_k ? a.k_weight : nullptr;
+  if (weight != nullptr) {
+    float w[E], sq[RPW];
+    load_table<E>(weight + d0, w);
+#pragma unroll
+    for (int r = 0; r < RPW; ++r) {
+      sq[r] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < E; ++i) sq[r] = fmaf(x[r][i], x[r][i], sq[r]);
     }
-  }
-
-  const int hqk = a.hq + a.hk;
+    const float own = inv_sqrt(rows_sum<RPW>(sq, lane) * (1.0f / D) + a.eps);
 #pragma unroll
-  for (int r = 0; r < RPW; ++r) {
-    const int j = j0 + r;
-    if (j >= a.rows) break;
-    const float* weight = j < a.hq ? a.q_weight : j < hqk ? a.k_weight : nullptr;
-    if (weight != nullptr) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < E; ++i) sum = fmaf(x[r][i], x[r][i], sum);
-      sum = warp_sum(sum);
-      const float inv = 1.0f / sqrtf(sum * (1.0f / D) + a.eps);
-      float w[E];
-      load_table<E>(weight + d0, w);
+    for (int r = 0; r < RPW; ++r) {
+      const float inv = RPW == 1 ? own : __shfl_sync(0xFFFFFFFFu, own, (r >> 1) * 16 + (r & 1) * 8);
 #pragma unroll
       for (int i = 0; i < E; ++i) x[r][i] = x[r][i] * inv * w[i];
     }
-    if (turn && j < hqk) {
+  }
+  if (turn) {
+    const int hop = half / E;
+    const int partner = (d0 < half ? lane + hop : lane - hop) & 31;
+#pragma unroll
+    for (int r = 0; r < RPW; ++r) {
       float o[E];
       if (a.interleaved) {
 #pragma unroll
@@ -243,41 +287,75 @@ rows_kernel(const RowsArgs a) {
         for (int i = 0; i < E; ++i) x[r][i] = fmaf(x[r][i], c[i], o[i] * s[i]);
       }
     }
-    if (j < a.hq) {
-      store_row<T, E>(static_cast<T*>(a.q_out) + (t * a.hq + j) * D + d0, x[r]);
-      continue;
-    }
-    const bool is_v = j >= hqk;
-    const int h = is_v ? j - hqk : j - a.hq;
-    if (a.slot == nullptr) {
-      store_row<T, E>(static_cast<T*>(a.k_out) + (t * a.hk + h) * D + d0, x[r]);
-      continue;
-    }
-    if (slot < 0) continue;
-    float m = 0.0f;
+  }
+
+  if (!stored) {
+    T* dst = is_q ? static_cast<T*>(a.q_out) + ((int64_t)t * a.hq + h0) * D + d0
+                  : static_cast<T*>(a.k_out) + ((int64_t)t * a.hk + h0) * D + d0;
 #pragma unroll
-    for (int i = 0; i < E; ++i) m = fmaxf(m, non_finite(x[r][i]) ? 0.0f : fabsf(x[r][i]));
-    m = fmaxf(warp_max(m), kLeastMax);
-    const float top = a.format == RQ_KV_E4M3 ? 448.0f : 127.0f;
-    const float mul = __fmul_rn(top, __frcp_rn(m));
-    alignas(8) uint8_t b[E];
-    if (a.format == RQ_KV_E4M3) {
+    for (int r = 0; r < RPW; ++r)
+      if (r < n) store_row<T, E>(dst + r * D, x[r]);
+    return;
+  }
+  if (slot >= a.slots) {
+    if (lane == 0) atomicOr(&g_kv_error, 2u);
+    slot = -1;
+  }
+  if (slot < 0) return;
+  const bool e4m3 = a.format == RQ_KV_E4M3;
+  const float top = e4m3 ? 448.0f : 127.0f;
+  const int64_t page = slot >> a.lg_page;
+  // heads of a token lie a page's tokens apart
+  const int64_t row = ((page * a.hkv + h0) << a.lg_page) + (slot & ((1 << a.lg_page) - 1));
+  uint32_t most[RPW], own = 0u;  // largest magnitudes, as bits; lane r keeps row r's
 #pragma unroll
-      for (int i = 0; i < E; ++i) b[i] = (uint8_t)encode_e4m3(x[r][i], mul);
+  for (int r = 0; r < RPW; ++r) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < E; ++i) m = max(m, __float_as_uint(x[r][i]) & 0x7FFFFFFFu);
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    most[r] = m;
+    if (m >= 0x7F800000u) {  // something is not finite: the largest of the rest
+      m = 0u;
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (!non_finite(x[r][i])) m = max(m, __float_as_uint(x[r][i]) & 0x7FFFFFFFu);
+      m = __reduce_max_sync(0xFFFFFFFFu, m);
+    }
+    if (lane == r) own = m;
+  }
+  // the rows' divisions side by side, a lane each
+  const float own_max = fmaxf(__uint_as_float(own), kLeastMax);
+  const float own_mul = __fmul_rn(top, __frcp_rn(own_max));
+  if (lane < n) (is_k ? a.ks : a.vs)[row + ((int64_t)lane << a.lg_page)] = __fdiv_rn(own_max, top);
+  uint8_t* dst = (is_k ? a.kc : a.vc) + row * D + d0;
+#pragma unroll
+  for (int r = 0; r < RPW; ++r) {
+    const float mul = RPW == 1 ? __shfl_sync(0xFFFFFFFFu, own_mul, 0)
+                               : __shfl_sync(0xFFFFFFFFu, own_mul, r);
+    if (r >= n) break;
+    uint32_t code[(E + 3) / 4];
+    if (most[r] < 0x7F800000u) {
+      code[0] = encode2(e4m3, x[r][0], x[r][1], mul);
+#pragma unroll
+      for (int i = 2; i < E; i += 2) {
+        const uint32_t two = encode2(e4m3, x[r][i], x[r][i + 1], mul);
+        code[i / 4] = (i & 3) ? code[i / 4] | two << 16 : two;
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < E; ++i) b[i] = (uint8_t)encode_i8(x[r][i], mul);
+      for (int i = 0; i < E; ++i) {
+        const uint32_t one = e4m3 ? encode_e4m3(x[r][i], mul) : encode_i8(x[r][i], mul);
+        code[i / 4] = (i & 3) ? code[i / 4] | one << (8 * (i & 3)) : one;
+      }
     }
-    const int64_t page = slot >> a.lg_page;
-    const int64_t row = ((page * a.hkv + h) << a.lg_page) + (slot & ((1 << a.lg_page) - 1));
-    uint8_t* dst = (is_v ? a.vc : a.kc) + row * D + d0;
+    uint8_t* to = dst + (((int64_t)r << a.lg_page) * D);
     if constexpr (E == 2)
-      *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(b);
+      *reinterpret_cast<uint16_t*>(to) = (uint16_t)code[0];
     else if constexpr (E == 4)
-      *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(b);
+      *reinterpret_cast<uint32_t*>(to) = code[0];
     else
-      *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(b);
-    if (lane == 0) (is_v ? a.vs : a.ks)[row] = __fdiv_rn(m, top);
+      *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[1]);
   }
 }
 
@@ -287,8 +365,14 @@ rq_status launch_rows_rpw(RowsArgs a, cudaStream_t st) {
   // token's rows then run side by side.  Four rows per warp otherwise, so
   // that cos, sin and the slot are fetched once for four and the loads of
   // four rows are in flight together.
-  const int rpw = (int64_t)a.tokens * a.rows <= 8 * (int64_t)device_sm_count() ? 1 : 4;
-  a.tasks = (a.rows + rpw - 1) / rpw;
+  const int rows = a.hq + a.hk + a.hv;
+  const int rpw = (int64_t)a.tokens * rows <= 8 * (int64_t)device_sm_count() ? 1 : 4;
+  a.tq = (a.hq + rpw - 1) / rpw;
+  a.tk = (a.hk + rpw - 1) / rpw;
+  a.tasks = a.tq + a.tk + (a.hv + rpw - 1) / rpw;
+  a.task_shift = 0;
+  while ((1ull << a.task_shift) < (unsigned long long)a.tasks) ++a.task_shift;
+  a.task_mul = (uint32_t)((((1ull << a.task_shift) - (unsigned)a.tasks) << 32) / (unsigned)a.tasks) + 1u;
   const int64_t warps = (int64_t)a.tokens * a.tasks;
   const unsigned grid = (unsigned)((warps + kRowThreads / 32 - 1) / (kRowThreads / 32));
   return rpw == 1 ? launch_kernel(rows_kernel<T, E, 1>, grid, kRowThreads, 0, st, a)
@@ -332,37 +416,55 @@ void set_cache(RowsArgs& a, const rq_kv_cache& c, const int64_t* slot) {
 
 // ----------------------------------------------------------- read back --
 
-// One thread takes 8 codes of k and the same 8 of v.
+// A thread takes kReadRuns runs of 8 codes of k and the same of v, 256 runs
+// apart, so that the warps' stores stay whole lines and several loads are in
+// flight behind each slot's (30000 tokens of 4 heads of 128: 16.1 us, 5.8 TB/s with two
+// runs, 18.1 us with one, 16.3 us with four).
+constexpr int kReadRuns = 2;
 template <typename T>
 __global__ void __launch_bounds__(256)
 read_kernel(const rq_kv_cache c, const int64_t* __restrict__ slot, int tokens, int lg_page,
             int lg_chunks, T* __restrict__ k_out, T* __restrict__ v_out) {
   pdl_wait();
   pdl_trigger();
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = id >> lg_chunks;  // token * kv_heads + head
-  const int64_t t = row / c.kv_heads;
-  if (t >= tokens) return;
-  const int h = (int)(row - t * c.kv_heads);
-  int64_t s = slot[t];
-  if (s >= c.pages << lg_page) {
-    atomicOr(&g_kv_error, 2u);
-    s = -1;
-  }
-  float x[2][8] = {};
-  if (s >= 0) {
-    const int64_t src =
-        (((s >> lg_page) * c.kv_heads + h) << lg_page) + (s & ((1 << lg_page) - 1));
-    const int64_t chunk = (src << lg_chunks) + (id & ((1 << lg_chunks) - 1));
-    const uint2 kb = __ldg(reinterpret_cast<const uint2*>(c.k) + chunk);
-    const uint2 vb = __ldg(reinterpret_cast<const uint2*>(c.v) + chunk);
-    const float sc[2] = {__ldg(c.k_scale + src), __ldg(c.v_scale + src)};
-    const uint32_t w[2][2] = {{kb.x, kb.y}, {vb.x, vb.y}};
+  const int64_t id0 = (int64_t)blockIdx.x * (256 * kReadRuns) + threadIdx.x;
+  uint2 codes[kReadRuns][2];
+  float scale[kReadRuns][2];
+  bool live[kReadRuns];
 #pragma unroll
-    for (int o = 0; o < 2; ++o)
+  for (int u = 0; u < kReadRuns; ++u) {
+    const int64_t id = id0 + 256 * u;
+    const uint32_t at = (uint32_t)(id >> lg_chunks);  // token * kv_heads + head, below 2^31
+    const uint32_t t = at / (uint32_t)c.kv_heads;
+    const int h = (int)(at - t * (uint32_t)c.kv_heads);
+    live[u] = t < (uint32_t)tokens;
+    int64_t s = live[u] ? slot[t] : -1;
+    if (s >= c.pages << lg_page) {
+      atomicOr(&g_kv_error, 2u);
+      s = -1;
+    }
+    codes[u][0] = codes[u][1] = make_uint2(0u, 0u);
+    scale[u][0] = scale[u][1] = 0.0f;
+    if (s >= 0) {
+      const int64_t src =
+          (((s >> lg_page) * c.kv_heads + h) << lg_page) + (s & ((1 << lg_page) - 1));
+      const int64_t chunk = (src << lg_chunks) + (id & ((1 << lg_chunks) - 1));
+      codes[u][0] = __ldg(static_cast<const uint2*>(c.k) + chunk);
+      codes[u][1] = __ldg(static_cast<const uint2*>(c.v) + chunk);
+      scale[u][0] = __ldg(c.k_scale + src);
+      scale[u][1] = __ldg(c.v_scale + src);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kReadRuns; ++u) {
+    if (!live[u]) continue;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      const uint32_t w[2] = {codes[u][o].x, codes[u][o].y};
+      float x[8];
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
-        const uint32_t pair = w[o][i / 4] >> (8 * (i & 3));
+        const uint32_t pair = w[i / 4] >> (8 * (i & 3));
         float lo, hi;
         if (c.format == RQ_KV_E4M3) {
           uint32_t h2;
@@ -374,12 +476,12 @@ read_kernel(const rq_kv_cache c, const int64_t* __restrict__ slot, int tokens, i
           lo = (float)(int8_t)(pair & 0xFFu);
           hi = (float)(int8_t)((pair >> 8) & 0xFFu);
         }
-        x[o][i] = lo * sc[o];
-        x[o][i + 1] = hi * sc[o];
+        x[i] = lo * scale[u][o];
+        x[i + 1] = hi * scale[u][o];
       }
+      store_row<T, 8>((o == 0 ? k_out : v_out) + (id0 + 256 * u) * 8, x);
+    }
   }
-  store_row<T, 8>(k_out + id * 8, x[0]);
-  store_row<T, 8>(v_out + id * 8, x[1]);
 }
 
 template <typename T>
@@ -387,7 +489,7 @@ rq_status launch_read_t(const rq_kv_cache& c, const int64_t* slot, void* k_out, 
                         int tokens, cudaStream_t st) {
   const int lg_chunks = log2_of(c.head_dim / 8);
   const int64_t threads = ((int64_t)tokens * c.kv_heads) << lg_chunks;
-  return launch_kernel(read_kernel<T>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st,
+  return launch_kernel(read_kernel<T>, dim3((unsigned)((threads + 256 * kReadRuns - 1) / (256 * kReadRuns))), dim3(256), 0, st,
                        c, slot, tokens, log2_of(c.page_size), lg_chunks, static_cast<T*>(k_out),
                        static_cast<T*>(v_out));
 }
@@ -429,7 +531,6 @@ rq_status launch_qkv_rows(const rq_qk_params* p, int dtype, const void* q, int64
   }
   a.hk = k != nullptr ? hkv : 0;
   a.hv = v != nullptr ? hkv : 0;
-  a.rows = a.hq + a.hk + a.hv;
   if (cache != nullptr) set_cache(a, *cache, slot);
   return launch_rows(a, dtype, head_dim, st);
 }

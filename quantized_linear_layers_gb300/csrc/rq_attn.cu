@@ -142,7 +142,7 @@ attn_kernel(const AttnArgs a) {
 
   prefetch_l2(a.q, a.q_bytes);
   prefetch_l2(a.table, (int64_t)a.batch * a.max_pages * 4);
-  Cutter<kRows, kKeys, W, 4> cutter(a, tail.cut);
+  Cutter<kRows, kKeys, W, 6> cutter(a, tail.cut);
   cutter.template choose<G::kThreads>();
   Segment seg;
   if (!cutter.begin(seg)) return;
@@ -150,14 +150,17 @@ attn_kernel(const AttnArgs a) {
   // -------- the warp's loads, S units ahead of its products
   Segment ld = seg;
   int unit = ld.first + warp;          // next unit to load
-  int in_window = 32, pages_of = 0;    // lane i: page of the window's unit i, W units apart
+  int in_window = 0, pages_of = 0;     // lane i: page of the window's unit i, W units apart
   int ld_stage = 0;
-  auto page_window = [&]() {
+  auto page_window = [&]() {  // (looked at when they are used)
     in_window = 0;
     const int64_t u = unit + (int64_t)lane * W;
     pages_of = 0;
-    if (u < ld.end && u * kKeys < ld.kv) pages_of = page_of(a, ld.item / a.row_tiles, u * kKeys);
+    if (u < ld.end && u * kKeys < ld.kv)
+      pages_of = a.table[(int64_t)cutter.sequence(ld.item) * a.max_pages +
+                         ((u * kKeys) >> a.lg_page)];
   };
+  page_window();
   const int page_mask = (1 << a.lg_page) - 1;
   // where this lane's first piece of a unit goes
   const int piece_row = lane * 16 / D, piece_chunk = lane * 16 % D / 16;
@@ -171,8 +174,12 @@ attn_kernel(const AttnArgs a) {
     }
     if (unit < ld.end && ld.kv > 0) {
       if (in_window == 32) page_window();
-      const int page = __shfl_sync(0xFFFFFFFFu, pages_of, in_window);
+      int page = __shfl_sync(0xFFFFFFFFu, pages_of, in_window);
       ++in_window;
+      if (page < 0 || page >= a.pages) {
+        if (lane == 0) atomicOr(a.error, 2u);
+        page = 0;
+      }
       const int64_t row = ((int64_t)(page * a.kv_heads + ld.head) << a.lg_page) +
                           ((unit * kKeys) & page_mask);
       const uint32_t to = ring + ld_stage * (2 * G::kBytes) + piece;
@@ -192,19 +199,19 @@ attn_kernel(const AttnArgs a) {
       swizzled<G::kPanel>(((lane >> 3) & 1) * 8 + (lane & 7), lane >> 4);
   int st = 0;  // ring stage of the next unit
   for (int nseg = 0;; ++nseg) {
-    const int b = seg.item / a.row_tiles, rt = seg.item - b * a.row_tiles;
+    const int b = cutter.sequence(seg.item), rt = seg.item - b * a.row_tiles;
     const int kv = seg.kv;
     // this thread's row: g
     const int row_of = rt * kRows + g;
     const bool live = row_of < a.rows;
-    const int tok = live ? row_of / a.group : 0;
+    const int tok = live ? (int)quotient((uint32_t)row_of, a.by_group) : 0;
     unsigned long long bits = 0;
     if (live && a.tree != nullptr) bits = a.tree[(int64_t)b * a.new_tokens + tok];
     float c;  // powers of two per unit of the raw score x = (q . k8) ks
     uint32_t qa[D / 16][4];
     {
       const int64_t off = ((int64_t)b * a.new_tokens + tok) * a.q_stride +
-                          (int64_t)(seg.head * a.group + (live ? row_of % a.group : 0)) * D;
+                          (int64_t)(seg.head * a.group + (live ? row_of - tok * a.group : 0)) * D;
       // the first loads of keys and values go out while q is on its way (or
       // before it, where its raw values would not stay in registers)
       if (nseg == 0 && D == 256)
@@ -553,8 +560,9 @@ attn_kernel(const AttnArgs a) {
         // nothing seen: zeros (a NaN sum stays a NaN)
         const float r1 = sum[k] == 0.0f ? 0.0f : 1.0f / sum[k];
         const float4 y = make_float4(v[k].x * r1, v[k].y * r1, v[k].z * r1, v[k].w * r1);
-        const int64_t dst = (((int64_t)b * a.new_tokens + row / a.group) * a.q_heads +
-                             seg.head * a.group + row % a.group) * D + d;
+        const int tk = (int)quotient((uint32_t)row, a.by_group);
+        const int64_t dst = (((int64_t)b * a.new_tokens + tk) * a.q_heads + seg.head * a.group +
+                             row - tk * a.group) * D + d;
         if (a.dtype == RQ_F32) {
           *reinterpret_cast<float4*>(static_cast<float*>(a.out) + dst) = y;
         } else if (a.dtype == RQ_F16) {
@@ -626,6 +634,9 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
   a.group = call.q_heads / c.kv_heads;
   a.rows = call.new_tokens * a.group;
   a.row_tiles = (a.rows + kRows - 1) / kRows;
+  a.by_heads = divisor((uint32_t)a.kv_heads);
+  a.by_group = divisor((uint32_t)a.group);
+  a.by_tiles = divisor((uint32_t)a.row_tiles);
   a.max_pages = call.max_pages;
   a.lg_page = lg(c.page_size);
   a.pages = c.pages;

@@ -20,6 +20,7 @@ struct AttnArgs {
   const int32_t *table, *length;
   const unsigned long long* tree;
   int batch, new_tokens, q_heads, kv_heads, group, rows, row_tiles;
+  Divisor by_heads, by_group, by_tiles;  // kv_heads, group, row_tiles
   int max_pages, lg_page;
   int64_t pages;
   float scale_log2;
@@ -163,6 +164,10 @@ struct Cutter {
   __device__ __forceinline__ Cutter(const AttnArgs& args, CutShared& shared)
       : a(args), sh(shared) {}
 
+  __device__ __forceinline__ int sequence(int item) const {
+    return (int)quotient((uint32_t)item, a.by_tiles);
+  }
+
   // Places that row tile rt of a sequence of n cached tokens may see.  Up to
   // 64 new tokens every tile takes them all: a chain is then cut as a tree of
   // one branch is, and gives its bits.
@@ -177,7 +182,7 @@ struct Cutter {
     if (a.new_tokens > 64) {
       int last = (rt + 1) * ROWS;
       last = (last < a.rows ? last : a.rows) - 1;
-      const int64_t end = (int64_t)n + last / a.group + 1;
+      const int64_t end = (int64_t)n + quotient((uint32_t)last, a.by_group) + 1;
       kv = end < kv ? end : kv;
     }
     return (int)(kv < 0x7FFFFF00 ? kv : 0x7FFFFF00);
@@ -208,7 +213,7 @@ struct Cutter {
       const int i = base + tid;
       int n = 0;
       if (i < items) {
-        const int b = i / a.row_tiles, rt = i - b * a.row_tiles;
+        const int b = sequence(i), rt = i - b * a.row_tiles;
         const int len = a.length[b];
         if (rt == 0) sh.length[b] = len;
         n = units_of(places(len, rt));
@@ -241,9 +246,10 @@ struct Cutter {
       const int64_t segments = (int64_t)items * a.kv_heads;
       int cut = kWhole, split = 1;
       if (segments <= grid) {
-        split = min(grid / (int)segments, (most + kLeast - 1) / kLeast);
-        const int64_t even = (units + (int64_t)grid * STEP - 1) / ((int64_t)grid * STEP);
-        cut = (most + split * STEP - 1) / (split * STEP) <= even + ROUNDS ? kParts : kRun;
+        split = (int)min((uint32_t)grid / (uint32_t)segments, (uint32_t)(most + kLeast - 1) / kLeast);
+        // the longest part's rounds against an even share's
+        const int64_t longest = ((int64_t)most + split - 1) * grid;
+        cut = longest <= (units + (int64_t)ROUNDS * STEP * grid) * split ? kParts : kRun;
       } else if (most > kLeast) {
         cut = kRun;
       }
@@ -256,7 +262,7 @@ struct Cutter {
   }
 
   __device__ __forceinline__ void open(Segment& g) const {  // item, head, first, left are set
-    const int b = g.item / a.row_tiles;
+    const int b = sequence(g.item);
     g.kv = places(length(b), g.item - b * a.row_tiles);
     const int n = units_of(g.kv);
     if (sh.cut == kRun) {
@@ -277,13 +283,15 @@ struct Cutter {
     open(g);
   }
 
-  // kParts: units [first, end) of a segment of n that are part `part` of it.
+  // kParts: units [first, end) of a segment of n that are part `part` of it,
+  // of *parts.
   __device__ __forceinline__ bool part_of(int n, int part, int* parts, int* first, int* end) const {
-    *parts = min(sh.split, (n + kLeast - 1) / kLeast);
-    if (part >= *parts) return false;
-    *first = (int)((int64_t)n * part / *parts);
-    *end = (int)((int64_t)n * (part + 1) / *parts);
-    return true;
+    const uint32_t want = min((uint32_t)sh.split, (uint32_t)(n + kLeast - 1) / kLeast);
+    const uint32_t each = ((uint32_t)n + want - 1u) / want;
+    *parts = (int)(((uint32_t)n + each - 1u) / each);
+    *first = part * (int)each;
+    *end = min(n, *first + (int)each);
+    return part < *parts;
   }
 
   // This CTA's first segment; false if it has no work.
@@ -313,7 +321,7 @@ struct Cutter {
     const int segments = items * a.kv_heads;
     int s0 = (int)blockIdx.x, s1 = s0 + 1;
     if (sh.cut == kParts) {
-      s0 /= sh.split;
+      s0 = (int)((uint32_t)s0 / (uint32_t)sh.split);
       s1 = s0 + 1;
       if (s0 >= segments) return false;
     } else if (!a.direct) {
@@ -321,7 +329,7 @@ struct Cutter {
       s1 = (int)((int64_t)segments * (blockIdx.x + 1) / grid);
       if (s0 >= s1) return false;
     }
-    g.item = s0 / a.kv_heads;
+    g.item = (int)quotient((uint32_t)s0, a.by_heads);
     g.head = s0 - g.item * a.kv_heads;
     g.left = s1 - s0;
     open(g);
@@ -351,7 +359,7 @@ struct Cutter {
       r.part = (int)(blockIdx.x - r.cta0);
       r.second = sh.units * r.cta0 / grid < s0;
     } else if (sh.cut == kParts) {
-      r.part = (int)blockIdx.x % sh.split;
+      r.part = (int)(blockIdx.x % (uint32_t)sh.split);
       r.cta0 = (int64_t)blockIdx.x - r.part;
       int first, end;
       part_of(units_of(g.kv), r.part, &r.parts, &first, &end);

@@ -284,7 +284,7 @@ struct PageWindow {
   int cur, nxt, window;
   __device__ __forceinline__ int load(const AttnArgs& a, const Segment& g, int w, int lane) const {
     const int64_t place = ((int64_t)w * 32 + lane) * 16;
-    return place < g.kv ? page_of(a, g.item / a.row_tiles, place) * a.kv_heads + g.head : 0;
+    return place < g.kv ? page_of(a, (int)quotient((uint32_t)g.item, a.by_tiles), place) * a.kv_heads + g.head : 0;
   }
   __device__ __forceinline__ void open(const AttnArgs& a, const Segment& g, int u, int lane) {
     window = u >> 3;
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
     uint32_t units = 0;            // of this row tile so far
     uint32_t all_units = 0;        // of the CTA: the scales' ring
     for (;;) {
-      const int b = seg.item / a.row_tiles, rt = seg.item - b * a.row_tiles;
+      const int b = cutter.sequence(seg.item), rt = seg.item - b * a.row_tiles;
       const int row0 = rt * kRows + w * kTileRows;
       const int n_units = seg.end - seg.first;
       float l = 0.0f, ref = -INFINITY, c = 0.0f, vref = 0x1p-112f;
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         constexpr int E = D / 32;
         const int my_row = row0 + quad * 32 + lane;
         const bool live = my_row < a.rows;
-        const int tok = live ? my_row / a.group : 0;
+        const int tok = live ? (int)quotient((uint32_t)my_row, a.by_group) : 0;
         const int64_t my_off =
             ((int64_t)b * a.new_tokens + tok) * a.q_stride +
             (int64_t)(seg.head * a.group + (live ? my_row - tok * a.group : 0)) * D;
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         const int my = w * kTileRows + quad * 32;  // the warp's first row of the segment
         const int my_row = rt * kRows + my + lane;
         const bool live = my_row < a.rows;
-        const int tok = live ? my_row / a.group : 0;
+        const int tok = live ? (int)quotient((uint32_t)my_row, a.by_group) : 0;
         const int64_t my_dst = (((int64_t)b * a.new_tokens + tok) * a.q_heads +
                                 seg.head * a.group + (live ? my_row - tok * a.group : 0)) * D;
         const float back = vref * (1.0f / kUp);
@@ -875,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       commit(smem_u32(&tail.s_full[w][my_no & 1u]));
     };
     for (;;) {
-      const int b = seg.item / a.row_tiles, rt = seg.item - b * a.row_tiles;
+      const int b = cutter.sequence(seg.item), rt = seg.item - b * a.row_tiles;
       const int nw = rt * kRows + kTileRows < a.rows ? 2 : 1;
       const int n = seg.end - seg.first;
       // the first scores of the segment
@@ -1053,6 +1053,7 @@ rq_status launch_rows(const AttnArgs& a, unsigned grid, cudaStream_t st) {
 rq_status launch_attention_rows(AttnArgs a, int head_dim, bool i8, AttnScratch* scratch,
                                 cudaStream_t st) {
   a.row_tiles = (a.rows + kRows - 1) / kRows;
+  a.by_tiles = divisor((uint32_t)a.row_tiles);
   const int64_t items = (int64_t)a.batch * a.row_tiles;
   const int64_t segments = items * a.kv_heads;
   int64_t grid = device_sm_count();

@@ -242,6 +242,12 @@ __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// n / d.d for n < 2^31 (rq_internal.h, divisor).
+template <typename D>
+__device__ __forceinline__ uint32_t quotient(uint32_t n, const D& d) {
+  return (__umulhi(n, d.mul) + n) >> d.shift;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);

@@ -16,6 +16,19 @@ inline rq_status launch_status() { return cuda_status(cudaGetLastError()); }
 
 int device_sm_count();
 
+// Division of n < 2^31 by a d >= 1 known on the host: (hi32(n mul) + n) >>
+// shift with mul = floor(2^32 (2^shift - d) / d) + 1 and shift = ceil(log2 d)
+// (the round-up method of Granlund and Montgomery); quotient() on the device.
+struct Divisor {
+  uint32_t mul, shift, d;
+};
+inline Divisor divisor(uint32_t d) {
+  Divisor r = {0u, 0u, d};
+  while ((1ull << r.shift) < d) ++r.shift;
+  r.mul = (uint32_t)((((1ull << r.shift) - d) << 32) / d) + 1u;
+  return r;
+}
+
 // Programmatic dependent launch of the library's kernels (on unless the
 // environment sets RQ_PDL=0 when the library first launches).
 bool pdl_enabled();

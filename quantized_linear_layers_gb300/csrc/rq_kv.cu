@@ -35,17 +35,10 @@ struct RowsArgs {
   int lg_page, hkv, format;
   int hq, hk, hv;  // rows of each kind per token (0: that side is left out)
   int tq, tk;      // tasks of q and of k rows per token
-  int tasks;       // tasks per token; a warp takes one
-  uint32_t task_mul, task_shift;  // quotients by tasks: see divide
+  Divisor tasks;   // tasks per token; a warp takes one
   int tokens, rotary, interleaved;
   float eps;
 };
-
-// n / d for n < 2^31 as a product with m = floor(2^32 (2^s - d) / d) + 1, s =
-// ceil(log2 d) (the round-up method of Granlund and Montgomery).
-__device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t mul, uint32_t shift) {
-  return (__umulhi(n, mul) + n) >> shift;
-}
 
 // E consecutive values of an activation row as floats, and back.
 template <typename T, int E>
@@ -199,9 +192,9 @@ rows_kernel(const RowsArgs a) {
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const uint32_t task = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const uint32_t t = divide(task, a.task_mul, a.task_shift);
+  const uint32_t t = quotient(task, a.tasks);
   if (t >= (uint32_t)a.tokens) return;
-  const int j = (int)(task - t * a.tasks);
+  const int j = (int)(task - t * a.tasks.d);
   const int d0 = lane * E;
 
   // the task's rows
@@ -369,11 +362,8 @@ rq_status launch_rows_rpw(RowsArgs a, cudaStream_t st) {
   const int rpw = (int64_t)a.tokens * rows <= 8 * (int64_t)device_sm_count() ? 1 : 4;
   a.tq = (a.hq + rpw - 1) / rpw;
   a.tk = (a.hk + rpw - 1) / rpw;
-  a.tasks = a.tq + a.tk + (a.hv + rpw - 1) / rpw;
-  a.task_shift = 0;
-  while ((1ull << a.task_shift) < (unsigned long long)a.tasks) ++a.task_shift;
-  a.task_mul = (uint32_t)((((1ull << a.task_shift) - (unsigned)a.tasks) << 32) / (unsigned)a.tasks) + 1u;
-  const int64_t warps = (int64_t)a.tokens * a.tasks;
+  a.tasks = divisor((uint32_t)(a.tq + a.tk + (a.hv + rpw - 1) / rpw));
+  const int64_t warps = (int64_t)a.tokens * a.tasks.d;
   const unsigned grid = (unsigned)((warps + kRowThreads / 32 - 1) / (kRowThreads / 32));
   return rpw == 1 ? launch_kernel(rows_kernel<T, E, 1>, grid, kRowThreads, 0, st, a)
                   : launch_kernel(rows_kernel<T, E, 4>, grid, kRowThreads, 0, st, a);
@@ -424,7 +414,7 @@ constexpr int kReadRuns = 2;
 template <typename T>
 __global__ void __launch_bounds__(256)
 read_kernel(const rq_kv_cache c, const int64_t* __restrict__ slot, int tokens, int lg_page,
-            int lg_chunks, T* __restrict__ k_out, T* __restrict__ v_out) {
+            int lg_chunks, const Divisor heads, T* __restrict__ k_out, T* __restrict__ v_out) {
   pdl_wait();
   pdl_trigger();
   const int64_t id0 = (int64_t)blockIdx.x * (256 * kReadRuns) + threadIdx.x;
@@ -435,8 +425,8 @@ read_kernel(const rq_kv_cache c, const int64_t* __restrict__ slot, int tokens, i
   for (int u = 0; u < kReadRuns; ++u) {
     const int64_t id = id0 + 256 * u;
     const uint32_t at = (uint32_t)(id >> lg_chunks);  // token * kv_heads + head, below 2^31
-    const uint32_t t = at / (uint32_t)c.kv_heads;
-    const int h = (int)(at - t * (uint32_t)c.kv_heads);
+    const uint32_t t = quotient(at, heads);
+    const int h = (int)(at - t * heads.d);
     live[u] = t < (uint32_t)tokens;
     int64_t s = live[u] ? slot[t] : -1;
     if (s >= c.pages << lg_page) {
@@ -489,9 +479,10 @@ rq_status launch_read_t(const rq_kv_cache& c, const int64_t* slot, void* k_out, 
                         int tokens, cudaStream_t st) {
   const int lg_chunks = log2_of(c.head_dim / 8);
   const int64_t threads = ((int64_t)tokens * c.kv_heads) << lg_chunks;
-  return launch_kernel(read_kernel<T>, dim3((unsigned)((threads + 256 * kReadRuns - 1) / (256 * kReadRuns))), dim3(256), 0, st,
-                       c, slot, tokens, log2_of(c.page_size), lg_chunks, static_cast<T*>(k_out),
-                       static_cast<T*>(v_out));
+  const unsigned grid = (unsigned)((threads + 256 * kReadRuns - 1) / (256 * kReadRuns));
+  return launch_kernel(read_kernel<T>, dim3(grid), dim3(256), 0, st, c, slot, tokens,
+                       log2_of(c.page_size), lg_chunks, divisor((uint32_t)c.kv_heads),
+                       static_cast<T*>(k_out), static_cast<T*>(v_out));
 }
 
 }  // namespace

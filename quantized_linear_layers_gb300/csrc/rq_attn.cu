@@ -147,7 +147,7 @@ attn_kernel(const AttnArgs a) {
   Segment seg;
   if (!cutter.begin(seg)) return;
 
-  // -------- the warp's loads, S units ahead of its products
+  // -------- the warp's loads, S - 1 units ahead of its products
   Segment ld = seg;
   int unit = ld.first + warp;          // next unit to load
   int in_window = 0, pages_of = 0;     // lane i: page of the window's unit i, W units apart
@@ -215,7 +215,7 @@ attn_kernel(const AttnArgs a) {
       // the first loads of keys and values go out while q is on its way (or
       // before it, where its raw values would not stay in registers)
       if (nseg == 0 && D == 256)
-        for (int i = 0; i < S; ++i) load_one();
+        for (int i = 0; i < S - 1; ++i) load_one();
       float x[D / 16][4];
       float top = 0.0f;
       if (a.dtype == RQ_F32) {
@@ -238,7 +238,7 @@ attn_kernel(const AttnArgs a) {
         }
       }
       if (nseg == 0 && D < 256)
-        for (int i = 0; i < S; ++i) load_one();
+        for (int i = 0; i < S - 1; ++i) load_one();
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         if (a.dtype != RQ_F32) {
@@ -292,7 +292,7 @@ attn_kernel(const AttnArgs a) {
     float vref = 0x1p-112f;  // power of two at or above every vs so far
 
     for (int u = seg.first + warp; u < seg.end; u += W) {
-      copy_wait<S - 1>();
+      copy_wait<S - 2>();
       __syncwarp();
       const int first = u * kKeys;  // place of the first key
       const bool all = first + kKeys <= len;
@@ -320,6 +320,9 @@ attn_kernel(const AttnArgs a) {
           mma(s[k & 1], qa[i + (k >> 1)], b0, b1);
         }
       }
+      // the unit S - 1 ahead goes into the stage that the last one left, while
+      // the products are under way
+      load_one();
       // ---- scales: this thread's keys are 2 t4, 2 t4 + 1 and 8 more
       const float* sc = &tail.scale[warp][st][0][0];
       const float2 ka = *reinterpret_cast<const float2*>(sc + 2 * t4);
@@ -363,22 +366,24 @@ attn_kernel(const AttnArgs a) {
       const float xm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
       if (__any_sync(0xFFFFFFFFu,
                      xm > m || fmaxf(fmaxf(vv[0], vv[1]), fmaxf(vv[2], vv[3])) > vref)) {
-        float vt = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) vt = fmaxf(vt, vv[k] <= 1e37f ? vv[k] : 0.0f);  // no NaN, Inf
         float mn = fmaxf(xm, __shfl_xor_sync(0xFFFFFFFFu, xm, 1));
         mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 2));
         mn = fmaxf(mn, m);
-        vt = fmaxf(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, 1));
-        vt = fmaxf(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, 2));
+        uint32_t vt = 0u;  // bits of what is not negative are in its order
 #pragma unroll
-        for (int i = 4; i < 32; i <<= 1) vt = fmaxf(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, i));
-        float vnew = vref;
-        if (vt > vref)  // four times the next power of two: rarely passed again
-          vnew = __uint_as_float((__float_as_uint(vt) & 0x7F800000u) + (2u << 23));
+        for (int k = 0; k < 4; ++k)
+          if (vv[k] >= 0.0f && vv[k] <= 1e37f) vt = max(vt, __float_as_uint(vv[k]));  // no NaN, Inf
+        vt = __reduce_max_sync(0xFFFFFFFFu, vt);
         const float al = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
-        const float f = al * (vref / vnew);
-        vref = vnew;
+        float f = al;
+        const uint32_t vbits = __float_as_uint(vref);
+        if (vt > vbits) {  // four times the next power of two: rarely passed again
+          const uint32_t vnew = (vt & 0x7F800000u) + (2u << 23);
+          vref = __uint_as_float(vnew);
+          // times old / new, a power of two (0 where that is below f32's)
+          const int e = (int)(vbits >> 23) - (int)(vnew >> 23) + 127;
+          f *= e > 0 ? __uint_as_float((uint32_t)e << 23) : 0.0f;
+        }
         l *= al;
         m = mn;
 #pragma unroll
@@ -415,7 +420,6 @@ attn_kernel(const AttnArgs a) {
       }
       __syncwarp();
       st = st == S - 1 ? 0 : st + 1;
-      load_one();
     }
 
     // ---- join the warps: every lane of a row's four holds part of its sum

@@ -22,32 +22,36 @@ namespace {
 __device__ unsigned int g_attn_error = 0;
 
 constexpr int kKeys = 16;            // keys of a unit: one warp's step
-constexpr int kCtas = 2;             // per SM
 constexpr int kRows = 8;             // query rows of a segment
 constexpr int kJoin = 8;             // partials joined at once
 
 // From this many query rows per kv head on, rq_attn_rows.cu's kernel runs.
 constexpr int kManyRows = 64;
 
-template <int D>
+template <int D, bool WIDE>
 struct Geometry {
   static constexpr int kPanel = D < 128 ? D : 128;  // bytes of a row in one swizzled panel
   static constexpr int kPanels = D / kPanel;
   static constexpr int kBytes = kKeys * D;          // codes of K (or V) in a unit
-  // Two CTAs per SM, so that one streams while the other begins or joins a
-  // segment, and as many warps as the registers hold: the output rows alone
-  // are D / 2 registers a thread, the query rows D / 4.
-  static constexpr int kWarps = D == 64 ? 8 : D == 128 ? 6 : 4;
+  // As many warps on an SM as the registers hold: the output rows alone are
+  // D / 2 registers a thread, the query rows D / 4.  WIDE: in one CTA, for
+  // launches of no more segments than SMs, where a CTA has one part of one
+  // segment (one token over 500 cached ones 8.2 us
+  // against 10.4 in two, over 131000
+  // 32.1 against 36.1).  Otherwise in two, so that one streams while the other begins
+  // or joins a segment (64 sequences of up to 8192 tokens 153 us, 182 in one).
+  static constexpr int kCtas = WIDE ? 1 : 2;
+  static constexpr int kWarps = (D == 64 ? 16 : D == 128 ? 12 : 8) / kCtas;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStages = D == 256 ? 2 : 3;  // units in flight per warp
   static constexpr int kRing = kWarps * kStages * 2 * kBytes;
 };
 
 // Shared memory after the ring.
-template <int D>
+template <int D, bool WIDE>
 struct Tail {
-  static constexpr int kWarps = Geometry<D>::kWarps;
-  static constexpr int kStages = Geometry<D>::kStages;
+  static constexpr int kWarps = Geometry<D, WIDE>::kWarps;
+  static constexpr int kStages = Geometry<D, WIDE>::kStages;
   float scale[kWarps][kStages][2][kKeys];  // ks, vs of the units in flight
   float o[kWarps][kRows][D + 4];
   float m[kWarps][kRows], l[kWarps][kRows];
@@ -126,11 +130,11 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, const uint8_t* src) {
 // joined when the segment ends.  A warp's 16-row tile holds the
 // high f16 parts of 8 query rows and below them their low parts: an f32 row
 // costs no product more than an f16 one would.
-template <int D, bool I8>
-__global__ void __launch_bounds__(Geometry<D>::kThreads, kCtas)
+template <int D, bool I8, bool WIDE>
+__global__ void __launch_bounds__(Geometry<D, WIDE>::kThreads, Geometry<D, WIDE>::kCtas)
 attn_kernel(const AttnArgs a) {
-  using G = Geometry<D>;
-  using TailT = Tail<D>;
+  using G = Geometry<D, WIDE>;
+  using TailT = Tail<D, WIDE>;
   constexpr int W = G::kWarps, S = G::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   TailT& tail = *reinterpret_cast<TailT*>(smem + G::kRing);
@@ -595,19 +599,27 @@ int lg(int v) {
   return l;
 }
 
-template <int D, bool I8>
-rq_status launch_d(const AttnArgs& a, unsigned grid, cudaStream_t st) {
-  constexpr int bytes = Geometry<D>::kRing + (int)sizeof(Tail<D>);
-  static_assert(kCtas * (bytes + 1024) <= 233472, "shared memory of an SM");
+template <int D, bool I8, bool WIDE>
+rq_status launch_kind(const AttnArgs& a, unsigned grid, cudaStream_t st) {
+  using G = Geometry<D, WIDE>;
+  constexpr int bytes = G::kRing + (int)sizeof(Tail<D, WIDE>);
+  static_assert(bytes <= 232448 && G::kCtas * (bytes + 1024) <= 233472, "shared memory of an SM");
   static bool ready = false;
   if (!ready) {
-    if (cudaFuncSetAttribute(attn_kernel<D, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(attn_kernel<D, I8, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              bytes) != cudaSuccess)
       return RQ_ERR_CUDA;
     ready = true;
   }
-  return launch_kernel(attn_kernel<D, I8>, dim3(grid), dim3(Geometry<D>::kThreads), (size_t)bytes,
-                       st, a);
+  return launch_kernel(attn_kernel<D, I8, WIDE>, dim3(grid), dim3(G::kThreads), (size_t)bytes, st,
+                       a);
+}
+
+template <int D>
+rq_status launch_d(const AttnArgs& a, bool i8, bool wide, unsigned grid, cudaStream_t st) {
+  if (wide)
+    return i8 ? launch_kind<D, true, true>(a, grid, st) : launch_kind<D, false, true>(a, grid, st);
+  return i8 ? launch_kind<D, true, false>(a, grid, st) : launch_kind<D, false, false>(a, grid, st);
 }
 
 }  // namespace
@@ -652,7 +664,8 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
 
   const int64_t items = (int64_t)call.batch * a.row_tiles;
   const int64_t segments = items * c.kv_heads;
-  int64_t grid = (int64_t)kCtas * device_sm_count();
+  const bool wide = segments <= device_sm_count();
+  int64_t grid = (int64_t)(wide ? 1 : 2) * device_sm_count();
   a.direct = items > kMaxItems;
   if (a.direct) {
     grid = segments;
@@ -667,11 +680,9 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
   const unsigned g = (unsigned)grid;
   const bool i8 = c.format == RQ_KV_I8;
   switch (c.head_dim) {
-    case 64: return i8 ? launch_d<64, true>(a, g, st) : launch_d<64, false>(a, g, st);
-    case 128:
-      return i8 ? launch_d<128, true>(a, g, st) : launch_d<128, false>(a, g, st);
-    default:
-      return i8 ? launch_d<256, true>(a, g, st) : launch_d<256, false>(a, g, st);
+    case 64: return launch_d<64>(a, i8, wide, g, st);
+    case 128: return launch_d<128>(a, i8, wide, g, st);
+    default: return launch_d<256>(a, i8, wide, g, st);
   }
 }
 

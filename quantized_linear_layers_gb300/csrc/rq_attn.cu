@@ -25,8 +25,16 @@ constexpr int kKeys = 16;            // keys of a unit: one warp's step
 constexpr int kRows = 8;             // query rows of a segment
 constexpr int kJoin = 8;             // partials joined at once
 
-// From this many query rows per kv head on, rq_attn_rows.cu's kernel runs.
-constexpr int kManyRows = 64;
+// rq_attn_rows.cu's kernel runs from kManyRows query rows per kv head on, for
+// launches of at least kManyWork row-key pairs (with the places that the page
+// table has room for).  It costs about 20 us before its first product and
+// then hardly more for 250 rows than for 8, this file's kernel 8 us and then a
+// pass over the cache for every 8 rows.  Measured, this / that: 8 sequences of
+// up to 8000 tokens, f32, 28 rows 47 / 55 us, 42 rows 61 / 55, 112 rows 124 /
+// 58; one of 8000, 56 rows 19 / 29, 112 rows 31 / 33, 224 rows 48 / 40; one of
+// 500, 224 rows 10 / 27.
+constexpr int kManyRows = 40;
+constexpr double kManyWork = 3e6;
 
 template <int D, bool WIDE>
 struct Geometry {
@@ -36,10 +44,10 @@ struct Geometry {
   // As many warps on an SM as the registers hold: the output rows alone are
   // D / 2 registers a thread, the query rows D / 4.  WIDE: in one CTA, for
   // launches of no more segments than SMs, where a CTA has one part of one
-  // segment (one token over 500 cached ones 8.2 us
-  // against 10.4 in two, over 131000
-  // 32.1 against 36.1).  Otherwise in two, so that one streams while the other begins
-  // or joins a segment (64 sequences of up to 8192 tokens 153 us, 182 in one).
+  // segment (one token over 500 cached ones 8.2 us against 10.4 in two, over
+  // 131000 32.1 against 36.1).  Otherwise in two, so that one streams while
+  // the other begins or joins a segment (64 sequences of up to 8192 tokens
+  // 153 us, 182 in one).
   static constexpr int kCtas = WIDE ? 1 : 2;
   static constexpr int kWarps = (D == 64 ? 16 : D == 128 ? 12 : 8) / kCtas;
   static constexpr int kThreads = 32 * kWarps;
@@ -291,7 +299,13 @@ attn_kernel(const AttnArgs a) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
     const int n_all = cutter.length(b);
-    const int len = n_all < 0 ? 0 : n_all < kv ? n_all : kv;  // places every row sees
+    const int len = n_all < 0 ? 0 : n_all < kv ? n_all : kv;  // places cached before
+    // places that every row sees: without a tree also the new ones up to the
+    // first row's own
+    const int sure =
+        a.tree == nullptr
+            ? min(kv, len + (int)quotient((uint32_t)(rt * kRows), a.by_group) + 1)
+            : len;
     float m = -INFINITY, l = 0.0f;
     float vref = 0x1p-112f;  // power of two at or above every vs so far
 
@@ -299,7 +313,7 @@ attn_kernel(const AttnArgs a) {
       copy_wait<S - 2>();
       __syncwarp();
       const int first = u * kKeys;  // place of the first key
-      const bool all = first + kKeys <= len;
+      const bool all = first + kKeys <= sure;
       const uint32_t kd = ring + st * (2 * G::kBytes), vd = kd + G::kBytes;
       // ldmatrix's matrix lane / 8: keys 0-7 or 8-15, 16 dims i or i + 1 (i
       // even, so that it only flips bits of the swizzled place)
@@ -659,7 +673,8 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
   a.scale_log2 = (float)((double)call.scale * 1.4426950408889634);
   a.dtype = call.dtype;
 
-  if (a.rows >= kManyRows && c.head_dim <= 128)
+  const double work = (double)call.max_pages * c.page_size * c.kv_heads * call.batch * a.rows;
+  if (a.rows >= kManyRows && work >= kManyWork && c.head_dim <= 128)
     return launch_attention_rows(a, c.head_dim, c.format == RQ_KV_I8, scratch, st);
 
   const int64_t items = (int64_t)call.batch * a.row_tiles;

@@ -11,6 +11,7 @@ namespace rq {
 
 constexpr int kMaxItems = 1024;  // (sequence, row tile) pairs that a launch cuts by length
 
+struct SharedSegment;
 struct AttnArgs {
   const void* q;
   void* out;
@@ -28,7 +29,7 @@ struct AttnArgs {
   int direct;  // one CTA per segment, no splitting
   float* part;
   unsigned int* counter;
-  int4* shares;         // per segment, for a join after the launch (null: none)
+  SharedSegment* shares;  // per CTA: the segment it begins for several (null: no join)
   unsigned int* error;  // bit 1: an index outside its array
 };
 
@@ -132,14 +133,23 @@ __device__ __forceinline__ int page_of(const AttnArgs& a, int b, int64_t place) 
 struct Segment {
   int item, head, first, end;
   int kv;        // places its rows may see, 0: an unused sequence
-  int64_t left;  // units (kRun) or segments (else) of the CTA's work after it
+  int64_t left;  // cost (kRun) or segments (else) of the CTA's work after it
+};
+
+// A segment that several CTAs share, as its first one notes it.
+struct SharedSegment {
+  int parts;          // how many, 0: found from the rest
+  int segment;        // item * kv_heads + head, -1: none
+  int second;         // the first one's part lies in its second set of rows
+  int ctas;
+  int64_t last, cost;  // the last sharer is the CTA ((last + 1) ctas - 1) / cost
 };
 
 struct CutShared {
   int warp_sum[32], warp_most[32];
-  int cut, split;
-  int64_t units;                  // of all segments
-  int item_start[kMaxItems + 1];  // units before each item, for one kv head
+  int cut, split, ctas;
+  int64_t cost;                   // of all segments
+  int item_start[kMaxItems + 1];  // cost of the items before each, for one kv head
   int length[kMaxItems];          // the sequences' lengths
 };
 
@@ -149,15 +159,17 @@ struct CutShared {
 // knows:
 //   kParts: every segment in up to `split` equal parts, one CTA each;
 //   kWhole: a run of whole segments per CTA;
-//   kRun: an equal run of units per CTA, wherever segments begin or end.
-// Joining a segment over CTAs costs as much as about ROUNDS rounds, and so
-// does beginning another one: no part is made smaller than that, segments
-// that short stay whole, and a run may begin and end inside segments only
-// where that evens out more.
-template <int ROWS, int KEYS, int STEP, int ROUNDS>
+//   kRun: an equal run of cost per CTA, wherever segments begin or end; a
+//     unit is its CTA's in whose run it begins.
+// A unit costs WHOLE, or PART in a row tile of at most ROWS / 2 rows.  Joining
+// a segment over CTAs costs as much as about ROUNDS rounds, and so does
+// beginning another one: no part is made smaller than that, segments that
+// short stay whole, and a run may begin and end inside segments only where
+// that evens out more.
+template <int ROWS, int KEYS, int STEP, int ROUNDS, int WHOLE = 1, int PART = 1>
 struct Cutter {
   enum { kParts, kWhole, kRun };
-  static constexpr int kLeast = ROUNDS * STEP;
+  static constexpr int kLeast = ROUNDS * STEP * WHOLE;  // cost of the smallest part
   const AttnArgs& a;
   CutShared& sh;
 
@@ -191,6 +203,16 @@ struct Cutter {
   __device__ __forceinline__ int units_of(int kv) const {
     return kv < 1 ? 1 : (kv + KEYS - 1) / KEYS;
   }
+  __device__ __forceinline__ int cost_of(int rt) const {  // of a unit
+    return WHOLE == PART || a.rows - rt * ROWS > ROWS / 2 ? WHOLE : PART;
+  }
+  // x / c rounded up, c a unit's cost
+  __device__ __forceinline__ static uint32_t units_in(uint32_t x, uint32_t c) {
+    return WHOLE == PART || c == WHOLE ? (x + WHOLE - 1u) / WHOLE : (x + PART - 1u) / PART;
+  }
+  __device__ __forceinline__ int tile(const Segment& g) const {
+    return g.item - sequence(g.item) * a.row_tiles;
+  }
 
   __device__ __forceinline__ int length(int b) const { return a.direct ? a.length[b] : sh.length[b]; }
 
@@ -216,7 +238,7 @@ struct Cutter {
         const int b = sequence(i), rt = i - b * a.row_tiles;
         const int len = a.length[b];
         if (rt == 0) sh.length[b] = len;
-        n = units_of(places(len, rt));
+        n = units_of(places(len, rt)) * cost_of(rt);
       }
       int scan = n, top = n;
 #pragma unroll
@@ -242,34 +264,41 @@ struct Cutter {
       if (i < items) sh.item_start[i] = before + scan - n;
     }
     if (tid == 0) {
-      const int64_t units = (int64_t)carry * a.kv_heads;
+      const int64_t cost = (int64_t)carry * a.kv_heads;
       const int64_t segments = (int64_t)items * a.kv_heads;
       int cut = kWhole, split = 1;
       if (segments <= grid) {
         split = (int)min((uint32_t)grid / (uint32_t)segments, (uint32_t)(most + kLeast - 1) / kLeast);
         // the longest part's rounds against an even share's
         const int64_t longest = ((int64_t)most + split - 1) * grid;
-        cut = longest <= (units + (int64_t)ROUNDS * STEP * grid) * split ? kParts : kRun;
+        cut = longest <= (cost + (int64_t)kLeast * grid) * split ? kParts : kRun;
       } else if (most > kLeast) {
         cut = kRun;
       }
       sh.item_start[items] = carry;
-      sh.units = units;
+      sh.cost = cost;
       sh.cut = cut;
       sh.split = split;
+      // a unit begins in every run: a CTA without one would be counted among
+      // a segment's and leave no part
+      sh.ctas = (int)min((int64_t)grid, max((int64_t)1, cost / WHOLE));
     }
     __syncthreads();
   }
 
-  __device__ __forceinline__ void open(Segment& g) const {  // item, head, first, left are set
-    const int b = sequence(g.item);
-    g.kv = places(length(b), g.item - b * a.row_tiles);
+  // Sets end and left; item, head, first are set, and left: under kRun the
+  // cost from the segment's beginning to the run's end.
+  __device__ __forceinline__ void open(Segment& g) const {
+    const int b = sequence(g.item), rt = g.item - b * a.row_tiles;
+    g.kv = places(length(b), rt);
     const int n = units_of(g.kv);
+    g.end = n;
     if (sh.cut == kRun) {
-      g.end = g.left < n - g.first ? g.first + (int)g.left : n;
-      g.left -= g.end - g.first;
+      const int c = cost_of(rt);
+      const int64_t all = (int64_t)n * c;
+      if (g.left < all) g.end = (int)units_in((uint32_t)g.left, (uint32_t)c);
+      g.left -= all;
     } else {
-      g.end = n;
       --g.left;
     }
   }
@@ -285,8 +314,10 @@ struct Cutter {
 
   // kParts: units [first, end) of a segment of n that are part `part` of it,
   // of *parts.
-  __device__ __forceinline__ bool part_of(int n, int part, int* parts, int* first, int* end) const {
-    const uint32_t want = min((uint32_t)sh.split, (uint32_t)(n + kLeast - 1) / kLeast);
+  __device__ __forceinline__ bool part_of(int n, int cost, int part, int* parts, int* first,
+                                          int* end) const {
+    const uint32_t want =
+        min((uint32_t)sh.split, ((uint32_t)n * (uint32_t)cost + kLeast - 1u) / kLeast);
     const uint32_t each = ((uint32_t)n + want - 1u) / want;
     *parts = (int)(((uint32_t)n + each - 1u) / each);
     *first = part * (int)each;
@@ -299,23 +330,29 @@ struct Cutter {
     const int grid = (int)gridDim.x, items = a.batch * a.row_tiles;
     g.first = 0;
     if (sh.cut == kRun) {
-      const int64_t u0 = sh.units * blockIdx.x / grid, u1 = sh.units * (blockIdx.x + 1) / grid;
-      if (u0 >= u1) return false;
+      if ((int)blockIdx.x >= sh.ctas) return false;
+      const int64_t x0 = sh.cost * blockIdx.x / sh.ctas, x1 = sh.cost * (blockIdx.x + 1) / sh.ctas;
       int lo = 0, hi = items - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)sh.item_start[mid] * a.kv_heads <= u0)
+        if ((int64_t)sh.item_start[mid] * a.kv_heads <= x0)
           lo = mid;
         else
           hi = mid - 1;
       }
-      const int n = sh.item_start[lo + 1] - sh.item_start[lo];
-      const int rest = (int)(u0 - (int64_t)sh.item_start[lo] * a.kv_heads);
+      const uint32_t all = (uint32_t)(sh.item_start[lo + 1] - sh.item_start[lo]);
+      const int64_t from = x0 - (int64_t)sh.item_start[lo] * a.kv_heads;
       g.item = lo;
-      g.head = rest / n;
-      g.first = rest - g.head * n;
-      g.left = u1 - u0;
+      g.head = (int)(from / all);
+      const uint32_t rest = (uint32_t)(from - (int64_t)g.head * all);
+      g.left = x1 - x0 + rest;
+      g.first = (int)units_in(rest, (uint32_t)cost_of(tile(g)));
+      const int skip = g.first;
       open(g);
+      if (skip >= g.end) {  // its last unit began in the run before
+        if (g.left <= 0) return false;
+        next(g);
+      }
       return true;
     }
     const int segments = items * a.kv_heads;
@@ -335,36 +372,76 @@ struct Cutter {
     open(g);
     if (sh.cut == kParts) {
       int parts;
-      return part_of(g.end, (int)blockIdx.x - s0 * sh.split, &parts, &g.first, &g.end);
+      return part_of(g.end, cost_of(tile(g)), (int)blockIdx.x - s0 * sh.split, &parts, &g.first,
+                     &g.end);
     }
     return true;
   }
 
-  // Which CTAs share the segment: `parts` from CTA cta0 on, of which this is
-  // number `part`; second: the first one's part lies in that CTA's second set
-  // of partial rows, because its work began in an earlier segment.
+  // Whether the segment is all this CTA's, and which of the CTA's two sets of
+  // partial rows its part goes to: the second where its work began earlier.
+  __device__ __forceinline__ bool whole(const Segment& g) const {
+    return g.first == 0 && g.end == units_of(g.kv);
+  }
+  __device__ __forceinline__ bool second_set(const Segment& g, bool first_of_cta) const {
+    return sh.cut == kRun && g.first == 0 && !first_of_cta;
+  }
+
+  // Which CTAs share a segment that is not whole: `parts` from CTA cta0 on,
+  // of which this is number `part`; second: where the first one's part lies.
   struct Sharers {
     int64_t cta0;
     int parts, part;
     bool second;
   };
+  __device__ __forceinline__ int64_t owner(int64_t x) const {  // whose run x lies in
+    return ((x + 1) * sh.ctas - 1) / sh.cost;
+  }
   __device__ __forceinline__ Sharers sharers(const Segment& g) const {
     Sharers r = {(int64_t)blockIdx.x, 1, 0, false};
+    if (whole(g)) return r;
     if (sh.cut == kRun) {
-      const int grid = (int)gridDim.x;
-      const int n = sh.item_start[g.item + 1] - sh.item_start[g.item];
-      const int64_t s0 = (int64_t)sh.item_start[g.item] * a.kv_heads + (int64_t)g.head * n;
-      r.cta0 = ((s0 + 1) * grid - 1) / sh.units;
-      r.parts = (int)(((s0 + n) * grid - 1) / sh.units - r.cta0) + 1;
+      const int all = sh.item_start[g.item + 1] - sh.item_start[g.item];
+      const int64_t s0 = (int64_t)sh.item_start[g.item] * a.kv_heads + (int64_t)g.head * all;
+      r.cta0 = owner(s0);
+      r.parts = (int)(owner(s0 + all - cost_of(tile(g))) - r.cta0) + 1;
       r.part = (int)(blockIdx.x - r.cta0);
-      r.second = sh.units * r.cta0 / grid < s0;
+      // the first one's run began in an earlier segment, and had a unit there
+      const int64_t x0 = sh.cost * r.cta0 / sh.ctas;
+      r.second = x0 < s0 && begins_before(x0, s0, g);
     } else if (sh.cut == kParts) {
       r.part = (int)(blockIdx.x % (uint32_t)sh.split);
       r.cta0 = (int64_t)blockIdx.x - r.part;
       int first, end;
-      part_of(units_of(g.kv), r.part, &r.parts, &first, &end);
+      part_of(units_of(g.kv), cost_of(tile(g)), r.part, &r.parts, &first, &end);
     }
     return r;
+  }
+
+  // What a join after the launch has to know of the segment that this CTA
+  // begins and others finish.  (Left to it: the division that finds the last
+  // of them, which would cost the kernel's roles registers.)
+  __device__ __forceinline__ SharedSegment note(const Segment& g, bool first_of_cta) const {
+    SharedSegment r = {0, g.item * a.kv_heads + g.head, second_set(g, first_of_cta) ? 1 : 0,
+                       sh.ctas, 0, sh.cost};
+    if (sh.cut == kRun) {
+      const int all = sh.item_start[g.item + 1] - sh.item_start[g.item];
+      r.last = (int64_t)sh.item_start[g.item] * a.kv_heads + (int64_t)(g.head + 1) * all -
+               cost_of(tile(g));
+    } else if (sh.cut == kParts) {
+      int first, end;
+      part_of(units_of(g.kv), cost_of(tile(g)), 0, &r.parts, &first, &end);
+    }
+    return r;
+  }
+
+ private:
+  // Whether a unit begins in [x, s0), s0 being where segment g begins: the
+  // last unit before s0 does unless it began before x.
+  __device__ __forceinline__ bool begins_before(int64_t x, int64_t s0, const Segment& g) const {
+    const int item = g.head > 0 ? g.item : g.item - 1;
+    const int rt = item - sequence(item) * a.row_tiles;
+    return s0 - cost_of(rt) >= x;
   }
 };
 

@@ -7,8 +7,9 @@
 //   warps 0-3, 4-7   softmax of tile 0 and 1: a thread owns a row
 //   warps 8-15       codes of K and V to f16 in shared memory, two units deep
 //   warp 16          allocates TMEM; one thread issues the products
-//   warp 17          the scales
-//   warp 18          asks codes into L2, three units ahead (19 idle)
+//   warp 17          the scales; asks codes into L2, three units ahead; notes
+//                    for the join which segment goes on in other CTAs
+//   warps 18, 19     idle
 // S = Q K^T (A = Q from shared memory) lands in one of two TMEM buffers per
 // row tile; its softmax writes P over it, as f16 high and low parts for f32
 // rows (64 + 64 keys in S's 64 columns), and P V takes A = P from TMEM and
@@ -57,7 +58,7 @@ struct Wide {
 
 struct RowsTail {
   float ks[kScales][kKeys], vs[kScales][kKeys];  // vs relative to vref, times kUp
-  float vref[kScales];
+  float vref[kScales];  // negative: not all of vs are finite
   uint64_t q_full[2], k_full[2], k_free[2], v_full[2], v_free[2], sc_full[kScales];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2], drained;
   uint32_t tmem;
@@ -138,29 +139,60 @@ __device__ __forceinline__ void commit(uint32_t bar) {
       : "memory");
 }
 
+// The wait is part of the load: until it, the registers named as results do
+// not hold them, and nothing may be made of them, a spill to the stack least.
+__device__ __forceinline__ void tmem_ld64(uint32_t addr, float* v) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tadd.u32 a, %64, 32;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [a];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+        "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+        "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]),
+        "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]),
+        "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31]), "=r"(u[32]), "=r"(u[33]), "=r"(u[34]),
+        "=r"(u[35]), "=r"(u[36]), "=r"(u[37]), "=r"(u[38]), "=r"(u[39]), "=r"(u[40]), "=r"(u[41]),
+        "=r"(u[42]), "=r"(u[43]), "=r"(u[44]), "=r"(u[45]), "=r"(u[46]), "=r"(u[47]), "=r"(u[48]),
+        "=r"(u[49]), "=r"(u[50]), "=r"(u[51]), "=r"(u[52]), "=r"(u[53]), "=r"(u[54]), "=r"(u[55]),
+        "=r"(u[56]), "=r"(u[57]), "=r"(u[58]), "=r"(u[59]), "=r"(u[60]), "=r"(u[61]), "=r"(u[62]),
+        "=r"(u[63])
+      : "r"(addr)
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* v) {
   uint32_t* u = reinterpret_cast<uint32_t*>(v);
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
       : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
         "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
-        "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]),
-        "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]),
-        "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
-      : "r"(addr));
+        "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]),
+        "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]),
+        "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(addr)
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, float* v) {
   uint32_t* u = reinterpret_cast<uint32_t*>(v);
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
       : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
         "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
         "=r"(u[14]), "=r"(u[15])
-      : "r"(addr));
+      : "r"(addr)
+      : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* u) {
@@ -173,9 +205,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* u) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld_wait() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -344,27 +373,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
   pdl_trigger();
   prefetch_l2(a.q, a.q_bytes);
   prefetch_l2(a.table, (int64_t)a.batch * a.max_pages * 4);
-  Cutter<kRows, kKeys, 1, 8> cutter(a, tail.cut);
+  Cutter<kRows, kKeys, 1, 8, 8, 5> cutter(a, tail.cut);  // a unit takes 1.9 us, or 1.2
   cutter.template choose<kThreads>();
   Segment seg;
   const bool work = cutter.begin(seg);
+  if (!work && tid == 0 && a.shares != nullptr) a.shares[blockIdx.x].segment = -1;
   bool ok = true;
 
-  if (warp < 8)
+  // Each group of warps moves its registers at the head of its own branch,
+  // never before one: what follows is compiled for the count it names.
+  if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-  else if (warp < kIssueWarp)
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
-  else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-
-  if (work && warp < 8) {
+    if (work) {
     // ------------------------------------------------------- softmax ----
     const int w = warp >> 2, quad = warp & 3;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const uint32_t s_col = tmem + w * 256 + lanes, o_col = s_col + 128;
     uint32_t units = 0;            // of this row tile so far
     uint32_t all_units = 0;        // of the CTA: the scales' ring
-    for (;;) {
+    for (bool first_seg = true;; first_seg = false) {
       const int b = cutter.sequence(seg.item), rt = seg.item - b * a.row_tiles;
       const int row0 = rt * kRows + w * kTileRows;
       const int n_units = seg.end - seg.first;
@@ -386,21 +413,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
             const int64_t off = __shfl_sync(0xFFFFFFFFu, my_off, r0 + r) + lane * E;
             load_q<E, SPLIT>(a, off, x[r]);
           }
-          float top[16];
+          // largest magnitudes, as bits: a NaN counts as above infinity.  (A
+          // row past the last one stands in for the sequence's first: what it
+          // gives is not written.)
+          uint32_t top[16];
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
-            const bool row_live = row0 + quad * 32 + r0 + r < a.rows;
-            top[r] = 0.0f;
+            top[r] = 0u;
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-              x[r][i] = row_live ? q_value<E, SPLIT>(a.dtype == RQ_F16, x[r], i) : 0.0f;
-            }
+            for (int i = 0; i < E; ++i) x[r][i] = q_value<E, SPLIT>(a.dtype == RQ_F16, x[r], i);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-              // a NaN counts as an infinity
-              const float m = fabsf(x[r][i]);
-              top[r] = fmaxf(top[r], m == m ? m : INFINITY);
-            }
+            for (int i = 0; i < E; ++i)
+              top[r] = max(top[r], __float_as_uint(x[r][i]) & 0x7FFFFFFFu);
           }
           // the rows' maxima, sixteen at once: each step halves the rows that
           // a lane holds; lane bits 4, 3, 2, 1 are the row's bits 3, 2, 1, 0
@@ -409,20 +433,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
             const bool up_half = (lane & o) != 0;
 #pragma unroll
             for (int i = 0; i < n; ++i) {
-              const float keep = up_half ? top[i + n] : top[i];
-              const float give = up_half ? top[i] : top[i + n];
-              top[i] = fmaxf(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
+              const uint32_t keep = up_half ? top[i + n] : top[i];
+              const uint32_t give = up_half ? top[i] : top[i + n];
+              top[i] = max(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
             }
           }
-          const float most = fmaxf(top[0], __shfl_xor_sync(0xFFFFFFFFu, top[0], 1));
+          const uint32_t most = max(top[0], __shfl_xor_sync(0xFFFFFFFFu, top[0], 1));
           // times a power of two: the largest entry in [2^13, 2^14); a row
           // that is not finite becomes NaN
           int e = 0;
-          if (most > 0.0f) {
-            e = 13 - (int)((__float_as_uint(most) >> 23) & 0xFFu) + 127;
+          if (most > 0u) {
+            e = 13 - (int)(most >> 23) + 127;
             e = e < -126 ? -126 : e > 100 ? 100 : e;
           }
-          const float own = most <= 3.4e38f ? __uint_as_float((uint32_t)(e + 127) << 23) : NAN;
+          const float own = most < 0x7F800000u ? __uint_as_float((uint32_t)(e + 127) << 23) : NAN;
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const float up = __shfl_sync(
@@ -466,17 +490,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         const int kv = seg.kv;
         const int n_all = cutter.length(b);
         const int len = n_all < 0 ? 0 : n_all < kv ? n_all : kv;
+        // places that all of the warp's rows see: without a tree also the new
+        // ones up to its first row's own
+        const int sure =
+            a.tree == nullptr ? min(kv, len + __shfl_sync(0xFFFFFFFFu, tok, 0) + 1) : len;
 
         for (int u = 0; u < n_units; ++u) {
           const uint32_t sc = (all_units + u) % kScales;
           const uint32_t buf = units & 1u;
-          wait(ok, tail.sc_full[sc], (all_units + u) / kScales, a.error);
+          // Scores of a unit mean that the weights of the one two before were
+          // taken, so the scales' barrier is past its last turn: a tile that
+          // sat out a segment does not mistake an older turn for this one.
           wait(ok, tail.s_full[w][buf], units >> 1, a.error);
+          wait(ok, tail.sc_full[sc], (all_units + u) / kScales, a.error);
           fence_after();
           float x[kKeys];
-          tmem_ld32(s_col + buf * kKeys, x);
-          tmem_ld32(s_col + buf * kKeys + 32, x + 32);
-          tmem_ld_wait();
+          tmem_ld64(s_col + buf * kKeys, x);
           const float4* ks = reinterpret_cast<const float4*>(tail.ks[sc]);
           float mx = -INFINITY;
 #pragma unroll
@@ -490,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
             x[4 * i + 3] = xb.y;
           }
           const int p0 = (seg.first + u) * kKeys;
-          const bool edge = p0 + kKeys > len;
+          const bool edge = p0 + kKeys > sure;
           if (edge) {
             // bit k: key k of the unit is seen
             const int before = len - p0;  // keys that every row sees
@@ -522,7 +551,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
           // when a score passes it by 2^8 (f16 has room for that), so that O
           // is seldom scaled anew.
           const float now = mx * c;  // powers of two
-          const float vnow = tail.vref[sc];
+          const float vnow = fabsf(tail.vref[sc]);
+          // a scale that is not finite must not reach rows that do not see it
+          const bool odd = tail.vref[sc] < 0.0f;
           const bool moves = now > ref + kLazy || vnow != vref;
           if (__any_sync(0xFFFFFFFFu, moves)) {
             const float to = fmaxf(ref, now);
@@ -538,7 +569,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
               for (int d = 0; d < D; d += 16) {
                 float o[16];
                 tmem_ld16(o_col + d, o);
-                tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[i] *= f;
                 tmem_st16(o_col + d, reinterpret_cast<const uint32_t*>(o));
@@ -564,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
                 p.y = ex2(p.y);
                 l2 = add2(l2, p);
                 float2 wt = mul2(p, k == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
-                if (edge) {  // a scale under a cleared bit may be anything
+                if (odd) {
                   wt.x = p.x == 0.0f ? 0.0f : wt.x;
                   wt.y = p.y == 0.0f ? 0.0f : wt.y;
                 }
@@ -581,6 +611,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
           tmem_st_wait();
           fence_before();
           __syncwarp();
+          // A barrier's parity tells a turn from the one before only, and a
+          // warp can be a unit ahead of the others: the products of the unit
+          // before the last are seen to be done while the last ones' cannot be.
+          if (u > 0 && u + 1 == n_units) wait(ok, tail.pv_done[w], units - 1u, a.error);
           if (lane == 0) mbar_arrive(smem_u32(&tail.p_full[w][buf]));
           ++units;
         }
@@ -592,14 +626,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
 
       // a.part holds per CTA two sets of kRows rows of D values, reference
       // and sum (D + 4 floats); the join kernel learns which sets are whose
-      const auto share = cutter.sharers(seg);
-      const int parts = share.parts;
-      if (tid == 0 && a.shares != nullptr)
-        a.shares[seg.item * a.kv_heads + seg.head] =
-            make_int4(parts, (int)share.cta0, share.second ? 1 : 0, 0);
+      const bool whole = cutter.whole(seg);
       if (row0 < a.rows) {
-        float* set = a.part + ((int64_t)blockIdx.x * 2 +
-                               (share.part == 0 && share.second ? 1 : 0)) *
+        float* set = a.part + ((int64_t)blockIdx.x * 2 + (cutter.second_set(seg, first_seg) ? 1 : 0)) *
                                   (int64_t)kRows * kPartRow<D>;
         const int my = w * kTileRows + quad * 32;  // the warp's first row of the segment
         const int my_row = rt * kRows + my + lane;
@@ -608,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         const int64_t my_dst = (((int64_t)b * a.new_tokens + tok) * a.q_heads +
                                 seg.head * a.group + (live ? my_row - tok * a.group : 0)) * D;
         const float back = vref * (1.0f / kUp);
-        const float r1 = parts > 1 ? back : l == 0.0f ? 0.0f : back / l;
+        const float r1 = !whole ? back : l == 0.0f ? 0.0f : back / l;
         // A thread holds a row; memory wants a warp to write one.  The rows
         // pass through the warp's part of the query tile, which the segment's
         // products are done with: as wide as a query row there, in 16-byte
@@ -623,7 +652,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
           for (int d = 0; d < kCols; d += 32) {
             float o[32];
             tmem_ld32(o_col + d0 + d, o);
-            tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] *= r1;
             uint32_t h[kWide ? 32 : 16];
@@ -662,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
                          : "memory");
             if (rt * kRows + my + r >= a.rows) continue;
             const uint4 v = make_uint4(h[0], h[1], h[2], h[3]);
-            if (parts > 1)
+            if (!whole)
               __stcg(reinterpret_cast<uint4*>(set + (my + r) * kPartRow<D> + d0) + piece, v);
             else if (kWide)
               *(reinterpret_cast<uint4*>(static_cast<float*>(a.out) + dst) + piece) = v;
@@ -673,13 +701,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         };
         if (SPLIT) {
           pass(Wide<true>(), 0);
-        } else if (parts > 1) {
+        } else if (!whole) {
           pass(Wide<true>(), 0);
           pass(Wide<true>(), D / 2);
         } else {
           pass(Wide<false>(), 0);
         }
-        if (parts > 1 && live)
+        if (!whole && live)
           __stcg(reinterpret_cast<float2*>(set + (my + lane) * kPartRow<D> + D),
                  make_float2(ref, l));
         fence_before();
@@ -689,7 +717,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       if (seg.left <= 0) break;
       cutter.next(seg);
     }
-  } else if (work && warp < kIssueWarp) {
+    }
+  } else if (warp < kIssueWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
+    if (work) {
     // --------------------------------------------------- conversion ----
     constexpr int kChunks = D / 16;                    // 16-code chunks of a row
     constexpr int N = kKeys * kChunks / kConvert;      // of K (and of V) per thread and unit
@@ -776,14 +807,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       fetch(vc, a.v);
       ++units;
     }
-  } else if (work && warp == kIssueWarp + 1) {
-    // -------------------------------------------------------- scales ----
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (work && warp == kIssueWarp + 1) {
+    // ------------------------------------------- scales, and codes into L2 --
     uint32_t units = 0;
-    const int page_mask = (1 << a.lg_page) - 1;
+    bool first_seg = true;
+    const int page_mask = (1 << a.lg_page) - 1, page_bytes = D << a.lg_page;
     for (;;) {
       float vref = 0x1p-112f;
-      PageWindow pages;
+      PageWindow pages, ahead;
       pages.open(a, seg, seg.first, lane);
+      ahead = pages;
+      int asked = seg.first + 1;
       float s[4];
       auto fetch = [&](int u) {  // of keys lane and lane + 32
 #pragma unroll
@@ -800,13 +837,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       };
       fetch(seg.first);
       for (int u = seg.first; u < seg.end; ++u, ++units) {
+        // codes of the units up to kAhead on: lanes 0-3 the boxes of K, 4-7
+        // those of V
+        for (; asked <= u + kAhead && asked < seg.end; ++asked) {
+          ahead.step(a, seg, asked, lane);
+          const int key = (lane & 3) * 16;
+          const int plane = ahead.plane(asked * 4 + (lane & 3));
+          if (lane < 8 && asked * kKeys + key < seg.kv) {
+            const uint8_t* at = (lane < 4 ? a.k : a.v) + (int64_t)plane * page_bytes +
+                                ((asked * kKeys + key) & page_mask) * D;
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "n"(16 * D)
+                         : "memory");
+          }
+        }
         // value scales relative to a power of two at or above all so far;
         // four times the next one when it moves, so that it seldom does
         float vt = fmaxf(s[1] <= 1e37f ? s[1] : 0.0f, s[3] <= 1e37f ? s[3] : 0.0f);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) vt = fmaxf(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, o));
         if (vt > vref) vref = __uint_as_float((__float_as_uint(vt) & 0x7F800000u) + (2u << 23));
-        const float inv = kUp / vref;
+        // kUp / vref, both powers of two
+        const float inv = __uint_as_float(((254u + 7u) << 23) - __float_as_uint(vref));
         // the ring's place is free once the unit two before is done with
         // (its own occupant was the one four before)
         const uint32_t sc = units % kScales;
@@ -815,7 +866,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         tail.ks[sc][lane + 32] = s[2];
         tail.vs[sc][lane] = s[1] * inv;
         tail.vs[sc][lane + 32] = s[3] * inv;
-        if (lane == 0) tail.vref[sc] = vref;
+        const bool odd = __any_sync(0xFFFFFFFFu, !(fabsf(s[1]) <= 3.4e38f && fabsf(s[3]) <= 3.4e38f));
+        if (lane == 0) tail.vref[sc] = odd ? -vref : vref;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&tail.sc_full[sc]));
         if (u + 1 < seg.end) {
@@ -825,32 +877,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       }
       if (seg.left <= 0) break;
       cutter.next(seg);
+      first_seg = false;
     }
-  } else if (work && warp == kIssueWarp + 2) {
-    // -------- codes into L2, kAhead units before they are fetched: lanes
-    // 0-3 the boxes of K, 4-7 those of V
-    uint32_t units = 0;
-    const int page_mask = (1 << a.lg_page) - 1, page_bytes = D << a.lg_page;
-    for (;;) {
-      PageWindow pages;
-      pages.open(a, seg, seg.first, lane);
-      int asked = seg.first + 1;
-      for (int u = seg.first; u < seg.end; ++u, ++units) {
-        for (; asked <= u + kAhead && asked < seg.end; ++asked) {
-          pages.step(a, seg, asked, lane);
-          const int key = (lane & 3) * 16;
-          const int plane = pages.plane(asked * 4 + (lane & 3));
-          if (lane < 8 && asked * kKeys + key < seg.kv) {
-            const uint8_t* at = (lane < 4 ? a.k : a.v) + (int64_t)plane * page_bytes +
-                                ((asked * kKeys + key) & page_mask) * D;
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "n"(16 * D)
-                         : "memory");
-          }
-        }
-        wait(ok, tail.v_free[units & 1u], (units >> 1) ^ 1u, a.error);
-      }
-      if (seg.left <= 0) break;
-      cutter.next(seg);
+    // for the join: the segment that this CTA begins and others go on with, if
+    // any -- the last one of its work
+    if (a.shares != nullptr && lane == 0) {
+      SharedSegment note = {0, -1, 0, 0, 0, 0};
+      if (!cutter.whole(seg) && seg.first == 0) note = cutter.note(seg, first_seg);
+      a.shares[blockIdx.x] = note;
     }
   } else if (work && warp == kIssueWarp) {
     // ------------------------------------------------------ products ----
@@ -901,6 +935,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
           if (w < nw) {
             const uint32_t p = mine[w]++;  // this unit's number of the row tile
             if (more) {
+              // The scores go where the weights two units back are: products
+              // into different accumulators are not ordered by themselves.
+              if (u > 0) wait(ok, tail.pv_done[w], p - 1u, a.error);
               fence_after();
               if (elect_one()) {
                 scores(w, cur + 1, p + 1);
@@ -937,11 +974,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
     bool drained = true;
     wait(drained, tail.drained, 0, a.error);
   }
+  }
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == kIssueWarp)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if ((threadIdx.x >> 5) == kIssueWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tail.tmem)
+                 : "memory");
 }
 
 // Joins the partial rows of segments that several CTAs share.  A warp takes a
@@ -953,18 +992,21 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const AttnArgs a) {
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   constexpr int kBlocks = kRows / 8;  // CTAs per segment, eight rows each
-  const int s = (int)(blockIdx.x / kBlocks);
-  const int4 share = a.shares[s];
-  const int parts = share.x;
-  if (parts <= 1) return;
-  const int item = s / a.kv_heads, head = s - item * a.kv_heads;
-  const int b = item / a.row_tiles, rt = item - b * a.row_tiles;
+  const int cta0 = (int)(blockIdx.x / kBlocks);
+  const SharedSegment share = a.shares[cta0];
+  if (share.segment < 0) return;
+  const int parts = share.parts > 0
+                        ? share.parts
+                        : (int)(((share.last + 1) * share.ctas - 1) / share.cost) - cta0 + 1;
+  const int item = (int)quotient((uint32_t)share.segment, a.by_heads);
+  const int head = share.segment - item * a.kv_heads;
+  const int b = (int)quotient((uint32_t)item, a.by_tiles), rt = item - b * a.row_tiles;
   const int r = (int)(blockIdx.x % kBlocks) * 8 + (threadIdx.x >> 5);
   const int row = rt * kRows + r;
   if (row >= a.rows) return;
   auto row_at = [&](int p) -> const float* {
     return a.part +
-           (((int64_t)(share.y + p) * 2 + (p == 0 ? share.z : 0)) * kRows + r) * kPartRow<D>;
+           (((int64_t)(cta0 + p) * 2 + (p == 0 ? share.second : 0)) * kRows + r) * kPartRow<D>;
   };
   float top = -INFINITY;
   for (int p = lane; p < parts; p += 32) top = fmaxf(top, __ldcg(row_at(p) + D));
@@ -1002,7 +1044,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const AttnArgs a) {
   const float r1 = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
   for (int i = 0; i < E; ++i) v[i] *= r1;
-  const int tok = row / a.group;
+  const int tok = (int)quotient((uint32_t)row, a.by_group);
   const int64_t dst = (((int64_t)b * a.new_tokens + tok) * a.q_heads + head * a.group + row -
                        tok * a.group) * D + lane * E;
   if (a.dtype == RQ_F32) {
@@ -1044,8 +1086,7 @@ rq_status launch_rows(const AttnArgs& a, unsigned grid, cudaStream_t st) {
   const rq_status s = launch_kernel(attn_rows_kernel<D, I8, SPLIT>, dim3(grid), dim3(kThreads),
                                     (size_t)bytes, st, a);
   if (s != RQ_OK || a.shares == nullptr) return s;
-  const unsigned segments = (unsigned)(a.batch * a.row_tiles * a.kv_heads);
-  return launch_kernel(join_rows_kernel<D>, dim3(segments * (kRows / 8)), dim3(256), 0, st, a);
+  return launch_kernel(join_rows_kernel<D>, dim3(grid * (kRows / 8)), dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -1062,12 +1103,12 @@ rq_status launch_attention_rows(AttnArgs a, int head_dim, bool i8, AttnScratch* 
     grid = segments;
     if (grid > 0x7FFFFFFF) return RQ_ERR_SHAPE;
   } else {
-    // partial rows, and behind them who shares which segment
+    // partial rows, and behind them, per CTA, the segment it begins for several
     const size_t part = sizeof(float) * 2 * (size_t)grid * kRows * (head_dim + 4);
-    const rq_status s = scratch->reserve(part + sizeof(int4) * (size_t)segments, 0, st);
+    const rq_status s = scratch->reserve(part + sizeof(SharedSegment) * (size_t)grid, 0, st);
     if (s != RQ_OK) return s;
     a.part = scratch->part;
-    a.shares = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(scratch->part) + part);
+    a.shares = reinterpret_cast<SharedSegment*>(reinterpret_cast<uint8_t*>(scratch->part) + part);
   }
   const unsigned g = (unsigned)grid;
   const bool split = a.dtype == RQ_F32;

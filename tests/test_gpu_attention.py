@@ -289,3 +289,32 @@ def test_other_stream_and_graph(rq):
         torch.cuda.synchronize()
         c.check(out.cpu())
     own.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("batch,long", [(77, 1150), (90, 1300), (130, 2000), (200, 3000)])
+def test_one_longer_sequence_among_many_short_ones(rq, ctx, batch, long, dtype):
+    """Runs of cost that are shorter than a unit somewhere; every part counted
+    in a join has to be there."""
+    lengths = [i % 9 for i in range(batch)]
+    lengths[batch // 3] = long
+    c = Case(rq, batch, lengths, 1, 4, 1, 128, dtype, 0, 16)
+    c.spoil()
+    got = c.run(ctx)
+    c.check(got)
+    assert torch.equal(c.run(ctx), got)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths,new,heads", [
+    ([5000, 3, 900, 40, 2500], 40, (28, 4, 128)),      # two row tiles, one of them half empty
+    ([12000], 64, (8, 1, 128)), ([3000, 2900, 700], 19, (14, 2, 64))])
+def test_shared_segments_of_many_rows(rq, ctx, lengths, new, heads, dtype):
+    g = gen(new)
+    c = Case(rq, new, lengths, new, *heads, dtype, 0, 64, tree=random_tree(g, len(lengths), new))
+    c.spoil()
+    got = c.run(ctx)
+    c.check(got)
+    for _ in range(2):
+        assert torch.equal(c.run(ctx), got)
+    assert rq.rq_get_device_status() == 0

@@ -23,7 +23,7 @@ __device__ unsigned int g_attn_error = 0;
 
 constexpr int kKeys = 16;            // keys of a unit: one warp's step
 constexpr int kRows = 8;             // query rows of a segment
-constexpr int kJoin = 8;             // partials joined at once
+constexpr int kJoin = 8;             // neighbouring partials that are joined first
 
 // rq_attn_rows.cu's kernel runs from kManyRows query rows per kv head on, for
 // launches of at least kManyWork row-key pairs (with the places that the page
@@ -160,16 +160,16 @@ attn_kernel(const AttnArgs a) {
   if (!cutter.begin(seg)) return;
 
   // -------- the warp's loads, S - 1 units ahead of its products
-  Segment ld = seg;
-  int unit = ld.first + warp;          // next unit to load
+  Segment ahead = seg;
+  int unit = seg.first + warp;         // next unit to load
   int in_window = 0, pages_of = 0;     // lane i: page of the window's unit i, W units apart
   int ld_stage = 0;
   auto page_window = [&]() {  // (looked at when they are used)
     in_window = 0;
     const int64_t u = unit + (int64_t)lane * W;
     pages_of = 0;
-    if (u < ld.end && u * kKeys < ld.kv)
-      pages_of = a.table[(int64_t)cutter.sequence(ld.item) * a.max_pages +
+    if (u < ahead.end && u * kKeys < ahead.kv)
+      pages_of = a.table[(int64_t)cutter.sequence(ahead.item) * a.max_pages +
                          ((u * kKeys) >> a.lg_page)];
   };
   page_window();
@@ -179,12 +179,12 @@ attn_kernel(const AttnArgs a) {
   const uint32_t piece = (piece_chunk / (G::kPanel / 16)) * (kKeys * G::kPanel) +
                          swizzled<G::kPanel>(piece_row, piece_chunk % (G::kPanel / 16));
   auto load_one = [&]() {  // starts copying the warp's next unit, if there is one
-    while (unit >= ld.end && ld.left > 0) {
-      cutter.next(ld);
+    while (unit >= ahead.end && ahead.left > 0) {
+      cutter.next(ahead);
       unit = warp;
       in_window = 32;
     }
-    if (unit < ld.end && ld.kv > 0) {
+    if (unit < ahead.end && ahead.kv > 0) {
       if (in_window == 32) page_window();
       int page = __shfl_sync(0xFFFFFFFFu, pages_of, in_window);
       ++in_window;
@@ -192,7 +192,7 @@ attn_kernel(const AttnArgs a) {
         if (lane == 0) atomicOr(a.error, 2u);
         page = 0;
       }
-      const int64_t row = ((int64_t)(page * a.kv_heads + ld.head) << a.lg_page) +
+      const int64_t row = ((int64_t)(page * a.kv_heads + ahead.head) << a.lg_page) +
                           ((unit * kKeys) & page_mask);
       const uint32_t to = ring + ld_stage * (2 * G::kBytes) + piece;
       copy_rows<D>(to, a.k + row * D + lane * 16);
@@ -309,7 +309,7 @@ attn_kernel(const AttnArgs a) {
     float m = -INFINITY, l = 0.0f;
     float vref = 0x1p-112f;  // power of two at or above every vs so far
 
-    for (int u = seg.first + warp; u < seg.end; u += W) {
+    for (int u = seg.first + warp, end = seg.end; u < end; u += W) {
       copy_wait<S - 2>();
       __syncwarp();
       const int first = u * kKeys;  // place of the first key
@@ -458,33 +458,35 @@ attn_kernel(const AttnArgs a) {
     __syncthreads();
 
     const auto share = cutter.sharers(seg);
-    const int64_t cta0 = share.cta0;
+    const int cta0 = share.cta0;
     const int parts = share.parts, part = share.part;
     const bool second = share.second;
     constexpr int kVec = D / 4;
     constexpr int kPartRow = D + 4;  // output, then max and sum
     // A partial row set of this segment, by part number.
-    auto part_at = [&](int64_t p) -> int64_t { return (cta0 + p) * 2 + (p == 0 && second ? 1 : 0); };
+    auto part_at = [&](int p) -> int { return (cta0 + p) * 2 + (p == 0 && second ? 1 : 0); };
     // Join this thread's piece of `count` partials, `step` parts apart from
-    // part p0 on, eight loads in flight at a time; in part order.
-    auto join = [&](int64_t p0, int64_t step, int count, int r, int d, float4& v, float& mx,
+    // part p0 on, several loads in flight at a time (four of two CTAs' threads,
+    // whose registers eight would spill); in part order.
+    constexpr int kLoads = WIDE ? 8 : 4;
+    auto join = [&](int p0, int step, int count, int r, int d, float4& v, float& mx,
                     float& sum) {
       const float cr = tail.c[r];
-      for (int q0 = 0; q0 < count; q0 += kJoin) {
-        float4 ov[kJoin];
-        float2 ml[kJoin];
+      for (int q0 = 0; q0 < count; q0 += kLoads) {
+        float4 ov[kLoads];
+        float2 ml[kLoads];
 #pragma unroll
-        for (int k = 0; k < kJoin; ++k) {
+        for (int k = 0; k < kLoads; ++k) {
           ml[k] = make_float2(-INFINITY, 0.0f);
           ov[k] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (q0 + k < count) {
-            const float* part = a.part + (part_at(p0 + (q0 + k) * step) * kRows + r) * kPartRow;
+            const float* part = a.part + ((int64_t)part_at(p0 + (q0 + k) * step) * kRows + r) * kPartRow;
             ov[k] = __ldcg(reinterpret_cast<const float4*>(part + d));
             ml[k] = __ldcg(reinterpret_cast<const float2*>(part + D));
           }
         }
 #pragma unroll
-        for (int k = 0; k < kJoin; ++k) merge(v, mx, sum, ov[k], ml[k], cr);
+        for (int k = 0; k < kLoads; ++k) merge(v, mx, sum, ov[k], ml[k], cr);
       }
     };
     auto arrive = [&](unsigned int* ctr, unsigned int of) -> bool {
@@ -500,8 +502,8 @@ attn_kernel(const AttnArgs a) {
       __threadfence();
       return is_last;
     };
-    auto store_part = [&](int64_t slot, int r, int d, const float4& v, float mx, float sum) {
-      float* part = a.part + (slot * kRows + r) * kPartRow;
+    auto store_part = [&](int slot, int r, int d, const float4& v, float mx, float sum) {
+      float* part = a.part + ((int64_t)slot * kRows + r) * kPartRow;
       __stcg(reinterpret_cast<float4*>(part + d), v);
       if (d == 0) __stcg(reinterpret_cast<float2*>(part + D), make_float2(mx, sum));
     };
@@ -549,7 +551,7 @@ attn_kernel(const AttnArgs a) {
         const int i = tid + k * G::kThreads, r = i / kVec, d = (i % kVec) * 4;
         if (mine[k]) store_part(part_at(part), r, d, v[k], mx[k], sum[k]);
       }
-      const int64_t slot = part_at(first_of);
+      const int slot = part_at(first_of);
       last = arrive(a.counter + slot, (unsigned int)members);
       for (int level = 0; last && level < 2; ++level) {
         if (level == 1) {
@@ -681,7 +683,7 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
   const int64_t segments = items * c.kv_heads;
   const bool wide = segments <= device_sm_count();
   int64_t grid = (int64_t)(wide ? 1 : 2) * device_sm_count();
-  a.direct = items > kMaxItems;
+  a.direct = !Cutter<kRows, kKeys, 1, 6>::cuts(a, items);
   if (a.direct) {
     grid = segments;
     if (grid > 0x7FFFFFFF) return RQ_ERR_SHAPE;

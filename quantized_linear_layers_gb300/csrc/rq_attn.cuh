@@ -133,7 +133,7 @@ __device__ __forceinline__ int page_of(const AttnArgs& a, int b, int64_t place) 
 struct Segment {
   int item, head, first, end;
   int kv;        // places its rows may see, 0: an unused sequence
-  int64_t left;  // cost (kRun) or segments (else) of the CTA's work after it
+  int left;      // cost (kRun) or segments (else) of the CTA's work after it
 };
 
 // A segment that several CTAs share, as its first one notes it.
@@ -142,13 +142,13 @@ struct SharedSegment {
   int segment;        // item * kv_heads + head, -1: none
   int second;         // the first one's part lies in its second set of rows
   int ctas;
-  int64_t last, cost;  // the last sharer is the CTA ((last + 1) ctas - 1) / cost
+  int last, cost;  // the last sharer is the CTA ((last + 1) ctas - 1) / cost
 };
 
 struct CutShared {
   int warp_sum[32], warp_most[32];
   int cut, split, ctas;
-  int64_t cost;                   // of all segments
+  int cost;                       // of all segments
   int item_start[kMaxItems + 1];  // cost of the items before each, for one kv head
   int length[kMaxItems];          // the sequences' lengths
 };
@@ -170,6 +170,14 @@ template <int ROWS, int KEYS, int STEP, int ROUNDS, int WHOLE = 1, int PART = 1>
 struct Cutter {
   enum { kParts, kWhole, kRun };
   static constexpr int kLeast = ROUNDS * STEP * WHOLE;  // cost of the smallest part
+
+  // Host: whether a launch is cut by length.  Costs are 32-bit numbers; where
+  // the page table has room for more, or there are more items, each CTA takes
+  // one whole segment.
+  static bool cuts(const AttnArgs& a, int64_t items) {
+    const int64_t units = (((int64_t)a.max_pages << a.lg_page) + KEYS - 1) / KEYS;
+    return items <= kMaxItems && units * WHOLE * items <= 0x7FFFFFFF / a.kv_heads;
+  }
   const AttnArgs& a;
   CutShared& sh;
 
@@ -264,7 +272,7 @@ struct Cutter {
       if (i < items) sh.item_start[i] = before + scan - n;
     }
     if (tid == 0) {
-      const int64_t cost = (int64_t)carry * a.kv_heads;
+      const int cost = carry * a.kv_heads;
       const int64_t segments = (int64_t)items * a.kv_heads;
       int cut = kWhole, split = 1;
       if (segments <= grid) {
@@ -281,7 +289,7 @@ struct Cutter {
       sh.split = split;
       // a unit begins in every run: a CTA without one would be counted among
       // a segment's and leave no part
-      sh.ctas = (int)min((int64_t)grid, max((int64_t)1, cost / WHOLE));
+      sh.ctas = (int)min((int64_t)grid, max((int64_t)1, (int64_t)(cost / WHOLE)));
     }
     __syncthreads();
   }
@@ -295,7 +303,7 @@ struct Cutter {
     g.end = n;
     if (sh.cut == kRun) {
       const int c = cost_of(rt);
-      const int64_t all = (int64_t)n * c;
+      const int all = n * c;
       if (g.left < all) g.end = (int)units_in((uint32_t)g.left, (uint32_t)c);
       g.left -= all;
     } else {
@@ -331,21 +339,21 @@ struct Cutter {
     g.first = 0;
     if (sh.cut == kRun) {
       if ((int)blockIdx.x >= sh.ctas) return false;
-      const int64_t x0 = sh.cost * blockIdx.x / sh.ctas, x1 = sh.cost * (blockIdx.x + 1) / sh.ctas;
+      const int x0 = begin_of(blockIdx.x), x1 = begin_of(blockIdx.x + 1);
       int lo = 0, hi = items - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((int64_t)sh.item_start[mid] * a.kv_heads <= x0)
+        if (sh.item_start[mid] * a.kv_heads <= x0)
           lo = mid;
         else
           hi = mid - 1;
       }
       const uint32_t all = (uint32_t)(sh.item_start[lo + 1] - sh.item_start[lo]);
-      const int64_t from = x0 - (int64_t)sh.item_start[lo] * a.kv_heads;
+      const uint32_t from = (uint32_t)(x0 - sh.item_start[lo] * a.kv_heads);
       g.item = lo;
       g.head = (int)(from / all);
-      const uint32_t rest = (uint32_t)(from - (int64_t)g.head * all);
-      g.left = x1 - x0 + rest;
+      const uint32_t rest = from - (uint32_t)g.head * all;
+      g.left = x1 - x0 + (int)rest;
       g.first = (int)units_in(rest, (uint32_t)cost_of(tile(g)));
       const int skip = g.first;
       open(g);
@@ -390,28 +398,30 @@ struct Cutter {
   // Which CTAs share a segment that is not whole: `parts` from CTA cta0 on,
   // of which this is number `part`; second: where the first one's part lies.
   struct Sharers {
-    int64_t cta0;
-    int parts, part;
+    int cta0, parts, part;
     bool second;
   };
-  __device__ __forceinline__ int64_t owner(int64_t x) const {  // whose run x lies in
-    return ((x + 1) * sh.ctas - 1) / sh.cost;
+  __device__ __forceinline__ int begin_of(uint32_t cta) const {  // of its run
+    return (int)((int64_t)sh.cost * cta / sh.ctas);
+  }
+  __device__ __forceinline__ int owner(int x) const {  // whose run x lies in
+    return (int)((((int64_t)x + 1) * sh.ctas - 1) / sh.cost);
   }
   __device__ __forceinline__ Sharers sharers(const Segment& g) const {
-    Sharers r = {(int64_t)blockIdx.x, 1, 0, false};
+    Sharers r = {(int)blockIdx.x, 1, 0, false};
     if (whole(g)) return r;
     if (sh.cut == kRun) {
       const int all = sh.item_start[g.item + 1] - sh.item_start[g.item];
-      const int64_t s0 = (int64_t)sh.item_start[g.item] * a.kv_heads + (int64_t)g.head * all;
+      const int s0 = sh.item_start[g.item] * a.kv_heads + g.head * all;
       r.cta0 = owner(s0);
-      r.parts = (int)(owner(s0 + all - cost_of(tile(g))) - r.cta0) + 1;
-      r.part = (int)(blockIdx.x - r.cta0);
+      r.parts = owner(s0 + all - cost_of(tile(g))) - r.cta0 + 1;
+      r.part = (int)blockIdx.x - r.cta0;
       // the first one's run began in an earlier segment, and had a unit there
-      const int64_t x0 = sh.cost * r.cta0 / sh.ctas;
+      const int x0 = begin_of((uint32_t)r.cta0);
       r.second = x0 < s0 && begins_before(x0, s0, g);
     } else if (sh.cut == kParts) {
       r.part = (int)(blockIdx.x % (uint32_t)sh.split);
-      r.cta0 = (int64_t)blockIdx.x - r.part;
+      r.cta0 = (int)blockIdx.x - r.part;
       int first, end;
       part_of(units_of(g.kv), cost_of(tile(g)), r.part, &r.parts, &first, &end);
     }
@@ -426,8 +436,7 @@ struct Cutter {
                        sh.ctas, 0, sh.cost};
     if (sh.cut == kRun) {
       const int all = sh.item_start[g.item + 1] - sh.item_start[g.item];
-      r.last = (int64_t)sh.item_start[g.item] * a.kv_heads + (int64_t)(g.head + 1) * all -
-               cost_of(tile(g));
+      r.last = sh.item_start[g.item] * a.kv_heads + (g.head + 1) * all - cost_of(tile(g));
     } else if (sh.cut == kParts) {
       int first, end;
       part_of(units_of(g.kv), cost_of(tile(g)), 0, &r.parts, &first, &end);
@@ -438,7 +447,7 @@ struct Cutter {
  private:
   // Whether a unit begins in [x, s0), s0 being where segment g begins: the
   // last unit before s0 does unless it began before x.
-  __device__ __forceinline__ bool begins_before(int64_t x, int64_t s0, const Segment& g) const {
+  __device__ __forceinline__ bool begins_before(int x, int s0, const Segment& g) const {
     const int item = g.head > 0 ? g.item : g.item - 1;
     const int rt = item - sequence(item) * a.row_tiles;
     return s0 - cost_of(rt) >= x;

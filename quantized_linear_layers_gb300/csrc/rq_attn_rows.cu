@@ -56,6 +56,9 @@ struct Wide {
   static constexpr bool value = W;
 };
 
+// (a unit takes 1.9 us, or 1.2 in a half row tile)
+using Cutting = Cutter<kRows, kKeys, 1, 8, 8, 5>;
+
 struct RowsTail {
   float ks[kScales][kKeys], vs[kScales][kKeys];  // vs relative to vref, times kUp
   float vref[kScales];  // negative: not all of vs are finite
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
   pdl_trigger();
   prefetch_l2(a.q, a.q_bytes);
   prefetch_l2(a.table, (int64_t)a.batch * a.max_pages * 4);
-  Cutter<kRows, kKeys, 1, 8, 8, 5> cutter(a, tail.cut);  // a unit takes 1.9 us, or 1.2
+  Cutting cutter(a, tail.cut);
   cutter.template choose<kThreads>();
   Segment seg;
   const bool work = cutter.begin(seg);
@@ -997,7 +1000,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const AttnArgs a) {
   if (share.segment < 0) return;
   const int parts = share.parts > 0
                         ? share.parts
-                        : (int)(((share.last + 1) * share.ctas - 1) / share.cost) - cta0 + 1;
+                        : (int)((((int64_t)share.last + 1) * share.ctas - 1) / share.cost) - cta0 + 1;
   const int item = (int)quotient((uint32_t)share.segment, a.by_heads);
   const int head = share.segment - item * a.kv_heads;
   const int b = (int)quotient((uint32_t)item, a.by_tiles), rt = item - b * a.row_tiles;
@@ -1098,7 +1101,7 @@ rq_status launch_attention_rows(AttnArgs a, int head_dim, bool i8, AttnScratch* 
   const int64_t items = (int64_t)a.batch * a.row_tiles;
   const int64_t segments = items * a.kv_heads;
   int64_t grid = device_sm_count();
-  a.direct = items > kMaxItems;
+  a.direct = !Cutting::cuts(a, items);
   if (a.direct) {
     grid = segments;
     if (grid > 0x7FFFFFFF) return RQ_ERR_SHAPE;

@@ -63,7 +63,7 @@ struct RowsTail {
   float ks[kScales][kKeys], vs[kScales][kKeys];  // vs relative to vref, times kUp
   float vref[kScales];  // negative: not all of vs are finite
   uint64_t q_full[2], k_full[2], k_free[2], v_full[2], v_free[2], sc_full[kScales];
-  uint64_t s_full[2][2], p_full[2][2], pv_done[2], drained;
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2], drained[2];
   uint32_t tmem;
   CutShared cut;
 };
@@ -350,8 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       mbar_init(smem_u32(&tail.q_full[i]), 4);
       mbar_init(smem_u32(&tail.k_full[i]), kConvert / 32);
       mbar_init(smem_u32(&tail.v_full[i]), kConvert / 32);
-      mbar_init(smem_u32(&tail.k_free[i]), 1);
-      mbar_init(smem_u32(&tail.v_free[i]), 1);
+      mbar_init(smem_u32(&tail.k_free[i]), 2);  // of both row tiles
+      mbar_init(smem_u32(&tail.v_free[i]), 2);
+      mbar_init(smem_u32(&tail.drained[i]), 1);
       mbar_init(smem_u32(&tail.pv_done[i]), 1);
       for (int j = 0; j < 2; ++j) {
         mbar_init(smem_u32(&tail.s_full[i][j]), 1);
@@ -359,7 +360,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       }
     }
     for (int i = 0; i < kScales; ++i) mbar_init(smem_u32(&tail.sc_full[i]), 1);
-    mbar_init(smem_u32(&tail.drained), 1);
     mbar_fence_init();
   }
   if (warp == kIssueWarp) {
@@ -889,12 +889,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       if (!cutter.whole(seg) && seg.first == 0) note = cutter.note(seg, first_seg);
       a.shares[blockIdx.x] = note;
     }
-  } else if (work && warp == kIssueWarp) {
+  } else if (work && warp != kIssueWarp + 3) {
     // ------------------------------------------------------ products ----
-    // (the whole warp walks along, one lane issues)
+    // A warp for each row tile (the whole warp walks along, one lane issues).
+    const int w = (warp - kIssueWarp) >> 1;
     constexpr uint32_t kS = instr(kKeys, false), kO = instr(D, true);
-    uint32_t units = 0, segs[2] = {0, 0}, mine[2] = {0, 0};
-    auto scores = [&](int w, uint32_t unit_no, uint32_t my_no) {  // by one thread
+    uint32_t units = 0, segs = 0, mine = 0;
+    auto scores = [&](uint32_t unit_no, uint32_t my_no) {  // by one thread
       const uint32_t d = tmem + w * 256 + (my_no & 1u) * kKeys;
       const uint32_t qd = desc_k_major(q_base + w * ((SPLIT ? 2 : 1) * L::kQTile));
       const uint32_t kd = desc_k_major(kv_base + (unit_no & 1u) * (2 * L::kB));
@@ -910,72 +911,67 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         for (int k = 0; k < 4; ++k) mma_ss<true>(d, at + 2 * k, kp + 2 * k, kS);
       }
       commit(smem_u32(&tail.s_full[w][my_no & 1u]));
+      commit(smem_u32(&tail.k_free[unit_no & 1u]));
     };
     for (;;) {
       const int b = cutter.sequence(seg.item), rt = seg.item - b * a.row_tiles;
-      const int nw = rt * kRows + kTileRows < a.rows ? 2 : 1;
       const int n = seg.end - seg.first;
-      // the first scores of the segment
-      wait(ok, tail.k_full[units & 1u], units >> 1, a.error);
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-        if (w < nw) {
-          wait(ok, tail.q_full[w], segs[w], a.error);
-          fence_after();
-          if (elect_one()) {
-            scores(w, units, mine[w]);
-            if (w == nw - 1) commit(smem_u32(&tail.k_free[units & 1u]));
-          }
-          __syncwarp();
-          ++segs[w];
+      if (rt * kRows + w * kTileRows >= a.rows) {
+        // no rows: the codes are the other tile's alone
+        for (int u = 0; u < n; ++u) {
+          const uint32_t cur = units + u;
+          wait(ok, tail.k_full[cur & 1u], cur >> 1, a.error);
+          if (lane == 0) mbar_arrive(smem_u32(&tail.k_free[cur & 1u]));
+          wait(ok, tail.v_full[cur & 1u], cur >> 1, a.error);
+          if (lane == 0) mbar_arrive(smem_u32(&tail.v_free[cur & 1u]));
         }
-      for (int u = 0; u < n; ++u) {
-        const uint32_t cur = units + u, buf = cur & 1u;
-        const bool more = u + 1 < n;
-        if (more) wait(ok, tail.k_full[(cur + 1) & 1u], (cur + 1) >> 1, a.error);
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-          if (w < nw) {
-            const uint32_t p = mine[w]++;  // this unit's number of the row tile
-            if (more) {
-              // The scores go where the weights two units back are: products
-              // into different accumulators are not ordered by themselves.
-              if (u > 0) wait(ok, tail.pv_done[w], p - 1u, a.error);
-              fence_after();
-              if (elect_one()) {
-                scores(w, cur + 1, p + 1);
-                if (w == nw - 1) commit(smem_u32(&tail.k_free[(cur + 1) & 1u]));
-              }
-              __syncwarp();
-            }
-            if (w == 0) wait(ok, tail.v_full[buf], cur >> 1, a.error);
-            wait(ok, tail.p_full[w][p & 1u], p >> 1, a.error);
+      } else {
+        // the first scores of the segment
+        wait(ok, tail.k_full[units & 1u], units >> 1, a.error);
+        wait(ok, tail.q_full[w], segs, a.error);
+        ++segs;
+        fence_after();
+        if (elect_one()) scores(units, mine);
+        __syncwarp();
+        for (int u = 0; u < n; ++u) {
+          const uint32_t cur = units + u, buf = cur & 1u;
+          const uint32_t p = mine++;  // this unit's number of the row tile
+          if (u + 1 < n) {
+            wait(ok, tail.k_full[buf ^ 1u], (cur + 1) >> 1, a.error);
+            // The scores go where the weights two units back are: products
+            // into different accumulators are not ordered by themselves.
+            if (u > 0) wait(ok, tail.pv_done[w], p - 1u, a.error);
             fence_after();
-            if (elect_one()) {
-              const uint32_t d = tmem + w * 256 + 128;
-              const uint32_t pa = tmem + w * 256 + (p & 1u) * kKeys;
-              const uint32_t vd =
-                  desc_n_major(kv_base + buf * (2 * L::kB) + L::kB, L::kPanel);
-#pragma unroll
-              for (int s = 0; s < (SPLIT ? 2 : 1); ++s)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_ts(d, pa + s * 32 + k * 8, vd + k * (2048 >> 4), kO, u | s | k);
-              commit(smem_u32(&tail.pv_done[w]));
-              if (w == nw - 1) commit(smem_u32(&tail.v_free[buf]));
-            }
+            if (elect_one()) scores(cur + 1, p + 1);
             __syncwarp();
           }
+          wait(ok, tail.v_full[buf], cur >> 1, a.error);
+          wait(ok, tail.p_full[w][p & 1u], p >> 1, a.error);
+          fence_after();
+          if (elect_one()) {
+            const uint32_t d = tmem + w * 256 + 128;
+            const uint32_t pa = tmem + w * 256 + (p & 1u) * kKeys;
+            const uint32_t vd = desc_n_major(kv_base + buf * (2 * L::kB) + L::kB, L::kPanel);
+#pragma unroll
+            for (int s = 0; s < (SPLIT ? 2 : 1); ++s)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts(d, pa + s * 32 + k * 8, vd + k * (2048 >> 4), kO, u | s | k);
+            commit(smem_u32(&tail.pv_done[w]));
+            commit(smem_u32(&tail.v_free[buf]));
+          }
+          __syncwarp();
+        }
       }
       units += n;
       if (seg.left <= 0) break;
       cutter.next(seg);
     }
     // every product has completed before TMEM is released
-    if (elect_one()) commit(smem_u32(&tail.drained));
+    if (elect_one()) commit(smem_u32(&tail.drained[w]));
     __syncwarp();
     bool drained = true;
-    wait(drained, tail.drained, 0, a.error);
+    wait(drained, tail.drained[w], 0, a.error);
   }
   }
   fence_before();

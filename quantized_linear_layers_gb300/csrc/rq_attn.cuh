@@ -161,12 +161,13 @@ struct CutShared {
 //   kWhole: a run of whole segments per CTA;
 //   kRun: an equal run of cost per CTA, wherever segments begin or end; a
 //     unit is its CTA's in whose run it begins.
-// A unit costs WHOLE, or PART in a row tile of at most ROWS / 2 rows.  Joining
+// A unit costs WHOLE, or PART in a row tile of at most ROWS / 2 rows, and a
+// segment BEGIN before its first unit.  Joining
 // a segment over CTAs costs as much as about ROUNDS rounds, and so does
 // beginning another one: no part is made smaller than that, segments that
 // short stay whole, and a run may begin and end inside segments only where
 // that evens out more.
-template <int ROWS, int KEYS, int STEP, int ROUNDS, int WHOLE = 1, int PART = 1>
+template <int ROWS, int KEYS, int STEP, int ROUNDS, int WHOLE = 1, int PART = 1, int BEGIN = 0>
 struct Cutter {
   enum { kParts, kWhole, kRun };
   static constexpr int kLeast = ROUNDS * STEP * WHOLE;  // cost of the smallest part
@@ -176,7 +177,7 @@ struct Cutter {
   // one whole segment.
   static bool cuts(const AttnArgs& a, int64_t items) {
     const int64_t units = (((int64_t)a.max_pages << a.lg_page) + KEYS - 1) / KEYS;
-    return items <= kMaxItems && units * WHOLE * items <= 0x7FFFFFFF / a.kv_heads;
+    return items <= kMaxItems && (units * WHOLE + BEGIN) * items <= 0x7FFFFFFF / a.kv_heads;
   }
   const AttnArgs& a;
   CutShared& sh;
@@ -246,7 +247,7 @@ struct Cutter {
         const int b = sequence(i), rt = i - b * a.row_tiles;
         const int len = a.length[b];
         if (rt == 0) sh.length[b] = len;
-        n = units_of(places(len, rt)) * cost_of(rt);
+        n = BEGIN + units_of(places(len, rt)) * cost_of(rt);
       }
       int scan = n, top = n;
 #pragma unroll
@@ -278,7 +279,7 @@ struct Cutter {
       if (segments <= grid) {
         split = (int)min((uint32_t)grid / (uint32_t)segments, (uint32_t)(most + kLeast - 1) / kLeast);
         // the longest part's rounds against an even share's
-        const int64_t longest = ((int64_t)most + split - 1) * grid;
+        const int64_t longest = ((int64_t)(most - BEGIN) + (int64_t)(BEGIN + 1) * split - 1) * grid;
         cut = longest <= (cost + (int64_t)kLeast * grid) * split ? kParts : kRun;
       } else if (most > kLeast) {
         cut = kRun;
@@ -289,13 +290,13 @@ struct Cutter {
       sh.split = split;
       // a unit begins in every run: a CTA without one would be counted among
       // a segment's and leave no part
-      sh.ctas = (int)min((int64_t)grid, max((int64_t)1, (int64_t)(cost / WHOLE)));
+      sh.ctas = min(grid, max(1, cost / (WHOLE + BEGIN)));
     }
     __syncthreads();
   }
 
   // Sets end and left; item, head, first are set, and left: under kRun the
-  // cost from the segment's beginning to the run's end.
+  // cost from the segment's first unit to the run's end.
   __device__ __forceinline__ void open(Segment& g) const {
     const int b = sequence(g.item), rt = g.item - b * a.row_tiles;
     g.kv = places(length(b), rt);
@@ -305,7 +306,7 @@ struct Cutter {
       const int c = cost_of(rt);
       const int all = n * c;
       if (g.left < all) g.end = (int)units_in((uint32_t)g.left, (uint32_t)c);
-      g.left -= all;
+      g.left -= all + BEGIN;
     } else {
       --g.left;
     }
@@ -353,8 +354,8 @@ struct Cutter {
       g.item = lo;
       g.head = (int)(from / all);
       const uint32_t rest = from - (uint32_t)g.head * all;
-      g.left = x1 - x0 + (int)rest;
-      g.first = (int)units_in(rest, (uint32_t)cost_of(tile(g)));
+      g.left = x1 - x0 + (int)rest - BEGIN;
+      g.first = rest > BEGIN ? (int)units_in(rest - BEGIN, (uint32_t)cost_of(tile(g))) : 0;
       const int skip = g.first;
       open(g);
       if (skip >= g.end) {  // its last unit began in the run before
@@ -413,7 +414,7 @@ struct Cutter {
     if (sh.cut == kRun) {
       const int all = sh.item_start[g.item + 1] - sh.item_start[g.item];
       const int s0 = sh.item_start[g.item] * a.kv_heads + g.head * all;
-      r.cta0 = owner(s0);
+      r.cta0 = owner(s0 + BEGIN);
       r.parts = owner(s0 + all - cost_of(tile(g))) - r.cta0 + 1;
       r.part = (int)blockIdx.x - r.cta0;
       // the first one's run began in an earlier segment, and had a unit there

@@ -56,8 +56,9 @@ struct Wide {
   static constexpr bool value = W;
 };
 
-// (a unit takes 1.9 us, or 1.2 in a half row tile)
-using Cutting = Cutter<kRows, kKeys, 1, 8, 8, 5>;
+// (a unit takes 1.4 to 1.7 us, in a half row tile 1.1 to 1.3, and the change from
+// one segment to the next 5.5)
+using Cutting = Cutter<kRows, kKeys, 1, 8, 8, 6, 28>;
 
 struct RowsTail {
   float ks[kScales][kKeys], vs[kScales][kKeys];  // vs relative to vref, times kUp

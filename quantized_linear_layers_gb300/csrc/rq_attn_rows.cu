@@ -52,7 +52,7 @@ template <int D>
 constexpr int kPartRow = D + 4;  // a partial row: output, reference, sum
 
 template <bool W>
-struct Wide {
+struct Flag {
   static constexpr bool value = W;
 };
 
@@ -291,10 +291,10 @@ __device__ __forceinline__ float q_value(bool f16, const float (&x)[E], int i) {
   return __uint_as_float((i & 1) ? w & 0xFFFF0000u : w << 16);
 }
 
-// A warp's wait for a barrier phase; after one wait has run out, no further
+// A thread's wait for a barrier phase; after one wait has run out, no further
 // one is made, so that every role comes to its end.
-__device__ __forceinline__ void wait(bool& ok, const uint64_t& bar, uint32_t parity,
-                                     unsigned int* error) {
+__device__ __forceinline__ void wait_one(bool& ok, const uint64_t& bar, uint32_t parity,
+                                         unsigned int* error) {
   if (ok) {  // (in line: a call would spill what the roles hold in registers)
     const uint32_t addr = smem_u32(&bar);
     bool done = mbar_try_wait(addr, parity & 1u);
@@ -307,6 +307,12 @@ __device__ __forceinline__ void wait(bool& ok, const uint64_t& bar, uint32_t par
     }
     ok = done;
   }
+}
+
+// A warp's.
+__device__ __forceinline__ void wait(bool& ok, const uint64_t& bar, uint32_t parity,
+                                     unsigned int* error) {
+  wait_one(ok, bar, parity, error);
   ok = __all_sync(0xFFFFFFFFu, ok);
 }
 
@@ -584,33 +590,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
           const float4* vs = reinterpret_cast<const float4*>(tail.vs[sc]);
           const float2 c2 = make_float2(c, c), nb = make_float2(-base, -base);
           float2 l2 = make_float2(0.0f, 0.0f);
+          // (two copies of the loop, the rare one with its tests: 2 % of a bf16
+          // prompt's time)
+          auto weights = [&](auto zeros) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t hi[16], lo[16];
+            for (int half = 0; half < 2; ++half) {
+              uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 v4 = vs[8 * half + i];
-              const float* xi = x + 32 * half + 4 * i;
+              for (int i = 0; i < 8; ++i) {
+                const float4 v4 = vs[8 * half + i];
+                const float* xi = x + 32 * half + 4 * i;
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                float2 p = fma2(make_float2(xi[2 * k], xi[2 * k + 1]), c2, nb);
-                p.x = ex2(p.x);
-                p.y = ex2(p.y);
-                l2 = add2(l2, p);
-                float2 wt = mul2(p, k == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
-                if (odd) {
-                  wt.x = p.x == 0.0f ? 0.0f : wt.x;
-                  wt.y = p.y == 0.0f ? 0.0f : wt.y;
+                for (int k = 0; k < 2; ++k) {
+                  float2 p = fma2(make_float2(xi[2 * k], xi[2 * k + 1]), c2, nb);
+                  p.x = ex2(p.x);
+                  p.y = ex2(p.y);
+                  l2 = add2(l2, p);
+                  float2 wt = mul2(p, k == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
+                  if constexpr (decltype(zeros)::value) {
+                    wt.x = p.x == 0.0f ? 0.0f : wt.x;
+                    wt.y = p.y == 0.0f ? 0.0f : wt.y;
+                  }
+                  if constexpr (SPLIT)
+                    hi[2 * i + k] = cut_half2(wt, lo[2 * i + k]);
+                  else
+                    hi[2 * i + k] = pack_half2(wt.x, wt.y);
                 }
-                if constexpr (SPLIT)
-                  hi[2 * i + k] = cut_half2(wt, lo[2 * i + k]);
-                else
-                  hi[2 * i + k] = pack_half2(wt.x, wt.y);
               }
+              tmem_st16(s_col + buf * kKeys + 16 * half, hi);
+              if constexpr (SPLIT) tmem_st16(s_col + buf * kKeys + 32 + 16 * half, lo);
             }
-            tmem_st16(s_col + buf * kKeys + 16 * half, hi);
-            if constexpr (SPLIT) tmem_st16(s_col + buf * kKeys + 32 + 16 * half, lo);
-          }
+          };
+          if (odd)
+            weights(Flag<true>());
+          else
+            weights(Flag<false>());
           l += l2.x + l2.y;
           tmem_st_wait();
           fence_before();
@@ -704,12 +718,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
           __syncwarp();
         };
         if (SPLIT) {
-          pass(Wide<true>(), 0);
+          pass(Flag<true>(), 0);
         } else if (!whole) {
-          pass(Wide<true>(), 0);
-          pass(Wide<true>(), D / 2);
+          pass(Flag<true>(), 0);
+          pass(Flag<true>(), D / 2);
         } else {
-          pass(Wide<false>(), 0);
+          pass(Flag<false>(), 0);
         }
         if (!whole && live)
           __stcg(reinterpret_cast<float2*>(set + (my + lane) * kPartRow<D> + D),
@@ -892,7 +906,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
     }
   } else if (work && warp != kIssueWarp + 3) {
     // ------------------------------------------------------ products ----
-    // A warp for each row tile (the whole warp walks along, one lane issues).
+    // A thread for each row tile: a warp's votes in the waits would add to the
+    // way from one unit's weights to the scores two units on.
     const int w = (warp - kIssueWarp) >> 1;
     constexpr uint32_t kS = instr(kKeys, false), kO = instr(D, true);
     uint32_t units = 0, segs = 0, mine = 0;
@@ -914,6 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       commit(smem_u32(&tail.s_full[w][my_no & 1u]));
       commit(smem_u32(&tail.k_free[unit_no & 1u]));
     };
+    if (elect_one())
     for (;;) {
       const int b = cutter.sequence(seg.item), rt = seg.item - b * a.row_tiles;
       const int n = seg.end - seg.first;
@@ -921,53 +937,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         // no rows: the codes are the other tile's alone
         for (int u = 0; u < n; ++u) {
           const uint32_t cur = units + u;
-          wait(ok, tail.k_full[cur & 1u], cur >> 1, a.error);
-          if (lane == 0) mbar_arrive(smem_u32(&tail.k_free[cur & 1u]));
-          wait(ok, tail.v_full[cur & 1u], cur >> 1, a.error);
-          if (lane == 0) mbar_arrive(smem_u32(&tail.v_free[cur & 1u]));
+          wait_one(ok, tail.k_full[cur & 1u], cur >> 1, a.error);
+          mbar_arrive(smem_u32(&tail.k_free[cur & 1u]));
+          wait_one(ok, tail.v_full[cur & 1u], cur >> 1, a.error);
+          mbar_arrive(smem_u32(&tail.v_free[cur & 1u]));
         }
       } else {
         // the first scores of the segment
-        wait(ok, tail.k_full[units & 1u], units >> 1, a.error);
-        wait(ok, tail.q_full[w], segs, a.error);
+        wait_one(ok, tail.k_full[units & 1u], units >> 1, a.error);
+        wait_one(ok, tail.q_full[w], segs, a.error);
         ++segs;
         fence_after();
-        if (elect_one()) scores(units, mine);
-        __syncwarp();
+        scores(units, mine);
         for (int u = 0; u < n; ++u) {
           const uint32_t cur = units + u, buf = cur & 1u;
           const uint32_t p = mine++;  // this unit's number of the row tile
           if (u + 1 < n) {
-            wait(ok, tail.k_full[buf ^ 1u], (cur + 1) >> 1, a.error);
+            wait_one(ok, tail.k_full[buf ^ 1u], (cur + 1) >> 1, a.error);
             // The scores go where the weights two units back are: products
             // into different accumulators are not ordered by themselves.
-            if (u > 0) wait(ok, tail.pv_done[w], p - 1u, a.error);
+            if (u > 0) wait_one(ok, tail.pv_done[w], p - 1u, a.error);
             fence_after();
-            if (elect_one()) scores(cur + 1, p + 1);
-            __syncwarp();
+            scores(cur + 1, p + 1);
           }
-          wait(ok, tail.v_full[buf], cur >> 1, a.error);
-          wait(ok, tail.p_full[w][p & 1u], p >> 1, a.error);
+          wait_one(ok, tail.v_full[buf], cur >> 1, a.error);
+          wait_one(ok, tail.p_full[w][p & 1u], p >> 1, a.error);
           fence_after();
-          if (elect_one()) {
-            const uint32_t d = tmem + w * 256 + 128;
-            const uint32_t pa = tmem + w * 256 + (p & 1u) * kKeys;
-            const uint32_t vd = desc_n_major(kv_base + buf * (2 * L::kB) + L::kB, L::kPanel);
+          const uint32_t d = tmem + w * 256 + 128;
+          const uint32_t pa = tmem + w * 256 + (p & 1u) * kKeys;
+          const uint32_t vd = desc_n_major(kv_base + buf * (2 * L::kB) + L::kB, L::kPanel);
 #pragma unroll
-            for (int s = 0; s < (SPLIT ? 2 : 1); ++s)
+          for (int s = 0; s < (SPLIT ? 2 : 1); ++s)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_ts(d, pa + s * 32 + k * 8, vd + k * (2048 >> 4), kO, u | s | k);
-            commit(smem_u32(&tail.pv_done[w]));
-            commit(smem_u32(&tail.v_free[buf]));
-          }
-          __syncwarp();
+            for (int k = 0; k < 4; ++k)
+              mma_ts(d, pa + s * 32 + k * 8, vd + k * (2048 >> 4), kO, u | s | k);
+          commit(smem_u32(&tail.pv_done[w]));
+          commit(smem_u32(&tail.v_free[buf]));
         }
       }
       units += n;
       if (seg.left <= 0) break;
       cutter.next(seg);
     }
+    __syncwarp();
     // every product has completed before TMEM is released
     if (elect_one()) commit(smem_u32(&tail.drained[w]));
     __syncwarp();

@@ -149,6 +149,7 @@ struct CutShared {
   int warp_sum[32], warp_most[32];
   int cut, split, ctas;
   int cost;                       // of all segments
+  int each, over;                 // cost / ctas, cost % ctas
   int item_start[kMaxItems + 1];  // cost of the items before each, for one kv head
   int length[kMaxItems];          // the sequences' lengths
 };
@@ -291,6 +292,8 @@ struct Cutter {
       // a unit begins in every run: a CTA without one would be counted among
       // a segment's and leave no part
       sh.ctas = min(grid, max(1, cost / (WHOLE + BEGIN)));
+      sh.each = cost / sh.ctas;
+      sh.over = cost - sh.each * sh.ctas;
     }
     __syncthreads();
   }
@@ -402,8 +405,8 @@ struct Cutter {
     int cta0, parts, part;
     bool second;
   };
-  __device__ __forceinline__ int begin_of(uint32_t cta) const {  // of its run
-    return (int)((int64_t)sh.cost * cta / sh.ctas);
+  __device__ __forceinline__ int begin_of(uint32_t cta) const {  // of its run: cost * cta / ctas
+    return (int)(cta * (uint32_t)sh.each + cta * (uint32_t)sh.over / (uint32_t)sh.ctas);
   }
   __device__ __forceinline__ int owner(int x) const {  // whose run x lies in
     return (int)((((int64_t)x + 1) * sh.ctas - 1) / sh.cost);

@@ -246,51 +246,40 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 __device__ __forceinline__ uint32_t cut_half2(float2 w, uint32_t& lo) {
   const float2 h = make_float2(__uint_as_float(__float_as_uint(w.x) & 0xFFFFE000u),
                                __uint_as_float(__float_as_uint(w.y) & 0xFFFFE000u));
-  const float2 r = add2(w, make_float2(-h.x, -h.y));
+  const float2 r = fma2(h, make_float2(-1.0f, -1.0f), w);
   lo = pack_half2(r.x, r.y);
   return pack_half2(h.x, h.y);
 }
 
-// E values of a query row as they lie in memory (16-bit ones two to a word, in
-// x[0 .. E / 2)), and value i of them.
-template <int E, bool F32>
-__device__ __forceinline__ void load_q(const AttnArgs& a, int64_t off, float (&x)[E]) {
-  if constexpr (F32) {
-    const float* p = static_cast<const float*>(a.q) + off;
-    if constexpr (E == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p);
-      x[0] = v.x;
-      x[1] = v.y;
-      x[2] = v.z;
-      x[3] = v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(p);
-      x[0] = v.x;
-      x[1] = v.y;
-    }
+// Words of a query row as they lie in memory from element `at` on, and value i
+// of them (16-bit ones two to a word).
+template <int WORDS>
+__device__ __forceinline__ void load_q(const void* q, int size, int64_t at, uint32_t (&w)[WORDS]) {
+  const uint8_t* p = static_cast<const uint8_t*>(q) + at * size;
+  if constexpr (WORDS == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else if constexpr (WORDS == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
   } else {
-    const uint16_t* p = static_cast<const uint16_t*>(a.q) + off;
-    if constexpr (E == 4) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      x[2] = __uint_as_float(v.x);
-      x[3] = __uint_as_float(v.y);
-    } else {
-      x[1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(p));
-    }
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
   }
 }
-// (in the order i = 0, 1, ...: the words lie at the end, and value i overwrites x[i])
-template <int E, bool F32>
-__device__ __forceinline__ float q_value(bool f16, const float (&x)[E], int i) {
-  if constexpr (F32) return x[i];
-  const uint32_t w = __float_as_uint(x[E / 2 + i / 2]);
+template <int E, bool F32, int WORDS>
+__device__ __forceinline__ float q_value(bool f16, const uint32_t (&words)[WORDS], int i) {
+  if constexpr (F32) return __uint_as_float(words[i]);
+  const uint32_t w = words[i / 2 % WORDS];
   if (f16) {
     const float2 f = half_pair(w);
     return (i & 1) ? f.y : f.x;
   }
   return __uint_as_float((i & 1) ? w & 0xFFFF0000u : w << 16);
 }
-
 // A thread's wait for a barrier phase; after one wait has run out, no further
 // one is made, so that every role comes to its end.
 __device__ __forceinline__ void wait_one(bool& ok, const uint64_t& bar, uint32_t parity,
@@ -416,30 +405,39 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
             ((int64_t)b * a.new_tokens + tok) * a.q_stride +
             (int64_t)(seg.head * a.group + (live ? my_row - tok * a.group : 0)) * D;
         const uint32_t q_at = q_base + w * ((SPLIT ? 2 : 1) * L::kQTile) + quad * 32 * 128;
-        for (int r0 = 0; r0 < 32; r0 += 16) {  // sixteen rows' loads in flight
-          float x[16][E];
+        // eight or sixteen rows at a time, the next ones' loads in flight
+        constexpr int kStep = SPLIT ? 8 : 16;
+        constexpr int kLg = SPLIT ? 3 : 4;
+        constexpr int kWords = SPLIT ? E : E / 2;
+        uint32_t raw[kStep][kWords];
+        auto load = [&](int r0) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int64_t off = __shfl_sync(0xFFFFFFFFu, my_off, r0 + r) + lane * E;
-            load_q<E, SPLIT>(a, off, x[r]);
-          }
+          for (int r = 0; r < kStep; ++r)
+            load_q<kWords>(a.q, SPLIT ? 4 : 2, __shfl_sync(0xFFFFFFFFu, my_off, r0 + r) + lane * E,
+                           raw[r]);
+        };
+        load(0);
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += kStep) {
+          float x[kStep][E];
           // largest magnitudes, as bits: a NaN counts as above infinity.  (A
           // row past the last one stands in for the sequence's first: what it
           // gives is not written.)
-          uint32_t top[16];
+          uint32_t top[kStep];
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
+          for (int r = 0; r < kStep; ++r) {
             top[r] = 0u;
 #pragma unroll
-            for (int i = 0; i < E; ++i) x[r][i] = q_value<E, SPLIT>(a.dtype == RQ_F16, x[r], i);
-#pragma unroll
-            for (int i = 0; i < E; ++i)
+            for (int i = 0; i < E; ++i) {
+              x[r][i] = q_value<E, SPLIT>(a.dtype == RQ_F16, raw[r], i);
               top[r] = max(top[r], __float_as_uint(x[r][i]) & 0x7FFFFFFFu);
+            }
           }
-          // the rows' maxima, sixteen at once: each step halves the rows that
-          // a lane holds; lane bits 4, 3, 2, 1 are the row's bits 3, 2, 1, 0
+          if (r0 + kStep < 32) load(r0 + kStep);
+          // the rows' maxima, all at once: each step halves the rows that a
+          // lane holds; lane bits from 4 down are the row's bits from the top
 #pragma unroll
-          for (int n = 8, o = 16; n >= 1; n >>= 1, o >>= 1) {
+          for (int n = kStep / 2, o = 16; n >= 1; n >>= 1, o >>= 1) {
             const bool up_half = (lane & o) != 0;
 #pragma unroll
             for (int i = 0; i < n; ++i) {
@@ -448,7 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
               top[i] = max(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
             }
           }
-          const uint32_t most = max(top[0], __shfl_xor_sync(0xFFFFFFFFu, top[0], 1));
+          uint32_t most = max(top[0], __shfl_xor_sync(0xFFFFFFFFu, top[0], 1));
+          if (kLg == 3) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
           // times a power of two: the largest entry in [2^13, 2^14); a row
           // that is not finite becomes NaN
           int e = 0;
@@ -458,10 +457,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
           }
           const float own = most < 0x7F800000u ? __uint_as_float((uint32_t)(e + 127) << 23) : NAN;
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const float up = __shfl_sync(
-                0xFFFFFFFFu, own,
-                ((r >> 3) & 1) * 16 + ((r >> 2) & 1) * 8 + ((r >> 1) & 1) * 4 + (r & 1) * 2);
+          for (int r = 0; r < kStep; ++r) {
+            int from = 0;  // the row's bits, the top one at lane bit 4
+#pragma unroll
+            for (int k = 0; k < kLg; ++k) from |= ((r >> (kLg - 1 - k)) & 1) << (4 - k);
+            const float up = __shfl_sync(0xFFFFFFFFu, own, from);
             if (lane == r0 + r) c = up;
             const int byte = lane * E * 2;
             const uint32_t at = q_at + (byte >> 7) * L::kQPanel + (r0 + r) * 128 +
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
             uint32_t hi[E / 2], lo[E / 2];
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) {
-              const float2 v = make_float2(x[r][2 * i] * up, x[r][2 * i + 1] * up);
+              const float2 v = mul2(make_float2(x[r][2 * i], x[r][2 * i + 1]), make_float2(up, up));
               if (SPLIT)
                 hi[i] = cut_half2(v, lo[i]);
               else
@@ -995,15 +995,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
                  : "memory");
 }
 
-// Joins the partial rows of segments that several CTAs share.  A warp takes a
-// row: its lanes hold the parts' weights 2^(ref_p - max ref) / sum, then the
-// row's columns.
+// Joins the partial rows of segments that several CTAs share, in part order: a
+// thread takes four columns of kJoinRows rows, with kJoinParts parts of each
+// in flight.
+constexpr int kJoinRows = 2, kJoinParts = 2;
+template <int D>
+constexpr int kJoinBlock = 256 / (D / 4) * kJoinRows;  // rows of a CTA
+
 template <int D>
 __global__ void __launch_bounds__(256) join_rows_kernel(const AttnArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  constexpr int kBlocks = kRows / 8;  // CTAs per segment, eight rows each
+  constexpr int kBlocks = kRows / kJoinBlock<D>;  // CTAs per segment
+  constexpr int kAtOnce = kJoinBlock<D> / kJoinRows;
   const int cta0 = (int)(blockIdx.x / kBlocks);
   const SharedSegment share = a.shares[cta0];
   if (share.segment < 0) return;
@@ -1013,75 +1017,59 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const AttnArgs a) {
   const int item = (int)quotient((uint32_t)share.segment, a.by_heads);
   const int head = share.segment - item * a.kv_heads;
   const int b = (int)quotient((uint32_t)item, a.by_tiles), rt = item - b * a.row_tiles;
-  const int r = (int)(blockIdx.x % kBlocks) * 8 + (threadIdx.x >> 5);
-  const int row = rt * kRows + r;
-  if (row >= a.rows) return;
-  auto row_at = [&](int p) -> const float* {
-    return a.part +
-           (((int64_t)(cta0 + p) * 2 + (p == 0 ? share.second : 0)) * kRows + r) * kPartRow<D>;
-  };
-  float top = -INFINITY;
-  for (int p = lane; p < parts; p += 32) top = fmaxf(top, __ldcg(row_at(p) + D));
+  const int d = (int)(threadIdx.x % (D / 4)) * 4;
+  const int r0 = (int)(blockIdx.x % kBlocks) * kJoinBlock<D> + (int)(threadIdx.x / (D / 4));
+  float4 v[kJoinRows];
+  float top[kJoinRows], sum[kJoinRows];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  const float base = top == -INFINITY ? 0.0f : top;
-  constexpr int E = D / 32;
-  float v[E] = {}, sum = 0.0f;
-  for (int p0 = 0; p0 < parts; p0 += 32) {
-    float f = 0.0f, l = 0.0f;
-    if (p0 + lane < parts) {
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(row_at(p0 + lane) + D));
-      f = ex2(ml.x - base);
-      // a part whose scores are all NaN has no reference, but its sum counts
-      l = ml.x == -INFINITY ? ml.y : ml.y * f;
-    }
-    sum += warp_sum(l);
-    const int n = min(32, parts - p0);
-#pragma unroll 8
-    for (int p = 0; p < n; ++p) {
-      const float fp = __shfl_sync(0xFFFFFFFFu, f, p);
-      if constexpr (E == 4) {
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(row_at(p0 + p)) + lane);
-        v[0] = fmaf(o.x, fp, v[0]);
-        v[1] = fmaf(o.y, fp, v[1]);
-        v[2] = fmaf(o.z, fp, v[2]);
-        v[3] = fmaf(o.w, fp, v[3]);
-      } else {
-        const float2 o = __ldcg(reinterpret_cast<const float2*>(row_at(p0 + p)) + lane);
-        v[0] = fmaf(o.x, fp, v[0]);
-        v[1] = fmaf(o.y, fp, v[1]);
+  for (int k = 0; k < kJoinRows; ++k) {
+    v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    top[k] = -INFINITY;
+    sum[k] = 0.0f;
+  }
+  for (int p0 = 0; p0 < parts; p0 += kJoinParts) {
+    float4 o[kJoinRows][kJoinParts];
+    float2 ml[kJoinRows][kJoinParts];
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k)
+#pragma unroll
+      for (int p = 0; p < kJoinParts; ++p) {
+        const int r = r0 + k * kAtOnce;
+        o[k][p] = make_float4(0.f, 0.f, 0.f, 0.f);
+        ml[k][p] = make_float2(-INFINITY, 0.0f);
+        if (p0 + p < parts && rt * kRows + r < a.rows) {
+          const int set = (cta0 + p0 + p) * 2 + (p0 + p == 0 ? share.second : 0);
+          const float* row = a.part + ((int64_t)set * kRows + r) * kPartRow<D>;
+          o[k][p] = __ldcg(reinterpret_cast<const float4*>(row + d));
+          ml[k][p] = __ldcg(reinterpret_cast<const float2*>(row + D));
+        }
       }
-    }
-  }
-  const float r1 = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-  for (int i = 0; i < E; ++i) v[i] *= r1;
-  const int tok = (int)quotient((uint32_t)row, a.by_group);
-  const int64_t dst = (((int64_t)b * a.new_tokens + tok) * a.q_heads + head * a.group + row -
-                       tok * a.group) * D + lane * E;
-  if (a.dtype == RQ_F32) {
-    float* out = static_cast<float*>(a.out) + dst;
-    if constexpr (E == 4)
-      *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-      *reinterpret_cast<float2*>(out) = make_float2(v[0], v[1]);
-    return;
-  }
-  uint32_t h[E / 2];
+    for (int k = 0; k < kJoinRows; ++k)
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
-    if (a.dtype == RQ_F16) {
-      h[i] = pack_half2(v[2 * i], v[2 * i + 1]);
+      for (int p = 0; p < kJoinParts; ++p) merge(v[k], top[k], sum[k], o[k][p], ml[k][p], 1.0f);
+  }
+#pragma unroll
+  for (int k = 0; k < kJoinRows; ++k) {
+    const int row = rt * kRows + r0 + k * kAtOnce;
+    if (row >= a.rows) continue;
+    const float r1 = sum[k] == 0.0f ? 0.0f : 1.0f / sum[k];
+    const float4 y = make_float4(v[k].x * r1, v[k].y * r1, v[k].z * r1, v[k].w * r1);
+    const int tok = (int)quotient((uint32_t)row, a.by_group);
+    const int64_t dst = (((int64_t)b * a.new_tokens + tok) * a.q_heads + head * a.group + row -
+                         tok * a.group) * D + d;
+    if (a.dtype == RQ_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + dst) = y;
+    } else if (a.dtype == RQ_F16) {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + dst) =
+          make_uint2(pack_half2(y.x, y.y), pack_half2(y.z, y.w));
     } else {
-      const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-      h[i] = *reinterpret_cast<const uint32_t*>(&t);
+      const __nv_bfloat162 h0 = __floats2bfloat162_rn(y.x, y.y);
+      const __nv_bfloat162 h1 = __floats2bfloat162_rn(y.z, y.w);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + dst) = make_uint2(
+          *reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
     }
   }
-  uint16_t* out = static_cast<uint16_t*>(a.out) + dst;
-  if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(out) = make_uint2(h[0], h[1]);
-  else
-    *reinterpret_cast<uint32_t*>(out) = h[0];
 }
 
 template <int D, bool I8, bool SPLIT>
@@ -1098,7 +1086,7 @@ rq_status launch_rows(const AttnArgs& a, unsigned grid, cudaStream_t st) {
   const rq_status s = launch_kernel(attn_rows_kernel<D, I8, SPLIT>, dim3(grid), dim3(kThreads),
                                     (size_t)bytes, st, a);
   if (s != RQ_OK || a.shares == nullptr) return s;
-  return launch_kernel(join_rows_kernel<D>, dim3(grid * (kRows / 8)), dim3(256), 0, st, a);
+  return launch_kernel(join_rows_kernel<D>, dim3(grid * (kRows / kJoinBlock<D>)), dim3(256), 0, st, a);
 }
 
 }  // namespace

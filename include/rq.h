@@ -424,8 +424,10 @@ rq_status rq_kv_read(const rq_kv_cache *cache_host, int dtype, const int64_t *sl
  * What lies in the cache behind a sequence's places, or under a cleared
  * bit, does not reach the output.
  * Accuracy: with f32 activations q, the probabilities and both products are
- * carried to about 22 bits (each f32 operand split into two f16 parts, codes
- * exact in f16, f32 sums); with f16 / bf16 activations q and the
+ * carried to about 21 bits (each f32 operand split into two f16 parts, codes
+ * exact in f16, f32 sums, whose additions the tensor cores cut off rather than
+ * round: about 1e-6 of the result, 6e-6 for single tokens of dozens of
+ * sequences of 60000); with f16 / bf16 activations q and the
  * probabilities are f16 operands (11 bits).
  * Partial results of split sequences live in scratch owned by ctx, which
  * grows on a call that needs more (allocating: call once at the largest

@@ -27,13 +27,14 @@ constexpr int kJoin = 8;             // neighbouring partials that are joined fi
 
 // rq_attn_rows.cu's kernel runs from kManyRows query rows per kv head on, for
 // launches of at least kManyWork row-key pairs (with the places that the page
-// table has room for).  It costs about 20 us before its first product and
-// then hardly more for 250 rows than for 8, this file's kernel 8 us and then a
-// pass over the cache for every 8 rows.  Measured, this / that: 8 sequences of
-// up to 8000 tokens, f32, 28 rows 47 / 55 us, 42 rows 61 / 55, 112 rows 124 /
-// 58; one of 8000, 56 rows 19 / 29, 112 rows 31 / 33, 224 rows 48 / 40; one of
-// 500, 224 rows 10 / 27.
-constexpr int kManyRows = 40;
+// table has room for).  It costs about 20 us before and after its products and
+// then hardly more for 112 rows than for 8, this file's kernel 8 us and then a
+// pass over the cache for every 8 rows.  Measured, that / this (f32, 28 query
+// heads, 4 kv heads, microseconds): 8 sequences of 8000 tokens, 21 rows 48 /
+// 37, 28 rows 48 / 47, 42 rows 48 / 62, 112 rows 49 / 126; of 2000 tokens, 42
+// rows 29 / 27, 56 rows 29 / 30; one of 8000, 84 rows 30 / 24, 112 rows 31 /
+// 32, 224 rows 36 / 48; one of 500, 224 rows 23 / 10.
+constexpr int kManyRows = 32;
 constexpr double kManyWork = 3e6;
 
 template <int D, bool WIDE>

@@ -26,10 +26,11 @@ struct AttnArgs {
   int64_t pages;
   float scale_log2;
   int dtype;
-  int direct;  // one CTA per segment, no splitting
+  int direct;  // whole segments only
   float* part;
   unsigned int* counter;
   SharedSegment* shares;  // per CTA: the segment it begins for several (null: no join)
+  float4* flushed;        // per CTA: sums of output rows taken out of TMEM
   unsigned int* error;  // bit 1: an index outside its array
 };
 
@@ -373,7 +374,7 @@ struct Cutter {
       s0 = (int)((uint32_t)s0 / (uint32_t)sh.split);
       s1 = s0 + 1;
       if (s0 >= segments) return false;
-    } else if (!a.direct) {
+    } else {
       s0 = (int)((int64_t)segments * blockIdx.x / grid);
       s1 = (int)((int64_t)segments * (blockIdx.x + 1) / grid);
       if (s0 >= s1) return false;

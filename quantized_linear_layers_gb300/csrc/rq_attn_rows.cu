@@ -6,16 +6,27 @@
 // share 64 keys at a time:
 //   warps 0-3, 4-7   softmax of tile 0 and 1: a thread owns a row
 //   warps 8-15       codes of K and V to f16 in shared memory, two units deep
-//   warp 16          allocates TMEM; one thread issues the products
+//   warps 16, 18     a thread of each issues the products of tile 0 and 1;
+//                    warp 16 allocates TMEM
 //   warp 17          the scales; asks codes into L2, three units ahead; notes
 //                    for the join which segment goes on in other CTAs
-//   warps 18, 19     idle
+//   warp 19          idle
 // S = Q K^T (A = Q from shared memory) lands in one of two TMEM buffers per
 // row tile; its softmax writes P over it, as f16 high and low parts for f32
 // rows (64 + 64 keys in S's 64 columns), and P V takes A = P from TMEM and
 // adds to O in TMEM.  While a row tile's softmax runs, the tensor cores work
 // on its next scores and on the other tile.  f32 rows take both products
 // twice (Q high and low, P high and low), 16-bit rows once.
+//
+// Measured (28 query, 4 kv heads of 128): trees of 48 over 8 sequences of 8000
+// tokens, f32, 118 us (292 TFLOP/s, each product counted once); two prompts of
+// 1500 tokens behind 600, bf16, 109 us (502 TFLOP/s).  A unit of 256 rows takes
+// 1.4 us in bf16, 1.7 in f32, of which the tensor pipe works 0.6 and 1.25.  No
+// pipe is full: what bounds it is the way from scores over softmax, barrier,
+// products and barrier back to scores (all exponentials, scales and maxima
+// left out of a copy, it still took 1.35 us), and around the units the
+// prologue (4 us), the first query rows (4), the change of segments (5) and
+// the join (about 6).
 #include "rq_attn.cuh"
 
 namespace rq {
@@ -35,6 +46,14 @@ constexpr int kIssueWarp = (kSoft + kConvert) / 32;
 constexpr int kScales = 4;                // units whose scales are kept
 constexpr int kAhead = 3;                 // units that codes are asked into L2 ahead of use
 constexpr float kLazy = 8.0f;             // a maximum is kept while scores pass it by less than 2^8
+// The tensor cores cut their sums off towards zero.  With f32 rows, whose
+// products are carried to 21 bits, the output's sum therefore leaves TMEM every
+// kFlush units for one with rounded additions, in the CTA's own scratch (in
+// L2).  Relative error over 8000 keys, and trees of 48 over 8 such sequences:
+// 5.7e-6, 107 us without; 2.4e-6 every 16 units; 1.4e-6, 116 us every 8;
+// 1.1e-6, 118 us every 6; 0.9e-6, 124 us every 4.  (f32 sums in plain form:
+// 1.5e-6 there, 0.9e-6 over 2000 keys.)
+constexpr int kFlush = 6;
 constexpr float kUp = 128.0f;             // weights p vs / vref are kept 2^7 times larger in f16
 
 template <int D, bool SPLIT>
@@ -330,6 +349,13 @@ struct PageWindow {
   }
 };
 
+// Whether unit u of a segment begins row tile w's output anew: the two tiles in
+// turn, so that one works on while the other's sum is taken out.
+template <bool SPLIT>
+__device__ __forceinline__ bool starts_anew(int u, int w) {
+  return u == 0 || (SPLIT && (u + w * (kFlush / 2)) % kFlush == 0);
+}
+
 // ------------------------------------------------------------- the kernel --
 
 template <int D, bool I8, bool SPLIT>
@@ -395,6 +421,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       const int row0 = rt * kRows + w * kTileRows;
       const int n_units = seg.end - seg.first;
       float l = 0.0f, ref = -INFINITY, c = 0.0f, vref = 0x1p-112f;
+      // what the flushed sum is relative to; it lies column by column of four,
+      // the warp's rows one after another
+      float ref_kept = -INFINITY, vref_kept = 0.0f;
+      bool kept = false;
+      auto to_now = [&]() -> float {  // the kept sum's factor
+        return ref_kept == -INFINITY ? 0.0f : ex2(ref_kept - ref) * (vref_kept / vref);
+      };
+      float4* const sum_at = SPLIT ? a.flushed + ((int64_t)blockIdx.x * 8 + warp) * (D * 8) + lane
+                                   : nullptr;
       if (row0 < a.rows) {
         // ---- this warp's 32 query rows, to f16 parts in shared memory
         constexpr int E = D / 32;
@@ -508,12 +543,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         for (int u = 0; u < n_units; ++u) {
           const uint32_t sc = (all_units + u) % kScales;
           const uint32_t buf = units & 1u;
+          const bool fresh = starts_anew<SPLIT>(u, w);  // O begins again from zero
           // Scores of a unit mean that the weights of the one two before were
           // taken, so the scales' barrier is past its last turn: a tile that
           // sat out a segment does not mistake an older turn for this one.
           wait(ok, tail.s_full[w][buf], units >> 1, a.error);
           wait(ok, tail.sc_full[sc], (all_units + u) / kScales, a.error);
           fence_after();
+          if (SPLIT && fresh && u > 0) {
+            const float f = to_now();
+            // (waited for after the scores, which came after the turn before)
+            wait(ok, tail.pv_done[w], units - 1u, a.error);
+            fence_after();
+#pragma unroll
+            for (int d = 0; d < D; d += 32) {
+              float o[32];
+              float4 v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                v[i] = kept ? __ldcg(sum_at + (d / 4 + i) * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+              tmem_ld32(o_col + d, o);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                __stcg(sum_at + (d / 4 + i) * 32,
+                       make_float4(fmaf(v[i].x, f, o[4 * i]), fmaf(v[i].y, f, o[4 * i + 1]),
+                                   fmaf(v[i].z, f, o[4 * i + 2]), fmaf(v[i].w, f, o[4 * i + 3])));
+            }
+            kept = true;
+            ref_kept = ref;
+            vref_kept = vref;
+          }
           float x[kKeys];
           tmem_ld64(s_col + buf * kKeys, x);
           const float4* ks = reinterpret_cast<const float4*>(tail.ks[sc]);
@@ -572,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
             l *= al;
             ref = to;
             vref = vnow;
-            if (u > 0) {
+            if (!fresh) {
               wait(ok, tail.pv_done[w], units - 1u, a.error);
               fence_after();
 #pragma unroll
@@ -655,6 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         const int64_t my_dst = (((int64_t)b * a.new_tokens + tok) * a.q_heads +
                                 seg.head * a.group + (live ? my_row - tok * a.group : 0)) * D;
         const float back = vref * (1.0f / kUp);
+        const float f_kept = SPLIT ? to_now() : 0.0f;
         const float r1 = !whole ? back : l == 0.0f ? 0.0f : back / l;
         // A thread holds a row; memory wants a warp to write one.  The rows
         // pass through the warp's part of the query tile, which the segment's
@@ -670,6 +730,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
           for (int d = 0; d < kCols; d += 32) {
             float o[32];
             tmem_ld32(o_col + d0 + d, o);
+            if (SPLIT && kept) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 v = __ldcg(sum_at + ((d0 + d) / 4 + i) * 32);
+                o[4 * i] = fmaf(v.x, f_kept, o[4 * i]);
+                o[4 * i + 1] = fmaf(v.y, f_kept, o[4 * i + 1]);
+                o[4 * i + 2] = fmaf(v.z, f_kept, o[4 * i + 2]);
+                o[4 * i + 3] = fmaf(v.w, f_kept, o[4 * i + 3]);
+              }
+            }
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] *= r1;
             uint32_t h[kWide ? 32 : 16];
@@ -915,16 +985,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       const uint32_t d = tmem + w * 256 + (my_no & 1u) * kKeys;
       const uint32_t qd = desc_k_major(q_base + w * ((SPLIT ? 2 : 1) * L::kQTile));
       const uint32_t kd = desc_k_major(kv_base + (unit_no & 1u) * (2 * L::kB));
-      mma_ss<false>(d, qd, kd, kS);
+      // The low parts first: the tensor cores cut each sum off towards zero,
+      // and those of the low parts are small.
 #pragma unroll
-      for (int k = 1; k < 4; ++k) mma_ss<true>(d, qd + 2 * k, kd + 2 * k, kS);
-#pragma unroll
-      for (int i = 1; i < (SPLIT ? 2 : 1) * L::kPanels; ++i) {
-        // (the low part follows the high one)
-        const uint32_t at = qd + i * (L::kQPanel >> 4);
+      for (int i = 0; i < (SPLIT ? 2 : 1) * L::kPanels; ++i) {
+        const uint32_t at = qd + (SPLIT ? (i + L::kPanels) % (2 * L::kPanels) : i) * (L::kQPanel >> 4);
         const uint32_t kp = kd + (i % L::kPanels) * (L::kPanel >> 4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_ss<true>(d, at + 2 * k, kp + 2 * k, kS);
+        for (int k = 0; k < 4; ++k) {
+          if (i + k == 0)
+            mma_ss<false>(d, at, kp, kS);
+          else
+            mma_ss<true>(d, at + 2 * k, kp + 2 * k, kS);
+        }
       }
       commit(smem_u32(&tail.s_full[w][my_no & 1u]));
       commit(smem_u32(&tail.k_free[unit_no & 1u]));
@@ -970,7 +1043,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
           for (int s = 0; s < (SPLIT ? 2 : 1); ++s)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_ts(d, pa + s * 32 + k * 8, vd + k * (2048 >> 4), kO, u | s | k);
+              mma_ts(d, pa + s * 32 + k * 8, vd + k * (2048 >> 4), kO,
+                     (starts_anew<SPLIT>(u, w) ? 0u : 1u) | s | k);
           commit(smem_u32(&tail.pv_done[w]));
           commit(smem_u32(&tail.v_free[buf]));
         }
@@ -1097,21 +1171,26 @@ rq_status launch_attention_rows(AttnArgs a, int head_dim, bool i8, AttnScratch* 
   a.by_tiles = divisor((uint32_t)a.row_tiles);
   const int64_t items = (int64_t)a.batch * a.row_tiles;
   const int64_t segments = items * a.kv_heads;
-  int64_t grid = device_sm_count();
+  const int64_t grid = device_sm_count();
+  if (segments > 0x7FFFFFFF) return RQ_ERR_SHAPE;
   a.direct = !Cutting::cuts(a, items);
-  if (a.direct) {
-    grid = segments;
-    if (grid > 0x7FFFFFFF) return RQ_ERR_SHAPE;
-  } else {
-    // partial rows, and behind them, per CTA, the segment it begins for several
-    const size_t part = sizeof(float) * 2 * (size_t)grid * kRows * (head_dim + 4);
-    const rq_status s = scratch->reserve(part + sizeof(SharedSegment) * (size_t)grid, 0, st);
+  const bool split = a.dtype == RQ_F32;
+  // partial rows, behind them, per CTA, the segment it begins for several, and
+  // the sums that left TMEM
+  const size_t part = a.direct ? 0 : sizeof(float) * 2 * (size_t)grid * kRows * (head_dim + 4);
+  const size_t shares = a.direct ? 0 : ((sizeof(SharedSegment) * (size_t)grid + 15) & ~(size_t)15);
+  const size_t sums = split ? sizeof(float) * (size_t)grid * kRows * head_dim : 0;
+  if (part + shares + sums > 0) {
+    const rq_status s = scratch->reserve(part + shares + sums, 0, st);
     if (s != RQ_OK) return s;
-    a.part = scratch->part;
-    a.shares = reinterpret_cast<SharedSegment*>(reinterpret_cast<uint8_t*>(scratch->part) + part);
+    uint8_t* at = reinterpret_cast<uint8_t*>(scratch->part);
+    if (!a.direct) {
+      a.part = scratch->part;
+      a.shares = reinterpret_cast<SharedSegment*>(at + part);
+    }
+    a.flushed = reinterpret_cast<float4*>(at + part + shares);
   }
   const unsigned g = (unsigned)grid;
-  const bool split = a.dtype == RQ_F32;
   if (head_dim == 64) {
     if (i8)
       return split ? launch_rows<64, true, true>(a, g, st) : launch_rows<64, true, false>(a, g, st);

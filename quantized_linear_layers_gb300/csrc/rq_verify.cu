@@ -14,6 +14,11 @@
 // memory, and finds the token by itself in the part that holds the point: one
 // cluster barrier per draw, no scratch, no atomics across CTAs, one launch;
 // the walk down a tree is a loop of draws inside it.
+//
+// Bound by how many loads 8 SMs a sequence keep in flight: 32 chains of 7
+// drafts over 131072 entries take 11.9 us, 2.8 TB/s of the rows that they
+// read; a tree by the latency of its draws one after another, about 3 us each
+// (6 trees of 40 drafts over 50001 entries: 13 to 15 us).
 #include "rq_device.cuh"
 #include "rq_internal.h"
 

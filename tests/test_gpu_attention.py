@@ -318,3 +318,16 @@ def test_shared_segments_of_many_rows(rq, ctx, lengths, new, heads, dtype):
     for _ in range(2):
         assert torch.equal(c.run(ctx), got)
     assert rq.rq_get_device_status() == 0
+
+
+def test_long_sums_of_many_rows(rq, ctx):
+    # The tensor cores cut sums off: at most 2^-23 of the sum at each of the 8
+    # additions of a unit of 64 keys, on average half of that, in the 6 units
+    # that are summed there before a rounded addition (2.9e-6); 16 in a score
+    # of magnitude up to about 4, half of them small (1.9e-6).
+    g = gen(77)
+    c = Case(rq, 77, [8000] * 8, 48, 28, 4, 128, "f32", 0, 64, tree=random_tree(g, 8, 48))
+    got = c.run(ctx).double()[:1]
+    ref, _ = attention(c.q[:1], values(c.k, c.ks), values(c.v, c.vs), c.table[:1], c.lengths[:1],
+                       c.tree[:1], c.scale, c.dtype, c.page)
+    assert float((got - ref).norm() / ref.norm()) <= 4.8e-6

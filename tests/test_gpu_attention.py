@@ -331,3 +331,18 @@ def test_long_sums_of_many_rows(rq, ctx):
     ref, _ = attention(c.q[:1], values(c.k, c.ks), values(c.v, c.vs), c.table[:1], c.lengths[:1],
                        c.tree[:1], c.scale, c.dtype, c.page)
     assert float((got - ref).norm() / ref.norm()) <= 4.8e-6
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("batch,new,heads", [(1100, 1, (2, 1, 64)), (300, 160, (8, 1, 64))])
+def test_more_tiles_than_are_cut_by_length(rq, ctx, batch, new, heads, dtype):
+    lengths = [(37 * i) % 90 for i in range(batch)]
+    lengths[7], lengths[batch - 1], lengths[20] = 900, 700, -1
+    c = Case(rq, 78, lengths, new, *heads, dtype, 0, 64)
+    got = c.run(ctx).double()
+    sel = torch.tensor([0, 1, 7, 20, 21, batch // 2, batch - 1])
+    ref, tol = attention(c.q[sel], values(c.k, c.ks), values(c.v, c.vs), c.table[sel],
+                         c.lengths[sel], None, c.scale, c.dtype, c.page)
+    assert bool(((got[sel] - ref).abs() <= tol).all())
+    assert bool((c.run(ctx).double() == got).all())
+    assert rq.rq_get_device_status() == 0

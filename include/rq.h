@@ -431,7 +431,7 @@ rq_status rq_kv_read(const rq_kv_cache *cache_host, int dtype, const int64_t *sl
  * probabilities are f16 operands (11 bits).
  * Partial results of split sequences live in scratch owned by ctx, which
  * grows on a call that needs more (allocating: call once at the largest
- * sizes before a stream capture); they are joined in a fixed order, so equal
+ * sizes of each type before a stream capture); they are joined in a fixed order, so equal
  * calls give equal bits.
  * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_QTYPE (dtype or format),
  * RQ_ERR_ALLOC, RQ_ERR_CUDA. */

@@ -26,16 +26,19 @@ constexpr int kRows = 8;             // query rows of a segment
 constexpr int kJoin = 8;             // neighbouring partials that are joined first
 
 // rq_attn_rows.cu's kernel runs from kManyRows query rows per kv head on, for
-// launches of at least kManyWork row-key pairs (with the places that the page
-// table has room for).  It costs about 20 us before and after its products and
+// launches of at least kManyWork: rows times keys (the places that the page
+// table has room for), and kBeginning keys more a row for what beginning its 8
+// rows costs here.  It costs about 20 us before and after its products and
 // then hardly more for 112 rows than for 8, this file's kernel 8 us and then a
-// pass over the cache for every 8 rows.  Measured, that / this (f32, 28 query
-// heads, 4 kv heads, microseconds): 8 sequences of 8000 tokens, 21 rows 48 /
+// pass over the cache for every 8 rows.  Measured, that / this (28 query heads,
+// 4 kv heads of 128, microseconds): 8 sequences of 8000 tokens, 21 rows 48 /
 // 37, 28 rows 48 / 47, 42 rows 48 / 62, 112 rows 49 / 126; of 2000 tokens, 42
-// rows 29 / 27, 56 rows 29 / 30; one of 8000, 84 rows 30 / 24, 112 rows 31 /
-// 32, 224 rows 36 / 48; one of 500, 224 rows 23 / 10.
+// rows (3.3e6) 29 / 27, 56 rows (4.4e6) 29 / 30; one of 8000, 84 rows (2.8e6)
+// 30 / 24, 112 rows (3.8e6) 31 / 32; prompts of 100 tokens behind 50 (1.7e6)
+// 16 / 13, 200 behind 10 (3.7e6) 18 / 22, 400 behind 100 (10e6) 23 / 53.
 constexpr int kManyRows = 32;
-constexpr double kManyWork = 3e6;
+constexpr int kBeginning = 400;
+constexpr double kManyWork = 3.4e6;
 
 template <int D, bool WIDE>
 struct Geometry {
@@ -676,7 +679,8 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
   a.scale_log2 = (float)((double)call.scale * 1.4426950408889634);
   a.dtype = call.dtype;
 
-  const double work = (double)call.max_pages * c.page_size * c.kv_heads * call.batch * a.rows;
+  const double work = ((double)call.max_pages * c.page_size + kBeginning) * c.kv_heads *
+                      call.batch * a.rows;
   if (a.rows >= kManyRows && work >= kManyWork && c.head_dim <= 128)
     return launch_attention_rows(a, c.head_dim, c.format == RQ_KV_I8, scratch, st);
 

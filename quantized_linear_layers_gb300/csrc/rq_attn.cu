@@ -575,7 +575,16 @@ attn_kernel(const AttnArgs a) {
             join(first_of, 1, members, r, d, v[k], mx[k], sum[k]);
           else
             join(0, kJoin, groups, r, d, v[k], mx[k], sum[k]);
-          if (level == 0 && groups > 1) store_part(slot, r, d, v[k], mx[k], sum[k]);
+        }
+        if (level == 0 && groups > 1) {
+          // the joined row takes the place of the group's first member, whose
+          // maximum and sum every thread of the row has read by now
+          __syncthreads();
+#pragma unroll
+          for (int k = 0; k < kPieces; ++k) {
+            const int i = tid + k * G::kThreads, r = i / kVec, d = (i % kVec) * 4;
+            if (mine[k]) store_part(slot, r, d, v[k], mx[k], sum[k]);
+          }
         }
       }
     }

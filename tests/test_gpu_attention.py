@@ -346,3 +346,20 @@ def test_more_tiles_than_are_cut_by_length(rq, ctx, batch, new, heads, dtype):
     assert bool(((got[sel] - ref).abs() <= tol).all())
     assert bool((c.run(ctx).double() == got).all())
     assert rq.rq_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("heads,new,lengths", [
+    ((4, 1, 256), 1, [8000]), ((8, 1, 256), 1, [40000]), ((8, 1, 256), 6, [40000]),
+    ((4, 1, 128), 1, [40000]), ((3, 1, 64), 1, [60000])])
+def test_joins_of_more_than_one_level(rq, ctx, heads, new, lengths, fmt, dtype):
+    """One sequence in more than 8 parts: groups of neighbours are joined, then
+    the groups.  At head size 256 two warps share a row of the join."""
+    c = Case(rq, 90 + new, lengths, new, *heads, dtype, fmt, 64)
+    c.spoil()
+    got = c.run(ctx)
+    c.check(got)
+    for _ in range(4):
+        assert torch.equal(c.run(ctx), got)
+    assert rq.rq_get_device_status() == 0

@@ -429,10 +429,11 @@ rq_status rq_kv_read(const rq_kv_cache *cache_host, int dtype, const int64_t *sl
  * round: about 1e-6 of the result, 6e-6 for single tokens of dozens of
  * sequences of 60000); with f16 / bf16 activations q and the
  * probabilities are f16 operands (11 bits).
- * Partial results of split sequences live in scratch owned by ctx, which
- * grows on a call that needs more (allocating: call once at the largest
- * sizes of each type before a stream capture); they are joined in a fixed order, so equal
- * calls give equal bits.
+ * Partial results of split sequences live in scratch owned by ctx: about 61
+ * MB, allocated by the first call that needs it (which waits for the stream,
+ * and inside a stream capture gives RQ_ERR_ALLOC: call once before) and kept
+ * until ctx is destroyed, whatever later calls' sizes.  They are joined in a
+ * fixed order, so equal calls give equal bits.
  * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_QTYPE (dtype or format),
  * RQ_ERR_ALLOC, RQ_ERR_CUDA. */
 rq_status rq_cache_attention(rq_ctx *ctx, const rq_kv_cache *cache_host, int dtype,

@@ -9,6 +9,7 @@
 // instructions with f32 sums: an f32 operand (q, p vs) is split into a high
 // and a low f16 part, 22 bits in all, which occupy two rows of the tile.
 
+#include <algorithm>
 #include <cmath>
 #include <cstdlib>
 
@@ -560,8 +561,8 @@ attn_kernel(const AttnArgs a) {
       for (int level = 0; last && level < 2; ++level) {
         if (level == 1) {
           if (groups == 1) break;
-          last = arrive(a.counter + 2 * gridDim.x + (int64_t)seg.item * a.kv_heads + seg.head,
-                        (unsigned int)groups);
+          // (a CTA is the first of one shared segment at most)
+          last = arrive(a.counter + 2 * gridDim.x + part_at(0), (unsigned int)groups);
           if (!last) break;
         }
 #pragma unroll
@@ -702,10 +703,9 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
     grid = segments;
     if (grid > 0x7FFFFFFF) return RQ_ERR_SHAPE;
   } else {
-    const size_t part = sizeof(float) * 2 * (size_t)grid * kRows * (c.head_dim + 4);
-    const rq_status s = scratch->reserve(part, 2 * (size_t)grid + (size_t)segments, st);
+    const rq_status s = scratch->reserve(st);
     if (s != RQ_OK) return s;
-    a.part = scratch->part;
+    a.part = reinterpret_cast<float*>(scratch->part);
     a.counter = scratch->counter;
   }
   const unsigned g = (unsigned)grid;
@@ -717,42 +717,38 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
   }
 }
 
-rq_status AttnScratch::reserve(size_t part_bytes, size_t counters, cudaStream_t st) {
-  if (part_bytes > part_cap) {
-    if (part) cudaFree(part);
-    part = nullptr;
-    part_cap = 0;
-    void* p = nullptr;
-    if (cudaMalloc(&p, part_bytes) != cudaSuccess) {
-      cudaGetLastError();
-      return RQ_ERR_ALLOC;
-    }
-    part = static_cast<float*>(p);
-    part_cap = part_bytes;
+// Two sets of partial rows of the largest head for each of at most two CTAs an
+// SM, or what the other kernel needs; a counter of arrivals for every set of
+// rows, and one for the groups of the segment that begins with it.
+rq_status AttnScratch::reserve(cudaStream_t st) {
+  if (part != nullptr) return RQ_OK;
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(st, &capture) != cudaSuccess) return RQ_ERR_CUDA;
+  if (capture != cudaStreamCaptureStatusNone) return RQ_ERR_ALLOC;
+  const size_t ctas = 2 * (size_t)device_sm_count();
+  const size_t few = sizeof(float) * 2 * ctas * kRows * (256 + 4);
+  const size_t bytes = ((std::max(few, attention_rows_scratch()) + 255) & ~(size_t)255);
+  const size_t words = sizeof(unsigned int) * 4 * ctas;
+  void* p = nullptr;
+  if (cudaMalloc(&p, bytes + words) != cudaSuccess) {
+    cudaGetLastError();
+    return RQ_ERR_ALLOC;
   }
-  if (counters > counter_cap) {
-    if (counter) cudaFree(counter);
-    counter = nullptr;
-    counter_cap = 0;
-    void* p = nullptr;
-    if (cudaMalloc(&p, counters * sizeof(unsigned int)) != cudaSuccess) {
-      cudaGetLastError();
-      return RQ_ERR_ALLOC;
-    }
-    // every launch leaves its counters at zero again
-    if (cudaMemsetAsync(p, 0, counters * sizeof(unsigned int), st) != cudaSuccess) {
-      cudaFree(p);
-      return RQ_ERR_CUDA;
-    }
-    counter = static_cast<unsigned int*>(p);
-    counter_cap = counters;
+  // Every launch leaves its counters at zero again.  (Waited for, so that the
+  // next call may be on another stream.)
+  uint8_t* const at = static_cast<uint8_t*>(p);
+  if (cudaMemsetAsync(at + bytes, 0, words, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess) {
+    cudaFree(p);
+    return RQ_ERR_CUDA;
   }
+  part = at;
+  counter = reinterpret_cast<unsigned int*>(at + bytes);
   return RQ_OK;
 }
 
 void AttnScratch::release() {
   if (part) cudaFree(part);
-  if (counter) cudaFree(counter);
   *this = AttnScratch();
 }
 

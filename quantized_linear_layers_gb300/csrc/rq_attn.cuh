@@ -459,7 +459,9 @@ struct Cutter {
   }
 };
 
-// rq_attn_rows.cu: the kernel for many query rows per sequence.
+// rq_attn_rows.cu: the kernel for many query rows per sequence, and the bytes
+// of scratch that it needs at most.
+size_t attention_rows_scratch();
 rq_status launch_attention_rows(AttnArgs a, int head_dim, bool i8, AttnScratch* scratch,
                                 cudaStream_t st);
 

@@ -1163,7 +1163,19 @@ rq_status launch_rows(const AttnArgs& a, unsigned grid, cudaStream_t st) {
   return launch_kernel(join_rows_kernel<D>, dim3(grid * (kRows / kJoinBlock<D>)), dim3(256), 0, st, a);
 }
 
+// Partial rows, behind them, per CTA, the segment it begins for several, and
+// the sums that left TMEM.
+size_t part_bytes(size_t grid, int head_dim) {
+  return sizeof(float) * 2 * grid * kRows * (head_dim + 4);
+}
+size_t share_bytes(size_t grid) { return (sizeof(SharedSegment) * grid + 15) & ~(size_t)15; }
+
 }  // namespace
+
+size_t attention_rows_scratch() {
+  const size_t grid = (size_t)device_sm_count();
+  return part_bytes(grid, 128) + share_bytes(grid) + sizeof(float) * grid * kRows * 128;
+}
 
 rq_status launch_attention_rows(AttnArgs a, int head_dim, bool i8, AttnScratch* scratch,
                                 cudaStream_t st) {
@@ -1175,20 +1187,17 @@ rq_status launch_attention_rows(AttnArgs a, int head_dim, bool i8, AttnScratch* 
   if (segments > 0x7FFFFFFF) return RQ_ERR_SHAPE;
   a.direct = !Cutting::cuts(a, items);
   const bool split = a.dtype == RQ_F32;
-  // partial rows, behind them, per CTA, the segment it begins for several, and
-  // the sums that left TMEM
-  const size_t part = a.direct ? 0 : sizeof(float) * 2 * (size_t)grid * kRows * (head_dim + 4);
-  const size_t shares = a.direct ? 0 : ((sizeof(SharedSegment) * (size_t)grid + 15) & ~(size_t)15);
-  const size_t sums = split ? sizeof(float) * (size_t)grid * kRows * head_dim : 0;
-  if (part + shares + sums > 0) {
-    const rq_status s = scratch->reserve(part + shares + sums, 0, st);
+  if (!a.direct || split) {
+    const rq_status s = scratch->reserve(st);
     if (s != RQ_OK) return s;
-    uint8_t* at = reinterpret_cast<uint8_t*>(scratch->part);
+    uint8_t* at = scratch->part;
     if (!a.direct) {
-      a.part = scratch->part;
-      a.shares = reinterpret_cast<SharedSegment*>(at + part);
+      a.part = reinterpret_cast<float*>(at);
+      at += part_bytes((size_t)grid, head_dim);
+      a.shares = reinterpret_cast<SharedSegment*>(at);
+      at += share_bytes((size_t)grid);
     }
-    a.flushed = reinterpret_cast<float4*>(at + part + shares);
+    a.flushed = reinterpret_cast<float4*>(at);
   }
   const unsigned g = (unsigned)grid;
   if (head_dim == 64) {

@@ -170,13 +170,13 @@ struct AttnCall {
   float scale;
 };
 // Scratch of split sequences: partial rows, and the arrival counters of the
-// joins, at zero between launches.  Used on one stream at a time.
+// joins, at zero between launches.  Allocated once, at a size that the SM count
+// bounds, so that it never moves under a captured graph.  Used on one stream at
+// a time.
 struct AttnScratch {
-  float* part = nullptr;
-  size_t part_cap = 0;
+  uint8_t* part = nullptr;
   unsigned int* counter = nullptr;
-  size_t counter_cap = 0;
-  rq_status reserve(size_t part_bytes, size_t counters, cudaStream_t st);
+  rq_status reserve(cudaStream_t st);
   void release();
 };
 rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cudaStream_t st);

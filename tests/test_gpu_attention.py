@@ -363,3 +363,56 @@ def test_joins_of_more_than_one_level(rq, ctx, heads, new, lengths, fmt, dtype):
     for _ in range(4):
         assert torch.equal(c.run(ctx), got)
     assert rq.rq_get_device_status() == 0
+
+
+def test_scratch_stays_where_a_captured_graph_uses_it(rq):
+    """Single tokens are captured; then the context serves a prompt of many
+    rows, and what the allocator has to give is overwritten."""
+    own = rq.Context()
+    c = Case(rq, 51, [6000, 100], 1, 14, 2, 64, "f32", 0, 64)
+    cache = rq.KVCache.from_tensors(c.k.cuda(), c.v.cuda(), c.ks.cuda(), c.vs.cuda())
+    q, table, n = c.q.cuda(), c.table.cuda(), c.lengths.cuda()
+    out = torch.empty_like(q)
+
+    def call():
+        own.rq_cache_attention(cache, q, out, table, n, 2, 1, 14, c.scale)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            call()
+    prompt = Case(rq, 52, [3000, 700], 40, 28, 4, 128, "f32", 0, 64)
+    prompt.check(prompt.run(own))
+    batch = Case(rq, 53, [500 + 7 * i for i in range(90)], 1, 32, 8, 128, "bf16", 0, 64)
+    batch.run(own)
+    spoiled = [torch.full((1 << 24,), float("nan"), device="cuda") for _ in range(4)]
+    for i in range(2):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check(out.cpu())
+    assert all(bool(torch.isnan(x).all()) for x in spoiled)
+    own.close()
+
+
+def test_first_call_inside_a_capture_is_refused(rq):
+    own = rq.Context()
+    c = Case(rq, 54, [70], 1, 4, 2, 64, "f32", 0, 16)
+    cache = rq.KVCache.from_tensors(c.k.cuda(), c.v.cuda(), c.ks.cuda(), c.vs.cuda())
+    q, table, n = c.q.cuda(), c.table.cuda(), c.lengths.cuda()
+    out = torch.zeros_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(rq.RqError) as e:
+            own.rq_cache_attention(cache, q, out, table, n, 1, 1, 4, c.scale)
+        assert e.value.status == 5
+        out += 1.0                               # the capture goes on
+    graph.replay()
+    torch.cuda.synchronize()
+    assert bool((out == 1.0).all())
+    c.check(c.run(own))
+    own.close()

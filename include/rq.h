@@ -442,6 +442,13 @@ rq_status rq_cache_attention(rq_ctx *ctx, const rq_kv_cache *cache_host, int dty
                              int max_pages, const int32_t *length,
                              const uint64_t *tree, float scale, rq_stream_t stream);
 
+/* Host-side counters: calls of rq_cache_attention on ctx that launched the
+ * kernel for few query rows per kv head, and the one for many (sizes choose;
+ * the results of both keep to what is stated above).  Either pointer may be
+ * NULL.  Errors: RQ_ERR_NULL (ctx). */
+rq_status rq_ctx_attention_launches(const rq_ctx *ctx, int64_t *few_rows_host,
+                                    int64_t *many_rows_host);
+
 /* ------------------------------------- verification of drafted tokens -- */
 
 /* Keep or reject a chain of drafted tokens per sequence, and draw the next

@@ -76,6 +76,7 @@ _SIGS = {
     "rq_kv_read": ([_vp, _i32, _vp, _vp, _vp, _i32, _vp], _i32),
     "rq_cache_attention": ([_vp, _vp, _i32, _vp, _i64, _vp, _i32, _i32, _i32, _vp, _i32, _vp,
                             _vp, ctypes.c_float, _vp], _i32),
+    "rq_ctx_attention_launches": ([_vp, _vp, _vp], _i32),
     "rq_verify_chain": ([_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp], _i32),
     "rq_verify_tree": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp], _i32),
 }
@@ -450,6 +451,14 @@ class Context:
                                        _ptr(out), batch, new_tokens, q_heads, _ptr(page_table),
                                        max_pages, _ptr(length), _ptr(tree), scale,
                                        _stream(stream)), "rq_cache_attention")
+
+    def attention_launches(self):
+        """How many rq_cache_attention calls launched the kernel for few query
+        rows, and the one for many."""
+        few, many = _i64(), _i64()
+        _check(_lib.rq_ctx_attention_launches(self._h, ctypes.byref(few), ctypes.byref(many)),
+               "rq_ctx_attention_launches")
+        return few.value, many.value
 
     TRACE_KINDS = ("gemv", "absmax", "quant", "gemm", "wcache")
 

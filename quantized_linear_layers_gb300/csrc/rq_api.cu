@@ -765,6 +765,14 @@ rq_status rq_cache_attention(rq_ctx* ctx, const rq_kv_cache* cache, int dtype, c
   return launch_cache_attention(call, &ctx->attn, reinterpret_cast<cudaStream_t>(stream));
 }
 
+rq_status rq_ctx_attention_launches(const rq_ctx* ctx, int64_t* few_rows_host,
+                                    int64_t* many_rows_host) {
+  if (ctx == nullptr) return RQ_ERR_NULL;
+  if (few_rows_host) *few_rows_host = ctx->attn.few_rows;
+  if (many_rows_host) *many_rows_host = ctx->attn.many_rows;
+  return RQ_OK;
+}
+
 // ---------------------------------------------- verification of drafts --
 
 static rq_status check_verify(const int32_t* token, const float* p, const float* u,

@@ -691,8 +691,11 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
 
   const double work = ((double)call.max_pages * c.page_size + kBeginning) * c.kv_heads *
                       call.batch * a.rows;
-  if (a.rows >= kManyRows && work >= kManyWork && c.head_dim <= 128)
+  if (a.rows >= kManyRows && work >= kManyWork && c.head_dim <= 128) {
+    ++scratch->many_rows;
     return launch_attention_rows(a, c.head_dim, c.format == RQ_KV_I8, scratch, st);
+  }
+  ++scratch->few_rows;
 
   const int64_t items = (int64_t)call.batch * a.row_tiles;
   const int64_t segments = items * c.kv_heads;

@@ -176,6 +176,7 @@ struct AttnCall {
 struct AttnScratch {
   uint8_t* part = nullptr;
   unsigned int* counter = nullptr;
+  int64_t few_rows = 0, many_rows = 0;  // launches of either kernel
   rq_status reserve(cudaStream_t st);
   void release();
 };

@@ -1,0 +1,159 @@
+"""GPU: what rq_cache_attention promises, on the kernel for few query rows per
+kv head and on the tcgen05 kernel for many alike.  Which one runs is a matter
+of sizes, the room of the page table among them; every test here asserts it."""
+import pytest
+import torch
+
+from serving_util import gen
+from test_gpu_attention import Case, random_tree, signed
+
+pytestmark = pytest.mark.gpu
+FORMS = pytest.mark.parametrize("many", [False, True], ids=["few", "many"])
+TYPES = [("f32", 0), ("f32", 1), ("f16", 0), ("f16", 1), ("bf16", 0), ("bf16", 1)]
+
+
+@pytest.fixture(scope="module")
+def rq():
+    import quantized_linear_layers_gb300 as rq
+    return rq
+
+
+@pytest.fixture(scope="module")
+def ctx(rq):
+    c = rq.Context()
+    yield c
+    c.close()
+
+
+def run(ctx, c, many, q=None):
+    """The case's output from the kernel for many rows (a table with room for
+    the work that it starts at) or from the other (the table as it is)."""
+    if many:
+        hk = c.k.shape[1]
+        rows = c.new * (c.hq // hk)
+        room = -(-3400000 // (hk * len(c.lengths) * rows * c.page)) + 1
+        if c.table.shape[1] < room:
+            table = torch.full((len(c.lengths), room), -9, dtype=torch.int32)
+            table[:, :c.table.shape[1]] = c.table
+            c.table = table
+    few0, many0 = ctx.attention_launches()
+    got = c.run(ctx, q=q)
+    few1, many1 = ctx.attention_launches()
+    assert (few1 - few0, many1 - many0) == ((0, 1) if many else (1, 0))
+    return got
+
+
+@FORMS
+@pytest.mark.parametrize("dtype,fmt", TYPES)
+@pytest.mark.parametrize("heads", [(6, 2, 64), (10, 2, 128)], ids=str)
+@pytest.mark.parametrize("mask,new,page", [("chain", 13, 16), ("tree", 29, 32),
+                                           ("prompt", 77, 256), ("prompt", 70, 128)])
+def test_types_and_masks(rq, ctx, mask, new, page, heads, dtype, fmt, many):
+    lengths = [130, 0, -1, 61]
+    tree = random_tree(gen(new), len(lengths), new) if mask == "tree" else None
+    c = Case(rq, 200 + new, lengths, new, *heads, dtype, fmt, page, tree=tree)
+    c.spoil()
+    c.check(run(ctx, c, many))
+    assert rq.rq_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,fmt", [("f32", 1), ("bf16", 0), ("f16", 1)])
+@pytest.mark.parametrize("new,heads", [
+    (32, (1, 1, 64)), (33, (2, 2, 128)), (64, (1, 1, 128)), (16, (7, 1, 64)), (18, (7, 1, 128)),
+    (127, (1, 1, 128)), (128, (1, 1, 64)), (129, (1, 1, 128)), (51, (5, 1, 64)),
+    (64, (4, 1, 128)), (257, (1, 1, 64)), (39, (10, 1, 128)), (55, (7, 1, 64))])
+def test_partial_tiles(rq, ctx, new, heads, dtype, fmt):
+    """32 .. 390 rows in tiles of 128, two to a segment."""
+    c = Case(rq, 300 + new, [100, 7], new, *heads, dtype, fmt, 64)
+    c.spoil()
+    c.check(run(ctx, c, True))
+    assert rq.rq_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,fmt", [("f32", 1), ("f16", 0), ("bf16", 1)])
+@pytest.mark.parametrize("lengths,new,heads,tree", [
+    ([1500] * 30, 8, (16, 4, 64), False),          # whole segments, a thread block each
+    ([1500] * 35, 16, (4, 2, 128), True),          # equal parts
+    ([2900, 40, 1100, 0, 17], 24, (6, 2, 128), True),   # runs of cost
+    ([290 - 5 * i for i in range(50)], 9, (16, 4, 64), False),   # several whole segments
+    ([900], 600, (2, 1, 128), False), ([60, 700], 333, (4, 2, 64), False)])   # prompts
+def test_cuts(rq, ctx, lengths, new, heads, tree, dtype, fmt):
+    words = random_tree(gen(3), len(lengths), new) if tree else None
+    c = Case(rq, 400 + new, lengths, new, *heads, dtype, fmt, 32, tree=words)
+    c.spoil()
+    got = run(ctx, c, True)
+    c.check(got)
+    assert torch.equal(run(ctx, c, True), got)
+    assert rq.rq_get_device_status() == 0
+
+
+@FORMS
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_that_see_nothing_are_zero(rq, ctx, d, dtype, many):
+    new = 20
+    tree = torch.zeros((2, new), dtype=torch.int64)
+    tree[1, 4] = signed(1 << 2)
+    c = Case(rq, 5, [0, 0], new, 14, 2, d, dtype, 0, 16, tree=tree)
+    got = run(ctx, c, many)
+    c.check(got)
+    got[1, 4] = 0
+    assert not got.any()
+
+
+@FORMS
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_bits_past_the_new_tokens_are_ignored(rq, ctx, dtype, many):
+    new = 11
+    words = [(2 << i) - 1 for i in range(new)]
+    c = Case(rq, 9, [50], new, 12, 2, 64, dtype, 1, 16, tree=torch.tensor([words]))
+    want = run(ctx, c, many)
+    c.tree = torch.tensor([[signed(w | (1 << 64) - (1 << new + i % 3)) for i, w in enumerate(words)]])
+    assert torch.equal(run(ctx, c, many), want)
+
+
+@FORMS
+@pytest.mark.parametrize("dtype,fmt", [("f32", 0), ("f16", 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_chain_of_drafts_is_a_tree_of_one_branch(rq, ctx, d, dtype, fmt, many):
+    new = 17
+    c = Case(rq, 3, [333, 20], new, 14, 2, d, dtype, fmt, 64)
+    chain = run(ctx, c, many)
+    c.tree = torch.tensor([[(2 << i) - 1 for i in range(new)]] * 2, dtype=torch.int64)
+    assert torch.equal(run(ctx, c, many), chain)
+    c.check(chain)
+
+
+@FORMS
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_not_finite_queries_stay_in_their_rows(rq, ctx, d, dtype, many):
+    c = Case(rq, 8, [100], 9, 8, 2, d, dtype, 0, 16)
+    want = run(ctx, c, many)
+    c.q[0, 1, 3, 5] = float("inf")
+    c.q[0, 2, 0, 0] = float("nan")
+    c.q[0, 8, 7, d - 1] = float("-inf")
+    got = run(ctx, c, many)
+    bad = torch.isnan(got).all(-1)[0]
+    assert bad[1, 3] and bad[2, 0] and bad[8, 7] and int(bad.sum()) == 3
+    same = ~bad[None, ..., None].expand_as(got)
+    assert torch.equal(got[same], want[same])
+
+
+@FORMS
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_strided_q(rq, ctx, dtype, many):
+    c = Case(rq, 21, [200, 30], 12, 6, 2, 128, dtype, 0, 16)
+    want = run(ctx, c, many)
+    wide = torch.randn((2, 12, 10, 128)).to(c.q.dtype).cuda()
+    wide[:, :, 2:8] = c.q.cuda()
+    assert torch.equal(run(ctx, c, many, q=wide[:, :, 2:8]), want)
+
+
+@FORMS
+@pytest.mark.parametrize("q_scale", [1e-12, 30.0, 1e6])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_ranges_of_q(rq, ctx, dtype, q_scale, many):
+    c = Case(rq, 77, [300, 90], 9, 8, 2, 64, dtype, 1, 32, q_scale=q_scale)
+    c.vs *= torch.exp(torch.randn(c.vs.shape, generator=gen(1)))
+    c.check(run(ctx, c, many))

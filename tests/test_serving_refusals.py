@@ -177,3 +177,7 @@ def test_binding_refuses_tensors_that_are_not_rows(rq):
         rq.QKParams(2, 1, 64, q_weight=torch.ones(32))
     with pytest.raises(rq.RqError):
         rq.QKParams(2, 1, 64, cos=torch.ones(8, 32), sin=torch.ones(8, 16))
+
+
+def test_attention_counters_want_a_context(rq):
+    assert rq.lib().rq_ctx_attention_launches(NULL, NULL, NULL) == 1

@@ -411,8 +411,9 @@ rq_status rq_kv_read(const rq_kv_cache *cache_host, int dtype, const int64_t *sl
  *   tree != NULL:  new token j where bit j of tree[b, i] is set (the draft
  *                  itself and those before it on its path, say); bits from
  *                  new_tokens on are ignored.  new_tokens <= 64.
- * A row that sees nothing gives zeros.  length[b] < 0 marks an unused
- * sequence: zeros.  A row whose q is not finite gives NaN.
+ * A row that sees nothing gives zeros, whatever its q.  length[b] < 0 marks an
+ * unused sequence: zeros.  Any other row whose q is not finite gives NaN; so
+ * may one whose scores (in powers of two: 1.45 scale q . k) leave f32's range.
  *   q: [batch * new_tokens][q_heads][head_dim] of dtype, consecutive tokens
  *     q_stride elements apart.   out: the same shape, dense.
  *   page_table: int32 [batch][max_pages]; place p of sequence b is offset

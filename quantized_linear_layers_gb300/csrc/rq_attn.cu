@@ -234,7 +234,7 @@ attn_kernel(const AttnArgs a) {
       if (nseg == 0 && D == 256)
         for (int i = 0; i < S - 1; ++i) load_one();
       float x[D / 16][4];
-      float top = 0.0f;
+      uint32_t top = 0u;  // largest magnitude, as bits: a NaN counts as above infinity
       if (a.dtype == RQ_F32) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -276,21 +276,22 @@ attn_kernel(const AttnArgs a) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (!live) x[i][k] = 0.0f;
-          top = fmaxf(top, fabsf(x[i][k]));
+          top = max(top, __float_as_uint(x[i][k]) & 0x7FFFFFFFu);
         }
       }
       // the row times a power of two, so that its f16 parts lie well inside
-      // f16's range: largest entry in [2^13, 2^14)
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+      // f16's range: largest entry in [2^13, 2^14).  A row that is not finite
+      // becomes NaN, and so do its scores; c stays finite, so that what the
+      // row does not see weighs 0 all the same.
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
       int e = 0;
-      if (top > 0.0f && top <= 3.4e38f) {
-        e = 13 - (int)((__float_as_uint(top) >> 23) & 0xFFu) + 127;
+      if (top > 0u) {
+        e = 13 - (int)(top >> 23) + 127;
         e = e < -126 ? -126 : e > 100 ? 100 : e;
       }
-      const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-      c = fmaxf(a.scale_log2 / up, 0x1p-126f);
-      if (!(top <= 3.4e38f)) c = NAN;  // an infinity in q
+      const float up = top < 0x7F800000u ? __uint_as_float((uint32_t)(e + 127) << 23) : NAN;
+      c = fmaxf(a.scale_log2 / up, 0x1p-126f);  // (of a NaN: 2^-126)
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
         qa[i][0] = split_half2(x[i][0] * up, x[i][1] * up, qa[i][1]);

@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
           uint32_t most = max(top[0], __shfl_xor_sync(0xFFFFFFFFu, top[0], 1));
           if (kLg == 3) most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
           // times a power of two: the largest entry in [2^13, 2^14); a row
-          // that is not finite becomes NaN
+          // that is not finite becomes NaN, and so do its scores
           int e = 0;
           if (most > 0u) {
             e = 13 - (int)(most >> 23) + 127;
@@ -525,7 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
             }
           }
         }
-        c = c == c ? fmaxf(a.scale_log2 / c, 0x1p-126f) : NAN;
+        // (2^-126 where c is a NaN: what the row does not see weighs 0 all the same)
+        c = fmaxf(a.scale_log2 / c, 0x1p-126f);
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&tail.q_full[w]));

@@ -157,3 +157,50 @@ def test_ranges_of_q(rq, ctx, dtype, q_scale, many):
     c = Case(rq, 77, [300, 90], 9, 8, 2, 64, dtype, 1, 32, q_scale=q_scale)
     c.vs *= torch.exp(torch.randn(c.vs.shape, generator=gen(1)))
     c.check(run(ctx, c, many))
+
+
+@FORMS
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("bad", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_that_see_nothing_are_zero_whatever_their_queries(rq, ctx, d, bad, dtype, many):
+    """Unused sequences, and rows under empty mask words, of queries that nobody
+    wrote; rows between them that see something are NaN or not by their own."""
+    new = 20
+    tree = torch.zeros((3, new), dtype=torch.int64)
+    tree[2, 5] = tree[2, 6] = 1
+    c = Case(rq, 5, [0, -1, 0], new, 14, 2, d, dtype, 0, 16, tree=tree)
+    finite = c.q[2, 5].clone()
+    c.q[:] = float(bad)
+    c.q[2, 5] = finite
+    got = run(ctx, c, many)
+    assert bool(torch.isnan(got[2, 6]).all()) and bool(torch.isfinite(got[2, 5]).all())
+    got[2, 5:7] = 0
+    assert not got.any()
+    c.tree = None                      # every row sees the tokens before it
+    c.lengths[0] = -3
+    got = run(ctx, c, many)
+    assert not got[:2].any()
+    assert bool(torch.isnan(got[2, :5]).all()) and bool(torch.isnan(got[2, 6:]).all())
+    assert bool(torch.isfinite(got[2, 5]).all())
+
+
+def test_largest_finite_queries(rq, ctx):
+    """Up to the largest f32: one key takes all, and nothing is NaN.  (The kernel
+    for few rows takes differences of scores before it scales them; the other
+    one's scores have to stay in f32's range, as the header says.)"""
+    c = Case(rq, 6, [60], 9, 8, 2, 64, "f32", 1, 16)
+    c.q[0, 4, 2] *= 3.4028e38 / float(c.q[0, 4, 2].abs().max())
+    c.q[0, 5, 1] = torch.finfo(torch.float32).max
+    assert bool(torch.isfinite(c.q).all()) and float(c.q[0, 4, 2].abs().max()) > 3.4e38
+    assert bool(torch.isfinite(run(ctx, c, False)).all())
+
+
+def test_one_head_of_256_keeps_the_same_rules(rq, ctx):
+    tree = torch.zeros((2, 3), dtype=torch.int64)
+    c = Case(rq, 7, [0, -1], 3, 2, 1, 256, "bf16", 0, 16, tree=tree)
+    for bad in ("nan", "inf"):
+        c.q[:] = float(bad)
+        assert not run(ctx, c, False).any()
+    c.tree = None
+    assert bool(torch.isnan(run(ctx, c, False)[0]).all())

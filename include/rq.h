@@ -317,9 +317,10 @@ typedef enum { RQ_F32 = 0, RQ_F16 = 1, RQ_BF16 = 2 } rq_dtype;
  * largest finite magnitude, A' = max(A, 2^-100) and top the format's largest
  * value (448 or 127):  scale = A' / top,  code = rn(x * (top * (1 / A'))),
  * each operation one correctly rounded f32 operation and rn the round to
- * nearest even into the format, limited to +-top.  A value that is not finite takes +-top with its own
- * sign, so the NaN codes of E4M3 are never written (they must not be in rows
- * that are read). */
+ * nearest even into the format, limited to +-top.  A value that is not finite
+ * takes +-top with its own sign, so the NaN codes of E4M3 are never written.
+ * (A caller who fills a cache otherwise leaves none in rows that a query sees;
+ * in rows that are not seen they do no harm.) */
 typedef enum { RQ_KV_E4M3 = 0, RQ_KV_I8 = 1 } rq_kv_format;
 
 /* A paged cache, described by the caller, who owns its memory:

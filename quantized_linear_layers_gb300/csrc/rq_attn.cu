@@ -357,16 +357,25 @@ attn_kernel(const AttnArgs a) {
                     (s[1][0] + s[1][2]) * kb.x, (s[1][1] + s[1][3]) * kb.y};
       float vv[4] = {va.x, va.y, vb.x, vb.y};
       if (!all) {
-        // what lies past the last place: no scores, and zeros in place of V
-        // (its codes could be anything, and 0 * NaN is not 0)
-        if (first + kKeys > kv) {
+        // what a row does not see: no scores; V's codes there may be anything,
+        // and 0 * NaN is not 0: zeros past the last place, no NaN before it
+        if (!I8 || first + kKeys > kv) {
           const int keys = kv > first ? kv - first : 0;
-          for (int i = keys * (D / 16) + lane; i < kKeys * (D / 16); i += 32) {
+          for (int i = (I8 ? keys * (D / 16) : 0) + lane; i < kKeys * (D / 16); i += 32) {
             const int r = i / (D / 16), ch = i % (D / 16);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             vd + (ch / (G::kPanel / 16)) * (kKeys * G::kPanel) +
-                             swizzled<G::kPanel>(r, ch % (G::kPanel / 16))),
-                         "r"(0)
+            const uint32_t at = vd + (ch / (G::kPanel / 16)) * (kKeys * G::kPanel) +
+                                swizzled<G::kPanel>(r, ch % (G::kPanel / 16));
+            uint32_t v[4] = {0u, 0u, 0u, 0u};
+            if (!I8 && r < keys) {
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                           : "r"(at)
+                           : "memory");
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[k] = without_nan(v[k]);
+            }
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]),
+                         "r"(v[1]), "r"(v[2]), "r"(v[3])
                          : "memory");
           }
           __syncwarp();

@@ -61,6 +61,14 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t two) {
   return h;
 }
 
+// Four E4M3 codes, its NaN (0x7F, 0xFF) made zero.  A V row that some query
+// rows see and others do not takes part in the product with weights of 0 for
+// these, and 0 * NaN is not 0.
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) {
+  const uint32_t t = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // a byte's top bit: NaN
+  return w & ~(t | (t - (t >> 7)));
+}
+
 __device__ __forceinline__ uint32_t minus_1152(uint32_t h) {
   const uint32_t bias = 0x64806480u;
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h),

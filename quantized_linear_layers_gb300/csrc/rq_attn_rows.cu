@@ -838,11 +838,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         if (off[n] >= 0) c[n] = ldg_nc_v4(codes + off[n]);
       }
     };
-    auto convert = [&](const uint4 (&codes)[N], uint32_t base) {
+    // the segment's places that every row sees come before `seen`
+    int seen = cutter.length(cutter.sequence(seg.item));
+    auto convert = [&](const uint4 (&codes)[N], uint32_t base, bool drop) {
 #pragma unroll
       for (int n = 0; n < N; ++n) {
         const int r = row_a + n * kRowStep;
-        const uint32_t words[4] = {codes[n].x, codes[n].y, codes[n].z, codes[n].w};
+        uint32_t words[4] = {codes[n].x, codes[n].y, codes[n].z, codes[n].w};
+        if (!I8 && drop) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) words[i] = without_nan(words[i]);
+        }
         uint32_t h[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) codes_in_order<I8>(words[i], h[2 * i], h[2 * i + 1]);
@@ -866,12 +872,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
       const uint32_t buf = units & 1u, turn = (units >> 1) ^ 1u;
       const uint32_t kb = kv_base + buf * (2 * L::kB);
       wait(ok, tail.k_free[buf], turn, a.error);
-      convert(kc, kb);
+      convert(kc, kb, false);
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&tail.k_full[buf]));
       // the next unit's codes are fetched as soon as this one's have left
       // their registers
+      const bool drop = (u + 1) * kKeys > seen;  // of V: new tokens' codes
       bool more = true;
       if (++u < seg.end) {
         pages.step(a, seg, u, lane);
@@ -880,6 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         if (more) {
           cutter.next(seg);
           u = seg.first;
+          seen = cutter.length(cutter.sequence(seg.item));
           pages.open(a, seg, u, lane);
         }
       }
@@ -888,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         fetch(kc, a.k);
       }
       wait(ok, tail.v_free[buf], turn, a.error);
-      convert(vc, kb + L::kB);
+      convert(vc, kb + L::kB, drop);
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&tail.v_full[buf]));

@@ -204,3 +204,56 @@ def test_one_head_of_256_keeps_the_same_rules(rq, ctx):
         assert not run(ctx, c, False).any()
     c.tree = None
     assert bool(torch.isnan(run(ctx, c, False)[0]).all())
+
+
+def spoil_codes(c, sequence, place):
+    """NaN codes of both signs at one place of the cache."""
+    page, offset = int(c.table[sequence, place // c.page]), place % c.page
+    for codes in (c.k, c.v):
+        row = codes.view(torch.uint8)[page, :, offset]
+        row[:, 0::3] = 0x7F
+        row[:, 1::3] = 0xFF
+
+
+HIDDEN = [("f32", 64), ("f32", 128), ("f16", 64), ("bf16", 128)]
+
+
+@FORMS
+@pytest.mark.parametrize("dtype,d", HIDDEN)
+def test_codes_under_cleared_bits_do_not_reach_the_output(rq, ctx, d, dtype, many):
+    """NaN codes where drafts were never written: under bits that no row sets,
+    and under bits that some rows set, whose own output they may spoil."""
+    new = 22
+    words = [((1 << new) - 1) & ~(1 << 3) & ~(1 << 17) for _ in range(new)]
+    c = Case(rq, 11, [100, 0, 63], new, 14, 2, d, dtype, 0, 16, tree=torch.tensor([words] * 3))
+    want = run(ctx, c, many)
+    c.check(want)
+    for b, n in enumerate(c.lengths.tolist()):
+        spoil_codes(c, b, n + 3)
+        spoil_codes(c, b, n + 17)
+    assert torch.equal(run(ctx, c, many), want)
+    c.tree[:, 9] |= 1 << 17
+    got = run(ctx, c, many)
+    got[:, 9] = want[:, 9]
+    assert torch.equal(got, want)
+
+
+@FORMS
+@pytest.mark.parametrize("dtype,d", HIDDEN)
+@pytest.mark.parametrize("new", [21, 75])
+def test_codes_of_later_tokens_do_not_reach_earlier_ones(rq, ctx, new, d, dtype, many):
+    c = Case(rq, 12, [100, 0], new, 10, 2, d, dtype, 0, 32)
+    want = run(ctx, c, many)
+    for b, n in enumerate(c.lengths.tolist()):
+        for place in (n + new - 1, n + new - 4):
+            spoil_codes(c, b, place)
+    got = run(ctx, c, many)
+    assert torch.equal(got[:, :new - 4], want[:, :new - 4])
+
+
+def test_hidden_codes_at_head_size_256(rq, ctx):
+    c = Case(rq, 13, [50, 0], 5, 4, 1, 256, "f32", 0, 16)
+    want = run(ctx, c, False)
+    for b, n in enumerate(c.lengths.tolist()):
+        spoil_codes(c, b, n + 3)
+    assert torch.equal(run(ctx, c, False)[:, :3], want[:, :3])

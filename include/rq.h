@@ -423,8 +423,9 @@ rq_status rq_kv_read(const rq_kv_cache *cache_host, int dtype, const int64_t *sl
  *     page 0, places past max_pages pages are not seen; both record
  *     RQ_ERR_INDEX.
  *   scale: finite, above 0.   q_heads: a multiple of kv_heads.
- * What lies in the cache behind a sequence's places, or under a cleared
- * bit, does not reach the output.
+ * What lies in the cache behind a sequence's places, at later new tokens or
+ * under a cleared bit, does not reach a row's output: its bits stay whatever
+ * the codes and scales there are.
  * Accuracy: with f32 activations q, the probabilities and both products are
  * carried to about 21 bits (each f32 operand split into two f16 parts, codes
  * exact in f16, f32 sums, whose additions the tensor cores cut off rather than

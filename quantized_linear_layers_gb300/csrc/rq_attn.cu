@@ -313,7 +313,7 @@ attn_kernel(const AttnArgs a) {
             ? min(kv, len + (int)quotient((uint32_t)(rt * kRows), a.by_group) + 1)
             : len;
     float m = -INFINITY, l = 0.0f;
-    float vref = 0x1p-112f;  // power of two at or above every vs so far
+    float vref = 0x1p-112f;  // power of two at or above every vs that the row has seen
 
     for (int u = seg.first + warp, end = seg.end; u < end; u += W) {
       copy_wait<S - 2>();
@@ -406,7 +406,9 @@ attn_kernel(const AttnArgs a) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           if (vv[k] >= 0.0f && vv[k] <= 1e37f) vt = max(vt, __float_as_uint(vv[k]));  // no NaN, Inf
-        vt = __reduce_max_sync(0xFFFFFFFFu, vt);
+        // of this row alone: another row's keys may be hidden from it
+        vt = max(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, 1));
+        vt = max(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, 2));
         const float al = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
         float f = al;
         const uint32_t vbits = __float_as_uint(vref);

@@ -80,8 +80,10 @@ struct Flag {
 using Cutting = Cutter<kRows, kKeys, 1, 8, 8, 6, 28>;
 
 struct RowsTail {
-  float ks[kScales][kKeys], vs[kScales][kKeys];  // vs relative to vref, times kUp
-  float vref[kScales];  // negative: not all of vs are finite
+  // vs relative to vref, times kUp, and vr as they are
+  float ks[kScales][kKeys], vs[kScales][kKeys], vr[kScales][kKeys];
+  float vref[kScales];   // of all keys so far; negative: a scale is out of range
+  float vmost[kScales];  // largest scale of the unit
   uint64_t q_full[2], k_full[2], k_free[2], v_full[2], v_free[2], sc_full[kScales];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2], drained[2];
   uint32_t tmem;
@@ -299,6 +301,17 @@ __device__ __forceinline__ float q_value(bool f16, const uint32_t (&words)[WORDS
   }
   return __uint_as_float((i & 1) ? w & 0xFFFF0000u : w << 16);
 }
+
+// Value scales are kept relative to a power of two: four times the next one
+// above the largest so far, so that it seldom moves; and kUp over it.
+constexpr float kMostScale = 1e37f;  // larger ones, and NaN, do not count
+__device__ __forceinline__ float next_scale(float v) {
+  return __uint_as_float((__float_as_uint(v) & 0x7F800000u) + (2u << 23));
+}
+__device__ __forceinline__ float up_over(float vref) {
+  return __uint_as_float(((254u + 7u) << 23) - __float_as_uint(vref));
+}
+
 // A thread's wait for a barrier phase; after one wait has run out, no further
 // one is made, so that every role comes to its end.
 __device__ __forceinline__ void wait_one(bool& ok, const uint64_t& bar, uint32_t parity,
@@ -590,6 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
           }
           const int p0 = (seg.first + u) * kKeys;
           const bool edge = p0 + kKeys > sure;
+          // The row's value scales are kept relative to a power of two above
+          // those that it sees: for all rows alike but for those that do not
+          // see the unit that raised it.
+          float need = tail.vmost[sc];
           if (edge) {
             // bit k: key k of the unit is seen
             const int before = len - p0;  // keys that every row sees
@@ -610,6 +627,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
               if (!((s0 >> i) & 1u)) x[i] = -INFINITY;
               if (!((s1 >> i) & 1u)) x[32 + i] = -INFINITY;
             }
+            // (looked at one by one only where the unit raises the power of two:
+            // a bf16 prompt of 110 us takes 137 with the loop in every such unit)
+            const bool raises = __any_sync(0xFFFFFFFFu, need > vref);
+            need = 0.0f;
+            if (raises) {
+#pragma unroll 1
+              for (int i = 0; i < kKeys; i += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(&tail.vr[sc][i]);
+                const uint32_t bits4 = (uint32_t)(see >> i);
+                if ((bits4 & 1u) && v.x <= kMostScale) need = fmaxf(need, v.x);
+                if ((bits4 & 2u) && v.y <= kMostScale) need = fmaxf(need, v.y);
+                if ((bits4 & 4u) && v.z <= kMostScale) need = fmaxf(need, v.z);
+                if ((bits4 & 8u) && v.w <= kMostScale) need = fmaxf(need, v.w);
+              }
+            }
           }
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -621,12 +653,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
           // when a score passes it by 2^8 (f16 has room for that), so that O
           // is seldom scaled anew.
           const float now = mx * c;  // powers of two
-          const float vnow = fabsf(tail.vref[sc]);
-          // a scale that is not finite must not reach rows that do not see it
-          const bool odd = tail.vref[sc] < 0.0f;
+          const float vall = fabsf(tail.vref[sc]);
+          // (rows past the last one go with the others)
+          const float vnow = !live ? vall : need > vref ? next_scale(need) : vref;
           const bool moves = now > ref + kLazy || vnow != vref;
           if (__any_sync(0xFFFFFFFFu, moves)) {
-            const float to = fmaxf(ref, now);
+            const float to = now > ref + kLazy ? now : ref;
             const float al = ref == -INFINITY ? 0.0f : ex2(ref - to);
             const float f = al * (vref / vnow);
             l *= al;
@@ -647,12 +679,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
             }
           }
           const float base = ref == -INFINITY ? 0.0f : ref;
-          const float4* vs = reinterpret_cast<const float4*>(tail.vs[sc]);
+          // What a row does not see must not reach it: a scale out of range
+          // (times a weight of 0 it may be no 0), or one that others' are
+          // relative to.  Then the scales are taken as they are.
+          const bool rare = __any_sync(0xFFFFFFFFu, vref != vall) || tail.vref[sc] < 0.0f;
+          const float4* vs = reinterpret_cast<const float4*>(rare ? tail.vr[sc] : tail.vs[sc]);
+          const float inv = up_over(vref);
           const float2 c2 = make_float2(c, c), nb = make_float2(-base, -base);
           float2 l2 = make_float2(0.0f, 0.0f);
           // (two copies of the loop, the rare one with its tests: 2 % of a bf16
           // prompt's time)
-          auto weights = [&](auto zeros) {
+          auto weights = [&](auto own) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               uint32_t hi[16], lo[16];
@@ -666,8 +703,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
                   p.x = ex2(p.x);
                   p.y = ex2(p.y);
                   l2 = add2(l2, p);
-                  float2 wt = mul2(p, k == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
-                  if constexpr (decltype(zeros)::value) {
+                  float2 v2 = k == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w);
+                  if constexpr (decltype(own)::value) v2 = mul2(v2, make_float2(inv, inv));
+                  float2 wt = mul2(p, v2);
+                  if constexpr (decltype(own)::value) {
                     wt.x = p.x == 0.0f ? 0.0f : wt.x;
                     wt.y = p.y == 0.0f ? 0.0f : wt.y;
                   }
@@ -681,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
               if constexpr (SPLIT) tmem_st16(s_col + buf * kKeys + 32 + 16 * half, lo);
             }
           };
-          if (odd)
+          if (rare)
             weights(Flag<true>());
           else
             weights(Flag<false>());
@@ -947,14 +986,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
                          : "memory");
           }
         }
-        // value scales relative to a power of two at or above all so far;
-        // four times the next one when it moves, so that it seldom does
-        float vt = fmaxf(s[1] <= 1e37f ? s[1] : 0.0f, s[3] <= 1e37f ? s[3] : 0.0f);
+        // value scales relative to a power of two above all so far
+        float vt = fmaxf(s[1] <= kMostScale ? s[1] : 0.0f, s[3] <= kMostScale ? s[3] : 0.0f);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) vt = fmaxf(vt, __shfl_xor_sync(0xFFFFFFFFu, vt, o));
-        if (vt > vref) vref = __uint_as_float((__float_as_uint(vt) & 0x7F800000u) + (2u << 23));
-        // kUp / vref, both powers of two
-        const float inv = __uint_as_float(((254u + 7u) << 23) - __float_as_uint(vref));
+        if (vt > vref) vref = next_scale(vt);
+        const float inv = up_over(vref);
         // the ring's place is free once the unit two before is done with
         // (its own occupant was the one four before)
         const uint32_t sc = units % kScales;
@@ -963,8 +1000,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows_kernel(const AttnArgs a
         tail.ks[sc][lane + 32] = s[2];
         tail.vs[sc][lane] = s[1] * inv;
         tail.vs[sc][lane + 32] = s[3] * inv;
-        const bool odd = __any_sync(0xFFFFFFFFu, !(fabsf(s[1]) <= 3.4e38f && fabsf(s[3]) <= 3.4e38f));
-        if (lane == 0) tail.vref[sc] = odd ? -vref : vref;
+        tail.vr[sc][lane] = s[1];
+        tail.vr[sc][lane + 32] = s[3];
+        const bool odd = __any_sync(0xFFFFFFFFu, !(s[1] >= 0.0f && s[1] <= kMostScale &&
+                                                   s[3] >= 0.0f && s[3] <= kMostScale));
+        if (lane == 0) {
+          tail.vref[sc] = odd ? -vref : vref;
+          tail.vmost[sc] = vt;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&tail.sc_full[sc]));
         if (u + 1 < seg.end) {

@@ -257,3 +257,69 @@ def test_hidden_codes_at_head_size_256(rq, ctx):
     for b, n in enumerate(c.lengths.tolist()):
         spoil_codes(c, b, n + 3)
     assert torch.equal(run(ctx, c, False)[:, :3], want[:, :3])
+
+
+SCALES = [1e30, 1e6, 30.0, float("nan"), float("inf"), -1e30, -float("inf"), 3e38]
+
+
+def spoil_scales(c, sequence, place, k_scale, v_scale):
+    page, offset = int(c.table[sequence, place // c.page]), place % c.page
+    c.ks[page, :, offset], c.vs[page, :, offset] = k_scale, v_scale
+
+
+@FORMS
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("dtype,fmt,d", [("f32", 0, 64), ("f32", 1, 128), ("bf16", 0, 128)])
+def test_scales_under_cleared_bits_do_not_reach_the_output(rq, ctx, d, dtype, fmt, scale, many):
+    """Large and odd scales under bits that no row sets, and under bits that
+    one row sets: the bits of all other rows stay."""
+    new = 26
+    words = [((1 << new) - 1) & ~(1 << 2) & ~(1 << 17) for _ in range(new)]
+    c = Case(rq, 14, [100, 0, 63], new, 14, 2, d, dtype, fmt, 16, tree=torch.tensor([words] * 3))
+    want = run(ctx, c, many)
+    c.check(want)
+    for b, n in enumerate(c.lengths.tolist()):
+        spoil_scales(c, b, n + 2, scale, scale)
+        spoil_scales(c, b, n + 17, scale, scale)
+    assert torch.equal(run(ctx, c, many), want)
+    c.tree[:, 9] |= 1 << 2
+    got = run(ctx, c, many)
+    got[:, 9] = want[:, 9]
+    assert torch.equal(got, want)
+
+
+@FORMS
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("new,dtype,d", [(21, "f32", 128), (75, "bf16", 64), (140, "f32", 64)])
+def test_scales_of_later_tokens_do_not_reach_earlier_ones(rq, ctx, new, dtype, d, scale, many):
+    c = Case(rq, 15, [100, 0], new, 4, 2, d, dtype, 1, 32)
+    want = run(ctx, c, many)
+    c.check(want)
+    for b, n in enumerate(c.lengths.tolist()):
+        for i in (new - 9, new - 2):
+            spoil_scales(c, b, n + i, scale, scale)
+    got = run(ctx, c, many)
+    assert torch.equal(got[:, :new - 9], want[:, :new - 9])
+
+
+@FORMS
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_rows_see_values_of_very_different_scales(rq, ctx, dtype, many):
+    """Some rows see a value of scale 1e9, those beside them do not: each is
+    within its own bound."""
+    new = 24
+    tree = torch.tensor([[(1 << new) - 1 if i % 3 == 0 else ((1 << new) - 1) & ~(1 << 5)
+                          for i in range(new)]])
+    c = Case(rq, 16, [90], new, 14, 2, 128, dtype, 1, 16, tree=tree)
+    page, offset = int(c.table[0, 95 // 16]), 95 % 16
+    c.vs[page, :, offset] = 1e9 if dtype == "f32" else 1e3
+    c.check(run(ctx, c, many))
+
+
+def test_hidden_scales_at_head_size_256(rq, ctx):
+    for scale in SCALES:
+        c = Case(rq, 17, [50, 0], 5, 4, 1, 256, "f32", 0, 16)
+        want = run(ctx, c, False)
+        for b, n in enumerate(c.lengths.tolist()):
+            spoil_scales(c, b, n + 3, scale, scale)
+        assert torch.equal(run(ctx, c, False)[:, :3], want[:, :3])

@@ -293,13 +293,14 @@ def _row_stride(t, heads, head_dim, stride, where):
     if t.is_contiguous():
         return row
     shape, st = t.shape, t.stride()
-    if shape[-1] not in (head_dim, row) or st[-1] != 1:
-        raise RqError(2, where)
     lead = len(shape) - 1
-    if shape[-1] == head_dim and len(shape) > 2:
+    if shape[-1] != row:        # a token's heads are an axis of their own
         lead -= 1
-        if shape[lead] > 1 and st[lead] != head_dim:
+        if (shape[-1] != head_dim or lead < 0 or shape[lead] != heads or
+                st[lead] != head_dim):
             raise RqError(2, where)
+    if st[-1] != 1:
+        raise RqError(2, where)
     # what is left counts tokens: one distance throughout
     token, step = None, None
     for i in range(lead - 1, -1, -1):

@@ -181,3 +181,20 @@ def test_binding_refuses_tensors_that_are_not_rows(rq):
 
 def test_attention_counters_want_a_context(rq):
     assert rq.lib().rq_ctx_attention_launches(NULL, NULL, NULL) == 1
+
+
+def test_binding_tells_tokens_from_a_single_head(rq):
+    """[batch, tokens, head_dim] of one head: the second axis is tokens, not
+    heads, and heads that are not as many as the call's are refused."""
+    import torch
+    x = torch.zeros(3, 5, 64)
+    with pytest.raises(rq.RqError):      # batches lie further apart than tokens
+        rq._row_stride(x[:, :4], 1, 64, None, "x")
+    assert rq._row_stride(x[:, ::5], 1, 64, None, "x") == 320
+    assert rq._row_stride(torch.zeros(3, 4, 96)[..., :64], 1, 64, None, "x") == 96
+    assert rq._row_stride(torch.zeros(3, 4, 1, 96)[..., :64], 1, 64, None, "x") == 96
+    assert rq._row_stride(torch.zeros(7, 96)[:, :64], 1, 64, None, "x") == 96
+    y = torch.zeros(6, 8, 64)
+    for bad, heads in ((y[::2], 4), (y[:, 1:4], 2), (torch.zeros(2, 512)[:, :64], 2)):
+        with pytest.raises(rq.RqError):
+            rq._row_stride(bad, heads, 64, None, "x")

@@ -106,6 +106,25 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_dtypes = {}
+
+
+def _dense(t, kind, where):
+    """Address of a dense tensor of torch's dtype `kind` (names, "|" between
+    them), or None."""
+    if t is None or isinstance(t, int):
+        return t
+    want = _dtypes.get(kind)
+    if want is None:
+        import torch
+        want = _dtypes[kind] = tuple(getattr(torch, name) for name in kind.split("|"))
+    if t.dtype not in want:
+        raise RqError(3, "%s is not %s" % (where, kind))
+    if not t.is_contiguous():
+        raise RqError(2, "%s is not dense" % where)
+    return t.data_ptr()
+
+
 _raw_stream = None      # torch's current-stream handle without a Stream object
 
 
@@ -323,8 +342,9 @@ def rq_qk_norm_rope(params, q, k, position, q_out, k_out, tokens, dtype=None, q_
     qs = _row_stride(q, params.q_heads, d, q_stride, "rq_qk_norm_rope: q")
     ks = _row_stride(k, params.kv_heads, d, k_stride, "rq_qk_norm_rope: k")
     _check(_lib.rq_qk_norm_rope(params.address, _dtype(k if q is None else q, dtype), _ptr(q), qs,
-                                _ptr(k), ks, _ptr(position), _ptr(q_out), _ptr(k_out), tokens,
-                                _stream(stream)), "rq_qk_norm_rope")
+                                _ptr(k), ks, _dense(position, "int32", "rq_qk_norm_rope: position"),
+                                _ptr(q_out), _ptr(k_out), tokens, _stream(stream)),
+           "rq_qk_norm_rope")
 
 
 def rq_qkv_to_cache(params, q, k, v, position, q_out, cache, slot, tokens, dtype=None,
@@ -335,8 +355,10 @@ def rq_qkv_to_cache(params, q, k, v, position, q_out, cache, slot, tokens, dtype
     ks = _row_stride(k, hk, d, k_stride, "rq_qkv_to_cache: k")
     vs = _row_stride(v, hk, d, v_stride, "rq_qkv_to_cache: v")
     _check(_lib.rq_qkv_to_cache(params.address, _dtype(k, dtype), _ptr(q), qs, _ptr(k), ks,
-                                _ptr(v), vs, _ptr(position), _ptr(q_out), cache.address,
-                                _ptr(slot), tokens, _stream(stream)), "rq_qkv_to_cache")
+                                _ptr(v), vs, _dense(position, "int32", "rq_qkv_to_cache: position"),
+                                _ptr(q_out), cache.address,
+                                _dense(slot, "int64", "rq_qkv_to_cache: slot"), tokens,
+                                _stream(stream)), "rq_qkv_to_cache")
 
 
 def rq_kv_write(cache, k, v, slot, tokens, dtype=None, k_stride=None, v_stride=None,
@@ -344,28 +366,39 @@ def rq_kv_write(cache, k, v, slot, tokens, dtype=None, k_stride=None, v_stride=N
     """Quantize k and v rows into the cache at slot (int64)."""
     ks = _row_stride(k, cache.kv_heads, cache.head_dim, k_stride, "rq_kv_write: k")
     vs = _row_stride(v, cache.kv_heads, cache.head_dim, v_stride, "rq_kv_write: v")
-    _check(_lib.rq_kv_write(cache.address, _dtype(k, dtype), _ptr(k), ks, _ptr(v), vs, _ptr(slot),
-                            tokens, _stream(stream)), "rq_kv_write")
+    _check(_lib.rq_kv_write(cache.address, _dtype(k, dtype), _ptr(k), ks, _ptr(v), vs,
+                            _dense(slot, "int64", "rq_kv_write: slot"), tokens, _stream(stream)),
+           "rq_kv_write")
 
 
 def rq_kv_read(cache, slot, k_out, v_out, tokens, dtype=None, stream=None):
     """Read the cache back at slot (int64) into dense rows."""
-    _check(_lib.rq_kv_read(cache.address, _dtype(k_out, dtype), _ptr(slot), _ptr(k_out),
-                           _ptr(v_out), tokens, _stream(stream)), "rq_kv_read")
+    _check(_lib.rq_kv_read(cache.address, _dtype(k_out, dtype),
+                           _dense(slot, "int64", "rq_kv_read: slot"), _ptr(k_out), _ptr(v_out),
+                           tokens, _stream(stream)), "rq_kv_read")
 
 
 def rq_verify_chain(token, p, q, u, accepted, next, batch, drafts, vocab, stream=None):
     """Keep or reject chains of drafts and draw the next token (q may be None)."""
-    _check(_lib.rq_verify_chain(_ptr(token), _ptr(p), _ptr(q), _ptr(u), _ptr(accepted),
-                                _ptr(next), batch, drafts, vocab, _stream(stream)),
-           "rq_verify_chain")
+    _check(_lib.rq_verify_chain(_dense(token, "int32", "rq_verify_chain: token"),
+                                _dense(p, "float32", "rq_verify_chain: p"),
+                                _dense(q, "float32", "rq_verify_chain: q"),
+                                _dense(u, "float32", "rq_verify_chain: u"),
+                                _dense(accepted, "int32", "rq_verify_chain: accepted"),
+                                _dense(next, "int32", "rq_verify_chain: next"), batch, drafts,
+                                vocab, _stream(stream)), "rq_verify_chain")
 
 
 def rq_verify_tree(token, parent, p, u, accepted, next, path, batch, drafts, vocab, stream=None):
     """Walk trees of drafts by draws from the target, and draw the next token."""
-    _check(_lib.rq_verify_tree(_ptr(token), _ptr(parent), _ptr(p), _ptr(u), _ptr(accepted),
-                               _ptr(next), _ptr(path), batch, drafts, vocab, _stream(stream)),
-           "rq_verify_tree")
+    _check(_lib.rq_verify_tree(_dense(token, "int32", "rq_verify_tree: token"),
+                               _dense(parent, "int32", "rq_verify_tree: parent"),
+                               _dense(p, "float32", "rq_verify_tree: p"),
+                               _dense(u, "float32", "rq_verify_tree: u"),
+                               _dense(accepted, "int32", "rq_verify_tree: accepted"),
+                               _dense(next, "int32", "rq_verify_tree: next"),
+                               _dense(path, "int32", "rq_verify_tree: path"), batch, drafts, vocab,
+                               _stream(stream)), "rq_verify_tree")
 
 
 class Context:
@@ -444,14 +477,22 @@ class Context:
                            scale, tree=None, max_pages=None, dtype=None, q_stride=None,
                            stream=None):
         """Attention of batch x new_tokens tokens over the cache; tree: 64-bit
-        words [batch, new_tokens] of visible new tokens, None: causal."""
+        words [batch, new_tokens] of visible new tokens, None: causal.
+        page_table [batch, max_pages] and length are dense int32 tensors (of a
+        wider table, its part in use is taken as a dense copy, or the table
+        whole)."""
         qs = _row_stride(q, q_heads, cache.head_dim, q_stride, "rq_cache_attention: q")
-        if max_pages is None:
+        if not isinstance(page_table, int):
+            if page_table.dim() != 2 or max_pages not in (None, page_table.shape[1]):
+                raise RqError(2, "rq_cache_attention: page_table is [batch, max_pages]")
             max_pages = page_table.shape[1]
         _check(_lib.rq_cache_attention(self._h, cache.address, _dtype(q, dtype), _ptr(q), qs,
-                                       _ptr(out), batch, new_tokens, q_heads, _ptr(page_table),
-                                       max_pages, _ptr(length), _ptr(tree), scale,
-                                       _stream(stream)), "rq_cache_attention")
+                                       _ptr(out), batch, new_tokens, q_heads,
+                                       _dense(page_table, "int32", "rq_cache_attention: page_table"),
+                                       max_pages,
+                                       _dense(length, "int32", "rq_cache_attention: length"),
+                                       _dense(tree, "int64|uint64", "rq_cache_attention: tree"),
+                                       scale, _stream(stream)), "rq_cache_attention")
 
     def attention_launches(self):
         """How many rq_cache_attention calls launched the kernel for few query

@@ -198,3 +198,70 @@ def test_binding_tells_tokens_from_a_single_head(rq):
     for bad, heads in ((y[::2], 4), (y[:, 1:4], 2), (torch.zeros(2, 512)[:, :64], 2)):
         with pytest.raises(rq.RqError):
             rq._row_stride(bad, heads, 64, None, "x")
+
+
+def refused(rq, status, call, *args, **kw):
+    with pytest.raises(rq.RqError) as e:
+        call(*args, **kw)
+    assert e.value.status == status, e.value
+
+
+def small_cache(rq, **over):
+    import torch
+    k = torch.zeros(8, 2, 16, 64, dtype=torch.int8)
+    s = torch.zeros(8, 2, 16)
+    return rq.KVCache.from_tensors(k, k.clone(), s, s.clone(), **dict(dict(format=rq.RQ_KV_I8), **over))
+
+
+class NoContext:
+    """Stands for a Context where the binding refuses before the library."""
+    _h = None
+
+
+def test_binding_refuses_index_arrays_that_are_not_what_the_kernels_read(rq):
+    import torch
+    c, st = small_cache(rq), dict(stream=0)
+    p = rq.QKParams(4, 2, 64, cos=torch.zeros(8, 32), sin=torch.zeros(8, 32))
+    q, k, v = torch.zeros(4, 4, 64), torch.zeros(4, 2, 64), torch.zeros(4, 2, 64)
+    pos, slot = torch.arange(4, dtype=torch.int32), torch.arange(4)
+    for bad, status in ((pos.long(), 3), (torch.arange(8, dtype=torch.int32)[::2], 2)):
+        refused(rq, status, rq.rq_qk_norm_rope, p, q, k, bad, q.clone(), k.clone(), 4, **st)
+        refused(rq, status, rq.rq_qkv_to_cache, p, q, k, v, bad, q.clone(), c, slot, 4, **st)
+    for bad, status in ((slot.int(), 3), (torch.arange(8)[::2], 2)):
+        refused(rq, status, rq.rq_qkv_to_cache, p, q, k, v, pos, q.clone(), c, bad, 4, **st)
+        refused(rq, status, rq.rq_kv_write, c, k, v, bad, 4, **st)
+        refused(rq, status, rq.rq_kv_read, c, bad, k.clone(), v.clone(), 4, **st)
+
+    attend = rq.Context.rq_cache_attention
+    q4 = torch.zeros(2, 3, 4, 64)
+    table = torch.zeros(2, 6, dtype=torch.int32)
+    length = torch.zeros(2, dtype=torch.int32)
+    tree = torch.zeros(2, 3, dtype=torch.int64)
+
+    def call(table=table, length=length, tree=tree, **kw):
+        attend(NoContext, c, q4, q4.clone(), table, length, 2, 3, 4, 0.1, tree=tree, stream=0, **kw)
+
+    refused(rq, 1, call, tree=tree.view(torch.uint64))
+    refused(rq, 1, call)                            # what is right reaches the library: no context
+    refused(rq, 2, call, table=table[:, :4])        # the pages in use of a wider table
+    refused(rq, 2, call, table=table.t())
+    refused(rq, 2, call, table=table.view(-1))
+    refused(rq, 2, call, max_pages=4)
+    refused(rq, 3, call, table=table.long())
+    refused(rq, 3, call, length=length.long())
+    refused(rq, 2, call, length=torch.zeros(4, dtype=torch.int32)[::2])
+    refused(rq, 3, call, tree=tree.int())
+    refused(rq, 2, call, tree=torch.zeros(2, 6, dtype=torch.int64)[:, :3])
+
+    token = torch.zeros(2, 3, dtype=torch.int32)
+    prob, draft, u = torch.zeros(2, 4, 10), torch.zeros(2, 3, 10), torch.zeros(2, 4)
+    out, path = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 3, dtype=torch.int32)
+    good = dict(token=token, p=prob, q=draft, u=u, accepted=out, next=out.clone())
+    tree_good = dict(token=token, parent=token.clone(), p=prob, u=u, accepted=out,
+                     next=out.clone(), path=path)
+    for call, args in ((rq.rq_verify_chain, good), (rq.rq_verify_tree, tree_good)):
+        for name, t in args.items():
+            other = t.long() if t.dtype == torch.int32 else t.double()
+            apart = torch.stack([t, t], -1)[..., 0]
+            refused(rq, 3, call, batch=2, drafts=3, vocab=10, stream=0, **dict(args, **{name: other}))
+            refused(rq, 2, call, batch=2, drafts=3, vocab=10, stream=0, **dict(args, **{name: apart}))

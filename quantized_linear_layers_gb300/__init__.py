@@ -213,6 +213,10 @@ def rq_gemv_exact_outputs(stream=None):
     return n.value
 
 
+def _is_f32(t):
+    return t.element_size() == 4 and t.is_floating_point()
+
+
 class _KVCacheStruct(ctypes.Structure):
     _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("pages", _i64),
                 ("page_size", _i32), ("kv_heads", _i32), ("head_dim", _i32), ("format", _i32)]
@@ -251,7 +255,7 @@ class KVCache:
                 raise RqError(2, "KVCache: tensors must be dense")
         if (k.dim() != 4 or v.shape != k.shape or k_scale.shape != k.shape[:3] or
                 v_scale.shape != k.shape[:3] or k.element_size() != 1 or v.element_size() != 1 or
-                k_scale.element_size() != 4 or v_scale.element_size() != 4):
+                not _is_f32(k_scale) or not _is_f32(v_scale)):
             raise RqError(2, "KVCache")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.format = format
@@ -271,7 +275,7 @@ class QKParams:
         if rotary_dim is None:
             rotary_dim = 0 if cos is None else head_dim
         for t in (q_weight, k_weight, cos, sin):
-            if t is not None and not (t.is_contiguous() and t.element_size() == 4):
+            if t is not None and not (t.is_contiguous() and _is_f32(t)):
                 raise RqError(2, "QKParams: weights and tables are dense f32")
         for t in (q_weight, k_weight):
             if t is not None and t.numel() != head_dim:
@@ -290,14 +294,32 @@ class QKParams:
 _DTYPES = {}
 
 
-def _dtype(t, dtype):
-    """rq_dtype of a tensor, or the given one where t is an address."""
+def _dtype(dtype, where, *tensors):
+    """The one rq_dtype of a call's tensors; `dtype` where it is given (and
+    vouched for by the caller: tensors may be addresses then)."""
     if dtype is not None:
         return dtype
+    first = None
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        if first is None:
+            first = t.dtype
+        elif t.dtype is not first:
+            raise RqError(3, where + ": tensors of different types")
     if not _DTYPES:
         import torch
         _DTYPES.update({torch.float32: RQ_F32, torch.float16: RQ_F16, torch.bfloat16: RQ_BF16})
-    return _DTYPES.get(t.dtype, -1)
+    return _DTYPES.get(first, -1)
+
+
+def _rows(t, where):
+    """Address of an output's rows, which are dense."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_contiguous():
+        raise RqError(2, where + " is not dense")
+    return t.data_ptr()
 
 
 def _row_stride(t, heads, head_dim, stride, where):
@@ -341,9 +363,11 @@ def rq_qk_norm_rope(params, q, k, position, q_out, k_out, tokens, dtype=None, q_
     d = params.head_dim
     qs = _row_stride(q, params.q_heads, d, q_stride, "rq_qk_norm_rope: q")
     ks = _row_stride(k, params.kv_heads, d, k_stride, "rq_qk_norm_rope: k")
-    _check(_lib.rq_qk_norm_rope(params.address, _dtype(k if q is None else q, dtype), _ptr(q), qs,
+    _check(_lib.rq_qk_norm_rope(params.address,
+                                _dtype(dtype, "rq_qk_norm_rope", q, k, q_out, k_out), _ptr(q), qs,
                                 _ptr(k), ks, _dense(position, "int32", "rq_qk_norm_rope: position"),
-                                _ptr(q_out), _ptr(k_out), tokens, _stream(stream)),
+                                _rows(q_out, "rq_qk_norm_rope: q_out"),
+                                _rows(k_out, "rq_qk_norm_rope: k_out"), tokens, _stream(stream)),
            "rq_qk_norm_rope")
 
 
@@ -354,9 +378,10 @@ def rq_qkv_to_cache(params, q, k, v, position, q_out, cache, slot, tokens, dtype
     qs = _row_stride(q, params.q_heads, d, q_stride, "rq_qkv_to_cache: q")
     ks = _row_stride(k, hk, d, k_stride, "rq_qkv_to_cache: k")
     vs = _row_stride(v, hk, d, v_stride, "rq_qkv_to_cache: v")
-    _check(_lib.rq_qkv_to_cache(params.address, _dtype(k, dtype), _ptr(q), qs, _ptr(k), ks,
-                                _ptr(v), vs, _dense(position, "int32", "rq_qkv_to_cache: position"),
-                                _ptr(q_out), cache.address,
+    _check(_lib.rq_qkv_to_cache(params.address, _dtype(dtype, "rq_qkv_to_cache", q, k, v, q_out),
+                                _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
+                                _dense(position, "int32", "rq_qkv_to_cache: position"),
+                                _rows(q_out, "rq_qkv_to_cache: q_out"), cache.address,
                                 _dense(slot, "int64", "rq_qkv_to_cache: slot"), tokens,
                                 _stream(stream)), "rq_qkv_to_cache")
 
@@ -366,15 +391,16 @@ def rq_kv_write(cache, k, v, slot, tokens, dtype=None, k_stride=None, v_stride=N
     """Quantize k and v rows into the cache at slot (int64)."""
     ks = _row_stride(k, cache.kv_heads, cache.head_dim, k_stride, "rq_kv_write: k")
     vs = _row_stride(v, cache.kv_heads, cache.head_dim, v_stride, "rq_kv_write: v")
-    _check(_lib.rq_kv_write(cache.address, _dtype(k, dtype), _ptr(k), ks, _ptr(v), vs,
+    _check(_lib.rq_kv_write(cache.address, _dtype(dtype, "rq_kv_write", k, v), _ptr(k), ks, _ptr(v), vs,
                             _dense(slot, "int64", "rq_kv_write: slot"), tokens, _stream(stream)),
            "rq_kv_write")
 
 
 def rq_kv_read(cache, slot, k_out, v_out, tokens, dtype=None, stream=None):
     """Read the cache back at slot (int64) into dense rows."""
-    _check(_lib.rq_kv_read(cache.address, _dtype(k_out, dtype),
-                           _dense(slot, "int64", "rq_kv_read: slot"), _ptr(k_out), _ptr(v_out),
+    _check(_lib.rq_kv_read(cache.address, _dtype(dtype, "rq_kv_read", k_out, v_out),
+                           _dense(slot, "int64", "rq_kv_read: slot"),
+                           _rows(k_out, "rq_kv_read: k_out"), _rows(v_out, "rq_kv_read: v_out"),
                            tokens, _stream(stream)), "rq_kv_read")
 
 
@@ -486,8 +512,10 @@ class Context:
             if page_table.dim() != 2 or max_pages not in (None, page_table.shape[1]):
                 raise RqError(2, "rq_cache_attention: page_table is [batch, max_pages]")
             max_pages = page_table.shape[1]
-        _check(_lib.rq_cache_attention(self._h, cache.address, _dtype(q, dtype), _ptr(q), qs,
-                                       _ptr(out), batch, new_tokens, q_heads,
+        _check(_lib.rq_cache_attention(self._h, cache.address,
+                                       _dtype(dtype, "rq_cache_attention", q, out), _ptr(q), qs,
+                                       _rows(out, "rq_cache_attention: out"), batch, new_tokens,
+                                       q_heads,
                                        _dense(page_table, "int32", "rq_cache_attention: page_table"),
                                        max_pages,
                                        _dense(length, "int32", "rq_cache_attention: length"),

@@ -265,3 +265,37 @@ def test_binding_refuses_index_arrays_that_are_not_what_the_kernels_read(rq):
             apart = torch.stack([t, t], -1)[..., 0]
             refused(rq, 3, call, batch=2, drafts=3, vocab=10, stream=0, **dict(args, **{name: other}))
             refused(rq, 2, call, batch=2, drafts=3, vocab=10, stream=0, **dict(args, **{name: apart}))
+
+
+def test_binding_refuses_rows_of_different_types_and_outputs_that_are_not_dense(rq):
+    import torch
+    c, st = small_cache(rq), dict(stream=0)
+    p = rq.QKParams(4, 2, 64, cos=torch.zeros(8, 32), sin=torch.zeros(8, 32))
+    q, k, v = torch.zeros(4, 4, 64), torch.zeros(4, 2, 64), torch.zeros(4, 2, 64)
+    pos, slot = torch.arange(4, dtype=torch.int32), torch.arange(4)
+    apart = torch.zeros(4, 8, 64)
+    for q1, k1, v1, o1, status in (
+            (q.bfloat16(), k, v, q.clone(), 3), (q, k.half(), v, q.clone(), 3),
+            (q, k, v.half(), q.clone(), 3), (q, k, v, q.bfloat16(), 3),
+            (q, k, v, apart[:, :4], 2), (q.double(), k.double(), v.double(), q.double(), 3)):
+        refused(rq, status, rq.rq_qkv_to_cache, p, q1, k1, v1, pos, o1, c, slot, 4, **st)
+    for q1, k1, qo, ko, status in (
+            (q, k.half(), q.clone(), k.half(), 3), (q, k, q.half(), k.clone(), 3),
+            (q, k, q.clone(), k.bfloat16(), 3), (q, k, apart[:, 4:], k.clone(), 2),
+            (q, k, q.clone(), apart[:, ::4], 2), (None, k, None, k.half(), 3)):
+        refused(rq, status, rq.rq_qk_norm_rope, p, q1, k1, pos, qo, ko, 4, **st)
+    refused(rq, 3, rq.rq_kv_write, c, k, v.half(), slot, 4, **st)
+    refused(rq, 3, rq.rq_kv_write, c, k.double(), v.double(), slot, 4, **st)
+    refused(rq, 3, rq.rq_kv_read, c, slot, k.half(), v.clone(), 4, **st)
+    refused(rq, 2, rq.rq_kv_read, c, slot, apart[:, :2], v.clone(), 4, **st)
+    refused(rq, 2, rq.rq_kv_read, c, slot, k.clone(), apart[:, 1:3], 4, **st)
+
+    q4 = torch.zeros(2, 3, 4, 64)
+    table, length = torch.zeros(2, 6, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for out, status in ((q4.half(), 3), (torch.zeros(2, 3, 8, 64)[:, :, :4], 2), (q4.clone(), 1)):
+        refused(rq, status, rq.Context.rq_cache_attention, NoContext, c, q4, out, table, length, 2,
+                3, 4, 0.1, stream=0)
+    with pytest.raises(rq.RqError):
+        rq.QKParams(4, 2, 64, q_weight=torch.ones(64, dtype=torch.int32))
+    with pytest.raises(rq.RqError):
+        rq.KVCache.from_tensors(c.k, c.v, c.k_scale.int(), c.v_scale, format=rq.RQ_KV_I8)

@@ -244,7 +244,15 @@ class KVCache:
                   torch.zeros(shape, dtype=torch.float32, device=device), format)
 
     @classmethod
-    def from_tensors(cls, k, v, k_scale, v_scale, format=RQ_KV_E4M3):
+    def from_tensors(cls, k, v, k_scale, v_scale, format=None):
+        """The format follows from the codes' type: float8_e4m3fn or int8; bytes
+        of another type hold `format`, E4M3 unless it is given."""
+        import torch
+        named = {torch.float8_e4m3fn: RQ_KV_E4M3, torch.int8: RQ_KV_I8}.get(k.dtype)
+        if v.dtype is not k.dtype or named is not None and format not in (None, named):
+            raise RqError(3, "KVCache: codes are not of the format")
+        if format is None:
+            format = RQ_KV_E4M3 if named is None else named
         c = cls.__new__(cls)
         c._set(k, v, k_scale, v_scale, format)
         return c

@@ -299,3 +299,18 @@ def test_binding_refuses_rows_of_different_types_and_outputs_that_are_not_dense(
         rq.QKParams(4, 2, 64, q_weight=torch.ones(64, dtype=torch.int32))
     with pytest.raises(rq.RqError):
         rq.KVCache.from_tensors(c.k, c.v, c.k_scale.int(), c.v_scale, format=rq.RQ_KV_I8)
+
+
+def test_the_format_of_a_cache_is_its_codes_type(rq):
+    import torch
+    k, s = torch.zeros(8, 2, 16, 64, dtype=torch.int8), torch.zeros(8, 2, 16)
+    e4m3, raw = k.view(torch.float8_e4m3fn), k.view(torch.uint8)
+    make = rq.KVCache.from_tensors
+    assert make(k, k, s, s).struct.format == rq.RQ_KV_I8
+    assert make(k, k, s, s, format=rq.RQ_KV_I8).struct.format == rq.RQ_KV_I8
+    assert make(e4m3, e4m3, s, s).struct.format == rq.RQ_KV_E4M3
+    assert make(raw, raw, s, s).struct.format == rq.RQ_KV_E4M3
+    assert make(raw, raw, s, s, format=rq.RQ_KV_I8).struct.format == rq.RQ_KV_I8
+    refused(rq, 3, make, k, k, s, s, format=rq.RQ_KV_E4M3)
+    refused(rq, 3, make, e4m3, e4m3, s, s, format=rq.RQ_KV_I8)
+    refused(rq, 3, make, k, e4m3, s, s)

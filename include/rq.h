@@ -476,7 +476,8 @@ rq_status rq_ctx_attention_launches(const rq_ctx *ctx, int64_t *few_rows_host,
  * floor(U * total / 2^24), U = floor(u * 2^24) limited to 0 .. 2^24-1, so
  * that it depends on no order of summation; -1 if p has no weight either.
  *   accepted, next: int32 [batch].
- * drafts >= 0 (token, q may be NULL at 0), 1 <= vocab <= 2^20, batch >= 1.
+ * 0 <= drafts <= 2^30 (token, q may be NULL at 0), 1 <= vocab <= 2^20,
+ * 0 <= batch <= 2^27 (0 does nothing).
  * p and q: 4-byte aligned.
  * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_CUDA. */
 rq_status rq_verify_chain(const int32_t *token, const float *p, const float *q,

@@ -781,9 +781,10 @@ static rq_status check_verify(const int32_t* token, const float* p, const float*
   if (p == nullptr || u == nullptr || accepted == nullptr || next == nullptr ||
       (drafts > 0 && token == nullptr))
     return RQ_ERR_NULL;
-  if (batch < 0 || batch > (1 << 27) || drafts < 0 || vocab < 1 || vocab > (1 << 20) ||
-      !aligned(p, 4) || !aligned(u, 4) || !aligned(token, 4) || !aligned(accepted, 4) ||
-      !aligned(next, 4))
+  // (drafts + 1 rows, counted in steps of a block's threads, in 32 bits)
+  if (batch < 0 || batch > (1 << 27) || drafts < 0 || drafts > (1 << 30) || vocab < 1 ||
+      vocab > (1 << 20) || !aligned(p, 4) || !aligned(u, 4) || !aligned(token, 4) ||
+      !aligned(accepted, 4) || !aligned(next, 4))
     return RQ_ERR_SHAPE;
   return RQ_OK;
 }

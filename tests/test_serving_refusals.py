@@ -314,3 +314,10 @@ def test_the_format_of_a_cache_is_its_codes_type(rq):
     refused(rq, 3, make, k, k, s, s, format=rq.RQ_KV_E4M3)
     refused(rq, 3, make, e4m3, e4m3, s, s, format=rq.RQ_KV_I8)
     refused(rq, 3, make, k, e4m3, s, s)
+
+
+def test_more_drafts_than_rows_are_counted_in(rq):
+    lib = rq.lib()
+    for n in ((1 << 30) + 1, 0x7FFFFFFF - 511, 0x7FFFFFFF):
+        assert lib.rq_verify_chain(A, A, NULL, A, A, A, 1, n, 1, NULL) == 2
+        assert lib.rq_verify_tree(A, A, A, A, A, A, A, 1, n, 1, NULL) == 2

@@ -429,9 +429,11 @@ rq_status rq_kv_read(const rq_kv_cache *cache_host, int dtype, const int64_t *sl
  * Accuracy: with f32 activations q, the probabilities and both products are
  * carried to about 21 bits (each f32 operand split into two f16 parts, codes
  * exact in f16, f32 sums, whose additions the tensor cores cut off rather than
- * round: about 1e-6 of the result, 6e-6 for single tokens of dozens of
- * sequences of 60000); with f16 / bf16 activations q and the
- * probabilities are f16 operands (11 bits).
+ * round, and which are therefore taken over into rounded sums every few
+ * hundred keys: about 1e-6 of the result whatever the length); with f16 / bf16
+ * activations q and the probabilities may be f16 operands (11 bits).  A key's
+ * weight is carried relative to the largest value scale that its row has seen:
+ * what is below 2^-30 of that is lost.
  * Partial results of split sequences live in scratch owned by ctx: about 61
  * MB, allocated by the first call that needs it (which waits for the stream,
  * and inside a stream capture gives RQ_ERR_ALLOC: call once before) and kept

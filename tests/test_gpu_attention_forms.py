@@ -4,7 +4,7 @@ of sizes, the room of the page table among them; every test here asserts it."""
 import pytest
 import torch
 
-from serving_util import gen
+from serving_util import attention, gen, random_pool, values
 from test_gpu_attention import Case, random_tree, signed
 
 pytestmark = pytest.mark.gpu
@@ -323,3 +323,35 @@ def test_hidden_scales_at_head_size_256(rq, ctx):
         for b, n in enumerate(c.lengths.tolist()):
             spoil_scales(c, b, n + 3, scale, scale)
         assert torch.equal(run(ctx, c, False)[:, :3], want[:, :3])
+
+
+@pytest.mark.parametrize("heads,page,batch", [
+    ((4, 1, 64), 256, 1025), ((4, 1, 128), 128, 1025), ((4, 1, 256), 256, 1025),
+    ((8, 1, 128), 64, 40), ((2, 1, 256), 16, 40), ((28, 4, 128), 64, 1)])
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_long_sums_of_few_rows(rq, ctx, heads, page, batch, fmt):
+    # The tensor cores cut sums off: at most 2^-23 of the sum at each of the 2
+    # additions of a unit of 16 keys, on average half of that, in the 16 units
+    # that are summed there before a rounded addition (32 x 2^-24), and D / 8
+    # such additions in a score of magnitude up to about 4 whose partial sums
+    # are half of it on average (D / 4 x 2^-24).  More than 1024 sequences are
+    # not cut; all of them read the same pages.
+    hq, hk, d = heads
+    n = 60000
+    pages = -(-(n + 1) // page)
+    k, v, ks, vs = random_pool(18, pages, hk, page, d, fmt)
+    cache = rq.KVCache.from_tensors(k.cuda(), v.cuda(), ks.cuda(), vs.cuda(), format=fmt)
+    table = torch.randperm(pages, generator=gen(19)).int()[None].expand(batch, -1).contiguous()
+    lengths = torch.full((batch,), n, dtype=torch.int32)
+    q = torch.randn((batch, 1, hq, d), generator=gen(20))
+    out = torch.empty_like(q, device="cuda")
+    few0, _ = ctx.attention_launches()
+    ctx.rq_cache_attention(cache, q.cuda(), out, table.cuda(), lengths.cuda(), batch, 1, hq,
+                           d ** -0.5)
+    assert ctx.attention_launches()[0] == few0 + 1
+    pick = torch.tensor(sorted({0, batch // 2, batch - 1}))
+    ref, _ = attention(q[pick], values(k, ks), values(v, vs), table[pick], lengths[pick], None,
+                       d ** -0.5, "f32", page)
+    err = float((out.cpu().double()[pick] - ref).norm() / ref.norm())
+    print("relative error %.2e, bound %.2e" % (err, (32 + d / 4) * 2.0 ** -24))
+    assert err <= (32 + d / 4) * 2.0 ** -24

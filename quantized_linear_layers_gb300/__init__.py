@@ -106,23 +106,27 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_dtypes = {}
+class _Kinds(dict):
+    """Names of torch dtypes, "|" between them -> a tuple of those."""
+
+    def __missing__(self, kind):
+        import torch
+        self[kind] = tuple(getattr(torch, name) for name in kind.split("|"))
+        return self[kind]
+
+
+_kinds = _Kinds()
 
 
 def _dense(t, kind, where):
-    """Address of a dense tensor of torch's dtype `kind` (names, "|" between
-    them), or None."""
+    """Address of a dense tensor of torch's dtype `kind`, or None."""
     if t is None or isinstance(t, int):
         return t
-    want = _dtypes.get(kind)
-    if want is None:
-        import torch
-        want = _dtypes[kind] = tuple(getattr(torch, name) for name in kind.split("|"))
-    if t.dtype not in want:
-        raise RqError(3, "%s is not %s" % (where, kind))
-    if not t.is_contiguous():
-        raise RqError(2, "%s is not dense" % where)
-    return t.data_ptr()
+    if t.dtype in _kinds[kind] and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype in _kinds[kind]:
+        raise RqError(2, where + " is not dense")
+    raise RqError(3, "%s is not %s" % (where, kind))
 
 
 _raw_stream = None      # torch's current-stream handle without a Stream object
@@ -311,10 +315,11 @@ def _dtype(dtype, where, *tensors):
     for t in tensors:
         if t is None or isinstance(t, int):
             continue
-        if first is None:
-            first = t.dtype
-        elif t.dtype is not first:
-            raise RqError(3, where + ": tensors of different types")
+        kind = t.dtype
+        if kind is not first:
+            if first is not None:
+                raise RqError(3, where + ": tensors of different types")
+            first = kind
     if not _DTYPES:
         import torch
         _DTYPES.update({torch.float32: RQ_F32, torch.float16: RQ_F16, torch.bfloat16: RQ_BF16})
@@ -325,9 +330,9 @@ def _rows(t, where):
     """Address of an output's rows, which are dense."""
     if t is None or isinstance(t, int):
         return t
-    if not t.is_contiguous():
-        raise RqError(2, where + " is not dense")
-    return t.data_ptr()
+    if t.is_contiguous():
+        return t.data_ptr()
+    raise RqError(2, where + " is not dense")
 
 
 def _row_stride(t, heads, head_dim, stride, where):
@@ -517,9 +522,10 @@ class Context:
         whole)."""
         qs = _row_stride(q, q_heads, cache.head_dim, q_stride, "rq_cache_attention: q")
         if not isinstance(page_table, int):
-            if page_table.dim() != 2 or max_pages not in (None, page_table.shape[1]):
+            shape = page_table.shape
+            if len(shape) != 2 or max_pages not in (None, shape[1]):
                 raise RqError(2, "rq_cache_attention: page_table is [batch, max_pages]")
-            max_pages = page_table.shape[1]
+            max_pages = shape[1]
         _check(_lib.rq_cache_attention(self._h, cache.address,
                                        _dtype(dtype, "rq_cache_attention", q, out), _ptr(q), qs,
                                        _rows(out, "rq_cache_attention: out"), batch, new_tokens,

@@ -120,10 +120,11 @@ _kinds = _Kinds()
 
 def _dense(t, kind, where):
     """Address of a dense tensor of torch's dtype `kind`, or None."""
-    if t is None or isinstance(t, int):
-        return t
-    if t.dtype in _kinds[kind] and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype in _kinds[kind] and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        return _ptr(t)
     if t.dtype in _kinds[kind]:
         raise RqError(2, where + " is not dense")
     raise RqError(3, "%s is not %s" % (where, kind))
@@ -152,7 +153,7 @@ def _current_stream():
 
 def _stream(stream):
     if stream is None:
-        return _current_stream()
+        return _current_stream() if _raw_stream is None else _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -328,11 +329,24 @@ def _dtype(dtype, where, *tensors):
 
 def _rows(t, where):
     """Address of an output's rows, which are dense."""
-    if t is None or isinstance(t, int):
-        return t
-    if t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        return _ptr(t)
     raise RqError(2, where + " is not dense")
+
+
+def _strided_rows(t, heads, head_dim, stride, where):
+    """Address of an input's rows, and the elements between its tokens."""
+    try:
+        if stride is None:
+            if t.is_contiguous():
+                return t.data_ptr(), heads * head_dim
+            return t.data_ptr(), _view_stride(t, heads, head_dim, where)
+    except AttributeError:
+        pass
+    return _ptr(t), _row_stride(t, heads, head_dim, stride, where)
 
 
 def _row_stride(t, heads, head_dim, stride, where):
@@ -344,8 +358,12 @@ def _row_stride(t, heads, head_dim, stride, where):
         return stride
     if t is None or isinstance(t, int):
         return row
-    if t.is_contiguous():
-        return row
+    return row if t.is_contiguous() else _view_stride(t, heads, head_dim, where)
+
+
+def _view_stride(t, heads, head_dim, where):
+    """The same of a tensor that is not dense."""
+    row = heads * head_dim
     shape, st = t.shape, t.stride()
     lead = len(shape) - 1
     if shape[-1] != row:        # a token's heads are an axis of their own
@@ -374,11 +392,11 @@ def rq_qk_norm_rope(params, q, k, position, q_out, k_out, tokens, dtype=None, q_
     """Per-head norm and position rotation: q -> q_out, k -> k_out (either
     pair may be None)."""
     d = params.head_dim
-    qs = _row_stride(q, params.q_heads, d, q_stride, "rq_qk_norm_rope: q")
-    ks = _row_stride(k, params.kv_heads, d, k_stride, "rq_qk_norm_rope: k")
+    qp, qs = _strided_rows(q, params.q_heads, d, q_stride, "rq_qk_norm_rope: q")
+    kp, ks = _strided_rows(k, params.kv_heads, d, k_stride, "rq_qk_norm_rope: k")
     _check(_lib.rq_qk_norm_rope(params.address,
-                                _dtype(dtype, "rq_qk_norm_rope", q, k, q_out, k_out), _ptr(q), qs,
-                                _ptr(k), ks, _dense(position, "int32", "rq_qk_norm_rope: position"),
+                                _dtype(dtype, "rq_qk_norm_rope", q, k, q_out, k_out), qp, qs,
+                                kp, ks, _dense(position, "int32", "rq_qk_norm_rope: position"),
                                 _rows(q_out, "rq_qk_norm_rope: q_out"),
                                 _rows(k_out, "rq_qk_norm_rope: k_out"), tokens, _stream(stream)),
            "rq_qk_norm_rope")
@@ -388,11 +406,11 @@ def rq_qkv_to_cache(params, q, k, v, position, q_out, cache, slot, tokens, dtype
                     q_stride=None, k_stride=None, v_stride=None, stream=None):
     """The same, with k and v quantized into the cache at slot (int64)."""
     d, hk = params.head_dim, params.kv_heads
-    qs = _row_stride(q, params.q_heads, d, q_stride, "rq_qkv_to_cache: q")
-    ks = _row_stride(k, hk, d, k_stride, "rq_qkv_to_cache: k")
-    vs = _row_stride(v, hk, d, v_stride, "rq_qkv_to_cache: v")
+    qp, qs = _strided_rows(q, params.q_heads, d, q_stride, "rq_qkv_to_cache: q")
+    kp, ks = _strided_rows(k, hk, d, k_stride, "rq_qkv_to_cache: k")
+    vp, vs = _strided_rows(v, hk, d, v_stride, "rq_qkv_to_cache: v")
     _check(_lib.rq_qkv_to_cache(params.address, _dtype(dtype, "rq_qkv_to_cache", q, k, v, q_out),
-                                _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
+                                qp, qs, kp, ks, vp, vs,
                                 _dense(position, "int32", "rq_qkv_to_cache: position"),
                                 _rows(q_out, "rq_qkv_to_cache: q_out"), cache.address,
                                 _dense(slot, "int64", "rq_qkv_to_cache: slot"), tokens,
@@ -402,9 +420,9 @@ def rq_qkv_to_cache(params, q, k, v, position, q_out, cache, slot, tokens, dtype
 def rq_kv_write(cache, k, v, slot, tokens, dtype=None, k_stride=None, v_stride=None,
                 stream=None):
     """Quantize k and v rows into the cache at slot (int64)."""
-    ks = _row_stride(k, cache.kv_heads, cache.head_dim, k_stride, "rq_kv_write: k")
-    vs = _row_stride(v, cache.kv_heads, cache.head_dim, v_stride, "rq_kv_write: v")
-    _check(_lib.rq_kv_write(cache.address, _dtype(dtype, "rq_kv_write", k, v), _ptr(k), ks, _ptr(v), vs,
+    kp, ks = _strided_rows(k, cache.kv_heads, cache.head_dim, k_stride, "rq_kv_write: k")
+    vp, vs = _strided_rows(v, cache.kv_heads, cache.head_dim, v_stride, "rq_kv_write: v")
+    _check(_lib.rq_kv_write(cache.address, _dtype(dtype, "rq_kv_write", k, v), kp, ks, vp, vs,
                             _dense(slot, "int64", "rq_kv_write: slot"), tokens, _stream(stream)),
            "rq_kv_write")
 
@@ -421,6 +439,7 @@ def rq_verify_chain(token, p, q, u, accepted, next, batch, drafts, vocab, stream
     """Keep or reject chains of drafts and draw the next token (q may be None)."""
     _check(_lib.rq_verify_chain(_dense(token, "int32", "rq_verify_chain: token"),
                                 _dense(p, "float32", "rq_verify_chain: p"),
+                                None if q is None else
                                 _dense(q, "float32", "rq_verify_chain: q"),
                                 _dense(u, "float32", "rq_verify_chain: u"),
                                 _dense(accepted, "int32", "rq_verify_chain: accepted"),
@@ -520,19 +539,20 @@ class Context:
         page_table [batch, max_pages] and length are dense int32 tensors (of a
         wider table, its part in use is taken as a dense copy, or the table
         whole)."""
-        qs = _row_stride(q, q_heads, cache.head_dim, q_stride, "rq_cache_attention: q")
+        qp, qs = _strided_rows(q, q_heads, cache.head_dim, q_stride, "rq_cache_attention: q")
         if not isinstance(page_table, int):
             shape = page_table.shape
             if len(shape) != 2 or max_pages not in (None, shape[1]):
                 raise RqError(2, "rq_cache_attention: page_table is [batch, max_pages]")
             max_pages = shape[1]
         _check(_lib.rq_cache_attention(self._h, cache.address,
-                                       _dtype(dtype, "rq_cache_attention", q, out), _ptr(q), qs,
+                                       _dtype(dtype, "rq_cache_attention", q, out), qp, qs,
                                        _rows(out, "rq_cache_attention: out"), batch, new_tokens,
                                        q_heads,
                                        _dense(page_table, "int32", "rq_cache_attention: page_table"),
                                        max_pages,
                                        _dense(length, "int32", "rq_cache_attention: length"),
+                                       None if tree is None else
                                        _dense(tree, "int64|uint64", "rq_cache_attention: tree"),
                                        scale, _stream(stream)), "rq_cache_attention")
 

@@ -35,15 +35,19 @@ constexpr int kFlush = 16;
 
 // rq_attn_rows.cu's kernel runs from kManyRows query rows per kv head on, for
 // launches of at least kManyWork: rows times keys (the places that the page
-// table has room for), and kBeginning keys more a row for what beginning its 8
-// rows costs here.  It costs about 20 us before and after its products and
-// then hardly more for 112 rows than for 8, this file's kernel 8 us and then a
-// pass over the cache for every 8 rows.  Measured, that / this (28 query heads,
-// 4 kv heads of 128, microseconds): 8 sequences of 8000 tokens, 21 rows 48 /
-// 37, 28 rows 48 / 47, 42 rows 48 / 62, 112 rows 49 / 126; of 2000 tokens, 42
-// rows (3.3e6) 29 / 27, 56 rows (4.4e6) 29 / 30; one of 8000, 84 rows (2.8e6)
-// 30 / 24, 112 rows (3.8e6) 31 / 32; prompts of 100 tokens behind 50 (1.7e6)
-// 16 / 13, 200 behind 10 (3.7e6) 18 / 22, 400 behind 100 (10e6) 23 / 53.
+// table has room for: the lengths are on the device), and kBeginning keys more
+// a row for what beginning its 8 rows costs here.  It costs about 20 us before
+// and after its products and then hardly more for 112 rows than for 8, this
+// file's kernel 8 us and then a pass over the cache for every 8 rows.
+// Measured, that / this (28 query heads, 4 kv heads of 128, bf16, tables that
+// fit, cold L2, microseconds with the events' own 6): 8 sequences of 8000
+// tokens, 21 rows 59 / 45, 28 rows 59 / 55, 42 rows 61 / 68, 112 rows 61 / 133;
+// of 2000 tokens, 42 rows (3.3e6) 37 / 33, 56 rows (4.4e6) 37 / 35; one of
+// 8000, 84 rows (2.8e6) 35 / 29, 112 rows (3.8e6) 35 / 37; prompts of 100
+// tokens behind 50 (1.7e6) 23 / 18, 200 behind 10 (3.7e6) 25 / 27, 400 behind
+// 100 (10e6) 29 / 57.  f32 takes that kernel 4 to 10 us more and this one the
+// same.  Where the table has room to spare the choice can be the dearer one: 8
+// tokens behind 500 take 14 us with a table of 9 pages and 31 with one of 2048.
 constexpr int kManyRows = 32;
 constexpr int kBeginning = 400;
 constexpr double kManyWork = 3.4e6;
@@ -56,10 +60,10 @@ struct Geometry {
   // As many warps on an SM as the registers hold: the output rows alone are
   // D / 2 registers a thread, the query rows D / 4.  WIDE: in one CTA, for
   // launches of no more segments than SMs, where a CTA has one part of one
-  // segment (one token over 500 cached ones 8.2 us against 10.4 in two, over
-  // 131000 32.1 against 36.1).  Otherwise in two, so that one streams while
+  // segment (one token over 500 cached ones 8.6 us against 10.9 in two, over
+  // 131000 33.3 against 40.1).  Otherwise in two, so that one streams while
   // the other begins or joins a segment (64 sequences of up to 8192 tokens
-  // 153 us, 182 in one).
+  // 155 us, 165 in one).
   static constexpr int kCtas = WIDE ? 1 : 2;
   static constexpr int kWarps = (D == 64 ? 16 : D == 128 ? 12 : 8) / kCtas;
   static constexpr int kThreads = 32 * kWarps;

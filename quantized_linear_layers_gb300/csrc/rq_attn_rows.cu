@@ -16,11 +16,13 @@
 // rows (64 + 64 keys in S's 64 columns), and P V takes A = P from TMEM and
 // adds to O in TMEM.  While a row tile's softmax runs, the tensor cores work
 // on its next scores and on the other tile.  f32 rows take both products
-// twice (Q high and low, P high and low), 16-bit rows once.
+// twice (Q high and low, P high and low), 16-bit rows once: their P is rounded
+// to f16, 11 bits, which is finer than a bf16 output and as fine as an f16 one,
+// and a second product would cost them 0.3 us a unit.
 //
 // Measured (28 query, 4 kv heads of 128): trees of 48 over 8 sequences of 8000
-// tokens, f32, 118 us (292 TFLOP/s, each product counted once); two prompts of
-// 1500 tokens behind 600, bf16, 109 us (502 TFLOP/s).  A unit of 256 rows takes
+// tokens, f32, 118 us (291 TFLOP/s, each product counted once); two prompts of
+// 1500 tokens behind 600, bf16, 110 us (498 TFLOP/s).  A unit of 256 rows takes
 // 1.4 us in bf16, 1.7 in f32, of which the tensor pipe works 0.6 and 1.25.  No
 // pipe is full: what bounds it is the way from scores over softmax, barrier,
 // products and barrier back to scores (all exponentials, scales and maxima

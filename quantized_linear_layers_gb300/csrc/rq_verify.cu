@@ -15,10 +15,12 @@
 // cluster barrier per draw, no scratch, no atomics across CTAs, one launch;
 // the walk down a tree is a loop of draws inside it.
 //
-// Bound by how many loads 8 SMs a sequence keep in flight: 32 chains of 7
-// drafts over 131072 entries take 11.9 us, 2.8 TB/s of the rows that they
-// read; a tree by the latency of its draws one after another, about 3 us each
-// (6 trees of 40 drafts over 50001 entries: 13 to 15 us).
+// Bound by steps one after another: 32 chains of 7 drafts take 5 us over 1000
+// entries already (the drafts' test, the sum, the cluster barrier, and two
+// searches by one warp that reads its part of the row again), and 10.5 over
+// 131072, of which reading the rows is the rest (in a replayed graph; 11.4 with
+// cold inputs and the host's call).  A tree's draws follow one another, about 3
+// us each (6 trees of 40 drafts over 50001 entries, up to four draws: 13.2 us).
 #include "rq_device.cuh"
 #include "rq_internal.h"
 

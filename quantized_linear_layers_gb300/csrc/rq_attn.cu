@@ -774,7 +774,10 @@ rq_status launch_cache_attention(const AttnCall& call, AttnScratch* scratch, cud
 rq_status AttnScratch::reserve(cudaStream_t st) {
   if (part != nullptr) return RQ_OK;
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(st, &capture) != cudaSuccess) return RQ_ERR_CUDA;
+  if (cudaStreamIsCapturing(st, &capture) != cudaSuccess) {
+    cudaGetLastError();  // (the legacy stream while another one is captured)
+    return RQ_ERR_ALLOC;
+  }
   if (capture != cudaStreamCaptureStatusNone) return RQ_ERR_ALLOC;
   const size_t ctas = 2 * (size_t)device_sm_count();
   const size_t few = sizeof(float) * 2 * ctas * kRows * (256 + 4);

@@ -301,6 +301,148 @@ rq_status rq_fp8_linear_noalloc(const float *x, const uint8_t *w_fp8,
 /* Forget the cached FP8 activation (bump the generation). */
 rq_status rq_act_cache_invalidate(rq_ctx *ctx);
 
+/* --------------------------------- FP8 product with a fused epilogue --- */
+
+/* What is done to a product's sums before they are stored, in f32:
+ *   y = residual + mul * act(sum + bias),  rounded once, to y's type.
+ *   bias: f32 [N], 4-byte aligned, or NULL.   act: rq_act.
+ *   mul, residual: [M][N] of y's type, consecutive tokens mul_stride /
+ *     residual_stride elements apart (at least N), or NULL.  mul is the up
+ *     product of a gated layer, say; residual the stream that the block's
+ *     output is added to.  Either may be y itself, with y's stride; neither
+ *     may overlap y in another way.
+ * SiLU z / (1 + e^-z); GELU z/2 (1 + erf(z / sqrt 2)); GELU_TANH z/2 (1 +
+ * tanh(sqrt(2/pi) (z + 0.044715 z^3))); RELU max(z, 0) (a NaN stays one).  The struct is read
+ * on the host during the call. */
+typedef enum {
+    RQ_ACT_NONE = 0,
+    RQ_ACT_SILU = 1,
+    RQ_ACT_GELU = 2,
+    RQ_ACT_GELU_TANH = 3,
+    RQ_ACT_RELU = 4
+} rq_act;
+
+typedef struct {
+    const float *bias;
+    int act; /* rq_act */
+    const void *mul, *residual;
+    int64_t mul_stride, residual_stride;
+} rq_epilogue;
+
+/* rq_fp8_gemm with an epilogue and an output of dtype (RQ_F32, RQ_F16,
+ * RQ_BF16; see below), tokens y_stride elements apart (at least N):
+ *   sum[m, n] = (sum_k e4m3(x_fp8[m, k]) * e4m3(w_fp8[n, k]))
+ *               * (*x_dequant) * (*w_dequant).
+ * x_fp8, w_fp8 and the scales as for rq_fp8_gemm, for any M from a single
+ * token on; y, mul and residual need their element's alignment only.
+ * Accuracy of the sums: the tensor cores add in f32 and cut off; measured
+ * about 6e-8 of the result for K up to 4096 and 1.5e-6 at K = 18944.
+ * epilogue_host NULL: the product alone.  Equal calls give equal bits.
+ * Errors: RQ_ERR_NULL, RQ_ERR_QTYPE (dtype or act), RQ_ERR_SHAPE (as
+ * rq_fp8_gemm, strides, alignment), RQ_ERR_CUDA. */
+rq_status rq_fp8_gemm_epilogue(const uint8_t *x_fp8, const float *x_dequant,
+                               const uint8_t *w_fp8, const float *w_dequant,
+                               const rq_epilogue *epilogue_host, int dtype, void *y,
+                               int64_t y_stride, int M, int N, int K,
+                               rq_stream_t stream);
+
+/* The FP8 route of rq_linear with an epilogue, at every M (the threshold does
+ * not apply: the weight is read as one byte per value even for one token):
+ * FP8 weight cache, FP8 activation of x with its cache (both as rq_linear's,
+ * and shared with it), rq_fp8_gemm_epilogue.
+ * Errors: RQ_ERR_QTYPE (qtype, dtype or act), those of rq_linear and of
+ * rq_fp8_gemm_epilogue. */
+rq_status rq_linear_epilogue(rq_ctx *ctx, rq_qtype qtype, const void *w, const float *x,
+                             const rq_epilogue *epilogue_host, int dtype, void *y,
+                             int64_t y_stride, int M, int N, int K, rq_stream_t stream);
+
+/* ------------------------------------- norms between a layer's blocks -- */
+
+/* What stands between two blocks, fixed for the layer:
+ *   width: values per token, 1 .. 16384.
+ *   norms: RQ_NORM_POST and RQ_NORM_PRE, either or both or none.  A norm is
+ *     x * rsqrt(mean(x^2) + eps) * weight over the token's values.
+ *   post_weight, pre_weight: f32 [width], 4-byte aligned, or NULL for ones.
+ *   scale: multiplies the block's output (finite). */
+typedef enum { RQ_NORM_POST = 1, RQ_NORM_PRE = 2 } rq_norms;
+
+typedef struct {
+    const float *post_weight, *pre_weight;
+    int width;
+    int norms;
+    float eps, scale;
+} rq_norm_params;
+
+/* The norm after a block, its gated and scaled sum with the residual stream
+ * and the norm before the next block, in one pass over each token:
+ *   h' = h + scale * (gate * post(y)),     x = pre(h').
+ *   y: [tokens][width] of dtype, the block's output, tokens y_stride elements
+ *     apart; NULL for none (h' = h; h_out must be NULL then).
+ *   gate: [width] of dtype with gate_stride 0, one for all tokens, or
+ *     [tokens][width] with gate_stride elements between tokens; NULL: ones.
+ *   h: [tokens][width] of h_dtype, which is dtype or RQ_F32, h_stride.
+ *   h_out: like h, dense, or NULL.   x_out: [tokens][width] of dtype, dense,
+ *     or NULL (not both).  h_out may be h and x_out may be y where those are
+ *     dense; otherwise outputs overlap nothing.
+ *   absmax_bits: one device word, or NULL: IEEE bits of the largest |x| over
+ *     all tokens, NaNs skipped, as rq_absmax leaves it (so that rq_quant_e4m3
+ *     can follow).  Needs dtype RQ_F32 and x_out; written whatever was there.
+ * All arithmetic is f32; x is taken from h' before h' is rounded to h_dtype.
+ * Strides are at least width; every pointer needs its element's alignment
+ * (16-byte aligned rows of a multiple of 16 bytes are read 16 bytes at a
+ * time).  tokens == 0 does nothing (but sets *absmax_bits to 0).
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_QTYPE (dtype, h_dtype, or
+ * absmax_bits with 16-bit x), RQ_ERR_CUDA. */
+rq_status rq_residual_norm(const rq_norm_params *params_host, int dtype, const void *y,
+                           int64_t y_stride, const void *gate, int64_t gate_stride,
+                           int h_dtype, const void *h, int64_t h_stride, void *h_out,
+                           void *x_out, uint32_t *absmax_bits, int tokens,
+                           rq_stream_t stream);
+
+/* -------------------------------------------- the places of a pass ----- */
+
+/* Cache slots, positions and page tables of a pass's new tokens, from the
+ * lengths of its sequences, on the GPU:
+ *   length: int32 [batch], cached tokens of each sequence (< 0: unused, it has
+ *     no new tokens).   count: int32 [batch], its new tokens (below 0 counts as
+ *     0), or NULL: new_tokens each.
+ *   new_tokens > 0: `rows` = batch * new_tokens rows, row b * new_tokens + i is
+ *     new token i of sequence b (the layout of rq_cache_attention); a count
+ *     above new_tokens is cut to it and records RQ_ERR_INDEX.
+ *   new_tokens == 0: the tokens of the sequences one behind another in `rows`
+ *     rows (count is needed); what does not fit has no row and records
+ *     RQ_ERR_INDEX.
+ *   page_table: int32 [batch][max_pages], in and out.  The first
+ *     ceil(length / page_size) entries are read; the entries of pages that the
+ *     new tokens begin are written; all others stay as they are.
+ *   free_pages: int32 [free_capacity], a stack of unused pages, of which the
+ *     first *free_count (a device word) are valid.  New pages are taken from
+ *     its end: page i of the pass, counted over the sequences in order, is
+ *     free_pages[*free_count - 1 - i].
+ *   free_left: one device word, *free_count less the pages that the pass
+ *     needs; below zero where the stack did not hold enough.  Must not be
+ *     free_count.
+ *   slot: int64 [rows], page * page_size + offset; position: int32 [rows], the
+ *     token's place in its sequence; sequence: int32 [rows] or NULL.  Rows
+ *     without a token (padding, unused sequences) get slot -1, which writes
+ *     nothing, position 0 and sequence -1.
+ *   row_start: int32 [batch + 1] or NULL, the first row of each sequence and
+ *     the rows used.   next_length: int32 [batch] or NULL, length + count (an
+ *     unused sequence's length as it is); must not be length.
+ * A token whose page is missing (past the table or the stack, or a negative
+ * entry) gets slot -1 and records RQ_ERR_INDEX (rq_get_device_status); a
+ * missing new page is written as -1 where the table has room.
+ * page_size: 16, 32, 64, 128 or 256.  batch <= 65536, max_pages >= 1.
+ * batch == 0 does nothing but fill `rows` and free_left.  int32 arrays are
+ * 4-byte aligned, slot 8-byte.  One launch, no scratch.
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_CUDA. */
+rq_status rq_batch_plan(const int32_t *length, const int32_t *count, int batch,
+                        int new_tokens, int page_size, int32_t *page_table,
+                        int max_pages, const int32_t *free_pages, int free_capacity,
+                        const int32_t *free_count, int32_t *free_left, int64_t *slot,
+                        int32_t *position, int32_t *sequence, int rows,
+                        int32_t *row_start, int32_t *next_length, rq_stream_t stream);
+
 /* ------------------------------------------ quantized K/V cache ------- */
 
 /* The steps of a decoder layer between its q/k/v products and its o product,
@@ -502,6 +644,53 @@ rq_status rq_verify_chain(const int32_t *token, const float *p, const float *q,
 rq_status rq_verify_tree(const int32_t *token, const int32_t *parent, const float *p,
                          const float *u, int32_t *accepted, int32_t *next,
                          int32_t *path, int batch, int drafts, int vocab,
+                         rq_stream_t stream);
+
+/* ---------------------------------------- from logits to tokens -------- */
+
+/* Each row's own filters: device arrays [rows], 4-byte aligned; NULL leaves a
+ * filter out for every row.  The struct is read on the host during the call.
+ *   temperature T (NULL: 1).  T <= 0 or NaN: the likeliest token alone.
+ *   top_k: <= 0 is off.   top_p: >= 1 or NaN is off.   min_p: <= 0 or NaN is
+ *   off, above 1 counts as 1. */
+typedef struct {
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p;
+    const float *min_p;
+} rq_sampling;
+
+/* The distribution that a token is drawn from.  Tokens stand in order of their
+ * logits, largest first, equal ones by index, and have whole weights
+ *   W = floor(2^42 e^((logit - largest) / T))
+ * (2^42 for the largest itself; the others within one of that, from a power
+ * carried to about 2^-43).  A NaN counts as -Inf; next to +Inf all
+ * finite logits weigh 0.  A token stays if
+ *   W > 0 and W >= min_p 2^42                                   (min-p),
+ *   fewer than top_k of those stand before it                   (top-k), and
+ *   the weights before it, of what those two leave, sum to less than top_p
+ *   times their total; the first always stays                   (top-p).
+ * Sums are whole numbers of 64 bits, so no order of summation matters. */
+
+/* Draw a token per row from u: f32 [rows] random numbers in [0, 1), as
+ * rq_verify_chain draws: the first token by index whose running sum of staying
+ * weights exceeds floor(U total / 2^24), U = floor(u 2^24) limited to 0 ..
+ * 2^24-1.
+ *   logits: [rows][vocab] of dtype, rows `stride` elements apart (at least
+ *   vocab), aligned to their element.   token: int32 [rows]; -1 for a row of
+ *   NaN and -Inf only.
+ * 1 <= vocab <= 2^20, 0 <= rows <= 2^27 (0 does nothing).  No scratch.
+ * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_QTYPE (dtype), RQ_ERR_CUDA. */
+rq_status rq_sample(const rq_sampling *sampling_host, int dtype, const void *logits,
+                    int64_t stride, const float *u, int32_t *token, int rows, int vocab,
+                    rq_stream_t stream);
+
+/* The same distribution written out, as rq_verify_chain and rq_verify_tree
+ * take it:  p: f32 [rows][vocab], dense, W / total of the tokens that stay and
+ * 0 elsewhere (a row of NaN and -Inf only: zeros); must not overlap the logits.
+ * Errors: as rq_sample. */
+rq_status rq_token_probs(const rq_sampling *sampling_host, int dtype, const void *logits,
+                         int64_t stride, float *p, int rows, int vocab,
                          rq_stream_t stream);
 
 /* ----------------------------------------------------------- tracing --- */

@@ -21,6 +21,10 @@ RQ_Q4K = 12
 RQ_Q6K = 14
 RQ_F32, RQ_F16, RQ_BF16 = 0, 1, 2
 RQ_KV_E4M3, RQ_KV_I8 = 0, 1
+RQ_NORM_POST, RQ_NORM_PRE = 1, 2
+RQ_ACT_NONE, RQ_ACT_SILU, RQ_ACT_GELU, RQ_ACT_GELU_TANH, RQ_ACT_RELU = range(5)
+ACTIVATIONS = {"none": RQ_ACT_NONE, "silu": RQ_ACT_SILU, "gelu": RQ_ACT_GELU,
+               "gelu_tanh": RQ_ACT_GELU_TANH, "relu": RQ_ACT_RELU}
 STATUS = {0: "RQ_OK", 1: "RQ_ERR_NULL", 2: "RQ_ERR_SHAPE", 3: "RQ_ERR_QTYPE",
           4: "RQ_ERR_NOT_CACHED", 5: "RQ_ERR_ALLOC", 6: "RQ_ERR_CUDA",
           7: "RQ_ERR_TIMEOUT", 8: "RQ_ERR_ARCH", 9: "RQ_ERR_INDEX"}
@@ -77,6 +81,16 @@ _SIGS = {
     "rq_cache_attention": ([_vp, _vp, _i32, _vp, _i64, _vp, _i32, _i32, _i32, _vp, _i32, _vp,
                             _vp, ctypes.c_float, _vp], _i32),
     "rq_ctx_attention_launches": ([_vp, _vp, _vp], _i32),
+    "rq_fp8_gemm_epilogue": ([_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _i32, _i32, _i32, _vp],
+                             _i32),
+    "rq_linear_epilogue": ([_vp, _i32, _vp, _vp, _vp, _i32, _vp, _i64, _i32, _i32, _i32, _vp],
+                           _i32),
+    "rq_residual_norm": ([_vp, _i32, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _i32,
+                          _vp], _i32),
+    "rq_batch_plan": ([_vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
+                       _i32, _vp, _vp, _vp], _i32),
+    "rq_sample": ([_vp, _i32, _vp, _i64, _vp, _vp, _i32, _i32, _vp], _i32),
+    "rq_token_probs": ([_vp, _i32, _vp, _i64, _vp, _i32, _i32, _vp], _i32),
     "rq_verify_chain": ([_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp], _i32),
     "rq_verify_tree": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp], _i32),
 }
@@ -459,6 +473,192 @@ def rq_verify_tree(token, parent, p, u, accepted, next, path, batch, drafts, voc
                                _stream(stream)), "rq_verify_tree")
 
 
+# ------------------------------------------------------------------------
+# The steps of a pass between the linears.  Their tensors lie on the current
+# device; their addresses (ints) are vouched for by the caller.
+
+_current_device = None      # index of torch's current device
+
+
+def _here(t, where):
+    """Address of a tensor on the current device (None stays None)."""
+    global _current_device
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise RqError(2, where + " is not on the GPU")
+    if _current_device is None:
+        import torch
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    if t.get_device() != _current_device():
+        raise RqError(2, where + " is on another device than the current one")
+    return t.data_ptr()
+
+
+def _array(t, kind, where, count=None):
+    """Address of a dense tensor of dtype `kind`, of `count` entries at least."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype not in _kinds[kind]:
+        raise RqError(3, "%s is not %s" % (where, kind))
+    if not t.is_contiguous() or count is not None and t.numel() < count:
+        raise RqError(2, where + " is not dense, or too short")
+    return _here(t, where)
+
+
+def _matrix(t, rows, cols, where, stride=None, dense=False):
+    """Address of `rows` rows of `cols` elements, and the elements between
+    them: any tensor whose last axis is `cols` dense elements and whose other
+    axes count rows at one distance."""
+    if t is None or isinstance(t, int):
+        return t, cols if stride is None else stride
+    if t.numel() < rows * cols or t.numel() % cols or t.shape[-1] != cols:
+        raise RqError(2, where + " does not hold the rows")
+    at = _here(t, where)
+    if t.is_contiguous():
+        return at, cols
+    if dense:
+        raise RqError(2, where + " is not dense")
+    return at, _view_stride(t, 1, cols, where)
+
+
+class _EpilogueStruct(ctypes.Structure):
+    _fields_ = [("bias", _vp), ("act", _i32), ("mul", _vp), ("residual", _vp),
+                ("mul_stride", _i64), ("residual_stride", _i64)]
+
+
+class _NormStruct(ctypes.Structure):
+    _fields_ = [("post_weight", _vp), ("pre_weight", _vp), ("width", _i32), ("norms", _i32),
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class _SamplingStruct(ctypes.Structure):
+    _fields_ = [("temperature", _vp), ("top_k", _vp), ("top_p", _vp), ("min_p", _vp)]
+
+
+def _epilogue(where, M, N, y, act, bias, mul, residual, dtype):
+    """(epilogue struct, dtype, y's address and stride)."""
+    if isinstance(act, str):
+        if act not in ACTIVATIONS:
+            raise RqError(3, "%s: no activation %r" % (where, act))
+        act = ACTIVATIONS[act]
+    dtype = _dtype(dtype, where, y, mul, residual)
+    yp, ys = _matrix(y, M, N, where + ": y")
+    mp, ms = _matrix(mul, M, N, where + ": mul")
+    rp, rs = _matrix(residual, M, N, where + ": residual")
+    bp = _array(bias, "float32", where + ": bias", N)
+    return _EpilogueStruct(bp, act, mp, rp, ms, rs), dtype, yp, ys
+
+
+_E4M3 = "float8_e4m3fn|uint8"
+
+
+def rq_fp8_gemm_epilogue(x_fp8, x_dequant, w_fp8, w_dequant, y, M, N, K, act="none", bias=None,
+                         mul=None, residual=None, dtype=None, stream=None):
+    """y = residual + mul * act(x . w^T + bias) of E4M3 operands; y, mul and
+    residual are [M, N] of one type (rows may be apart), bias f32 [N]."""
+    e, dtype, yp, ys = _epilogue("rq_fp8_gemm_epilogue", M, N, y, act, bias, mul, residual, dtype)
+    _check(_lib.rq_fp8_gemm_epilogue(
+        _array(x_fp8, _E4M3, "rq_fp8_gemm_epilogue: x_fp8", (M + 15) // 16 * 16 * K),
+        _array(x_dequant, "float32", "rq_fp8_gemm_epilogue: x_dequant", 1),
+        _array(w_fp8, _E4M3, "rq_fp8_gemm_epilogue: w_fp8", N * K),
+        _array(w_dequant, "float32", "rq_fp8_gemm_epilogue: w_dequant", 1), ctypes.byref(e), dtype,
+        yp, ys, M, N, K, _stream(stream)), "rq_fp8_gemm_epilogue")
+
+
+class NormParams:
+    """What stands between two blocks of a layer (rq_norm_params): which norms,
+    their f32 weights [width] (None: ones), eps and the block output's scale."""
+
+    def __init__(self, width, post=True, pre=True, post_weight=None, pre_weight=None, eps=1e-6,
+                 scale=1.0):
+        at = [_array(t, "float32", "NormParams: weight", width)
+              for t in (post_weight, pre_weight)]
+        self.tensors = (post_weight, pre_weight)
+        self.width = width
+        self.struct = _NormStruct(at[0], at[1], width,
+                                  (RQ_NORM_POST if post else 0) | (RQ_NORM_PRE if pre else 0),
+                                  eps, scale)
+        self.address = ctypes.addressof(self.struct)
+
+
+def rq_residual_norm(params, y, h, h_out, x_out, tokens, gate=None, absmax_bits=None, dtype=None,
+                     h_dtype=None, stream=None):
+    """h_out = h + scale * (gate * post(y)), x_out = pre(h_out).  y None: no
+    block before; gate: [width], or [tokens, width] like y; either output may
+    be None."""
+    n, where = params.width, "rq_residual_norm"
+    dtype = _dtype(dtype, where, y, gate, x_out) if dtype is not None or y is not None or \
+        x_out is not None else _dtype(None, where, h)
+    h_dtype = _dtype(h_dtype, where, h, h_out)
+    yp, ys = _matrix(y, tokens, n, where + ": y")
+    hp, hs = _matrix(h, tokens, n, where + ": h")
+    gp, gs = None, 0
+    if gate is not None:
+        per_token = isinstance(gate, int) or gate.dim() > 1
+        gp, gs = _matrix(gate, tokens if per_token else 1, n, where + ": gate")
+        gs = gs if per_token else 0
+    _check(_lib.rq_residual_norm(params.address, dtype, yp, ys, gp, gs, h_dtype, hp, hs,
+                                 _matrix(h_out, tokens, n, where + ": h_out", dense=True)[0],
+                                 _matrix(x_out, tokens, n, where + ": x_out", dense=True)[0],
+                                 _array(absmax_bits, "int32|uint32", where + ": absmax_bits", 1),
+                                 tokens, _stream(stream)), where)
+
+
+def rq_batch_plan(length, page_table, free_pages, free_count, free_left, slot, position, page_size,
+                  count=None, new_tokens=0, sequence=None, row_start=None, next_length=None,
+                  stream=None):
+    """Slots, positions and new page-table entries of a pass's new tokens:
+    `count` of each sequence in batch * new_tokens rows, or with new_tokens 0
+    one behind another in as many rows as `slot` has."""
+    where = "rq_batch_plan"
+    if len(page_table.shape) != 2 or page_table.shape[0] != length.numel():
+        raise RqError(2, where + ": page_table is [batch, max_pages]")
+    batch, max_pages = page_table.shape
+    rows = slot.numel()
+    _check(_lib.rq_batch_plan(
+        _array(length, "int32", where + ": length"),
+        _array(count, "int32", where + ": count", batch), batch, new_tokens, page_size,
+        _array(page_table, "int32", where + ": page_table"), max_pages,
+        _array(free_pages, "int32", where + ": free_pages"), free_pages.numel(),
+        _array(free_count, "int32", where + ": free_count", 1),
+        _array(free_left, "int32", where + ": free_left", 1),
+        _array(slot, "int64", where + ": slot"),
+        _array(position, "int32", where + ": position", rows),
+        _array(sequence, "int32", where + ": sequence", rows), rows,
+        _array(row_start, "int32", where + ": row_start", batch + 1),
+        _array(next_length, "int32", where + ": next_length", batch), _stream(stream)), where)
+
+
+def _sampling(where, rows, temperature, top_k, top_p, min_p):
+    return _SamplingStruct(_array(temperature, "float32", where + ": temperature", rows),
+                           _array(top_k, "int32", where + ": top_k", rows),
+                           _array(top_p, "float32", where + ": top_p", rows),
+                           _array(min_p, "float32", where + ": min_p", rows))
+
+
+def rq_sample(logits, u, token, rows, vocab, temperature=None, top_k=None, top_p=None, min_p=None,
+              dtype=None, stride=None, stream=None):
+    """A token per row of logits, drawn with u from what the filters leave; the
+    filters are tensors [rows] or None."""
+    f = _sampling("rq_sample", rows, temperature, top_k, top_p, min_p)
+    at, step = _matrix(logits, rows, vocab, "rq_sample: logits", stride)
+    _check(_lib.rq_sample(ctypes.byref(f), _dtype(dtype, "rq_sample", logits), at, step,
+                          _array(u, "float32", "rq_sample: u", rows),
+                          _array(token, "int32", "rq_sample: token", rows), rows, vocab,
+                          _stream(stream)), "rq_sample")
+
+
+def rq_token_probs(logits, p, rows, vocab, temperature=None, top_k=None, top_p=None, min_p=None,
+                   dtype=None, stride=None, stream=None):
+    """The probabilities p (f32 [rows, vocab]) of what the filters leave."""
+    f = _sampling("rq_token_probs", rows, temperature, top_k, top_p, min_p)
+    at, step = _matrix(logits, rows, vocab, "rq_token_probs: logits", stride)
+    _check(_lib.rq_token_probs(ctypes.byref(f), _dtype(dtype, "rq_token_probs", logits), at, step,
+                               _array(p, "float32", "rq_token_probs: p", rows * vocab), rows,
+                               vocab, _stream(stream)), "rq_token_probs")
+
+
 class Context:
     """Owns an rq_ctx: FP8 weight cache, activation scratch, device scalars."""
 
@@ -530,6 +730,20 @@ class Context:
     def rq_linear(self, qtype, w, x, y, M, N, K, stream=None):
         _check(_lib.rq_linear(self._h, qtype, _ptr(w), _ptr(x), _ptr(y), M, N, K,
                               _stream(stream)), "rq_linear")
+
+    def rq_linear_epilogue(self, qtype, w, x, y, M, N, K, act="none", bias=None, mul=None,
+                           residual=None, dtype=None, stream=None):
+        """The FP8 route of rq_linear with the epilogue of
+        rq_fp8_gemm_epilogue, at every M."""
+        where = "rq_linear_epilogue"
+        e, dtype, yp, ys = _epilogue(where, M, N, y, act, bias, mul, residual, dtype)
+        if not isinstance(w, int) and (not w.is_contiguous() or w.numel() * w.element_size() <
+                                       N * (K // 256) * (144 if qtype == RQ_Q4K else 210)):
+            raise RqError(2, where + ": w is not dense, or too short")
+        _check(_lib.rq_linear_epilogue(self._h, qtype, _here(w, where + ": w"),
+                                       _array(x, "float32", where + ": x", M * K),
+                                       ctypes.byref(e), dtype, yp, ys, M, N, K,
+                                       _stream(stream)), where)
 
     def rq_cache_attention(self, cache, q, out, page_table, length, batch, new_tokens, q_heads,
                            scale, tree=None, max_pages=None, dtype=None, q_stride=None,

@@ -16,7 +16,7 @@ OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "librq.so")
 SOURCES = ["rq_api.cu", "rq_quant.cu", "rq_gemv.cu", "rq_wcache.cu", "rq_gemm.cu",
            "rq_noalloc.cu", "rq_kv.cu", "rq_attn.cu", "rq_attn_rows.cu",
-           "rq_verify.cu"]
+           "rq_verify.cu", "rq_norm.cu", "rq_plan.cu", "rq_sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-Wall", "--expt-relaxed-constexpr"]

@@ -600,13 +600,149 @@ rq_status rq_linear_group(rq_ctx* ctx, int count, const rq_qtype* qtypes, const 
                                K, st, hit);
 }
 
-// ------------------------------------------------- quantized K/V cache --
-
 static rq_status check_dtype(int dtype) {
   return dtype == RQ_F32 || dtype == RQ_F16 || dtype == RQ_BF16 ? RQ_OK : RQ_ERR_QTYPE;
 }
 
 static int width_of(int dtype) { return dtype == RQ_F32 ? 4 : 2; }
+
+// ---------------------------------- FP8 product with a fused epilogue --
+
+static bool stride_ok(int64_t stride, int64_t row) {
+  return stride >= row && stride <= (int64_t)1 << 40;
+}
+
+static rq_status check_epilogue(const rq_epilogue& e, int dtype, const void* y, int64_t y_stride,
+                                int N) {
+  rq_status s = check_dtype(dtype);
+  if (s != RQ_OK) return s;
+  if (e.act < RQ_ACT_NONE || e.act > RQ_ACT_RELU) return RQ_ERR_QTYPE;
+  const int w = width_of(dtype);
+  if (!aligned(y, w) || !aligned(e.mul, w) || !aligned(e.residual, w) || !aligned(e.bias, 4) ||
+      !stride_ok(y_stride, N) || (e.mul != nullptr && !stride_ok(e.mul_stride, N)) ||
+      (e.residual != nullptr && !stride_ok(e.residual_stride, N)))
+    return RQ_ERR_SHAPE;
+  // an operand in y's place has y's stride
+  if ((e.mul == y && e.mul_stride != y_stride) ||
+      (e.residual == y && e.residual_stride != y_stride))
+    return RQ_ERR_SHAPE;
+  return RQ_OK;
+}
+
+rq_status rq_fp8_gemm_epilogue(const uint8_t* x_fp8, const float* x_dequant,
+                               const uint8_t* w_fp8, const float* w_dequant,
+                               const rq_epilogue* epilogue, int dtype, void* y, int64_t y_stride,
+                               int M, int N, int K, rq_stream_t stream) {
+  if (x_fp8 == nullptr || x_dequant == nullptr || w_fp8 == nullptr || w_dequant == nullptr ||
+      y == nullptr)
+    return RQ_ERR_NULL;
+  const rq_epilogue none = {};
+  const rq_epilogue& e = epilogue != nullptr ? *epilogue : none;
+  const rq_status s = check_epilogue(e, dtype, y, y_stride, N);
+  if (s != RQ_OK) return s;
+  if (M < 1 || N < 1 || K < 128 || K % 128 != 0 || !aligned(x_fp8, 16) || !aligned(w_fp8, 16) ||
+      !aligned(x_dequant, 4) || !aligned(w_dequant, 4))
+    return RQ_ERR_SHAPE;
+  return launch_fp8_gemm_epilogue(x_fp8, x_dequant, w_fp8, w_dequant, e, dtype, y, y_stride, M, N,
+                                  K, reinterpret_cast<cudaStream_t>(stream), false);
+}
+
+rq_status rq_linear_epilogue(rq_ctx* ctx, rq_qtype qtype, const void* w, const float* x,
+                             const rq_epilogue* epilogue, int dtype, void* y, int64_t y_stride,
+                             int M, int N, int K, rq_stream_t stream) {
+  if (ctx == nullptr || w == nullptr || x == nullptr || y == nullptr) return RQ_ERR_NULL;
+  rq_status s = check_quant_shape(qtype, N, K);
+  if (s != RQ_OK) return s;
+  const rq_epilogue none = {};
+  const rq_epilogue& e = epilogue != nullptr ? *epilogue : none;
+  s = check_epilogue(e, dtype, y, y_stride, N);
+  if (s != RQ_OK) return s;
+  if (M < 1 || !aligned(w, qtype == RQ_Q4K ? 16 : 4) || !aligned(x, 16)) return RQ_ERR_SHAPE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const uint8_t* wq = nullptr;
+  const float* wdeq = nullptr;
+  const bool miss = ctx->weights.find(WeightKey{w, (int)qtype, N, K}) == ctx->weights.end();
+  {
+    TraceScope ts(miss ? ctx : nullptr, RQ_TRACE_WCACHE, st);
+    ts.kernels(2);  // decode + absmax, decode + encode
+    s = rq_fp8_weight_cache(ctx, qtype, w, N, K, &wq, &wdeq, stream);
+  }
+  if (s != RQ_OK) return s;
+  const uint8_t* xq = nullptr;
+  const float* xdeq = nullptr;
+  s = rq_fp8_act_cache(ctx, x, M, K, &xq, &xdeq, stream);
+  if (s != RQ_OK) return s;
+  TraceScope ts(ctx, RQ_TRACE_GEMM, st);
+  return launch_fp8_gemm_epilogue(xq, xdeq, wq, wdeq, e, dtype, y, y_stride, M, N, K, st, !miss);
+}
+
+// --------------------------------------- norms between a layer's blocks --
+
+rq_status rq_residual_norm(const rq_norm_params* params, int dtype, const void* y,
+                           int64_t y_stride, const void* gate, int64_t gate_stride, int h_dtype,
+                           const void* h, int64_t h_stride, void* h_out, void* x_out,
+                           uint32_t* absmax_bits, int tokens, rq_stream_t stream) {
+  if (params == nullptr ||
+      (tokens != 0 && (h == nullptr || (h_out == nullptr && x_out == nullptr) ||
+                       (y == nullptr && (h_out != nullptr || gate != nullptr)) ||
+                       (absmax_bits != nullptr && x_out == nullptr))))
+    return RQ_ERR_NULL;
+  rq_status s = check_dtype(dtype);
+  if (s != RQ_OK) return s;
+  if ((h_dtype != dtype && h_dtype != RQ_F32) || (absmax_bits != nullptr && dtype != RQ_F32))
+    return RQ_ERR_QTYPE;
+  const int64_t n = params->width;
+  const int w = width_of(dtype), wh = width_of(h_dtype);
+  if (n < 1 || n > 16384 || tokens < 0 || (params->norms & ~(RQ_NORM_POST | RQ_NORM_PRE)) != 0 ||
+      !(params->eps >= 0.0f) || !(params->scale - params->scale == 0.0f) ||
+      !aligned(params->post_weight, 4) || !aligned(params->pre_weight, 4))
+    return RQ_ERR_SHAPE;
+  if (!aligned(y, w) || !aligned(gate, w) || !aligned(h, wh) || !aligned(h_out, wh) ||
+      !aligned(x_out, w) || !aligned(absmax_bits, 4) || !stride_ok(h_stride, n) ||
+      (y != nullptr && !stride_ok(y_stride, n)) ||
+      (gate != nullptr && gate_stride != 0 && !stride_ok(gate_stride, n)))
+    return RQ_ERR_SHAPE;
+  // in place where the input is dense; the two outputs are apart
+  if ((h_out != nullptr && h_out == h && h_stride != n) || (x_out != nullptr && x_out == y && y_stride != n) ||
+      (h_out != nullptr && h_out == x_out) || (x_out != nullptr && (x_out == h || x_out == gate)) ||
+      (h_out != nullptr && (h_out == y || h_out == gate)))
+    return RQ_ERR_SHAPE;
+  return launch_residual_norm(*params, dtype, y, y_stride, gate, gate_stride, h_dtype, h, h_stride,
+                              h_out, x_out, absmax_bits, tokens,
+                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------ the places of a pass --
+
+rq_status rq_batch_plan(const int32_t* length, const int32_t* count, int batch, int new_tokens,
+                        int page_size, int32_t* page_table, int max_pages,
+                        const int32_t* free_pages, int free_capacity, const int32_t* free_count,
+                        int32_t* free_left, int64_t* slot, int32_t* position, int32_t* sequence,
+                        int rows, int32_t* row_start, int32_t* next_length, rq_stream_t stream) {
+  if (free_count == nullptr || free_left == nullptr ||
+      (batch != 0 && (length == nullptr || page_table == nullptr)) ||
+      (free_capacity != 0 && free_pages == nullptr) ||
+      (rows != 0 && (slot == nullptr || position == nullptr)) ||
+      (new_tokens == 0 && batch != 0 && count == nullptr))
+    return RQ_ERR_NULL;
+  if (batch < 0 || batch > 65536 || new_tokens < 0 || max_pages < 1 || free_capacity < 0 ||
+      rows < 0 || (new_tokens > 0 && (int64_t)batch * new_tokens != rows) ||
+      (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 &&
+       page_size != 256))
+    return RQ_ERR_SHAPE;
+  if (!aligned(length, 4) || !aligned(count, 4) || !aligned(page_table, 4) ||
+      !aligned(free_pages, 4) || !aligned(free_count, 4) || !aligned(free_left, 4) ||
+      !aligned(slot, 8) || !aligned(position, 4) || !aligned(sequence, 4) ||
+      !aligned(row_start, 4) || !aligned(next_length, 4) || free_left == free_count ||
+      (next_length != nullptr && next_length == length))
+    return RQ_ERR_SHAPE;
+  return launch_batch_plan(length, count, batch, new_tokens, page_size, page_table, max_pages,
+                           free_pages, free_capacity, free_count, free_left, slot, position,
+                           sequence, rows, row_start, next_length,
+                           reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------- quantized K/V cache --
 
 static bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
 
@@ -810,6 +946,42 @@ rq_status rq_verify_tree(const int32_t* token, const int32_t* parent, const floa
   if (batch == 0) return RQ_OK;
   return launch_verify_tree(token, parent, p, u, accepted, next, path, batch, drafts, vocab,
                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+// -------------------------------------------------- logits to tokens --
+
+static rq_status check_sampling(const rq_sampling* f, int dtype, const void* logits,
+                                int64_t stride, int rows, int vocab) {
+  if (f == nullptr || (rows != 0 && logits == nullptr)) return RQ_ERR_NULL;
+  const rq_status s = check_dtype(dtype);
+  if (s != RQ_OK) return s;
+  if (rows < 0 || rows > (1 << 27) || vocab < 1 || vocab > (1 << 20) || !stride_ok(stride, vocab) ||
+      !aligned(logits, width_of(dtype)) || !aligned(f->temperature, 4) || !aligned(f->top_k, 4) ||
+      !aligned(f->top_p, 4) || !aligned(f->min_p, 4))
+    return RQ_ERR_SHAPE;
+  return RQ_OK;
+}
+
+rq_status rq_sample(const rq_sampling* sampling, int dtype, const void* logits, int64_t stride,
+                    const float* u, int32_t* token, int rows, int vocab, rq_stream_t stream) {
+  if (rows != 0 && (u == nullptr || token == nullptr)) return RQ_ERR_NULL;
+  const rq_status s = check_sampling(sampling, dtype, logits, stride, rows, vocab);
+  if (s != RQ_OK) return s;
+  if (!aligned(u, 4) || !aligned(token, 4)) return RQ_ERR_SHAPE;
+  if (rows == 0) return RQ_OK;
+  return launch_sample(*sampling, dtype, logits, stride, u, token, nullptr, rows, vocab,
+                       reinterpret_cast<cudaStream_t>(stream));
+}
+
+rq_status rq_token_probs(const rq_sampling* sampling, int dtype, const void* logits,
+                         int64_t stride, float* p, int rows, int vocab, rq_stream_t stream) {
+  if (rows != 0 && p == nullptr) return RQ_ERR_NULL;
+  const rq_status s = check_sampling(sampling, dtype, logits, stride, rows, vocab);
+  if (s != RQ_OK) return s;
+  if (rows == 0) return RQ_OK;
+  if (!aligned(p, 4) || static_cast<const void*>(p) == logits) return RQ_ERR_SHAPE;
+  return launch_sample(*sampling, dtype, logits, stride, nullptr, nullptr, p, rows, vocab,
+                       reinterpret_cast<cudaStream_t>(stream));
 }
 
 rq_status rq_ctx_trace_begin(rq_ctx* ctx, int capacity) {

@@ -31,6 +31,7 @@
 #include <cstdlib>
 
 #include "rq_device.cuh"
+#include "rq_elem.cuh"
 #include "rq_internal.h"
 
 namespace rq {
@@ -149,6 +150,49 @@ __device__ __forceinline__ int seg_of(const OutSegs& o, int n) {
   return i;
 }
 
+// What the kernels do with a finished sum.  SegOut: scale and store to the
+// member's f32 output.  FusedOut<T>: y = residual + mul * act(sum + bias) in
+// f32, rounded once to T; y may be mul or residual (each element is read
+// by the thread that then writes it).
+struct SegOut {
+  static constexpr bool kFused = false;
+};
+
+template <typename T>
+struct FusedOut {
+  static constexpr bool kFused = true;
+  using Elem = T;
+  T* y;
+  const T *mul, *residual;  // null: none
+  int64_t y_stride, mul_stride, residual_stride;
+  const float* bias;        // null: none
+  int act;                  // rq_act
+};
+
+// The activation.  16-bit outputs take SiLU's power and quotient from the
+// fast units: their errors, about 2^-21 |z| and 2^-22, are far below half a step of
+// 2^-9; f32 outputs keep the exact functions.
+template <bool kFast>
+__device__ __forceinline__ float activate(float z, int act) {
+  if (act == RQ_ACT_NONE) return z;
+  if (act == RQ_ACT_SILU) {
+    // (z < -88 makes the power +Inf and the quotient -0, its limit)
+    if constexpr (kFast) return z < -80.0f ? -0.0f : __fdividef(z, 1.0f + __expf(-z));
+    return z / (1.0f + expf(-z));
+  }
+  if (act == RQ_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  if (act == RQ_ACT_GELU_TANH) {
+    const float a = 0.79788456080286536f * fmaf(0.044715f * z * z, z, z);
+    return 0.5f * z * (1.0f + tanhf(a));
+  }
+  return z < 0.0f ? 0.0f : z;  // (NaN stays NaN)
+}
+
+template <typename T>
+__device__ __forceinline__ T fused_value(float z, int act, float mul, float residual) {
+  return float_elem<T>(fmaf(mul, activate<sizeof(T) == 2>(z, act), residual));
+}
+
 struct GemmArgs {
   const float* x_deq;
   OutSegs out;
@@ -162,9 +206,41 @@ struct GemmArgs {
   uint64_t wait_limit_ns;
 };
 
+// One warp's part of a tile with an epilogue: TMEM lanes hold output row n of
+// this lane, columns the tokens m0 + c for c in [c_lo, c_hi).  Lanes are
+// neighbouring outputs of one token, so loads and stores are whole segments;
+// sixteen tokens' loads are in flight while the accumulator is read.
+template <typename T>
+__device__ __forceinline__ void fused_columns(const FusedOut<T>& out, uint32_t taddr, int c_lo,
+                                              int c_hi, int m0, int M, int n, bool live,
+                                              float scale_x, float scale_w) {
+  const float bias = live && out.bias != nullptr ? out.bias[n] : 0.0f;
+  for (int c = c_lo; c < c_hi; c += 16) {
+    float mul[16], res[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int m = m0 + c + j;
+      const bool in = live && m < M;
+      mul[j] = in && out.mul != nullptr ? elem_float(out.mul[m * out.mul_stride + n]) : 1.0f;
+      res[j] = in && out.residual != nullptr
+                   ? elem_float(out.residual[m * out.residual_stride + n])
+                   : 0.0f;
+    }
+    uint32_t v[16];
+    tmem_ld16(taddr + (uint32_t)c, v);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int m = m0 + c + j;
+      const float z = fmaf(__uint_as_float(v[j]) * scale_x, scale_w, bias);
+      if (live && m < M) out.y[m * out.y_stride + n] = fused_value<T>(z, out.act, mul[j], res[j]);
+    }
+  }
+}
+
+template <typename Out>
 __global__ void __launch_bounds__(kThreads, 1)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w,
-                const __grid_constant__ CUtensorMap tmap_x, const GemmArgs args) {
+                const __grid_constant__ CUtensorMap tmap_x, const GemmArgs args, const Out out) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -316,18 +392,22 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w,
       const int n = tn * kBM + quad * 32 + lane;
       const int m0 = tm * bn;
       const int sg = seg_of(args.out, n);
-      const int ns = args.out.start[sg + 1] - args.out.start[sg];
-      float* yr = args.out.y[sg] + (n - args.out.start[sg]);
       const float scale_w = n < args.N ? *args.out.w_deq[sg] : 0.f;
       const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * bn);
-      for (int c = 0; c < bn; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(taddr + (uint32_t)c, v);
-        if (n < args.N) {
+      if constexpr (Out::kFused) {
+        fused_columns(out, taddr, 0, bn, m0, args.M, n, n < args.N, scale_x, scale_w);
+      } else {
+        const int ns = args.out.start[sg + 1] - args.out.start[sg];
+        float* yr = args.out.y[sg] + (n - args.out.start[sg]);
+        for (int c = 0; c < bn; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(taddr + (uint32_t)c, v);
+          if (n < args.N) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int m = m0 + c + j;
-            if (m < args.M) yr[(size_t)m * ns] = (__uint_as_float(v[j]) * scale_x) * scale_w;
+            for (int j = 0; j < 16; ++j) {
+              const int m = m0 + c + j;
+              if (m < args.M) yr[(size_t)m * ns] = (__uint_as_float(v[j]) * scale_x) * scale_w;
+            }
           }
         }
       }
@@ -432,9 +512,11 @@ __device__ __forceinline__ void mma_commit_pair_local(uint32_t bar) {
       : "memory");
 }
 
+template <typename Out>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsPair, 1)
 fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_w,
-                     const __grid_constant__ CUtensorMap tmap_x, const GemmArgs args) {
+                     const __grid_constant__ CUtensorMap tmap_x, const GemmArgs args,
+                     const Out out) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -594,18 +676,22 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_w,
       const int n = tn * 256 + (int)rank * kBM + quad * 32 + lane;
       const int m0 = tm * bn;
       const int sg = seg_of(args.out, n);
-      const int ns = args.out.start[sg + 1] - args.out.start[sg];
-      float* yr = args.out.y[sg] + (n - args.out.start[sg]);
       const float scale_w = n < args.N ? *args.out.w_deq[sg] : 0.f;
       const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * bn);
-      for (int c = c_lo; c < c_hi; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(taddr + (uint32_t)c, v);
-        if (n < args.N) {
+      if constexpr (Out::kFused) {
+        fused_columns(out, taddr, c_lo, c_hi, m0, args.M, n, n < args.N, scale_x, scale_w);
+      } else {
+        const int ns = args.out.start[sg + 1] - args.out.start[sg];
+        float* yr = args.out.y[sg] + (n - args.out.start[sg]);
+        for (int c = c_lo; c < c_hi; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(taddr + (uint32_t)c, v);
+          if (n < args.N) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int m = m0 + c + j;
-            if (m < args.M) yr[(size_t)m * ns] = (__uint_as_float(v[j]) * scale_x) * scale_w;
+            for (int j = 0; j < 16; ++j) {
+              const int m = m0 + c + j;
+              if (m < args.M) yr[(size_t)m * ns] = (__uint_as_float(v[j]) * scale_x) * scale_w;
+            }
           }
         }
       }
@@ -668,9 +754,11 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 
 constexpr int kMaxSplits = 8;
 
+template <typename Out>
 __global__ void __launch_bounds__(kThreads, 1)
 fp8_gemm_splitk_kernel(const __grid_constant__ CUtensorMap tmap_w,
-                       const __grid_constant__ CUtensorMap tmap_x, const SplitArgs args) {
+                       const __grid_constant__ CUtensorMap tmap_x, const SplitArgs args,
+                       const Out out) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -822,17 +910,24 @@ fp8_gemm_splitk_kernel(const __grid_constant__ CUtensorMap tmap_w,
   float* yrow[4];
   int ystride[4];
   float rscale[4];
+  float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (Out::kFused) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int ne = n + e;
-    const int sg = seg_of(args.out, ne < args.N ? ne : args.N - 1);
-    ystride[e] = args.out.start[sg + 1] - args.out.start[sg];
-    yrow[e] = ne < args.N ? args.out.y[sg] + (ne - args.out.start[sg]) : nullptr;
-    float sc = seg_scale[0];
+    for (int e = 0; e < 4; ++e)
+      if (out.bias != nullptr && n + e < args.N) bias[e] = out.bias[n + e];
+  } else {
 #pragma unroll
-    for (int i = 1; i < kMaxSegs; ++i)
-      if (sg == i) sc = seg_scale[i];
-    rscale[e] = sc;
+    for (int e = 0; e < 4; ++e) {
+      const int ne = n + e;
+      const int sg = seg_of(args.out, ne < args.N ? ne : args.N - 1);
+      ystride[e] = args.out.start[sg + 1] - args.out.start[sg];
+      yrow[e] = ne < args.N ? args.out.y[sg] + (ne - args.out.start[sg]) : nullptr;
+      float sc = seg_scale[0];
+#pragma unroll
+      for (int i = 1; i < kMaxSegs; ++i)
+        if (sg == i) sc = seg_scale[i];
+      rscale[e] = sc;
+    }
   }
   const uint32_t roff = (uint32_t)(r * 4);
   for (int c = c0 + (int)(threadIdx.x >> 5); c < c1; c += (int)(blockDim.x >> 5)) {
@@ -853,9 +948,27 @@ fp8_gemm_splitk_kernel(const __grid_constant__ CUtensorMap tmap_w,
     const int m = tm * bn + c;
     if (m < args.M) {
       const float o[4] = {sum.x, sum.y, sum.z, sum.w};
+      if constexpr (Out::kFused) {
+        using T = typename Out::Elem;
+        float mul[4], res[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (yrow[e] != nullptr) yrow[e][(size_t)m * ystride[e]] = o[e] * rscale[e];
+        for (int e = 0; e < 4; ++e) {
+          const bool in = n + e < args.N;
+          mul[e] = in && out.mul != nullptr ? elem_float(out.mul[m * out.mul_stride + n + e]) : 1.0f;
+          res[e] = in && out.residual != nullptr
+                       ? elem_float(out.residual[m * out.residual_stride + n + e])
+                       : 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < args.N)
+            out.y[m * out.y_stride + n + e] =
+                fused_value<T>(fmaf(o[e], seg_scale[0], bias[e]), out.act, mul[e], res[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (yrow[e] != nullptr) yrow[e][(size_t)m * ystride[e]] = o[e] * rscale[e];
+      }
     }
   }
   cluster_sync();  // no CTA leaves while a peer may still read its memory
@@ -999,6 +1112,7 @@ int choose_bn_pair(int m_pad, int N, int pairs) {
 }
 
 // Number of CTA pairs of the pair kernel that fit on the GPU at once.
+template <typename Out>
 int resident_pairs(int sms) {
   static int cached = 0;
   if (cached == 0) {
@@ -1007,9 +1121,10 @@ int resident_pairs(int sms) {
     cfg.blockDim = dim3(kThreadsPair);
     cfg.dynamicSmemBytes = kSmemBytes2;
     int n = 0;
-    cudaFuncSetAttribute(fp8_gemm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaFuncSetAttribute(fp8_gemm_pair_kernel<Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          kSmemLimit);
-    if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_pair_kernel, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_pair_kernel<Out>, &cfg) != cudaSuccess ||
+        n < 1) {
       cudaGetLastError();
       n = 1;
     }
@@ -1065,16 +1180,19 @@ static int choose_splits(int m_pad, int N, int K, int sms, int* bn_out) {
   return S < 2 ? 1 : S;
 }
 
+template <typename Out>
 static rq_status launch_fp8_gemm_splitk(const uint8_t* x_fp8, const float* x_deq,
-                                        const uint8_t* w_fp8, const OutSegs& out, int M, int N,
-                                        int K, int bn, int S, bool w_early, cudaStream_t st) {
+                                        const uint8_t* w_fp8, const OutSegs& out,
+                                        const Out& fused, int M, int N, int K, int bn, int S,
+                                        bool w_early, cudaStream_t st) {
   const int m_pad = (M + 15) / 16 * 16;
   CUtensorMap tw, tx;
   if (!make_map(&tw, w_fp8, N, K, kBM) || !make_map(&tx, x_fp8, m_pad, K, bn))
     return RQ_ERR_CUDA;
   static bool attr_done = false;
   if (!attr_done) {
-    if (cudaFuncSetAttribute(fp8_gemm_splitk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(fp8_gemm_splitk_kernel<Out>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemLimit) != cudaSuccess)
       return RQ_ERR_CUDA;
     attr_done = true;
@@ -1115,36 +1233,24 @@ static rq_status launch_fp8_gemm_splitk(const uint8_t* x_fp8, const float* x_deq
   // it; 256 tokens: 3.84 -> 3.43 ms), while narrow tiles gain from it.
   const bool pdl = pdl_enabled() && !(bn >= 128 && S >= 3);
   cfg.numAttrs = pdl ? 2 : 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, fp8_gemm_splitk_kernel, tw, tx, a));
+  return cuda_status(cudaLaunchKernelEx(&cfg, fp8_gemm_splitk_kernel<Out>, tw, tx, a, fused));
 }
 
-rq_status launch_fp8_gemm_group(const uint8_t* x_fp8, const float* x_deq,
-                                const uint8_t* w_fp8, int count, const int* starts,
-                                float* const* ys, const float* const* w_deqs, int M, int K,
-                                cudaStream_t st, bool w_early) {
-  if (count < 1 || count > kMaxSegs) return RQ_ERR_SHAPE;
+// The launch that sizes choose, for either kind of output.
+template <typename Out>
+static rq_status launch_fp8_gemm_out(const uint8_t* x_fp8, const float* x_deq,
+                                     const uint8_t* w_fp8, const OutSegs& out, const Out& fused,
+                                     int M, int N, int K, cudaStream_t st, bool w_early) {
   // RQ_GEMM_EARLY=0: no weight loads before the wait (A/B measurements)
   if (const char* e = std::getenv("RQ_GEMM_EARLY")) w_early = w_early && std::atoi(e) != 0;
-  OutSegs out;
-  out.count = count;
-  for (int i = 0; i <= count; ++i) out.start[i] = starts[i];
-  for (int i = 0; i < count; ++i) {
-    out.y[i] = ys[i];
-    out.w_deq[i] = w_deqs[i];
-  }
-  for (int i = count; i < kMaxSegs; ++i) {
-    out.start[i + 1] = starts[count];
-    out.y[i] = nullptr;
-    out.w_deq[i] = nullptr;
-  }
-  const int N = starts[count];
   const int m_pad = (M + 15) / 16 * 16;
   const int sms = device_sm_count();
   int bn_split = 0;
   const int S = choose_splits(m_pad, N, K, sms, &bn_split);
   if (S > 1)
-    return launch_fp8_gemm_splitk(x_fp8, x_deq, w_fp8, out, M, N, K, bn_split, S, w_early, st);
-  const int pairs = sms >= 2 ? resident_pairs(sms) : 0;
+    return launch_fp8_gemm_splitk(x_fp8, x_deq, w_fp8, out, fused, M, N, K, bn_split, S, w_early,
+                                  st);
+  const int pairs = sms >= 2 ? resident_pairs<Out>(sms) : 0;
   const int bn_pair = sms >= 2 ? choose_bn_pair(m_pad, N, pairs) : 0;
   const int bn_single = choose_bn(m_pad, N, sms);
   const bool pair = sms >= 2 && use_pair_kernel(m_pad, N, sms, pairs, bn_pair, bn_single);
@@ -1168,7 +1274,8 @@ rq_status launch_fp8_gemm_group(const uint8_t* x_fp8, const float* x_deq,
   if (pair) {
     static bool attr2 = false;
     if (!attr2) {
-      if (cudaFuncSetAttribute(fp8_gemm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      if (cudaFuncSetAttribute(fp8_gemm_pair_kernel<Out>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
                                kSmemLimit) != cudaSuccess)
         return RQ_ERR_CUDA;
       attr2 = true;
@@ -1177,17 +1284,17 @@ rq_status launch_fp8_gemm_group(const uint8_t* x_fp8, const float* x_deq,
     a.stages = gemm_stages(b_stride, kStages2, 0);
     // A persistent grid must be resident at once: not every SM can be
     // paired inside its GPC, so the grid is the number of pairs that fit.
-    const int max_pairs = resident_pairs(sms);
+    const int max_pairs = resident_pairs<Out>(sms);
     const int grid = 2 * (tiles < max_pairs ? tiles : max_pairs);
     if (std::getenv("RQ_GEMM_LOG") != nullptr)
       std::fprintf(stderr, "rq_gemm: pair M=%d N=%d K=%d bn=%d tiles=%d grid=%d stages=%d\n", M,
                    N, K, bn, tiles, grid, a.stages);
-    return launch_kernel(fp8_gemm_pair_kernel, grid, kThreadsPair,
-                         gemm_smem_bytes(a.stages, b_stride), st, tw, tx, a);
+    return launch_kernel(fp8_gemm_pair_kernel<Out>, grid, kThreadsPair,
+                         gemm_smem_bytes(a.stages, b_stride), st, tw, tx, a, fused);
   }
   static bool attr_done = false;
   if (!attr_done) {
-    if (cudaFuncSetAttribute(fp8_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(fp8_gemm_kernel<Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemLimit) != cudaSuccess)
       return RQ_ERR_CUDA;
     attr_done = true;
@@ -1197,8 +1304,29 @@ rq_status launch_fp8_gemm_group(const uint8_t* x_fp8, const float* x_deq,
   if (std::getenv("RQ_GEMM_LOG") != nullptr)
     std::fprintf(stderr, "rq_gemm: single M=%d N=%d K=%d bn=%d tiles=%d grid=%d stages=%d\n", M,
                  N, K, bn, tiles, grid, a.stages);
-  return launch_kernel(fp8_gemm_kernel, grid, kThreads, gemm_smem_bytes(a.stages, bn * kBK), st,
-                       tw, tx, a);
+  return launch_kernel(fp8_gemm_kernel<Out>, grid, kThreads, gemm_smem_bytes(a.stages, bn * kBK), st,
+                       tw, tx, a, fused);
+}
+
+rq_status launch_fp8_gemm_group(const uint8_t* x_fp8, const float* x_deq,
+                                const uint8_t* w_fp8, int count, const int* starts,
+                                float* const* ys, const float* const* w_deqs, int M, int K,
+                                cudaStream_t st, bool w_early) {
+  if (count < 1 || count > kMaxSegs) return RQ_ERR_SHAPE;
+  OutSegs out;
+  out.count = count;
+  for (int i = 0; i <= count; ++i) out.start[i] = starts[i];
+  for (int i = 0; i < count; ++i) {
+    out.y[i] = ys[i];
+    out.w_deq[i] = w_deqs[i];
+  }
+  for (int i = count; i < kMaxSegs; ++i) {
+    out.start[i + 1] = starts[count];
+    out.y[i] = nullptr;
+    out.w_deq[i] = nullptr;
+  }
+  return launch_fp8_gemm_out(x_fp8, x_deq, w_fp8, out, SegOut{}, M, starts[count], K, st,
+                             w_early);
 }
 
 rq_status launch_fp8_gemm(const uint8_t* x_fp8, const float* x_deq,
@@ -1206,6 +1334,38 @@ rq_status launch_fp8_gemm(const uint8_t* x_fp8, const float* x_deq,
                           int M, int N, int K, cudaStream_t st, bool w_early) {
   const int starts[2] = {0, N};
   return launch_fp8_gemm_group(x_fp8, x_deq, w_fp8, 1, starts, &y, &w_deq, M, K, st, w_early);
+}
+
+template <typename T>
+static rq_status launch_fused(const uint8_t* x_fp8, const float* x_deq, const uint8_t* w_fp8,
+                              const float* w_deq, const rq_epilogue& e, void* y,
+                              int64_t y_stride, int M, int N, int K, cudaStream_t st,
+                              bool w_early) {
+  OutSegs out = {};  // one segment, for its scale
+  out.count = 1;
+  for (int i = 1; i <= kMaxSegs; ++i) out.start[i] = N;
+  out.w_deq[0] = w_deq;
+  const FusedOut<T> f = {static_cast<T*>(y),
+                         static_cast<const T*>(e.mul),
+                         static_cast<const T*>(e.residual),
+                         y_stride,
+                         e.mul_stride,
+                         e.residual_stride,
+                         e.bias,
+                         e.act};
+  return launch_fp8_gemm_out(x_fp8, x_deq, w_fp8, out, f, M, N, K, st, w_early);
+}
+
+rq_status launch_fp8_gemm_epilogue(const uint8_t* x_fp8, const float* x_deq,
+                                   const uint8_t* w_fp8, const float* w_deq,
+                                   const rq_epilogue& e, int dtype, void* y, int64_t y_stride,
+                                   int M, int N, int K, cudaStream_t st, bool w_early) {
+  if (dtype == RQ_F32)
+    return launch_fused<float>(x_fp8, x_deq, w_fp8, w_deq, e, y, y_stride, M, N, K, st, w_early);
+  if (dtype == RQ_F16)
+    return launch_fused<__half>(x_fp8, x_deq, w_fp8, w_deq, e, y, y_stride, M, N, K, st, w_early);
+  return launch_fused<__nv_bfloat16>(x_fp8, x_deq, w_fp8, w_deq, e, y, y_stride, M, N, K, st,
+                                     w_early);
 }
 
 rq_status read_and_clear_device_error(cudaStream_t st) {
@@ -1218,6 +1378,8 @@ rq_status read_and_clear_device_error(cudaStream_t st) {
   if (attn == RQ_ERR_CUDA) return attn;
   const rq_status kv = read_and_clear_kv_error();
   if (kv == RQ_ERR_CUDA) return kv;
+  const rq_status plan = read_and_clear_plan_error();
+  if (plan == RQ_ERR_CUDA) return plan;
   unsigned int v = 0;
   if (cudaMemcpyFromSymbol(&v, g_rq_device_error, sizeof(v)) != cudaSuccess)
     return RQ_ERR_CUDA;
@@ -1225,7 +1387,7 @@ rq_status read_and_clear_device_error(cudaStream_t st) {
     // a timeout first, then an index
     for (rq_status s : {gemv, quant, attn, kv})
       if (s == RQ_ERR_TIMEOUT) return s;
-    return attn != RQ_OK ? attn : kv;
+    return attn != RQ_OK ? attn : kv != RQ_OK ? kv : plan;
   }
   const unsigned int zero = 0;
   if (cudaMemcpyToSymbol(g_rq_device_error, &zero, sizeof(zero)) != cudaSuccess)

@@ -139,7 +139,34 @@ rq_status launch_fp8_gemm_group(const uint8_t* x_fp8, const float* x_deq,
                                 const uint8_t* w_fp8, int count, const int* starts,
                                 float* const* ys, const float* const* w_deqs, int M, int K,
                                 cudaStream_t st, bool w_early = false);
+// The same product with an epilogue (rq_fp8_gemm_epilogue), y of dtype.
+rq_status launch_fp8_gemm_epilogue(const uint8_t* x_fp8, const float* x_deq,
+                                   const uint8_t* w_fp8, const float* w_deq,
+                                   const rq_epilogue& e, int dtype, void* y, int64_t y_stride,
+                                   int M, int N, int K, cudaStream_t st, bool w_early);
 rq_status read_and_clear_device_error(cudaStream_t st);
+
+// rq_norm.cu ----------------------------------------------------------------
+rq_status launch_residual_norm(const rq_norm_params& p, int dtype, const void* y,
+                               int64_t y_stride, const void* gate, int64_t gate_stride,
+                               int h_dtype, const void* h, int64_t h_stride, void* h_out,
+                               void* x_out, uint32_t* absmax, int tokens, cudaStream_t st);
+
+// rq_plan.cu ----------------------------------------------------------------
+rq_status launch_batch_plan(const int32_t* length, const int32_t* count, int batch,
+                            int new_tokens, int page_size, int32_t* page_table, int max_pages,
+                            const int32_t* free_pages, int free_capacity,
+                            const int32_t* free_count, int32_t* free_left, int64_t* slot,
+                            int32_t* position, int32_t* sequence, int rows, int32_t* row_start,
+                            int32_t* next_length, cudaStream_t st);
+// Read and clear the plan kernel's device error word (after a sync).
+rq_status read_and_clear_plan_error();
+
+// rq_sample.cu --------------------------------------------------------------
+// token null: the probabilities p; p null: the tokens drawn with u.
+rq_status launch_sample(const rq_sampling& f, int dtype, const void* logits, int64_t stride,
+                        const float* u, int32_t* token, float* p, int rows, int vocab,
+                        cudaStream_t st);
 
 // rq_kv.cu ------------------------------------------------------------------
 // Norm (p's weights, if any) and rotation of q and k rows; k and v rows into

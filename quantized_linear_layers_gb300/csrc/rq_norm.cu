@@ -1,0 +1,264 @@
+// rq_norm.cu -- the norm after a block, the gated and scaled sum with the
+// residual stream and the norm before the next block (sm_103a).
+//
+// Per token, over its width values, in f32:
+//   p = y * rsqrt(mean(y^2) + eps) * post_weight     (or y)
+//   h' = h + scale * (gate * p)
+//   x = h' * rsqrt(mean(h'^2) + eps) * pre_weight    (or h')
+//
+// A group of threads keeps its token in registers between the two sums: y and
+// h are read once and h' and x written once, which is what the operator cannot
+// do without.
+#include "rq_device.cuh"
+#include "rq_elem.cuh"
+#include "rq_internal.h"
+
+namespace rq {
+
+namespace {
+
+constexpr int kMaxWarps = 32;
+
+struct NormArgs {
+  const void *y, *gate, *h;
+  int64_t y_stride, gate_stride, h_stride;
+  const float *post_weight, *pre_weight;
+  void *h_out, *x_out;
+  uint32_t* absmax;
+  int width, tokens;
+  int post, pre, alone;  // alone: one CTA holds every token
+  float eps, scale, inv_width;
+};
+
+// Sum over the warps of a token's group.  `part` is written once per launch.
+template <bool kOneWarp>
+__device__ __forceinline__ float group_sum(float v, float* part) {
+  v = warp_sum(v);
+  if constexpr (!kOneWarp) {
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = warp_sum(lane < warps ? part[lane] : 0.0f);
+  }
+  return v;
+}
+
+// T: type of y, gate and x; R: of the residual stream; V: values a thread
+// takes at a time; G: how many such groups it holds.  kOneWarp: a token is one
+// warp's, several to a CTA; else a CTA's.
+template <typename T, typename R, int V, int G, bool kOneWarp>
+__global__ void __launch_bounds__(1024) residual_norm_kernel(const NormArgs a) {
+  __shared__ float part[2][kMaxWarps];
+  __shared__ unsigned int top;
+  const int group = kOneWarp ? 32 : (int)blockDim.x;
+  const int lane = kOneWarp ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
+  const int64_t t = kOneWarp ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)
+                             : (int64_t)blockIdx.x;
+  if (threadIdx.x == 0) top = 0u;
+  pdl_wait();
+  pdl_trigger();
+  const bool live = t < a.tokens;
+  float most = 0.0f;
+  if (live) {
+    const T* yp = static_cast<const T*>(a.y) + t * a.y_stride;
+    const T* gp = static_cast<const T*>(a.gate) + t * a.gate_stride;
+    const R* hp = static_cast<const R*>(a.h) + t * a.h_stride;
+    float y[G][V], h[G][V];
+    float sum = 0.0f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int c = (g * group + lane) * V;
+      if (c < a.width) {
+        load_elems<R, V>(hp + c, h[g]);
+        if (a.y != nullptr) load_elems<T, V>(yp + c, y[g]);
+      }
+    }
+    if (a.y != nullptr) {
+      float r = a.scale;
+      if (a.post) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          if ((g * group + lane) * V < a.width) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum = fmaf(y[g][j], y[g][j], sum);
+          }
+        sum = group_sum<kOneWarp>(sum, part[0]);
+        r = rsqrtf(fmaf(sum, a.inv_width, a.eps));
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int c = (g * group + lane) * V;
+        if (c < a.width) {
+          float q[V];
+          if (a.post) {
+            if (a.post_weight != nullptr) {
+              load_elems<float, V>(a.post_weight + c, q);
+#pragma unroll
+              for (int j = 0; j < V; ++j) y[g][j] *= r * q[j];
+            } else {
+#pragma unroll
+              for (int j = 0; j < V; ++j) y[g][j] *= r;
+            }
+          }
+          if (a.gate != nullptr) {
+            load_elems<T, V>(gp + c, q);
+#pragma unroll
+            for (int j = 0; j < V; ++j) y[g][j] *= q[j];
+          }
+#pragma unroll
+          for (int j = 0; j < V; ++j) h[g][j] = fmaf(a.scale, y[g][j], h[g][j]);
+        }
+      }
+      if (a.h_out != nullptr) {
+        R* ho = static_cast<R*>(a.h_out) + t * a.width;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const int c = (g * group + lane) * V;
+          if (c < a.width) store_elems<R, V>(ho + c, h[g]);
+        }
+      }
+    }
+    if (a.x_out != nullptr) {
+      float r = 1.0f;
+      if (a.pre) {
+        sum = 0.0f;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          if ((g * group + lane) * V < a.width) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum = fmaf(h[g][j], h[g][j], sum);
+          }
+        sum = group_sum<kOneWarp>(sum, part[1]);
+        r = rsqrtf(fmaf(sum, a.inv_width, a.eps));
+      }
+      T* xo = static_cast<T*>(a.x_out) + t * a.width;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int c = (g * group + lane) * V;
+        if (c < a.width) {
+          if (a.pre) {
+            if (a.pre_weight != nullptr) {
+              float q[V];
+              load_elems<float, V>(a.pre_weight + c, q);
+#pragma unroll
+              for (int j = 0; j < V; ++j) h[g][j] *= r * q[j];
+            } else {
+#pragma unroll
+              for (int j = 0; j < V; ++j) h[g][j] *= r;
+            }
+          }
+          if (a.absmax != nullptr) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) most = fmaxf(most, fabsf(h[g][j]));  // (a NaN is passed over)
+          }
+          store_elems<T, V>(xo + c, h[g]);
+        }
+      }
+    }
+  }
+  if (a.absmax != nullptr) {
+    // non-negative floats are ordered as their bits
+    const unsigned int m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) atomicMax(&top, m);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      if (a.alone)
+        *a.absmax = top;
+      else
+        atomicMax(a.absmax, top);
+    }
+  }
+}
+
+template <typename T, typename R, int V, int G>
+rq_status launch_groups(const NormArgs& a, int threads, int per_cta, cudaStream_t st) {
+  const unsigned ctas = (unsigned)((a.tokens + per_cta - 1) / per_cta);
+  if (threads == 32)
+    return launch_kernel(residual_norm_kernel<T, R, V, G, true>, dim3(ctas), dim3(32 * per_cta),
+                         0, st, a);
+  return launch_kernel(residual_norm_kernel<T, R, V, G, false>, dim3(ctas), dim3(threads), 0, st,
+                       a);
+}
+
+// G groups of V values a thread; `groups` of V values in a row.
+template <typename T, typename R, int V>
+rq_status launch_width(NormArgs a, cudaStream_t st) {
+  constexpr int kMost = 16 / V;  // groups that fit 16 values a thread
+  const int groups = (a.width + V - 1) / V;
+  // few tokens: as many threads as the row has groups, so that each thread
+  // waits for one load; many: four loads in flight a thread
+  const bool few = a.tokens <= 2 * device_sm_count();
+  int G = few ? 1 : 4;
+  if (G > kMost) G = kMost;
+  while (G < kMost && (groups + G - 1) / G > 1024) G *= 2;
+  if (!few && (groups + G - 1) / G <= 32 && G > 1 && groups <= 32) G = 1;
+  int threads = ((groups + G - 1) / G + 31) / 32 * 32;
+  const int per_cta = threads == 32 ? 4 : 1;
+  a.alone = a.tokens <= per_cta;
+  if (a.absmax != nullptr && !a.alone) {
+    const cudaError_t e = cudaMemsetAsync(a.absmax, 0, sizeof(uint32_t), st);
+    if (e != cudaSuccess) return RQ_ERR_CUDA;
+  }
+  if constexpr (kMost >= 16)
+    if (G == 16) return launch_groups<T, R, V, 16>(a, threads, per_cta, st);
+  if constexpr (kMost >= 8)
+    if (G == 8) return launch_groups<T, R, V, 8>(a, threads, per_cta, st);
+  if constexpr (kMost >= 4)
+    if (G == 4) return launch_groups<T, R, V, 4>(a, threads, per_cta, st);
+  if constexpr (kMost >= 2)
+    if (G == 2) return launch_groups<T, R, V, 2>(a, threads, per_cta, st);
+  return launch_groups<T, R, V, 1>(a, threads, per_cta, st);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+template <typename T, typename R>
+rq_status launch_types(const NormArgs& a, cudaStream_t st) {
+  constexpr int V = 16 / (int)sizeof(T);  // values of 16 bytes of the narrower type
+  const auto whole = [](int64_t stride, size_t size) { return stride * size % 16 == 0; };
+  if (a.width % V == 0 && aligned16(a.y) && aligned16(a.gate) && aligned16(a.h) &&
+      aligned16(a.post_weight) && aligned16(a.pre_weight) && aligned16(a.h_out) &&
+      aligned16(a.x_out) && whole(a.y_stride, sizeof(T)) && whole(a.gate_stride, sizeof(T)) &&
+      whole(a.h_stride, sizeof(R)))
+    return launch_width<T, R, V>(a, st);
+  return launch_width<T, R, 1>(a, st);
+}
+
+}  // namespace
+
+rq_status launch_residual_norm(const rq_norm_params& p, int dtype, const void* y,
+                               int64_t y_stride, const void* gate, int64_t gate_stride,
+                               int h_dtype, const void* h, int64_t h_stride, void* h_out,
+                               void* x_out, uint32_t* absmax, int tokens, cudaStream_t st) {
+  NormArgs a = {};
+  a.y = y;
+  a.gate = y != nullptr ? gate : nullptr;
+  a.h = h;
+  a.y_stride = y != nullptr ? y_stride : 0;
+  a.gate_stride = a.gate != nullptr ? gate_stride : 0;
+  a.h_stride = h_stride;
+  a.post = (p.norms & RQ_NORM_POST) != 0 && y != nullptr;
+  a.pre = (p.norms & RQ_NORM_PRE) != 0 && x_out != nullptr;
+  a.post_weight = a.post ? p.post_weight : nullptr;
+  a.pre_weight = a.pre ? p.pre_weight : nullptr;
+  a.h_out = h_out;
+  a.x_out = x_out;
+  a.absmax = absmax;
+  a.width = p.width;
+  a.tokens = tokens;
+  a.eps = p.eps;
+  a.scale = p.scale;
+  a.inv_width = 1.0f / (float)p.width;
+  if (tokens == 0)
+    return absmax == nullptr ? RQ_OK
+                             : cuda_status(cudaMemsetAsync(absmax, 0, sizeof(uint32_t), st));
+  if (dtype == RQ_F32) return launch_types<float, float>(a, st);
+  if (dtype == RQ_F16)
+    return h_dtype == RQ_F32 ? launch_types<__half, float>(a, st)
+                             : launch_types<__half, __half>(a, st);
+  return h_dtype == RQ_F32 ? launch_types<__nv_bfloat16, float>(a, st)
+                           : launch_types<__nv_bfloat16, __nv_bfloat16>(a, st);
+}
+
+}  // namespace rq

@@ -28,6 +28,30 @@ __device__ __forceinline__ __nv_bfloat16 float_elem<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+// Two 16-bit elements of a word (the first in its low half) as floats, and back.
+template <typename T>
+__device__ __forceinline__ float2 word_floats(uint32_t w);
+template <>
+__device__ __forceinline__ float2 word_floats<__half>(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 word_floats<__nv_bfloat16>(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t floats_word(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t floats_word<__half>(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t floats_word<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // V consecutive elements: one element, or whole 16-byte groups.
 template <typename T, int V>
 __device__ __forceinline__ void load_elems(const T* p, float (&x)[V]) {

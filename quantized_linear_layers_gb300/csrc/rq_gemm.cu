@@ -29,6 +29,7 @@
 
 #include <cstdio>
 #include <cstdlib>
+#include <type_traits>
 
 #include "rq_device.cuh"
 #include "rq_elem.cuh"
@@ -167,25 +168,78 @@ struct FusedOut {
   int64_t y_stride, mul_stride, residual_stride;
   const float* bias;        // null: none
   int act;                  // rq_act
+  int pairs;                // two 16-bit outputs may move at a time
 };
 
-// The activation.  16-bit outputs take SiLU's power and quotient from the
-// fast units: their errors, about 2^-21 |z| and 2^-22, are far below half a step of
-// 2^-9; f32 outputs keep the exact functions.
+// e^x from the special function unit: its power of two is within 2^-22, and
+// for f32 outputs the rounding of x log2(e) is made good (x up to 88 would
+// lose six bits by it); 16-bit outputs, half a step of 2^-9 or 2^-12, need that not.
+template <bool kFast>
+__device__ __forceinline__ float power(float x) {
+  constexpr float kH = 1.44269502162933349609f, kL = 1.92596299112661746887e-8f;  // log2 e
+  const float t = x * kH;
+  float e;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+  if constexpr (!kFast) {
+    const float rest = fmaf(x, kL, fmaf(x, kH, -t));
+    // (an overflow of either side leaves e as it is)
+    if (fabsf(t) < 127.0f) e = fmaf(e, rest * 0.693147182464599609375f, e);
+  }
+  return e;
+}
+
+// z / (1 + e^-a).  (e^-a = +Inf makes the quotient 0, its limit.)
+template <bool kFast>
+__device__ __forceinline__ float logistic_times(float z, float a) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + power<kFast>(-a)));
+  return z * r;
+}
+
+// The activation, 2 special function instructions and at most a dozen others:
+// the library's functions, with their own branches, made the epilogue longer
+// than the products (2048 x 18944 x 3584, SiLU to f32: 305 us, of which 90 the
+// products).  GELU: erfc(x) = (a1 t + .. + a5 t^5) e^(-x^2), t = 1 / (1 + p x),
+// within 1.5e-7 (Abramowitz and Stegun 7.1.26).  (1 + tanh a) / 2 = 1 / (1 + e^-2a).
 template <bool kFast>
 __device__ __forceinline__ float activate(float z, int act) {
   if (act == RQ_ACT_NONE) return z;
-  if (act == RQ_ACT_SILU) {
-    // (z < -88 makes the power +Inf and the quotient -0, its limit)
-    if constexpr (kFast) return z < -80.0f ? -0.0f : __fdividef(z, 1.0f + __expf(-z));
-    return z / (1.0f + expf(-z));
-  }
-  if (act == RQ_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-  if (act == RQ_ACT_GELU_TANH) {
-    const float a = 0.79788456080286536f * fmaf(0.044715f * z * z, z, z);
-    return 0.5f * z * (1.0f + tanhf(a));
+  if (act == RQ_ACT_SILU) return logistic_times<kFast>(z, z);
+  if (act == RQ_ACT_GELU_TANH)
+    return logistic_times<kFast>(z, 1.59576912160573072f * fmaf(0.044715f * z * z, z, z));
+  if (act == RQ_ACT_GELU) {
+    const float x = fabsf(z) * 0.70710678118654752f;
+    float t;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3275911f, x, 1.0f)));
+    float q = fmaf(t, 1.061405429f, -1.453152027f);
+    q = fmaf(t, q, 1.421413741f);
+    q = fmaf(t, q, -0.284496736f);
+    q = fmaf(t, q, 0.254829592f);
+    q *= t * power<kFast>(-x * x);  // erfc
+    const float h = 0.5f * fminf(fabsf(z), 100.0f) * q;  // (q is 0 there; z may be infinite)
+    return z > 0.0f ? z - h : -h;
   }
   return z < 0.0f ? 0.0f : z;  // (NaN stays NaN)
+}
+
+// The activation of a batch: one branch for all of it.
+template <bool kFast, int kN>
+__device__ __forceinline__ void activate_all(float (&z)[kN], int act) {
+  if (act == RQ_ACT_SILU) {
+#pragma unroll
+    for (int j = 0; j < kN; ++j) z[j] = activate<kFast>(z[j], RQ_ACT_SILU);
+  } else if (act != RQ_ACT_NONE) {
+    if (act == RQ_ACT_GELU) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) z[j] = activate<kFast>(z[j], RQ_ACT_GELU);
+    } else if (act == RQ_ACT_GELU_TANH) {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) z[j] = activate<kFast>(z[j], RQ_ACT_GELU_TANH);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kN; ++j) z[j] = activate<kFast>(z[j], RQ_ACT_RELU);
+    }
+  }
 }
 
 template <typename T>
@@ -206,35 +260,168 @@ struct GemmArgs {
   uint64_t wait_limit_ns;
 };
 
-// One warp's part of a tile with an epilogue: TMEM lanes hold output row n of
-// this lane, columns the tokens m0 + c for c in [c_lo, c_hi).  Lanes are
-// neighbouring outputs of one token, so loads and stores are whole segments;
-// sixteen tokens' loads are in flight while the accumulator is read.
-template <typename T>
-__device__ __forceinline__ void fused_columns(const FusedOut<T>& out, uint32_t taddr, int c_lo,
-                                              int c_hi, int m0, int M, int n, bool live,
-                                              float scale_x, float scale_w) {
-  const float bias = live && out.bias != nullptr ? out.bias[n] : 0.0f;
-  for (int c = c_lo; c < c_hi; c += 16) {
-    float mul[16], res[16];
+// One warp's part of a tile with an epilogue: TMEM lanes hold output n0 + lane,
+// columns the tokens m0 + c for c in [c_lo, c_hi).
+//
+// A tile's operands are sent for, into L2, before its accumulator is waited for,
+// and a batch's loads are made before the accumulator is read: their latency,
+// not their bytes, is what such an epilogue takes (bf16 factor, 2048 x 18944 x
+// 3584: 377 us without either, 96 with, 86 without a factor).  Loads of tokens
+// and outputs that are not there are made at clamped places rather than skipped, since a
+// branch around each would wait for it.  Keeping the next batch's operands in
+// registers instead took 141 us (SiLU and factor; 103 now), and 12 or 16 warps
+// of fewer registers 115 and 104.
+//
+// Lanes are neighbouring outputs of one token.  16-bit outputs whose rows
+// allow it go in pairs (kPair): neighbouring lanes exchange one of two tokens'
+// values, so that each has two outputs of one token, and a load or store
+// moves 4 bytes a lane instead of 2.
+template <typename T, bool kPair, bool kFull>
+struct FusedColumns {
+  static constexpr int kBatch = 16;
+  using Word = typename std::conditional<kPair, uint32_t, T>::type;
+  static constexpr int kWords = kPair ? kBatch / 2 : kBatch;
+  static constexpr int kStep = kPair ? 2 : 1;  // tokens between a lane's words
+
+  const FusedOut<T>& out;
+  int M, m_first, n;
+  bool live;
+  float bias, scale_x, scale_w;
+
+  // m0: the tile's first token; n0: the warp's first output.  kFull: every
+  // output of every token is there.
+  __device__ __forceinline__ FusedColumns(const FusedOut<T>& o, int m0, int M_, int n0, int N,
+                                          float sx, float sw)
+      : out(o), M(M_), scale_x(sx), scale_w(sw) {
+    const int lane = threadIdx.x & 31;
+    const int own = n0 + lane;
+    live = kFull || own < N;
+    bias = live && o.bias != nullptr ? o.bias[own] : 0.0f;
+    n = kPair ? own & ~1 : own;
+    if (!kFull) n = min(n, kPair ? N - 2 : N - 1);
+    m_first = m0 + (kPair ? lane & 1 : 0);
+  }
+
+  __device__ __forceinline__ void fetch(const T* base, int64_t stride, int c,
+                                        Word (&w)[kWords]) const {
+    if constexpr (kFull) {
+      const T* p = base + (m_first + c) * stride + n;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int m = m0 + c + j;
-      const bool in = live && m < M;
-      mul[j] = in && out.mul != nullptr ? elem_float(out.mul[m * out.mul_stride + n]) : 1.0f;
-      res[j] = in && out.residual != nullptr
-                   ? elem_float(out.residual[m * out.residual_stride + n])
-                   : 0.0f;
-    }
-    uint32_t v[16];
-    tmem_ld16(taddr + (uint32_t)c, v);
+      for (int j = 0; j < kWords; ++j) {
+        w[j] = *reinterpret_cast<const Word*>(p);
+        p += kStep * stride;
+      }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int m = m0 + c + j;
-      const float z = fmaf(__uint_as_float(v[j]) * scale_x, scale_w, bias);
-      if (live && m < M) out.y[m * out.y_stride + n] = fused_value<T>(z, out.act, mul[j], res[j]);
+      for (int j = 0; j < kWords; ++j) {
+        const int m = min(m_first + c + kStep * j, M - 1);
+        w[j] = *reinterpret_cast<const Word*>(base + m * stride + n);
+      }
     }
   }
+
+  // The operands of tokens [c_lo, c_hi) on their way into L2, a token a lane.
+  __device__ __forceinline__ void prefetch(const T* base, int64_t stride, int n0, int n1, int m0,
+                                           int c_lo, int c_hi) const {
+    for (int c = c_lo + (int)(threadIdx.x & 31); c < c_hi && m0 + c < M; c += 32) {
+      const T* p = base + (m0 + c) * stride;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p + n0));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p + n1));
+    }
+  }
+
+  __device__ __forceinline__ void run(uint32_t taddr, int c_lo, int c_hi) {
+    for (int c = c_lo; c < c_hi; c += kBatch) {
+      Word w_mul[kWords], w_res[kWords];
+      if (out.mul != nullptr) fetch(out.mul, out.mul_stride, c, w_mul);
+      if (out.residual != nullptr) fetch(out.residual, out.residual_stride, c, w_res);
+      uint32_t v[16];
+      tmem_ld16(taddr + (uint32_t)c, v);
+      float a[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        a[j] = fmaf(__uint_as_float(v[j]) * scale_x, scale_w, bias);
+      activate_all<sizeof(T) == 2>(a, out.act);
+      if constexpr (kPair) {
+        const bool odd = (threadIdx.x & 1) != 0;
+#pragma unroll
+        for (int j = 0; j < kBatch; j += 2) {
+          const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? a[j] : a[j + 1], 1);
+          a[j] = odd ? got : a[j];
+          a[j + 1] = odd ? a[j + 1] : got;
+        }
+      }
+      if (out.mul != nullptr) {
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          if constexpr (kPair) {
+            const float2 f = word_floats<T>(w_mul[j]);
+            a[2 * j] *= f.x;
+            a[2 * j + 1] *= f.y;
+          } else {
+            a[j] *= elem_float(w_mul[j]);
+          }
+        }
+      }
+      if (out.residual != nullptr) {
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          if constexpr (kPair) {
+            const float2 f = word_floats<T>(w_res[j]);
+            a[2 * j] += f.x;
+            a[2 * j + 1] += f.y;
+          } else {
+            a[j] += elem_float(w_res[j]);
+          }
+        }
+      }
+      T* p = out.y + (m_first + c) * out.y_stride + n;
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) {
+        Word t;
+        if constexpr (kPair)
+          t = floats_word<T>(a[2 * j], a[2 * j + 1]);
+        else
+          t = float_elem<T>(a[j]);
+        if (kFull || (live && m_first + c + kStep * j < M)) *reinterpret_cast<Word*>(p) = t;
+        p += kStep * out.y_stride;
+      }
+    }
+  }
+};
+
+// The same for a warp of either tile kernel, `ready` waiting for the
+// accumulator.  False: it did not come.
+template <typename T, bool kPair, bool kFull, typename Ready>
+__device__ __forceinline__ bool fused_part(const FusedOut<T>& out, uint32_t taddr, int c_lo,
+                                           int c_hi, int m0, int M, int n0, int N, float sx,
+                                           float sw, Ready ready) {
+  FusedColumns<T, kPair, kFull> f(out, m0, M, n0, N, sx, sw);
+  const int n1 = min(n0 + 31, N - 1);
+  if (n0 < N && out.mul != nullptr)
+    f.prefetch(out.mul, out.mul_stride, n0, n1, m0, c_lo, c_hi);
+  if (n0 < N && out.residual != nullptr)
+    f.prefetch(out.residual, out.residual_stride, n0, n1, m0, c_lo, c_hi);
+  if (!ready()) return false;
+  f.run(taddr, c_lo, c_hi);
+  return true;
+}
+
+template <typename T, typename Ready>
+__device__ __forceinline__ bool fused_columns(const FusedOut<T>& out, uint32_t taddr, int c_lo,
+                                              int c_hi, int m0, int M, int n0, int N, float sx,
+                                              float sw, Ready ready) {
+  const bool full = m0 + c_hi <= M && n0 + 32 <= N;
+  if constexpr (sizeof(T) == 2) {
+    if (out.pairs) {
+      if (full)
+        return fused_part<T, true, true>(out, taddr, c_lo, c_hi, m0, M, n0, N, sx, sw, ready);
+      return fused_part<T, true, false>(out, taddr, c_lo, c_hi, m0, M, n0, N, sx, sw, ready);
+    }
+  }
+  if (full)
+    return fused_part<T, false, true>(out, taddr, c_lo, c_hi, m0, M, n0, N, sx, sw, ready);
+  return fused_part<T, false, false>(out, taddr, c_lo, c_hi, m0, M, n0, N, sx, sw, ready);
 }
 
 template <typename Out>
@@ -385,18 +572,24 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmap_w,
       const int tn = t / args.tiles_m, tm = t - tn * args.tiles_m;
       // every lane polls; the outcome is made warp-uniform before the
       // .sync.aligned TMEM loads below
-      const bool ready =
-          mbar_wait_fast(tfull0 + 8 * acc, acc_phase, args.wait_limit_ns, &g_rq_device_error);
-      if (!__all_sync(0xFFFFFFFFu, ready)) break;
-      tc_fence_after();
-      const int n = tn * kBM + quad * 32 + lane;
+      const auto wait = [&] {
+        const bool ready =
+            mbar_wait_fast(tfull0 + 8 * acc, acc_phase, args.wait_limit_ns, &g_rq_device_error);
+        if (!__all_sync(0xFFFFFFFFu, ready)) return false;
+        tc_fence_after();
+        return true;
+      };
       const int m0 = tm * bn;
-      const int sg = seg_of(args.out, n);
-      const float scale_w = n < args.N ? *args.out.w_deq[sg] : 0.f;
       const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * bn);
       if constexpr (Out::kFused) {
-        fused_columns(out, taddr, 0, bn, m0, args.M, n, n < args.N, scale_x, scale_w);
+        if (!fused_columns(out, taddr, 0, bn, m0, args.M, tn * kBM + quad * 32, args.N, scale_x,
+                           *args.out.w_deq[0], wait))
+          break;
       } else {
+        if (!wait()) break;
+        const int n = tn * kBM + quad * 32 + lane;
+        const int sg = seg_of(args.out, n);
+        const float scale_w = n < args.N ? *args.out.w_deq[sg] : 0.f;
         const int ns = args.out.start[sg + 1] - args.out.start[sg];
         float* yr = args.out.y[sg] + (n - args.out.start[sg]);
         for (int c = 0; c < bn; c += 16) {
@@ -669,18 +862,25 @@ fp8_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_w,
     uint32_t acc_phase = 0;
     for (int t = pair; t < ntiles; t += npairs) {
       const int tn = t / args.tiles_m, tm = t - tn * args.tiles_m;
-      const bool ready =
-          mbar_wait_fast(tfull0 + 8 * acc, acc_phase, args.wait_limit_ns, &g_rq_device_error);
-      if (!__all_sync(0xFFFFFFFFu, ready)) break;
-      tc_fence_after();
-      const int n = tn * 256 + (int)rank * kBM + quad * 32 + lane;
+      const auto wait = [&] {
+        const bool ready =
+            mbar_wait_fast(tfull0 + 8 * acc, acc_phase, args.wait_limit_ns, &g_rq_device_error);
+        if (!__all_sync(0xFFFFFFFFu, ready)) return false;
+        tc_fence_after();
+        return true;
+      };
       const int m0 = tm * bn;
-      const int sg = seg_of(args.out, n);
-      const float scale_w = n < args.N ? *args.out.w_deq[sg] : 0.f;
       const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(acc * bn);
       if constexpr (Out::kFused) {
-        fused_columns(out, taddr, c_lo, c_hi, m0, args.M, n, n < args.N, scale_x, scale_w);
+        if (!fused_columns(out, taddr, c_lo, c_hi, m0, args.M,
+                           tn * 256 + (int)rank * kBM + quad * 32, args.N, scale_x,
+                           *args.out.w_deq[0], wait))
+          break;
       } else {
+        if (!wait()) break;
+        const int n = tn * 256 + (int)rank * kBM + quad * 32 + lane;
+        const int sg = seg_of(args.out, n);
+        const float scale_w = n < args.N ? *args.out.w_deq[sg] : 0.f;
         const int ns = args.out.start[sg + 1] - args.out.start[sg];
         float* yr = args.out.y[sg] + (n - args.out.start[sg]);
         for (int c = c_lo; c < c_hi; c += 16) {
@@ -1336,6 +1536,16 @@ rq_status launch_fp8_gemm(const uint8_t* x_fp8, const float* x_deq,
   return launch_fp8_gemm_group(x_fp8, x_deq, w_fp8, 1, starts, &y, &w_deq, M, K, st, w_early);
 }
 
+// Whether two neighbouring outputs of every row lie in one aligned word.
+template <typename T>
+static int paired(const rq_epilogue& e, const void* y, int64_t y_stride, int N) {
+  const auto even = [](const void* p, int64_t stride) {
+    return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 4 == 0 && stride % 2 == 0);
+  };
+  return sizeof(T) == 2 && N % 2 == 0 && even(y, y_stride) && even(e.mul, e.mul_stride) &&
+         even(e.residual, e.residual_stride);
+}
+
 template <typename T>
 static rq_status launch_fused(const uint8_t* x_fp8, const float* x_deq, const uint8_t* w_fp8,
                               const float* w_deq, const rq_epilogue& e, void* y,
@@ -1352,7 +1562,8 @@ static rq_status launch_fused(const uint8_t* x_fp8, const float* x_deq, const ui
                          e.mul_stride,
                          e.residual_stride,
                          e.bias,
-                         e.act};
+                         e.act,
+                         paired<T>(e, y, y_stride, N)};
   return launch_fp8_gemm_out(x_fp8, x_deq, w_fp8, out, f, M, N, K, st, w_early);
 }
 

@@ -650,7 +650,8 @@ rq_status rq_verify_tree(const int32_t *token, const int32_t *parent, const floa
 
 /* Each row's own filters: device arrays [rows], 4-byte aligned; NULL leaves a
  * filter out for every row.  The struct is read on the host during the call.
- *   temperature T (NULL: 1).  T <= 0 or NaN: the likeliest token alone.
+ *   temperature T (NULL: 1).  T <= 0 or NaN: the likeliest token alone; below
+ *   2^-116 counts as that.
  *   top_k: <= 0 is off.   top_p: >= 1 or NaN is off.   min_p: <= 0 or NaN is
  *   off, above 1 counts as 1. */
 typedef struct {
@@ -663,8 +664,8 @@ typedef struct {
 /* The distribution that a token is drawn from.  Tokens stand in order of their
  * logits, largest first, equal ones by index, and have whole weights
  *   W = floor(2^42 e^((logit - largest) / T))
- * (2^42 for the largest itself; the others within one of that, from a power
- * carried to about 2^-43).  A NaN counts as -Inf; next to +Inf all
+ * (2^42 for the largest itself; the others within 2^-32 of their value and one
+ * unit of that).  A NaN counts as -Inf; next to +Inf all
  * finite logits weigh 0.  A token stays if
  *   W > 0 and W >= min_p 2^42                                   (min-p),
  *   fewer than top_k of those stand before it                   (top-k), and
@@ -686,8 +687,9 @@ rq_status rq_sample(const rq_sampling *sampling_host, int dtype, const void *log
                     rq_stream_t stream);
 
 /* The same distribution written out, as rq_verify_chain and rq_verify_tree
- * take it:  p: f32 [rows][vocab], dense, W / total of the tokens that stay and
- * 0 elsewhere (a row of NaN and -Inf only: zeros); must not overlap the logits.
+ * take it:  p: f32 [rows][vocab], dense, W / total of the tokens that stay, to
+ * 2^-21 of itself, and 0 elsewhere (a row of NaN and -Inf only: zeros); must
+ * not overlap the logits.
  * Errors: as rq_sample. */
 rq_status rq_token_probs(const rq_sampling *sampling_host, int dtype, const void *logits,
                          int64_t stride, float *p, int rows, int vocab,

@@ -3,28 +3,46 @@
 //
 // Whole weights W = floor(2^42 e^((l - largest) / T)) make every sum exact:
 // where a nucleus ends and which token a random number meets depend on no
-// order of summation, however a row is cut up.  42 bits, because a nucleus of
-// 10^5 tokens ends at probabilities of 10^-6, so that sums of f32 weights
-// (2^-24 each) would move its border; 2^20 tokens of 2^42 still fit 64 bits.
+// order of summation, however a row is cut up.  f32 weights would not do: a
+// nucleus of 10^5 tokens ends at probabilities of 10^-6, where sums of
+// weights within 2^-24 differ by tokens.  2^20 tokens of 2^42 still fit 64 bits.
 //
-// The power.  y = (largest - l) log2(e) / T is carried as a sum of two floats
-// (the difference and the products with their rounding errors), and
-//   2^-y = 2^-n  2^(-j/256)  e^(-z),   n + j/256 the nearest of 256ths, |z| < 0.0014:
-// a table of the 256 powers as sums of two floats, and four terms of the
-// series of e^-z, of which only the first needs more than 24 bits.  That is
-// about 45 f32 operations per token, relative error about 2^-43.  (64-bit
-// floats would need fewer, at 1/64 of the rate.)
+// The power.  y = 512 log2(e) (largest - l) / T is carried as a sum of two
+// floats (the difference and the products with their rounding errors), and
+//   2^(-y/512) = 2^-n 2^(-j/512) 2^(-z/512),   512 n + j = rint(y), |z| <= 1/2:
+// a table of the 512 powers in 42 bits, less its product with a cubic in z
+// that is below 2^-10, so that f32 roundings in it stay below 2^-33 of the
+// weight (2^-35.6 on the average, measured).  About 34 instructions a token.  (64-bit floats would need fewer,
+// at 1/64 of the rate.)
 //
-// Finding where top-k and top-p cut.  Sorting a row is not needed: a histogram
-// of y finds the bin that the cut falls in, the bin's tokens (a hundred, say) are
-// listed and each counts what stands before it.  A bin of more tokens than the
-// list holds is divided again by the bits of its logits; equal logits, however
-// many, are cut by counting in order of index.
+// Finding where top-k and top-p cut.  Sorting a row is not needed.  Counts of
+// tokens in 512 bins of y give top-k's bin, and, since a bin's weights lie
+// within 6 % of each other, the few bins that a nucleus can end in.  One pass of exact
+// weights then sums what stands before those bins and after them, and divides
+// them into 128 finer ones; the few tokens of the bin that the cut falls in are listed
+// and each counts what stands before it.  What is not divided far enough is
+// divided by the bits of the logits; equal logits, however many, are cut by
+// counting in order of index.  A small top-k lists all tokens down to its bin
+// and needs no further look at the row.
 //
 // One cluster of CTAs takes a row and keeps it in shared memory: logits are
-// read from memory once.  Every CTA gets the merged histogram and the whole
-// list through distributed shared memory and decides by itself, so decisions
-// are never sent back.
+// read from memory once.  Every CTA reads the others' histograms through
+// distributed shared memory, receives the whole list and decides by itself:
+// one cluster barrier per exchange, and no decision is sent back.
+//
+// Threads hold consecutive tokens (loads from memory are made in order all
+// the same and scattered into shared memory), so that a warp's scan of its
+// lanes' sums is a scan by index.
+//
+// Bound by instruction issue: 64 rows of 131072 f32 logits without filters take
+// 35 us, of which reading them is 5 and loading, the maximum and the barriers
+// are 20 (the likeliest token alone); the exact pass issues 45 instructions a
+// token.  With top-k 50 35 us, with a nucleus of 0.9 64 us (196 with a
+// histogram of exact weights over the whole row).  One row: 13, 15 and 24 us,
+// about 8 us of which are 5 to 7 barriers and what follows them (with cold
+// inputs, launch and events included).
+#include <type_traits>
+
 #include "rq_device.cuh"
 #include "rq_elem.cuh"
 #include "rq_internal.h"
@@ -36,55 +54,61 @@ namespace {
 constexpr int kSThreads = 512;
 constexpr int kSWarps = kSThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 1024;
-constexpr int kList = 512;           // tokens of a bin that are ranked directly
-constexpr int kTable = 256;
-constexpr float kFar = 43.0f;        // 2^42 2^-y is below 1 from y = 42 on
-constexpr int kUnitBits = 42;
-constexpr int kCacheMax = 40 * 1024; // logits of a CTA kept in shared memory
+constexpr int kParts = kMaxCluster * kSWarps;
+constexpr int kBins = 512;           // one a thread
+constexpr int kFine = 128;           // of what is divided further
+constexpr int kList = 128;           // tokens that are ranked one by one
+constexpr int kTable = 512;
+constexpr float kFar = 43.0f * kTable;  // 2^42 2^-y/512 is below 1 from 42 octaves on
+constexpr int kCacheBytes = 176 * 1024;  // of a row's part, at most
 
-// 2^(-j/256) as a sum of two floats.
+// 2^(42 - j/512).
 struct PowerTable {
-  float hi[kTable], lo[kTable];
-  constexpr PowerTable() : hi(), lo() {
+  unsigned long long t[kTable];
+  constexpr PowerTable() : t() {
     for (int j = 0; j < kTable; ++j) {
-      // e^-x by its series, x < ln 2: the 20th term is below 2^-70
+      // e^-x by its series, x < ln 2: the 24th term is below 2^-90
       const double x = 0.693147180559945309417 * j / kTable;
       double term = 1.0, sum = 1.0;
       for (int i = 1; i <= 24; ++i) {
         term *= -x / i;
         sum += term;
       }
-      hi[j] = (float)sum;
-      lo[j] = (float)(sum - (double)hi[j]);
+      t[j] = (unsigned long long)(sum * 4398046511104.0 + 0.5);
     }
   }
 };
 __device__ const PowerTable g_power;
 
-struct Cut {
-  uint32_t key;  // tokens of a larger key stay, and those of this key up to
-  int index;     // this index
+// A bin of a CTA's histogram as the others read it.
+struct __align__(16) Bin {
+  unsigned long long w;
+  unsigned int n, unused;
 };
 
 struct SampleShared {
-  float2 power[kTable];
-  unsigned long long merged_w[kBins];
-  unsigned long long sums[kMaxCluster * kSWarps];
-  unsigned long long list_w[kList];
+  unsigned long long power[kTable];
+  // this CTA's histograms: of the row (the last: tokens of no bin), and of what
+  // is divided
+  unsigned int count[kBins + 1], count_fine[kFine];
+  Bin bins[kFine];
+  // sums of the weights' bits 0 .. 14, 15 .. 28 and 29 .. 42: 2^17 tokens a
+  // CTA do not wrap them, and nothing is carried between atomics
+  unsigned int weight[3][kFine];
+  unsigned long long sums[2][kParts];
+  unsigned long long found[3][kList];  // this CTA's tokens of the lists
+  unsigned long long list[kList], list_w[kList];
+  unsigned long long cut;              // tokens from this order on stay
   unsigned long long tmp_w[kSWarps];
-  unsigned long long above_w, total;
-  uint32_t count[kBins], lo[kBins], hi[kBins];  // this CTA's part of the row
-  uint32_t merged_n[kBins];
-  uint32_t list_key[2][kList];  // top-k's and top-p's candidates
-  int list_index[2][kList];
-  uint32_t tmp_n[kSWarps];
-  uint32_t key_min[kMaxCluster], key_max[kMaxCluster];
+  unsigned long long above_w, total, goal;
+  unsigned int tmp_n[kSWarps];
+  unsigned int key_min[kMaxCluster], key_max[kMaxCluster];
   float top[kMaxCluster];
+  float tmp_f[2][kSWarps];
   int first[kMaxCluster];
-  uint32_t above_n, bin_n, pushed, base;
-  int bin, found;
-  Cut cut;
+  unsigned int above_n, bin_n;
+  unsigned int pushed[3];
+  int bin, bin_last, equal;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -118,10 +142,28 @@ __device__ __forceinline__ void put_u32(const void* p, uint32_t rank, uint32_t v
 __device__ __forceinline__ void put_u64(const void* p, uint32_t rank, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(map_rank(p, rank)), "l"(v) : "memory");
 }
+// (After a cluster barrier; no clobber, so that several are in flight.)
 __device__ __forceinline__ uint32_t get_u32(const void* p, uint32_t rank) {
   uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_rank(p, rank)) : "memory");
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_rank(p, rank)));
   return v;
+}
+__device__ __forceinline__ unsigned long long get_u64(const void* p, uint32_t rank) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(map_rank(p, rank)));
+  return v;
+}
+__device__ __forceinline__ Bin get_bin(const Bin* p, uint32_t rank) {
+  Bin b;
+  asm volatile("{.reg .b32 u; ld.shared::cluster.v4.b32 {%0, %1, %2, u}, [%3];}"
+               : "=r"(reinterpret_cast<unsigned int*>(&b.w)[0]),
+                 "=r"(reinterpret_cast<unsigned int*>(&b.w)[1]), "=r"(b.n)
+               : "r"(map_rank(p, rank)));
+  return b;
+}
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
 }
 
 // Floats in order as unsigned integers.
@@ -134,6 +176,14 @@ __device__ __forceinline__ float float_of(uint32_t key) {
   return __uint_as_float(key ^ ((key >> 31) != 0u ? 0x80000000u : 0xFFFFFFFFu));
 }
 
+// Tokens in order as unsigned integers: larger logits, then smaller indices.
+__device__ __forceinline__ unsigned long long order_of(int v, float l) {
+  return (unsigned long long)key_of(l) << 32 | (0xFFFFFFFFu - (unsigned int)v);
+}
+__device__ __forceinline__ int index_of(unsigned long long order) {
+  return (int)(0xFFFFFFFFu - (unsigned int)order);
+}
+
 template <typename I>
 __device__ __forceinline__ I warp_scan_add(I v, int lane) {
 #pragma unroll
@@ -144,63 +194,76 @@ __device__ __forceinline__ I warp_scan_add(I v, int lane) {
   return v;
 }
 
-template <typename I>
-__device__ __forceinline__ I warp_add(I v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
-
 // A row's scale: y = (top - l) (ch + cl).
 struct Scale {
   float top;
-  // 1, or for a temperature past 2^100 a small power of two that keeps
+  // 1, or for a temperature past 2^90 a small power of two that keeps
   // differences of any two floats finite and ch normal
   float pre;
-  float near, ch, cl;  // top pre; log2(e) / T / pre
-  const float2* power;
+  float near, ch, cl;  // top pre; 512 log2(e) / T / pre
+  const unsigned long long* power;
 
   __device__ __forceinline__ void set(float t) {
-    const double c = 1.4426950408889634074 / (double)t;
-    pre = c < 0x1p-100 ? 0x1p-64f : 1.0f;
+    if (top == INFINITY) {
+      // next to +Inf nothing finite weighs anything: near - l pre is -Inf for
+      // it, y 0, and beyond kFar for all others
+      pre = 0.5f;
+      near = 3.0e38f;
+      ch = 1.0f;
+      cl = 0.0f;
+      return;
+    }
+    pre = t > 0x1p90f ? 0x1p-64f : 1.0f;
     near = top * pre;
-    ch = (float)(c / (double)pre);
-    cl = (float)(c / (double)pre - (double)ch);
+    // 512 log2(e) as a sum of two floats, over t
+    const float kh = t > 0x1p90f ? 738.65985107421875f * 0x1p64f : 738.65985107421875f;
+    const float kl = t > 0x1p90f ? 9.860930513e-6f * 0x1p64f : 9.860930513e-6f;
+    ch = __fdiv_rn(kh, t);
+    cl = t < INFINITY ? __fdiv_rn(fmaf(-ch, t, kh) + kl, t) : 0.0f;
   }
 
+  // y's larger part, 0 .. kFar (never rises with l); a NaN gives kFar.
   __device__ __forceinline__ float far(float l) const {
-    return l == top ? 0.0f : fmaf(-l, pre, near) * ch;
+    return fmaxf(fminf(fmaf(-l, pre, near) * ch, kFar), 0.0f);
   }
 
-  __device__ __forceinline__ unsigned long long weight(float l) const {
-    if (l == top) return 1ull << kUnitBits;
+  // W, and far(l).
+  __device__ __forceinline__ unsigned long long weight(float l, float& ph) const {
     // (top - l) pre = s + e exactly
-    l *= pre;
-    const float s = near - l, t = s - near;
-    const float e = (near - (s - t)) - (l + t);
-    const float ph = s * ch;
-    if (!(ph < kFar)) return 0ull;
-    const float pl = fmaf(s, ch, -ph) + fmaf(s, cl, e * ch);
-    // the nearest 256th, by the addition of 1.5 2^23
-    const float mf = fmaf(ph, 256.0f, 12582912.0f);
-    const int m = (int)(__float_as_uint(mf) - 0x4B400000u);
-    const float r = fmaf(mf - 12582912.0f, -0x1p-8f, ph);
-    // z = (r + pl) ln 2 in two parts, e^-z - 1 = -zh + el
-    constexpr float kLn2H = 0.693147182464599609375f, kLn2L = -1.904654299957768e-9f;
-    const float zh = r * kLn2H;
-    const float zl = fmaf(r, kLn2H, -zh) + fmaf(r, kLn2L, pl * kLn2H);
-    const float z = zh + zl;
-    const float el = fmaf(z * z, fmaf(z, fmaf(z, 1.0f / 24.0f, -1.0f / 6.0f), 0.5f), -zl);
-    // times the table's power, in two parts: v + rest
-    const float2 p = power[m & (kTable - 1)];
-    const float a = -p.x * zh, b = fmaf(-p.x, zh, -a);
-    const float v = p.x + a, ve = a - (v - p.x);
-    const float rest = ve + (b + fmaf(-p.y, zh, fmaf(p.x, el, p.y)));
-    // v is a multiple of 2^-25 up to 1, |rest| < 2^-18
-    const long long f =
-        ((long long)__float2int_rz(v * 0x1p30f) << 19) + __float2int_rd(rest * 0x1p49f);
-    const int shift = (m >> 8) + 49 - kUnitBits;
-    return (unsigned long long)(f >> shift);
+    const float lp = l * pre;
+    const float s = fmaf(-l, pre, near), t = s - near;
+    const float e = (near - (s - t)) - (lp + t);
+    const float yh = s * ch;
+    const float pl = fmaf(e, ch, fmaf(s, cl, fmaf(s, ch, -yh)));
+    // (-Inf and NaN: kFar, weight 0, whatever the rest below)
+    ph = fmaxf(fminf(yh, kFar), 0.0f);
+    // the nearest whole number, by the addition of 1.5 2^23
+    const float mf = ph + 12582912.0f;
+    const unsigned int m = __float_as_uint(mf) - 0x4B400000u;
+    const float z = (ph - (mf - 12582912.0f)) + pl;
+    // 1 - 2^(-z/512) = z (k1 - z (k2 - z k3)), k_i = (ln 2 / 512)^i / i!
+    constexpr float k1 = 1.35380308703114e-3f, k2 = 9.16391399231e-7f, k3 = 4.1353784e-10f;
+    const float q = z * fmaf(-z, fmaf(-z, k3, k2), k1);
+    const unsigned long long p = power[m & (kTable - 1)];
+    // 2^31 2^(-j/512) to 2^-25 of itself
+    const float pf = __uint2float_rn((unsigned int)(p >> 11));
+    const int d = __float2int_rn(pf * (q * 0x1p10f));  // halves: 31 bits (a NaN: 0)
+    return (p - 2ll * d) >> (m / kTable);
+  }
+
+  // 2^-42 W within 2^-22 (the special function unit's power of two) and two
+  // roundings of itself.
+  __device__ __forceinline__ float share(float l) const {
+    const float lp = l * pre;
+    const float s = fmaf(-l, pre, near), t = s - near;
+    const float e0 = (near - (s - t)) - (lp + t);
+    const float yh = s * ch;
+    const float pl = fmaf(e0, ch, fmaf(s, cl, fmaf(s, ch, -yh)));
+    const float ph = fmaxf(fminf(yh, kFar), 0.0f);
+    float e;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(ph * (-1.0f / kTable)));
+    // (pl is no number where y is none)
+    return ph >= 42.0f * kTable ? 0.0f : ph > 0.0f ? fmaf(e, pl * -1.35380308703114e-3f, e) : 1.0f;
   }
 };
 
@@ -213,96 +276,109 @@ struct SampleArgs {
   int32_t* token;
   float* p;
   int vocab;
-  int run;     // logits of a warp, a multiple of 4
-  int vector;  // rows may be read four logits at a time
+  int groups;       // 16-byte groups of logits that a thread holds
+  int pitch;        // groups between two threads' in shared memory: odd
+  Divisor by;       // groups
 };
 
-template <typename T>
-__device__ __forceinline__ float4 four(const T* p) {
-  if constexpr (sizeof(T) == 4) {
-    return *reinterpret_cast<const float4*>(p);
-  } else {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    const T* t = reinterpret_cast<const T*>(&u);
-    return make_float4(elem_float(t[0]), elem_float(t[1]), elem_float(t[2]), elem_float(t[3]));
-  }
-}
-
-// A NaN counts as -Inf.
-__device__ __forceinline__ float plain(float x) { return x == x ? x : -INFINITY; }
-
-// One cluster's row.  Everything but `cache` and the histogram is the same in
-// every CTA after each exchange, so that all take the same branches.
+// One cluster's row.  The row is read in aligned 16-byte groups: place 0 is the
+// first logit of the group that holds token 0, and token v stands at place
+// v + skew.  Everything but the row's parts is the same in every CTA after each
+// exchange, so that all take the same branches.
 template <typename T, bool kCached>
 struct RowSampler {
+  static constexpr int kPer = 16 / (int)sizeof(T);  // logits of a group
   SampleShared& sh;
-  float* cache;            // this CTA's part of the row (kCached)
+  uint4* cache;            // this CTA's part of the row (kCached)
   const T* row;
   const SampleArgs& a;
   int rank, ranks, tid, lane, warp;
-  int begin;               // first token of this warp's run
+  int skew;
+  int first;               // this thread's first place, in groups
   Scale scale;
   unsigned long long least;  // weights below it are left out (min-p)
+  unsigned long long marks;  // this thread's tokens that a nucleus may end at
   bool has_cut;
-  Cut cut;
+  float cut_l;             // tokens of a larger logit stay, and of this one
+  int cut_v;               // those up to this index
 
-  // Four logits of this warp's run at offset i (a multiple of 4); -Inf past it
-  // and past the row.
-  __device__ __forceinline__ float4 read(int i) const {
-    float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    if (i >= a.run || begin + i >= a.vocab) return v;
-    if constexpr (kCached) return *reinterpret_cast<const float4*>(cache + warp * a.run + i);
-    return load(i);
-  }
-  __device__ __forceinline__ float4 load(int i) const {
-    const int at = begin + i;
-    float4 v;
-    if (a.vector && at + 4 <= a.vocab) {
-      v = four<T>(row + at);
-    } else {
-      v.x = elem_float(row[at]);
-      v.y = at + 1 < a.vocab ? elem_float(row[at + 1]) : -INFINITY;
-      v.z = at + 2 < a.vocab ? elem_float(row[at + 2]) : -INFINITY;
-      v.w = at + 3 < a.vocab ? elem_float(row[at + 3]) : -INFINITY;
-    }
-    v.x = plain(v.x);
-    v.y = plain(v.y);
-    v.z = plain(v.z);
-    v.w = plain(v.w);
-    return v;
+  // A group from memory; -Inf where the row is not.
+  __device__ __forceinline__ uint4 load(int group) const {
+    const int v0 = group * kPer - skew;
+    if (v0 >= 0 && v0 + kPer <= a.vocab) return *reinterpret_cast<const uint4*>(row + v0);
+    alignas(16) T t[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      t[i] = v0 + i >= 0 && v0 + i < a.vocab ? row[v0 + i] : float_elem<T>(-INFINITY);
+    return *reinterpret_cast<const uint4*>(t);
   }
 
-  // f(token, logit) over this warp's run, in order of index by rounds.
+  __device__ __forceinline__ uint4 read(int i) const {
+    if constexpr (kCached) return cache[(warp * 32 + lane) * a.pitch + i];
+    return load(first + i);
+  }
+
+  // f(token, logit) over this thread's tokens, in order; outside the row the
+  // logit is -Inf.
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    for (int i = 4 * lane; i - 4 * lane < a.run; i += 128) {
-      const float4 v = read(i);
-      f(begin + i, v.x);
-      f(begin + i + 1, v.y);
-      f(begin + i + 2, v.z);
-      f(begin + i + 3, v.w);
+#pragma unroll 2
+    for (int i = 0; i < a.groups; ++i) {
+      const uint4 g = read(i);
+      const T* t = reinterpret_cast<const T*>(&g);
+      const int v = (first + i) * kPer - skew;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) f(v + j, elem_float(t[j]));
     }
   }
 
-  // The row into shared memory, and the row's largest logit.
-  __device__ __forceinline__ float fill() {
-    float most = -INFINITY;
-    constexpr int kAhead = 4;
-    for (int i0 = 4 * lane; i0 - 4 * lane < a.run; i0 += 128 * kAhead) {
-      float4 v[kAhead];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int i = i0 + 128 * j;
-        v[j] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        if (i < a.run && begin + i < a.vocab) v[j] = load(i);
-      }
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int i = i0 + 128 * j;
-        if (kCached && i < a.run) *reinterpret_cast<float4*>(cache + warp * a.run + i) = v[j];
-        most = fmaxf(most, fmaxf(fmaxf(v[j].x, v[j].y), fmaxf(v[j].z, v[j].w)));
+  // f over the tokens that are marked, which are few; over all of a thread
+  // that has more tokens than marks.
+  template <bool kMarked, typename F>
+  __device__ __forceinline__ void some(F f) const {
+    if (!kMarked || a.groups * kPer > 64) {
+      each(f);
+    } else {
+      for (unsigned long long m = marks; m != 0ull; m &= m - 1ull) {
+        const int i = __ffsll((long long)m) - 1;
+        f(first * kPer - skew + i, one(lane, i));
       }
     }
+  }
+
+  // One logit of this warp's thread q.
+  __device__ __forceinline__ float one(int q, int i) const {
+    if constexpr (kCached) {
+      const T* t = reinterpret_cast<const T*>(cache + (warp * 32 + q) * a.pitch);
+      return elem_float(t[i]);
+    } else {
+      const int v = (first + (q - lane) * a.groups) * kPer + i - skew;
+      return v >= 0 && v < a.vocab ? elem_float(row[v]) : -INFINITY;
+    }
+  }
+
+  // The row into shared memory, with the table's power of this thread, and the
+  // row's largest logit.
+  __device__ __forceinline__ float fill(unsigned long long power) {
+    const int mine = first - lane * a.groups;  // the warp's first group
+    if constexpr (kCached) {
+      for (int i = lane; i < 32 * a.groups; i += 32) {
+        const int q = (int)quotient((uint32_t)i, a.by);
+        uint4* to = cache + (warp * 32 + q) * a.pitch + (i - q * a.groups);
+        const int v0 = (mine + i) * kPer - skew;
+        if (v0 >= 0 && v0 + kPer <= a.vocab)
+          copy16(to, row + v0);
+        else
+          *to = load(mine + i);
+      }
+      sh.power[tid] = power;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+    } else {
+      sh.power[tid] = power;
+    }
+    float most = -INFINITY;
+    each([&](int, float l) { most = fmaxf(most, l); });  // (a NaN is passed over)
     const uint32_t k = __reduce_max_sync(0xFFFFFFFFu, key_of(most));
     if (lane == 0) sh.tmp_n[warp] = k;
     __syncthreads();
@@ -320,7 +396,7 @@ struct RowSampler {
   __device__ __forceinline__ int likeliest() {
     int at = 0x7FFFFFFF;
     each([&](int v, float l) {
-      if (l == scale.top && v < at) at = v;
+      if (l == scale.top) at = min(at, v);
     });
     at = __reduce_min_sync(0xFFFFFFFFu, at);
     if (lane == 0) sh.tmp_n[warp] = (uint32_t)at;
@@ -335,152 +411,211 @@ struct RowSampler {
   }
 
   __device__ __forceinline__ unsigned long long weight_kept(float l) const {
-    const unsigned long long w = scale.weight(l);
-    return w >= least ? w : 0ull;
+    float y;
+    const unsigned long long w = scale.weight(l, y);
+    return least > 1ull && w < least ? 0ull : w;
   }
 
-  // A bin's entry; 64-bit sums in two words, the carry passed on by whoever
-  // wraps the lower one.
-  __device__ __forceinline__ void enter(int bin, unsigned long long w) {
-    atomicAdd(&sh.count[bin], 1u);
-    const uint32_t lo = (uint32_t)w;
-    uint32_t hi = (uint32_t)(w >> 32);
-    if (lo != 0u && atomicAdd(&sh.lo[bin], lo) > 0xFFFFFFFFu - lo) ++hi;
-    if (hi != 0u) atomicAdd(&sh.hi[bin], hi);
+  // A token's place in the first histogram: bin (int)place(l), kBins (or
+  // more by a rounding) for tokens of no weight.
+  __device__ __forceinline__ float place(float l) const {
+    return scale.far(l) * (kBins / kFar);
+  }
+  // Its bin in one that divides the bins [b0, b0 + kFine / step) finer.
+  __device__ __forceinline__ static int finer(float x, int b0, float step) {
+    return min((int)((x - (float)b0) * step), kFine - 1);
   }
 
-  __device__ __forceinline__ int first_bin(float l) const {
-    const float y = scale.far(l);
-    return y < kFar ? min((int)(y * (kBins / kFar)), kBins - 1) : -1;
+  __device__ __forceinline__ void enter(int bin, unsigned long long w) const {
+    atomicAdd(&sh.count_fine[bin], 1u);
+    atomicAdd(&sh.weight[0][bin], (unsigned int)w & 0x7FFFu);
+    atomicAdd(&sh.weight[1][bin], (unsigned int)(w >> 15) & 0x3FFFu);
+    atomicAdd(&sh.weight[2][bin], (unsigned int)(w >> 29));
   }
 
-  // The cluster's histogram into every CTA's merged_n / merged_w.
-  // bin_of(l): a token's bin, or -1.
-  template <typename F>
-  __device__ __forceinline__ void histogram(F bin_of, bool weights) {
-    for (int i = tid; i < kBins; i += kSThreads) sh.count[i] = sh.lo[i] = sh.hi[i] = 0u;
+  // The finer histogram; seen by the cluster after its barrier, and cleared
+  // again only after another one that follows every CTA's last look at it.
+  __device__ __forceinline__ void clear() const {
+    if (tid < kFine)
+      sh.count_fine[tid] = sh.weight[0][tid] = sh.weight[1][tid] = sh.weight[2][tid] = 0u;
     __syncthreads();
-    each([&](int, float l) {
-      const int b = bin_of(l);
-      if (b >= 0) enter(b, weights ? weight_kept(l) : 0ull);
-    });
-    cluster_sync();
-    const int per = kBins / ranks;
-    for (int i = tid; i < per; i += kSThreads) {
-      const int b = rank * per + i;
-      uint32_t n = 0;
-      unsigned long long w = 0;
-      for (int q = 0; q < ranks; ++q) {
-        n += get_u32(&sh.count[b], q);
-        w += ((unsigned long long)get_u32(&sh.hi[b], q) << 32) + get_u32(&sh.lo[b], q);
-      }
-      for (int q = 0; q < ranks; ++q) {
-        put_u32(&sh.merged_n[b], q, n);
-        put_u64(&sh.merged_w[b], q, w);
-      }
+  }
+  // (before the barrier, where weights were entered)
+  __device__ __forceinline__ void gather() const {
+    __syncthreads();
+    if (tid < kFine)
+      sh.bins[tid] = Bin{sh.weight[0][tid] + ((unsigned long long)sh.weight[1][tid] << 15) +
+                             ((unsigned long long)sh.weight[2][tid] << 29),
+                         sh.count_fine[tid], 0u};
+  }
+
+  // f(rank), each CTA beginning with its own, so that not all read one at a time.
+  template <typename F>
+  __device__ __forceinline__ void each_rank(F f) const {
+    int q = rank;
+#pragma unroll 4
+    for (int i = 0; i < ranks; ++i) {
+      f(q);
+      q = q + 1 < ranks ? q + 1 : 0;
     }
+  }
+
+  // Counts of the row's tokens by place.
+  __device__ __forceinline__ void count_places() const {
+    sh.count[tid] = 0u;
+    __syncthreads();
+    each([&](int, float l) { atomicAdd(&sh.count[min((int)place(l), kBins)], 1u); });
     cluster_sync();
   }
 
-  // The bin in which the running count reaches `goal` (by_weight: the running
-  // weight), after `n0` tokens of weight `w0`: bin (-1: none), above_n, above_w,
-  // bin_n.
-  __device__ __forceinline__ void find(bool by_weight, unsigned long long goal, uint32_t n0,
-                                       unsigned long long w0) {
-    constexpr int kPer = kBins / kSThreads;
-    uint32_t n[kPer], my_n = 0;
-    unsigned long long w[kPer], my_w = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      n[i] = sh.merged_n[tid * kPer + i];
-      w[i] = sh.merged_w[tid * kPer + i];
-      my_n += n[i];
-      my_w += w[i];
+  // The bin of the row's counts, or of the finer histogram, in which the
+  // running count reaches `goal` (by_weight: the running weight), after n0
+  // tokens of weight w0: bin (-1: none), bin_n, above_n, above_w.
+  __device__ __forceinline__ void find(bool fine, bool by_weight, unsigned long long goal,
+                                       uint32_t n0, unsigned long long w0) {
+    uint32_t n = 0;
+    unsigned long long w = 0;
+    if (fine && tid >= kFine)
+      ;  // (no such bin)
+    else if (by_weight)
+      each_rank([&](int q) {
+        const Bin b = get_bin(&sh.bins[tid], q);
+        n += b.n;
+        w += b.w;
+      });
+    else {
+      const unsigned int* c = fine ? &sh.count_fine[tid] : &sh.count[tid];
+      each_rank([&](int q) { n += get_u32(c, q); });
     }
-    const uint32_t scan_n = warp_scan_add(my_n, lane);
-    const unsigned long long scan_w = warp_scan_add(my_w, lane);
+    const uint32_t scan_n = warp_scan_add(n, lane);
+    const unsigned long long scan_w = by_weight ? warp_scan_add(w, lane) : 0ull;
     if (lane == 31) {
       sh.tmp_n[warp] = scan_n;
       sh.tmp_w[warp] = scan_w;
     }
     if (tid == 0) sh.bin = -1;
     __syncthreads();
-    uint32_t run_n = n0 + scan_n - my_n;
-    unsigned long long run_w = w0 + scan_w - my_w;
+    uint32_t run_n = n0 + scan_n - n;
+    unsigned long long run_w = w0 + scan_w - w;
     for (int q = 0; q < warp; ++q) {
       run_n += sh.tmp_n[q];
       run_w += sh.tmp_w[q];
     }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const unsigned long long before = by_weight ? run_w : run_n;
-      if (before < goal && goal <= before + (by_weight ? w[i] : n[i])) {
-        sh.bin = tid * kPer + i;
-        sh.above_n = run_n;
-        sh.above_w = run_w;
-        sh.bin_n = n[i];
-      }
-      run_n += n[i];
-      run_w += w[i];
+    const unsigned long long before = by_weight ? run_w : run_n;
+    if (before < goal && goal <= before + (by_weight ? w : n)) {
+      sh.bin = tid;
+      sh.above_n = run_n;
+      sh.above_w = run_w;
+      sh.bin_n = n;
     }
     __syncthreads();
   }
 
-  // Lists the bin's tokens in every CTA and finds the one at which the count
-  // (the weight) reaches `goal`.  Sets sh.cut and sh.total, the weight up to it.
-  template <typename F>
-  __device__ __forceinline__ void resolve(F bin_of, int which, bool by_weight,
-                                          unsigned long long goal) {
-    const int bin = sh.bin;
-    const int n = (int)sh.bin_n;
-    if (warp == 0) {
-      uint32_t c = lane < ranks ? get_u32(&sh.count[bin], lane) : 0u;
-      const uint32_t upto = warp_scan_add(c, lane);
-      if (lane == rank) sh.base = upto - c;
-      if (lane == 0) sh.pushed = 0u;
+  // The bins [bin, bin_last] of the counts in which a nucleus of top_p ends.
+  // kSure: in which it can end at all, between bounds of the weights before each
+  // bin, its own from its edges, a thousandth for roundings on either side
+  // (about a tenth of the tokens).  Else where it ends if every token weighs
+  // its bin's mean, and the neighbour that is nearer than a quarter of a bin: a
+  // bin or two, and if the exact sums say otherwise the search is repeated.
+  // `last` is top-k's bin.
+  template <bool kSure>
+  __device__ __forceinline__ void bracket(float top_p, int last) {
+    uint32_t n = 0;
+    each_rank([&](int q) { n += get_u32(&sh.count[tid], q); });
+    constexpr float kOctaves = kFar / (kBins * kTable);
+    const float upper = exp2f(-kOctaves * (float)tid) * (kSure ? 1.001f : 0.9712f);
+    const float lower = kSure ? exp2f(-kOctaves * (float)(tid + 1)) * 0.999f : upper;
+    const float floor = __ull2float_rn(least) * 0x1p-42f;
+    const float most = tid <= last && upper >= floor ? (float)n * upper : 0.0f;
+    const float fewest =
+        tid <= last - (kSure ? 1 : 0) && lower >= floor ? (float)n * lower : 0.0f;
+    float run_most = warp_scan_add(most, lane), run_fewest = warp_scan_add(fewest, lane);
+    if (lane == 31) {
+      sh.tmp_f[0][warp] = run_most;
+      sh.tmp_f[1][warp] = run_fewest;
+    }
+    if (tid == 0) {
+      sh.bin = kBins - 1;
+      sh.bin_last = 0;
     }
     __syncthreads();
-    each([&](int v, float l) {
-      if (bin_of(l) == bin) {
-        const uint32_t at = sh.base + atomicAdd(&sh.pushed, 1u);
-        for (int q = 0; q < ranks; ++q) {
-          put_u32(&sh.list_key[which][at], q, key_of(l));
-          put_u32(&sh.list_index[which][at], q, (uint32_t)v);
-        }
+    float all_most = 0.0f, all_fewest = 0.0f;
+    for (int q = 0; q < kSWarps; ++q) {
+      if (q == warp) {
+        run_most += all_most;
+        run_fewest += all_fewest;
       }
+      all_most += sh.tmp_f[0][q];
+      all_fewest += sh.tmp_f[1][q];
+    }
+    const float p = fmaxf(top_p, 0.0f);
+    if constexpr (kSure) {
+      if (run_most * 1.001f >= p * all_fewest) atomicMin(&sh.bin, tid);
+      if ((run_fewest - fewest) * 0.999f < p * all_most * 1.001f) atomicMax(&sh.bin_last, tid);
+    } else {
+      const float goal = p * all_most;
+      if (run_most + 0.25f * most >= goal) atomicMin(&sh.bin, tid);
+      if (run_most - 1.25f * most < goal) atomicMax(&sh.bin_last, tid);
+    }
+    __syncthreads();
+  }
+
+  // Lists in every CTA the n tokens for which in_list(l) holds, and their
+  // weights.  kMarked: only marked tokens are asked.  (A CTA's own part is read by the
+  // others until their next cluster barrier.)
+  template <bool kMarked, typename F>
+  __device__ __forceinline__ void list(F in_list, int which, int n) {
+    some<kMarked>([&](int v, float l) {
+      if (in_list(l)) sh.found[which][atomicAdd(&sh.pushed[which], 1u)] = order_of(v, l);
     });
     cluster_sync();
-    for (int i = tid; i < n; i += kSThreads)
-      sh.list_w[i] = weight_kept(float_of(sh.list_key[which][i]));
+    const uint32_t mine = lane < ranks ? get_u32(&sh.pushed[which], lane) : 0u;
+    int i = tid, q = 0;
+    for (int x = 0; x < ranks - 1; ++x) {
+      const int c = (int)__shfl_sync(0xFFFFFFFFu, mine, x);
+      if (q == x && i >= c) {
+        i -= c;
+        ++q;
+      }
+    }
+    if (tid < n) {
+      const unsigned long long o = get_u64(&sh.found[which][i], q);
+      sh.list[tid] = o;
+      sh.list_w[tid] = weight_kept(float_of((uint32_t)(o >> 32)));
+    }
     __syncthreads();
-    // g threads to a candidate
-    int g = 1;
-    while (g < 32 && 2 * g * n <= kSThreads) g *= 2;
-    const int i = tid / g, sub = tid % g;
+  }
+
+  // Of n listed tokens, the one at which the count (the weight) reaches
+  // `goal`, after above_n tokens of weight above_w: sh.cut, and sh.total, the
+  // weight up to it.
+  __device__ __forceinline__ void rank_list(int n, bool by_weight, unsigned long long goal,
+                                            uint32_t above_n, unsigned long long above_w) {
+    constexpr int g = kSThreads / kList;  // threads to a token
+    const int i = tid / g;
     uint32_t before_n = 0;
     unsigned long long before_w = 0;
     if (i < n) {
-      const uint32_t key = sh.list_key[which][i];
-      const int index = sh.list_index[which][i];
-      for (int j = sub; j < n; j += g) {
-        const uint32_t kj = sh.list_key[which][j];
-        if (kj > key || (kj == key && sh.list_index[which][j] < index)) {
-          ++before_n;
-          before_w += sh.list_w[j];
-        }
+      const unsigned long long o = sh.list[i];
+#pragma unroll 4
+      for (int j = tid % g; j < n; j += g) {
+        const bool before = sh.list[j] > o;
+        before_n += before ? 1u : 0u;
+        before_w += before ? sh.list_w[j] : 0ull;
       }
     }
+#pragma unroll
     for (int o = 1; o < g; o *= 2) {
       before_n += __shfl_xor_sync(0xFFFFFFFFu, before_n, o);
       before_w += __shfl_xor_sync(0xFFFFFFFFu, before_w, o);
     }
-    if (i < n && sub == 0) {
-      before_w += sh.above_w;
-      before_n += sh.above_n;
+    if (i < n && tid % g == 0) {
+      before_w += above_w;
+      before_n += above_n;
       const unsigned long long b = by_weight ? before_w : before_n;
       const unsigned long long mine = by_weight ? sh.list_w[i] : 1ull;
       if (b < goal && goal <= b + mine) {
-        sh.cut = Cut{sh.list_key[which][i], sh.list_index[which][i]};
+        sh.cut = sh.list[i];
         sh.total = before_w + sh.list_w[i];
       }
     }
@@ -489,70 +624,82 @@ struct RowSampler {
 
   // Of more equal logits than the list holds, the one at which the goal is
   // reached: the m-th by index.
-  __device__ __forceinline__ void resolve_equal(uint32_t key, bool by_weight,
-                                                unsigned long long goal) {
+  __device__ __forceinline__ void rank_equal(uint32_t key, bool by_weight,
+                                             unsigned long long goal) {
     const float l = float_of(key);
     const unsigned long long w = weight_kept(l);
     const unsigned long long m = by_weight ? (goal - sh.above_w + w - 1) / w : goal - sh.above_n;
     uint32_t mine = 0;
     each([&](int, float x) { mine += x == l ? 1u : 0u; });
-    mine = warp_add(mine);
-    if (lane < ranks) put_u64(&sh.sums[rank * kSWarps + warp], lane, mine);
-    cluster_sync();
-    unsigned long long before = 0;
-    for (int q = 0; q < rank * kSWarps + warp; ++q) before += sh.sums[q];
+    const uint32_t upto = warp_scan_add(mine, lane);
+    exchange(__shfl_sync(0xFFFFFFFFu, upto, 31));
+    unsigned long long all, before = parts_before(0, &all);
+    before += upto - mine;
     if (before < m && m <= before + mine) {
-      // this warp's run holds it
-      for (int i = 4 * lane; i - 4 * lane < a.run; i += 128) {
-        const float4 v = read(i);
-        const float x[4] = {v.x, v.y, v.z, v.w};
-        uint32_t c = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c += x[j] == l ? 1u : 0u;
-        const uint32_t scan = warp_scan_add(c, lane);
-        unsigned long long run = before + scan - c;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (x[j] == l && ++run == m)
-            for (int q = 0; q < ranks; ++q) put_u32(&sh.found, q, (uint32_t)(begin + i + j));
-        before += __shfl_sync(0xFFFFFFFFu, scan, 31);
-      }
+      each([&](int v, float x) {
+        if (x == l && ++before == m)
+          for (int q = 0; q < ranks; ++q) put_u32(&sh.equal, q, (uint32_t)v);
+      });
     }
     cluster_sync();
     if (tid == 0) {
-      sh.cut = Cut{key, sh.found};
+      sh.cut = order_of(sh.equal, l);
       sh.total = sh.above_w + m * w;
     }
     __syncthreads();
   }
 
-  // Where the running count (weight) reaches the goal, from the row's first
-  // histogram on, which `fresh` says is in place (and is no more, if divided
-  // further).  False: it does not.
-  __device__ __forceinline__ bool search(bool by_weight, unsigned long long goal, bool weights,
-                                         bool* fresh) {
-    const auto bin0 = [this](float l) { return first_bin(l); };
-    if (!*fresh) histogram(bin0, weights);
-    *fresh = true;
-    find(by_weight, goal, 0u, 0ull);
-    if (sh.bin < 0) return false;
-    const int which = by_weight ? 1 : 0;
-    if (sh.bin_n <= kList) {
-      resolve(bin0, which, by_weight, goal);
-      return true;
+  // Every warp's sum to every CTA.
+  __device__ __forceinline__ void exchange(unsigned long long sum) {
+    if (lane < ranks) put_u64(&sh.sums[0][rank * kSWarps + warp], lane, sum);
+    cluster_sync();
+  }
+  // The sums of the warps before this one, and of all.
+  __device__ __forceinline__ unsigned long long parts_before(int which,
+                                                             unsigned long long* all) const {
+    constexpr int kEach = kParts / 32;
+    const int me = rank * kSWarps + warp;
+    unsigned long long before = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int q = lane + 32 * i;
+      const unsigned long long s = q < ranks * kSWarps ? sh.sums[which][q] : 0ull;
+      total += s;
+      before += q < me ? s : 0ull;
     }
-    *fresh = false;
-    // the bin's range of logits, then a histogram of its bits, until few are
-    // left or all are equal
-    int bin = sh.bin;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+      before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+    }
+    *all = total;
+    return before;
+  }
+
+  // Where the running count (weight) reaches the goal within `bin` of a
+  // histogram by bin_of, of which sh.bin_n tokens are in that bin after
+  // sh.above_n of weight sh.above_w: sh.cut, and sh.total, the weight up to it.
+  // (Divided further in the same buffer: the exchange of the range stands
+  // between the last look at it and the next use.)
+  template <bool kMarked, typename F>
+  __device__ __forceinline__ void resolve(F bin_of, bool by_weight, unsigned long long goal) {
+    const int which = by_weight ? 1 : 0;
+    const int bin = sh.bin;
+    const int n = (int)sh.bin_n;
+    if (n <= kList) {
+      list<kMarked>([&](float l) { return bin_of(l) == bin; }, which, n);
+      rank_list(n, by_weight, goal, sh.above_n, sh.above_w);
+      return;
+    }
     uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-    each([&](int, float l) {
-      if (first_bin(l) == bin) {
+    some<kMarked>([&](int, float l) {
+      if (bin_of(l) == bin) {
         lo = min(lo, key_of(l));
         hi = max(hi, key_of(l));
       }
     });
     for (;;) {
+      // the range of what is left; none of its tokens may be this warp's
       lo = __reduce_min_sync(0xFFFFFFFFu, lo);
       hi = __reduce_max_sync(0xFFFFFFFFu, hi);
       if (lane == 0) {
@@ -574,145 +721,291 @@ struct RowSampler {
         hi = max(hi, sh.key_max[q]);
       }
       if (lo == hi) {
-        resolve_equal(lo, by_weight, goal);
-        return true;
+        rank_equal(lo, by_weight, goal);
+        return;
       }
       const uint32_t klo = lo, khi = hi;
       int shift = 0;
-      while (((khi - klo) >> shift) >= (uint32_t)kBins) ++shift;
+      while (((khi - klo) >> shift) >= (uint32_t)kFine) ++shift;
       const auto bits = [=](float l) {
         const uint32_t k = key_of(l);
         return k >= klo && k <= khi ? (int)((khi - k) >> shift) : -1;
       };
       const uint32_t above_n = sh.above_n;
       const unsigned long long above_w = sh.above_w;
-      histogram(bits, weights);
-      find(by_weight, goal, above_n, above_w);
-      if (sh.bin_n <= kList) {
-        resolve(bits, which, by_weight, goal);
-        return true;
+      clear();
+      some<kMarked>([&](int, float l) {
+        const int x = bits(l);
+        if (x < 0) return;
+        if (by_weight)
+          enter(x, weight_kept(l));
+        else
+          atomicAdd(&sh.count_fine[x], 1u);
+      });
+      if (by_weight) gather();
+      cluster_sync();
+      find(true, by_weight, goal, above_n, above_w);
+      const int b = sh.bin;
+      const int left = (int)sh.bin_n;
+      if (left <= kList) {
+        list<kMarked>([&](float l) { return bits(l) == b; }, which, left);
+        rank_list(left, by_weight, goal, sh.above_n, sh.above_w);
+        return;
       }
-      bin = sh.bin;
       lo = 0xFFFFFFFFu;
       hi = 0u;
-      each([&](int, float l) {
-        if (bits(l) == bin) {
+      some<kMarked>([&](int, float l) {
+        if (bits(l) == b) {
           lo = min(lo, key_of(l));
           hi = max(hi, key_of(l));
         }
       });
-      __syncthreads();  // every thread has read sh.bin and the like
     }
   }
 
-  __device__ __forceinline__ unsigned long long staying(int v, float l) const {
-    if (has_cut) {
-      const uint32_t k = key_of(l);
-      if (k < cut.key || (k == cut.key && v > cut.index)) return 0ull;
+  // Top-k's cut, in bin b of the counts.
+  __device__ __forceinline__ void cut_count(int b, unsigned long long k) {
+    const auto bin_of = [this, b](float l) {
+      const float x = place(l);
+      return (int)x == b ? finer(x, b, (float)kFine) : -1;
+    };
+    const uint32_t above_n = sh.above_n;
+    clear();
+    each([&](int, float l) {
+      const int x = bin_of(l);
+      if (x >= 0) atomicAdd(&sh.count_fine[x], 1u);
+    });
+    cluster_sync();
+    find(true, false, k, above_n, 0ull);
+    resolve<false>(bin_of, false, k);
+  }
+
+  // The nucleus' cut among the bins [b0, b1] of the counts, or false.  *mine:
+  // this thread's weight of the bins before b0.
+  __device__ __forceinline__ bool cut_weight(int b0, int b1, float top_p,
+                                             unsigned long long* mine) {
+    const float step = (float)kFine / (float)(b1 - b0 + 1);
+    const auto bin_of = [=](float l) {
+      const float x = place(l);
+      const int b = (int)x;
+      return b >= b0 && b <= b1 ? finer(x, b0, step) : -1;
+    };
+    clear();
+    unsigned long long above = 0, all = 0;
+    marks = 0;
+    const auto pass = [&](auto plain) {
+      int i = 0;
+      each([&](int v, float l) {
+        float y;
+        unsigned long long w = scale.weight(l, y);
+        if (!plain.value && (w < least || (has_cut && !before_cut(v, l)))) w = 0ull;
+        const float x = y * (kBins / kFar);
+        const int b = (int)x;
+        all += w;
+        above += b < b0 ? w : 0ull;
+        if (b >= b0 && b <= b1) {
+          enter(finer(x, b0, step), w);
+          marks |= 1ull << (i & 63);
+        }
+        ++i;
+      });
+    };
+    if (has_cut || least > 1ull)
+      pass(std::false_type());
+    else
+      pass(std::true_type());
+    unsigned long long rest = all - above;
+    gather();
+    *mine = above;
+    above = __shfl_sync(0xFFFFFFFFu, warp_scan_add(above, lane), 31);
+    rest = __shfl_sync(0xFFFFFFFFu, warp_scan_add(rest, lane), 31);
+    if (lane < ranks) put_u64(&sh.sums[1][rank * kSWarps + warp], lane, rest);
+    exchange(above);
+    unsigned long long before, others;
+    parts_before(0, &before);
+    parts_before(1, &others);
+    if (tid == 0)
+      sh.goal = max(1ull, (unsigned long long)ceil((double)fmaxf(top_p, 0.0f) *
+                                                   (double)(before + others)));
+    __syncthreads();
+    const unsigned long long goal = sh.goal;
+    find(true, true, goal, 0u, before);
+    if (sh.bin < 0) return false;
+    resolve<true>(bin_of, true, goal);
+    return true;
+  }
+
+  // The nucleus' cut, top-k's in bin `last` (or none).  Returns this thread's
+  // weight of what stays.
+  __device__ __forceinline__ unsigned long long cut_nucleus(float top_p, int last, bool draws) {
+    bracket<false>(top_p, last);
+    int b0 = sh.bin, b1 = max(sh.bin, sh.bin_last);
+    unsigned long long mine;
+    if (!cut_weight(b0, b1, top_p, &mine)) {
+      cluster_sync();  // (the second buffer has been read)
+      bracket<true>(top_p, last);
+      b0 = sh.bin;
+      b1 = max(sh.bin, sh.bin_last);
+      cut_weight(b0, b1, top_p, &mine);
     }
+    take_cut();
+    if (draws)
+      some<true>([&](int v, float l) {
+        const int b = (int)place(l);
+        if (b >= b0 && b <= b1) mine += staying(v, l);
+      });
+    return mine;
+  }
+
+  __device__ __forceinline__ bool before_cut(int v, float l) const {
+    return l > cut_l || (l == cut_l && v <= cut_v);
+  }
+  __device__ __forceinline__ unsigned long long staying(int v, float l) const {
+    if (has_cut && !before_cut(v, l)) return 0ull;
     return weight_kept(l);
   }
-
-  // The token that the random number meets.
-  __device__ __forceinline__ void draw(float u, int32_t* out) {
+  __device__ __forceinline__ void take_cut() {
+    has_cut = true;
+    cut_l = float_of((uint32_t)(sh.cut >> 32));
+    cut_v = index_of(sh.cut);
+  }
+  // This thread's weight of what stays.
+  __device__ __forceinline__ unsigned long long sum() const {
     unsigned long long mine = 0;
-    each([&](int v, float l) { mine += staying(v, l); });
-    mine = warp_add(mine);
-    if (lane < ranks) put_u64(&sh.sums[rank * kSWarps + warp], lane, mine);
-    cluster_sync();
-    unsigned long long before = 0, total = 0;
-    for (int q = 0; q < ranks * kSWarps; ++q) {
-      const unsigned long long s = sh.sums[q];
-      if (q < rank * kSWarps + warp) before += s;
-      total += s;
-    }
+    if (has_cut || least > 1ull)
+      each([&](int v, float l) { mine += staying(v, l); });
+    else
+      each([&](int, float l) {
+        float y;
+        mine += scale.weight(l, y);
+      });
+    return mine;
+  }
+
+  __device__ __forceinline__ static unsigned long long point_of(float u,
+                                                                unsigned long long total) {
     unsigned int un = 0;
     if (u > 0.0f) un = (unsigned int)fminf(u * 0x1p24f, 16777215.0f);
-    const unsigned long long point =
-        un * (total >> 24) + ((un * (total & 0xFFFFFFull)) >> 24);
-    if (before > point || point >= before + mine) return;
-    // in this warp's run
-    for (int i = 4 * lane; i - 4 * lane < a.run; i += 128) {
-      const float4 v = read(i);
-      const float x[4] = {v.x, v.y, v.z, v.w};
-      unsigned long long w[4], c = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) c += w[j] = staying(begin + i + j, x[j]);
-      const unsigned long long scan = warp_scan_add(c, lane);
-      unsigned long long run = before + scan - c;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (run <= point && point < run + w[j]) *out = begin + i + j;
-        run += w[j];
-      }
-      before += __shfl_sync(0xFFFFFFFFu, scan, 31);
+    return un * (total >> 24) + ((un * (total & 0xFFFFFFull)) >> 24);
+  }
+
+  // The token that the random number meets; `mine` is this thread's weight of
+  // the tokens that stay.
+  __device__ __forceinline__ void draw(float u, int32_t* out, unsigned long long mine) {
+    const unsigned long long upto = warp_scan_add(mine, lane);
+    const unsigned long long sum = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    exchange(sum);
+    unsigned long long total, before = parts_before(0, &total);
+    const unsigned long long point = point_of(u, total);
+    if (before > point || point >= before + sum) return;
+    // in this warp's part: the thread that holds it, whose tokens the warp
+    // then takes one each
+    const int q = __ffs((int)__ballot_sync(0xFFFFFFFFu, before + upto > point)) - 1;
+    before += __shfl_sync(0xFFFFFFFFu, upto - mine, q);
+    const int v0 = (first + (q - lane) * a.groups) * kPer - skew;
+    for (int i = 0; i < a.groups * kPer; i += 32) {
+      const int at = i + lane;
+      const float l = at < a.groups * kPer ? one(q, at) : -INFINITY;
+      const unsigned long long w = staying(v0 + at, l);
+      const unsigned long long run = before + warp_scan_add(w, lane);
+      if (run - w <= point && point < run) *out = v0 + at;
+      before = __shfl_sync(0xFFFFFFFFu, run, 31);
       if (before > point) break;
     }
   }
 
-  // p = weight / total.
-  __device__ __forceinline__ void write(float* p) {
+  // The same among n listed tokens, those up to the cut.
+  __device__ __forceinline__ void draw_listed(int n, float u, int32_t* out) const {
+    const unsigned long long point = point_of(u, sh.total), cut = sh.cut;
+    constexpr int g = kSThreads / kList;
+    const int i = tid / g;
+    unsigned long long before = 0, mine = 0;
+    int index = 0;
+    if (i < n) {
+      const unsigned long long o = sh.list[i];
+      index = index_of(o);
+      mine = o >= cut ? sh.list_w[i] : 0ull;
+#pragma unroll 4
+      for (int j = tid % g; j < n; j += g) {
+        const unsigned long long oj = sh.list[j];
+        before += oj >= cut && index_of(oj) < index ? sh.list_w[j] : 0ull;
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < g; o *= 2) before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+    if (i < n && tid % g == 0 && before <= point && point < before + mine) *out = index;
+  }
+
+  // p = weight / total; consecutive tokens by consecutive threads.  Without
+  // min-p, which goes by W, the weights may be f32 powers.
+  __device__ __forceinline__ void write(float* p, bool summed) {
     unsigned long long total = sh.total;
-    if (!has_cut) {
-      unsigned long long mine = 0;
-      each([&](int v, float l) { mine += staying(v, l); });
-      mine = warp_add(mine);
-      if (lane < ranks) put_u64(&sh.sums[rank * kSWarps + warp], lane, mine);
-      cluster_sync();
-      total = 0;
-      for (int q = 0; q < ranks * kSWarps; ++q) total += sh.sums[q];
+    if (!summed) {
+      exchange(__shfl_sync(0xFFFFFFFFu, warp_scan_add(sum(), lane), 31));
+      parts_before(0, &total);
     }
     const float inv = 1.0f / __ull2float_rn(total);
-    each([&](int v, float l) {
-      if (v < a.vocab && v < begin + a.run) p[v] = __ull2float_rn(staying(v, l)) * inv;
-    });
+    if (least > 1ull)
+      each_place([&](int v, float l) { p[v] = __ull2float_rn(staying(v, l)) * inv; });
+    else
+      each_place([&](int v, float l) {
+        p[v] = has_cut && !before_cut(v, l) ? 0.0f : scale.share(l) * (0x1p42f * inv);
+      });
+  }
+
+  // f(token, logit) over the warp's tokens, neighbours by neighbouring threads.
+  template <typename F>
+  __device__ __forceinline__ void each_place(F f) const {
+    const int mine = (first - lane * a.groups) * kPer - skew;
+    const int width = a.groups * kPer;
+    for (int i = lane; i < 32 * width; i += 32) {
+      const int v = mine + i;
+      if (v < 0 || v >= a.vocab) continue;
+      float l;
+      if constexpr (kCached) {
+        const int q = (int)quotient((uint32_t)(i / kPer), a.by);
+        l = elem_float(reinterpret_cast<const T*>(cache + (warp * 32 + q) * a.pitch)[i - q * width]);
+      } else {
+        l = elem_float(row[v]);
+      }
+      f(v, l);
+    }
   }
 };
 
 template <typename T, bool kCached, bool kProbs>
-__global__ void __launch_bounds__(kSThreads) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(16) uint8_t raw[];
   SampleShared& sh = *reinterpret_cast<SampleShared*>(raw);
-  float* cache = reinterpret_cast<float*>(raw + (sizeof(SampleShared) + 15) / 16 * 16);
-  cluster_arrive();
+  uint4* cache = reinterpret_cast<uint4*>(raw + (sizeof(SampleShared) + 15) / 16 * 16);
   const int tid = threadIdx.x;
-  for (int i = tid; i < kTable; i += kSThreads)
-    sh.power[i] = make_float2(g_power.hi[i], g_power.lo[i]);
+  if (tid < 3) sh.pushed[tid] = 0u;
+  static_assert(kTable == kSThreads, "a power a thread");
+  const unsigned long long power = g_power.t[tid];
+  cluster_arrive();
   pdl_wait();
   pdl_trigger();
   const int ranks = (int)cluster_size(), rank = (int)cluster_rank();
   const int64_t r = blockIdx.x / ranks;
   const int warp = tid >> 5, lane = tid & 31;
-  RowSampler<T, kCached> s{sh,   cache, static_cast<const T*>(a.logits) + r * a.stride,
-                           a,    rank,  ranks,
-                           tid,  lane,  warp,
-                           (rank * kSWarps + warp) * a.run};
+  const T* row = static_cast<const T*>(a.logits) + r * a.stride;
+  RowSampler<T, kCached> s{sh,   cache, row,  a,    rank, ranks, tid, lane, warp,
+                           (int)(reinterpret_cast<uintptr_t>(row) % 16 / sizeof(T)),
+                           ((rank * kSWarps + warp) * 32 + lane) * a.groups};
+  // (looked at after the row is on its way)
   float t = a.temperature != nullptr ? a.temperature[r] : 1.0f;
   int k = a.top_k != nullptr ? a.top_k[r] : 0;
   const float top_p = a.top_p != nullptr ? a.top_p[r] : 1.0f;
   const float min_p = a.min_p != nullptr ? a.min_p[r] : 0.0f;
-  if (!(t > 0.0f)) {
-    t = 1.0f;
-    k = 1;
-  }
-  s.scale.top = s.fill();
-  if (!(s.scale.top > -INFINITY)) {
-    // nothing to draw from
+  s.scale.top = s.fill(power);
+  if (!(t > 0.0f)) k = 1;
+  t = fmaxf(t, 0x1p-116f);  // (ch stays finite)
+  float* p = a.p + r * a.vocab;
+  if (!(s.scale.top > -INFINITY) || k == 1) {
+    // nothing to draw from, or one token
+    const int best = s.scale.top > -INFINITY ? s.likeliest() : -1;
     if constexpr (kProbs) {
-      s.each([&](int v, float) {
-        if (v < a.vocab && v < s.begin + a.run) a.p[r * a.vocab + v] = 0.0f;
-      });
-    } else if (rank == 0 && tid == 0) {
-      a.token[r] = -1;
-    }
-    return;
-  }
-  if (k == 1) {
-    const int best = s.likeliest();
-    if constexpr (kProbs) {
-      s.each([&](int v, float) {
-        if (v < a.vocab && v < s.begin + a.run) a.p[r * a.vocab + v] = v == best ? 1.0f : 0.0f;
-      });
+      s.each_place([&](int v, float) { p[v] = v == best ? 1.0f : 0.0f; });
     } else if (rank == 0 && tid == 0) {
       a.token[r] = best;
     }
@@ -720,51 +1013,69 @@ __global__ void __launch_bounds__(kSThreads) sample_kernel(const SampleArgs a) {
   }
   s.scale.set(t);
   s.scale.power = sh.power;
-  s.least = 1ull;
-  if (min_p > 0.0f) s.least = max(1ull, (unsigned long long)ceil((double)fminf(min_p, 1.0f) * 0x1p42));
+  s.least = min_p > 0.0f ? max(1ull, (unsigned long long)ceilf(fminf(min_p, 1.0f) * 0x1p42f)) : 1ull;
   s.has_cut = false;
   const bool nucleus = top_p < 1.0f;
-  if (k > 1 || nucleus) {
-    bool fresh = false;
-    bool cut = k > 1 && s.search(false, (unsigned long long)k, nucleus || kProbs, &fresh);
-    if (cut) {
-      s.has_cut = true;
-      s.cut = sh.cut;
+  int last = kBins - 1;  // top-k's bin
+  if (k > 1 || nucleus) s.count_places();
+  if (k > 1) {
+    s.find(false, false, (unsigned long long)k, 0u, 0ull);
+    const int b = sh.bin;
+    const int n = b < 0 ? kList + 1 : (int)(sh.above_n + sh.bin_n);
+    if (n <= kList) {
+      // all of what top-k leaves can be listed
+      s.template list<false>([&](float l) { return (int)s.place(l) <= b; }, 2, n);
+      s.rank_list(n, false, (unsigned long long)k, 0u, 0ull);
+      if (nucleus) {
+        if (tid == 0)
+          sh.goal = max(1ull, (unsigned long long)ceil((double)fmaxf(top_p, 0.0f) *
+                                                       (double)sh.total));
+        __syncthreads();
+        s.rank_list(n, true, sh.goal, 0u, 0ull);
+      }
+      s.take_cut();
+      cluster_arrive();  // (the lists' parts have been read)
+      if constexpr (kProbs)
+        s.write(p, true);
+      else if (rank == 0)
+        s.draw_listed(n, a.u[r], a.token + r);
+      cluster_wait();
+      return;
     }
-    if (nucleus) {
-      unsigned long long total = sh.total;
-      if (!cut) {
-        if (!fresh) s.histogram([&](float l) { return s.first_bin(l); }, true);
-        fresh = true;
-        s.find(true, ~0ull, 0u, 0ull);  // (met by no bin: leaves the scan's sums)
-        total = 0;
-        for (int q = 0; q < kSWarps; ++q) total += sh.tmp_w[q];
-      }
-      const double goal = ceil((double)fmaxf(top_p, 0.0f) * (double)total);
-      __syncthreads();  // sh.total, sh.cut and the scan's sums have been read
-      if (s.search(true, max(1ull, (unsigned long long)goal), true, &fresh)) {
-        s.has_cut = true;
-        s.cut = sh.cut;
-      }
+    if (b >= 0) {
+      last = b;
+      s.cut_count(b, (unsigned long long)k);
+      s.take_cut();
     }
   }
+  if (nucleus) {
+    const unsigned long long mine = s.cut_nucleus(top_p, last, !kProbs);
+    if constexpr (kProbs) {
+      cluster_arrive();  // (the lists' parts have been read)
+      s.write(p, true);
+      cluster_wait();
+    } else {
+      s.draw(a.u[r], a.token + r, mine);
+    }
+    return;
+  }
+  if constexpr (!kProbs) {
+    s.draw(a.u[r], a.token + r, s.sum());
+  }
   if constexpr (kProbs)
-    s.write(a.p + r * a.vocab);
-  else
-    s.draw(a.u[r], a.token + r);
+    s.write(p, false);
 }
 
 template <typename T, bool kCached, bool kProbs>
 rq_status launch_row(const SampleArgs& a, int rows, int ranks, cudaStream_t st) {
-  const size_t smem = (sizeof(SampleShared) + 15) / 16 * 16 +
-                      (kCached ? (size_t)a.run * kSWarps * sizeof(float) : 0);
-  constexpr size_t kMost = (sizeof(SampleShared) + 15) / 16 * 16 + kCacheMax * sizeof(float);
-  static_assert(kMost <= 227 * 1024, "shared memory of a CTA");
+  constexpr size_t kShared = (sizeof(SampleShared) + 15) / 16 * 16;
+  static_assert(kShared + kCacheBytes <= 227 * 1024, "shared memory of a CTA");
+  const size_t smem = kShared + (kCached ? (size_t)a.pitch * kSThreads * 16 : 0);
   auto kernel = sample_kernel<T, kCached, kProbs>;
   static bool ready = false;
   if (!ready) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost) !=
-        cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kShared + kCacheBytes)) != cudaSuccess)
       return RQ_ERR_CUDA;
     ready = true;
   }
@@ -787,12 +1098,23 @@ rq_status launch_row(const SampleArgs& a, int rows, int ranks, cudaStream_t st) 
 
 template <typename T>
 rq_status launch_type(SampleArgs a, int rows, cudaStream_t st) {
-  a.vector = reinterpret_cast<uintptr_t>(a.logits) % (4 * sizeof(T)) == 0 && a.stride % 4 == 0;
-  int ranks = kMaxCluster;
-  while (ranks > 1 && a.vocab <= 4096 * (ranks / 2)) ranks /= 2;
-  const int per = (a.vocab + ranks * kSWarps - 1) / (ranks * kSWarps);
-  a.run = (per + 3) / 4 * 4;
-  const bool cached = a.run * kSWarps <= kCacheMax;
+  constexpr int kPer = 16 / (int)sizeof(T);
+  // groups of a row, whatever its skew
+  const int all = (a.vocab + 2 * (kPer - 1)) / kPer;
+  // As many CTAs as two to an SM, at most 64 logits a thread (as many as are
+  // marked), at least two groups: a larger cluster pays its barriers more
+  // often (256 rows of 50001 16-bit logits, nucleus: 66 us with clusters of 2,
+  // 84 with 4, 233 with 8; 64 rows of 131072: 100 with 8, 126 with 4).
+  const auto groups_of = [&](int n) { return (all + n * kSThreads - 1) / (n * kSThreads); };
+  int ranks = 1;
+  while (ranks < kMaxCluster &&
+         ((int64_t)rows * ranks < 2 * device_sm_count() || groups_of(ranks) * kPer > 64) &&
+         groups_of(ranks) > 2)
+    ranks *= 2;
+  a.groups = (all + ranks * kSThreads - 1) / (ranks * kSThreads);
+  a.pitch = a.groups | 1;
+  a.by = divisor((uint32_t)a.groups);
+  const bool cached = (size_t)a.pitch * kSThreads * 16 <= (size_t)kCacheBytes;
   if (a.p != nullptr)
     return cached ? launch_row<T, true, true>(a, rows, ranks, st)
                   : launch_row<T, false, true>(a, rows, ranks, st);

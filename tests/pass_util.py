@@ -149,11 +149,18 @@ def weights(logits, t):
     return np.floor(np.exp(far) * UNIT).astype(np.int64)
 
 
-def staying(logits, t=1.0, k=0, p=1.0, m=0.0, slack=0):
-    """(weights by index with zeros for what goes, tokens within `slack` units
-    of a nucleus' or of min-p's border, which may fall to either side)."""
+def slack_of(w):
+    """How far sums of the device's weights may be from the definition's: each
+    is within 2^-32 of its value and one unit."""
+    return int(w.sum()) / 2.0 ** 32 + len(w) + 1
+
+
+def staying(logits, t=1.0, k=0, p=1.0, m=0.0):
+    """(weights by index with zeros for what goes, tokens so near to a nucleus'
+    or to min-p's border that they may fall to either side)."""
     if not t > 0:
         t, k = 1.0, 1
+    t = max(t, 2.0 ** -116)
     w = weights(logits, t)
     if w is None:
         return None, None
@@ -161,9 +168,10 @@ def staying(logits, t=1.0, k=0, p=1.0, m=0.0, slack=0):
     order = np.lexsort((np.arange(len(l)), -l))
     s = w[order]
     near = np.zeros(len(l), dtype=bool)
+    slack = slack_of(w)
     if m > 0:
         least = math.ceil(min(np.float64(np.float32(m)), 1.0) * UNIT)
-        near |= np.abs(s - least) <= 2 * (least != UNIT)
+        near |= (np.abs(s - least) <= least / 2.0 ** 32 + 2) & (least != UNIT)
         s = np.where(s >= least, s, 0)
     if k > 0:
         s = np.where(np.cumsum(s > 0) <= k, s, 0)

@@ -36,16 +36,15 @@ def run(rq, logits, u=None, t=None, k=None, p=None, m=None, dtype=None):
 
 def check(rq, logits, u, t=None, k=None, p=None, m=None):
     """Compares both entry points with the definition.  The device's weights are
-    within 2 units of the definition's, so running sums are within 2 a token:
-    what stands closer than that to a border may fall to either side, and a
+    within 2^-32 of their value and a unit of the definition's: what stands
+    closer than their sum's error to a border may fall to either side, and a
     random number's point may meet either neighbour there."""
     rows, vocab = logits.shape
     tokens, probs = run(rq, logits, u, t, k, p, m)
     host = logits.float().cpu().numpy()
-    slack = 2 * vocab + 4
     for r in range(rows):
         w, near = ref.staying(host[r], 1.0 if t is None else t[r], 0 if k is None else k[r],
-                              1.0 if p is None else p[r], 0.0 if m is None else m[r], slack)
+                              1.0 if p is None else p[r], 0.0 if m is None else m[r])
         if w is None:
             assert tokens[r] == -1 and not probs[r].any()
             continue
@@ -53,9 +52,12 @@ def check(rq, logits, u, t=None, k=None, p=None, m=None):
         assert np.array_equal(got[~near] > 0, w[~near] > 0) or \
             (w[(got > 0) != (w > 0)] <= 2).all()
         if not near.any():
-            total = float(w.sum())
-            # a weight of 2 units' error, and three roundings of f32
-            tol = (2.0 + slack * (w / total)) / total + 4 * ref.U * (w / total)
+            total, slack = float(w.sum()), ref.slack_of(w)
+            # the weight's own error and the total's; the power of two is
+            # within 2^-22 (ex2.approx), and the correction of its argument,
+            # the total's inverse and the two products round four times more:
+            # 2^-22 + 4 2^-24 = 8 u
+            tol = (w / 2.0 ** 32 + 2.0 + slack * (w / total)) / total + 8 * ref.U * (w / total)
             assert (np.abs(got - w / total) <= tol).all()
             want, point, run_ = ref.drawn(w, u[r])
             if tokens[r] != want:

@@ -12,6 +12,7 @@ Function names are those of the C ABI (``rq_absmax``, ``rq_quant_e4m3``,
 """
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "librq.so")
@@ -477,54 +478,71 @@ def rq_verify_tree(token, parent, p, u, accepted, next, path, batch, drafts, voc
 # The steps of a pass between the linears.  Their tensors lie on the current
 # device; their addresses (ints) are vouched for by the caller.
 
-_current_device = None      # index of torch's current device
+class _Types:
+    """torch's dtypes and current device, looked up at the first call."""
 
-
-def _here(t, where):
-    """Address of a tensor on the current device (None stays None)."""
-    global _current_device
-    if t is None or isinstance(t, int):
-        return t
-    if not t.is_cuda:
-        raise RqError(2, where + " is not on the GPU")
-    if _current_device is None:
+    def __getattr__(self, name):
         import torch
-        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-    if t.get_device() != _current_device():
-        raise RqError(2, where + " is on another device than the current one")
+        self.i32, self.i64, self.f32 = torch.int32, torch.int64, torch.float32
+        self.codes = (torch.float8_e4m3fn, torch.uint8)
+        self.bits = (torch.int32, torch.uint32)
+        # (the bare function takes 0.1 us, torch.cuda.current_device 1)
+        bare = getattr(torch._C, "_cuda_getDevice", None)
+        self.device = bare if bare is not None and torch.cuda.is_available() else (
+            torch.cuda.current_device if torch.cuda.is_available() else lambda: 0)
+        return self.__dict__[name]
+
+
+_types = _Types()
+
+
+def _on_device(t, dev, where, name):
+    """Address of a tensor on device `dev`."""
+    at = t.get_device()
+    if at < 0:
+        raise RqError(2, "%s: %s is not on the GPU" % (where, name))
+    if at != dev:
+        raise RqError(2, "%s: %s is on another device than the current one" % (where, name))
     return t.data_ptr()
 
 
-def _array(t, kind, where, count=None):
-    """Address of a dense tensor of dtype `kind`, of `count` entries at least."""
-    if t is None or isinstance(t, int):
+def _array(t, kind, dev, where, name, count=0):
+    """Address of a dense tensor of dtype `kind` (or one of several), of
+    `count` entries at least, on device `dev`; None and addresses as they are."""
+    try:
+        if t.dtype is kind and t.get_device() == dev and t.is_contiguous() and t.numel() >= count:
+            return t.data_ptr()
+    except AttributeError:
         return t
-    if t.dtype not in _kinds[kind]:
-        raise RqError(3, "%s is not %s" % (where, kind))
-    if not t.is_contiguous() or count is not None and t.numel() < count:
-        raise RqError(2, where + " is not dense, or too short")
-    return _here(t, where)
+    if t.dtype is not kind and not (isinstance(kind, tuple) and t.dtype in kind):
+        raise RqError(3, "%s: %s is not %s" % (where, name, kind))
+    if not t.is_contiguous() or t.numel() < count:
+        raise RqError(2, "%s: %s is not dense, or too short" % (where, name))
+    return _on_device(t, dev, where, name)
 
 
-def _matrix(t, rows, cols, where, stride=None, dense=False):
+def _matrix(t, rows, cols, dev, where, name, stride=None, dense=False):
     """Address of `rows` rows of `cols` elements, and the elements between
     them: any tensor whose last axis is `cols` dense elements and whose other
     axes count rows at one distance."""
-    if t is None or isinstance(t, int):
+    try:
+        n = t.numel()
+    except AttributeError:
         return t, cols if stride is None else stride
-    if t.numel() < rows * cols or t.numel() % cols or t.shape[-1] != cols:
-        raise RqError(2, where + " does not hold the rows")
-    at = _here(t, where)
+    if n < rows * cols or n % cols or t.dim() < 1 or t.size(-1) != cols:
+        raise RqError(2, "%s: %s does not hold the rows" % (where, name))
+    at = _on_device(t, dev, where, name)
     if t.is_contiguous():
         return at, cols
     if dense:
-        raise RqError(2, where + " is not dense")
+        raise RqError(2, "%s: %s is not dense" % (where, name))
     return at, _view_stride(t, 1, cols, where)
 
 
-class _EpilogueStruct(ctypes.Structure):
-    _fields_ = [("bias", _vp), ("act", _i32), ("mul", _vp), ("residual", _vp),
-                ("mul_stride", _i64), ("residual_stride", _i64)]
+# What a call describes by a struct of the C ABI goes as its bytes, made anew
+# (a ctypes structure takes three times as long).
+_EPILOGUE = struct.Struct("@PiPPqq")
+_SAMPLING = struct.Struct("@PPPP")
 
 
 class _NormStruct(ctypes.Structure):
@@ -532,38 +550,32 @@ class _NormStruct(ctypes.Structure):
                 ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
 
 
-class _SamplingStruct(ctypes.Structure):
-    _fields_ = [("temperature", _vp), ("top_k", _vp), ("top_p", _vp), ("min_p", _vp)]
-
-
-def _epilogue(where, M, N, y, act, bias, mul, residual, dtype):
-    """(epilogue struct, dtype, y's address and stride)."""
+def _epilogue(where, dev, M, N, y, act, bias, mul, residual, dtype):
+    """(epilogue, dtype, y's address and stride)."""
     if isinstance(act, str):
         if act not in ACTIVATIONS:
             raise RqError(3, "%s: no activation %r" % (where, act))
         act = ACTIVATIONS[act]
     dtype = _dtype(dtype, where, y, mul, residual)
-    yp, ys = _matrix(y, M, N, where + ": y")
-    mp, ms = _matrix(mul, M, N, where + ": mul")
-    rp, rs = _matrix(residual, M, N, where + ": residual")
-    bp = _array(bias, "float32", where + ": bias", N)
-    return _EpilogueStruct(bp, act, mp, rp, ms, rs), dtype, yp, ys
-
-
-_E4M3 = "float8_e4m3fn|uint8"
+    yp, ys = _matrix(y, M, N, dev, where, "y")
+    mp, ms = (0, 0) if mul is None else _matrix(mul, M, N, dev, where, "mul")
+    rp, rs = (0, 0) if residual is None else _matrix(residual, M, N, dev, where, "residual")
+    bp = 0 if bias is None else _array(bias, _types.f32, dev, where, "bias", N)
+    return _EPILOGUE.pack(bp, act, mp, rp, ms, rs), dtype, yp, ys
 
 
 def rq_fp8_gemm_epilogue(x_fp8, x_dequant, w_fp8, w_dequant, y, M, N, K, act="none", bias=None,
                          mul=None, residual=None, dtype=None, stream=None):
     """y = residual + mul * act(x . w^T + bias) of E4M3 operands; y, mul and
     residual are [M, N] of one type (rows may be apart), bias f32 [N]."""
-    e, dtype, yp, ys = _epilogue("rq_fp8_gemm_epilogue", M, N, y, act, bias, mul, residual, dtype)
+    where, dev = "rq_fp8_gemm_epilogue", _types.device()
+    e, dtype, yp, ys = _epilogue(where, dev, M, N, y, act, bias, mul, residual, dtype)
     _check(_lib.rq_fp8_gemm_epilogue(
-        _array(x_fp8, _E4M3, "rq_fp8_gemm_epilogue: x_fp8", (M + 15) // 16 * 16 * K),
-        _array(x_dequant, "float32", "rq_fp8_gemm_epilogue: x_dequant", 1),
-        _array(w_fp8, _E4M3, "rq_fp8_gemm_epilogue: w_fp8", N * K),
-        _array(w_dequant, "float32", "rq_fp8_gemm_epilogue: w_dequant", 1), ctypes.byref(e), dtype,
-        yp, ys, M, N, K, _stream(stream)), "rq_fp8_gemm_epilogue")
+        _array(x_fp8, _types.codes, dev, where, "x_fp8", (M + 15) // 16 * 16 * K),
+        _array(x_dequant, _types.f32, dev, where, "x_dequant", 1),
+        _array(w_fp8, _types.codes, dev, where, "w_fp8", N * K),
+        _array(w_dequant, _types.f32, dev, where, "w_dequant", 1), e, dtype, yp, ys, M, N, K,
+        _stream(stream)), where)
 
 
 class NormParams:
@@ -572,7 +584,8 @@ class NormParams:
 
     def __init__(self, width, post=True, pre=True, post_weight=None, pre_weight=None, eps=1e-6,
                  scale=1.0):
-        at = [_array(t, "float32", "NormParams: weight", width)
+        dev = _types.device()
+        at = [_array(t, _types.f32, dev, "NormParams", "a weight", width)
               for t in (post_weight, pre_weight)]
         self.tensors = (post_weight, pre_weight)
         self.width = width
@@ -587,21 +600,24 @@ def rq_residual_norm(params, y, h, h_out, x_out, tokens, gate=None, absmax_bits=
     """h_out = h + scale * (gate * post(y)), x_out = pre(h_out).  y None: no
     block before; gate: [width], or [tokens, width] like y; either output may
     be None."""
-    n, where = params.width, "rq_residual_norm"
-    dtype = _dtype(dtype, where, y, gate, x_out) if dtype is not None or y is not None or \
-        x_out is not None else _dtype(None, where, h)
-    h_dtype = _dtype(h_dtype, where, h, h_out)
-    yp, ys = _matrix(y, tokens, n, where + ": y")
-    hp, hs = _matrix(h, tokens, n, where + ": h")
+    n, where, dev = params.width, "rq_residual_norm", _types.device()
+    if dtype is None:
+        dtype = _dtype(None, where, y, gate, x_out) if y is not None or x_out is not None else \
+            _dtype(None, where, h)
+    yp, ys = _matrix(y, tokens, n, dev, where, "y")
+    hp, hs = _matrix(h, tokens, n, dev, where, "h")
     gp, gs = None, 0
     if gate is not None:
-        per_token = isinstance(gate, int) or gate.dim() > 1
-        gp, gs = _matrix(gate, tokens if per_token else 1, n, where + ": gate")
-        gs = gs if per_token else 0
-    _check(_lib.rq_residual_norm(params.address, dtype, yp, ys, gp, gs, h_dtype, hp, hs,
-                                 _matrix(h_out, tokens, n, where + ": h_out", dense=True)[0],
-                                 _matrix(x_out, tokens, n, where + ": x_out", dense=True)[0],
-                                 _array(absmax_bits, "int32|uint32", where + ": absmax_bits", 1),
+        if isinstance(gate, int) or gate.dim() > 1:
+            gp, gs = _matrix(gate, tokens, n, dev, where, "gate")
+        else:
+            gp = _matrix(gate, 1, n, dev, where, "gate")[0]
+    _check(_lib.rq_residual_norm(params.address, dtype, yp, ys, gp, gs,
+                                 _dtype(h_dtype, where, h, h_out), hp, hs,
+                                 _matrix(h_out, tokens, n, dev, where, "h_out", None, True)[0],
+                                 _matrix(x_out, tokens, n, dev, where, "x_out", None, True)[0],
+                                 None if absmax_bits is None else
+                                 _array(absmax_bits, _types.bits, dev, where, "absmax_bits", 1),
                                  tokens, _stream(stream)), where)
 
 
@@ -611,52 +627,55 @@ def rq_batch_plan(length, page_table, free_pages, free_count, free_left, slot, p
     """Slots, positions and new page-table entries of a pass's new tokens:
     `count` of each sequence in batch * new_tokens rows, or with new_tokens 0
     one behind another in as many rows as `slot` has."""
-    where = "rq_batch_plan"
-    if len(page_table.shape) != 2 or page_table.shape[0] != length.numel():
+    where, dev, i32 = "rq_batch_plan", _types.device(), _types.i32
+    batch, rows = length.numel(), slot.numel()
+    if page_table.dim() != 2 or page_table.size(0) != batch:
         raise RqError(2, where + ": page_table is [batch, max_pages]")
-    batch, max_pages = page_table.shape
-    rows = slot.numel()
     _check(_lib.rq_batch_plan(
-        _array(length, "int32", where + ": length"),
-        _array(count, "int32", where + ": count", batch), batch, new_tokens, page_size,
-        _array(page_table, "int32", where + ": page_table"), max_pages,
-        _array(free_pages, "int32", where + ": free_pages"), free_pages.numel(),
-        _array(free_count, "int32", where + ": free_count", 1),
-        _array(free_left, "int32", where + ": free_left", 1),
-        _array(slot, "int64", where + ": slot"),
-        _array(position, "int32", where + ": position", rows),
-        _array(sequence, "int32", where + ": sequence", rows), rows,
-        _array(row_start, "int32", where + ": row_start", batch + 1),
-        _array(next_length, "int32", where + ": next_length", batch), _stream(stream)), where)
+        _array(length, i32, dev, where, "length"),
+        _array(count, i32, dev, where, "count", batch), batch, new_tokens, page_size,
+        _array(page_table, i32, dev, where, "page_table"), page_table.size(1),
+        _array(free_pages, i32, dev, where, "free_pages"), free_pages.numel(),
+        _array(free_count, i32, dev, where, "free_count", 1),
+        _array(free_left, i32, dev, where, "free_left", 1),
+        _array(slot, _types.i64, dev, where, "slot"),
+        _array(position, i32, dev, where, "position", rows),
+        _array(sequence, i32, dev, where, "sequence", rows), rows,
+        _array(row_start, i32, dev, where, "row_start", batch + 1),
+        _array(next_length, i32, dev, where, "next_length", batch), _stream(stream)), where)
 
 
-def _sampling(where, rows, temperature, top_k, top_p, min_p):
-    return _SamplingStruct(_array(temperature, "float32", where + ": temperature", rows),
-                           _array(top_k, "int32", where + ": top_k", rows),
-                           _array(top_p, "float32", where + ": top_p", rows),
-                           _array(min_p, "float32", where + ": min_p", rows))
+def _sampling(where, dev, rows, temperature, top_k, top_p, min_p):
+    f32 = _types.f32
+    return _SAMPLING.pack(
+        0 if temperature is None else _array(temperature, f32, dev, where, "temperature", rows),
+        0 if top_k is None else _array(top_k, _types.i32, dev, where, "top_k", rows),
+        0 if top_p is None else _array(top_p, f32, dev, where, "top_p", rows),
+        0 if min_p is None else _array(min_p, f32, dev, where, "min_p", rows))
 
 
 def rq_sample(logits, u, token, rows, vocab, temperature=None, top_k=None, top_p=None, min_p=None,
               dtype=None, stride=None, stream=None):
     """A token per row of logits, drawn with u from what the filters leave; the
     filters are tensors [rows] or None."""
-    f = _sampling("rq_sample", rows, temperature, top_k, top_p, min_p)
-    at, step = _matrix(logits, rows, vocab, "rq_sample: logits", stride)
-    _check(_lib.rq_sample(ctypes.byref(f), _dtype(dtype, "rq_sample", logits), at, step,
-                          _array(u, "float32", "rq_sample: u", rows),
-                          _array(token, "int32", "rq_sample: token", rows), rows, vocab,
-                          _stream(stream)), "rq_sample")
+    where, dev = "rq_sample", _types.device()
+    f = _sampling(where, dev, rows, temperature, top_k, top_p, min_p)
+    at, step = _matrix(logits, rows, vocab, dev, where, "logits", stride)
+    _check(_lib.rq_sample(f, _dtype(dtype, where, logits), at, step,
+                          _array(u, _types.f32, dev, where, "u", rows),
+                          _array(token, _types.i32, dev, where, "token", rows), rows, vocab,
+                          _stream(stream)), where)
 
 
 def rq_token_probs(logits, p, rows, vocab, temperature=None, top_k=None, top_p=None, min_p=None,
                    dtype=None, stride=None, stream=None):
     """The probabilities p (f32 [rows, vocab]) of what the filters leave."""
-    f = _sampling("rq_token_probs", rows, temperature, top_k, top_p, min_p)
-    at, step = _matrix(logits, rows, vocab, "rq_token_probs: logits", stride)
-    _check(_lib.rq_token_probs(ctypes.byref(f), _dtype(dtype, "rq_token_probs", logits), at, step,
-                               _array(p, "float32", "rq_token_probs: p", rows * vocab), rows,
-                               vocab, _stream(stream)), "rq_token_probs")
+    where, dev = "rq_token_probs", _types.device()
+    f = _sampling(where, dev, rows, temperature, top_k, top_p, min_p)
+    at, step = _matrix(logits, rows, vocab, dev, where, "logits", stride)
+    _check(_lib.rq_token_probs(f, _dtype(dtype, where, logits), at, step,
+                               _array(p, _types.f32, dev, where, "p", rows * vocab), rows, vocab,
+                               _stream(stream)), where)
 
 
 class Context:
@@ -735,15 +754,17 @@ class Context:
                            residual=None, dtype=None, stream=None):
         """The FP8 route of rq_linear with the epilogue of
         rq_fp8_gemm_epilogue, at every M."""
-        where = "rq_linear_epilogue"
-        e, dtype, yp, ys = _epilogue(where, M, N, y, act, bias, mul, residual, dtype)
-        if not isinstance(w, int) and (not w.is_contiguous() or w.numel() * w.element_size() <
-                                       N * (K // 256) * (144 if qtype == RQ_Q4K else 210)):
-            raise RqError(2, where + ": w is not dense, or too short")
-        _check(_lib.rq_linear_epilogue(self._h, qtype, _here(w, where + ": w"),
-                                       _array(x, "float32", where + ": x", M * K),
-                                       ctypes.byref(e), dtype, yp, ys, M, N, K,
-                                       _stream(stream)), where)
+        where, dev = "rq_linear_epilogue", _types.device()
+        e, dtype, yp, ys = _epilogue(where, dev, M, N, y, act, bias, mul, residual, dtype)
+        wp = w
+        if not isinstance(w, int):
+            if not w.is_contiguous() or w.numel() * w.element_size() < \
+                    N * (K // 256) * (144 if qtype == RQ_Q4K else 210):
+                raise RqError(2, where + ": w is not dense, or too short")
+            wp = _on_device(w, dev, where, "w")
+        _check(_lib.rq_linear_epilogue(self._h, qtype, wp,
+                                       _array(x, _types.f32, dev, where, "x", M * K), e, dtype, yp,
+                                       ys, M, N, K, _stream(stream)), where)
 
     def rq_cache_attention(self, cache, q, out, page_table, length, batch, new_tokens, q_heads,
                            scale, tree=None, max_pages=None, dtype=None, q_stride=None,

@@ -21,7 +21,7 @@ def rq():
 def epilogue(rq, **over):
     f = dict(bias=A, act=1, mul=A, residual=A, mul_stride=64, residual_stride=64)
     f.update(over)
-    return ctypes.byref(rq._EpilogueStruct(**f))
+    return rq._EPILOGUE.pack(*f.values())
 
 
 def norm(rq, **over):
@@ -33,7 +33,7 @@ def norm(rq, **over):
 def filters(rq, **over):
     f = dict(temperature=A, top_k=A, top_p=A, min_p=A)
     f.update(over)
-    return ctypes.byref(rq._SamplingStruct(**f))
+    return rq._SAMPLING.pack(*f.values())
 
 
 @pytest.mark.parametrize("over,status", [
@@ -195,11 +195,11 @@ def test_rows_and_their_distance(rq):
     t = torch.zeros(6, 96)
 
     def at(x, rows, cols, **more):
-        saved, rq._here = rq._here, lambda t, where: t.data_ptr()
+        saved, rq._on_device = rq._on_device, lambda t, dev, where, name: t.data_ptr()
         try:
-            return rq._matrix(x, rows, cols, where, **more)
+            return rq._matrix(x, rows, cols, 0, where, "t", **more)
         finally:
-            rq._here = saved
+            rq._on_device = saved
 
     assert at(t, 6, 96) == (t.data_ptr(), 96)
     assert at(t[:, 32:], 6, 64) == (t.data_ptr() + 128, 96)

@@ -5,19 +5,26 @@ A decoder of seeded Q4_K / Q6_K weights: its linears are rq_linear and
 rq_linear_group, its attention runs over a paged 8-bit cache, and its tokens
 are drafted from the text so far and verified by the decoder:
 
+  cache slots, positions and pages of the new tokens
+          rq_batch_plan
+  residual sums and norms between the blocks
+          rq_residual_norm
   q/k/v   rq_linear_group     (one launch for the three)
   norm of q and k per head, rotation, quantized write of k and v
           rq_qkv_to_cache     (one pass)
   attention of the last token and its drafts, causal or a tree
           Context.rq_cache_attention
   o, gate/up, down, vocabulary
-          rq_linear, rq_linear_group
+          rq_linear, rq_linear_group; the gate product of a long prompt
+          rq_linear_epilogue
+  temperature, top-k, top-p and min-p
+          rq_token_probs
   which drafts stay, and the next token
           rq_verify_chain or rq_verify_tree
   accepted tokens of a tree to the places that follow the text
           rq_kv_read, rq_kv_write
 
-    python examples/speculative_decode.py [--drafts none|chain|tree] [--tokens N]
+    python examples/speculative_decode.py [--drafts none|chain|tree] [--tokens N] [--top-p P]
 """
 import argparse
 import os
@@ -43,10 +50,6 @@ def _normal(seed, *shape):
     return torch.from_numpy(synthetic.normal_f32(seed, n)[:n].reshape(shape).copy()).cuda()
 
 
-def _rms(x):
-    return x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6)
-
-
 class Decoder:
     """One sequence through a decoder of `layers` layers and a paged cache."""
 
@@ -65,10 +68,16 @@ class Decoder:
             -torch.arange(0, d, 2).double() / d)
         cos, sin = angle.cos().float().cuda(), angle.sin().float().cuda()
         self.layers = []
-        # pages in an order of their own: a page is found by the table only
+        # unused pages in an order of their own: a page is found by the table only
         pages = (max_tokens + page_size - 1) // page_size
-        self.table = torch.from_numpy(
+        self.free = torch.from_numpy(
             np.argsort(synthetic.u64(synthetic.substream(seed, 2), pages)).astype(np.int32)).cuda()
+        self.left = torch.empty(1, dtype=torch.int32, device="cuda")
+        self.table = torch.zeros(1, pages, dtype=torch.int32, device="cuda")
+        self.slot = None
+        # a norm after each block and before the next, without weights of their own
+        self.first_norm = rq.NormParams(hidden, post=False)
+        self.norms = rq.NormParams(hidden)
         for i in range(layers):
             s = [synthetic.substream(seed, 100 * (i + 1) + j) for j in range(9)]
             self.layers.append(dict(
@@ -84,22 +93,23 @@ class Decoder:
                 cache=rq.KVCache(pages, page_size, kv_heads, d, format)))
         self.page_size = page_size
 
-    def slots(self, places):
-        """Cache slots of places in the text (int64 tensor on the device)."""
-        page = self.table[places // self.page_size].long()
-        return page * self.page_size + places % self.page_size
-
     def forward(self, tokens, length, depth=None, tree=None):
         """Logits [n, vocab] after each of n new tokens that follow `length`
         cached ones; depth: their places in the text beyond length, and tree
         the new tokens that each sees (None: one after another)."""
         n = len(tokens)
         assert length + n <= self.max_tokens
-        place = length + torch.arange(n, device="cuda")
-        slot = self.slots(place)
-        position = (place if depth is None else
-                    length + torch.tensor(depth, device="cuda")).int()
         lengths = torch.tensor([length], dtype=torch.int32, device="cuda")
+        # the first pages of the stack's end hold the text; those that drafts
+        # took which were not kept are taken again
+        held = -(-length // self.page_size)
+        count = torch.tensor([len(self.free) - held], dtype=torch.int32, device="cuda")
+        slot = self.slot = torch.empty(n, dtype=torch.int64, device="cuda")
+        position = torch.empty(n, dtype=torch.int32, device="cuda")
+        rq.rq_batch_plan(lengths, self.table, self.free, count, self.left, slot, position,
+                         self.page_size, new_tokens=n)
+        if depth is not None:
+            position = (length + torch.tensor(depth, device="cuda")).int()
         words = None
         if tree is not None:
             words = torch.tensor([tree], dtype=torch.int64, device="cuda")
@@ -108,28 +118,39 @@ class Decoder:
             return torch.empty(n, cols, device="cuda")
 
         x = self.embedding[torch.tensor(tokens, device="cuda")]
+        normed = f32(self.hidden)
+        rq.rq_residual_norm(self.first_norm, None, x, None, normed, n)
         for layer in self.layers:
             qkv = [f32(rows) for rows in layer["rows"]]
-            self.ctx.rq_linear_group(layer["types"], layer["qkv"], _rms(x), qkv, layer["rows"], n,
+            self.ctx.rq_act_cache_invalidate()      # normed is written in place
+            self.ctx.rq_linear_group(layer["types"], layer["qkv"], normed, qkv, layer["rows"], n,
                                      self.hidden)
             q, k, v = (t.view(n, -1, self.head_dim) for t in qkv)
             rq.rq_qkv_to_cache(layer["params"], q, k, v, position, q, layer["cache"], slot, n)
             out = torch.empty_like(q)
-            self.ctx.rq_cache_attention(layer["cache"], q, out, self.table[None], lengths, 1, n,
+            self.ctx.rq_cache_attention(layer["cache"], q, out, self.table, lengths, 1, n,
                                         self.heads, self.head_dim ** -0.5, tree=words)
             y = f32(self.hidden)
             self.ctx.rq_linear(Q4K, layer["o"], out, y, n, self.hidden,
                                self.heads * self.head_dim)
-            x = x + _rms(y)
+            rq.rq_residual_norm(self.norms, y, x, x, normed, n)
+            self.ctx.rq_act_cache_invalidate()
             gate, up = f32(self.intermediate), f32(self.intermediate)
-            self.ctx.rq_linear_group([Q4K, Q4K], layer["up"], _rms(x), [gate, up],
-                                     [self.intermediate] * 2, n, self.hidden)
-            y = f32(self.hidden)
-            self.ctx.rq_linear(Q4K, layer["down"], torch.nn.functional.silu(gate) * up, y, n,
-                               self.hidden, self.intermediate)
-            x = x + _rms(y)
+            if n < self.ctx.gemm_threshold:
+                self.ctx.rq_linear_group([Q4K, Q4K], layer["up"], normed, [gate, up],
+                                         [self.intermediate] * 2, n, self.hidden)
+                gated = torch.nn.functional.silu(gate) * up
+            else:
+                self.ctx.rq_linear(Q4K, layer["up"][1], normed, up, n, self.intermediate,
+                                   self.hidden)
+                self.ctx.rq_linear_epilogue(Q4K, layer["up"][0], normed, gate, n,
+                                            self.intermediate, self.hidden, act="silu", mul=up)
+                gated = gate
+            self.ctx.rq_linear(Q4K, layer["down"], gated, y, n, self.hidden, self.intermediate)
+            rq.rq_residual_norm(self.norms, y, x, x, normed, n)
+        self.ctx.rq_act_cache_invalidate()
         logits = f32(self.vocab)
-        self.ctx.rq_linear(Q6K, self.head, _rms(x), logits, n, self.vocab, self.hidden)
+        self.ctx.rq_linear(Q6K, self.head, normed, logits, n, self.vocab, self.hidden)
         return logits
 
     def keep(self, length, path):
@@ -138,8 +159,8 @@ class Decoder:
         if list(path) == list(range(len(path))):
             return
         n = len(path)
-        old = self.slots(length + torch.tensor(path, device="cuda"))
-        new = self.slots(length + torch.arange(n, device="cuda"))
+        old = self.slot[torch.tensor(path, device="cuda")]
+        new = self.slot[:n].contiguous()
         for layer in self.layers:
             k = torch.empty(n, self.kv_heads, self.head_dim, device="cuda")
             v = torch.empty_like(k)
@@ -178,7 +199,8 @@ def as_tree(runs):
     return tokens, parents
 
 
-def generate(decoder, prompt, count, drafts="tree", width=3, depth=4, temperature=1.0, seed=7):
+def generate(decoder, prompt, count, drafts="tree", width=3, depth=4, temperature=1.0, top_k=0,
+             top_p=1.0, min_p=0.0, seed=7):
     """(`count` tokens after the prompt, passes that took): with a tree or
     without drafts the draw at each place uses that place's random number, so
     both write the same text."""
@@ -199,7 +221,13 @@ def generate(decoder, prompt, count, drafts="tree", width=3, depth=4, temperatur
             sees.append(sees[p + 1] | 1 << (i + 1))
         logits = decoder.forward(new, length, levels, sees if drafts == "tree" else None)
         passes += 1
-        p = torch.softmax(logits / temperature, -1)[None]
+        rows = len(new)
+        p = torch.empty(1, rows, decoder.vocab, device="cuda")
+        rq.rq_token_probs(logits, p, rows, decoder.vocab,
+                          temperature=torch.full((rows,), temperature, device="cuda"),
+                          top_k=torch.full((rows,), top_k, dtype=torch.int32, device="cuda"),
+                          top_p=torch.full((rows,), top_p, device="cuda"),
+                          min_p=torch.full((rows,), min_p, device="cuda"))
         token = torch.tensor([tokens], dtype=torch.int32, device="cuda")
         accepted = torch.empty(1, dtype=torch.int32, device="cuda")
         following = torch.empty_like(accepted)
@@ -228,9 +256,13 @@ def main():
     ap.add_argument("--drafts", choices=("none", "chain", "tree"), default="tree")
     ap.add_argument("--tokens", type=int, default=96)
     ap.add_argument("--temperature", type=float, default=0.5)
+    ap.add_argument("--top-k", type=int, default=0)
+    ap.add_argument("--top-p", type=float, default=1.0)
+    ap.add_argument("--min-p", type=float, default=0.0)
     args = ap.parse_args()
     text, passes = generate(Decoder(), [3, 141, 59, 26, 53], args.tokens, args.drafts,
-                            temperature=args.temperature)
+                            temperature=args.temperature, top_k=args.top_k, top_p=args.top_p,
+                            min_p=args.min_p)
     print(" ".join(map(str, text)))
     print("%d tokens in %d passes" % (len(text), passes))
 

@@ -35,12 +35,14 @@
 // lanes' sums is a scan by index.
 //
 // Bound by instruction issue: 64 rows of 131072 f32 logits without filters take
-// 35 us, of which reading them is 5 and loading, the maximum and the barriers
+// 35 us, of which reading them is 5, and reading, the maximum and the barriers
 // are 20 (the likeliest token alone); the exact pass issues 45 instructions a
-// token.  With top-k 50 35 us, with a nucleus of 0.9 64 us (196 with a
+// token.  With top-k 50 34 us, with a nucleus of 0.9 63 us (196 with a
 // histogram of exact weights over the whole row).  One row: 13, 15 and 24 us,
 // about 8 us of which are 5 to 7 barriers and what follows them (with cold
-// inputs, launch and events included).
+// inputs, launch and events included).  What top-k leaves is marked in a word of
+// bits a thread, and later passes look at marked tokens only: top-k 300,
+// nucleus and min-p on one row 24 -> 16 us.
 #include <type_traits>
 
 #include "rq_device.cuh"
@@ -297,7 +299,8 @@ struct RowSampler {
   int first;               // this thread's first place, in groups
   Scale scale;
   unsigned long long least;  // weights below it are left out (min-p)
-  unsigned long long marks;  // this thread's tokens that a nucleus may end at
+  bool marked;               // `marks` are this thread's tokens that may stay
+  unsigned long long marks;
   bool has_cut;
   float cut_l;             // tokens of a larger logit stay, and of this one
   int cut_v;               // those up to this index
@@ -332,11 +335,11 @@ struct RowSampler {
     }
   }
 
-  // f over the tokens that are marked, which are few; over all of a thread
-  // that has more tokens than marks.
-  template <bool kMarked, typename F>
+  // f over the tokens that are marked, which are few; over all of them where
+  // none are marked yet or a thread has more than there are marks.
+  template <typename F>
   __device__ __forceinline__ void some(F f) const {
-    if (!kMarked || a.groups * kPer > 64) {
+    if (!marked) {
       each(f);
     } else {
       for (unsigned long long m = marks; m != 0ull; m &= m - 1ull) {
@@ -344,6 +347,11 @@ struct RowSampler {
         f(first * kPer - skew + i, one(lane, i));
       }
     }
+  }
+  __device__ __forceinline__ bool can_mark() const { return a.groups * kPer <= 64; }
+  // A token's mark.
+  __device__ __forceinline__ unsigned long long mark_of(int v) const {
+    return 1ull << ((v + skew - first * kPer) & 63);
   }
 
   // One logit of this warp's thread q.
@@ -561,11 +569,11 @@ struct RowSampler {
   }
 
   // Lists in every CTA the n tokens for which in_list(l) holds, and their
-  // weights.  kMarked: only marked tokens are asked.  (A CTA's own part is read by the
-  // others until their next cluster barrier.)
-  template <bool kMarked, typename F>
+  // weights.  (A CTA's own part is read by the others until their next cluster
+  // barrier.)
+  template <typename F>
   __device__ __forceinline__ void list(F in_list, int which, int n) {
-    some<kMarked>([&](int v, float l) {
+    some([&](int v, float l) {
       if (in_list(l)) sh.found[which][atomicAdd(&sh.pushed[which], 1u)] = order_of(v, l);
     });
     cluster_sync();
@@ -681,18 +689,18 @@ struct RowSampler {
   // sh.above_n of weight sh.above_w: sh.cut, and sh.total, the weight up to it.
   // (Divided further in the same buffer: the exchange of the range stands
   // between the last look at it and the next use.)
-  template <bool kMarked, typename F>
+  template <typename F>
   __device__ __forceinline__ void resolve(F bin_of, bool by_weight, unsigned long long goal) {
     const int which = by_weight ? 1 : 0;
     const int bin = sh.bin;
     const int n = (int)sh.bin_n;
     if (n <= kList) {
-      list<kMarked>([&](float l) { return bin_of(l) == bin; }, which, n);
+      list([&](float l) { return bin_of(l) == bin; }, which, n);
       rank_list(n, by_weight, goal, sh.above_n, sh.above_w);
       return;
     }
     uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-    some<kMarked>([&](int, float l) {
+    some([&](int, float l) {
       if (bin_of(l) == bin) {
         lo = min(lo, key_of(l));
         hi = max(hi, key_of(l));
@@ -734,7 +742,7 @@ struct RowSampler {
       const uint32_t above_n = sh.above_n;
       const unsigned long long above_w = sh.above_w;
       clear();
-      some<kMarked>([&](int, float l) {
+      some([&](int, float l) {
         const int x = bits(l);
         if (x < 0) return;
         if (by_weight)
@@ -748,13 +756,13 @@ struct RowSampler {
       const int b = sh.bin;
       const int left = (int)sh.bin_n;
       if (left <= kList) {
-        list<kMarked>([&](float l) { return bits(l) == b; }, which, left);
+        list([&](float l) { return bits(l) == b; }, which, left);
         rank_list(left, by_weight, goal, sh.above_n, sh.above_w);
         return;
       }
       lo = 0xFFFFFFFFu;
       hi = 0u;
-      some<kMarked>([&](int, float l) {
+      some([&](int, float l) {
         if (bits(l) == b) {
           lo = min(lo, key_of(l));
           hi = max(hi, key_of(l));
@@ -771,13 +779,16 @@ struct RowSampler {
     };
     const uint32_t above_n = sh.above_n;
     clear();
-    each([&](int, float l) {
-      const int x = bin_of(l);
-      if (x >= 0) atomicAdd(&sh.count_fine[x], 1u);
+    marks = 0;
+    each([&](int v, float l) {
+      const float x = place(l);
+      if ((int)x <= b) marks |= mark_of(v);
+      if ((int)x == b) atomicAdd(&sh.count_fine[finer(x, b, (float)kFine)], 1u);
     });
+    marked = can_mark();
     cluster_sync();
     find(true, false, k, above_n, 0ull);
-    resolve<false>(bin_of, false, k);
+    resolve(bin_of, false, k);
   }
 
   // The nucleus' cut among the bins [b0, b1] of the counts, or false.  *mine:
@@ -791,29 +802,24 @@ struct RowSampler {
       return b >= b0 && b <= b1 ? finer(x, b0, step) : -1;
     };
     clear();
-    unsigned long long above = 0, all = 0;
-    marks = 0;
-    const auto pass = [&](auto plain) {
-      int i = 0;
-      each([&](int v, float l) {
-        float y;
-        unsigned long long w = scale.weight(l, y);
-        if (!plain.value && (w < least || (has_cut && !before_cut(v, l)))) w = 0ull;
-        const float x = y * (kBins / kFar);
-        const int b = (int)x;
-        all += w;
-        above += b < b0 ? w : 0ull;
-        if (b >= b0 && b <= b1) {
-          enter(finer(x, b0, step), w);
-          marks |= 1ull << (i & 63);
-        }
-        ++i;
-      });
+    unsigned long long above = 0, all = 0, ends = 0;
+    const auto take = [&](int v, float l, auto plain) {
+      float y;
+      unsigned long long w = scale.weight(l, y);
+      if (!plain.value && (w < least || (has_cut && !before_cut(v, l)))) w = 0ull;
+      const float x = y * (kBins / kFar);
+      const int b = (int)x;
+      all += w;
+      above += b < b0 ? w : 0ull;
+      if (b >= b0 && b <= b1) {
+        enter(finer(x, b0, step), w);
+        ends |= mark_of(v);
+      }
     };
     if (has_cut || least > 1ull)
-      pass(std::false_type());
+      some([&](int v, float l) { take(v, l, std::false_type()); });
     else
-      pass(std::true_type());
+      each([&](int v, float l) { take(v, l, std::true_type()); });
     unsigned long long rest = all - above;
     gather();
     *mine = above;
@@ -831,7 +837,9 @@ struct RowSampler {
     const unsigned long long goal = sh.goal;
     find(true, true, goal, 0u, before);
     if (sh.bin < 0) return false;
-    resolve<true>(bin_of, true, goal);
+    marks = ends;
+    marked = can_mark();
+    resolve(bin_of, true, goal);
     return true;
   }
 
@@ -850,7 +858,7 @@ struct RowSampler {
     }
     take_cut();
     if (draws)
-      some<true>([&](int v, float l) {
+      some([&](int v, float l) {
         const int b = (int)place(l);
         if (b >= b0 && b <= b1) mine += staying(v, l);
       });
@@ -873,7 +881,7 @@ struct RowSampler {
   __device__ __forceinline__ unsigned long long sum() const {
     unsigned long long mine = 0;
     if (has_cut || least > 1ull)
-      each([&](int v, float l) { mine += staying(v, l); });
+      some([&](int v, float l) { mine += staying(v, l); });
     else
       each([&](int, float l) {
         float y;
@@ -1015,6 +1023,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
   s.scale.power = sh.power;
   s.least = min_p > 0.0f ? max(1ull, (unsigned long long)ceilf(fminf(min_p, 1.0f) * 0x1p42f)) : 1ull;
   s.has_cut = false;
+  s.marked = false;
   const bool nucleus = top_p < 1.0f;
   int last = kBins - 1;  // top-k's bin
   if (k > 1 || nucleus) s.count_places();
@@ -1024,7 +1033,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     const int n = b < 0 ? kList + 1 : (int)(sh.above_n + sh.bin_n);
     if (n <= kList) {
       // all of what top-k leaves can be listed
-      s.template list<false>([&](float l) { return (int)s.place(l) <= b; }, 2, n);
+      s.list([&](float l) { return (int)s.place(l) <= b; }, 2, n);
       s.rank_list(n, false, (unsigned long long)k, 0u, 0ull);
       if (nucleus) {
         if (tid == 0)

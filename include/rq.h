@@ -431,7 +431,9 @@ rq_status rq_residual_norm(const rq_norm_params *params_host, int dtype, const v
  *     unused sequence's length as it is); must not be length.
  * A token whose page is missing (past the table or the stack, or a negative
  * entry) gets slot -1 and records RQ_ERR_INDEX (rq_get_device_status); a
- * missing new page is written as -1 where the table has room.
+ * missing new page is written as -1 where the table has room.  Drafts that are
+ * not kept give their pages back when the count is raised again by as many: the
+ * pages lie at the stack's end in the order in which they are taken.
  * page_size: 16, 32, 64, 128 or 256.  batch <= 65536, max_pages >= 1.
  * batch == 0 does nothing but fill `rows` and free_left.  int32 arrays are
  * 4-byte aligned, slot 8-byte.  One launch, no scratch.

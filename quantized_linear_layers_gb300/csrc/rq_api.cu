@@ -734,7 +734,8 @@ rq_status rq_batch_plan(const int32_t* length, const int32_t* count, int batch, 
       !aligned(free_pages, 4) || !aligned(free_count, 4) || !aligned(free_left, 4) ||
       !aligned(slot, 8) || !aligned(position, 4) || !aligned(sequence, 4) ||
       !aligned(row_start, 4) || !aligned(next_length, 4) || free_left == free_count ||
-      (next_length != nullptr && next_length == length))
+      (next_length != nullptr && (next_length == length || next_length == count)) ||
+      (row_start != nullptr && (row_start == length || row_start == count)))
     return RQ_ERR_SHAPE;
   return launch_batch_plan(length, count, batch, new_tokens, page_size, page_table, max_pages,
                            free_pages, free_capacity, free_count, free_left, slot, position,

@@ -94,8 +94,8 @@ struct SampleShared {
   // is divided
   unsigned int count[kBins + 1], count_fine[kFine];
   Bin bins[kFine];
-  // sums of the weights' bits 0 .. 14, 15 .. 28 and 29 .. 42: 2^17 tokens a
-  // CTA do not wrap them, and nothing is carried between atomics
+  // sums of the weights' bits 0 .. 13, 14 .. 27 and 28 .. 42: up to 2^18 - 1
+  // tokens a CTA do not wrap them, and nothing is carried between atomics
   unsigned int weight[3][kFine];
   unsigned long long sums[2][kParts];
   unsigned long long found[3][kList];  // this CTA's tokens of the lists
@@ -436,9 +436,9 @@ struct RowSampler {
 
   __device__ __forceinline__ void enter(int bin, unsigned long long w) const {
     atomicAdd(&sh.count_fine[bin], 1u);
-    atomicAdd(&sh.weight[0][bin], (unsigned int)w & 0x7FFFu);
-    atomicAdd(&sh.weight[1][bin], (unsigned int)(w >> 15) & 0x3FFFu);
-    atomicAdd(&sh.weight[2][bin], (unsigned int)(w >> 29));
+    atomicAdd(&sh.weight[0][bin], (unsigned int)w & 0x3FFFu);
+    atomicAdd(&sh.weight[1][bin], (unsigned int)(w >> 14) & 0x3FFFu);
+    atomicAdd(&sh.weight[2][bin], (unsigned int)(w >> 28));
   }
 
   // The finer histogram; seen by the cluster after its barrier, and cleared
@@ -452,8 +452,8 @@ struct RowSampler {
   __device__ __forceinline__ void gather() const {
     __syncthreads();
     if (tid < kFine)
-      sh.bins[tid] = Bin{sh.weight[0][tid] + ((unsigned long long)sh.weight[1][tid] << 15) +
-                             ((unsigned long long)sh.weight[2][tid] << 29),
+      sh.bins[tid] = Bin{sh.weight[0][tid] + ((unsigned long long)sh.weight[1][tid] << 14) +
+                             ((unsigned long long)sh.weight[2][tid] << 28),
                          sh.count_fine[tid], 0u};
   }
 
@@ -854,7 +854,13 @@ struct RowSampler {
       bracket<true>(top_p, last);
       b0 = sh.bin;
       b1 = max(sh.bin, sh.bin_last);
-      cut_weight(b0, b1, top_p, &mine);
+      if (!cut_weight(b0, b1, top_p, &mine)) {
+        // (not reached while the bounds' thousandth covers their roundings)
+        cluster_sync();
+        b0 = 0;
+        b1 = kBins - 1;
+        cut_weight(b0, b1, top_p, &mine);
+      }
     }
     take_cut();
     if (draws)
@@ -1123,6 +1129,7 @@ rq_status launch_type(SampleArgs a, int rows, cudaStream_t st) {
   a.groups = (all + ranks * kSThreads - 1) / (ranks * kSThreads);
   a.pitch = a.groups | 1;
   a.by = divisor((uint32_t)a.groups);
+  static_assert((1 << 20) / kMaxCluster + 64 * kSThreads < 1 << 18, "tokens of a CTA");
   const bool cached = (size_t)a.pitch * kSThreads * 16 <= (size_t)kCacheBytes;
   if (a.p != nullptr)
     return cached ? launch_row<T, true, true>(a, rows, ranks, st)

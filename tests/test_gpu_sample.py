@@ -141,6 +141,39 @@ def test_crowded_logits(rq):
         check(rq, logits, u, t=[30.0] * 4, k=[9000] * 4, p=[p] * 4)
 
 
+def test_weights_at_the_edges_of_their_bins(rq):
+    # likely tokens at the upper edges of the 43/512 octave wide bins that
+    # places are guessed by, unlikely ones at the lower edges: a nucleus that
+    # ends a bin and more before the guess, and one behind it
+    octaves = 43.0 / 512
+    upper = torch.arange(60).double() * octaves + 0.0005
+    lower = (60 + torch.arange(60).double()) * octaves + octaves - 0.0005
+    y = torch.cat([torch.zeros(1).double(), upper.repeat_interleave(40), lower.repeat_interleave(160)])
+    flipped = torch.cat([torch.zeros(1).double(),
+                         (upper + octaves - 0.001).repeat_interleave(40),
+                         (lower - octaves + 0.001).repeat_interleave(160)])
+    for places in (y, flipped):
+        logits = (-places * np.log(2.0)).float()
+        order = torch.randperm(len(logits), generator=ref.gen(4))
+        logits = logits[order][None].expand(24, -1).contiguous().cuda()
+        w = ref.weights(logits[0].cpu().numpy(), 1.0).astype(np.float64)
+        likely = float(w[logits[0].cpu().numpy() > -60.0 * octaves * np.log(2.0)].sum() / w.sum())
+        p = [likely + 0.01 * d for d in np.linspace(-2.5, 2.5, 24)]
+        check(rq, logits, uniform(ref.gen(5), 24), p=p)
+        check(rq, logits, uniform(ref.gen(6), 24), p=p, k=[9000] * 24, m=[1e-6] * 24)
+
+
+def test_weights_of_many_set_bits_in_one_bin(rq):
+    # 2^20 tokens of one weight whose low bits are set: sums of its parts
+    n = 1 << 20
+    best = min((float(x) for x in np.linspace(0.5, 0.6, 20000).astype(np.float32)),
+               key=lambda x: int(~ref.weights(np.array([0.0, -x], np.float32), 1.0)[1] & 0x3FFF))
+    logits = torch.full((2, n), -best)
+    logits[0, 77] = 0.0
+    logits[1, 1 << 19] = 0.0
+    check(rq, logits.cuda(), [0.25, 0.75], p=[0.5, 0.999])
+
+
 def test_infinities_and_nans(rq):
     inf, nan = float("inf"), float("nan")
     rows = torch.zeros(8, 700)

@@ -117,7 +117,7 @@ def test_bad_plans(rq):
     lib = rq.lib()
 
     def call(length=A, count=A, batch=2, new=3, page=16, table=A, pages=4, free=A, capacity=8,
-             available=A, left=B, slot=A, position=A, sequence=A, rows=6, start=A, following=B):
+             available=A, left=B, slot=A, position=A, sequence=A, rows=6, start=B, following=B):
         return lib.rq_batch_plan(length, count, batch, new, page, table, pages, free, capacity,
                                  available, left, slot, position, sequence, rows, start, following,
                                  NULL)
@@ -135,7 +135,9 @@ def test_bad_plans(rq):
                  "start", "following"):
         assert call(**{name: A + 2}) == 2
     assert call(slot=A + 4) == 2
-    assert call(left=A) == 2 and call(following=A) == 2   # read by blocks that run on
+    # inputs that other blocks still read
+    assert call(left=A) == 2 and call(following=A) == 2 and call(start=A) == 2
+    assert call(length=0x30000, following=A) == 2 and call(length=0x30000, start=A) == 2
 
 
 def test_bad_sampling(rq):

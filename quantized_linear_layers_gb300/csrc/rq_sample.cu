@@ -325,7 +325,6 @@ struct RowSampler {
   // logit is -Inf.
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-#pragma unroll 2
     for (int i = 0; i < a.groups; ++i) {
       const uint4 g = read(i);
       const T* t = reinterpret_cast<const T*>(&g);

@@ -87,14 +87,26 @@ __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_kernel(const No
   if (t < a.tokens) {
     const T* yp = static_cast<const T*>(a.y) + t * a.y_stride;
     const R* hp = static_cast<const R*>(a.h) + t * a.h_stride;
+    const T* gp = static_cast<const T*>(a.gate) + t * a.gate_stride;
     Raw<T, V> y[G];
     Raw<R, V> hr[G];
+    // a thread of few values sends for weights and gate with them; one of many
+    // keeps its registers for those
+    constexpr bool kEarly = G * V <= 8;
+    constexpr int E = kEarly ? G : 1;
+    Raw<float, V> post[E], pre[E];
+    Raw<T, V> gate[E];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const int c = (g * group + lane) * V;
       if (c < a.width) {
         if (a.y != nullptr) y[g].load(yp + c);
         hr[g].load(hp + c);
+        if constexpr (kEarly) {
+          if (a.post_weight != nullptr) post[g].load(a.post_weight + c);
+          if (a.gate != nullptr) gate[g].load(gp + c);
+          if (a.pre_weight != nullptr) pre[g].load(a.pre_weight + c);
+        }
       }
     }
     float r = a.scale;
@@ -118,18 +130,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_kernel(const No
 #pragma unroll
       for (int j = 0; j < V; ++j) h[g][j] = hr[g][j];
       if (a.y != nullptr) {
-        float f[V], q[V];
+        constexpr bool kLate = !kEarly;
+        const int e = kEarly ? g : 0;
+        float f[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) f[j] = a.post ? y[g][j] * r : y[g][j];
         if (a.post_weight != nullptr) {
-          load_elems<float, V>(a.post_weight + c, q);
+          if constexpr (kLate) post[e].load(a.post_weight + c);
 #pragma unroll
-          for (int j = 0; j < V; ++j) f[j] *= q[j];
+          for (int j = 0; j < V; ++j) f[j] *= post[e][j];
         }
         if (a.gate != nullptr) {
-          load_elems<T, V>(static_cast<const T*>(a.gate) + t * a.gate_stride + c, q);
+          if constexpr (kLate) gate[e].load(gp + c);
 #pragma unroll
-          for (int j = 0; j < V; ++j) f[j] *= q[j];
+          for (int j = 0; j < V; ++j) f[j] *= gate[e][j];
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) h[g][j] = fmaf(a.scale, f[j], h[g][j]);
@@ -153,10 +167,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_kernel(const No
 #pragma unroll
         for (int j = 0; j < V; ++j) h[g][j] *= r;
         if (a.pre_weight != nullptr) {
-          float q[V];
-          load_elems<float, V>(a.pre_weight + c, q);
+          const int e = kEarly ? g : 0;
+          if constexpr (!kEarly) pre[e].load(a.pre_weight + c);
 #pragma unroll
-          for (int j = 0; j < V; ++j) h[g][j] *= q[j];
+          for (int j = 0; j < V; ++j) h[g][j] *= pre[e][j];
         }
         if (a.absmax != nullptr) {
 #pragma unroll

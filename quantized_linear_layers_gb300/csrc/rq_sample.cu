@@ -38,11 +38,11 @@
 // 35 us, of which reading them is 5, and reading, the maximum and the barriers
 // are 20 (the likeliest token alone); the exact pass issues 45 instructions a
 // token.  With top-k 50 34 us, with a nucleus of 0.9 63 us (196 with a
-// histogram of exact weights over the whole row).  One row: 13, 15 and 24 us,
+// histogram of exact weights over the whole row).  One row: 13, 15 and 23 us,
 // about 8 us of which are 5 to 7 barriers and what follows them (with cold
-// inputs, launch and events included).  What top-k leaves is marked in a word of
-// bits a thread, and later passes look at marked tokens only: top-k 300,
-// nucleus and min-p on one row 24 -> 16 us.
+// inputs, launch and events included); clusters of 16 CTAs made that 13, 15 and
+// 24.  What a larger top-k leaves is marked in a word of bits a thread, and later passes look at
+// marked tokens only.
 #include <type_traits>
 
 #include "rq_device.cuh"
@@ -60,6 +60,7 @@ constexpr int kParts = kMaxCluster * kSWarps;
 constexpr int kBins = 512;           // one a thread
 constexpr int kFine = 128;           // of what is divided further
 constexpr int kList = 128;           // tokens that are ranked one by one
+constexpr int kSort = kSThreads;     // tokens that top-k leaves and that are sorted
 constexpr int kTable = 512;
 constexpr float kFar = 43.0f * kTable;  // 2^42 2^-y/512 is below 1 from 42 octaves on
 constexpr int kCacheBytes = 176 * 1024;  // of a row's part, at most
@@ -98,8 +99,10 @@ struct SampleShared {
   // tokens a CTA do not wrap them, and nothing is carried between atomics
   unsigned int weight[3][kFine];
   unsigned long long sums[2][kParts];
-  unsigned long long found[3][kList];  // this CTA's tokens of the lists
-  unsigned long long list[kList], list_w[kList];
+  // this CTA's tokens of the lists: those that are ranked for top-k's and the
+  // nucleus' cut, and those that are sorted
+  unsigned long long found[2 * kList + kSort];
+  unsigned long long list[kSort], list_w[kSort];
   unsigned long long cut;              // tokens from this order on stay
   unsigned long long tmp_w[kSWarps];
   unsigned long long above_w, total, goal;
@@ -573,7 +576,8 @@ struct RowSampler {
   template <typename F>
   __device__ __forceinline__ void list(F in_list, int which, int n) {
     some([&](int v, float l) {
-      if (in_list(l)) sh.found[which][atomicAdd(&sh.pushed[which], 1u)] = order_of(v, l);
+      if (in_list(l))
+        sh.found[which * kList + atomicAdd(&sh.pushed[which], 1u)] = order_of(v, l);
     });
     cluster_sync();
     const uint32_t mine = lane < ranks ? get_u32(&sh.pushed[which], lane) : 0u;
@@ -586,7 +590,7 @@ struct RowSampler {
       }
     }
     if (tid < n) {
-      const unsigned long long o = get_u64(&sh.found[which][i], q);
+      const unsigned long long o = get_u64(&sh.found[which * kList + i], q);
       sh.list[tid] = o;
       sh.list_w[tid] = weight_kept(float_of((uint32_t)(o >> 32)));
     }
@@ -949,6 +953,81 @@ struct RowSampler {
     if (i < n && tid % g == 0 && before <= point && point < before + mine) *out = index;
   }
 
+  // Sorts a value a thread over the first m threads (a power of two), largest
+  // first: a bitonic network, by shuffles within a warp.
+  __device__ __forceinline__ unsigned long long sorted(unsigned long long v, int m) const {
+    for (int size = 2; size <= m; size *= 2)
+      for (int stride = size / 2; stride > 0; stride /= 2) {
+        unsigned long long other;
+        if (stride < 32) {
+          other = __shfl_xor_sync(0xFFFFFFFFu, v, stride);
+        } else {
+          sh.list[tid] = v;
+          __syncthreads();
+          other = sh.list[tid ^ stride];
+          __syncthreads();
+        }
+        const bool larger = ((tid & stride) == 0) == ((tid & size) == 0);
+        v = larger == (v > other) ? v : other;
+      }
+    return v;
+  }
+
+  // This thread's part of a running sum over the CTA, and the sum of all.
+  __device__ __forceinline__ unsigned long long sum_before(unsigned long long w,
+                                                           unsigned long long* all) {
+    const unsigned long long scan = warp_scan_add(w, lane);
+    __syncthreads();
+    if (lane == 31) sh.tmp_w[warp] = scan;
+    __syncthreads();
+    unsigned long long before = scan - w, total = 0;
+    for (int q = 0; q < kSWarps; ++q) {
+      before += q < warp ? sh.tmp_w[q] : 0ull;
+      total += sh.tmp_w[q];
+    }
+    *all = total;
+    return before;
+  }
+
+  // Of n listed tokens, among which all of top-k's are: both cuts (sh.cut, and
+  // sh.total, the weight of what stays), and for `draws` the token that the random
+  // number meets.
+  __device__ __forceinline__ void sort_list(int n, int k, float top_p, bool draws, float u,
+                                            int32_t* out) {
+    int m = 32;
+    while (m < n) m *= 2;
+    const unsigned long long o = sorted(tid < n ? sh.list[tid] : 0ull, m);
+    unsigned long long w = tid < n && tid < k ? weight_kept(float_of((uint32_t)(o >> 32))) : 0ull;
+    unsigned long long total;
+    const unsigned long long before = sum_before(w, &total);
+    if (tid == 0)
+      sh.goal = top_p < 1.0f
+                    ? max(1ull, (unsigned long long)ceil((double)fmaxf(top_p, 0.0f) *
+                                                         (double)total))
+                    : total;
+    __syncthreads();
+    const unsigned long long goal = sh.goal;
+    if (before < goal && goal <= before + w) {
+      sh.cut = o;
+      sh.total = before + w;
+    }
+    if (!draws) {
+      __syncthreads();
+      return;
+    }
+    // by index
+    if (before >= goal) w = 0ull;
+    sh.list_w[tid] = w;
+    const unsigned long long by_index = sorted(
+        w != 0ull ? (o << 32 | (unsigned long long)tid) | 1ull << 63 : 0ull, m);
+    __syncthreads();
+    w = by_index != 0ull ? sh.list_w[(unsigned int)by_index] : 0ull;
+    const unsigned long long run = sum_before(w, &total);
+    const unsigned long long point = point_of(u, total);
+    if (run <= point && point < run + w)
+      *out = (int)(0x7FFFFFFFu - ((unsigned int)(by_index >> 32) & 0x7FFFFFFFu));
+  }
+
   // p = weight / total; consecutive tokens by consecutive threads.  Without
   // min-p, which goes by W, the weights may be f32 powers.
   __device__ __forceinline__ void write(float* p, bool summed) {
@@ -1035,24 +1114,35 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
   if (k > 1) {
     s.find(false, false, (unsigned long long)k, 0u, 0ull);
     const int b = sh.bin;
-    const int n = b < 0 ? kList + 1 : (int)(sh.above_n + sh.bin_n);
-    if (n <= kList) {
+    const int n = b < 0 ? kSort + 1 : (int)(sh.above_n + sh.bin_n);
+    if (n <= kSort) {
       // all of what top-k leaves can be listed
       s.list([&](float l) { return (int)s.place(l) <= b; }, 2, n);
-      s.rank_list(n, false, (unsigned long long)k, 0u, 0ull);
-      if (nucleus) {
-        if (tid == 0)
-          sh.goal = max(1ull, (unsigned long long)ceil((double)fmaxf(top_p, 0.0f) *
-                                                       (double)sh.total));
-        __syncthreads();
-        s.rank_list(n, true, sh.goal, 0u, 0ull);
-      }
-      s.take_cut();
       cluster_arrive();  // (the lists' parts have been read)
-      if constexpr (kProbs)
+      // few are ranked by comparing all pairs, more are sorted (64 rows of
+      // 131072, top-k 50: 35 us by pairs, 37 sorted; one row, top-k 250,
+      // nucleus and min-p: 21 us sorted, 24 by the searches below)
+      const bool few = n <= kList;
+      if (few) {
+        s.rank_list(n, false, (unsigned long long)k, 0u, 0ull);
+        if (nucleus) {
+          if (tid == 0)
+            sh.goal = max(1ull, (unsigned long long)ceil((double)fmaxf(top_p, 0.0f) *
+                                                         (double)sh.total));
+          __syncthreads();
+          s.rank_list(n, true, sh.goal, 0u, 0ull);
+        }
+      }
+      if constexpr (kProbs) {
+        if (!few) s.sort_list(n, k, top_p, false, 0.0f, nullptr);
+        s.take_cut();
         s.write(p, true);
-      else if (rank == 0)
-        s.draw_listed(n, a.u[r], a.token + r);
+      } else if (rank == 0) {
+        if (few)
+          s.draw_listed(n, a.u[r], a.token + r);
+        else
+          s.sort_list(n, k, top_p, true, a.u[r], a.token + r);
+      }
       cluster_wait();
       return;
     }

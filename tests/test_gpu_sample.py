@@ -91,6 +91,21 @@ def test_filters(rq, vocab, dtype):
     check(rq, logits, u, t=t, k=k, p=p, m=m)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [600, 5000, 131072])
+def test_top_k_around_the_sizes_that_are_listed(rq, vocab, dtype):
+    g = ref.gen(vocab + 1)
+    ks = [2, 31, 32, 33, 64, 100, 120, 127, 128, 129, 200, 255, 256, 257, 400, 480, 500, 511, 512,
+          513, 560, 599]
+    rows = len(ks)
+    logits = (2.5 * torch.randn(rows, vocab, generator=g)).to(ref.DTYPES[dtype]).cuda()
+    u = uniform(g, rows)
+    check(rq, logits, u, k=ks)
+    check(rq, logits, u, k=ks, p=[0.8] * rows)
+    check(rq, logits, u, t=[1.5] * rows, k=ks, p=[0.999] * rows, m=[0.01] * rows)
+    check(rq, logits, u, k=ks, p=[0.0] * rows)
+
+
 def test_likeliest(rq):
     g = ref.gen(2)
     logits = torch.randn(6, 3001, generator=g)

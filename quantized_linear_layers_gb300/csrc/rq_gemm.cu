@@ -267,8 +267,8 @@ struct GemmArgs {
 // and a batch's loads are made before the accumulator is read: their latency,
 // not their bytes, is what such an epilogue takes (bf16 factor, 2048 x 18944 x
 // 3584: 377 us without either, 96 with, 86 without a factor).  Loads of tokens
-// and outputs that are not there are made at clamped places rather than skipped, since a
-// branch around each would wait for it.  Keeping the next batch's operands in
+// and outputs that are not there are made at clamped places rather than
+// skipped, since a branch around each would wait for it.  Keeping the next batch's operands in
 // registers instead took 141 us (SiLU and factor; 103 now), and 12 or 16 warps
 // of fewer registers 115 and 104.
 //
@@ -1154,7 +1154,8 @@ fp8_gemm_splitk_kernel(const __grid_constant__ CUtensorMap tmap_w,
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const bool in = n + e < args.N;
-          mul[e] = in && out.mul != nullptr ? elem_float(out.mul[m * out.mul_stride + n + e]) : 1.0f;
+          mul[e] =
+              in && out.mul != nullptr ? elem_float(out.mul[m * out.mul_stride + n + e]) : 1.0f;
           res[e] = in && out.residual != nullptr
                        ? elem_float(out.residual[m * out.residual_stride + n + e])
                        : 0.0f;
@@ -1504,8 +1505,8 @@ static rq_status launch_fp8_gemm_out(const uint8_t* x_fp8, const float* x_deq,
   if (std::getenv("RQ_GEMM_LOG") != nullptr)
     std::fprintf(stderr, "rq_gemm: single M=%d N=%d K=%d bn=%d tiles=%d grid=%d stages=%d\n", M,
                  N, K, bn, tiles, grid, a.stages);
-  return launch_kernel(fp8_gemm_kernel<Out>, grid, kThreads, gemm_smem_bytes(a.stages, bn * kBK), st,
-                       tw, tx, a, fused);
+  return launch_kernel(fp8_gemm_kernel<Out>, grid, kThreads, gemm_smem_bytes(a.stages, bn * kBK),
+                       st, tw, tx, a, fused);
 }
 
 rq_status launch_fp8_gemm_group(const uint8_t* x_fp8, const float* x_deq,

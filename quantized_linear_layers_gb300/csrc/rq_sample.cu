@@ -12,13 +12,13 @@
 //   2^(-y/512) = 2^-n 2^(-j/512) 2^(-z/512),   512 n + j = rint(y), |z| <= 1/2:
 // a table of the 512 powers in 42 bits, less its product with a cubic in z
 // that is below 2^-10, so that f32 roundings in it stay below 2^-33 of the
-// weight (2^-35.6 on the average, measured).  About 34 instructions a token.  (64-bit floats would need fewer,
-// at 1/64 of the rate.)
+// weight (2^-35.6 on the average, measured).  (64-bit floats would need fewer
+// instructions, at 1/64 of the rate.)
 //
 // Finding where top-k and top-p cut.  Sorting a row is not needed.  Counts of
 // tokens in 512 bins of y give top-k's bin, and, since a bin's weights lie
-// within 6 % of each other, the few bins that a nucleus can end in.  One pass of exact
-// weights then sums what stands before those bins and after them, and divides
+// within 6 % of each other, the few bins that a nucleus can end in.  One pass of
+// exact weights then sums what stands before those bins and after them, and divides
 // them into 128 finer ones; the few tokens of the bin that the cut falls in are listed
 // and each counts what stands before it.  What is not divided far enough is
 // divided by the bits of the logits; equal logits, however many, are cut by
@@ -853,7 +853,7 @@ struct RowSampler {
     int b0 = sh.bin, b1 = max(sh.bin, sh.bin_last);
     unsigned long long mine;
     if (!cut_weight(b0, b1, top_p, &mine)) {
-      cluster_sync();  // (the second buffer has been read)
+      cluster_sync();  // (the finer histogram has been read)
       bracket<true>(top_p, last);
       b0 = sh.bin;
       b1 = max(sh.bin, sh.bin_last);
@@ -1056,7 +1056,8 @@ struct RowSampler {
       float l;
       if constexpr (kCached) {
         const int q = (int)quotient((uint32_t)(i / kPer), a.by);
-        l = elem_float(reinterpret_cast<const T*>(cache + (warp * 32 + q) * a.pitch)[i - q * width]);
+        const T* t = reinterpret_cast<const T*>(cache + (warp * 32 + q) * a.pitch);
+        l = elem_float(t[i - q * width]);
       } else {
         l = elem_float(row[v]);
       }
@@ -1105,7 +1106,9 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
   }
   s.scale.set(t);
   s.scale.power = sh.power;
-  s.least = min_p > 0.0f ? max(1ull, (unsigned long long)ceilf(fminf(min_p, 1.0f) * 0x1p42f)) : 1ull;
+  s.least = 1ull;
+  if (min_p > 0.0f)
+    s.least = max(1ull, (unsigned long long)ceilf(fminf(min_p, 1.0f) * 0x1p42f));
   s.has_cut = false;
   s.marked = false;
   const bool nucleus = top_p < 1.0f;
@@ -1151,6 +1154,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
       s.cut_count(b, (unsigned long long)k);
       s.take_cut();
     }
+    __syncthreads();  // (what was found has been read by every thread)
   }
   if (nucleus) {
     const unsigned long long mine = s.cut_nucleus(top_p, last, !kProbs);

@@ -18,12 +18,13 @@
 // Finding where top-k and top-p cut.  Sorting a row is not needed.  Counts of
 // tokens in 512 bins of y give top-k's bin, and, since a bin's weights lie
 // within 6 % of each other, the few bins that a nucleus can end in.  One pass of
-// exact weights then sums what stands before those bins and after them, and divides
-// them into 128 finer ones; the few tokens of the bin that the cut falls in are listed
-// and each counts what stands before it.  What is not divided far enough is
-// divided by the bits of the logits; equal logits, however many, are cut by
-// counting in order of index.  A small top-k lists all tokens down to its bin
-// and needs no further look at the row.
+// exact weights then sums what stands before those bins and after them, and
+// divides them into 128 finer ones; the few tokens of the bin that the cut
+// falls in are listed and each counts what stands before it.  What is not
+// divided far enough is divided by the bits of the logits; equal logits,
+// however many, are cut by counting in order of index.  A top-k of up to 512
+// tokens, with its last bin, lists them all, ranks or sorts them, and needs no
+// further look at the row.
 //
 // One cluster of CTAs takes a row and keeps it in shared memory: logits are
 // read from memory once.  Every CTA reads the others' histograms through
@@ -41,8 +42,8 @@
 // histogram of exact weights over the whole row).  One row: 13, 15 and 23 us,
 // about 8 us of which are 5 to 7 barriers and what follows them (with cold
 // inputs, launch and events included); clusters of 16 CTAs made that 13, 15 and
-// 24.  What a larger top-k leaves is marked in a word of bits a thread, and later passes look at
-// marked tokens only.
+// 24.  What a larger top-k leaves is marked in a word of bits a thread, and
+// later passes look at marked tokens only.
 #include <type_traits>
 
 #include "rq_device.cuh"

@@ -13,7 +13,9 @@
 // 29.8 us (5.92 TB/s), bf16 throughout 23.0 (5.11: there a CTA's steps one
 // after another count).  y and h stay as they lie in memory until they are
 // used, which lets four CTAs of 224 threads onto an SM (16-bit rows as floats:
-// 27.3 us; six CTAs spill registers: 40.9 for f32).  One token: 2.3 us in a replayed graph.
+// 27.3 us; six CTAs spill registers: 40.9 for f32).  One token: 2.2 us in a
+// replayed graph.  Odd widths: 1091 tokens of 6245 f32 values 28 us (an element
+// at a time 40).
 #include "rq_device.cuh"
 #include "rq_elem.cuh"
 #include "rq_internal.h"
@@ -61,18 +63,39 @@ struct Raw {
     constexpr int kPer = 16 / (int)sizeof(T);
     return elem_float(reinterpret_cast<const T*>(&w[j / kPer])[j % kPer]);
   }
+  // values [c, c + V) of a row of which some may not be there (zeros)
+  __device__ __forceinline__ void load_some(const T* row, int c, int width) {
+    alignas(16) T t[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      t[j] = c + j >= 0 && c + j < width ? row[c + j] : float_elem<T>(0.0f);
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint4*>(t)[i];
+  }
 };
 template <typename T>
 struct Raw<T, 1> {
   T w;
   __device__ __forceinline__ void load(const T* p) { w = *p; }
+  __device__ __forceinline__ void load_some(const T*, int, int) {}
   __device__ __forceinline__ float operator[](int) const { return elem_float(w); }
 };
 
+// V values to a row, of which some may not be there.
+template <typename T, int V>
+__device__ __forceinline__ void store_some(T* row, int c, int width, const float (&x)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (c + j >= 0 && c + j < width) row[c + j] = float_elem<T>(x[j]);
+}
+
 // T: type of y, gate and x; R: of the residual stream; V: values a thread
 // takes at a time; G: how many such groups it holds.  kOneWarp: a token is one
-// warp's, several to a CTA; else a CTA's, of at most kThreads threads.
-template <typename T, typename R, int V, int G, bool kOneWarp, int kThreads, int kCtas>
+// warp's, several to a CTA; else a CTA's, of at most kThreads threads.  kSkew:
+// rows of a width that is no multiple of V, one behind another.  Groups are then
+// counted over all of them, so that they are aligned; a row's first and last
+// group are its own in part, and weights are read a value at a time.
+template <typename T, typename R, int V, int G, bool kOneWarp, bool kSkew, int kThreads, int kCtas>
 __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_kernel(const NormArgs a) {
   __shared__ float part[2][kMaxWarps];
   __shared__ unsigned int top;
@@ -88,20 +111,30 @@ __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_kernel(const No
     const T* yp = static_cast<const T*>(a.y) + t * a.y_stride;
     const R* hp = static_cast<const R*>(a.h) + t * a.h_stride;
     const T* gp = static_cast<const T*>(a.gate) + t * a.gate_stride;
+    const int skew = kSkew ? (int)(t * a.width % V) : 0;
+    // a thread's group g: its first value, whether it has any, and all
+    const auto at = [&](int g) { return (g * group + lane) * V - skew; };
+    const auto any = [&](int c) { return c < a.width; };
+    const auto whole = [&](int c) { return !kSkew || (c >= 0 && c + V <= a.width); };
     Raw<T, V> y[G];
     Raw<R, V> hr[G];
     // a thread of few values sends for weights and gate with them; one of many
     // keeps its registers for those
-    constexpr bool kEarly = G * V <= 8;
+    constexpr bool kEarly = G * V <= 8 && !kSkew;
     constexpr int E = kEarly ? G : 1;
     Raw<float, V> post[E], pre[E];
     Raw<T, V> gate[E];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const int c = (g * group + lane) * V;
-      if (c < a.width) {
-        if (a.y != nullptr) y[g].load(yp + c);
-        hr[g].load(hp + c);
+      const int c = at(g);
+      if (any(c)) {
+        if (whole(c)) {
+          if (a.y != nullptr) y[g].load(yp + c);
+          hr[g].load(hp + c);
+        } else {
+          if (a.y != nullptr) y[g].load_some(yp, c, a.width);
+          hr[g].load_some(hp, c, a.width);
+        }
         if constexpr (kEarly) {
           if (a.post_weight != nullptr) post[g].load(a.post_weight + c);
           if (a.gate != nullptr) gate[g].load(gp + c);
@@ -114,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_kernel(const No
       float sum = 0.0f;
 #pragma unroll
       for (int g = 0; g < G; ++g)
-        if ((g * group + lane) * V < a.width) {
+        if (any(at(g))) {
 #pragma unroll
           for (int j = 0; j < V; ++j) sum = fmaf(y[g][j], y[g][j], sum);
         }
@@ -125,8 +158,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_kernel(const No
     float square = 0.0f;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const int c = (g * group + lane) * V;
-      if (c >= a.width) continue;
+      const int c = at(g);
+      if (!any(c)) continue;
 #pragma unroll
       for (int j = 0; j < V; ++j) h[g][j] = hr[g][j];
       if (a.y != nullptr) {
@@ -136,19 +169,30 @@ __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_kernel(const No
 #pragma unroll
         for (int j = 0; j < V; ++j) f[j] = a.post ? y[g][j] * r : y[g][j];
         if (a.post_weight != nullptr) {
-          if constexpr (kLate) post[e].load(a.post_weight + c);
+          if constexpr (kSkew)
+            post[e].load_some(a.post_weight, c, a.width);
+          else if constexpr (kLate)
+            post[e].load(a.post_weight + c);
 #pragma unroll
           for (int j = 0; j < V; ++j) f[j] *= post[e][j];
         }
         if (a.gate != nullptr) {
-          if constexpr (kLate) gate[e].load(gp + c);
+          if (kSkew && (a.gate_stride == 0 || !whole(c)))
+            gate[e].load_some(gp, c, a.width);
+          else if constexpr (kLate)
+            gate[e].load(gp + c);
 #pragma unroll
           for (int j = 0; j < V; ++j) f[j] *= gate[e][j];
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) h[g][j] = fmaf(a.scale, f[j], h[g][j]);
-        if (a.h_out != nullptr)
-          store_elems<R, V>(static_cast<R*>(a.h_out) + t * a.width + c, h[g]);
+        if (a.h_out != nullptr) {
+          R* ho = static_cast<R*>(a.h_out) + t * a.width;
+          if (whole(c))
+            store_elems<R, V>(ho + c, h[g]);
+          else
+            store_some<R, V>(ho, c, a.width, h[g]);
+        }
       }
 #pragma unroll
       for (int j = 0; j < V; ++j) square = fmaf(h[g][j], h[g][j], square);
@@ -162,13 +206,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_kernel(const No
       T* xo = static_cast<T*>(a.x_out) + t * a.width;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const int c = (g * group + lane) * V;
-        if (c >= a.width) continue;
+        const int c = at(g);
+        if (!any(c)) continue;
 #pragma unroll
         for (int j = 0; j < V; ++j) h[g][j] *= r;
         if (a.pre_weight != nullptr) {
           const int e = kEarly ? g : 0;
-          if constexpr (!kEarly) pre[e].load(a.pre_weight + c);
+          if constexpr (kSkew)
+            pre[e].load_some(a.pre_weight, c, a.width);
+          else if constexpr (!kEarly)
+            pre[e].load(a.pre_weight + c);
 #pragma unroll
           for (int j = 0; j < V; ++j) h[g][j] *= pre[e][j];
         }
@@ -176,7 +223,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_kernel(const No
 #pragma unroll
           for (int j = 0; j < V; ++j) most = fmaxf(most, fabsf(h[g][j]));  // (a NaN is passed over)
         }
-        store_elems<T, V>(xo + c, h[g]);
+        if (whole(c))
+          store_elems<T, V>(xo + c, h[g]);
+        else
+          store_some<T, V>(xo, c, a.width, h[g]);
       }
     }
   }
@@ -203,24 +253,24 @@ __global__ void clear_word_kernel(uint32_t* word) {
   *word = 0u;
 }
 
-template <typename T, typename R, int V, int G>
+template <typename T, typename R, int V, int G, bool kSkew>
 rq_status launch_groups(const NormArgs& a, int threads, int per_cta, cudaStream_t st) {
   const unsigned ctas = (unsigned)((a.tokens + per_cta - 1) / per_cta);
   if (threads == 32)
-    return launch_kernel(residual_norm_kernel<T, R, V, G, true, 128, 1>, dim3(ctas),
+    return launch_kernel(residual_norm_kernel<T, R, V, G, true, kSkew, 128, 1>, dim3(ctas),
                          dim3(32 * per_cta), 0, st, a);
   if (threads <= 256)
-    return launch_kernel(residual_norm_kernel<T, R, V, G, false, 256, 4>, dim3(ctas),
+    return launch_kernel(residual_norm_kernel<T, R, V, G, false, kSkew, 256, 4>, dim3(ctas),
                          dim3(threads), 0, st, a);
-  return launch_kernel(residual_norm_kernel<T, R, V, G, false, 1024, 1>, dim3(ctas),
+  return launch_kernel(residual_norm_kernel<T, R, V, G, false, kSkew, 1024, 1>, dim3(ctas),
                        dim3(threads), 0, st, a);
 }
 
 // `groups` of V values in a row, G of them a thread.
-template <typename T, typename R, int V>
+template <typename T, typename R, int V, bool kSkew>
 rq_status launch_width(NormArgs a, cudaStream_t st) {
   constexpr int kMost = 16 / V;  // groups that fit 16 values a thread
-  const int groups = (a.width + V - 1) / V;
+  const int groups = (a.width + V - 1 + (kSkew ? V - 1 : 0)) / V;
   // few tokens: as many threads as the row has groups, so that each thread
   // waits for one load; many: as many loads in flight a thread as fit
   const bool few = a.tokens <= 2 * device_sm_count();
@@ -234,14 +284,14 @@ rq_status launch_width(NormArgs a, cudaStream_t st) {
     if (s != RQ_OK) return s;
   }
   if constexpr (kMost >= 16)
-    if (G == 16) return launch_groups<T, R, V, 16>(a, threads, per_cta, st);
+    if (G == 16) return launch_groups<T, R, V, 16, kSkew>(a, threads, per_cta, st);
   if constexpr (kMost >= 8)
-    if (G == 8) return launch_groups<T, R, V, 8>(a, threads, per_cta, st);
+    if (G == 8) return launch_groups<T, R, V, 8, kSkew>(a, threads, per_cta, st);
   if constexpr (kMost >= 4)
-    if (G == 4) return launch_groups<T, R, V, 4>(a, threads, per_cta, st);
+    if (G == 4) return launch_groups<T, R, V, 4, kSkew>(a, threads, per_cta, st);
   if constexpr (kMost >= 2)
-    if (G == 2) return launch_groups<T, R, V, 2>(a, threads, per_cta, st);
-  return launch_groups<T, R, V, 1>(a, threads, per_cta, st);
+    if (G == 2) return launch_groups<T, R, V, 2, kSkew>(a, threads, per_cta, st);
+  return launch_groups<T, R, V, 1, kSkew>(a, threads, per_cta, st);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -250,12 +300,18 @@ template <typename T, typename R>
 rq_status launch_types(const NormArgs& a, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(T);  // values of 16 bytes of the narrower type
   const auto whole = [](int64_t stride, size_t size) { return stride * size % 16 == 0; };
-  if (a.width % V == 0 && aligned16(a.y) && aligned16(a.gate) && aligned16(a.h) &&
-      aligned16(a.post_weight) && aligned16(a.pre_weight) && aligned16(a.h_out) &&
-      aligned16(a.x_out) && whole(a.y_stride, sizeof(T)) && whole(a.gate_stride, sizeof(T)) &&
+  const bool rows16 = aligned16(a.y) && aligned16(a.gate) && aligned16(a.h) &&
+                      aligned16(a.h_out) && aligned16(a.x_out);
+  if (a.width % V == 0 && rows16 && aligned16(a.post_weight) && aligned16(a.pre_weight) &&
+      whole(a.y_stride, sizeof(T)) && whole(a.gate_stride, sizeof(T)) &&
       whole(a.h_stride, sizeof(R)))
-    return launch_width<T, R, V>(a, st);
-  return launch_width<T, R, 1>(a, st);
+    return launch_width<T, R, V, false>(a, st);
+  // (a row's groups, its own and those it shares, must fit the threads)
+  if (rows16 && a.width <= 16384 - 2 * V && a.h_stride == a.width &&
+      (a.y == nullptr || a.y_stride == a.width) &&
+      (a.gate_stride == 0 || a.gate_stride == a.width))
+    return launch_width<T, R, V, true>(a, st);
+  return launch_width<T, R, 1, false>(a, st);
 }
 
 }  // namespace

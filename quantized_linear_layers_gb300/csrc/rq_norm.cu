@@ -14,8 +14,8 @@
 // after another count).  y and h stay as they lie in memory until they are
 // used, which lets four CTAs of 224 threads onto an SM (16-bit rows as floats:
 // 27.3 us; six CTAs spill registers: 40.9 for f32).  One token: 2.2 us in a
-// replayed graph.  Odd widths: 1091 tokens of 6245 f32 values 28 us (an element
-// at a time 40).
+// replayed graph.  Odd widths: 1091 tokens of 6245 f32 values with a gate a
+// token 34 us (an element at a time 40).
 #include "rq_device.cuh"
 #include "rq_elem.cuh"
 #include "rq_internal.h"

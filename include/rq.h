@@ -198,12 +198,18 @@ rq_status rq_fp8_gemm(const uint8_t *x_fp8, const float *x_dequant,
  * the ctx's scratch on a miss.  The bytes are those of rq_absmax followed by
  * rq_quant_e4m3, with rows M..M_pad-1 zero (M_pad = M rounded up to 16), so
  * the result feeds rq_fp8_gemm directly.  The key is (x, M, K, generation),
- * as for rq_linear, which calls this on its FP8 route.
+ * as for rq_linear, which calls this on its FP8 route.  A call on a stream that
+ * is being captured finds only what the same capture quantizes, so that every
+ * replay quantizes x anew, and a call that runs at once finds nothing captured:
+ * each kind has a scratch of its own, and captured graphs' scratch stays where
+ * it is until the ctx is destroyed, however much larger a later call is (a
+ * capture may allocate it).  All graphs of a ctx share it: they are replayed,
+ * like every call on the ctx, on one stream at a time.
  *   x: f32 [M x K], 16-byte aligned.   *x_fp8: E4M3 [M_pad x K] (owned by
  *   ctx).   *x_dequant: one device float (owned by ctx).
  * The pointers stay valid until a later miss on this ctx needs a larger
- * scratch, or the ctx is destroyed; a later miss of the same or smaller size
- * overwrites the bytes in stream order.  Allocates on a miss that needs a
+ * scratch (captured ones: always), or the ctx is destroyed; a later miss of the
+ * same or smaller size overwrites the bytes in stream order.  Allocates on a miss that needs a
  * larger scratch.  Errors: RQ_ERR_NULL, RQ_ERR_SHAPE (M, K < 1, x
  * misaligned), RQ_ERR_ALLOC, RQ_ERR_CUDA. */
 rq_status rq_fp8_act_cache(rq_ctx *ctx, const float *x, int M, int K,
@@ -232,7 +238,8 @@ rq_status rq_fp8_act_cache(rq_ctx *ctx, const float *x, int M, int K,
  *                   and RQ_ONE_PASS_QUANT=0 turn the first two off).
  * The activation cache ([gemm.rs], PMAT-084 reuse across Q/K/V and gate/up)
  * is keyed by (x, M, K, generation); rq_act_cache_invalidate bumps the
- * generation and must be called when x's contents change in place.
+ * generation and must be called when x's contents change in place.  Captured
+ * calls quantize x in the graph, whatever was cached before (rq_fp8_act_cache).
  * Errors: those of the routes taken. */
 rq_status rq_linear(rq_ctx *ctx, rq_qtype qtype, const void *w, const float *x,
                     float *y, int M, int N, int K, rq_stream_t stream);

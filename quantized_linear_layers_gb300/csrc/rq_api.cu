@@ -79,6 +79,19 @@ rq_status check_quant_shape(int qtype, int N, int K) {
 
 }  // namespace
 
+// E4M3 codes of one activation, followed (256-aligned) by their scale, and what
+// they were made of.
+struct ActScratch {
+  uint8_t* codes = nullptr;
+  float* deq = nullptr;
+  size_t cap = 0;
+  bool valid = false;
+  const float* x = nullptr;
+  int M = 0, K = 0;
+  uint64_t gen = 0;
+  unsigned long long capture = 0;  // the capture that records the quantization
+};
+
 struct TraceSlot {
   cudaEvent_t start = nullptr, stop = nullptr;
   int kind = 0;
@@ -96,10 +109,12 @@ struct rq_ctx {
   std::map<WeightKey, WeightEntry> weights;
   std::map<std::vector<WeightKey>, GroupEntry> groups;
   int64_t weight_bytes = 0;
-  uint8_t* act = nullptr;  // activation E4M3 scratch [M_pad x K]
-  size_t act_cap = 0;
+  // Activation scratch of calls that run at once, and of captured ones: a
+  // replay rewrites its codes at a time that the host does not see, so the two
+  // share none.  Buffers that captured graphs may use live until destroy.
+  ActScratch act[2];
+  std::vector<uint8_t*> act_kept;
   uint32_t* absmax = nullptr;  // device word
-  float* act_deq = nullptr;    // device float
   bool fused_ok = true;           // RQ_ONE_PASS_QUANT=0 keeps the two-kernel path
   int64_t fused_min = 1 << 20;    // fewer elements: two kernels (RQ_ONE_PASS_MIN)
   // at most this many elements: one cluster, one launch (RQ_CLUSTER_QUANT_MAX;
@@ -109,11 +124,7 @@ struct rq_ctx {
   uint32_t* slots = nullptr;      // per-CTA partial maxima of the two-kernel path
   unsigned long long* fused = nullptr;        // one-pass quantization barrier word
   unsigned long long* fused_slots = nullptr;  // and its per-CTA words (SM count)
-  // activation cache key
-  bool act_valid = false;
-  const float* act_x = nullptr;
-  int act_M = 0, act_K = 0;
-  uint64_t act_gen = 0, gen = 1;
+  uint64_t gen = 1;  // activation cache generation
   int64_t hits = 0, misses = 0;
   AttnScratch attn;  // partial rows of split sequences
 };
@@ -196,7 +207,6 @@ rq_status rq_ctx_create(rq_ctx** out) {
     return RQ_ERR_ALLOC;
   }
   c->absmax = static_cast<uint32_t*>(p);
-  c->act_deq = reinterpret_cast<float*>(static_cast<uint8_t*>(p) + 128);
   c->fused = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(p) + 192);
   if (cudaMemset(p, 0, 256) != cudaSuccess) {
     cudaFree(p);
@@ -246,7 +256,9 @@ void rq_ctx_destroy(rq_ctx* ctx) {
   }
   for (auto& kv : ctx->weights) cudaFree(kv.second.fp8);
   for (auto& kv : ctx->groups) cudaFree(kv.second.fp8);
-  if (ctx->act) cudaFree(ctx->act);
+  for (auto& a : ctx->act)
+    if (a.codes) cudaFree(a.codes);
+  for (uint8_t* p : ctx->act_kept) cudaFree(p);
   if (ctx->absmax) cudaFree(ctx->absmax);
   if (ctx->slots) cudaFree(ctx->slots);
   if (ctx->fused_slots) cudaFree(ctx->fused_slots);
@@ -371,45 +383,76 @@ rq_status rq_fp8_gemm(const uint8_t* x_fp8, const float* x_dequant, const uint8_
                          reinterpret_cast<cudaStream_t>(stream));
 }
 
-rq_status rq_fp8_act_cache(rq_ctx* ctx, const float* x, int M, int K,
-                           const uint8_t** x_fp8, const float** x_dequant,
-                           rq_stream_t stream) {
-  if (ctx == nullptr || x == nullptr || x_fp8 == nullptr || x_dequant == nullptr)
-    return RQ_ERR_NULL;
-  if (M < 1 || K < 1 || !aligned(x, 16)) return RQ_ERR_SHAPE;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  rq_status s = RQ_OK;
-  const bool hit = ctx->act_valid && ctx->act_x == x && ctx->act_M == M &&
-                   ctx->act_K == K && ctx->act_gen == ctx->gen;
+// The capture that `st` is in, 0 if none.
+static rq_status capture_of(cudaStream_t st, unsigned long long* id) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  *id = 0;
+  if (cudaStreamGetCaptureInfo(st, &status, id) != cudaSuccess) {
+    cudaGetLastError();  // (the legacy stream while another one is captured)
+    return RQ_ERR_CUDA;
+  }
+  if (status == cudaStreamCaptureStatusInvalidated) return RQ_ERR_CUDA;
+  if (status == cudaStreamCaptureStatusNone) *id = 0;
+  return RQ_OK;
+}
+
+// Room for `need` codes.  What ran at once is done with its buffer when it is
+// freed; a captured graph's stays, and the next is at least twice as large, so
+// that all of them together hold less than twice the last.
+static rq_status grow(rq_ctx* ctx, ActScratch* a, size_t need, bool captured) {
+  if (need <= a->cap) return RQ_OK;
+  if (captured && need < 2 * a->cap) need = 2 * a->cap;
+  const size_t body = (need + 255) / 256 * 256;
+  if (!captured && a->codes) {
+    cudaFree(a->codes);
+    *a = ActScratch();
+  }
+  // (an allocation is no work of the stream: it is made at once, and legal
+  // while the thread's captures are of the relaxed kind)
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (captured && cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return RQ_ERR_CUDA;
+  void* p = nullptr;
+  const cudaError_t e = cudaMalloc(&p, body + 256);
+  if (captured) cudaThreadExchangeStreamCaptureMode(&mode);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return RQ_ERR_ALLOC;
+  }
+  if (a->codes) ctx->act_kept.push_back(a->codes);
+  *a = ActScratch();
+  a->codes = static_cast<uint8_t*>(p);
+  a->deq = reinterpret_cast<float*>(a->codes + body);
+  a->cap = need;
+  return RQ_OK;
+}
+
+// rq_fp8_act_cache; `anew`: without a look at the cache.
+static rq_status act_codes(rq_ctx* ctx, const float* x, int M, int K, bool anew,
+                           const uint8_t** x_fp8, const float** x_dequant, cudaStream_t st) {
+  unsigned long long capture = 0;
+  rq_status s = capture_of(st, &capture);
+  if (s != RQ_OK) return s;
+  ActScratch& a = ctx->act[capture != 0 ? 1 : 0];
+  const bool hit = !anew && a.valid && a.x == x && a.M == M && a.K == K && a.gen == ctx->gen &&
+                   a.capture == capture;
   if (hit) {
     ++ctx->hits;
   } else {
     const int m_pad = (M + 15) / 16 * 16;
     const size_t need = (size_t)m_pad * (size_t)K;
-    if (need > ctx->act_cap) {
-      if (ctx->act) cudaFree(ctx->act);
-      ctx->act = nullptr;
-      ctx->act_cap = 0;
-      ctx->act_valid = false;
-      void* p = nullptr;
-      if (cudaMalloc(&p, need) != cudaSuccess) {
-        cudaGetLastError();
-        return RQ_ERR_ALLOC;
-      }
-      ctx->act = static_cast<uint8_t*>(p);
-      ctx->act_cap = need;
-    }
+    s = grow(ctx, &a, need, capture != 0);
+    if (s != RQ_OK) return s;
     const int64_t n = (int64_t)M * K;
     s = RQ_ERR_SHAPE;
     if (n <= ctx->cluster_max) {
       // a few tokens: one cluster reads x twice (the second time from L2)
       TraceScope ts(ctx, RQ_TRACE_QUANT, st);
-      s = launch_act_quant_cluster(x, n, (int64_t)need, ctx->act, ctx->absmax, ctx->act_deq, st);
+      s = launch_act_quant_cluster(x, n, (int64_t)need, a.codes, ctx->absmax, a.deq, st);
       if (s == RQ_ERR_SHAPE) ts.kernels(0);
-    } else if (ctx->fused_ok && n >= ctx->fused_min && act_quant_fused_fits(x, n, ctx->act)) {
+    } else if (ctx->fused_ok && n >= ctx->fused_min && act_quant_fused_fits(x, n, a.codes)) {
       TraceScope ts(ctx, RQ_TRACE_QUANT, st);
-      s = launch_act_quant_fused(x, n, (int64_t)need, ctx->act, ctx->absmax, ctx->act_deq,
-                                 ctx->fused, ctx->fused_slots, device_sm_count(), st);
+      s = launch_act_quant_fused(x, n, (int64_t)need, a.codes, ctx->absmax, a.deq, ctx->fused,
+                                 ctx->fused_slots, device_sm_count(), st);
       if (s == RQ_ERR_SHAPE) ts.kernels(0);
     }
     // RQ_ERR_SHAPE from the one-cluster or one-pass launcher: nothing was
@@ -418,23 +461,33 @@ rq_status rq_fp8_act_cache(rq_ctx* ctx, const float* x, int M, int K,
       // two kernels: per-CTA maxima into slots, then the encoding
       TraceScope ts(ctx, RQ_TRACE_QUANT, st);
       ts.kernels(2);
-      s = launch_act_quant_two_pass(x, n, (int64_t)need, ctx->act, ctx->slots, ctx->absmax,
-                                    ctx->act_deq, st);
+      s = launch_act_quant_two_pass(x, n, (int64_t)need, a.codes, ctx->slots, ctx->absmax, a.deq,
+                                    st);
     }
     if (s != RQ_OK) {
-      ctx->act_valid = false;
+      a.valid = false;
       return s;
     }
-    ctx->act_valid = true;
-    ctx->act_x = x;
-    ctx->act_M = M;
-    ctx->act_K = K;
-    ctx->act_gen = ctx->gen;
+    a.valid = true;
+    a.x = x;
+    a.M = M;
+    a.K = K;
+    a.gen = ctx->gen;
+    a.capture = capture;
     ++ctx->misses;
   }
-  *x_fp8 = ctx->act;
-  *x_dequant = ctx->act_deq;
+  *x_fp8 = a.codes;
+  *x_dequant = a.deq;
   return RQ_OK;
+}
+
+rq_status rq_fp8_act_cache(rq_ctx* ctx, const float* x, int M, int K,
+                           const uint8_t** x_fp8, const float** x_dequant,
+                           rq_stream_t stream) {
+  if (ctx == nullptr || x == nullptr || x_fp8 == nullptr || x_dequant == nullptr)
+    return RQ_ERR_NULL;
+  if (M < 1 || K < 1 || !aligned(x, 16)) return RQ_ERR_SHAPE;
+  return act_codes(ctx, x, M, K, false, x_fp8, x_dequant, reinterpret_cast<cudaStream_t>(stream));
 }
 
 rq_status rq_linear(rq_ctx* ctx, rq_qtype qtype, const void* w, const float* x, float* y,
@@ -1038,7 +1091,6 @@ rq_status rq_ctx_trace_end(rq_ctx* ctx, int64_t* counts_host, double* ms_host) {
 rq_status rq_act_cache_invalidate(rq_ctx* ctx) {
   if (ctx == nullptr) return RQ_ERR_NULL;
   ++ctx->gen;
-  ctx->act_valid = false;
   return RQ_OK;
 }
 

@@ -355,8 +355,13 @@ rq_status rq_fp8_gemm_epilogue(const uint8_t *x_fp8, const float *x_dequant,
 
 /* The FP8 route of rq_linear with an epilogue, at every M (the threshold does
  * not apply: the weight is read as one byte per value even for one token):
- * FP8 weight cache, FP8 activation of x with its cache (both as rq_linear's,
- * and shared with it), rq_fp8_gemm_epilogue.
+ * FP8 weight cache (rq_linear's, shared with it), FP8 activation of x,
+ * rq_fp8_gemm_epilogue.  For M at or above the threshold the activation cache is
+ * used, shared with rq_linear and under its rule: rq_act_cache_invalidate must
+ * be called when x's contents change in place (rq_residual_norm into the same x,
+ * say).  Below it, where rq_linear quantizes nothing, every call quantizes x.
+ * Call it once with a weight before a capture: the FP8 weight is allocated and
+ * made on the first call.
  * Errors: RQ_ERR_QTYPE (qtype, dtype or act), those of rq_linear and of
  * rq_fp8_gemm_epilogue. */
 rq_status rq_linear_epilogue(rq_ctx *ctx, rq_qtype qtype, const void *w, const float *x,

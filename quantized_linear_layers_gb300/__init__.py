@@ -753,7 +753,9 @@ class Context:
     def rq_linear_epilogue(self, qtype, w, x, y, M, N, K, act="none", bias=None, mul=None,
                            residual=None, dtype=None, stream=None):
         """The FP8 route of rq_linear with the epilogue of
-        rq_fp8_gemm_epilogue, at every M."""
+        rq_fp8_gemm_epilogue, at every M.  From the threshold on, an x that
+        was written in place wants rq_act_cache_invalidate first, as for
+        rq_linear."""
         where, dev = "rq_linear_epilogue", _types.device()
         e, dtype, yp, ys = _epilogue(where, dev, M, N, y, act, bias, mul, residual, dtype)
         wp = w

@@ -723,7 +723,9 @@ rq_status rq_linear_epilogue(rq_ctx* ctx, rq_qtype qtype, const void* w, const f
   if (s != RQ_OK) return s;
   const uint8_t* xq = nullptr;
   const float* xdeq = nullptr;
-  s = rq_fp8_act_cache(ctx, x, M, K, &xq, &xdeq, stream);
+  // below the threshold rq_linear reads x itself, and so its callers invalidate
+  // nothing there
+  s = act_codes(ctx, x, M, K, M < ctx->threshold, &xq, &xdeq, st);
   if (s != RQ_OK) return s;
   TraceScope ts(ctx, RQ_TRACE_GEMM, st);
   return launch_fp8_gemm_epilogue(xq, xdeq, wq, wdeq, e, dtype, y, y_stride, M, N, K, st, !miss);

@@ -228,9 +228,12 @@ struct Scale {
     cl = t < INFINITY ? __fdiv_rn(fmaf(-ch, t, kh) + kl, t) : 0.0f;
   }
 
-  // y's larger part, 0 .. kFar (never rises with l); a NaN gives kFar.
+  // y's larger part, 0 .. kFar (never rises with l); a NaN gives kFar.  (Products
+  // that decide a bin are rounded by themselves: fused into what follows them in
+  // one pass and not in another, a token would be counted in one bin and listed
+  // in its neighbour.)
   __device__ __forceinline__ float far(float l) const {
-    return fmaxf(fminf(fmaf(-l, pre, near) * ch, kFar), 0.0f);
+    return fmaxf(fminf(__fmul_rn(fmaf(-l, pre, near), ch), kFar), 0.0f);
   }
 
   // W, and far(l).
@@ -239,7 +242,7 @@ struct Scale {
     const float lp = l * pre;
     const float s = fmaf(-l, pre, near), t = s - near;
     const float e = (near - (s - t)) - (lp + t);
-    const float yh = s * ch;
+    const float yh = __fmul_rn(s, ch);
     const float pl = fmaf(e, ch, fmaf(s, cl, fmaf(s, ch, -yh)));
     // (-Inf and NaN: kFar, weight 0, whatever the rest below)
     ph = fmaxf(fminf(yh, kFar), 0.0f);
@@ -263,7 +266,7 @@ struct Scale {
     const float lp = l * pre;
     const float s = fmaf(-l, pre, near), t = s - near;
     const float e0 = (near - (s - t)) - (lp + t);
-    const float yh = s * ch;
+    const float yh = __fmul_rn(s, ch);
     const float pl = fmaf(e0, ch, fmaf(s, cl, fmaf(s, ch, -yh)));
     const float ph = fmaxf(fminf(yh, kFar), 0.0f);
     float e;
@@ -429,12 +432,13 @@ struct RowSampler {
 
   // A token's place in the first histogram: bin (int)place(l), kBins (or
   // more by a rounding) for tokens of no weight.
-  __device__ __forceinline__ float place(float l) const {
-    return scale.far(l) * (kBins / kFar);
+  __device__ __forceinline__ static float place_of(float far) {
+    return __fmul_rn(far, kBins / kFar);
   }
+  __device__ __forceinline__ float place(float l) const { return place_of(scale.far(l)); }
   // Its bin in one that divides the bins [b0, b0 + kFine / step) finer.
   __device__ __forceinline__ static int finer(float x, int b0, float step) {
-    return min((int)((x - (float)b0) * step), kFine - 1);
+    return min((int)__fmul_rn(__fsub_rn(x, (float)b0), step), kFine - 1);
   }
 
   __device__ __forceinline__ void enter(int bin, unsigned long long w) const {
@@ -811,7 +815,7 @@ struct RowSampler {
       float y;
       unsigned long long w = scale.weight(l, y);
       if (!plain.value && (w < least || (has_cut && !before_cut(v, l)))) w = 0ull;
-      const float x = y * (kBins / kFar);
+      const float x = place_of(y);
       const int b = (int)x;
       all += w;
       above += b < b0 ? w : 0ull;

@@ -319,8 +319,11 @@ rq_status rq_act_cache_invalidate(rq_ctx *ctx);
  *     output is added to.  Either may be y itself, with y's stride; neither
  *     may overlap y in another way.
  * SiLU z / (1 + e^-z); GELU z/2 (1 + erf(z / sqrt 2)); GELU_TANH z/2 (1 +
- * tanh(sqrt(2/pi) (z + 0.044715 z^3))); RELU max(z, 0) (a NaN stays one).  The struct is read
- * on the host during the call. */
+ * tanh(sqrt(2/pi) (z + 0.044715 z^3))); RELU max(z, 0) (a NaN stays one).
+ * Before the output's rounding they are within 2^-20 of their value, plus, of
+ * it, for 16-bit outputs 2^-23 |z| (SiLU) or 2^-23 z^2 (GELU), and for GELU_TANH
+ * 2^-21 |b|, b the tanh's argument doubled; and within 2^-120.  The struct is
+ * read on the host during the call. */
 typedef enum {
     RQ_ACT_NONE = 0,
     RQ_ACT_SILU = 1,

@@ -173,7 +173,8 @@ struct FusedOut {
 
 // e^x from the special function unit: its power of two is within 2^-22, and
 // for f32 outputs the rounding of x log2(e) is made good (x up to 88 would
-// lose six bits by it); 16-bit outputs, half a step of 2^-9 or 2^-12, need that not.
+// lose six bits by it).  16-bit outputs go without: |x| 2^-24 of the power is
+// 2^-17.5 at most, half their steps 2^-12 and 2^-9.
 template <bool kFast>
 __device__ __forceinline__ float power(float x) {
   constexpr float kH = 1.44269502162933349609f, kL = 1.92596299112661746887e-8f;  // log2 e
@@ -196,29 +197,63 @@ __device__ __forceinline__ float logistic_times(float z, float a) {
   return z * r;
 }
 
-// The activation, 2 special function instructions and at most a dozen others:
-// the library's functions, with their own branches, made the epilogue longer
+// GELU z/2 erfc(-z / sqrt 2), with its digits for every z (an erfc of small
+// absolute error, such as the 1.5e-7 of five terms in 1 / (1 + p x), has 5e-5 of
+// itself at z = -3, past half a step of f16 from -3.6 on).  With a = |z|,
+//   max(z, 0) - a/2 erfc(a / sqrt 2),   erfc(a / sqrt 2) / 2 = e^(-a^2/2) t P(t),
+// t = 1 / (1 + 0.35 a), P the polynomial of degree 8 whose largest relative
+// error over a = 0 .. 20 is smallest: 4.4e-8 (fitted by reweighted least
+// squares).  Near zero, where half of z cancels in that difference and P's
+// roundings are the result's, f32 takes z/2 + z^2 S(z^2) instead, S the same kind
+// of fit to erf(z / sqrt 2) / (2 z) for a < 0.75, 2.4e-9.  f32 results are within
+// 2^-20 of themselves (6e-7 met); for 16 bits the power's argument is rounded
+// twice more, another 1.25 z^2 2^-24.
+template <bool kFast>
+__device__ __forceinline__ float gelu(float z) {
+  constexpr float kH = 0.72134751081466675f, kL = 9.62981496e-9f;  // log2(e) / 2
+  const float a = fminf(fabsf(z), 24.0f), square = a * a;  // (the power is 0 from 15 on)
+  const float p = square * -kH;
+  float e;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(p));
+  if constexpr (!kFast) {
+    // what the square and its product left out
+    float rest = fmaf(square, -kH, -p);
+    rest = fmaf(square, -kL, rest);
+    rest = fmaf(fmaf(a, a, -square), -kH, rest);
+    e = fmaf(e, rest * 0.693147182464599609375f, e);
+  }
+  float t;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(t) : "f"(fmaf(fabsf(z), 0.35f, 1.0f)));  // (or NaN)
+  float q = fmaf(t, -2.853112295e-02f, 1.4127236605e-01f);
+  q = fmaf(t, q, -2.507376671e-01f);
+  q = fmaf(t, q, 1.541662961e-01f);
+  q = fmaf(t, q, -2.0117698235e-02f);
+  q = fmaf(t, q, 1.0442748665e-01f);
+  q = fmaf(t, q, 1.2006171795e-01f);
+  q = fmaf(t, q, 1.398360431e-01f);
+  q = fmaf(t, q, 1.396225840e-01f);
+  float y = fmaf(-e, (a * t) * q, fmaxf(z, 0.0f));
+  if constexpr (!kFast) {
+    float r = fmaf(square, 1.029405757e-04f, -1.181285013e-03f);
+    r = fmaf(square, r, 9.972348809e-03f);
+    r = fmaf(square, r, -6.649029255e-02f);
+    r = fmaf(square, r, 3.989422917e-01f);
+    if (a < 0.75f) y = fmaf(square, r, 0.5f * z);
+  }
+  return y;
+}
+
+// The activation, 2 special function instructions and at most a dozen others
+// (GELU 16, in f32 29): the library's functions, with their own branches, made the epilogue longer
 // than the products (2048 x 18944 x 3584, SiLU to f32: 305 us, of which 90 the
-// products).  GELU: erfc(x) = (a1 t + .. + a5 t^5) e^(-x^2), t = 1 / (1 + p x),
-// within 1.5e-7 (Abramowitz and Stegun 7.1.26).  (1 + tanh a) / 2 = 1 / (1 + e^-2a).
+// products).  (1 + tanh a) / 2 = 1 / (1 + e^-2a).
 template <bool kFast>
 __device__ __forceinline__ float activate(float z, int act) {
   if (act == RQ_ACT_NONE) return z;
   if (act == RQ_ACT_SILU) return logistic_times<kFast>(z, z);
   if (act == RQ_ACT_GELU_TANH)
     return logistic_times<kFast>(z, 1.59576912160573072f * fmaf(0.044715f * z * z, z, z));
-  if (act == RQ_ACT_GELU) {
-    const float x = fabsf(z) * 0.70710678118654752f;
-    float t;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(t) : "f"(fmaf(0.3275911f, x, 1.0f)));
-    float q = fmaf(t, 1.061405429f, -1.453152027f);
-    q = fmaf(t, q, 1.421413741f);
-    q = fmaf(t, q, -0.284496736f);
-    q = fmaf(t, q, 0.254829592f);
-    q *= t * power<kFast>(-x * x);  // erfc
-    const float h = 0.5f * fminf(fabsf(z), 100.0f) * q;  // (q is 0 there; z may be infinite)
-    return z > 0.0f ? z - h : -h;
-  }
+  if (act == RQ_ACT_GELU) return gelu<kFast>(z);
   return z < 0.0f ? 0.0f : z;  // (NaN stays NaN)
 }
 

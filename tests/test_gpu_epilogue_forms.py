@@ -1,8 +1,9 @@
 """GPU: what the epilogue's callers may rely on besides its sums: rows that are
-rewritten in place are read anew."""
+rewritten in place are read anew, and activations keep their digits."""
 import pytest
 import torch
 
+import pass_util as ref
 import synthetic
 
 pytestmark = pytest.mark.gpu
@@ -59,3 +60,59 @@ def test_a_norm_and_a_gated_product_layer_after_layer(rq, M):
         fresh.close()
         assert torch.equal(y, want)
     ctx.close()
+
+
+def activated(rq, z, act, dtype, tiles):
+    """act(z) by way of the bias.  tiles: enough tokens for the tile kernels (no
+    split of K), each of which then has the same row."""
+    N, K, M = len(z), 128, 300 if tiles else 1
+    args = (torch.zeros((M + 15) // 16 * 16, K).to(torch.float8_e4m3fn).cuda(), torch.ones(1).cuda(),
+            torch.zeros(N, K).to(torch.float8_e4m3fn).cuda(), torch.ones(1).cuda())
+    y = torch.empty(M, N, dtype=ref.DTYPES[dtype], device="cuda")
+    rq.rq_fp8_gemm_epilogue(*args, y, M, N, K, act=act, bias=z.cuda())
+    assert rq.rq_get_device_status() == 0
+    assert bool((y == y[0]).all())
+    return y[0].double().cpu()
+
+
+@pytest.mark.parametrize("tiles", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_gelu_keeps_its_digits(rq, dtype, tiles):
+    """z from -13 to 13, small and large: within 2^-20 of the result itself, then
+    rounded.  2^-20 = 16 u is the power's 2^-22 (4 u) and the reciprocal's 2^-23
+    (2 u), the fit's 4.4e-8 (1 u), the sum of nine terms whose magnitudes add up
+    to four times their sum (3 u), and the roundings of the root's argument, the
+    halves and three products (6 u).  16-bit results leave the rounding of the
+    power's argument, z^2 / 2 log2(e) 2^-24 ln 2, of log2(e) in it, a quarter of
+    that, and of z^2 / 2 itself: 1.25 z^2 u."""
+    g = ref.gen(60)
+    z = torch.cat([-13 + 26 * torch.rand(4000, generator=g),
+                   torch.randn(2000, generator=g),
+                   10.0 ** (-6 * torch.rand(1000, generator=g)),
+                   -(10.0 ** (-6 * torch.rand(1000, generator=g))),
+                   torch.tensor([0.0, -0.0, 0.75, -0.75, 0.55, -0.55, 40.0, -40.0, 1e30, -1e30])])
+    got = activated(rq, z, "gelu", dtype, tiles)
+    want = ref.act(z.double(), "gelu")
+    # (past where a 16-bit or a normal f32 result is one)
+    e = 2.0 ** -20 * want.abs()
+    if dtype != "f32":
+        e = e + 1.25 * ref.U * z.double().square() * want.abs()
+    tol = e + ref.ROUND[ref.DTYPES[dtype]] * (want.abs() + e) + \
+        (2.0 ** -126 if dtype != "f16" else ref.TINY[torch.float16])
+    off = (got - want).abs()
+    # (what its type cannot hold is infinite)
+    off = torch.where(want.abs() > torch.finfo(ref.DTYPES[dtype]).max,
+                      torch.where(got == float("inf"), 0.0, off), off)
+    worst = (off / tol).argmax()
+    assert bool((off <= tol).all()), (float(z[worst]), float(got[worst]), float(want[worst]))
+
+
+def test_gelu_of_normal_sums_is_as_near_as_the_plain_form(rq):
+    """f32: u of the result, as a norm: the last rounding is below that for each,
+    and the tail's 16 u are of values that are a tenth of the others."""
+    g = ref.gen(61)
+    for sigma in (0.05, 0.3, 1.0, 3.0):
+        z = sigma * torch.randn(20000, generator=g)
+        want = ref.act(z.double(), "gelu")
+        off = activated(rq, z, "gelu", "f32", False) - want
+        assert float(off.norm() / want.norm()) <= ref.U, sigma

@@ -84,6 +84,40 @@ def uniform(g, n):
     return torch.rand(n, generator=g).tolist()
 
 
+@pytest.mark.parametrize("vocab", [600, 5000, 131072])
+def test_equal_logits_are_cut_where_the_definition_cuts_them(rq, vocab):
+    # every weight is the same whole number: nothing is near a border
+    logits = torch.zeros(4, vocab, device="cuda")
+    logits[1, 1:] = -float("inf")
+    logits[1, ::3] = 2.0
+    logits[1, 1::3] = 2.0
+    logits[2, ::2] = -0.0
+    logits[3, : vocab // 2] = -float("inf")
+    u = [0.0, 0.3, 0.7, 0.999]
+    for p in (0.0, 1e-9, 0.1, 0.5, 0.75, 0.9, 0.99999):
+        assert check(rq, logits, u, p=[p] * 4) == 0
+        assert check(rq, logits, u, p=[p] * 4, k=[vocab // 3] * 4) == 0
+        assert check(rq, logits, u, p=[p] * 4, m=[1.0] * 4) == 0
+    for k in (2, 100, 128, 129, 512, 513, vocab // 2, vocab):
+        assert check(rq, logits, u, k=[k] * 4) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("vocab", [700, 4097, 50001, 131072])
+def test_what_each_filter_leaves(rq, vocab, dtype):
+    g = ref.gen(vocab + 7)
+    rows = 7
+    logits = (2.5 * torch.randn(rows, vocab, generator=g)).to(ref.DTYPES[dtype]).cuda()
+    u = uniform(g, rows)
+    t = [0.3 + 0.25 * i for i in range(rows)]
+    k = [2, 40, 128, 129, 600, vocab // 2, vocab]
+    p = [0.9, 0.5, 0.99, 0.0, 0.7, 0.01, 0.95]
+    m = [0.0, 0.05, 1e-6, 1.0, 0.3, 1e-3, 0.02]
+    for more in (dict(), dict(t=t), dict(t=t, k=k), dict(t=t, p=p), dict(t=t, m=m), dict(k=k, p=p),
+                 dict(t=t, k=k, p=p, m=m)):
+        check(rq, logits, u, **more)
+
+
 def test_tokens_at_the_edges_of_the_finer_bins(rq):
     """A cut's bin, a 512th of 43 octaves, is divided into 128: floats on both
     sides of those edges, which one pass counts and another lists."""

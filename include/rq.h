@@ -705,8 +705,8 @@ rq_status rq_sample(const rq_sampling *sampling_host, int dtype, const void *log
 
 /* The same distribution written out, as rq_verify_chain and rq_verify_tree
  * take it:  p: f32 [rows][vocab], dense, W / total of the tokens that stay, to
- * 2^-21 of itself, and 0 elsewhere (a row of NaN and -Inf only: zeros); must
- * not overlap the logits.
+ * 2^-21 of itself whatever W is, and 0 elsewhere (a row of NaN and -Inf only:
+ * zeros), so that rq_sample draws no token of p 0; must not overlap the logits.
  * Errors: as rq_sample. */
 rq_status rq_token_probs(const rq_sampling *sampling_host, int dtype, const void *logits,
                          int64_t stride, float *p, int rows, int vocab,

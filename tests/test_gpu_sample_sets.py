@@ -137,3 +137,48 @@ def test_tokens_at_the_edges_of_the_finer_bins(rq):
         assert int((probs[r] > 0).sum()) == k and probs[r][tokens[r]] > 0
     check(rq, rows, uniform(g, len(ks)), k=ks)
     check(rq, rows, uniform(g, len(ks)), p=[(i + 0.5) / len(ks) for i in range(len(ks))])
+
+
+def whole_number_weights(l, t):
+    """2^42 e^(l / t) with its fraction, of f32 differences l and a temperature."""
+    import decimal
+    decimal.getcontext().prec = 40
+    t = decimal.Decimal(float(np.float32(t)))
+    return [decimal.Decimal(float(x)) / t for x in l], decimal.Decimal(2) ** 42
+
+
+@pytest.mark.parametrize("t", [1.0, 0.7])
+def test_probabilities_of_the_smallest_weights(rq, t):
+    """p = W / total to 2^-21 of itself for W from 1 on, and 0 where W is 0: the
+    distribution that rq_sample draws from, whatever filters are on.  Only
+    weights whose value is not within a 2^-30th of a whole number are looked at,
+    so that W is the same however it is evaluated (to 2^-32)."""
+    g = ref.gen(13)
+    l = torch.cat([torch.zeros(1), -t * (14 + 15.5 * torch.rand(6000, generator=g)),
+                   -t * (27.5 + 2 * torch.rand(3000, generator=g))])
+    far, unit = whole_number_weights(l.numpy(), t)
+    value = [unit * x.exp() for x in far]
+    whole = np.array([int(v) for v in value], dtype=np.int64)
+    sure = np.array([min(v - int(v), int(v) + 1 - v) > v / 2 ** 30 for v in value])
+    sure[0] = True  # the largest
+    assert sure.sum() > 8000 and (whole[sure] == 0).any() and (whole[sure] == 1).any()
+    logits = l[None].cuda()
+    rows = []
+    for more in (dict(), dict(p=[0.9999999]), dict(k=[len(l)]), dict(m=[1e-30])):
+        _, probs = run(rq, logits, [0.5], t=[t], **more)
+        rows.append(probs[0])
+        if "p" in more:
+            continue  # (the cut takes some out)
+        got = probs[0].astype(np.float64)
+        total = float(whole.sum())
+        tol = 8 * ref.U * whole / total + 2.0 ** -149
+        assert np.array_equal(got[sure] > 0, whole[sure] > 0)
+        assert (np.abs(got - whole / total)[sure] <= tol[sure] + slack_of_total(whole, got)[sure]).all()
+    # a nucleus of 1 - 2^-23 has a total smaller by that, and the same weights
+    kept = (rows[1] > 0) & sure
+    assert (np.abs(rows[1] - rows[0])[kept] <= (2.0 ** -20 + 2.0 ** -22) * rows[0][kept]).all()
+
+
+def slack_of_total(whole, got):
+    """The total's own error: 2^-32 of it and a unit a token."""
+    return got * (2.0 ** -32 + len(whole) / float(whole.sum()))

@@ -588,6 +588,8 @@ class NormParams:
         at = [_array(t, _types.f32, dev, "NormParams", "a weight", width)
               for t in (post_weight, pre_weight)]
         self.tensors = (post_weight, pre_weight)
+        # the device of the weights (None: there are none)
+        self.device = dev if any(hasattr(t, "dtype") for t in self.tensors) else None
         self.width = width
         self.struct = _NormStruct(at[0], at[1], width,
                                   (RQ_NORM_POST if post else 0) | (RQ_NORM_PRE if pre else 0),
@@ -601,6 +603,8 @@ def rq_residual_norm(params, y, h, h_out, x_out, tokens, gate=None, absmax_bits=
     block before; gate: [width], or [tokens, width] like y; either output may
     be None."""
     n, where, dev = params.width, "rq_residual_norm", _types.device()
+    if params.device is not None and params.device != dev:
+        raise RqError(2, where + ": the norms' weights are on another device than the current one")
     if dtype is None:
         dtype = _dtype(None, where, y, gate, x_out) if y is not None or x_out is not None else \
             _dtype(None, where, h)

@@ -253,15 +253,23 @@ __global__ void clear_word_kernel(uint32_t* word) {
   *word = 0u;
 }
 
+// Groups of V values that a thread takes of many tokens' rows.
+template <int V>
+constexpr int kManyGroups = 16 / V < 4 ? 16 / V : 4;
+
 template <typename T, typename R, int V, int G, bool kSkew>
 rq_status launch_groups(const NormArgs& a, int threads, int per_cta, cudaStream_t st) {
   const unsigned ctas = (unsigned)((a.tokens + per_cta - 1) / per_cta);
-  if (threads == 32)
-    return launch_kernel(residual_norm_kernel<T, R, V, G, true, kSkew, 128, 1>, dim3(ctas),
-                         dim3(32 * per_cta), 0, st, a);
-  if (threads <= 256)
-    return launch_kernel(residual_norm_kernel<T, R, V, G, false, kSkew, 256, 4>, dim3(ctas),
-                         dim3(threads), 0, st, a);
+  // groups a thread other than few tokens' one and many tokens' four (or all)
+  // come from rows of more than 1024 threads' groups only
+  if constexpr (G == 1 || G == kManyGroups<V>) {
+    if (threads == 32)
+      return launch_kernel(residual_norm_kernel<T, R, V, G, true, kSkew, 128, 1>, dim3(ctas),
+                           dim3(32 * per_cta), 0, st, a);
+    if (threads <= 256)
+      return launch_kernel(residual_norm_kernel<T, R, V, G, false, kSkew, 256, 4>, dim3(ctas),
+                           dim3(threads), 0, st, a);
+  }
   return launch_kernel(residual_norm_kernel<T, R, V, G, false, kSkew, 1024, 1>, dim3(ctas),
                        dim3(threads), 0, st, a);
 }
@@ -274,7 +282,7 @@ rq_status launch_width(NormArgs a, cudaStream_t st) {
   // few tokens: as many threads as the row has groups, so that each thread
   // waits for one load; many: as many loads in flight a thread as fit
   const bool few = a.tokens <= 2 * device_sm_count();
-  int G = few || groups <= 32 ? 1 : 4 < kMost ? 4 : kMost;
+  int G = few || groups <= 32 ? 1 : kManyGroups<V>;
   while (G < kMost && (groups + G - 1) / G > 1024) G *= 2;
   const int threads = ((groups + G - 1) / G + 31) / 32 * 32;
   const int per_cta = threads == 32 ? 4 : 1;

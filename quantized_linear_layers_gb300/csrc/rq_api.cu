@@ -357,6 +357,10 @@ rq_status rq_fp8_weight_cache(rq_ctx* ctx, rq_qtype qtype, const void* w, int N,
     if (s == RQ_OK) s = launch_dequant_absmax(qtype, wb, N, K, ctx->absmax, st);
     if (s == RQ_OK)
       s = launch_dequant_encode(qtype, wb, N, K, ctx->absmax, e.fp8, e.deq, st);
+    // A product that finds this entry loads its first tiles before the launch ahead
+    // of it is done.  That launch must not be the encoding: what is no kernel waits
+    // for it, and the product for that.
+    if (s == RQ_OK) s = cuda_status(cudaMemsetAsync(ctx->absmax, 0, sizeof(uint32_t), st));
     if (s != RQ_OK) {
       cudaFree(p);
       return s;

@@ -1,5 +1,6 @@
 """GPU: what the epilogue's callers may rely on besides its sums: rows that are
-rewritten in place are read anew, and activations keep their digits."""
+rewritten in place are read anew, weights are waited for, and activations keep
+their digits."""
 import pytest
 import torch
 
@@ -58,6 +59,30 @@ def test_a_norm_and_a_gated_product_layer_after_layer(rq, M):
         fresh.rq_linear_epilogue(rq.RQ_Q4K, w, x.clone(), want, M, N, K, act="silu", mul=up)
         torch.cuda.synchronize()
         fresh.close()
+        assert torch.equal(y, want)
+    ctx.close()
+
+
+@pytest.mark.parametrize("M,N,K", [(8, 18944, 3584), (300, 18944, 3584), (2000, 9472, 3584)])
+def test_a_weight_cached_right_before_a_product_of_a_cached_activation(rq, M, N, K):
+    # nothing is launched between the weight's encoding and the product
+    ctx = rq.Context()
+    small, x = packed(rq, 11, 256, K), rows(12, M, K)
+    w = [packed(rq, 13, N, K) for _ in range(3)]
+    y, want = torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda")
+    aside = torch.empty(M, 256, device="cuda")
+    for i, linear in ((0, True), (1, False), (2, True)):
+        ctx.rq_linear(rq.RQ_Q4K, small, x, aside, M, 256, K)        # x is cached
+        hits = ctx.stats()["act_hits"]
+        ctx.rq_fp8_weight_cache(rq.RQ_Q4K, w[i], N, K)
+        if linear:
+            ctx.rq_linear(rq.RQ_Q4K, w[i], x, y, M, N, K)
+        else:
+            ctx.rq_linear_epilogue(rq.RQ_Q4K, w[i], x, y, M, N, K)
+        assert ctx.stats()["act_hits"] == hits + 1
+        torch.cuda.synchronize()
+        ctx.rq_linear(rq.RQ_Q4K, w[i], x, want, M, N, K)
+        torch.cuda.synchronize()
         assert torch.equal(y, want)
     ctx.close()
 

@@ -406,6 +406,9 @@ typedef struct {
  * Strides are at least width; every pointer needs its element's alignment
  * (16-byte aligned rows of a multiple of 16 bytes are read 16 bytes at a
  * time).  tokens == 0 does nothing (but sets *absmax_bits to 0).
+ * A linear that reads x_out as cached FP8 codes (rq_linear and
+ * rq_linear_epilogue from the threshold on) wants rq_act_cache_invalidate after
+ * each call that writes the same x_out.
  * Errors: RQ_ERR_NULL, RQ_ERR_SHAPE, RQ_ERR_QTYPE (dtype, h_dtype, or
  * absmax_bits with 16-bit x), RQ_ERR_CUDA. */
 rq_status rq_residual_norm(const rq_norm_params *params_host, int dtype, const void *y,

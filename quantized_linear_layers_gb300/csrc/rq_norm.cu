@@ -8,12 +8,13 @@
 //
 // A group of threads keeps its token in registers between the two sums: y and
 // h are read once and h' and x written once, which is what the operator cannot
-// do without.  Bound by memory: 4096 tokens of 3584 f32 values take 36.7 us
-// (6.40 TB/s, 96 % of a measured copy), 37.6 with the largest magnitude; bf16 on an f32 stream
-// 29.8 us (5.92 TB/s), bf16 throughout 23.0 (5.11: there a CTA's steps one
-// after another count).  y and h stay as they lie in memory until they are
-// used, which lets four CTAs of 224 threads onto an SM (16-bit rows as floats:
-// 27.3 us; six CTAs spill registers: 40.9 for f32).  One token: 2.2 us in a
+// do without.  Bound by memory: 4096 tokens of 3584 f32 values take 36.8 us
+// (6.39 TB/s, 95 % of a measured copy), 37.7 with the largest magnitude (calls one
+// behind another on three sets of tensors; 41 between other kernels with a cold
+// L2); bf16 on an f32 stream 29.8 us (5.90 TB/s), bf16 throughout 23.1 (5.07: there
+// a CTA's steps one after another count).  y and h stay as they lie in memory until
+// they are used, which lets four CTAs of 224 threads onto an SM (16-bit rows as
+// floats: 27.3 us; six CTAs spill registers: 40.9 for f32).  One token: 2.2 us in a
 // replayed graph.  Odd widths: 1091 tokens of 6245 f32 values with a gate a
 // token 34 us (an element at a time 40).
 #include "rq_device.cuh"

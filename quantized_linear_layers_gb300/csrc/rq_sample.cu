@@ -35,15 +35,16 @@
 // the same and scattered into shared memory), so that a warp's scan of its
 // lanes' sums is a scan by index.
 //
-// Bound by instruction issue: 64 rows of 131072 f32 logits without filters take
-// 35 us, of which reading them is 5, and reading, the maximum and the barriers
-// are 20 (the likeliest token alone); the exact pass issues 45 instructions a
-// token.  With top-k 50 34 us, with a nucleus of 0.9 63 us (196 with a
-// histogram of exact weights over the whole row).  One row: 13, 15 and 23 us,
-// about 8 us of which are 5 to 7 barriers and what follows them (with cold
-// inputs, launch and events included); clusters of 16 CTAs made that 13, 15 and
-// 24.  What a larger top-k leaves is marked in a word of bits a thread, and
-// later passes look at marked tokens only.
+// No one thing bounds it: 64 rows of 131072 f32 logits with mixed filters fill 35 %
+// of the issue slots, and warps wait at barriers most; 256 rows of 50001 with a
+// nucleus fill 50 %.  64 rows without filters take 35 us, of which reading them is
+// 5, and reading, the maximum and the barriers are 20 (the likeliest token alone);
+// the exact pass issues 45 instructions a token.  With top-k 50 34 us, with a
+// nucleus of 0.9 63 us (196 with a histogram of exact weights over the whole row).
+// One row: 13, 15 and 23 us, about 8 us of which are 5 to 7 barriers and what
+// follows them (with cold inputs, launch and events included); clusters of 16 CTAs
+// made that 13, 15 and 24.  What a larger top-k leaves is marked in a word of bits a
+// thread, and later passes look at marked tokens only.
 #include <type_traits>
 
 #include "rq_device.cuh"

@@ -208,10 +208,10 @@ rq_status rq_fp8_gemm(const uint8_t *x_fp8, const float *x_dequant,
  *   x: f32 [M x K], 16-byte aligned.   *x_fp8: E4M3 [M_pad x K] (owned by
  *   ctx).   *x_dequant: one device float (owned by ctx).
  * The pointers stay valid until a later miss on this ctx needs a larger
- * scratch (captured ones: always), or the ctx is destroyed; a later miss of the
- * same or smaller size overwrites the bytes in stream order.  Allocates on a miss that needs a
- * larger scratch.  Errors: RQ_ERR_NULL, RQ_ERR_SHAPE (M, K < 1, x
- * misaligned), RQ_ERR_ALLOC, RQ_ERR_CUDA. */
+ * scratch, those of a captured call until the ctx is destroyed; a later miss of
+ * the same or smaller size overwrites the bytes in stream order.  Allocates on a
+ * miss that needs a larger scratch.  Errors: RQ_ERR_NULL, RQ_ERR_SHAPE (M, K < 1,
+ * x misaligned), RQ_ERR_ALLOC, RQ_ERR_CUDA. */
 rq_status rq_fp8_act_cache(rq_ctx *ctx, const float *x, int M, int K,
                            const uint8_t **x_fp8, const float **x_dequant,
                            rq_stream_t stream);

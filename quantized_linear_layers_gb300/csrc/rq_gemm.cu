@@ -243,10 +243,10 @@ __device__ __forceinline__ float gelu(float z) {
   return y;
 }
 
-// The activation, 2 special function instructions and at most a dozen others
-// (GELU 16, in f32 29): the library's functions, with their own branches, made the epilogue longer
-// than the products (2048 x 18944 x 3584, SiLU to f32: 305 us, of which 90 the
-// products).  (1 + tanh a) / 2 = 1 / (1 + e^-2a).
+// The activation, 2 special function instructions and at most a dozen others (GELU
+// 16, in f32 29): the library's functions, with their own branches, made the
+// epilogue longer than the products (2048 x 18944 x 3584, SiLU to f32: 305 us, of
+// which 90 the products).  (1 + tanh a) / 2 = 1 / (1 + e^-2a).
 template <bool kFast>
 __device__ __forceinline__ float activate(float z, int act) {
   if (act == RQ_ACT_NONE) return z;

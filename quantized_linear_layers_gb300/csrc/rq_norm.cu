@@ -261,8 +261,8 @@ constexpr int kManyGroups = 16 / V < 4 ? 16 / V : 4;
 template <typename T, typename R, int V, int G, bool kSkew>
 rq_status launch_groups(const NormArgs& a, int threads, int per_cta, cudaStream_t st) {
   const unsigned ctas = (unsigned)((a.tokens + per_cta - 1) / per_cta);
-  // groups a thread other than few tokens' one and many tokens' four (or all)
-  // come from rows of more than 1024 threads' groups only
+  // (a thread takes another number of groups only where 1024 threads would not
+  // hold the row with fewer, and then there are more than 512)
   if constexpr (G == 1 || G == kManyGroups<V>) {
     if (threads == 32)
       return launch_kernel(residual_norm_kernel<T, R, V, G, true, kSkew, 128, 1>, dim3(ctas),

@@ -91,8 +91,9 @@ def activated(rq, z, act, dtype, tiles):
     """act(z) by way of the bias.  tiles: enough tokens for the tile kernels (no
     split of K), each of which then has the same row."""
     N, K, M = len(z), 128, 300 if tiles else 1
-    args = (torch.zeros((M + 15) // 16 * 16, K).to(torch.float8_e4m3fn).cuda(), torch.ones(1).cuda(),
-            torch.zeros(N, K).to(torch.float8_e4m3fn).cuda(), torch.ones(1).cuda())
+    x, w = torch.zeros((M + 15) // 16 * 16, K), torch.zeros(N, K)
+    args = (x.to(torch.float8_e4m3fn).cuda(), torch.ones(1).cuda(),
+            w.to(torch.float8_e4m3fn).cuda(), torch.ones(1).cuda())
     y = torch.empty(M, N, dtype=ref.DTYPES[dtype], device="cuda")
     rq.rq_fp8_gemm_epilogue(*args, y, M, N, K, act=act, bias=z.cuda())
     assert rq.rq_get_device_status() == 0

@@ -362,7 +362,8 @@ rq_status rq_fp8_gemm_epilogue(const uint8_t *x_fp8, const float *x_dequant,
  * rq_fp8_gemm_epilogue.  For M at or above the threshold the activation cache is
  * used, shared with rq_linear and under its rule: rq_act_cache_invalidate must
  * be called when x's contents change in place (rq_residual_norm into the same x,
- * say).  Below it, where rq_linear quantizes nothing, every call quantizes x.
+ * say).  Below it, where rq_linear quantizes nothing, every call quantizes x
+ * and leaves nothing in the cache.
  * Call it once with a weight before a capture: the FP8 weight is allocated and
  * made on the first call.
  * Errors: RQ_ERR_QTYPE (qtype, dtype or act), those of rq_linear and of

@@ -430,7 +430,8 @@ static rq_status grow(rq_ctx* ctx, ActScratch* a, size_t need, bool captured) {
   return RQ_OK;
 }
 
-// rq_fp8_act_cache; `anew`: without a look at the cache.
+// rq_fp8_act_cache; `anew`: without a look at the cache, and nothing is left in
+// it, since the caller of such a call does not say when x changes.
 static rq_status act_codes(rq_ctx* ctx, const float* x, int M, int K, bool anew,
                            const uint8_t** x_fp8, const float** x_dequant, cudaStream_t st) {
   unsigned long long capture = 0;
@@ -472,7 +473,7 @@ static rq_status act_codes(rq_ctx* ctx, const float* x, int M, int K, bool anew,
       a.valid = false;
       return s;
     }
-    a.valid = true;
+    a.valid = !anew;
     a.x = x;
     a.M = M;
     a.K = K;

@@ -42,6 +42,24 @@ def test_rows_rewritten_in_place_below_the_threshold(rq, M):
     ctx.close()
 
 
+def test_nothing_is_left_in_the_cache_below_the_threshold(rq):
+    # a call that asks for no invalidation is not what a later one finds
+    M, N, K = 2, 512, 1024
+    ctx, w = rq.Context(), packed(rq, 5, N, K)
+    x, y, want = rows(44, M, K), *(torch.empty(M, N, device="cuda") for _ in range(2))
+    ctx.rq_linear_epilogue(rq.RQ_Q4K, w, x, y, M, N, K)
+    x.copy_(rows(45, M, K))
+    ctx.set_gemm_threshold(1)
+    ctx.rq_linear(rq.RQ_Q4K, w, x, y, M, N, K)
+    fresh = rq.Context(gemm_threshold=1)
+    fresh.rq_linear(rq.RQ_Q4K, w, rows(45, M, K), want, M, N, K)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    assert ctx.stats()["act_hits"] == 0
+    fresh.close()
+    ctx.close()
+
+
 @pytest.mark.parametrize("M", [1, 3, 40])
 def test_a_norm_and_a_gated_product_layer_after_layer(rq, M):
     # x is written in place by each layer's norm
